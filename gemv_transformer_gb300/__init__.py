@@ -26,15 +26,51 @@ WQ_ERR_DEVICE_TIMEOUT, WQ_ERR_BAD_EXPERT, WQ_ERR_TOO_LARGE, WQ_ERR_BAD_INDEX = 4
 WQ_GEMM_NOALLOC_SCRATCH_BYTES = 16 << 20
 WQ_GEMV_MAX_N = 16
 WQ_MOE_WINDOW_SLOTS = 256
+WQ_ROPE_INTERLEAVED, WQ_ROPE_TRANSPOSE = 1, 2
+WQ_ROPE_PLAIN, WQ_ROPE_LINEAR, WQ_ROPE_NTK, WQ_ROPE_YARN, WQ_ROPE_BANDS = 0, 1, 2, 3, 4
 
 EXPORTS = ("wq_gemm", "wq_gemm_ws", "wq_gemm_alpha", "wq_gemm_dual", "wq_gemm_workspace_bytes",
            "wq_gemm_noalloc",
            "wq_gemm_ln_ws", "wq_gemm_ln_workspace_bytes", "wq_gemv",
            "wq_moe_gemv", "wq_weight_bytes", "wq_dequantize", "wq_embed", "wq_get_device_status",
-           "wq_status_string", "wq_set_wait_limit")
+           "wq_status_string", "wq_set_wait_limit",
+           "wq_rope_table", "wq_rope", "wq_kv_append", "wq_attn_paged",
+           "wq_attn_paged_workspace_bytes", "wq_kv_evict", "wq_kv_evict_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class RopeScaling(ctypes.Structure):
+    """wq_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int32), ("original", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class KvCache(ctypes.Structure):
+    """wq_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+def kv_cache(k, v) -> KvCache:
+    """The descriptor of two pools seen as [page][head][row][dim] (a view with any strides
+    but a last one of 1).  It keeps addresses, not the tensors: the caller keeps those."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        raise ValueError("k and v: two 4-D tensors of one shape, type and layout")
+    kinds = {torch.bfloat16: WQ_BF16, torch.float16: WQ_F16, torch.float32: WQ_F32}
+    if k.dtype not in kinds or k.stride(3) != 1:
+        raise ValueError("a cache holds bf16, f16 or f32 with contiguous dims")
+    pages, heads, rows, dims = k.shape
+    # A stride of an extent of 1 is never used; torch may give any value there.
+    step = [k.stride(i) if k.shape[i] > 1 else pages * heads * rows * dims for i in range(3)]
+    return KvCache(k.data_ptr(), v.data_ptr(), kinds[k.dtype], pages, rows, heads, dims, 0,
+                   step[0], step[1], step[2])
 
 
 class WqError(RuntimeError):
@@ -80,6 +116,24 @@ def _open(path: str):
     lib.wq_gemm_dual.restype = ci
     lib.wq_embed.argtypes = [ci, ci, ci, ci, vp, vp, vp, vp, vp, vp]
     lib.wq_embed.restype = ci
+    cl, cp = ctypes.c_int64, ctypes.POINTER(KvCache)
+    lib.wq_rope_table.argtypes = [ci, ci, ctypes.c_double, ctypes.POINTER(RopeScaling), vp, vp]
+    lib.wq_rope_table.restype = ci
+    lib.wq_rope.argtypes = [ci, ci, ci, ci, cu, vp, cl, vp, vp, ci, vp, cl, vp]
+    lib.wq_rope.restype = ci
+    lib.wq_kv_append.argtypes = [cp, ci, ci, ci, cu, vp, cl, vp, cl, vp, cl, vp, vp, ci, ci, vp,
+                                 vp, vp, ci, vp, cl, vp, vp, cl, vp]
+    lib.wq_kv_append.restype = ci
+    lib.wq_attn_paged.argtypes = [cp, ci, ci, ctypes.c_float, ci, vp, cl, vp, ci, vp, vp, cl, vp,
+                                  cl, vp, vp, vp, cl, vp, sz, vp]
+    lib.wq_attn_paged.restype = ci
+    lib.wq_attn_paged_workspace_bytes.argtypes = [cp, ci, ci, ci, ci]
+    lib.wq_attn_paged_workspace_bytes.restype = sz
+    lib.wq_kv_evict.argtypes = [cp, ci, vp, ci, vp, vp, ci, ci, ci, vp, vp, vp, vp, cl, vp, vp,
+                                sz, vp]
+    lib.wq_kv_evict.restype = ci
+    lib.wq_kv_evict_workspace_bytes.argtypes = [cp, ci, ci, ci]
+    lib.wq_kv_evict_workspace_bytes.restype = sz
     lib.wq_get_device_status.argtypes = [vp]
     lib.wq_get_device_status.restype = ci
     lib.wq_status_string.argtypes = [ci]
@@ -183,6 +237,51 @@ def wq_gemm_dual(n, m, k, dual, wtype, flags, alpha, X, W, bias=None, bias2=None
 def wq_embed(n_ids, rows, k, wtype, W, ids, pos=None, bias=None, out=None, stream=None) -> int:
     return load().wq_embed(n_ids, rows, k, wtype, _p(W), _p(ids), _p(pos), _p(bias), _p(out),
                            _s(stream))
+
+
+def wq_rope_table(rows, rot, base, scaling, table, stream=None) -> int:
+    return load().wq_rope_table(rows, rot, base, scaling, _p(table), _s(stream))
+
+
+def wq_rope(n, n_heads, head_dim, rot, flags, x, x_stride, pos, table, table_rows, out,
+            out_stride, stream=None) -> int:
+    return load().wq_rope(n, n_heads, head_dim, rot, flags, _p(x), x_stride, _p(pos), _p(table),
+                          table_rows, _p(out), out_stride, _s(stream))
+
+
+def wq_kv_append(cache, n_tok, h_q, rot, flags, q, q_stride, k, k_stride, v, v_stride, pos, table,
+                 table_rows, n_seq, seq, slot, page_table, max_pages, q_out=None, q_out_stride=0,
+                 acc=None, slot_pos=None, acc_stride=0, stream=None) -> int:
+    return load().wq_kv_append(cache, n_tok, h_q, rot, flags, _p(q), q_stride, _p(k), k_stride,
+                               _p(v), v_stride, _p(pos), _p(table), table_rows, n_seq, _p(seq),
+                               _p(slot), _p(page_table), max_pages, _p(q_out), q_out_stride,
+                               _p(acc), _p(slot_pos), acc_stride, _s(stream))
+
+
+def wq_attn_paged(cache, n_seq, h_q, scale, window, q, q_stride, page_table, max_pages, lens,
+                  mask=None, mask_stride=0, out=None, out_stride=0, lse=None, acc_in=None,
+                  acc_out=None, acc_stride=0, workspace=None, workspace_bytes=0,
+                  stream=None) -> int:
+    return load().wq_attn_paged(cache, n_seq, h_q, scale, window, _p(q), q_stride, _p(page_table),
+                                max_pages, _p(lens), _p(mask), mask_stride, _p(out), out_stride,
+                                _p(lse), _p(acc_in), _p(acc_out), acc_stride, _p(workspace),
+                                workspace_bytes, _s(stream))
+
+
+def wq_attn_paged_workspace_bytes(cache, n_seq, h_q, max_pages, with_acc) -> int:
+    return load().wq_attn_paged_workspace_bytes(cache, n_seq, h_q, max_pages, int(with_acc))
+
+
+def wq_kv_evict(cache, n_seq, page_table, max_pages, lens, seen, keep, sinks, recent, acc,
+                slot_pos, acc_out, pos_out, acc_stride, lens_out, workspace=None,
+                workspace_bytes=0, stream=None) -> int:
+    return load().wq_kv_evict(cache, n_seq, _p(page_table), max_pages, _p(lens), _p(seen), keep,
+                              sinks, recent, _p(acc), _p(slot_pos), _p(acc_out), _p(pos_out),
+                              acc_stride, _p(lens_out), _p(workspace), workspace_bytes, _s(stream))
+
+
+def wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep) -> int:
+    return load().wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep)
 
 
 def wq_get_device_status(stream=None) -> int:

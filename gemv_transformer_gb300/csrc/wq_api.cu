@@ -331,7 +331,7 @@ const char *wq_status_string(int status) {
     case WQ_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case WQ_ERR_BAD_EXPERT: return "expert id out of range";
     case WQ_ERR_TOO_LARGE: return "request exceeds the fixed scratch size";
-    case WQ_ERR_BAD_INDEX: return "embedding row id out of range";
+    case WQ_ERR_BAD_INDEX: return "row id, position, cache slot or page out of range";
     default: return "unknown status";
     }
 }

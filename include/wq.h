@@ -26,6 +26,13 @@
  *   - wq_embed: wavo 0.3.0, src/gpu/mod.rs, Recorder::embed (table row ids[i]
  *     plus a position row plus the table's bias, k values each) and its test
  *     gemv_and_embed.
+ *   - wq_rope, wq_rope_table: cortiq-engine 0.8.49, src/gpu_wgpu/nemotron_audio.rs,
+ *     kernel ae_qk (rotary q and k from a host-made cos/sin table); hanzo-ml 0.11.13,
+ *     src/wgpu_backend.rs, rope (both pair layouts).
+ *   - wq_kv_append: wavo 0.3.0, src/gpu/mod.rs, the decoder's key-value cache (pack).
+ *   - wq_attn_paged: wavo 0.3.0, src/gpu/mod.rs, attend / combine (one token's
+ *     attention with the keys split into parts that are joined).
+ *   - wq_kv_evict: no counterpart on the pages.
  *   - wq_get_device_status: wavo 0.3.0, Gpu "failure" (the first device error is
  *     reported by the next call) and its completion marks.
  *
@@ -123,7 +130,9 @@ typedef enum {
     WQ_ERR_DEVICE_TIMEOUT = 4, /* a kernel's bounded wait ran out (device status) */
     WQ_ERR_BAD_EXPERT = 5,     /* an expert id outside [0, n_experts) (device status) */
     WQ_ERR_TOO_LARGE = 6,      /* wq_gemm_noalloc: the call needs more than its fixed scratch */
-    WQ_ERR_BAD_INDEX = 7       /* wq_embed: a row id outside [0, rows) (device status) */
+    WQ_ERR_BAD_INDEX = 7       /* an index in device memory out of range: a row id of wq_embed, a
+                                  position, slot, page or length of the cache calls (device
+                                  status) */
 } wq_status;
 
 /* Largest n that wq_gemv accepts. */
@@ -318,6 +327,188 @@ WQ_API wq_status wq_gemm_dual(int n, int m, int k, int dual, int wtype, unsigned
 WQ_API wq_status wq_embed(int n_ids, int rows, int k, int wtype, const void *W,
                           const int32_t *ids, const float *pos, const float *bias, float *out,
                           wq_stream_t stream);
+
+/* ------------------------------------------------ rotary positions, paged cache --
+ *
+ * The part of a decoder layer between its q/k/v projection (wq_gemv and the others)
+ * and its output projection: rotate q and k by their positions, write k and v into
+ * the pages of a cache, attend with one new token per sequence, and keep the cache
+ * within a budget.  Activations are f32 as everywhere in this library; the cache
+ * holds bf16, f16 or f32.  All products and sums are f32 or better.
+ */
+
+/* Pair layout and direction of a rotation. */
+enum {
+    WQ_ROPE_INTERLEAVED = 1u, /* pairs (2i, 2i+1); without it (i, i + rot/2) */
+    WQ_ROPE_TRANSPOSE = 2u    /* by the negative angle: the gradient of the rotation */
+};
+
+/* How wq_rope_table's frequencies f_i = base^(-2i/rot) are scaled for contexts longer
+ * than the `original` positions that the weights were trained on. */
+enum {
+    WQ_ROPE_PLAIN = 0,
+    WQ_ROPE_LINEAR = 1, /* f_i / factor */
+    WQ_ROPE_NTK = 2,    /* base * factor^(rot/(rot-2)) for base */
+    WQ_ROPE_YARN = 3,   /* with c(r) = rot ln(original / (2 pi r)) / (2 ln base), a = max(0,
+                           floor(c(high))), b = min(rot - 1, ceil(c(low))), t_i = (i - a) /
+                           max(b - a, 0.001) held in [0, 1]: f_i (1 - t_i + t_i / factor);
+                           low and high count rotations over `original` (usually 1 and 32) */
+    WQ_ROPE_BANDS = 4   /* by turns n_i = original f_i / (2 pi): f_i where n_i > high, f_i /
+                           factor where n_i < low, between them f_i ((1-s)/factor + s) with
+                           s = (n_i - low) / (high - low) */
+};
+
+typedef struct {
+    int32_t kind;      /* WQ_ROPE_PLAIN ... */
+    int32_t original;  /* YARN, BANDS: > 0 */
+    double factor;     /* > 0 (all but PLAIN) */
+    double low, high;  /* YARN, BANDS: 0 < low < high */
+    double magnitude;  /* multiplies cos and sin; 0: 1, or 0.1 ln(factor) + 1 with YARN */
+} wq_rope_scaling;
+
+/* table[p][i] = (m cos(p f_i), m sin(p f_i)), f32 [rows][rot/2][2], 16-byte aligned, for
+ * p < rows and i < rot/2: computed in f64, rounded once.  Made once and kept; the other
+ * calls read it.  scaling NULL: WQ_ROPE_PLAIN with magnitude 1.
+ * Errors: WQ_ERR_INVALID_ARG for rows <= 0, rot <= 0 or odd or above 256, base <= 1 or not
+ * finite, a null or misaligned table, a bad scaling (for NTK also rot < 4). */
+WQ_API wq_status wq_rope_table(int rows, int rot, double base, const wq_rope_scaling *scaling,
+                               float *table, wq_stream_t stream);
+
+/*
+ * Rotate the first `rot` of the head_dim values of each head; the others are copied:
+ *   half layout:        out[i] = x[i] c_i - x[i+rot/2] s_i,  out[i+rot/2] = x[i] s_i + x[i+rot/2] c_i
+ *   WQ_ROPE_INTERLEAVED: the same with the pair (2i, 2i+1) in place of (i, i+rot/2)
+ * with (c_i, s_i) = table[pos[t]][i], i < rot/2.  WQ_ROPE_TRANSPOSE puts -s_i in place of
+ * s_i: with out's gradient as x it gives x's gradient.
+ * x, out: f32, row t at x + t * x_stride (in floats), its heads one after another; out may
+ * equal x with the same stride, else they do not overlap.  Any 4-byte aligned address and
+ * stride from n_heads * head_dim to 2^26 are taken; 16-byte multiples are faster.
+ * pos: int32 [n].  A position outside [0, table_rows) leaves its row of out unwritten and
+ * records WQ_ERR_BAD_INDEX in the device status.
+ * rot = 0 copies; table and pos may then be NULL.
+ * Errors: WQ_ERR_INVALID_ARG for n, n_heads <= 0, head_dim <= 0 or above 256, rot < 0, odd or
+ * above head_dim, null x or out, a null or (16-byte) misaligned table, null pos or
+ * table_rows <= 0 with rot > 0, x or out not 4-byte aligned, strides too small,
+ * unknown flags. */
+WQ_API wq_status wq_rope(int n, int n_heads, int head_dim, int rot, unsigned flags, const float *x,
+                         int64_t x_stride, const int32_t *pos, const float *table, int table_rows,
+                         float *out, int64_t out_stride, wq_stream_t stream);
+
+/*
+ * A paged key-value cache of one layer, described for a call (the struct is read on the
+ * host and not kept).  Element i of head h of the row r of page p is at
+ *   p * page_stride + h * head_stride + r * token_stride + i
+ * in both pools, so that [page][head][row][dim] and [page][row][head][dim] are both taken.
+ * Sequence s's slot j is row j % page_size of page page_table[s][j / page_size].
+ * Restrictions: dtype WQ_BF16, WQ_F16 or WQ_F32; head_dim % 8 == 0, at most 256; k and v
+ * 16-byte aligned, the strides multiples of 16 bytes and >= head_dim.
+ * Pages of different sequences may be shared as long as nothing writes them.
+ */
+typedef struct {
+    void *k, *v;
+    int32_t dtype;
+    int32_t n_pages, page_size;
+    int32_t n_heads, head_dim; /* kv heads */
+    int32_t reserved;          /* 0 */
+    int64_t page_stride, head_stride, token_stride; /* in elements */
+} wq_kv_cache;
+
+/*
+ * Append tokens to the cache: for t < n_tok, q_out[t] = R(pos[t]) q[t] (h_q heads, f32), and
+ * into slot slot[t] of sequence seq[t] R(pos[t]) k[t] and v[t] (cache->n_heads heads),
+ * each rounded once to the cache's type.  The rotation is wq_rope's (rot, flags, table).
+ * q, k, v: f32, row t at x + t * stride, e.g. the three parts of one fused projection's
+ * rows.  h_q = 0: no queries (q and q_out may be NULL).  q_out may equal q with the same
+ * stride.
+ * seq: int32 [n_tok], or NULL: token t is of sequence t.  slot: int32 [n_tok]; a token with a
+ * negative slot is padding: nothing is written for it.  Two tokens of a call may not
+ * have the same slot.  page_table: int32 [n_seq][max_pages].
+ * acc, slot_pos (each may be NULL): [n_seq][kv heads][acc_stride], the slots' accumulated
+ * attention weights (set to 0) and their tokens' positions (set to pos[t]), for
+ * wq_attn_paged and wq_kv_evict.
+ * A position, sequence, slot or page out of range leaves all of its token's outputs
+ * unwritten and records WQ_ERR_BAD_INDEX in the device status.
+ * Errors: as wq_rope and for the cache's restrictions; WQ_ERR_INVALID_ARG also for
+ * n_seq, max_pages <= 0, max_pages * page_size above 2^31 - 1, null k, v, slot or
+ * page_table, n_seq < n_tok with a null seq, acc or slot_pos with
+ * acc_stride < 1, a null pos with slot_pos. */
+WQ_API wq_status wq_kv_append(const wq_kv_cache *cache, int n_tok, int h_q, int rot,
+                              unsigned flags, const float *q, int64_t q_stride, const float *k,
+                              int64_t k_stride, const float *v, int64_t v_stride,
+                              const int32_t *pos, const float *table, int table_rows, int n_seq,
+                              const int32_t *seq, const int32_t *slot, const int32_t *page_table,
+                              int max_pages, float *q_out, int64_t q_out_stride, float *acc,
+                              int32_t *slot_pos, int64_t acc_stride, wq_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over its live slots j < lens[s]:
+ *   x_j = scale q . k_j + mask[s][j],   p = softmax(x),   out = sum_j p_j v_j,
+ *   lse = ln sum_j exp(x_j),
+ * for each of h_q query heads; query head h reads kv head h / (h_q / kv heads).
+ * window > 0: only the last `window` live slots (by slot number) take part.
+ * mask: f32 [n_seq][mask_stride] or NULL, added to the scores.  A slot with a mask of -inf takes
+ * no part, whatever its k and v hold; slots at or beyond lens[s], or before the window,
+ * are not read.  A mask of the type's lowest value is a number like another.
+ * Where nothing takes part (lens[s] <= 0, all masked) out is 0 and lse is -inf.
+ * q, out: f32 [n_seq] rows of h_q heads with strides in floats; lse: f32 [n_seq][h_q] or NULL.
+ * acc_out (NULL: not wanted): f32 [n_seq][kv heads][acc_stride]: for j < lens[s]
+ *   acc_out[s][g][j] = acc_in[s][g][j] + the sum of p_j over the query heads of g;
+ * acc_in NULL reads as 0 and may equal acc_out.  Slots at or beyond lens[s] are not
+ * written.
+ * A length above max_pages * page_size (or acc_stride, mask_stride) is cut to it, and a page
+ * out of range that holds live slots leaves them out; both record WQ_ERR_BAD_INDEX in the
+ * device status.
+ * workspace: at least wq_attn_paged_workspace_bytes(cache, n_seq, h_q, max_pages, acc_out !=
+ * NULL) bytes of device memory, 256-byte aligned, overlapping no other argument; it is
+ * overwritten.  It may be NULL when that is 0.
+ * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, h_q, max_pages <= 0, h_q not a
+ * multiple of the kv heads, window < 0, a scale that is not finite, null q, page_table,
+ * lens or out, acc_in without acc_out, q or out not 16-byte aligned or with a stride below
+ * h_q * head_dim or not a multiple of 4, a stride < 1 of a mask or acc that is given,
+ * max_pages * page_size above 2^31 - 1, a missing, misaligned or small workspace. */
+WQ_API wq_status wq_attn_paged(const wq_kv_cache *cache, int n_seq, int h_q, float scale,
+                               int window, const float *q, int64_t q_stride,
+                               const int32_t *page_table, int max_pages, const int32_t *lens,
+                               const float *mask, int64_t mask_stride, float *out,
+                               int64_t out_stride, float *lse, const float *acc_in,
+                               float *acc_out, int64_t acc_stride, void *workspace,
+                               size_t workspace_bytes, wq_stream_t stream);
+
+/* Workspace bytes of wq_attn_paged; 0 for invalid arguments. */
+WQ_API size_t wq_attn_paged_workspace_bytes(const wq_kv_cache *cache, int n_seq, int h_q,
+                                            int max_pages, int with_acc);
+
+/*
+ * Cut each sequence that has more than `keep` live slots to `keep`, separately in each kv
+ * head: the slots whose position is below `sinks` or at least seen[s] - recent stay, and of
+ * the others those of the largest accumulated weight acc; of equal weights the lower
+ * slot stays.  A NaN counts as the least weight.  The slots that stay below `keep` stay
+ * where they are; the i-th (by slot) that stays beyond it moves into the i-th slot below it
+ * that goes: its k, v, weight and position.
+ *   lens_out[s] = min(lens[s], keep); acc_out, pos_out [n_seq][kv heads][acc_stride]: the
+ * weights and positions of the slots below lens_out[s]; the others are not written.
+ * acc_out may equal acc, pos_out slot_pos, lens_out lens.  Sequences within the budget
+ * keep their slots (their acc_out, pos_out and lens_out are written).
+ * seen: int32 [n_seq], the tokens that the sequence has had (the newest position + 1).
+ * If more than `keep` slots are held by sinks and recent, the lower slots of those stay.
+ * Sequences may not share pages that this call writes.
+ * A length above max_pages * page_size or acc_stride is cut to it, and a page out of range
+ * is neither read nor written; both record WQ_ERR_BAD_INDEX in the device status.
+ * workspace: as wq_attn_paged's, of wq_kv_evict_workspace_bytes(...) bytes.
+ * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, max_pages, keep <= 0, sinks or
+ * recent < 0, sinks + recent > keep, null page_table, lens, seen, acc, slot_pos, acc_out,
+ * pos_out or lens_out, acc_stride < 1, max_pages * page_size above 2^31 - 1, a missing,
+ * misaligned or small workspace. */
+WQ_API wq_status wq_kv_evict(const wq_kv_cache *cache, int n_seq, const int32_t *page_table,
+                             int max_pages, const int32_t *lens, const int32_t *seen, int keep,
+                             int sinks, int recent, const float *acc, const int32_t *slot_pos,
+                             float *acc_out, int32_t *pos_out, int64_t acc_stride,
+                             int32_t *lens_out, void *workspace, size_t workspace_bytes,
+                             wq_stream_t stream);
+
+/* Workspace bytes of wq_kv_evict; 0 for invalid arguments. */
+WQ_API size_t wq_kv_evict_workspace_bytes(const wq_kv_cache *cache, int n_seq, int max_pages,
+                                          int keep);
 
 /* Synchronises `stream`, then returns and clears the current device's sticky
  * status word: WQ_OK, WQ_ERR_DEVICE_TIMEOUT, WQ_ERR_BAD_EXPERT or
