@@ -146,6 +146,8 @@ def _open(path: str):
 def load():
     """The process-wide libwq handle (raises if the library has not been built)."""
     global _lib
+    if _lib is not None:  # set once, under the lock
+        return _lib
     with _lock:
         if _lib is None:
             _lib = _open(LIB_PATH)
@@ -160,10 +162,26 @@ def _p(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream of the current device as a cudaStream_t."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        get, device = (getattr(torch._C, name, None)
+                       for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        # The raw getter takes 0.1 us where a Stream object takes 2.8 us on the host.
+        _raw_stream = (lambda: get(device())) if get and device else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

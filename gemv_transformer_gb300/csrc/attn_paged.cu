@@ -9,72 +9,89 @@
 // What bounds it: every live slot's k and v are read once and used group times (4 group
 // operations per 2 bytes of a bf16 cache), so the cache's bytes set the floor.
 //
-// Products: eight query heads of a kv head fill the 16 rows of mma.sync m16n8k8 (tf32) as
-// q = hi + lo with 11 bits each in rows g and g + 8 of a fragment; bf16 and f16 keys and
-// values are exact in tf32, f32 ones are split in the same way (two products).  The
-// weights p enter the second product as hi + lo too.  So every product is within 2^-22 of
-// exact, as everywhere in this library; 16-bit operands alone would leave 2^-9.  The
-// tensor core truncates when it accumulates (measured: 1 + 0.92 ulp added 1000 times
-// stays 1), so no accumulation is longer than head_dim / 16 steps of q.k, and every 16
-// slots' p.v is added to o by an f32 FMA that rescales it anyway.  Rate needed at the
-// memory floor: 2 x 300 TFLOP/s measured tf32 mma.sync is 2.9 times what eight heads of a
-// bf16 cache take.
+// Products: the heads of a group are the rows of mma.sync operands, eight heads to a
+// fragment, and an f32 value is split into terms of the operand's type that are exact
+// together, the first two in rows g and g + 8 of one product:
+//   bf16 cache  q and p as three bf16 terms (24 bits): a second product has the third;
+//   f16 cache   two f16 terms (22 bits) of q scaled by a power of two per head to a
+//               largest value near 2^10, and of 2^12 p, so that no term is subnormal;
+//   f32 cache   two tf32 terms (22 bits) of q, p, k and v.
+// 16-bit operands alone would leave 2^-9.  The tensor core truncates when it
+// accumulates (measured: 1 + 0.92 ulp added 1000 times stays 1), so no accumulation is
+// longer than head_dim / 16 steps of q.k, and every tile's p.v is added to o by an f32
+// FMA that rescales it anyway.
 //
-// Dims may be summed in any order, so a lane takes 16 bytes of a key's row (its own four or
-// eight dims) as operands as they are, with q laid out to match; p's accumulator
-// fragment is the next product's operand without a move.  No shuffles but the maxima.
+// p's accumulator fragment is the next product's operand without a move.
 //
-// Loads: each warp keeps a ring of kStages tiles of KT slots (k and v) in flight by cp.async,
-// 96 KB per CTA and two CTAs per SM, and waits for no other warp: a CTA's warps meet
-// only where a row (sequence, kv head, up to 16 query heads) ends.  A slot that takes no
-// part (beyond the length, masked by -inf, in a page out of range) is filled with zeros in
-// shared memory and not read.
+// Loads: each warp keeps a ring of tiles of KT slots (k and v) in flight by cp.async and
+// waits for no other warp: a CTA's warps meet only where a row (sequence, kv head, up to
+// 16 query heads) ends.  A slot that takes no part (beyond the length, masked by -inf, in
+// a page out of range) is filled with zeros in shared memory and not read.
 //
 // Work: the rows' tiles, one row after another, are dealt out in equal contiguous ranges to
 // a fixed grid, whatever the lengths; a CTA finds its range from the lengths.  A row within
-// one CTA is written by it, the parts of the others are joined by attn_join_kernel.
+// one CTA is written by it, the parts of the others are joined by attn_join_kernel.  Small
+// calls give each row a cluster of CTAs that join their parts through shared memory.
+#include <cooperative_groups.h>
+
 #include "kv_internal.h"
 #include "wq_device.cuh"
 
 namespace wq {
 namespace {
 
-constexpr int kStages = 3;
-constexpr int kMaxCtas = 304;  // two on each of 152 SMs
+namespace cg = cooperative_groups;
+
+constexpr int kMaxCtas = 456;  // three on each of 152 SMs
 
 template <int DT, int DP, int HT> struct Shape {
-    static constexpr int kEb = DT == kF32 ? 4 : 2;     // bytes of an element
+    static constexpr bool k16 = DT != kF32;
+    static constexpr int kEb = k16 ? 2 : 4;            // bytes of an element
     static constexpr int kRow = DP * kEb;              // bytes of a slot's row in the ring
     static constexpr int kEpc = 16 / kEb;              // elements of a 16-byte chunk
     static constexpr int kChunks = kRow / 16;
-    static constexpr int KT = kRow <= 256 ? 16 : 8;    // slots of a warp's tile
+    static constexpr int KT = k16 ? 16 : 8;            // slots of a warp's tile
     static constexpr int NT = KT / 8;
-    static constexpr int W = kRow == 128 ? 8 : kRow == 1024 ? 2 : 4;  // warps
+    static constexpr int W = DP == 256 ? 3 : 4;        // warps
+    static constexpr int kCtas = HT * DP == 256 ? 2 : 3;  // per SM
     static constexpr int kTile = 2 * KT * kRow;        // bytes: k, then v
+    static constexpr int kStages = DP == 64 ? 4 : HT * DP == 256 && DP == 128 ? 3 : 2;
     static constexpr int BT = W * KT;                  // slots of a CTA's tile
     static constexpr int kHeads = HT * 8;              // query heads of a row
-    static constexpr int kQ = W * kStages * kTile;                 // q fragments
-    static constexpr int kBias = kQ + HT * DP * 64;                // [W][kStages][KT]
-    static constexpr int kL = kBias + W * kStages * KT * 4;        // [W][kHeads]
-    static constexpr int kM = kL + W * kHeads * 4;                 // [W][kHeads], or in kBias
-    static constexpr bool kMInBias = KT >= kHeads;
-    static constexpr int kSmem = kM + (kMInBias ? 0 : W * kHeads * 4);
-    static constexpr int kPart = kHeads * (DP + 2);    // floats of a part: m, l, o
+    static constexpr bool kQReg = k16 && HT * DP <= 128;  // q's fragments in registers
+    static constexpr int kStep = k16 ? 16 : 8;         // dims of a product step
+    static constexpr int kSteps = DP / kStep;
+    static constexpr int kQWords = DT == kBF16 ? 6 : 4;   // registers of a step's fragment
+    static constexpr int kQ = W * kStages * kTile;     // q fragments, unless in registers
+    static constexpr int kQBytes = kQReg ? 0 : HT * kSteps * 32 * kQWords * 4;
+    static constexpr int kOff = kQ + kQBytes;                      // [W][KT] row offsets
+    static constexpr int kBias = kOff + W * KT * 8;                // [W][kStages][KT]
+    static constexpr int kM = kBias + W * kStages * KT * 4;        // [W][kHeads], then factors
+    static constexpr int kL = kM + W * kHeads * 4;                 // [W][kHeads]
+    static constexpr int kTop = kL + W * kHeads * 4;               // [kHeads]
+    static constexpr int kSum = kTop + kHeads * 4;                 // [kHeads]
+    static constexpr int kScale = kSum + kHeads * 4;               // [kHeads], f16's powers of two
+    static constexpr int kSmem = kScale + kHeads * 4;
+    static constexpr int kPart = kHeads * (DP + 2);    // floats of a part: m, l, o (16-byte rows)
     static_assert(kHeads * DP * 4 <= kTile, "a warp's o fits the tile just used");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
 };
+
+__device__ __forceinline__ long long div_any(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 
 // The schedule that every CTA derives from the lengths: rows of sequence s have
 // tiles(s) tiles each, never 0 (an empty row is written too).
 struct Sched {
-    int rows;            // rows per sequence: kv heads x head tiles
-    long long total;     // tiles of all rows
-    __device__ __forceinline__ long long start(int b, int grid) const {
-        const long long q = total / grid, r = total - q * grid;
-        return b * q + min((long long)b, r);
-    }
-    __device__ __forceinline__ int owner(long long t, int grid) const {
-        const long long q = total / grid, r = total - q * grid, cut = r * (q + 1);
-        return (int)(t < cut ? t / (q + 1) : r + (t - cut) / q);
+    long long total, q, r;  // tiles of all rows; total / grid and the rest
+    __device__ __forceinline__ Sched(long long t, int grid)
+        : total(t), q(div_any(t, grid)), r(t - q * grid) {}
+    __device__ __forceinline__ long long start(int b) const { return b * q + min((long long)b, r); }
+    __device__ __forceinline__ int owner(long long t) const {
+        const long long cut = r * (q + 1);
+        return (int)(t < cut ? div_any(t, q + 1) : r + div_any(t - cut, q));
     }
 };
 
@@ -90,16 +107,45 @@ __device__ __forceinline__ float exp_diff(float x, float m) {
     return x == -INFINITY ? 0.f : expf(x - m);
 }
 
+// ------------------------------------------------------------------- terms --
+
 __device__ __forceinline__ uint32_t tf32(float x) {
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
 // x - hi, the part that hi leaves; an infinity is left to hi.
-__device__ __forceinline__ uint32_t tf32_rest(float x, uint32_t hi) {
-    const float h = __uint_as_float(hi);
-    return __float_as_uint(fabsf(h) == INFINITY ? 0.f : x - h);
+__device__ __forceinline__ float rest(float x, float hi) {
+    return fabsf(hi) == INFINITY ? 0.f : x - hi;
 }
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// The terms of a pair, packed: t[0] + t[1] (+ t[2]) = (x, y).  `finite`: no infinities.
+template <int DT, bool finite>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3]) {
+    if (DT == kBF16) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            t[i] = bf16x2(x, y);
+            const float hx = bf16_lo(t[i]), hy = bf16_hi(t[i]);
+            x = finite ? x - hx : rest(x, hx);
+            y = finite ? y - hy : rest(y, hy);
+        }
+    } else {
+        t[0] = f16x2(x, y);
+        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&t[0]));
+        t[1] = finite ? f16x2(x - h.x, y - h.y) : f16x2(rest(x, h.x), rest(y, h.y));
+        t[2] = 0u;
+    }
+}
+
+// ---------------------------------------------------------------- products --
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -109,6 +155,30 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+template <int DT>
+__device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (DT == kBF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c += a * b with b in f32, split into its high 11 bits and the rest.
+__device__ __forceinline__ void mma_f32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    const uint32_t h0 = b0 & 0xFFFFE000u, h1 = b1 & 0xFFFFE000u;
+    mma_tf32(c, a, h0, h1);
+    mma_tf32(c, a, __float_as_uint(rest(__uint_as_float(b0), __uint_as_float(h0))),
+             __float_as_uint(rest(__uint_as_float(b1), __uint_as_float(h1))));
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
@@ -116,6 +186,22 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+// Four 8x8 matrices of 16-bit elements, their rows at the lanes' addresses.
+template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
 }
 
 // 16 bytes global -> shared, or 16 zero bytes.
@@ -131,44 +217,14 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Element pair j of a chunk as f32 bits (16-bit types: the two halves of word j).
-template <int DT> __device__ __forceinline__ void pair_of(const uint4 &v, int j, uint32_t &a,
-                                                          uint32_t &b) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if (DT == kBF16) {
-        a = w[j] << 16;
-        b = w[j] & 0xFFFF0000u;
-    } else if (DT == kF16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-        a = __float_as_uint(f.x);
-        b = __float_as_uint(f.y);
-    } else {
-        a = w[2 * j];
-        b = w[2 * j + 1];
-    }
+// Chunk ch of slot r lies at chunk ch ^ swizzle of the slot's row.  16-bit types: the
+// eight rows of a matrix at eight bank groups.  f32: a quarter warp reads two keys' four
+// chunks, or four values' two.
+template <int DT> __device__ __forceinline__ int swizzle_k(int r) {
+    return DT == kF32 ? (r & 1) << 2 : r & 7;
 }
-// Element e of a chunk.
-template <int DT> __device__ __forceinline__ uint32_t element_of(const uint4 &v, int e) {
-    if (DT == kF32) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        return w[e];
-    }
-    uint32_t a, b;
-    pair_of<DT>(v, e >> 1, a, b);
-    return e & 1 ? b : a;
-}
-
-// d += a * b with b exact in tf32, or in f32 (split: its high 11 bits and the rest).
-template <int DT>
-__device__ __forceinline__ void mma_kv(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                       uint32_t b1) {
-    if (DT == kF32) {
-        const uint32_t h0 = b0 & 0xFFFFE000u, h1 = b1 & 0xFFFFE000u;
-        mma_tf32(c, a, h0, h1);
-        mma_tf32(c, a, tf32_rest(__uint_as_float(b0), h0), tf32_rest(__uint_as_float(b1), h1));
-    } else {
-        mma_tf32(c, a, b0, b1);
-    }
+template <int DT> __device__ __forceinline__ int swizzle_v(int r) {
+    return DT == kF32 ? r & 6 : r & 7;
 }
 
 // A CTA's place in the rows' tiles.
@@ -208,79 +264,91 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part
     return r;
 }
 
-template <int DT, int DP, int HT>
-__global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
+// CL: a cluster of CTAs per row, no workspace parts and no second launch.
+template <int DT, int DP, int HT, bool CL>
+__global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::kCtas)
     attn_kernel(AttnArgs a, KvView kv, int head_tiles) {
     using S = Shape<DT, DP, HT>;
-    constexpr int NT = S::NT, KT = S::KT, W = S::W, kThreads = W * 32;
+    constexpr int NT = S::NT, KT = S::KT, W = S::W, kThreads = W * 32, kStages = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long s_scan[W], s_total;
-    __shared__ int s_seq;
-    __shared__ long long s_before;
-    pdl_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    pdl_launch();
     pdl_wait();
     const Room room = room_of(a.workspace, a.n_seq, a.h_q, S::kPart);
     const int rows = kv.n_heads * head_tiles;
 
-    // Tiles before each thread's share of the sequences, and in all.
-    auto tiles_of = [&](int s) {
-        const Span p = span_of(a, s);
-        return max(1, (p.len - p.first + S::BT - 1) / S::BT);
-    };
-    const int share = (a.n_seq + kThreads - 1) / kThreads;
-    const int s0 = min(a.n_seq, (int)threadIdx.x * share), s1 = min(a.n_seq, s0 + share);
-    long long mine = 0;
-    for (int s = s0; s < s1; ++s) {
-        mine += tiles_of(s);
-        if (blockIdx.x == 0 && __ldg(a.lens + s) > a.n_slots) record_status(a.status, kStBadIndex);
-    }
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long before = x - mine, total = 0;
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-    }
-    Sched sched{rows, total * rows};
-    const long long t0 = sched.start(blockIdx.x, gridDim.x),
-                    t1 = sched.start(blockIdx.x + 1, gridDim.x);
-    if (blockIdx.x == 0) {
-        long long at = before;
-        for (int s = s0; s < s1; ++s) {
-            room.before[s] = at;
-            at += tiles_of(s);
-        }
-        if (threadIdx.x == 0) room.before[a.n_seq] = total;
-    }
-    if (t0 >= t1) return;
-    if (t0 >= before * rows && t0 < (before + mine) * rows) {
-        int s = s0;
-        for (int n; t0 >= (before + (n = tiles_of(s))) * rows; ++s) before += n;
-        s_seq = s;
-        s_before = before;
-    }
-    __syncthreads();
     Cursor use;
-    use.s = s_seq;
-    use.load(a, S::BT);
-    {
+    long long left;  // tiles of this CTA
+    if (CL) {
+        const int size = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
+        const int id = blockIdx.x / size;
+        use.s = id / rows;
+        use.row = id - use.s * rows;
+        use.load(a, S::BT);
+        use.tile = use.tiles * rank / size;
+        left = use.tiles * (rank + 1) / size - use.tile;
+        if (threadIdx.x == 0 && rank == 0 && use.row == 0 && __ldg(a.lens + use.s) > a.n_slots)
+            record_status(a.status, kStBadIndex);
+    } else {
+        // Tiles before each thread's share of the sequences, and in all.
+        __shared__ long long s_scan[W], s_before;
+        __shared__ int s_seq;
+        auto tiles_of = [&](int s) {
+            const Span p = span_of(a, s);
+            return max(1, (p.len - p.first + S::BT - 1) / S::BT);
+        };
+        const int share = (a.n_seq + kThreads - 1) / kThreads;
+        const int s0 = min(a.n_seq, (int)threadIdx.x * share), s1 = min(a.n_seq, s0 + share);
+        long long mine = 0;
+        for (int s = s0; s < s1; ++s) {
+            mine += tiles_of(s);
+            if (blockIdx.x == 0 && __ldg(a.lens + s) > a.n_slots)
+                record_status(a.status, kStBadIndex);
+        }
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_scan[warp] = x;
+        __syncthreads();
+        long long before = x - mine, total = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
+        }
+        const Sched sched(total * rows, gridDim.x);
+        const long long t0 = sched.start(blockIdx.x), t1 = sched.start(blockIdx.x + 1);
+        if (blockIdx.x == 0) {
+            long long at = before;
+            for (int s = s0; s < s1; ++s) {
+                room.before[s] = at;
+                at += tiles_of(s);
+            }
+            if (threadIdx.x == 0) room.before[a.n_seq] = total;
+        }
+        if (t0 >= t1) return;
+        if (t0 >= before * rows && t0 < (before + mine) * rows) {
+            int s = s0;
+            for (int n; t0 >= (before + (n = tiles_of(s))) * rows; ++s) before += n;
+            s_seq = s;
+            s_before = before;
+        }
+        __syncthreads();
+        use.s = s_seq;
+        use.load(a, S::BT);
         const long long in = t0 - s_before * rows;
-        use.row = (int)(in / use.tiles);
+        use.row = (int)div_any(in, use.tiles);
         use.tile = (int)(in - (long long)use.row * use.tiles);
+        left = t1 - t0;
     }
     Cursor fetch = use;  // the tile whose page numbers are asked for next
-    long long left = t1 - t0, to_fetch = left;
+    long long to_fetch = left;
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * S::kTile;
-    const uint32_t qf = smem_addr(smem) + S::kQ;
     float *bias = reinterpret_cast<float *>(smem + S::kBias) + warp * kStages * KT;
+    long long *offs = reinterpret_cast<long long *>(smem + S::kOff) + warp * KT;
     const int live_chunks = kv.head_dim / S::kEpc;
 
     // Page numbers are asked for one tile ahead of the loads that need them.
@@ -314,41 +382,110 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
                      (long long)ask_in * kv.token_stride;
             }
         }
-        if (lane < KT) bias[stage * KT + lane] = b;
+        if (lane < KT) {
+            bias[stage * KT + lane] = b;
+            offs[lane] = at;
+        }
+        __syncwarp();
         const uint32_t base = ring + stage * S::kTile;
 #pragma unroll
         for (int i = 0; i < KT * S::kChunks / 32; ++i) {
             const int idx = i * 32 + lane, key = idx / S::kChunks, ch = idx % S::kChunks;
-            const long long from = __shfl_sync(0xFFFFFFFFu, at, key);
+            const long long from = offs[key];
             const bool live = from >= 0 && ch < live_chunks;
             const long long off = live ? from + ch * 16 : 0;
-            cp_async16(base + key * S::kRow + ((ch ^ ((key & 1) << 2)) << 4), kv.k + off, live);
-            cp_async16(base + KT * S::kRow + key * S::kRow + ((ch ^ (key & 6)) << 4), kv.v + off,
-                       live);
+            const uint32_t dst = base + key * S::kRow;
+            cp_async16(dst + ((ch ^ swizzle_k<DT>(key)) << 4), kv.k + off, live);
+            cp_async16(dst + KT * S::kRow + ((ch ^ swizzle_v<DT>(key)) << 4), kv.v + off, live);
         }
+        __syncwarp();  // offs is free
     };
 
-    // The row's query heads, scaled, as the first product's operand.
+    // The row's query heads, scaled, as the first product's operand: rows g and g + 8 of a
+    // fragment are the first two terms of head g.  In registers where they fit: every warp
+    // makes its own.  f16: `back` undoes the power of two that brings q near 2^10.
+    uint32_t qr[S::kQReg ? HT * S::kSteps : 1][S::kQWords];
+    float back[HT];
     auto load_q = [&](const Cursor &at) {
         const int h = at.row / head_tiles, ht0 = (at.row - h * head_tiles) * S::kHeads;
-        const float *q = a.q + at.s * a.q_stride + ((long long)h * a.group + ht0) * kv.head_dim;
-        for (int i = threadIdx.x; i < HT * DP / 8 * 32; i += kThreads) {
-            const int l = i & 31, ks = (i >> 5) % (DP / 8), ht = (i >> 5) / (DP / 8);
-            const int head = ht * 8 + (l >> 2);
-            const int dim = S::kEpc * (4 * (ks / (S::kEpc / 2)) + (l & 3)) +
-                            2 * (ks % (S::kEpc / 2));
+        const float *q0 = a.q + at.s * a.q_stride + ((long long)h * a.group + ht0) * kv.head_dim;
+        auto q2 = [&](int head, int dim) {
             float2 v = make_float2(0.f, 0.f);
             if (ht0 + head < a.group && dim < kv.head_dim)
-                v = *reinterpret_cast<const float2 *>(q + head * kv.head_dim + dim);
+                v = *reinterpret_cast<const float2 *>(q0 + head * kv.head_dim + dim);
             v.x *= a.scale;
             v.y *= a.scale;
-            uint4 f;
-            f.x = tf32(v.x);
-            f.y = tf32(__uint_as_float(tf32_rest(v.x, f.x)));
-            f.z = tf32(v.y);
-            f.w = tf32(__uint_as_float(tf32_rest(v.y, f.z)));
-            *reinterpret_cast<uint4 *>(smem + S::kQ + i * 16) = f;
+            return v;
+        };
+        if (!S::k16) {  // tf32: lane's dims are those of its 16-byte chunks of a key
+            for (int i = threadIdx.x; i < HT * S::kSteps * 32; i += kThreads) {
+                const int l = i & 31, ks = (i >> 5) % S::kSteps, ht = (i >> 5) / S::kSteps;
+                const float2 v = q2(ht * 8 + (l >> 2), 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1));
+                uint4 f;
+                f.x = tf32(v.x);
+                f.y = tf32(rest(v.x, __uint_as_float(f.x)));
+                f.z = tf32(v.y);
+                f.w = tf32(rest(v.y, __uint_as_float(f.z)));
+                *reinterpret_cast<uint4 *>(smem + S::kQ + i * 16) = f;
+            }
         }
+#pragma unroll
+        for (int ht = 0; ht < (S::k16 ? HT : 0); ++ht) {
+            if (!S::kQReg && ht != warp) continue;  // HT <= W
+            float up = 1.f;
+            if (DT == kF16) {
+                float top = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < S::kSteps; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = q2(ht * 8 + g, ks * 16 + i * 8 + 2 * c);
+                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                int e = 0;
+                if (top > 0.f && top < INFINITY) e = max(-100, ilogbf(top));
+                up = exp2f((float)(10 - e));
+                const float down = exp2f((float)(e - 10));
+                if (S::kQReg)
+                    back[ht] = down;
+                else if (c == 0)
+                    reinterpret_cast<float *>(smem + S::kScale)[ht * 8 + g] = down;
+            }
+#pragma unroll
+            for (int ks = 0; ks < S::kSteps; ++ks) {
+                uint32_t t0[3], t1[3];
+                const float2 x = q2(ht * 8 + g, ks * 16 + 2 * c);
+                const float2 y = q2(ht * 8 + g, ks * 16 + 8 + 2 * c);
+                split2<DT, false>(x.x * up, x.y * up, t0);
+                split2<DT, false>(y.x * up, y.y * up, t1);
+                const int f = ht * S::kSteps + ks;
+                if (S::kQReg) {
+                    qr[S::kQReg ? f : 0][0] = t0[0];
+                    qr[S::kQReg ? f : 0][1] = t0[1];
+                    qr[S::kQReg ? f : 0][2] = t1[0];
+                    qr[S::kQReg ? f : 0][3] = t1[1];
+                    if (DT == kBF16) {
+                        qr[S::kQReg ? f : 0][4 % S::kQWords] = t0[2];
+                        qr[S::kQReg ? f : 0][5 % S::kQWords] = t1[2];
+                    }
+                } else {
+                    *reinterpret_cast<uint4 *>(smem + S::kQ + (f * 32 + lane) * 16) =
+                        make_uint4(t0[0], t0[1], t1[0], t1[1]);
+                    if (DT == kBF16)
+                        *reinterpret_cast<uint2 *>(smem + S::kQ + HT * S::kSteps * 512 +
+                                                   (f * 32 + lane) * 8) = make_uint2(t0[2], t1[2]);
+                }
+            }
+        }
+    };
+    // After the barrier that follows load_q.
+    auto take_scales = [&]() {
+        if (DT == kF16 && !S::kQReg)
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+                back[h] = reinterpret_cast<const float *>(smem + S::kScale)[h * 8 + g];
     };
 
     ask();
@@ -360,55 +497,81 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
     }
     load_q(use);
     __syncthreads();
+    take_scales();
 
-    constexpr int OI = S::kChunks / 8;  // chunk groups of v per lane
-    float o[HT][OI][S::kEpc][2], m[HT], l[HT];
+    constexpr int OI = DP / 8;  // 16-bit: o[i] = dims 8 i + 2 c, + 1; f32: see its loop
+    float o[HT][OI][2], m[HT], l[HT];
     auto clear = [&]() {
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             m[h] = -INFINITY;
             l[h] = 0.f;
 #pragma unroll
-            for (int i = 0; i < OI; ++i)
-#pragma unroll
-                for (int e = 0; e < S::kEpc; ++e) o[h][i][e][0] = o[h][i][e][1] = 0.f;
+            for (int i = 0; i < OI; ++i) o[h][i][0] = o[h][i][1] = 0.f;
         }
     };
     clear();
     bool whole = use.tile == 0;  // does this CTA have the row from its first tile
     bool leads = true;           // is this the CTA's first row
     int stage = 0;
-    for (; left > 0; --left) {
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
+    const int mat = lane >> 3, mrow = lane & 7;  // ldmatrix: this lane's matrix and row
+
+    // One tile: x = q.k, the softmax step, o = o corr + p.v.
+    auto step = [&]() {
         const uint32_t kb = ring + stage * S::kTile, vb = kb + KT * S::kRow;
         const float *bs = bias + stage * KT;
-
-        // x = q.k: rows g and g + 8 hold the high and low parts of head g.
         float sc[HT][NT][2][4] = {};
+        if (S::k16) {
+            const int key = (mat >> 1) * 8 + mrow;
+            const uint32_t at = kb + key * S::kRow;
 #pragma unroll
-        for (int i = 0; i < S::kChunks / 4; ++i) {
-            uint4 kk[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                kk[n] = lds128(kb + (n * 8 + g) * S::kRow + (((4 * i + c) ^ ((g & 1) << 2)) << 4));
-#pragma unroll
-            for (int j = 0; j < S::kEpc / 2; ++j) {
-                const int ks = i * (S::kEpc / 2) + j;
+            for (int ks = 0; ks < S::kSteps; ++ks) {
+                if (2 * ks >= live_chunks) break;
+                uint32_t kf[4];
+                ldmatrix4<false>(kf, at + (((2 * ks + (mat & 1)) ^ mrow) << 4));
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
-                    const uint4 qv = lds128(qf + (((h * DP / 8 + ks) * 32 + lane) << 4));
-                    const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
+                    uint32_t q[6];
+                    const int f = h * S::kSteps + ks;
+                    if (S::kQReg) {
+#pragma unroll
+                        for (int i = 0; i < S::kQWords; ++i) q[i] = qr[S::kQReg ? f : 0][i];
+                    } else {
+                        const uint32_t qa = smem_addr(smem) + S::kQ;
+                        const uint4 v = lds128(qa + (f * 32 + lane) * 16);
+                        q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+                        if (DT == kBF16) {
+                            const uint2 u = lds64(qa + HT * S::kSteps * 512 + (f * 32 + lane) * 8);
+                            q[4] = u.x, q[5] = u.y;
+                        }
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        uint32_t b0, b1;
-                        pair_of<DT>(kk[n], j, b0, b1);
-                        mma_kv<DT>(sc[h][n][ks & 1], qa, b0, b1);
+                        mma_16<DT>(sc[h][n][0], q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1]);
+                        if (DT == kBF16)
+                            mma_16<DT>(sc[h][n][1], q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1]);
                     }
                 }
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < S::kChunks / 4; ++i) {
+                if (4 * i >= live_chunks) break;
+                const uint4 v = lds128(kb + g * S::kRow + (((4 * i + c) ^ swizzle_k<DT>(g)) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        const uint4 f = lds128(smem_addr(smem) + S::kQ +
+                                               ((h * S::kSteps + 2 * i + j) * 32 + lane) * 16);
+                        const uint32_t q[4] = {f.x, f.y, f.z, f.w};
+                        mma_f32(sc[h][0][j], q, w[2 * j], w[2 * j + 1]);
+                    }
+            }
         }
-        uint32_t pa[HT][NT][4];
+        uint32_t pt[HT][2][3];  // 16-bit: the terms of p at slots 2c, 2c + 1 (+ 8)
+        uint32_t pf[HT][4];     // f32: p's fragment
         float corr[HT];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
@@ -417,8 +580,12 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
             for (int n = 0; n < NT; ++n) {
                 const float2 b = *reinterpret_cast<const float2 *>(bs + n * 8 + 2 * c);
                 const float(&v)[2][4] = sc[h][n];
-                const float x0 = (v[0][0] + v[1][0]) + (v[0][2] + v[1][2]);
-                const float x1 = (v[0][1] + v[1][1]) + (v[0][3] + v[1][3]);
+                float x0 = (v[0][0] + v[1][0]) + (v[0][2] + v[1][2]);
+                float x1 = (v[0][1] + v[1][1]) + (v[0][3] + v[1][3]);
+                if (DT == kF16) {
+                    x0 *= back[h];
+                    x1 *= back[h];
+                }
                 xs[n][0] = b.x == -INFINITY ? -INFINITY : x0 + b.x;
                 xs[n][1] = b.y == -INFINITY ? -INFINITY : x1 + b.y;
                 top = fmaxf(top, fmaxf(xs[n][0], xs[n][1]));
@@ -444,101 +611,177 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float p0 = exp_diff(xs[n][0], top), p1 = exp_diff(xs[n][1], top);
+                float p0 = exp_diff(xs[n][0], top), p1 = exp_diff(xs[n][1], top);
+                if (DT == kF16) {
+                    p0 *= 4096.f;
+                    p1 *= 4096.f;
+                }
                 sum += p0 + p1;
-                pa[h][n][0] = tf32(p0);
-                pa[h][n][1] = tf32(p0 - __uint_as_float(pa[h][n][0]));
-                pa[h][n][2] = tf32(p1);
-                pa[h][n][3] = tf32(p1 - __uint_as_float(pa[h][n][2]));
+                if (S::k16) {
+                    split2<DT, true>(p0, p1, pt[h][n]);
+                } else {
+                    pf[h][0] = tf32(p0);
+                    pf[h][1] = tf32(p0 - __uint_as_float(pf[h][0]));
+                    pf[h][2] = tf32(p1);
+                    pf[h][3] = tf32(p1 - __uint_as_float(pf[h][2]));
+                }
             }
             l[h] = l[h] * corr[h] + sum;
         }
-        // o = o corr + p.v
+        if (S::k16) {
+            const int key = (mat & 1) * 8 + mrow;
+            const uint32_t at = vb + key * S::kRow;
 #pragma unroll
-        for (int i = 0; i < OI; ++i) {
-            if (8 * i >= live_chunks) break;
-            uint4 v0[NT], v1[NT];
+            for (int i = 0; i < DP / 16; ++i) {
+                if (2 * i >= live_chunks) break;
+                uint32_t vf[4];
+                ldmatrix4<true>(vf, at + (((2 * i + (mat >> 1)) ^ mrow) << 4));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = n * 8 + 2 * c;  // r & 6 is the same for r + 1
-                const uint32_t at = vb + r * S::kRow + (((g + 8 * i) ^ (2 * c)) << 4);
-                v0[n] = lds128(at);
-                v1[n] = lds128(at + S::kRow);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        float t[4] = {};
+                        mma_16<DT>(t, pt[h][0][0], pt[h][0][1], pt[h][NT - 1][0],
+                                   pt[h][NT - 1][1], vf[2 * u], vf[2 * u + 1]);
+                        if (DT == kBF16)
+                            mma_16<DT>(t, pt[h][0][2], 0u, pt[h][NT - 1][2], 0u, vf[2 * u],
+                                       vf[2 * u + 1]);
+                        float(&to)[2] = o[h][2 * i + u];
+                        to[0] = to[0] * corr[h] + (t[0] + t[2]);
+                        to[1] = to[1] * corr[h] + (t[1] + t[3]);
+                    }
             }
+        } else {
+            // Column g of product e is dim 4 (g + 8 i) + e.
 #pragma unroll
-            for (int e = 0; e < S::kEpc; ++e)
+            for (int i = 0; i < S::kChunks / 8; ++i) {
+                if (8 * i >= live_chunks) break;
+                const uint32_t at = vb + 2 * c * S::kRow + (((g + 8 * i) ^ (2 * c)) << 4);
+                const uint4 v0 = lds128(at), v1 = lds128(at + S::kRow);
+                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    float t[4] = {};
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_kv<DT>(t, pa[h][n], element_of<DT>(v0[n], e), element_of<DT>(v1[n], e));
-                    o[h][i][e][0] = o[h][i][e][0] * corr[h] + (t[0] + t[2]);
-                    o[h][i][e][1] = o[h][i][e][1] * corr[h] + (t[1] + t[3]);
-                }
+                    for (int h = 0; h < HT; ++h) {
+                        float t[4] = {};
+                        mma_f32(t, pf[h], w0[e], w1[e]);
+                        float(&to)[2] = o[h][i * 4 + e];
+                        to[0] = to[0] * corr[h] + (t[0] + t[2]);
+                        to[1] = to[1] * corr[h] + (t[1] + t[3]);
+                    }
+            }
         }
+    };
 
-        const bool ends = use.tile + 1 == use.tiles, last = left == 1;
-        if (ends || last) {
-            // The warps' parts, through the tiles just used.
-            float *mo = reinterpret_cast<float *>(smem + (warp * kStages + stage) * S::kTile);
-            float *s_l = reinterpret_cast<float *>(smem + S::kL);
-            float *s_m = reinterpret_cast<float *>(smem + (S::kMInBias ? S::kBias : S::kM));
-            const int m_step = S::kMInBias ? kStages * KT : S::kHeads;
-            const int m_off = S::kMInBias ? stage * KT : 0;
-            __syncwarp();  // every lane has read the tile and its biases
+    float *s_m = reinterpret_cast<float *>(smem + S::kM);
+    float *s_l = reinterpret_cast<float *>(smem + S::kL);
+    float *s_top = reinterpret_cast<float *>(smem + S::kTop);
+    float *s_sum = reinterpret_cast<float *>(smem + S::kSum);
+    auto slot_of = [&](int w) {  // a warp's tile just used, for its o
+        return reinterpret_cast<float *>(smem + (w * kStages + stage) * S::kTile);
+    };
+    // The warps' parts through shared memory: afterwards s_m holds the warps' factors and
+    // s_top, s_sum the joined m and l of each head.
+    auto meet = [&]() {
+        __syncwarp();  // every lane has read the tile
+        float *mo = slot_of(warp);
 #pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                float sum = l[h];
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                if (c == 0) {
-                    s_l[warp * S::kHeads + h * 8 + g] = sum;
-                    s_m[warp * m_step + m_off + h * 8 + g] = m[h];
-                }
+        for (int h = 0; h < HT; ++h) {
+            float sum = l[h];
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            const float unit = DT == kF16 ? 1.f / 4096.f : 1.f;
+            if (c == 0) {
+                s_m[warp * S::kHeads + h * 8 + g] = m[h];
+                s_l[warp * S::kHeads + h * 8 + g] = sum * unit;
+            }
+            float *to = mo + (h * 8 + g) * DP;
+            if (S::k16) {
 #pragma unroll
                 for (int i = 0; i < OI; ++i)
+                    *reinterpret_cast<float2 *>(to + 8 * i + 2 * c) =
+                        make_float2(o[h][i][0] * unit, o[h][i][1] * unit);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < S::kEpc; ++e) {
-                        float *to = mo + (h * 8 + g) * DP + S::kEpc * (2 * c + 8 * i) + e;
-                        to[0] = o[h][i][e][0];
-                        to[S::kEpc] = o[h][i][e][1];
-                    }
+                for (int i = 0; i < S::kChunks / 8; ++i)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        *reinterpret_cast<float4 *>(to + 4 * (2 * c + v + 8 * i)) =
+                            make_float4(o[h][i * 4][v], o[h][i * 4 + 1][v], o[h][i * 4 + 2][v],
+                                        o[h][i * 4 + 3][v]);
             }
-            __syncthreads();
+        }
+        __syncthreads();
+        if (threadIdx.x < S::kHeads) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * S::kHeads + threadIdx.x]);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f = exp_diff(s_m[w * S::kHeads + threadIdx.x], top);
+                sum += f * s_l[w * S::kHeads + threadIdx.x];
+                s_m[w * S::kHeads + threadIdx.x] = f;
+            }
+            s_top[threadIdx.x] = top;
+            s_sum[threadIdx.x] = sum;
+        }
+        __syncthreads();
+    };
+    // Four dims of the joined o.
+    auto joined = [&](int head, int idx4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = s_m[w * S::kHeads + head];
+            const float4 x = reinterpret_cast<const float4 *>(slot_of(w))[idx4];
+            v.x += f * x.x;
+            v.y += f * x.y;
+            v.z += f * x.z;
+            v.w += f * x.w;
+        }
+        return v;
+    };
+    auto is_none = [](float top, float sum) { return top == -INFINITY && sum == 0.f; };
+    // out of four dims from dim `dim` of a head, and its lse at dim 0.
+    auto finish = [&](const Cursor &at, int head, int dim, float4 v, float top, float sum) {
+        const int hr = at.row / head_tiles;
+        const int in_group = (at.row - hr * head_tiles) * S::kHeads + head;
+        if (in_group >= a.group || dim >= kv.head_dim) return;
+        const int qh = hr * a.group + in_group;
+        const float inv = is_none(top, sum) ? 0.f : 1.f / sum;
+        *reinterpret_cast<float4 *>(a.out + at.s * a.out_stride + (long long)qh * kv.head_dim +
+                                    dim) =
+            is_none(top, sum) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        if (dim == 0) {
+            const float e = is_none(top, sum) ? -INFINITY : top + logf(sum);
+            const long long to = (long long)at.s * a.h_q + qh;
+            if (a.lse) a.lse[to] = e;
+            if (!CL && a.acc_out) room.lse[to] = e;
+        }
+    };
+
+    const int first_tile = use.tile;
+    for (; left > 0; --left) {
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        step();
+        const bool ends = use.tile + 1 == use.tiles, last = left == 1;
+        if (!CL && (ends || last)) {
+            meet();
             whole = whole && ends;
-            const int hr = use.row / head_tiles, head0 = (use.row - hr * head_tiles) * S::kHeads;
             float *part = room.parts + (2ll * blockIdx.x + (leads ? 0 : 1)) * S::kPart;
-            for (int idx = threadIdx.x; idx < S::kHeads * DP; idx += kThreads) {
-                const int head = idx / DP, dim = idx % DP;
-                float top = -INFINITY, sum = 0.f, v = 0.f;
-#pragma unroll
-                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * m_step + m_off + head]);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float f = exp_diff(s_m[w * m_step + m_off + head], top);
-                    sum += f * s_l[w * S::kHeads + head];
-                    v += f * reinterpret_cast<const float *>(
-                                 smem + (w * kStages + stage) * S::kTile)[idx];
-                }
-                if (!whole) {
-                    part[2 * S::kHeads + idx] = v;
-                    if (dim == 0) {
-                        part[head] = top;
-                        part[S::kHeads + head] = sum;
-                    }
-                } else if (head0 + head < a.group && dim < kv.head_dim) {
-                    const int qh = hr * a.group + head0 + head;
-                    const bool none = top == -INFINITY && sum == 0.f;
-                    a.out[use.s * a.out_stride + (long long)qh * kv.head_dim + dim] =
-                        none ? 0.f : v / sum;
-                    if (dim == 0) {
-                        const float e = none ? -INFINITY : top + logf(sum);
-                        const long long at = (long long)use.s * a.h_q + qh;
-                        if (a.lse) a.lse[at] = e;
-                        if (a.acc_out) room.lse[at] = e;
-                    }
-                }
+            for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kThreads) {
+                const int head = i / (DP / 4), dim = i % (DP / 4) * 4;
+                const float4 v = joined(head, i);
+                if (whole)
+                    finish(use, head, dim, v, s_top[head], s_sum[head]);
+                else
+                    reinterpret_cast<float4 *>(part + 2 * S::kHeads)[i] = v;
+            }
+            if (!whole && threadIdx.x < S::kHeads) {
+                part[threadIdx.x] = s_top[threadIdx.x];
+                part[S::kHeads + threadIdx.x] = s_sum[threadIdx.x];
             }
             clear();
             leads = false;
@@ -549,128 +792,304 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, 2)
                 load_q(nx);
             }
             __syncthreads();
+            take_scales();
         }
-        use.next(a, rows, S::BT);
-        __syncwarp();
-        if (left > kStages) issue(stage);
-        cp_async_commit();
-        ask();
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (!CL || left > 1) {
+            use.next(a, rows, S::BT);
+            __syncwarp();
+            if (left > kStages) issue(stage);
+            cp_async_commit();
+            ask();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
     }
     cp_async_wait<0>();
+    if (CL) {
+        // Every CTA of the cluster, also one without tiles, shows its part; each then joins
+        // and writes its share of the dims.
+        cg::cluster_group cluster = cg::this_cluster();
+        const int size = cluster.num_blocks(), rank = cluster.block_rank();
+        __syncthreads();
+        meet();
+        float4 *mine = reinterpret_cast<float4 *>(slot_of(0));
+        for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kThreads)
+            mine[i] = joined(i / (DP / 4), i);  // reads the same elements that it replaces
+        // The slot's place depends on the tiles that a CTA had: all go to one place.
+        float4 *shown = reinterpret_cast<float4 *>(smem);
+        if (stage != 0) {
+            for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kThreads) shown[i] = mine[i];
+        }
+        cluster.sync();
+        auto join_heads = [&](int head, float &top, float &sum) {
+            top = -INFINITY;
+            for (int r = 0; r < size; ++r)
+                top = fmaxf(top, *cluster.map_shared_rank(s_top + head, r));
+            sum = 0.f;
+            for (int r = 0; r < size; ++r)
+                sum += exp_diff(*cluster.map_shared_rank(s_top + head, r), top) *
+                       *cluster.map_shared_rank(s_sum + head, r);
+        };
+        const int quads = S::kHeads * DP / 4;
+        for (int i = rank * kThreads + threadIdx.x; i < quads; i += size * kThreads) {
+            const int head = i / (DP / 4), dim = i % (DP / 4) * 4;
+            float top, sum;
+            join_heads(head, top, sum);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < size; ++r) {
+                const float f = exp_diff(*cluster.map_shared_rank(s_top + head, r), top);
+                const float4 x = *cluster.map_shared_rank(shown + i, r);
+                v.x += f * x.x;
+                v.y += f * x.y;
+                v.z += f * x.z;
+                v.w += f * x.w;
+            }
+            finish(use, head, dim, v, top, sum);
+        }
+        if (a.acc_out) {
+            // The weights of this CTA's own slots (head_tiles is 1), from its own scores.
+            float *s_lse = s_l;
+            if (threadIdx.x < S::kHeads) {
+                float top, sum;
+                join_heads(threadIdx.x, top, sum);
+                s_lse[threadIdx.x] = is_none(top, sum) ? -INFINITY : top + logf(sum);
+            }
+            __syncthreads();
+            const long long at = ((long long)use.s * kv.n_heads + use.row) * a.acc_stride;
+            const float *sc = room.scores + ((long long)use.s * a.h_q + use.row * a.group) * a.n_slots;
+            const int tile1 = use.tiles * (rank + 1) / size;
+            const int j0 = rank == 0 ? 0 : use.span.first + first_tile * S::BT;
+            const int j1 = min(use.span.len, use.span.first + tile1 * S::BT);
+            for (int j = j0 + threadIdx.x; j < j1; j += kThreads) {
+                float w = 0.f;
+                if (j >= use.span.first)
+                    for (int i = 0; i < a.group; ++i)
+                        if (s_lse[i] != -INFINITY)
+                            w += exp_diff(sc[(long long)i * a.n_slots + j], s_lse[i]);
+                a.acc_out[at + j] = (a.acc_in ? a.acc_in[at + j] : 0.f) + w;
+            }
+        }
+        cluster.sync();  // no CTA's shared memory goes while another reads it
+    }
 }
 
-// Joins the parts of the rows that several CTAs shared.  One block per (row, query head).
-__global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a, int n_heads, int head_dim,
-                                                        int head_tiles, int heads, int dp,
-                                                        int grid) {
+// After the split kernel: joins the parts of the rows that several CTAs shared, and sums the
+// weights, acc_out[s][h][j] = acc_in + sum over the group's heads of exp(x_j - lse).
+// Block (sequence and kv head, y): query head y of the group, and the y-th of `chunks`
+// pieces of the slots.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnArgs a, int n_heads,
+                                                                    int head_dim, int head_tiles,
+                                                                    int heads, int dp, int grid,
+                                                                    int chunks) {
     __shared__ float s_f[kMaxCtas];
+    __shared__ float4 s_o[kJoinWarps][64];
     __shared__ float s_red[2];
+    extern __shared__ float s_lse[];  // [group], for the weight sums
     pdl_enter();
     const int part_floats = heads * (dp + 2);
     const Room room = room_of(a.workspace, a.n_seq, a.h_q, part_floats);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x / n_heads, h = blockIdx.x - s * n_heads;
     const int rows = n_heads * head_tiles;
-    const int s = blockIdx.x / rows, row = blockIdx.x - s * rows;
-    const int hr = row / head_tiles, ht = row - hr * head_tiles;
-    const int head = blockIdx.y, in_group = ht * heads + head;
-    if (in_group >= a.group) return;
-    Sched sched{rows, room.before[a.n_seq] * rows};
     const long long b0 = room.before[s], tiles = room.before[s + 1] - b0;
-    const long long r0 = b0 * rows + row * tiles, r1 = r0 + tiles;
-    const int c0 = sched.owner(r0, grid), c1 = sched.owner(r1 - 1, grid);
-    if (c0 == c1) return;  // written by its CTA
-    const int n = c1 - c0 + 1;
-    const int at0 = r0 > sched.start(c0, grid) ? 1 : 0;
-    auto part = [&](int i) {
-        return room.parts + (2ll * (c0 + i) + (i == 0 ? at0 : 0)) * part_floats;
+    const Sched sched(room.before[a.n_seq] * rows, grid);
+
+    // The parts of one of the group's heads: their number, 1 for a row within one CTA.
+    struct Parts {
+        int first, n, skip, head;
     };
-    if (threadIdx.x < 32) {
-        float top = -INFINITY;
-        for (int i = threadIdx.x; i < n; i += 32) top = fmaxf(top, part(i)[head]);
+    auto parts_of = [&](int in_group) {
+        const int ht = in_group / heads;
+        const long long r0 = b0 * rows + (long long)(h * head_tiles + ht) * tiles;
+        Parts p;
+        p.first = sched.owner(r0);
+        p.n = sched.owner(r0 + tiles - 1) - p.first + 1;
+        p.skip = r0 > sched.start(p.first) ? 1 : 0;
+        p.head = in_group - ht * heads;
+        return p;
+    };
+    auto part = [&](const Parts &p, int i) {
+        return room.parts + (2ll * (p.first + i) + (i == 0 ? p.skip : 0)) * part_floats;
+    };
+    // m and l of a head, by one warp; factors go to f if given.
+    auto join_head = [&](const Parts &p, float *f, float &top, float &sum) {
+        top = -INFINITY;
+        for (int i = lane; i < p.n; i += 32) top = fmaxf(top, part(p, i)[p.head]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        float sum = 0.f;
-        for (int i = threadIdx.x; i < n; i += 32) {
-            const float f = exp_diff(part(i)[head], top);
-            s_f[i] = f;
-            sum += f * part(i)[heads + head];
+        sum = 0.f;
+        for (int i = lane; i < p.n; i += 32) {
+            const float x = exp_diff(part(p, i)[p.head], top);
+            if (f) f[i] = x;
+            sum += x * part(p, i)[heads + p.head];
         }
         sum = warp_sum(sum);
-        if (threadIdx.x == 0) {
-            s_red[0] = top;
-            s_red[1] = sum;
+    };
+    auto lse_of = [](float top, float sum) {
+        return top == -INFINITY && sum == 0.f ? -INFINITY : top + logf(sum);
+    };
+
+    if ((int)blockIdx.y < a.group) {
+        const Parts p = parts_of(blockIdx.y);
+        if (p.n > 1) {
+            if (warp == 0) {
+                float top, sum;
+                join_head(p, s_f, top, sum);
+                if (lane == 0) {
+                    s_red[0] = top;
+                    s_red[1] = sum;
+                }
+            }
+            // o's loads do not wait for the factors' maximum but for the barrier.
+            __syncthreads();
+            const float top = s_red[0], sum = s_red[1];
+            const bool none = top == -INFINITY && sum == 0.f;
+            const int qh = h * a.group + blockIdx.y;
+            for (int q0 = 0; q0 < head_dim / 4; q0 += 32) {
+                const int q = q0 + lane;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q < head_dim / 4) {
+#pragma unroll 4
+                    for (int i = warp; i < p.n; i += kJoinWarps) {
+                        const float f = s_f[i];
+                        const float4 x = *reinterpret_cast<const float4 *>(
+                            part(p, i) + 2 * heads + p.head * dp + 4 * q);
+                        v.x += f * x.x;
+                        v.y += f * x.y;
+                        v.z += f * x.z;
+                        v.w += f * x.w;
+                    }
+                }
+                s_o[warp][q & 63] = v;
+            }
+            __syncthreads();
+            for (int q = threadIdx.x; q < head_dim / 4; q += kJoinWarps * 32) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float inv = none ? 0.f : 1.f / sum;
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    v.x += s_o[w][q].x;
+                    v.y += s_o[w][q].y;
+                    v.z += s_o[w][q].z;
+                    v.w += s_o[w][q].w;
+                }
+                *reinterpret_cast<float4 *>(a.out + s * a.out_stride + (long long)qh * head_dim +
+                                            4 * q) =
+                    none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                         : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            }
+            if (threadIdx.x == 0 && a.lse) a.lse[(long long)s * a.h_q + qh] = lse_of(top, sum);
         }
     }
+    if (!a.acc_out || (int)blockIdx.y >= chunks) return;
+    const long long q0 = (long long)s * a.h_q + h * a.group;
+    for (int i = warp; i < a.group; i += kJoinWarps) {
+        const Parts p = parts_of(i);
+        float e;
+        if (p.n > 1) {
+            float top, sum;
+            join_head(p, nullptr, top, sum);
+            e = lse_of(top, sum);
+        } else {
+            e = room.lse[q0 + i];
+        }
+        if (lane == 0) s_lse[i] = e;
+    }
     __syncthreads();
-    const float top = s_red[0], sum = s_red[1];
-    const bool none = top == -INFINITY && sum == 0.f;
-    const int qh = hr * a.group + in_group;
-    for (int d = threadIdx.x; d < head_dim; d += 128) {
-        float v = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) v += s_f[i] * part(i)[2 * heads + head * dp + d];
-        a.out[s * a.out_stride + (long long)qh * head_dim + d] = none ? 0.f : v / sum;
-    }
-    if (threadIdx.x == 0) {
-        const float e = none ? -INFINITY : top + logf(sum);
-        const long long at = (long long)s * a.h_q + qh;
-        if (a.lse) a.lse[at] = e;
-        if (a.acc_out) room.lse[at] = e;
-    }
-}
-
-// acc_out[s][h][j] = acc_in + sum over the group's heads of exp(x - lse).
-__global__ void __launch_bounds__(256) attn_weights_kernel(AttnArgs a, int n_heads,
-                                                           size_t part_floats) {
-    pdl_enter();
-    const Room room = room_of(a.workspace, a.n_seq, a.h_q, part_floats);
-    const int s = blockIdx.x / n_heads, h = blockIdx.x - s * n_heads;
     const Span span = span_of(a, s);
     const long long at = ((long long)s * n_heads + h) * a.acc_stride;
-    const long long q0 = (long long)s * a.h_q + h * a.group;
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < span.len; j += gridDim.y * 256) {
+    for (int j = blockIdx.y * kJoinWarps * 32 + threadIdx.x; j < span.len;
+         j += chunks * kJoinWarps * 32) {
         float w = 0.f;
-        if (j >= span.first)
-            for (int g = 0; g < a.group; ++g) {
-                const float e = room.lse[q0 + g];
-                if (e != -INFINITY) w += exp_diff(room.scores[(q0 + g) * a.n_slots + j], e);
+        if (j >= span.first) {
+#pragma unroll 4
+            for (int i = 0; i < a.group; ++i) {
+                const float x = room.scores[(q0 + i) * a.n_slots + j], e = s_lse[i];
+                w += e == -INFINITY ? 0.f : exp_diff(x, e);
             }
+        }
         a.acc_out[at + j] = (a.acc_in ? a.acc_in[at + j] : 0.f) + w;
     }
 }
 
 // 16 query heads a row where a group has more than 8 (the cache is then read half as often),
-// while o and q leave room for it; 8 otherwise.
-int head_tile(int group, int dp) { return group > 8 && dp <= 128 ? 2 : 1; }
+// while o (registers) and q (shared memory) leave room for it; 8 otherwise.
+int head_tile(int group, int dp, int dtype) {
+    return group > 8 && dp <= (dtype == kF32 ? 64 : 128) ? 2 : 1;
+}
 int padded_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
+struct Plan {
+    int head_tiles, cluster;  // cluster 0: the split kernel and the join
+    int grid, tile;
+};
+
 template <int DT, int DP, int HT>
-cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, int head_tiles, int grid,
-                         const DeviceInfo &dev, cudaStream_t stream) {
+cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
+                         cudaStream_t stream) {
     using S = Shape<DT, DP, HT>;
+    const int head_tiles = (a.group + S::kHeads - 1) / S::kHeads;
+    const long long rows = (long long)a.n_seq * kv.n_heads * head_tiles;
+    const int slots = min(kMaxCtas, S::kCtas * dev.sm_count);
+    if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
+
+    // One cluster per row while every CTA of every row is resident at once and a CTA has at
+    // most four tiles.
+    int cluster = 1;
+    while (cluster < 8 && rows * cluster * 2 <= slots) cluster *= 2;
+    const bool small = rows * cluster <= slots &&
+                       a.n_slots <= 4ll * cluster * S::BT && (!a.acc_out || head_tiles == 1);
+    if (small) {
+        static std::atomic<unsigned long long> done{0};
+        cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, true>, S::kSmem, dev, done);
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(rows * cluster));
+        cfg.blockDim = dim3(S::W * 32);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, attn_kernel<DT, DP, HT, true>, a, kv, head_tiles);
+    }
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT>, S::kSmem, dev, done);
+    cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, false>, S::kSmem, dev, done);
     if (err != cudaSuccess) return err;
-    return launch_pdl(attn_kernel<DT, DP, HT>, dim3(grid), dim3(S::W * 32), S::kSmem, stream, a,
-                      kv, head_tiles);
+    err = launch_pdl(attn_kernel<DT, DP, HT, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
+                     a, kv, head_tiles);
+    if (err != cudaSuccess) return err;
+    const int chunks = a.acc_out ? min(64, (int)((a.n_slots + 511ll) / 512)) : 0;
+    return launch_pdl(attn_join_kernel,
+                      dim3((unsigned)(a.n_seq * kv.n_heads), max(a.group, chunks)),
+                      dim3(kJoinWarps * 32), a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads,
+                      kv.head_dim, head_tiles, S::kHeads, DP, slots, chunks);
 }
 
 template <int DT>
-cudaError_t launch_type(const AttnArgs &a, const KvView &kv, int dp, int ht, int head_tiles,
-                        int grid, const DeviceInfo &dev, cudaStream_t stream) {
+cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
+                        cudaStream_t stream) {
+    const int dp = padded_dim(kv.head_dim), ht = head_tile(a.group, dp, DT);
     if (dp == 64)
-        return ht == 2 ? launch_shape<DT, 64, 2>(a, kv, head_tiles, grid, dev, stream)
-                       : launch_shape<DT, 64, 1>(a, kv, head_tiles, grid, dev, stream);
-    if (dp == 128)
-        return ht == 2 ? launch_shape<DT, 128, 2>(a, kv, head_tiles, grid, dev, stream)
-                       : launch_shape<DT, 128, 1>(a, kv, head_tiles, grid, dev, stream);
-    return launch_shape<DT, 256, 1>(a, kv, head_tiles, grid, dev, stream);
+        return ht == 2 ? launch_shape<DT, 64, 2>(a, kv, dev, stream)
+                       : launch_shape<DT, 64, 1>(a, kv, dev, stream);
+    if (dp == 128) {
+        if constexpr (DT != kF32)
+            if (ht == 2) return launch_shape<DT, 128, 2>(a, kv, dev, stream);
+        return launch_shape<DT, 128, 1>(a, kv, dev, stream);
+    }
+    return launch_shape<DT, 256, 1>(a, kv, dev, stream);
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const KvView &kv, int n_seq, int h_q, int n_slots, bool with_acc) {
-    const int dp = padded_dim(kv.head_dim), ht = head_tile(h_q / kv.n_heads, dp);
+    const int dp = padded_dim(kv.head_dim), ht = head_tile(h_q / kv.n_heads, dp, kv.dtype);
     size_t bytes = up256((size_t)(n_seq + 1) * 8) +
                    up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4);
     if (with_acc)
@@ -680,25 +1099,11 @@ size_t attn_workspace_bytes(const KvView &kv, int n_seq, int h_q, int n_slots, b
 
 cudaError_t launch_attn_paged(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
                               cudaStream_t stream) {
-    const int dp = padded_dim(kv.head_dim), ht = head_tile(a.group, dp), heads = ht * 8;
-    const int head_tiles = (a.group + heads - 1) / heads;
-    const int grid = min(kMaxCtas, 2 * dev.sm_count);
-    const long long rows = (long long)a.n_seq * kv.n_heads * head_tiles;
-    if (rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    cudaError_t err;
     switch (kv.dtype) {
-    case kBF16: err = launch_type<kBF16>(a, kv, dp, ht, head_tiles, grid, dev, stream); break;
-    case kF16: err = launch_type<kF16>(a, kv, dp, ht, head_tiles, grid, dev, stream); break;
-    default: err = launch_type<kF32>(a, kv, dp, ht, head_tiles, grid, dev, stream); break;
+    case kBF16: return launch_type<kBF16>(a, kv, dev, stream);
+    case kF16: return launch_type<kF16>(a, kv, dev, stream);
+    default: return launch_type<kF32>(a, kv, dev, stream);
     }
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_join_kernel, dim3((unsigned)rows, heads < a.group ? heads : a.group),
-                     dim3(128), 0, stream, a, kv.n_heads, kv.head_dim, head_tiles, heads, dp, grid);
-    if (err != cudaSuccess || !a.acc_out) return err;
-    const int chunks = (int)((a.n_slots + 1023ll) / 1024);
-    return launch_pdl(attn_weights_kernel,
-                      dim3((unsigned)(a.n_seq * kv.n_heads), chunks > 64 ? 64 : chunks), dim3(256),
-                      0, stream, a, kv.n_heads, (size_t)heads * (dp + 2));
 }
 
 }  // namespace wq
