@@ -34,6 +34,8 @@
 // calls give each row a cluster of CTAs that join their parts through shared memory.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kv_internal.h"
 #include "wq_device.cuh"
 
@@ -147,37 +149,44 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3]) {
 
 // ---------------------------------------------------------------- products --
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a * b + c; c = 0 costs no registers.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
+          "f"(c2), "f"(c3));
 }
 template <int DT>
-__device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                       float c2, float c3) {
     if (DT == kBF16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+            "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+              "f"(c3));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+            "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+              "f"(c3));
 }
-// c += a * b with b in f32, split into its high 11 bits and the rest.
-__device__ __forceinline__ void mma_f32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+// d = a * b (+ d) with b in f32, split into its high 11 bits and the rest.
+template <bool FIRST>
+__device__ __forceinline__ void mma_f32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
     const uint32_t h0 = b0 & 0xFFFFE000u, h1 = b1 & 0xFFFFE000u;
-    mma_tf32(c, a, h0, h1);
-    mma_tf32(c, a, __float_as_uint(rest(__uint_as_float(b0), __uint_as_float(h0))),
-             __float_as_uint(rest(__uint_as_float(b1), __uint_as_float(h1))));
+    if (FIRST)
+        mma_tf32(d, a, h0, h1, 0.f, 0.f, 0.f, 0.f);
+    else
+        mma_tf32(d, a, h0, h1, d[0], d[1], d[2], d[3]);
+    mma_tf32(d, a, __float_as_uint(rest(__uint_as_float(b0), __uint_as_float(h0))),
+             __float_as_uint(rest(__uint_as_float(b1), __uint_as_float(h1))), d[0], d[1], d[2],
+             d[3]);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -272,7 +281,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     constexpr int NT = S::NT, KT = S::KT, W = S::W, kThreads = W * 32, kStages = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    pdl_launch();
     pdl_wait();
     const Room room = room_of(a.workspace, a.n_seq, a.h_q, S::kPart);
     const int rows = kv.n_heads * head_tiles;
@@ -351,6 +359,8 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     long long *offs = reinterpret_cast<long long *>(smem + S::kOff) + warp * KT;
     const int live_chunks = kv.head_dim / S::kEpc;
 
+    const long long v_from_k = kv.v - kv.k;
+
     // Page numbers are asked for one tile ahead of the loads that need them.
     int ask_page = -1, ask_in = 0, ask_head = 0;
     float ask_bias = -INFINITY;
@@ -382,22 +392,32 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                      (long long)ask_in * kv.token_stride;
             }
         }
+        // All of the tile's slots are there, and their rows fill the ring's: no checks.
+        const bool full = __all_sync(0xFFFFFFFFu, lane >= KT || at >= 0) &&
+                          live_chunks == S::kChunks;
         if (lane < KT) {
             bias[stage * KT + lane] = b;
             offs[lane] = at;
         }
         __syncwarp();
         const uint32_t base = ring + stage * S::kTile;
+        auto copy = [&](auto checked) {
 #pragma unroll
-        for (int i = 0; i < KT * S::kChunks / 32; ++i) {
-            const int idx = i * 32 + lane, key = idx / S::kChunks, ch = idx % S::kChunks;
-            const long long from = offs[key];
-            const bool live = from >= 0 && ch < live_chunks;
-            const long long off = live ? from + ch * 16 : 0;
-            const uint32_t dst = base + key * S::kRow;
-            cp_async16(dst + ((ch ^ swizzle_k<DT>(key)) << 4), kv.k + off, live);
-            cp_async16(dst + KT * S::kRow + ((ch ^ swizzle_v<DT>(key)) << 4), kv.v + off, live);
-        }
+            for (int i = 0; i < KT * S::kChunks / 32; ++i) {
+                const int idx = i * 32 + lane, key = idx / S::kChunks, ch = idx % S::kChunks;
+                const long long from = offs[key];
+                const bool live = !checked || (from >= 0 && ch < live_chunks);
+                const char *k = kv.k + (live ? from + ch * 16 : 0);
+                const uint32_t dst = base + key * S::kRow;
+                cp_async16(dst + ((ch ^ swizzle_k<DT>(key)) << 4), k, live);
+                cp_async16(dst + KT * S::kRow + ((ch ^ swizzle_v<DT>(key)) << 4),
+                           k + v_from_k, live);
+            }
+        };
+        if (full)
+            copy(std::false_type());
+        else
+            copy(std::true_type());
         __syncwarp();  // offs is free
     };
 
@@ -547,9 +567,12 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_16<DT>(sc[h][n][0], q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1]);
+                        float(&x)[4] = sc[h][n][0], (&y)[4] = sc[h][n][1];
+                        mma_16<DT>(x, q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1], x[0], x[1],
+                                   x[2], x[3]);
                         if (DT == kBF16)
-                            mma_16<DT>(sc[h][n][1], q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1]);
+                            mma_16<DT>(y, q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1], y[0], y[1],
+                                       y[2], y[3]);
                     }
                 }
             }
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                         const uint4 f = lds128(smem_addr(smem) + S::kQ +
                                                ((h * S::kSteps + 2 * i + j) * 32 + lane) * 16);
                         const uint32_t q[4] = {f.x, f.y, f.z, f.w};
-                        mma_f32(sc[h][0][j], q, w[2 * j], w[2 * j + 1]);
+                        mma_f32<false>(sc[h][0][j], q, w[2 * j], w[2 * j + 1]);
                     }
             }
         }
@@ -631,25 +654,35 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         if (S::k16) {
             const int key = (mat & 1) * 8 + mrow;
             const uint32_t at = vb + key * S::kRow;
+            // Four independent products at a time.
 #pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
+            for (int i = 0; i < DP / 16; i += 2) {
                 if (2 * i >= live_chunks) break;
-                uint32_t vf[4];
-                ldmatrix4<true>(vf, at + (((2 * i + (mat >> 1)) ^ mrow) << 4));
+                uint32_t vf[8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
+                    ldmatrix4<true>(reinterpret_cast<uint32_t(&)[4]>(vf[4 * u]),
+                                    at + (((2 * (i + u) + (mat >> 1)) ^ mrow) << 4));
 #pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        float t[4] = {};
-                        mma_16<DT>(t, pt[h][0][0], pt[h][0][1], pt[h][NT - 1][0],
-                                   pt[h][NT - 1][1], vf[2 * u], vf[2 * u + 1]);
-                        if (DT == kBF16)
-                            mma_16<DT>(t, pt[h][0][2], 0u, pt[h][NT - 1][2], 0u, vf[2 * u],
-                                       vf[2 * u + 1]);
+                for (int h = 0; h < HT; ++h) {
+                    const uint32_t(&p0)[3] = pt[h][0], (&p1)[3] = pt[h][1];
+                    float t[4][4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        mma_16<DT>(t[u], p0[0], p0[1], p1[0], p1[1], vf[2 * u], vf[2 * u + 1], 0.f,
+                                   0.f, 0.f, 0.f);
+                    if (DT == kBF16)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mma_16<DT>(t[u], p0[2], 0u, p1[2], 0u, vf[2 * u], vf[2 * u + 1],
+                                       t[u][0], t[u][1], t[u][2], t[u][3]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
                         float(&to)[2] = o[h][2 * i + u];
-                        to[0] = to[0] * corr[h] + (t[0] + t[2]);
-                        to[1] = to[1] * corr[h] + (t[1] + t[3]);
+                        to[0] = to[0] * corr[h] + (t[u][0] + t[u][2]);
+                        to[1] = to[1] * corr[h] + (t[u][1] + t[u][3]);
                     }
+                }
             }
         } else {
             // Column g of product e is dim 4 (g + 8 i) + e.
@@ -663,8 +696,8 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int h = 0; h < HT; ++h) {
-                        float t[4] = {};
-                        mma_f32(t, pf[h], w0[e], w1[e]);
+                        float t[4];
+                        mma_f32<true>(t, pf[h], w0[e], w1[e]);
                         float(&to)[2] = o[h][i * 4 + e];
                         to[0] = to[0] * corr[h] + (t[0] + t[2]);
                         to[1] = to[1] * corr[h] + (t[1] + t[3]);
@@ -803,6 +836,9 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
     }
+    // Not before: CTAs of the next kernel that wait beside these cost a third of the rate
+    // (131072 slots back to back: 130 us with the launch at the top, 96 us here).
+    pdl_launch();
     cp_async_wait<0>();
     if (CL) {
         // Every CTA of the cluster, also one without tiles, shows its part; each then joins
