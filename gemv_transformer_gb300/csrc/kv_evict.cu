@@ -1,14 +1,14 @@
 // kv_evict.cu -- a cache cut to a budget of slots by accumulated attention weight.
 //
-// Per row (sequence, kv head): the keep-th largest weight is found by radix selection, eight
-// bits of an order-preserving key at a time; the slots that stay but lie beyond the
+// Per row (sequence, kv head): the keep-th largest weight is found by radix selection,
+// eleven bits of an order-preserving key at a time; the slots that stay but lie beyond the
 // budget then move, in order, into the slots below it that go.  Only they move: a cache
 // over its budget by one slot a step moves one slot, not the half of the cache that keeping
 // the order would.
 //
 // What bounds it: 8 bytes read per slot (weight, position), 8 written per slot kept, and two
 // rows of k and v read and written per slot moved; with few rows, or one slot over, the
-// chain of four histograms.
+// chain of three histograms.
 //
 // A row is a cluster of 1, 2, 4 or 8 CTAs, so that a few long rows fill the GPU: each holds
 // the keys of its share of the slots in shared memory, the histograms and counts are
@@ -25,29 +25,44 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxKeys = 48 * 1024;  // keys that a CTA holds; beyond, they are read again
-constexpr int kBatch = 4;            // moves that a warp has in flight
+constexpr int kMaxKeys = 42 * 1024;  // keys that a CTA holds; beyond, they are read again
+constexpr int kBatch = 8;            // moves that a warp has in flight
+constexpr int kDigit = 11, kBins = 1 << kDigit, kPasses = 3;  // 11 + 11 + 10 bits
+constexpr int kShort = 128;          // moves that a single CTA lists in shared memory
+
+// One move.  The hole's owner writes `to` and `dst`, the mover's the rest.
+struct __align__(16) Move {
+    long long to, at;  // byte offsets of the rows, -1 for a page out of range
+    int dst;
+    float weight;
+    int pos, pad;
+};
+
+constexpr uint32_t kHeld = 0xFFFFFFFFu, kZero = 0x80000000u;
 
 // Keys in the order of the weights: a held slot above all, a NaN below all.
 __device__ __forceinline__ uint32_t key_of(float w, int pos, int sinks, int from) {
-    if (pos < sinks || pos >= from) return 0xFFFFFFFFu;
+    if (pos < sinks || pos >= from) return kHeld;
     if (w != w) return 0u;
     const uint32_t u = __float_as_uint(w + 0.f);  // -0 as 0
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-template <int T> struct Select {
-    static constexpr int W = T / 32;
-    int hist[4][256];  // one per pass, so that one barrier a pass is enough
-    int scan[2][W];
-    int counts[3];     // this CTA's ties, holes, movers
-    uint32_t prefix;
+template <int T, int C> struct __align__(16) Select {
+    // One per pass, so that one cluster barrier a pass is enough.  Of a row's C CTAs each
+    // holds the counts of its kBins / C bins for all of them.
+    int hist[kPasses][kBins];
+    int own[C > 1 ? kBins : 4];  // the first digit's counts of this CTA's slots alone
+    Move list[kShort];
+    int scan[2][T / 32];
+    int counts[3];             // this CTA's ties, holes, movers
+    uint32_t bound;            // the key's digits so far, then the bound itself
     int left, equal;
 };
 
 // Sums over the warps before this one of (a, b), and the totals.
-template <int T>
-__device__ __forceinline__ void warp_offsets(Select<T> &sh, int &a, int &b, int &ta, int &tb) {
+template <int T, int C>
+__device__ __forceinline__ void warp_offsets(Select<T, C> &sh, int &a, int &b, int &ta, int &tb) {
     const int warp = threadIdx.x >> 5;
     __syncthreads();
     if ((threadIdx.x & 31) == 0) {
@@ -65,17 +80,36 @@ __device__ __forceinline__ void warp_offsets(Select<T> &sh, int &a, int &b, int 
     }
 }
 
-template <int T>
-__global__ void __launch_bounds__(T) evict_kernel(EvictArgs a, KvView kv, int row_bytes,
+// C: the CTAs of a row; with one, its barriers are the CTA's.
+template <int T, int C>
+__global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView kv, int row_bytes,
                                                   int key_room) {
-    extern __shared__ uint32_t s_key[];
-    __shared__ Select<T> sh;
-    pdl_wait();
-    cg::cluster_group cluster = cg::this_cluster();
-    const int size = cluster.num_blocks(), rank = cluster.block_rank();
-    const int id = blockIdx.x / size, s = id / kv.n_heads, h = id - s * kv.n_heads;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Select<T, C> &sh = *reinterpret_cast<Select<T, C> *>(smem);
+    uint32_t *s_key = reinterpret_cast<uint32_t *>(smem + sizeof(Select<T, C>));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kPasses * kBins / 4; i += T)
+        reinterpret_cast<int4 *>(&sh.hist[0][0])[i] = make_int4(0, 0, 0, 0);
+    constexpr bool ONE = C == 1;
+    if (!ONE)
+        for (int i = threadIdx.x; i < kBins; i += T) sh.own[i] = 0;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (!ONE) cluster.sync();  // the counts are 0 before another CTA adds to them
+    pdl_wait();
+    const int rank = ONE ? 0 : cluster.block_rank();
+    auto sync_row = [&]() {
+        if (ONE)
+            __syncthreads();
+        else
+            cluster.sync();
+    };
+    auto of = [&](auto *p, int r) { return ONE ? p : cluster.map_shared_rank(p, r); };
+    auto counter = [&](int pass, int bin) {
+        return of(&sh.hist[pass][bin], bin / (kBins / C));
+    };
+    const int id = blockIdx.x / C, s = id / kv.n_heads, h = id - s * kv.n_heads;
     const int given = __ldg(a.lens + s), len = min(max(given, 0), a.n_slots);
+    const int from = __ldg(a.seen + s) - a.recent;
     const int keep = min(len, a.keep);
     if (threadIdx.x == 0 && rank == 0 && h == 0) {
         if (given > a.n_slots) record_status(a.status, kStBadIndex);
@@ -86,7 +120,7 @@ __global__ void __launch_bounds__(T) evict_kernel(EvictArgs a, KvView kv, int ro
     const int32_t *pos = a.slot_pos + base;
     const bool in_place = a.acc_out == a.acc && a.pos_out == a.slot_pos;
     // This CTA's slots.
-    const int share = ((len + size - 1) / size + 31) & ~31;
+    const int share = ((len + C - 1) / C + 31) & ~31;
     const int b0 = min(len, rank * share), b1 = min(len, b0 + share), mine = b1 - b0;
     if (len <= keep) {  // within the budget: the whole cluster leaves here
         if (!in_place)
@@ -96,167 +130,281 @@ __global__ void __launch_bounds__(T) evict_kernel(EvictArgs a, KvView kv, int ro
             }
         return;
     }
-    const int from = __ldg(a.seen + s) - a.recent;
     const bool held_keys = mine <= key_room;
     auto make_key = [&](int j) { return key_of(acc[j], pos[j], a.sinks, from); };
-    auto key = [&](int j) { return held_keys ? s_key[j - b0] : make_key(j); };
+    // The keys of four slots from j on (j - b0 is a multiple of 4); of slots beyond b1, 0.
+    auto keys4 = [&](int j, uint32_t (&x)[4]) {
+        if (held_keys) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(s_key + (j - b0));
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = j + i < b1 ? make_key(j + i) : 0u;
+        }
+    };
 
-    for (int i = threadIdx.x; i < 4 * 256; i += T) (&sh.hist[0][0])[i] = 0;
     if (threadIdx.x == 0) {
-        sh.prefix = 0;
+        sh.bound = 0;
         sh.left = keep;
     }
-    if (held_keys) {
-#pragma unroll 4
-        for (int j = b0 + threadIdx.x; j < b1; j += T) s_key[j - b0] = make_key(j);
-    }
-    __syncthreads();
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        const uint32_t prefix = sh.prefix;
-        // Weights share their top bits: a warp's equal bins are counted by one addition.
-        for (int j0 = b0 + warp * 32; j0 < b1; j0 += T) {
-            const int j = j0 + lane;
-            const uint32_t x = j < b1 ? key(j) : 0u;
-            const bool in = j < b1 && (pass == 0 || (x >> (shift + 8)) == prefix);
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
-            if (!who) continue;
-            if (in) {
-                const int bin = (x >> shift) & 255u;
-                const unsigned same = __match_any_sync(who, bin);
-                if (lane == __ffs(same) - 1) atomicAdd(&sh.hist[pass][bin], __popc(same));
+    // Slots below the budget keep their places for now: the moves overwrite the holes' copies.
+    for (int j0 = b0 + threadIdx.x; j0 < b1; j0 += 8 * T) {
+        float w[8];
+        int p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j0 + i * T < b1) w[i] = acc[j0 + i * T], p[i] = pos[j0 + i * T];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * T;
+            if (j >= b1) continue;
+            if (held_keys) s_key[j - b0] = key_of(w[i], p[i], a.sinks, from);
+            if (!in_place && j < keep) {
+                a.acc_out[base + j] = w[i];
+                a.pos_out[base + j] = p[i];
             }
         }
-        cluster.sync();
-        // The bin that holds the left-th largest: bins from the top, one per thread.
-        int count = 0;
-        if (threadIdx.x < 256) {
-            const int bin = 255 - threadIdx.x;
-            for (int r = 0; r < size; ++r)
-                count += *cluster.map_shared_rank(&sh.hist[pass][bin], r);
+    }
+    if (held_keys && threadIdx.x < 4 && ((mine + (int)threadIdx.x) & ~3) >= mine)
+        s_key[mine + threadIdx.x] = 0u;  // up to a multiple of four
+    __syncthreads();
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : kDigit;
+        const uint32_t above = sh.bound;  // the digits before this one, in place
+        // Held slots and sums that are still 0 are many of one key: counted apart.  The first
+        // digit's few bins are counted in this CTA and then added to the row's, later digits
+        // straight away: few slots are left.
+        auto add = [&](int bin, int n) {
+            atomicAdd(!ONE && pass == 0 ? &sh.own[bin % (ONE ? 4 : kBins)] : counter(pass, bin), n);
+        };
+        int held = 0, zero = 0;
+#pragma unroll 2
+        for (int j = b0 + 4 * threadIdx.x; j < b1; j += 4 * T) {
+            uint32_t x[4];
+            keys4(j, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (j + i >= b1 || (pass > 0 && (x[i] ^ above) >> (shift + bits))) continue;
+                if (x[i] == kHeld)
+                    ++held;
+                else if (x[i] == kZero)
+                    ++zero;
+                else
+                    add((x[i] >> shift) & ((1 << bits) - 1), 1);
+            }
         }
-        int incl = count;
+        held = __reduce_add_sync(0xFFFFFFFFu, held);
+        zero = __reduce_add_sync(0xFFFFFFFFu, zero);
+        if (lane == 0 && held) add((kHeld >> shift) & ((1 << bits) - 1), held);
+        if (lane == 0 && zero) add((kZero >> shift) & ((1 << bits) - 1), zero);
+        if (!ONE && pass == 0) {
+            __syncthreads();
+            for (int bin = threadIdx.x; bin < kBins; bin += T)
+                if (const int n = sh.own[bin]) atomicAdd(counter(0, bin), n);
+        }
+        sync_row();
+        // The bin that holds the left-th largest: each thread has kBins / T of them, from
+        // the top.
+        constexpr int kMine = kBins / T;
+        const int top = kBins - kMine * (threadIdx.x + 1);  // this thread's lowest bin
+        int count[kMine] = {}, sum = 0;
+        const int4 *counts4 = reinterpret_cast<const int4 *>(counter(pass, top));
+#pragma unroll
+        for (int i = 0; i < kMine / 4; ++i) {
+            const int4 v = counts4[i];
+            count[4 * i] = v.x, count[4 * i + 1] = v.y;
+            count[4 * i + 2] = v.z, count[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) sum += count[i];
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
             if (lane >= o) incl += y;
         }
-        if (lane == 31 && warp < 8) sh.scan[0][warp] = incl;
+        if (lane == 31) sh.scan[0][warp] = incl;
         const int left = sh.left;
         __syncthreads();
-        if (threadIdx.x < 256) {
-            for (int w = 0; w < warp; ++w) incl += sh.scan[0][w];
-            if (incl - count < left && left <= incl) {
-                sh.prefix = prefix << 8 | (uint32_t)(255 - threadIdx.x);
-                sh.left = left - (incl - count);
-                sh.equal = count;
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w)
+            if (w < warp) incl += sh.scan[0][w];
+        int before = incl - sum;
+        if (before < left && left <= incl) {
+#pragma unroll
+            for (int i = kMine - 1; i >= 0; --i) {
+                if (before < left && left <= before + count[i]) {
+                    sh.bound = above | (uint32_t)(top + i) << shift;
+                    sh.left = left - before;
+                    sh.equal = count[i];
+                }
+                before += count[i];
             }
         }
         __syncthreads();
+        if (sh.left == sh.equal) break;  // the whole bin stays: all keys >= bound do
     }
-    const uint32_t bound = sh.prefix;
-    const int ties = sh.left, equal = sh.equal;  // of `equal` slots with the bound's key, `ties` stay
+    const uint32_t bound = sh.bound;
+    const int ties = sh.left;
+    const bool all_ties = ties == sh.equal;  // else `ties` of the slots with the bound's key stay
 
-    // Each warp takes a contiguous piece, so that ranks follow the slots.
-    const int piece = ((mine + T / 32 - 1) / (T / 32) + 31) & ~31;
+    // Each warp takes a contiguous piece and each lane four slots of 128, so that ranks follow
+    // the slots.
+    const int piece = ((mine + T / 32 - 1) / (T / 32) + 127) & ~127;
     const int w0 = min(b1, b0 + warp * piece), w1 = min(b1, w0 + piece);
     int same = 0, none = 0, all_same, all_none;
-    const bool all_ties = ties == equal;
     if (!all_ties) {
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-            const int j = j0 + lane;
-            same += __popc(__ballot_sync(0xFFFFFFFFu, j < w1 && key(j) == bound));
+        for (int j = w0 + 4 * lane; j < w1; j += 128) {
+            uint32_t x[4];
+            keys4(j, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) same += j + i < w1 && x[i] == bound;
         }
-        warp_offsets<T>(sh, same, none, all_same, all_none);
-        if (threadIdx.x == 0) sh.counts[0] = all_same;
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) same += *cluster.map_shared_rank(&sh.counts[0], r);
-    }
-    const unsigned below_lane = (1u << lane) - 1u;
-    // Does slot j stay?  `tie` counts the bound's slots before the group of 32.
-    auto stays = [&](int j, int &tie) {
-        const bool live = j < w1;
-        const uint32_t x = live ? key(j) : 0u;
-        const bool at_bound = live && x == bound;
-        if (all_ties) return live && x >= bound;
-        const unsigned votes = __ballot_sync(0xFFFFFFFFu, at_bound);
-        const int rank_of = tie + __popc(votes & below_lane);
-        tie += __popc(votes);
-        return live && (x > bound || (at_bound && rank_of < ties));
-    };
-    int holes = 0, movers = 0, cta_holes, cta_movers, tie = same;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const bool stay = stays(j, tie);
-        holes += __popc(__ballot_sync(0xFFFFFFFFu, j < w1 && j < keep && !stay));
-        movers += __popc(__ballot_sync(0xFFFFFFFFu, stay && j >= keep));
-    }
-    warp_offsets<T>(sh, holes, movers, cta_holes, cta_movers);
-    if (threadIdx.x == 0) {
-        sh.counts[1] = cta_holes;
-        sh.counts[2] = cta_movers;
-    }
-    cluster.sync();
-    int total = 0;
-    for (int r = 0; r < size; ++r) {
-        const int x = *cluster.map_shared_rank(&sh.counts[1], r);
-        if (r < rank) {
-            holes += x;
-            movers += *cluster.map_shared_rank(&sh.counts[2], r);
-        }
-        total += x;
-    }
-    int2 *list = static_cast<int2 *>(a.workspace) + (long long)id * a.keep;  // (to, from)
-    tie = same;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const bool stay = stays(j, tie);
-        const bool hole = j < w1 && j < keep && !stay, mover = stay && j >= keep;
-        const unsigned hv = __ballot_sync(0xFFFFFFFFu, hole);
-        const unsigned mv = __ballot_sync(0xFFFFFFFFu, mover);
-        if (hole) list[holes + __popc(hv & below_lane)].x = j;
-        if (mover) list[movers + __popc(mv & below_lane)].y = j;
-        holes += __popc(hv);
-        movers += __popc(mv);
-        if (stay && !mover && !in_place) {
-            a.acc_out[base + j] = acc[j];
-            a.pos_out[base + j] = pos[j];
-        }
-    }
-    cluster.sync();  // the list is complete; no shared memory of another CTA is read below
-    pdl_launch();
-
-    const int warps = size * (T / 32), quads = row_bytes / 16;  // of k; as many of v
-    for (int i0 = (rank * (T / 32) + warp) * kBatch; i0 < total; i0 += warps * kBatch) {
-        long long to = -1, at = -1;
-        if (lane < kBatch && i0 + lane < total) {
-            const int2 m = list[i0 + lane];
-            a.acc_out[base + m.x] = acc[m.y];
-            a.pos_out[base + m.x] = pos[m.y];
-            to = kv.row(s, h, m.x);
-            at = kv.row(s, h, m.y);
-            if (to < 0 || at < 0) {
-                record_status(a.status, kStBadIndex);
-                to = -1;
+        same = __reduce_add_sync(0xFFFFFFFFu, same);
+        warp_offsets<T, C>(sh, same, none, all_same, all_none);
+        if (!ONE) {
+            if (threadIdx.x == 0) sh.counts[0] = all_same;
+            cluster.sync();
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                const int x = *cluster.map_shared_rank(&sh.counts[0], r);
+                if (r < rank) same += x;
             }
         }
+    }
+    // The sums of x over the lanes before this one and over all.
+    auto lane_offsets = [&](int x, int &all) {
+        int incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        return incl - x;
+    };
+    // Of this lane's four slots, those whose place changes hands (bits 0-3: holes below the
+    // budget, 4-7: movers beyond it).  `tie` counts the bound's slots before the 128.
+    auto vote = [&](int j, int &tie) {
+        uint32_t x[4] = {};
+        if (j < w1) keys4(j, x);
+        int rank_of = 0;
+        if (!all_ties) {
+            int mine_at = 0, all;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine_at += j + i < w1 && x[i] == bound;
+            rank_of = tie + lane_offsets(mine_at, all);
+            tie += all;
+        }
+        unsigned v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (j + i >= w1) continue;
+            bool stay = x[i] >= bound;
+            if (!all_ties && x[i] == bound) stay = rank_of++ < ties;
+            if (j + i < keep ? !stay : stay) v |= (j + i < keep ? 1u : 16u) << i;
+        }
+        return v;
+    };
+    int holes = 0, movers = 0, total, cta_movers, tie = same;
+    for (int j0 = w0; j0 < w1; j0 += 128) {
+        const unsigned v = vote(j0 + 4 * lane, tie);
+        holes += __popc(v & 15u);
+        movers += __popc(v >> 4);
+    }
+    holes = __reduce_add_sync(0xFFFFFFFFu, holes);
+    movers = __reduce_add_sync(0xFFFFFFFFu, movers);
+    warp_offsets<T, C>(sh, holes, movers, total, cta_movers);
+    if (!ONE) {
+        if (threadIdx.x == 0) {
+            sh.counts[1] = total;
+            sh.counts[2] = cta_movers;
+        }
+        cluster.sync();
+        total = 0;
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            const int x = *cluster.map_shared_rank(&sh.counts[1], r);
+            const int y = *cluster.map_shared_rank(&sh.counts[2], r);
+            if (r < rank) holes += x, movers += y;
+            total += x;
+        }
+    }
+    // Every move, in slot order.
+    Move *list = ONE && total <= kShort
+                     ? sh.list
+                     : static_cast<Move *>(a.workspace) + (long long)id * min(a.keep, a.n_slots);
+    tie = same;
+    for (int j0 = w0; j0 < w1; j0 += 128) {
+        const int j = j0 + 4 * lane;
+        const unsigned v = vote(j, tie);
+        if (!__any_sync(0xFFFFFFFFu, v)) continue;
+        int all;  // holes in the low half, movers in the high one
+        const int at = lane_offsets(__popc(v & 15u) | __popc(v >> 4) << 16, all);
+        Move *to_hole = list + holes + (at & 0xFFFF), *to_mover = list + movers + (at >> 16);
+        long long row[4];
+        float w[4];
+        int p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (v >> i & 17u) row[i] = kv.row(s, h, j + i);
+            if (v >> i & 16u) w[i] = acc[j + i], p[i] = pos[j + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!(v >> i & 17u)) continue;
+            if (row[i] < 0) record_status(a.status, kStBadIndex);
+            if (v >> i & 1u) {
+                to_hole->to = row[i];
+                to_hole++->dst = j + i;
+            } else {
+                to_mover->at = row[i];
+                to_mover->weight = w[i];
+                to_mover++->pos = p[i];
+            }
+        }
+        holes += all & 0xFFFF;
+        movers += all >> 16;
+    }
+    sync_row();  // the list is complete; no shared memory of another CTA is read below
+    pdl_launch();
+
+    // The moves, kBatch per warp at a time; the next batch is looked up while this one's rows
+    // are on their way.
+    const int warps = C * (T / 32), quads = row_bytes / 16;  // of k; as many of v
+    long long to, at;
+    auto look_up = [&](int i0) {
+        to = at = -1;
+        if (lane < kBatch && i0 + lane < total) {
+            const Move m = list[i0 + lane];
+            a.acc_out[base + m.dst] = m.weight;
+            a.pos_out[base + m.dst] = m.pos;
+            at = m.at;
+            to = m.at < 0 ? -1 : m.to;
+        }
+    };
+    int i0 = (rank * (T / 32) + warp) * kBatch;
+    look_up(i0);
+    for (; i0 < total; i0 += warps * kBatch) {
+        const long long to_now = to, at_now = at;
         for (int q0 = 0; q0 < 2 * quads; q0 += 32) {
             const int q = q0 + lane;
             const bool of_v = q >= quads;
             const long long in = 16ll * (of_v ? q - quads : q);
             char *pool = of_v ? kv.v : kv.k;
             uint4 x[kBatch];
-            long long dst[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                dst[i] = __shfl_sync(0xFFFFFFFFu, to, i);
-                const long long src = __shfl_sync(0xFFFFFFFFu, at, i);
-                if (q >= 2 * quads) dst[i] = -1;
-                if (dst[i] >= 0) x[i] = *reinterpret_cast<const uint4 *>(pool + src + in);
+                const bool live = __shfl_sync(0xFFFFFFFFu, to_now, i) >= 0 && q < 2 * quads;
+                const long long src = __shfl_sync(0xFFFFFFFFu, at_now, i);
+                if (live) x[i] = *reinterpret_cast<const uint4 *>(pool + src + in);
             }
+            if (q0 == 0) look_up(i0 + warps * kBatch);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (dst[i] >= 0) *reinterpret_cast<uint4 *>(pool + dst[i] + in) = x[i];
+            for (int i = 0; i < kBatch; ++i) {
+                const long long dst = __shfl_sync(0xFFFFFFFFu, to_now, i);
+                if (dst >= 0 && q < 2 * quads) *reinterpret_cast<uint4 *>(pool + dst + in) = x[i];
+            }
         }
     }
 }
@@ -268,36 +416,39 @@ __global__ void evict_lens_kernel(EvictArgs a) {
     if (s < a.n_seq) a.lens_out[s] = min(max(a.lens[s], 0), min(a.keep, a.n_slots));
 }
 
-template <int T>
-cudaError_t launch_rows(const EvictArgs &a, const KvView &kv, int cluster, const DeviceInfo &dev,
+template <int T, int C>
+cudaError_t launch_rows(const EvictArgs &a, const KvView &kv, const DeviceInfo &dev,
                         cudaStream_t stream) {
     const int row_bytes = kv.head_dim * (kv.dtype == kF32 ? 4 : 2);
-    const long long share = ((a.n_slots + (long long)cluster - 1) / cluster + 31) & ~31ll;
+    const long long share = ((a.n_slots + (long long)C - 1) / C + 31) & ~31ll;
     const int key_room = (int)(share < kMaxKeys ? share : kMaxKeys);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = ensure_smem(evict_kernel<T>, kMaxKeys * 4, dev, done);
+    constexpr int kFixed = sizeof(Select<T, C>);
+    static_assert(kFixed + kMaxKeys * 4 <= 227 * 1024, "shared memory");
+    cudaError_t err = ensure_smem(evict_kernel<T, C>, kFixed + kMaxKeys * 4, dev, done);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)a.n_seq * kv.n_heads * cluster));
+    cfg.gridDim = dim3((unsigned)((long long)a.n_seq * kv.n_heads * C));
     cfg.blockDim = dim3(T);
-    cfg.dynamicSmemBytes = (size_t)key_room * 4;
+    cfg.dynamicSmemBytes = kFixed + (size_t)key_room * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.x = C;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<T>, a, kv, row_bytes, key_room);
+    cfg.numAttrs = C == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, evict_kernel<T, C>, a, kv, row_bytes, key_room);
 }
 
 }  // namespace
 
-size_t evict_workspace_bytes(const KvView &kv, int n_seq, int, int keep) {
-    return ((size_t)n_seq * kv.n_heads * keep * 8 + 255) & ~(size_t)255;
+size_t evict_workspace_bytes(const KvView &kv, int n_seq, int n_slots, int keep) {
+    if (keep > n_slots) keep = n_slots;
+    return ((size_t)n_seq * kv.n_heads * keep * sizeof(Move) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -308,8 +459,16 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count && a.n_slots / cluster > 2048)
         cluster *= 2;
-    cudaError_t err = a.n_slots / cluster <= 4096 ? launch_rows<256>(a, kv, cluster, dev, stream)
-                                                  : launch_rows<512>(a, kv, cluster, dev, stream);
+    cudaError_t err;
+    switch (cluster) {
+    case 1:
+        err = a.n_slots <= 4096 ? launch_rows<256, 1>(a, kv, dev, stream)
+                                : launch_rows<512, 1>(a, kv, dev, stream);
+        break;
+    case 2: err = launch_rows<512, 2>(a, kv, dev, stream); break;
+    case 4: err = launch_rows<512, 4>(a, kv, dev, stream); break;
+    default: err = launch_rows<512, 8>(a, kv, dev, stream);
+    }
     if (err != cudaSuccess || a.lens_out != a.lens) return err;
     return launch_pdl(evict_lens_kernel, dim3((a.n_seq + 255) / 256), dim3(256), 0, stream, a);
 }

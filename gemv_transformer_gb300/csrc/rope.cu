@@ -180,40 +180,32 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs r, Deal deal, const 
     const unsigned t = deal.per_row.div(at), w = at - t * deal.per_row.d;
     const unsigned hg = deal.units.div(w), u = w - hg * deal.units.d;
     const Place p = place_of<N>(u, r.rot, r.flags);
-    Angles<N> cs;
-    if (r.rot > 0) {
-        const int pos = __ldg(r.pos + t);
-        if ((unsigned)pos >= (unsigned)r.table_rows) {
-            record_status(r.status, kStBadIndex);
-            return;
-        }
-        if (p.turn) cs = load_angles<N>(r.table + (long long)pos * (r.rot / 2) + u * N, r.flags);
-    }
-    const int h0 = hg * deal.heads_per;
+    const int pos = r.rot > 0 ? __ldg(r.pos + t) : 0;
+    const int h0 = hg * deal.heads_per, n = min(deal.heads_per, n_heads - h0);
     const float *xi = x + t * x_stride + (long long)h0 * r.head_dim;
     float *o = out + t * out_stride + (long long)h0 * r.head_dim;
     const bool both = N > 1 || p.b < r.head_dim;  // an odd head_dim ends in a single value
-    auto one = [&](Vals<N> &a, Vals<N> &b, float *to) {
-        if (p.turn) turn<N>(a, b, cs, r.flags);
-        store_vals(to + p.a, a);
-        if (both) store_vals(to + p.b, b);
-    };
-    if (deal.heads_per == kHeadsPer && h0 + kHeadsPer <= n_heads) {
-        Vals<N> a[kHeadsPer], b[kHeadsPer];
+    // The values do not wait for the position.
+    Vals<N> a[kHeadsPer], b[kHeadsPer];
 #pragma unroll
-        for (int i = 0; i < kHeadsPer; ++i) {
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) {
             a[i] = load_vals<N>(xi + i * r.head_dim + p.a);
             if (both) b[i] = load_vals<N>(xi + i * r.head_dim + p.b);
         }
-#pragma unroll
-        for (int i = 0; i < kHeadsPer; ++i) one(a[i], b[i], o + i * r.head_dim);
+    if (r.rot > 0 && (unsigned)pos >= (unsigned)r.table_rows) {
+        record_status(r.status, kStBadIndex);
         return;
     }
-    for (int i = 0; i < min(deal.heads_per, n_heads - h0); ++i) {
-        Vals<N> a = load_vals<N>(xi + i * r.head_dim + p.a), b = a;
-        if (both) b = load_vals<N>(xi + i * r.head_dim + p.b);
-        one(a, b, o + i * r.head_dim);
-    }
+    Angles<N> cs;
+    if (p.turn) cs = load_angles<N>(r.table + (long long)pos * (r.rot / 2) + u * N, r.flags);
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) {
+            if (p.turn) turn<N>(a[i], b[i], cs, r.flags);
+            store_vals(o + i * r.head_dim + p.a, a[i]);
+            if (both) store_vals(o + i * r.head_dim + p.b, b[i]);
+        }
 }
 
 template <int DT, int N>
@@ -230,6 +222,23 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a, KvView kv,
     const int slot = __ldg(a.slot + t);
     const int seq = a.seq ? __ldg(a.seq + t) : t;
     const int pos = r.pos ? __ldg(r.pos + t) : 0;
+    const Place p = place_of<N>(u, r.rot, r.flags);
+    const int heads = a.h_q + 2 * kv.n_heads;
+    const int h0 = hg * deal.heads_per, n = min(deal.heads_per, heads - h0);
+    // Heads in the order q, k, v.  The values do not wait for the slot.
+    Vals<N> lo[kHeadsPer], hi[kHeadsPer];
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) {
+            const int head = h0 + i;
+            const float *x =
+                head < a.h_q ? a.q + t * a.q_stride + (long long)head * r.head_dim
+                : head < a.h_q + kv.n_heads
+                    ? a.k + t * a.k_stride + (long long)(head - a.h_q) * r.head_dim
+                    : a.v + t * a.v_stride + (long long)(head - a.h_q - kv.n_heads) * r.head_dim;
+            lo[i] = load_vals<N>(x + p.a);
+            hi[i] = load_vals<N>(x + p.b);
+        }
     if (slot < 0) return;  // padding
     const bool in_range = (unsigned)seq < (unsigned)a.n_seq && slot < a.n_slots &&
                           (r.rot == 0 || (unsigned)pos < (unsigned)r.table_rows);
@@ -238,53 +247,30 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a, KvView kv,
         record_status(r.status, kStBadIndex);
         return;
     }
-    const Place p = place_of<N>(u, r.rot, r.flags);
     Angles<N> cs;
     if (p.turn) cs = load_angles<N>(r.table + (long long)pos * (r.rot / 2) + u * N, r.flags);
-    const int h0 = hg * deal.heads_per, heads = a.h_q + 2 * kv.n_heads;
-    // Heads in the order q, k, v.
-    auto source = [&](int head) {
-        return head < a.h_q ? a.q + t * a.q_stride + (long long)head * r.head_dim
-               : head < a.h_q + kv.n_heads
-                   ? a.k + t * a.k_stride + (long long)(head - a.h_q) * r.head_dim
-                   : a.v + t * a.v_stride + (long long)(head - a.h_q - kv.n_heads) * r.head_dim;
-    };
-    auto one = [&](int head, Vals<N> &lo, Vals<N> &hi) {
-        const bool is_q = head < a.h_q, is_k = !is_q && head < a.h_q + kv.n_heads;
-        if (p.turn && (is_q || is_k)) turn<N>(lo, hi, cs, r.flags);
-        if (is_q) {
-            float *o = a.q_out + t * a.q_out_stride + (long long)head * r.head_dim;
-            store_vals(o + p.a, lo);
-            store_vals(o + p.b, hi);
-            return;
-        }
-        const int h = head - a.h_q - (is_k ? 0 : kv.n_heads);
-        T *o = reinterpret_cast<T *>((is_k ? kv.k : kv.v) + row + h * kv.head_stride);
-        store_vals(o + p.a, lo);
-        store_vals(o + p.b, hi);
-        if (is_k && u == 0) {
-            const long long to = ((long long)seq * kv.n_heads + h) * a.acc_stride + slot;
-            if (a.acc) a.acc[to] = 0.f;
-            if (a.slot_pos) a.slot_pos[to] = pos;
-        }
-    };
-    if (deal.heads_per == kHeadsPer && h0 + kHeadsPer <= heads) {
-        Vals<N> lo[kHeadsPer], hi[kHeadsPer];
 #pragma unroll
-        for (int i = 0; i < kHeadsPer; ++i) {
-            const float *x = source(h0 + i);
-            lo[i] = load_vals<N>(x + p.a);
-            hi[i] = load_vals<N>(x + p.b);
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) {
+            const int head = h0 + i;
+            const bool is_q = head < a.h_q, is_k = !is_q && head < a.h_q + kv.n_heads;
+            if (p.turn && (is_q || is_k)) turn<N>(lo[i], hi[i], cs, r.flags);
+            if (is_q) {
+                float *o = a.q_out + t * a.q_out_stride + (long long)head * r.head_dim;
+                store_vals(o + p.a, lo[i]);
+                store_vals(o + p.b, hi[i]);
+                continue;
+            }
+            const int h = head - a.h_q - (is_k ? 0 : kv.n_heads);
+            T *o = reinterpret_cast<T *>((is_k ? kv.k : kv.v) + row + h * kv.head_stride);
+            store_vals(o + p.a, lo[i]);
+            store_vals(o + p.b, hi[i]);
+            if (is_k && u == 0) {
+                const long long to = ((long long)seq * kv.n_heads + h) * a.acc_stride + slot;
+                if (a.acc) a.acc[to] = 0.f;
+                if (a.slot_pos) a.slot_pos[to] = pos;
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kHeadsPer; ++i) one(h0 + i, lo[i], hi[i]);
-        return;
-    }
-    for (int head = h0; head < min(h0 + deal.heads_per, heads); ++head) {
-        const float *x = source(head);
-        Vals<N> lo = load_vals<N>(x + p.a), hi = load_vals<N>(x + p.b);
-        one(head, lo, hi);
-    }
 }
 
 bool all16(std::initializer_list<const void *> ps, std::initializer_list<long long> strides) {
