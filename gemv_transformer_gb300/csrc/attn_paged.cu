@@ -84,10 +84,13 @@ __device__ __forceinline__ long long div_any(long long a, long long b) {
     return a / b;
 }
 
-// The schedule that every CTA derives from the lengths: rows of sequence s have
-// tiles(s) tiles each, never 0 (an empty row is written too).
+// The schedule that every CTA derives from the lengths: a row of sequence s costs
+// tiles(s) + kRowCost, a tile 1 and the end of a row (the warps meet, new queries) kRowCost;
+// tiles(s) is never 0 (an empty row is written too).
+// Measured on 64 sequences of 1 to 8192 slots: cost 0 207 us, 1 188 us, 2 183 us.
+constexpr int kRowCost = 2;
 struct Sched {
-    long long total, q, r;  // tiles of all rows; total / grid and the rest
+    long long total, q, r;  // cost of all rows; total / grid and the rest
     __device__ __forceinline__ Sched(long long t, int grid)
         : total(t), q(div_any(t, grid)), r(t - q * grid) {}
     __device__ __forceinline__ long long start(int b) const { return b * q + min((long long)b, r); }
@@ -116,10 +119,6 @@ __device__ __forceinline__ uint32_t tf32(float x) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
-// x - hi, the part that hi leaves; an infinity is left to hi.
-__device__ __forceinline__ float rest(float x, float hi) {
-    return fabsf(hi) == INFINITY ? 0.f : x - hi;
-}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -128,21 +127,20 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// The terms of a pair, packed: t[0] + t[1] (+ t[2]) = (x, y).  `finite`: no infinities.
-template <int DT, bool finite>
+// The terms of a pair, packed: t[0] + t[1] (+ t[2]) = (x, y).
+template <int DT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3]) {
     if (DT == kBF16) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             t[i] = bf16x2(x, y);
-            const float hx = bf16_lo(t[i]), hy = bf16_hi(t[i]);
-            x = finite ? x - hx : rest(x, hx);
-            y = finite ? y - hy : rest(y, hy);
+            x -= bf16_lo(t[i]);
+            y -= bf16_hi(t[i]);
         }
     } else {
         t[0] = f16x2(x, y);
         const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&t[0]));
-        t[1] = finite ? f16x2(x - h.x, y - h.y) : f16x2(rest(x, h.x), rest(y, h.y));
+        t[1] = f16x2(x - h.x, y - h.y);
         t[2] = 0u;
     }
 }
@@ -175,18 +173,10 @@ __device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, 
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
               "f"(c3));
 }
-// d = a * b (+ d) with b in f32, split into its high 11 bits and the rest.
-template <bool FIRST>
-__device__ __forceinline__ void mma_f32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-    const uint32_t h0 = b0 & 0xFFFFE000u, h1 = b1 & 0xFFFFE000u;
-    if (FIRST)
-        mma_tf32(d, a, h0, h1, 0.f, 0.f, 0.f, 0.f);
-    else
-        mma_tf32(d, a, h0, h1, d[0], d[1], d[2], d[3]);
-    mma_tf32(d, a, __float_as_uint(rest(__uint_as_float(b0), __uint_as_float(h0))),
-             __float_as_uint(rest(__uint_as_float(b1), __uint_as_float(h1))), d[0], d[1], d[2],
-             d[3]);
+// An f32 value as its high 11 bits and the rest, for two tf32 products.
+__device__ __forceinline__ uint32_t high11(uint32_t x) { return x & 0xFFFFE000u; }
+__device__ __forceinline__ uint32_t rest11(uint32_t x) {
+    return __float_as_uint(__uint_as_float(x) - __uint_as_float(high11(x)));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -253,10 +243,12 @@ struct Cursor {
     }
 };
 
-// The workspace: tiles before each sequence, the parts, and for the weight sums the rows'
+// The workspace: the costs before each sequence, the parts, and for the weight sums the rows'
 // lse and every score.
 struct Room {
-    long long *before;  // [n_seq + 1], in rows' tiles (not times rows)
+    long long *before;  // [n_seq + 1], in costs of one row of each sequence
+    int4 *splits;       // [grid] the row that a CTA begins and others go on with: (sequence,
+                        // row, CTAs, the first's part); no CTAs: none
     float *parts, *lse, *scores;
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -265,6 +257,8 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part
     Room r;
     r.before = reinterpret_cast<long long *>(c);
     c += up256((size_t)(n_seq + 1) * 8);
+    r.splits = reinterpret_cast<int4 *>(c);
+    c += up256(kMaxCtas * 16);
     r.parts = reinterpret_cast<float *>(c);
     c += up256(2ull * kMaxCtas * part_floats * 4);
     r.lse = reinterpret_cast<float *>(c);
@@ -279,14 +273,16 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     attn_kernel(AttnArgs a, KvView kv, int head_tiles) {
     using S = Shape<DT, DP, HT>;
     constexpr int NT = S::NT, KT = S::KT, W = S::W, kThreads = W * 32, kStages = S::kStages;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
     const Room room = room_of(a.workspace, a.n_seq, a.h_q, S::kPart);
     const int rows = kv.n_heads * head_tiles;
+    __shared__ long long s_total;
 
     Cursor use;
-    long long left;  // tiles of this CTA
+    int left;           // cost that is left for this CTA; with clusters, tiles
+    bool leads = true;  // is this the row at the start of the CTA's range
     if (CL) {
         const int size = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
         const int id = blockIdx.x / size;
@@ -298,18 +294,18 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         if (threadIdx.x == 0 && rank == 0 && use.row == 0 && __ldg(a.lens + use.s) > a.n_slots)
             record_status(a.status, kStBadIndex);
     } else {
-        // Tiles before each thread's share of the sequences, and in all.
+        // The costs before each thread's share of the sequences, and of all.
         __shared__ long long s_scan[W], s_before;
         __shared__ int s_seq;
-        auto tiles_of = [&](int s) {
+        auto cost_of = [&](int s) {
             const Span p = span_of(a, s);
-            return max(1, (p.len - p.first + S::BT - 1) / S::BT);
+            return max(1, (p.len - p.first + S::BT - 1) / S::BT) + kRowCost;
         };
         const int share = (a.n_seq + kThreads - 1) / kThreads;
         const int s0 = min(a.n_seq, (int)threadIdx.x * share), s1 = min(a.n_seq, s0 + share);
         long long mine = 0;
         for (int s = s0; s < s1; ++s) {
-            mine += tiles_of(s);
+            mine += cost_of(s);
             if (blockIdx.x == 0 && __ldg(a.lens + s) > a.n_slots)
                 record_status(a.status, kStBadIndex);
         }
@@ -332,14 +328,18 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
             long long at = before;
             for (int s = s0; s < s1; ++s) {
                 room.before[s] = at;
-                at += tiles_of(s);
+                at += cost_of(s);
             }
             if (threadIdx.x == 0) room.before[a.n_seq] = total;
+        }
+        if (threadIdx.x == 0) {
+            room.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
+            s_total = sched.total;
         }
         if (t0 >= t1) return;
         if (t0 >= before * rows && t0 < (before + mine) * rows) {
             int s = s0;
-            for (int n; t0 >= (before + (n = tiles_of(s))) * rows; ++s) before += n;
+            for (int n; t0 >= (before + (n = cost_of(s))) * rows; ++s) before += n;
             s_seq = s;
             s_before = before;
         }
@@ -347,12 +347,18 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         use.s = s_seq;
         use.load(a, S::BT);
         const long long in = t0 - s_before * rows;
-        use.row = (int)div_any(in, use.tiles);
-        use.tile = (int)(in - (long long)use.row * use.tiles);
-        left = t1 - t0;
+        use.row = (int)div_any(in, use.tiles + kRowCost);
+        use.tile = (int)(in - (long long)use.row * (use.tiles + kRowCost));
+        left = (int)(t1 - t0);
+        if (use.tile >= use.tiles) {  // in the end of a row: the CTA before this one's
+            leads = false;
+            left -= use.tiles + kRowCost - use.tile;
+            use.tile = use.tiles - 1;
+            if (left > 0) use.next(a, rows, S::BT);
+        }
     }
     Cursor fetch = use;  // the tile whose page numbers are asked for next
-    long long to_fetch = left;
+    int to_fetch = left;
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * S::kTile;
     float *bias = reinterpret_cast<float *>(smem + S::kBias) + warp * kStages * KT;
@@ -362,34 +368,37 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     const long long v_from_k = kv.v - kv.k;
 
     // Page numbers are asked for one tile ahead of the loads that need them.
-    int ask_page = -1, ask_in = 0, ask_head = 0;
-    float ask_bias = -INFINITY;
-    bool ask_live = false;
+    struct Ask {
+        int page, in, head;
+        float bias;
+        bool live;
+    };
     auto ask = [&]() {
-        ask_live = false;
-        if (to_fetch <= 0) return;
-        --to_fetch;
+        Ask k{-1, 0, -1, -INFINITY, false};  // head -1: no tile
+        if (to_fetch <= 0) return k;
+        to_fetch -= !CL && fetch.tile + 1 == fetch.tiles ? 1 + kRowCost : 1;
         const int j = fetch.span.first + fetch.tile * S::BT + warp * KT + lane;
         if (lane < KT && j < fetch.span.len) {
             const uint32_t p = kv.page_size.div((uint32_t)j);
-            ask_page = __ldg(kv.page_table + (long long)fetch.s * kv.max_pages + p);
-            ask_in = j - (int)(p * kv.page_size.d);
-            ask_bias = a.mask ? __ldg(a.mask + fetch.s * a.mask_stride + j) : 0.f;
-            ask_live = true;
+            k.page = __ldg(kv.page_table + (long long)fetch.s * kv.max_pages + p);
+            k.in = j - (int)(p * kv.page_size.d);
+            k.bias = a.mask ? __ldg(a.mask + fetch.s * a.mask_stride + j) : 0.f;
+            k.live = true;
         }
-        ask_head = head_tiles == 1 ? fetch.row : fetch.row / head_tiles;
+        k.head = head_tiles == 1 ? fetch.row : fetch.row / head_tiles;
         fetch.next(a, rows, S::BT);
+        return k;
     };
-    auto issue = [&](int stage) {
+    auto issue = [&](int stage, const Ask &k) {
         long long at = -1;
         float b = -INFINITY;
-        if (ask_live) {
-            if ((unsigned)ask_page >= (unsigned)kv.n_pages) {
+        if (k.live) {
+            if ((unsigned)k.page >= (unsigned)kv.n_pages) {
                 record_status(a.status, kStBadIndex);
-            } else if (ask_bias != -INFINITY) {
-                b = ask_bias;
-                at = (long long)ask_page * kv.page_stride + (long long)ask_head * kv.head_stride +
-                     (long long)ask_in * kv.token_stride;
+            } else if (k.bias != -INFINITY) {
+                b = k.bias;
+                at = (long long)k.page * kv.page_stride + (long long)k.head * kv.head_stride +
+                     (long long)k.in * kv.token_stride;
             }
         }
         // All of the tile's slots are there, and their rows fill the ring's: no checks.
@@ -443,9 +452,9 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 const float2 v = q2(ht * 8 + (l >> 2), 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1));
                 uint4 f;
                 f.x = tf32(v.x);
-                f.y = tf32(rest(v.x, __uint_as_float(f.x)));
+                f.y = tf32(v.x - __uint_as_float(f.x));
                 f.z = tf32(v.y);
-                f.w = tf32(rest(v.y, __uint_as_float(f.z)));
+                f.w = tf32(v.y - __uint_as_float(f.z));
                 *reinterpret_cast<uint4 *>(smem + S::kQ + i * 16) = f;
             }
         }
@@ -478,8 +487,8 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 uint32_t t0[3], t1[3];
                 const float2 x = q2(ht * 8 + g, ks * 16 + 2 * c);
                 const float2 y = q2(ht * 8 + g, ks * 16 + 8 + 2 * c);
-                split2<DT, false>(x.x * up, x.y * up, t0);
-                split2<DT, false>(y.x * up, y.y * up, t1);
+                split2<DT>(x.x * up, x.y * up, t0);
+                split2<DT>(y.x * up, y.y * up, t1);
                 const int f = ht * S::kSteps + ks;
                 if (S::kQReg) {
                     qr[S::kQReg ? f : 0][0] = t0[0];
@@ -508,15 +517,23 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 back[h] = reinterpret_cast<const float *>(smem + S::kScale)[h * 8 + g];
     };
 
-    ask();
+    // The first tiles' page numbers and the queries are on their way together, ahead of
+    // the tiles, whose loads would hold them up.
+    Ask asked[kStages];
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) asked[st] = ask();
+    load_q(use);
 #pragma unroll
     for (int st = 0; st < kStages; ++st) {
-        issue(st);
+        issue(st, asked[st]);
         cp_async_commit();
-        ask();
     }
-    load_q(use);
+    Ask next_ask = ask();
     __syncthreads();
+    // The join's blocks wait beside the last of these CTAs.  They in turn let the next kernel
+    // in only when they are done: with both early, CTAs of a next call wait beside these and
+    // 131072 slots back to back take 130 us in place of 93.
+    if (!CL) pdl_launch();
     take_scales();
 
     constexpr int OI = DP / 8;  // 16-bit: o[i] = dims 8 i + 2 c, + 1; f32: see its loop
@@ -532,7 +549,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     };
     clear();
     bool whole = use.tile == 0;  // does this CTA have the row from its first tile
-    bool leads = true;           // is this the CTA's first row
     int stage = 0;
     const int mat = lane >> 3, mrow = lane & 7;  // ldmatrix: this lane's matrix and row
 
@@ -577,21 +593,33 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 }
             }
         } else {
+            float lo[HT][2][4] = {};
 #pragma unroll
             for (int i = 0; i < S::kChunks / 4; ++i) {
                 if (4 * i >= live_chunks) break;
                 const uint4 v = lds128(kb + g * S::kRow + (((4 * i + c) ^ swizzle_k<DT>(g)) << 4));
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int h = 0; h < HT; ++h)
 #pragma unroll
-                    for (int h = 0; h < HT; ++h) {
+                    for (int j = 0; j < 2; ++j) {
                         const uint4 f = lds128(smem_addr(smem) + S::kQ +
                                                ((h * S::kSteps + 2 * i + j) * 32 + lane) * 16);
                         const uint32_t q[4] = {f.x, f.y, f.z, f.w};
-                        mma_f32<false>(sc[h][0][j], q, w[2 * j], w[2 * j + 1]);
+                        // Four sums: high and low parts, even and odd steps.
+                        float(&x)[4] = sc[h][0][j], (&y)[4] = lo[h][j];
+                        mma_tf32(x, q, high11(w[2 * j]), high11(w[2 * j + 1]), x[0], x[1], x[2],
+                                 x[3]);
+                        mma_tf32(y, q, rest11(w[2 * j]), rest11(w[2 * j + 1]), y[0], y[1], y[2],
+                                 y[3]);
                     }
             }
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[h][0][j][i] += lo[h][j][i];
         }
         uint32_t pt[HT][2][3];  // 16-bit: the terms of p at slots 2c, 2c + 1 (+ 8)
         uint32_t pf[HT][4];     // f32: p's fragment
@@ -641,7 +669,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 }
                 sum += p0 + p1;
                 if (S::k16) {
-                    split2<DT, true>(p0, p1, pt[h][n]);
+                    split2<DT>(p0, p1, pt[h][n]);
                 } else {
                     pf[h][0] = tf32(p0);
                     pf[h][1] = tf32(p0 - __uint_as_float(pf[h][0]));
@@ -693,15 +721,22 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 const uint4 v0 = lds128(at), v1 = lds128(at + S::kRow);
                 const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int h = 0; h < HT; ++h) {
+                    float t[4][4];
 #pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        float t[4];
-                        mma_f32<true>(t, pf[h], w0[e], w1[e]);
+                    for (int e = 0; e < 4; ++e)
+                        mma_tf32(t[e], pf[h], high11(w0[e]), high11(w1[e]), 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mma_tf32(t[e], pf[h], rest11(w0[e]), rest11(w1[e]), t[e][0], t[e][1],
+                                 t[e][2], t[e][3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         float(&to)[2] = o[h][i * 4 + e];
-                        to[0] = to[0] * corr[h] + (t[0] + t[2]);
-                        to[1] = to[1] * corr[h] + (t[1] + t[3]);
+                        to[0] = to[0] * corr[h] + (t[e][0] + t[e][2]);
+                        to[1] = to[1] * corr[h] + (t[e][1] + t[e][3]);
                     }
+                }
             }
         }
     };
@@ -794,14 +829,23 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         }
     };
 
+    // The CTA of the last tile of the row that this CTA leaves unfinished.
+    auto owner_of_end = [&]() {
+        const Sched sched(s_total, gridDim.x);
+        return sched.owner(sched.start(blockIdx.x + 1) - 1 + (use.tiles - 1 - use.tile));
+    };
+
     const int first_tile = use.tile;
-    for (; left > 0; --left) {
+    while (left > 0) {
         cp_async_wait<kStages - 1>();
         __syncwarp();
         step();
-        const bool ends = use.tile + 1 == use.tiles, last = left == 1;
+        const bool ends = use.tile + 1 == use.tiles;
+        left -= !CL && ends ? 1 + kRowCost : 1;
+        const bool last = left <= 0;
         if (!CL && (ends || last)) {
             meet();
+            const bool begins = whole;  // the row's first tile is this CTA's
             whole = whole && ends;
             float *part = room.parts + (2ll * blockIdx.x + (leads ? 0 : 1)) * S::kPart;
             for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kThreads) {
@@ -816,6 +860,10 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 part[threadIdx.x] = s_top[threadIdx.x];
                 part[S::kHeads + threadIdx.x] = s_sum[threadIdx.x];
             }
+            if (!ends && begins && threadIdx.x == 0)
+                room.splits[blockIdx.x] =
+                    make_int4(use.s, use.row, owner_of_end() - (int)blockIdx.x + 1,
+                              leads ? 0 : 1);
             clear();
             leads = false;
             whole = true;
@@ -827,18 +875,16 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
             __syncthreads();
             take_scales();
         }
-        if (!CL || left > 1) {
+        if (!CL || !last) {
             use.next(a, rows, S::BT);
             __syncwarp();
-            if (left > kStages) issue(stage);
+            if (next_ask.head >= 0) issue(stage, next_ask);
             cp_async_commit();
-            ask();
+            next_ask = ask();
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
     }
-    // Not before: CTAs of the next kernel that wait beside these cost a third of the rate
-    // (131072 slots back to back: 130 us with the launch at the top, 96 us here).
-    pdl_launch();
+    if (CL) pdl_launch();
     cp_async_wait<0>();
     if (CL) {
         // Every CTA of the cluster, also one without tiles, shows its part; each then joins
@@ -908,122 +954,166 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     }
 }
 
-// After the split kernel: joins the parts of the rows that several CTAs shared, and sums the
-// weights, acc_out[s][h][j] = acc_in + sum over the group's heads of exp(x_j - lse).
-// Block (sequence and kv head, y): query head y of the group, and the y-th of `chunks`
-// pieces of the slots.
-constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnArgs a, int n_heads,
-                                                                    int head_dim, int head_tiles,
-                                                                    int heads, int dp, int grid,
-                                                                    int chunks) {
+// m and l of a row's head joined over n parts by one warp; the parts' factors go to f if given.
+template <typename Part>
+__device__ __forceinline__ void join_head(int n, int head, int heads, Part part, float *f,
+                                          float &top, float &sum) {
+    const int lane = threadIdx.x & 31;
+    float m[2], l[2];  // the first 64 parts' at once
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = lane + 32 * u;
+        m[u] = i < n ? part(i)[head] : -INFINITY;
+        l[u] = i < n ? part(i)[heads + head] : 0.f;
+    }
+    top = fmaxf(m[0], m[1]);
+    for (int i = lane + 64; i < n; i += 32) top = fmaxf(top, part(i)[head]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const float x = exp_diff(m[u], top);
+        if (f && lane + 32 * u < n) f[lane + 32 * u] = x;
+        sum += x * l[u];
+    }
+    for (int i = lane + 64; i < n; i += 32) {
+        const float x = exp_diff(part(i)[head], top);
+        if (f) f[i] = x;
+        sum += x * part(i)[heads + head];
+    }
+    sum = warp_sum(sum);
+}
+
+__device__ __forceinline__ float lse_of(float top, float sum) {
+    return top == -INFINITY && sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+// After the split kernel.  The first grid * row_heads blocks join the parts of the rows that
+// several CTAs shared: block (CTA, head) the row that the CTA begins.  The others sum the
+// weights, acc_out[s][h][j] = acc_in + sum over the group's heads of exp(x_j - lse): block
+// (sequence and kv head, piece of the slots).  Both are chains of loads that wait for one
+// another, so whatever does not wait (the parts' o, the scores) is asked for before it is
+// known what it is worth.
+constexpr int kJoinWarps = 8, kAhead = 4;
+constexpr int kSlotsPer = 4, kPiece = kSlotsPer * kJoinWarps * 32;  // slots of a block
+__global__ void __launch_bounds__(kJoinWarps * 32, 4)
+    attn_join_kernel(AttnArgs a, int n_heads, int head_dim, int head_tiles, int heads, int dp,
+                     int grid, int row_heads, int pieces) {
     __shared__ float s_f[kMaxCtas];
     __shared__ float4 s_o[kJoinWarps][64];
     __shared__ float s_red[2];
     extern __shared__ float s_lse[];  // [group], for the weight sums
-    pdl_enter();
+    pdl_wait();
     const int part_floats = heads * (dp + 2);
     const Room room = room_of(a.workspace, a.n_seq, a.h_q, part_floats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / n_heads, h = blockIdx.x - s * n_heads;
-    const int rows = n_heads * head_tiles;
-    const long long b0 = room.before[s], tiles = room.before[s + 1] - b0;
-    const Sched sched(room.before[a.n_seq] * rows, grid);
-
-    // The parts of one of the group's heads: their number, 1 for a row within one CTA.
-    struct Parts {
-        int first, n, skip, head;
-    };
-    auto parts_of = [&](int in_group) {
-        const int ht = in_group / heads;
-        const long long r0 = b0 * rows + (long long)(h * head_tiles + ht) * tiles;
-        Parts p;
-        p.first = sched.owner(r0);
-        p.n = sched.owner(r0 + tiles - 1) - p.first + 1;
-        p.skip = r0 > sched.start(p.first) ? 1 : 0;
-        p.head = in_group - ht * heads;
-        return p;
-    };
-    auto part = [&](const Parts &p, int i) {
-        return room.parts + (2ll * (p.first + i) + (i == 0 ? p.skip : 0)) * part_floats;
-    };
-    // m and l of a head, by one warp; factors go to f if given.
-    auto join_head = [&](const Parts &p, float *f, float &top, float &sum) {
-        top = -INFINITY;
-        for (int i = lane; i < p.n; i += 32) top = fmaxf(top, part(p, i)[p.head]);
+    if ((int)blockIdx.x < grid * row_heads) {
+        const int cta = blockIdx.x / row_heads, head = blockIdx.x - cta * row_heads;
+        const int4 split = room.splits[cta];
+        const int s = split.x, n = split.z;
+        const int h = split.y / head_tiles, in_group = (split.y - h * head_tiles) * heads + head;
+        if (n == 0 || in_group >= a.group) return;
+        auto part = [&](int i) {
+            return room.parts + (2ll * (cta + i) + (i == 0 ? split.w : 0)) * part_floats;
+        };
+        const int quads = head_dim / 4;
+        auto o_of = [&](int i, int q) {
+            return *reinterpret_cast<const float4 *>(part(i) + 2 * heads + head * dp + 4 * q);
+        };
+        float4 ahead[kAhead];  // this warp's first parts of dims 4 lane ..
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        sum = 0.f;
-        for (int i = lane; i < p.n; i += 32) {
-            const float x = exp_diff(part(p, i)[p.head], top);
-            if (f) f[i] = x;
-            sum += x * part(p, i)[heads + p.head];
-        }
-        sum = warp_sum(sum);
-    };
-    auto lse_of = [](float top, float sum) {
-        return top == -INFINITY && sum == 0.f ? -INFINITY : top + logf(sum);
-    };
-
-    if ((int)blockIdx.y < a.group) {
-        const Parts p = parts_of(blockIdx.y);
-        if (p.n > 1) {
-            if (warp == 0) {
-                float top, sum;
-                join_head(p, s_f, top, sum);
-                if (lane == 0) {
-                    s_red[0] = top;
-                    s_red[1] = sum;
-                }
-            }
-            // o's loads do not wait for the factors' maximum but for the barrier.
-            __syncthreads();
-            const float top = s_red[0], sum = s_red[1];
-            const bool none = top == -INFINITY && sum == 0.f;
-            const int qh = h * a.group + blockIdx.y;
-            for (int q0 = 0; q0 < head_dim / 4; q0 += 32) {
-                const int q = q0 + lane;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (q < head_dim / 4) {
-#pragma unroll 4
-                    for (int i = warp; i < p.n; i += kJoinWarps) {
-                        const float f = s_f[i];
-                        const float4 x = *reinterpret_cast<const float4 *>(
-                            part(p, i) + 2 * heads + p.head * dp + 4 * q);
-                        v.x += f * x.x;
-                        v.y += f * x.y;
-                        v.z += f * x.z;
-                        v.w += f * x.w;
-                    }
-                }
-                s_o[warp][q & 63] = v;
-            }
-            __syncthreads();
-            for (int q = threadIdx.x; q < head_dim / 4; q += kJoinWarps * 32) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float inv = none ? 0.f : 1.f / sum;
-                for (int w = 0; w < kJoinWarps; ++w) {
-                    v.x += s_o[w][q].x;
-                    v.y += s_o[w][q].y;
-                    v.z += s_o[w][q].z;
-                    v.w += s_o[w][q].w;
-                }
-                *reinterpret_cast<float4 *>(a.out + s * a.out_stride + (long long)qh * head_dim +
-                                            4 * q) =
-                    none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                         : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            }
-            if (threadIdx.x == 0 && a.lse) a.lse[(long long)s * a.h_q + qh] = lse_of(top, sum);
-        }
-    }
-    if (!a.acc_out || (int)blockIdx.y >= chunks) return;
-    const long long q0 = (long long)s * a.h_q + h * a.group;
-    for (int i = warp; i < a.group; i += kJoinWarps) {
-        const Parts p = parts_of(i);
-        float e;
-        if (p.n > 1) {
+        for (int u = 0; u < kAhead; ++u)
+            if (warp + u * kJoinWarps < n && lane < quads) ahead[u] = o_of(warp + u * kJoinWarps, lane);
+        if (warp == 0) {
             float top, sum;
-            join_head(p, nullptr, top, sum);
+            join_head(n, head, heads, part, s_f, top, sum);
+            if (lane == 0) {
+                s_red[0] = top;
+                s_red[1] = sum;
+            }
+        }
+        __syncthreads();
+        const float top = s_red[0], sum = s_red[1];
+        const bool none = top == -INFINITY && sum == 0.f;
+        const int qh = h * a.group + in_group;
+        for (int q = lane; q < quads; q += 32) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto add = [&](const float4 &x, float f) {
+                v.x += f * x.x;
+                v.y += f * x.y;
+                v.z += f * x.z;
+                v.w += f * x.w;
+            };
+            int i = warp;
+            if (q == lane) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (warp + u * kJoinWarps < n) add(ahead[u], s_f[warp + u * kJoinWarps]);
+                i += kAhead * kJoinWarps;
+            }
+#pragma unroll 4
+            for (; i < n; i += kJoinWarps) add(o_of(i, q), s_f[i]);
+            s_o[warp][q] = v;
+        }
+        __syncthreads();
+        for (int q = threadIdx.x; q < quads; q += kJoinWarps * 32) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                v.x += s_o[w][q].x;
+                v.y += s_o[w][q].y;
+                v.z += s_o[w][q].z;
+                v.w += s_o[w][q].w;
+            }
+            *reinterpret_cast<float4 *>(a.out + s * a.out_stride + (long long)qh * head_dim +
+                                        4 * q) =
+                none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
+        if (threadIdx.x == 0 && a.lse) a.lse[(long long)s * a.h_q + qh] = lse_of(top, sum);
+        return;
+    }
+
+    const int id = (blockIdx.x - grid * row_heads) / pieces;
+    const int piece = blockIdx.x - grid * row_heads - id * pieces;
+    const int s = id / n_heads, h = id - s * n_heads;
+    const Span span = span_of(a, s);
+    const int j0 = piece * kPiece + threadIdx.x;
+    if (piece * kPiece >= span.len) return;
+    const long long q0 = (long long)s * a.h_q + h * a.group;
+    const long long at = (long long)id * a.acc_stride;
+    auto score = [&](int i, int j) {  // of slots that take part; the others have none
+        return j < span.len && j >= span.first ? room.scores[(q0 + i) * a.n_slots + j] : -INFINITY;
+    };
+    float ahead[kSlotsPer][kAhead], w[kSlotsPer];
+#pragma unroll
+    for (int u = 0; u < kSlotsPer; ++u) {
+        const int j = j0 + u * kJoinWarps * 32;
+        w[u] = a.acc_in && j < span.len ? a.acc_in[at + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ahead[u][i] = i < a.group ? score(i, j) : -INFINITY;
+    }
+    // The group's lse: whole rows have theirs, the others' parts are found from the schedule.
+    const int rows = n_heads * head_tiles;
+    const long long b0 = room.before[s], cost = room.before[s + 1] - b0;
+    const Sched sched(room.before[a.n_seq] * rows, grid);
+    for (int i = warp; i < a.group; i += kJoinWarps) {
+        const int ht = i / heads;
+        const long long r0 = b0 * rows + (long long)(h * head_tiles + ht) * cost;
+        const int first = sched.owner(r0);
+        const int n = sched.owner(r0 + cost - kRowCost - 1) - first + 1;
+        const int skip = r0 > sched.start(first) ? 1 : 0;
+        float e;
+        if (n > 1) {
+            float top, sum;
+            join_head(
+                n, i - ht * heads, heads,
+                [&](int k) {
+                    return room.parts + (2ll * (first + k) + (k == 0 ? skip : 0)) * part_floats;
+                },
+                nullptr, top, sum);
             e = lse_of(top, sum);
         } else {
             e = room.lse[q0 + i];
@@ -1031,19 +1121,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnArgs a, 
         if (lane == 0) s_lse[i] = e;
     }
     __syncthreads();
-    const Span span = span_of(a, s);
-    const long long at = ((long long)s * n_heads + h) * a.acc_stride;
-    for (int j = blockIdx.y * kJoinWarps * 32 + threadIdx.x; j < span.len;
-         j += chunks * kJoinWarps * 32) {
-        float w = 0.f;
-        if (j >= span.first) {
+#pragma unroll
+    for (int u = 0; u < kSlotsPer; ++u) {
+        const int j = j0 + u * kJoinWarps * 32;
+        if (j >= span.len) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < a.group && s_lse[i] != -INFINITY) sum += exp_diff(ahead[u][i], s_lse[i]);
 #pragma unroll 4
-            for (int i = 0; i < a.group; ++i) {
-                const float x = room.scores[(q0 + i) * a.n_slots + j], e = s_lse[i];
-                w += e == -INFINITY ? 0.f : exp_diff(x, e);
-            }
+        for (int i = kAhead; i < a.group; ++i) {
+            const float x = score(i, j), e = s_lse[i];
+            sum += e == -INFINITY ? 0.f : exp_diff(x, e);
         }
-        a.acc_out[at + j] = (a.acc_in ? a.acc_in[at + j] : 0.f) + w;
+        a.acc_out[at + j] = w[u] + sum;
     }
 }
 
@@ -1100,11 +1191,13 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     err = launch_pdl(attn_kernel<DT, DP, HT, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
                      a, kv, head_tiles);
     if (err != cudaSuccess) return err;
-    const int chunks = a.acc_out ? min(64, (int)((a.n_slots + 511ll) / 512)) : 0;
-    return launch_pdl(attn_join_kernel,
-                      dim3((unsigned)(a.n_seq * kv.n_heads), max(a.group, chunks)),
-                      dim3(kJoinWarps * 32), a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads,
-                      kv.head_dim, head_tiles, S::kHeads, DP, slots, chunks);
+    const int row_heads = min(a.group, S::kHeads);
+    const int pieces = a.acc_out ? (int)((a.n_slots + (long long)kPiece - 1) / kPiece) : 0;
+    const long long blocks = (long long)slots * row_heads + (long long)a.n_seq * kv.n_heads * pieces;
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    return launch_pdl(attn_join_kernel, dim3((unsigned)blocks), dim3(kJoinWarps * 32),
+                      a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads, kv.head_dim, head_tiles,
+                      S::kHeads, DP, slots, row_heads, pieces);
 }
 
 template <int DT>
@@ -1126,7 +1219,7 @@ cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &d
 
 size_t attn_workspace_bytes(const KvView &kv, int n_seq, int h_q, int n_slots, bool with_acc) {
     const int dp = padded_dim(kv.head_dim), ht = head_tile(h_q / kv.n_heads, dp, kv.dtype);
-    size_t bytes = up256((size_t)(n_seq + 1) * 8) +
+    size_t bytes = up256((size_t)(n_seq + 1) * 8) + up256(kMaxCtas * 16) +
                    up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4);
     if (with_acc)
         bytes += up256((size_t)n_seq * h_q * 4) + up256((size_t)n_seq * h_q * n_slots * 4);
