@@ -243,10 +243,11 @@ struct Cursor {
     }
 };
 
-// The workspace: the costs before each sequence, the parts, and for the weight sums the rows'
-// lse and every score.
+// The workspace: the rows that are split, their parts, and for the weight sums where each row
+// is, its heads' lse and every score.
 struct Room {
-    long long *before;  // [n_seq + 1], in costs of one row of each sequence
+    int4 *rows;         // [n_seq * rows], for the weight sums: the row's first CTA, its CTAs,
+                        // the first's part
     int4 *splits;       // [grid] the row that a CTA begins and others go on with: (sequence,
                         // row, CTAs, the first's part); no CTAs: none
     float *parts, *lse, *scores;
@@ -255,12 +256,12 @@ __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)
 __host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part_floats) {
     char *c = static_cast<char *>(p);
     Room r;
-    r.before = reinterpret_cast<long long *>(c);
-    c += up256((size_t)(n_seq + 1) * 8);
     r.splits = reinterpret_cast<int4 *>(c);
     c += up256(kMaxCtas * 16);
     r.parts = reinterpret_cast<float *>(c);
     c += up256(2ull * kMaxCtas * part_floats * 4);
+    r.rows = reinterpret_cast<int4 *>(c);  // a row has a head at least
+    c += up256((size_t)n_seq * h_q * 16);
     r.lse = reinterpret_cast<float *>(c);
     c += up256((size_t)n_seq * h_q * 4);
     r.scores = reinterpret_cast<float *>(c);
@@ -324,14 +325,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         }
         const Sched sched(total * rows, gridDim.x);
         const long long t0 = sched.start(blockIdx.x), t1 = sched.start(blockIdx.x + 1);
-        if (blockIdx.x == 0) {
-            long long at = before;
-            for (int s = s0; s < s1; ++s) {
-                room.before[s] = at;
-                at += cost_of(s);
-            }
-            if (threadIdx.x == 0) room.before[a.n_seq] = total;
-        }
         if (threadIdx.x == 0) {
             room.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
             s_total = sched.total;
@@ -432,45 +425,63 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
 
     // The row's query heads, scaled, as the first product's operand: rows g and g + 8 of a
     // fragment are the first two terms of head g.  In registers where they fit: every warp
-    // makes its own.  f16: `back` undoes the power of two that brings q near 2^10.
+    // makes its own.  Else a 16-bit head tile is made by one warp, f32 ones by all.
+    // f16: `back` undoes the power of two that brings q near 2^10.
     uint32_t qr[S::kQReg ? HT * S::kSteps : 1][S::kQWords];
     float back[HT];
-    auto load_q = [&](const Cursor &at) {
+    // Asked for first and turned into operands later, so that other loads go in between.
+    constexpr int kRaw = S::kQReg ? HT * S::kSteps * 2
+                         : S::k16 ? S::kSteps * 2
+                                  : (HT * S::kSteps * 32 + kThreads - 1) / kThreads;
+    float2 raw[kRaw];
+    auto fetch_q = [&](const Cursor &at) {
         const int h = at.row / head_tiles, ht0 = (at.row - h * head_tiles) * S::kHeads;
         const float *q0 = a.q + at.s * a.q_stride + ((long long)h * a.group + ht0) * kv.head_dim;
         auto q2 = [&](int head, int dim) {
-            float2 v = make_float2(0.f, 0.f);
-            if (ht0 + head < a.group && dim < kv.head_dim)
-                v = *reinterpret_cast<const float2 *>(q0 + head * kv.head_dim + dim);
-            v.x *= a.scale;
-            v.y *= a.scale;
-            return v;
+            return ht0 + head < a.group && dim < kv.head_dim
+                       ? __ldg(reinterpret_cast<const float2 *>(q0 + head * kv.head_dim + dim))
+                       : make_float2(0.f, 0.f);
         };
-        if (!S::k16) {  // tf32: lane's dims are those of its 16-byte chunks of a key
-            for (int i = threadIdx.x; i < HT * S::kSteps * 32; i += kThreads) {
-                const int l = i & 31, ks = (i >> 5) % S::kSteps, ht = (i >> 5) / S::kSteps;
-                const float2 v = q2(ht * 8 + (l >> 2), 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1));
-                uint4 f;
-                f.x = tf32(v.x);
-                f.y = tf32(v.x - __uint_as_float(f.x));
-                f.z = tf32(v.y);
-                f.w = tf32(v.y - __uint_as_float(f.z));
-                *reinterpret_cast<uint4 *>(smem + S::kQ + i * 16) = f;
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i) {
+            if (S::k16) {
+                const int ht = S::kQReg ? i / (2 * S::kSteps) : warp;
+                if (ht >= HT) break;
+                raw[i] = q2(ht * 8 + g, i % (2 * S::kSteps) * 8 + 2 * c);
+            } else {  // tf32: a lane's dims are those of its 16-byte chunks of a key
+                const int f = i * kThreads + threadIdx.x;
+                const int l = f & 31, ks = (f >> 5) % S::kSteps, ht = (f >> 5) / S::kSteps;
+                if (ht < HT)
+                    raw[i] = q2(ht * 8 + (l >> 2), 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1));
+            }
+        }
+    };
+    auto make_q = [&]() {
+        if (!S::k16) {
+#pragma unroll
+            for (int i = 0; i < kRaw; ++i) {
+                const int f = i * kThreads + threadIdx.x;
+                if (f >= HT * S::kSteps * 32) break;
+                const float x = raw[i].x * a.scale, y = raw[i].y * a.scale;
+                uint4 t;
+                t.x = tf32(x);
+                t.y = tf32(x - __uint_as_float(t.x));
+                t.z = tf32(y);
+                t.w = tf32(y - __uint_as_float(t.z));
+                *reinterpret_cast<uint4 *>(smem + S::kQ + f * 16) = t;
             }
         }
 #pragma unroll
-        for (int ht = 0; ht < (S::k16 ? HT : 0); ++ht) {
-            if (!S::kQReg && ht != warp) continue;  // HT <= W
+        for (int u = 0; u < (S::kQReg ? HT : S::k16 ? 1 : 0); ++u) {
+            const int ht = S::kQReg ? u : warp;
+            if (ht >= HT) break;
+            const float2 *r = raw + (S::kQReg ? u * S::kSteps * 2 : 0);
             float up = 1.f;
             if (DT == kF16) {
                 float top = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < S::kSteps; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 v = q2(ht * 8 + g, ks * 16 + i * 8 + 2 * c);
-                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                    }
+                for (int i = 0; i < S::kSteps * 2; ++i)
+                    top = fmaxf(top, fmaxf(fabsf(r[i].x * a.scale), fabsf(r[i].y * a.scale)));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                 int e = 0;
@@ -478,27 +489,21 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 up = exp2f((float)(10 - e));
                 const float down = exp2f((float)(e - 10));
                 if (S::kQReg)
-                    back[ht] = down;
+                    back[u] = down;
                 else if (c == 0)
                     reinterpret_cast<float *>(smem + S::kScale)[ht * 8 + g] = down;
             }
 #pragma unroll
             for (int ks = 0; ks < S::kSteps; ++ks) {
                 uint32_t t0[3], t1[3];
-                const float2 x = q2(ht * 8 + g, ks * 16 + 2 * c);
-                const float2 y = q2(ht * 8 + g, ks * 16 + 8 + 2 * c);
-                split2<DT>(x.x * up, x.y * up, t0);
-                split2<DT>(y.x * up, y.y * up, t1);
+                const float2 x = r[2 * ks], y = r[2 * ks + 1];
+                split2<DT>(x.x * a.scale * up, x.y * a.scale * up, t0);
+                split2<DT>(y.x * a.scale * up, y.y * a.scale * up, t1);
                 const int f = ht * S::kSteps + ks;
                 if (S::kQReg) {
-                    qr[S::kQReg ? f : 0][0] = t0[0];
-                    qr[S::kQReg ? f : 0][1] = t0[1];
-                    qr[S::kQReg ? f : 0][2] = t1[0];
-                    qr[S::kQReg ? f : 0][3] = t1[1];
-                    if (DT == kBF16) {
-                        qr[S::kQReg ? f : 0][4 % S::kQWords] = t0[2];
-                        qr[S::kQReg ? f : 0][5 % S::kQWords] = t1[2];
-                    }
+                    uint32_t(&q)[S::kQWords] = qr[S::kQReg ? u * S::kSteps + ks : 0];
+                    q[0] = t0[0], q[1] = t0[1], q[2] = t1[0], q[3] = t1[1];
+                    if (DT == kBF16) q[4 % S::kQWords] = t0[2], q[5 % S::kQWords] = t1[2];
                 } else {
                     *reinterpret_cast<uint4 *>(smem + S::kQ + (f * 32 + lane) * 16) =
                         make_uint4(t0[0], t0[1], t1[0], t1[1]);
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
             }
         }
     };
-    // After the barrier that follows load_q.
+    // After the barrier that follows make_q.
     auto take_scales = [&]() {
         if (DT == kF16 && !S::kQReg)
 #pragma unroll
@@ -522,13 +527,14 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
     Ask asked[kStages];
 #pragma unroll
     for (int st = 0; st < kStages; ++st) asked[st] = ask();
-    load_q(use);
+    fetch_q(use);
 #pragma unroll
     for (int st = 0; st < kStages; ++st) {
         issue(st, asked[st]);
         cp_async_commit();
     }
     Ask next_ask = ask();
+    make_q();
     __syncthreads();
     // The join's blocks wait beside the last of these CTAs.  They in turn let the next kernel
     // in only when they are done: with both early, CTAs of a next call wait beside these and
@@ -650,8 +656,12 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const int j = use.span.first + use.tile * S::BT + warp * KT + n * 8 + 2 * c;
-                        if (j < use.span.len) to[j] = xs[n][0];
-                        if (j + 1 < use.span.len) to[j + 1] = xs[n][1];
+                        if (!((use.span.first | a.n_slots) & 1) && j + 1 < use.span.len) {
+                            *reinterpret_cast<float2 *>(to + j) = make_float2(xs[n][0], xs[n][1]);
+                        } else {
+                            if (j < use.span.len) to[j] = xs[n][0];
+                            if (j + 1 < use.span.len) to[j + 1] = xs[n][1];
+                        }
                     }
                 }
             }
@@ -860,17 +870,21 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 part[threadIdx.x] = s_top[threadIdx.x];
                 part[S::kHeads + threadIdx.x] = s_sum[threadIdx.x];
             }
-            if (!ends && begins && threadIdx.x == 0)
-                room.splits[blockIdx.x] =
-                    make_int4(use.s, use.row, owner_of_end() - (int)blockIdx.x + 1,
-                              leads ? 0 : 1);
+            if (begins && threadIdx.x == 0) {
+                const int n = ends ? 1 : owner_of_end() - (int)blockIdx.x + 1;
+                if (n > 1) room.splits[blockIdx.x] = make_int4(use.s, use.row, n, leads ? 0 : 1);
+                if (a.acc_out)
+                    room.rows[(long long)use.s * rows + use.row] =
+                        make_int4(blockIdx.x, n, leads ? 0 : 1, 0);
+            }
             clear();
             leads = false;
             whole = true;
             if (!last) {
                 Cursor nx = use;
                 nx.next(a, rows, S::BT);
-                load_q(nx);
+                fetch_q(nx);
+                make_q();
             }
             __syncthreads();
             take_scales();
@@ -1095,16 +1109,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) ahead[u][i] = i < a.group ? score(i, j) : -INFINITY;
     }
-    // The group's lse: whole rows have theirs, the others' parts are found from the schedule.
-    const int rows = n_heads * head_tiles;
-    const long long b0 = room.before[s], cost = room.before[s + 1] - b0;
-    const Sched sched(room.before[a.n_seq] * rows, grid);
+    // The group's lse: whole rows have theirs.
     for (int i = warp; i < a.group; i += kJoinWarps) {
         const int ht = i / heads;
-        const long long r0 = b0 * rows + (long long)(h * head_tiles + ht) * cost;
-        const int first = sched.owner(r0);
-        const int n = sched.owner(r0 + cost - kRowCost - 1) - first + 1;
-        const int skip = r0 > sched.start(first) ? 1 : 0;
+        const float whole = room.lse[q0 + i];  // of a split row: whatever is there, not used
+        const int4 row = room.rows[(long long)id * head_tiles + ht];
+        const int first = row.x, n = row.y, skip = row.z;
         float e;
         if (n > 1) {
             float top, sum;
@@ -1116,7 +1126,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
                 nullptr, top, sum);
             e = lse_of(top, sum);
         } else {
-            e = room.lse[q0 + i];
+            e = whole;
         }
         if (lane == 0) s_lse[i] = e;
     }
@@ -1219,10 +1229,10 @@ cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &d
 
 size_t attn_workspace_bytes(const KvView &kv, int n_seq, int h_q, int n_slots, bool with_acc) {
     const int dp = padded_dim(kv.head_dim), ht = head_tile(h_q / kv.n_heads, dp, kv.dtype);
-    size_t bytes = up256((size_t)(n_seq + 1) * 8) + up256(kMaxCtas * 16) +
-                   up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4);
+    size_t bytes = up256(kMaxCtas * 16) + up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4);
     if (with_acc)
-        bytes += up256((size_t)n_seq * h_q * 4) + up256((size_t)n_seq * h_q * n_slots * 4);
+        bytes += up256((size_t)n_seq * h_q * 16) + up256((size_t)n_seq * h_q * 4) +
+                 up256((size_t)n_seq * h_q * n_slots * 4);
     return bytes;
 }
 
