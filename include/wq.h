@@ -445,6 +445,9 @@ WQ_API wq_status wq_kv_append(const wq_kv_cache *cache, int n_tok, int h_q, int 
  *   x_j = scale q . k_j + mask[s][j],   p = softmax(x),   out = sum_j p_j v_j,
  *   lse = ln sum_j exp(x_j),
  * for each of h_q query heads; query head h reads kv head h / (h_q / kv heads).
+ * Each product is within 2^-22 of exact and every sum is f32: q, k, v and p are not rounded
+ * to the cache's type.  A k that is not finite and takes part makes its query heads' results
+ * not finite, such a v its dim of them.
  * window > 0: only the last `window` live slots (by slot number) take part.
  * mask: f32 [n_seq][mask_stride] or NULL, added to the scores.  A slot with a mask of -inf takes
  * no part, whatever its k and v hold; slots at or beyond lens[s], or before the window,

@@ -296,3 +296,57 @@ def test_shared_pages():
     c.pages[1, 0] = c.pages[0, 0]
     c.pages_dev = dev(c.pages)
     check(c, lens, 4, queries(g, 2, 4, 64), 0.125)
+
+
+def test_calls_of_a_step_are_captured_in_a_graph():
+    """Append, attention and eviction allocate nothing and do not synchronise: a captured
+    step replays to the same bits."""
+    g = np.random.default_rng(17)
+    lens = [300, 41]
+    c = Cache(g, lens, 2, 64, "bf16", 16)
+    n, hq, cap = 2, 4, c.max_pages * 16
+    x = torch.randn(n, (hq + 4) * 64, generator=torch.Generator().manual_seed(1)).cuda()
+    table = torch.empty(512 * 64, device="cuda")
+    wq.check(wq.wq_rope_table(512, 64, 10000.0, None, table))
+    slot = dev(np.array([x - 1 for x in lens], np.int32))
+    q, out = (torch.zeros(n, hq * 64, device="cuda") for _ in range(2))
+    acc0 = torch.rand(n, 2, cap, generator=torch.Generator().manual_seed(2)).cuda()
+    acc, acc2 = torch.zeros_like(acc0), torch.zeros_like(acc0)
+    pos = torch.arange(cap, dtype=torch.int32, device="cuda").expand(n, 2, cap).contiguous()
+    pos2, lensd = torch.zeros_like(pos), dev(np.array(lens, np.int32))
+    lens2 = torch.zeros_like(lensd)
+    size = max(wq.wq_attn_paged_workspace_bytes(c.desc, n, hq, c.max_pages, True),
+               wq.wq_kv_evict_workspace_bytes(c.desc, n, c.max_pages, 200))
+    room = workspace(size)
+
+    full = [p.clone() for p in c.pools]
+
+    def step(stream):
+        acc.copy_(acc0)
+        for p, p0 in zip(c.pools, full):  # the eviction moves rows
+            p.copy_(p0)
+        wq.check(wq.wq_kv_append(c.desc, n, hq, 64, 0, x, 8 * 64, x[:, hq * 64:], 8 * 64,
+                                 x[:, (hq + 2) * 64:], 8 * 64, slot, table, 512, n, None, slot,
+                                 c.pages_dev, c.max_pages, q, hq * 64, acc, pos, cap, stream=stream))
+        wq.check(wq.wq_attn_paged(c.desc, n, hq, 0.125, 0, q, hq * 64, c.pages_dev, c.max_pages,
+                                  lensd, None, 0, out, hq * 64, None, acc, acc, cap, room, size,
+                                  stream=stream))
+        wq.check(wq.wq_kv_evict(c.desc, n, c.pages_dev, c.max_pages, lensd, lensd, 200, 2, 50, acc,
+                                pos, acc2, pos2, cap, lens2, room, size, stream=stream))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(side)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (q, out, acc, acc2, pos2, lens2, *c.pools)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(side)
+    for _ in range(3):
+        for t in (q, out, acc2, pos2, lens2):
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((q, out, acc, acc2, pos2, lens2, *c.pools), want):
+        assert np.array_equal(bits(a), bits(b))
+    assert lens2.tolist() == [200, 41]
