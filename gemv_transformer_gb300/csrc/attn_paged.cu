@@ -12,7 +12,8 @@
 // Products: the heads of a group are the rows of mma.sync operands, eight heads to a
 // fragment, and an f32 value is split into terms of the operand's type that are exact
 // together, the first two in rows g and g + 8 of one product:
-//   bf16 cache  q and p as three bf16 terms (24 bits): a second product has the third;
+//   bf16 cache  q and p as three bf16 terms (24 bits): a second product has the third, or,
+//               of four heads or fewer, rows 4 to 7 of the first;
 //   f16 cache   two f16 terms (22 bits) of q scaled by a power of two per head to a
 //               largest value near 2^10, and of 2^12 p, so that no term is subnormal;
 //   f32 cache   two tf32 terms (22 bits) of q, p, k and v.
@@ -46,7 +47,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxCtas = 456;  // three on each of 152 SMs
 
-template <int DT, int DP, int HT> struct Shape {
+// Q4 (bf16): groups of at most four heads, whose third terms take rows 4 to 7 of the one
+// product.
+template <int DT, int DP, int HT, bool Q4> struct Shape {
     static constexpr bool k16 = DT != kF32;
     static constexpr int kEb = k16 ? 2 : 4;            // bytes of an element
     static constexpr int kRow = DP * kEb;              // bytes of a slot's row in the ring
@@ -63,11 +66,11 @@ template <int DT, int DP, int HT> struct Shape {
     static constexpr bool kQReg = k16 && HT * DP <= 128;  // q's fragments in registers
     static constexpr int kStep = k16 ? 16 : 8;         // dims of a product step
     static constexpr int kSteps = DP / kStep;
-    static constexpr int kQWords = DT == kBF16 ? 6 : 4;   // registers of a step's fragment
+    static constexpr bool k3 = DT == kBF16 && !Q4;     // a second product for the third term
+    static constexpr int kQWords = k3 ? 6 : 4;         // registers of a step's fragment
     static constexpr int kQ = W * kStages * kTile;     // q fragments, unless in registers
     static constexpr int kQBytes = kQReg ? 0 : HT * kSteps * 32 * kQWords * 4;
-    static constexpr int kOff = kQ + kQBytes;                      // [W][KT] row offsets
-    static constexpr int kBias = kOff + W * KT * 8;                // [W][kStages][KT]
+    static constexpr int kBias = kQ + kQBytes;                     // [W][kStages][KT]
     static constexpr int kM = kBias + W * kStages * KT * 4;        // [W][kHeads], then factors
     static constexpr int kL = kM + W * kHeads * 4;                 // [W][kHeads]
     static constexpr int kTop = kL + W * kHeads * 4;               // [kHeads]
@@ -269,10 +272,10 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part
 }
 
 // CL: a cluster of CTAs per row, no workspace parts and no second launch.
-template <int DT, int DP, int HT, bool CL>
-__global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::kCtas)
+template <int DT, int DP, int HT, bool Q4, bool CL>
+__global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, HT, Q4>::kCtas)
     attn_kernel(AttnArgs a, KvView kv, int head_tiles) {
-    using S = Shape<DT, DP, HT>;
+    using S = Shape<DT, DP, HT, Q4>;
     constexpr int NT = S::NT, KT = S::KT, W = S::W, kThreads = W * 32, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -355,7 +358,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
 
     const uint32_t ring = smem_addr(smem) + warp * kStages * S::kTile;
     float *bias = reinterpret_cast<float *>(smem + S::kBias) + warp * kStages * KT;
-    long long *offs = reinterpret_cast<long long *>(smem + S::kOff) + warp * KT;
     const int live_chunks = kv.head_dim / S::kEpc;
 
     const long long v_from_k = kv.v - kv.k;
@@ -397,30 +399,32 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
         // All of the tile's slots are there, and their rows fill the ring's: no checks.
         const bool full = __all_sync(0xFFFFFFFFu, lane >= KT || at >= 0) &&
                           live_chunks == S::kChunks;
-        if (lane < KT) {
-            bias[stage * KT + lane] = b;
-            offs[lane] = at;
-        }
-        __syncwarp();
-        const uint32_t base = ring + stage * S::kTile;
+        if (lane < KT) bias[stage * KT + lane] = b;
+        // Eight lanes copy 128 bytes of a row at a time, four rows at once.
+        const uint32_t to = ring + stage * S::kTile + (lane >> 3) * S::kRow;
+        const char *const mine = kv.k + (lane & 7) * 16;
         auto copy = [&](auto checked) {
 #pragma unroll
-            for (int i = 0; i < KT * S::kChunks / 32; ++i) {
-                const int idx = i * 32 + lane, key = idx / S::kChunks, ch = idx % S::kChunks;
-                const long long from = offs[key];
-                const bool live = !checked || (from >= 0 && ch < live_chunks);
-                const char *k = kv.k + (live ? from + ch * 16 : 0);
-                const uint32_t dst = base + key * S::kRow;
-                cp_async16(dst + ((ch ^ swizzle_k<DT>(key)) << 4), k, live);
-                cp_async16(dst + KT * S::kRow + ((ch ^ swizzle_v<DT>(key)) << 4),
-                           k + v_from_k, live);
+            for (int i = 0; i < KT / 4; ++i) {
+                const int key = 4 * i + (lane >> 3);
+                const long long from = __shfl_sync(0xFFFFFFFFu, at, key);
+                const char *k = mine + (!checked || from >= 0 ? from : 0);
+                const uint32_t dk = to + 4 * i * S::kRow + (((lane & 7) ^ swizzle_k<DT>(key)) << 4);
+                const uint32_t dv = to + (KT + 4 * i) * S::kRow +
+                                    (((lane & 7) ^ swizzle_v<DT>(key)) << 4);
+                const char *v = k + v_from_k;
+#pragma unroll
+                for (int u = 0; u < S::kRow / 128; ++u) {
+                    const bool live = !checked || (from >= 0 && (lane & 7) + 8 * u < live_chunks);
+                    cp_async16(dk + 128 * u, checked && !live ? kv.k : k + 128 * u, live);
+                    cp_async16(dv + 128 * u, checked && !live ? kv.k : v + 128 * u, live);
+                }
             }
         };
         if (full)
             copy(std::false_type());
         else
             copy(std::true_type());
-        __syncwarp();  // offs is free
     };
 
     // The row's query heads, scaled, as the first product's operand: rows g and g + 8 of a
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
             if (S::k16) {
                 const int ht = S::kQReg ? i / (2 * S::kSteps) : warp;
                 if (ht >= HT) break;
-                raw[i] = q2(ht * 8 + g, i % (2 * S::kSteps) * 8 + 2 * c);
+                raw[i] = q2(ht * 8 + (Q4 ? g & 3 : g), i % (2 * S::kSteps) * 8 + 2 * c);
             } else {  // tf32: a lane's dims are those of its 16-byte chunks of a key
                 const int f = i * kThreads + threadIdx.x;
                 const int l = f & 31, ks = (f >> 5) % S::kSteps, ht = (f >> 5) / S::kSteps;
@@ -500,14 +504,15 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 split2<DT>(x.x * a.scale * up, x.y * a.scale * up, t0);
                 split2<DT>(y.x * a.scale * up, y.y * a.scale * up, t1);
                 const int f = ht * S::kSteps + ks;
+                if (Q4 && g >= 4) t0[0] = t0[2], t1[0] = t1[2], t0[1] = t1[1] = 0u;
                 if (S::kQReg) {
                     uint32_t(&q)[S::kQWords] = qr[S::kQReg ? u * S::kSteps + ks : 0];
                     q[0] = t0[0], q[1] = t0[1], q[2] = t1[0], q[3] = t1[1];
-                    if (DT == kBF16) q[4 % S::kQWords] = t0[2], q[5 % S::kQWords] = t1[2];
+                    if (S::k3) q[4 % S::kQWords] = t0[2], q[5 % S::kQWords] = t1[2];
                 } else {
                     *reinterpret_cast<uint4 *>(smem + S::kQ + (f * 32 + lane) * 16) =
                         make_uint4(t0[0], t0[1], t1[0], t1[1]);
-                    if (DT == kBF16)
+                    if (S::k3)
                         *reinterpret_cast<uint2 *>(smem + S::kQ + HT * S::kSteps * 512 +
                                                    (f * 32 + lane) * 8) = make_uint2(t0[2], t1[2]);
                 }
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                         const uint32_t qa = smem_addr(smem) + S::kQ;
                         const uint4 v = lds128(qa + (f * 32 + lane) * 16);
                         q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
-                        if (DT == kBF16) {
+                        if (S::k3) {
                             const uint2 u = lds64(qa + HT * S::kSteps * 512 + (f * 32 + lane) * 8);
                             q[4] = u.x, q[5] = u.y;
                         }
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                         float(&x)[4] = sc[h][n][0], (&y)[4] = sc[h][n][1];
                         mma_16<DT>(x, q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1], x[0], x[1],
                                    x[2], x[3]);
-                        if (DT == kBF16)
+                        if (S::k3)
                             mma_16<DT>(y, q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1], y[0], y[1],
                                        y[2], y[3]);
                     }
@@ -643,6 +648,10 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                     x0 *= back[h];
                     x1 *= back[h];
                 }
+                if (Q4) {  // heads 0 to 3 now also in the lanes of rows 4 to 7
+                    x0 += __shfl_xor_sync(0xFFFFFFFFu, x0, 16);
+                    x1 += __shfl_xor_sync(0xFFFFFFFFu, x1, 16);
+                }
                 xs[n][0] = b.x == -INFINITY ? -INFINITY : x0 + b.x;
                 xs[n][1] = b.y == -INFINITY ? -INFINITY : x1 + b.y;
                 top = fmaxf(top, fmaxf(xs[n][0], xs[n][1]));
@@ -680,6 +689,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 sum += p0 + p1;
                 if (S::k16) {
                     split2<DT>(p0, p1, pt[h][n]);
+                    if (Q4 && g >= 4) pt[h][n][0] = pt[h][n][2], pt[h][n][1] = 0u;
                 } else {
                     pf[h][0] = tf32(p0);
                     pf[h][1] = tf32(p0 - __uint_as_float(pf[h][0]));
@@ -709,7 +719,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                     for (int u = 0; u < 4; ++u)
                         mma_16<DT>(t[u], p0[0], p0[1], p1[0], p1[1], vf[2 * u], vf[2 * u + 1], 0.f,
                                    0.f, 0.f, 0.f);
-                    if (DT == kBF16)
+                    if (S::k3)
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
                             mma_16<DT>(t[u], p0[2], 0u, p1[2], 0u, vf[2 * u], vf[2 * u + 1],
@@ -774,6 +784,13 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT>::W * 32, Shape<DT, DP, HT>::
                 s_l[warp * S::kHeads + h * 8 + g] = sum * unit;
             }
             float *to = mo + (h * 8 + g) * DP;
+            if (Q4) {
+#pragma unroll
+                for (int i = 0; i < OI; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        o[h][i][e] += __shfl_xor_sync(0xFFFFFFFFu, o[h][i][e], 16);
+            }
             if (S::k16) {
 #pragma unroll
                 for (int i = 0; i < OI; ++i)
@@ -1160,10 +1177,10 @@ struct Plan {
     int grid, tile;
 };
 
-template <int DT, int DP, int HT>
+template <int DT, int DP, int HT, bool Q4 = false>
 cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
                          cudaStream_t stream) {
-    using S = Shape<DT, DP, HT>;
+    using S = Shape<DT, DP, HT, Q4>;
     const int head_tiles = (a.group + S::kHeads - 1) / S::kHeads;
     const long long rows = (long long)a.n_seq * kv.n_heads * head_tiles;
     const int slots = min(kMaxCtas, S::kCtas * dev.sm_count);
@@ -1171,13 +1188,14 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
 
     // One cluster per row while every CTA of every row is resident at once and a CTA has at
     // most four tiles.
+    // No CTA of a cluster is without a tile where the cache is full.
     int cluster = 1;
-    while (cluster < 8 && rows * cluster * 2 <= slots) cluster *= 2;
+    while (cluster < 8 && rows * cluster * 2 <= slots && a.n_slots > cluster * S::BT) cluster *= 2;
     const bool small = rows * cluster <= slots &&
                        a.n_slots <= 4ll * cluster * S::BT && (!a.acc_out || head_tiles == 1);
     if (small) {
         static std::atomic<unsigned long long> done{0};
-        cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, true>, S::kSmem, dev, done);
+        cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, true>, S::kSmem, dev, done);
         if (err != cudaSuccess) return err;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(rows * cluster));
@@ -1193,12 +1211,12 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
         attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, attn_kernel<DT, DP, HT, true>, a, kv, head_tiles);
+        return cudaLaunchKernelEx(&cfg, attn_kernel<DT, DP, HT, Q4, true>, a, kv, head_tiles);
     }
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, false>, S::kSmem, dev, done);
+    cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, false>, S::kSmem, dev, done);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_kernel<DT, DP, HT, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
+    err = launch_pdl(attn_kernel<DT, DP, HT, Q4, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
                      a, kv, head_tiles);
     if (err != cudaSuccess) return err;
     const int row_heads = min(a.group, S::kHeads);
@@ -1214,6 +1232,11 @@ template <int DT>
 cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
                         cudaStream_t stream) {
     const int dp = padded_dim(kv.head_dim), ht = head_tile(a.group, dp, DT);
+    if constexpr (DT == kBF16)
+        if (a.group <= 4)
+            return dp == 64    ? launch_shape<DT, 64, 1, true>(a, kv, dev, stream)
+                   : dp == 128 ? launch_shape<DT, 128, 1, true>(a, kv, dev, stream)
+                               : launch_shape<DT, 256, 1, true>(a, kv, dev, stream);
     if (dp == 64)
         return ht == 2 ? launch_shape<DT, 64, 2>(a, kv, dev, stream)
                        : launch_shape<DT, 64, 1>(a, kv, dev, stream);

@@ -455,9 +455,12 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
                             cudaStream_t stream) {
     const long long rows = (long long)a.n_seq * kv.n_heads;
     if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
-    // More CTAs to a row while two per SM are not reached and each has 2048 slots or more.
+    // More CTAs to a row while two per SM are not reached and each has 2048 slots or more, or
+    // 64 moves or more.
+    const long long moves = a.keep < a.n_slots - a.keep ? a.keep : a.n_slots - a.keep;
     int cluster = 1;
-    while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count && a.n_slots / cluster > 2048)
+    while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&
+           (a.n_slots / cluster > 2048 || moves / cluster > 64))
         cluster *= 2;
     cudaError_t err;
     switch (cluster) {
