@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         // All of the tile's slots are there, and their rows fill the ring's: no checks.
         const bool full = __all_sync(0xFFFFFFFFu, lane >= KT || at >= 0) &&
                           live_chunks == S::kChunks;
+        if (!__any_sync(0xFFFFFFFFu, k.live)) return;
         if (lane < KT) bias[stage * KT + lane] = b;
         // Eight lanes copy 128 bytes of a row at a time, four rows at once.
         const uint32_t to = ring + stage * S::kTile + (lane >> 3) * S::kRow;
@@ -866,7 +867,8 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
     while (left > 0) {
         cp_async_wait<kStages - 1>();
         __syncwarp();
-        step();
+        // A warp beyond the row's last slot has nothing in its tile, nor asked for it.
+        if (use.span.first + use.tile * S::BT + warp * KT < use.span.len) step();
         const bool ends = use.tile + 1 == use.tiles;
         left -= !CL && ends ? 1 + kRowCost : 1;
         const bool last = left <= 0;
