@@ -106,7 +106,7 @@ struct Sched {
 struct Span { int len, first; };
 __device__ __forceinline__ Span span_of(const AttnArgs &a, int s) {
     Span p;
-    p.len = min(max(__ldg(a.lens + s), 0), a.n_slots);
+    p.len = min(max(a.lens[s], 0), a.n_slots);
     p.first = a.window > 0 && p.len > a.window ? p.len - a.window : 0;
     return p;
 }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         use.load(a, S::BT);
         use.tile = use.tiles * rank / size;
         left = use.tiles * (rank + 1) / size - use.tile;
-        if (threadIdx.x == 0 && rank == 0 && use.row == 0 && __ldg(a.lens + use.s) > a.n_slots)
+        if (threadIdx.x == 0 && rank == 0 && use.row == 0 && a.lens[use.s] > a.n_slots)
             record_status(a.status, kStBadIndex);
     } else {
         // The costs before each thread's share of the sequences, and of all.
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         long long mine = 0;
         for (int s = s0; s < s1; ++s) {
             mine += cost_of(s);
-            if (blockIdx.x == 0 && __ldg(a.lens + s) > a.n_slots)
+            if (blockIdx.x == 0 && a.lens[s] > a.n_slots)
                 record_status(a.status, kStBadIndex);
         }
         long long x = mine;
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         const int j = fetch.span.first + fetch.tile * S::BT + warp * KT + lane;
         if (lane < KT && j < fetch.span.len) {
             const uint32_t p = kv.page_size.div((uint32_t)j);
-            k.page = __ldg(kv.page_table + (long long)fetch.s * kv.max_pages + p);
+            k.page = kv.page_table[(long long)fetch.s * kv.max_pages + p];
             k.in = j - (int)(p * kv.page_size.d);
-            k.bias = a.mask ? __ldg(a.mask + fetch.s * a.mask_stride + j) : 0.f;
+            k.bias = a.mask ? a.mask[fetch.s * a.mask_stride + j] : 0.f;
             k.live = true;
         }
         k.head = head_tiles == 1 ? fetch.row : fetch.row / head_tiles;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         const float *q0 = a.q + at.s * a.q_stride + ((long long)h * a.group + ht0) * kv.head_dim;
         auto q2 = [&](int head, int dim) {
             return ht0 + head < a.group && dim < kv.head_dim
-                       ? __ldg(reinterpret_cast<const float2 *>(q0 + head * kv.head_dim + dim))
+                       ? *reinterpret_cast<const float2 *>(q0 + head * kv.head_dim + dim)
                        : make_float2(0.f, 0.f);
         };
 #pragma unroll

@@ -8,6 +8,7 @@ namespace wq {
 namespace {
 
 constexpr int kMaxHeadDim = 256;
+constexpr long long kMaxSlots = 1ll << 30;  // a slot number and a tile beyond it fit an int
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 wq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA; }
@@ -21,7 +22,7 @@ bool view_of(const wq_kv_cache *c, int n_seq, const int32_t *page_table, int max
     if (c->n_pages <= 0 || c->page_size <= 0 || c->n_heads <= 0 || c->head_dim <= 0) return false;
     if (c->head_dim % 8 || c->head_dim > kMaxHeadDim) return false;
     if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return false;
-    if ((long long)max_pages * c->page_size > 0x7FFFFFFFll) return false;
+    if ((long long)max_pages * c->page_size > kMaxSlots) return false;
     const int eb = element_bytes(c->dtype);
     const int64_t strides[3] = {c->page_stride, c->head_stride, c->token_stride};
     const int extents[3] = {c->n_pages, c->n_heads, c->page_size};

@@ -2,6 +2,10 @@
 //
 // Slot j of a sequence is row j % page_size of page page_table[j / page_size]; the
 // address of a row is 64-bit arithmetic throughout (pools pass 4 GiB).
+//
+// What these kernels read may have been written by the kernel just before them, beside whose
+// end they start (griddepcontrol.wait orders the two), so nothing is read through the
+// non-coherent path.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,7 +42,7 @@ struct KvView {
     // Byte offset of head h's row of slot j in both pools, or -1 for a page out of range.
     __device__ __forceinline__ long long row(int s, int h, int j) const {
         const uint32_t p = page_size.div((uint32_t)j);
-        const int page = __ldg(page_table + (long long)s * max_pages + p);
+        const int page = page_table[(long long)s * max_pages + p];
         if ((unsigned)page >= (unsigned)n_pages) return -1;
         return (long long)page * page_stride + (long long)h * head_stride +
                (long long)(j - (int)(p * page_size.d)) * token_stride;

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
         return of(&sh.hist[pass][bin], bin / (kBins / C));
     };
     const int id = blockIdx.x / C, s = id / kv.n_heads, h = id - s * kv.n_heads;
-    const int given = __ldg(a.lens + s), len = min(max(given, 0), a.n_slots);
-    const int from = __ldg(a.seen + s) - a.recent;
+    const int given = a.lens[s], len = min(max(given, 0), a.n_slots);
+    const int from = a.seen[s] - a.recent;
     const int keep = min(len, a.keep);
     if (threadIdx.x == 0 && rank == 0 && h == 0) {
         if (given > a.n_slots) record_status(a.status, kStBadIndex);

@@ -125,12 +125,12 @@ template <int N>
 __device__ __forceinline__ Angles<N> load_angles(const float2 *p, unsigned flags) {
     Angles<N> r;
     if constexpr (N == 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        const float4 y = reinterpret_cast<const float4 *>(p)[1];
         r.c[0] = x.x, r.s[0] = x.y, r.c[1] = x.z, r.s[1] = x.w;
         r.c[2] = y.x, r.s[2] = y.y, r.c[3] = y.z, r.s[3] = y.w;
     } else {
-        const float2 x = __ldg(p);
+        const float2 x = *p;
         r.c[0] = x.x, r.s[0] = x.y;
     }
     if (flags & WQ_ROPE_TRANSPOSE)
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs r, Deal deal, const 
     const unsigned t = deal.per_row.div(at), w = at - t * deal.per_row.d;
     const unsigned hg = deal.units.div(w), u = w - hg * deal.units.d;
     const Place p = place_of<N>(u, r.rot, r.flags);
-    const int pos = r.rot > 0 ? __ldg(r.pos + t) : 0;
+    const int pos = r.rot > 0 ? r.pos[t] : 0;
     const int h0 = hg * deal.heads_per, n = min(deal.heads_per, n_heads - h0);
     const float *xi = x + t * x_stride + (long long)h0 * r.head_dim;
     float *o = out + t * out_stride + (long long)h0 * r.head_dim;
@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a, KvView kv,
     const unsigned row_at = deal.per_row.div(at), w = at - row_at * deal.per_row.d;
     const unsigned hg = deal.units.div(w), u = w - hg * deal.units.d;
     const int t = t0 + (int)row_at;
-    const int slot = __ldg(a.slot + t);
-    const int seq = a.seq ? __ldg(a.seq + t) : t;
-    const int pos = r.pos ? __ldg(r.pos + t) : 0;
+    const int slot = a.slot[t];
+    const int seq = a.seq ? a.seq[t] : t;
+    const int pos = r.pos ? r.pos[t] : 0;
     const Place p = place_of<N>(u, r.rot, r.flags);
     const int heads = a.h_q + 2 * kv.n_heads;
     const int h0 = hg * deal.heads_per, n = min(deal.heads_per, heads - h0);

@@ -429,7 +429,7 @@ typedef struct {
  * A position, sequence, slot or page out of range leaves all of its token's outputs
  * unwritten and records WQ_ERR_BAD_INDEX in the device status.
  * Errors: as wq_rope and for the cache's restrictions; WQ_ERR_INVALID_ARG also for
- * n_seq, max_pages <= 0, max_pages * page_size above 2^31 - 1, null k, v, slot or
+ * n_seq, max_pages <= 0, max_pages * page_size above 2^30, null k, v, slot or
  * page_table, n_seq < n_tok with a null seq, acc or slot_pos with
  * acc_stride < 1, a null pos with slot_pos. */
 WQ_API wq_status wq_kv_append(const wq_kv_cache *cache, int n_tok, int h_q, int rot,
@@ -468,7 +468,7 @@ WQ_API wq_status wq_kv_append(const wq_kv_cache *cache, int n_tok, int h_q, int 
  * multiple of the kv heads, window < 0, a scale that is not finite, null q, page_table,
  * lens or out, acc_in without acc_out, q or out not 16-byte aligned or with a stride below
  * h_q * head_dim or not a multiple of 4, a stride < 1 of a mask or acc that is given,
- * max_pages * page_size above 2^31 - 1, a missing, misaligned or small workspace. */
+ * max_pages * page_size above 2^30, a missing, misaligned or small workspace. */
 WQ_API wq_status wq_attn_paged(const wq_kv_cache *cache, int n_seq, int h_q, float scale,
                                int window, const float *q, int64_t q_stride,
                                const int32_t *page_table, int max_pages, const int32_t *lens,
@@ -500,7 +500,7 @@ WQ_API size_t wq_attn_paged_workspace_bytes(const wq_kv_cache *cache, int n_seq,
  * workspace: as wq_attn_paged's, of wq_kv_evict_workspace_bytes(...) bytes.
  * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, max_pages, keep <= 0, sinks or
  * recent < 0, sinks + recent > keep, null page_table, lens, seen, acc, slot_pos, acc_out,
- * pos_out or lens_out, acc_stride < 1, max_pages * page_size above 2^31 - 1, a missing,
+ * pos_out or lens_out, acc_stride < 1, max_pages * page_size above 2^30, a missing,
  * misaligned or small workspace. */
 WQ_API wq_status wq_kv_evict(const wq_kv_cache *cache, int n_seq, const int32_t *page_table,
                              int max_pages, const int32_t *lens, const int32_t *seen, int keep,
