@@ -1188,13 +1188,18 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     const int slots = min(kMaxCtas, S::kCtas * dev.sm_count);
     if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
 
-    // One cluster per row while every CTA of every row is resident at once and a CTA has at
-    // most four tiles.
-    // No CTA of a cluster is without a tile where the cache is full.
+    // A cluster per row where a CTA has at most four tiles: no parts, no second launch (one
+    // sequence, 8 rows of 1024 slots: 7.9 us, split and joined 9.1; of 4096 15.9 and 12.8).
+    // More CTAs to a row while one per SM is not reached, or two where one has over two tiles
+    // (32 rows of 256 slots: 4 CTAs a row 6.6 us, 8 take 8.3; of 2048 15.9 and 13.3), and
+    // where rows alone are more than fit, one each (800 rows of 256: 30.0 us, split 32.9).
+    // The cache's size stands for the lengths, which are not known here.
+    const long long span = a.window > 0 && a.window < a.n_slots ? a.window : a.n_slots;
     int cluster = 1;
-    while (cluster < 8 && rows * cluster * 2 <= slots && a.n_slots > cluster * S::BT) cluster *= 2;
-    const bool small = rows * cluster <= slots &&
-                       a.n_slots <= 4ll * cluster * S::BT && (!a.acc_out || head_tiles == 1);
+    while (cluster < 8 && rows * cluster * 2 <= slots && span > cluster * S::BT &&
+           (rows * cluster * 2 <= dev.sm_count || span > 2 * cluster * S::BT))
+        cluster *= 2;
+    const bool small = span <= 4ll * cluster * S::BT && (!a.acc_out || head_tiles == 1);
     if (small) {
         static std::atomic<unsigned long long> done{0};
         cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, true>, S::kSmem, dev, done);

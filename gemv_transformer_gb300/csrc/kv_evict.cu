@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
     }
     const bool held_keys = mine <= key_room;
     auto make_key = [&](int j) { return key_of(acc[j], pos[j], a.sinks, from); };
-    // The keys of four slots from j on (j - b0 is a multiple of 4); of slots beyond b1, 0.
+    // The keys of four slots from j on (j - b0 is a multiple of 4).  Those of slots at or beyond
+    // b1 are whatever is there (key_room is a multiple of 32): every use checks the slot.
     auto keys4 = [&](int j, uint32_t (&x)[4]) {
         if (held_keys) {
             const uint4 v = *reinterpret_cast<const uint4 *>(s_key + (j - b0));
@@ -165,8 +166,6 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
             }
         }
     }
-    if (held_keys && threadIdx.x < 4 && ((mine + (int)threadIdx.x) & ~3) >= mine)
-        s_key[mine + threadIdx.x] = 0u;  // up to a multiple of four
     __syncthreads();
     for (int pass = 0; pass < kPasses; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : kDigit;
