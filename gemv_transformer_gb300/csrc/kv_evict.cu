@@ -454,18 +454,21 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
                             cudaStream_t stream) {
     const long long rows = (long long)a.n_seq * kv.n_heads;
     if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
-    // More CTAs to a row while two per SM are not reached and each has 2048 slots or more, or
-    // 64 moves or more.
+    // More CTAs to a row while two per SM are not reached and each has over 4096 slots or 128
+    // moves (8 rows of 20000 slots, one over: 1 CTA 17.5 us, 8 take 10.8; of 2049: 6.3 and 7.9;
+    // 8 rows of 4096 cut to 1024: 26.2 and 12.4).  512 threads while two such CTAs per SM hold
+    // all rows or the rows are long, else 256 (512 rows of 2049: 10.3 us, with 512 14.7;
+    // of 8193 37.1 and 30.8).
     const long long moves = a.keep < a.n_slots - a.keep ? a.keep : a.n_slots - a.keep;
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&
-           (a.n_slots / cluster > 2048 || moves / cluster > 64))
+           (a.n_slots / cluster > 4096 || moves / cluster > 128))
         cluster *= 2;
     cudaError_t err;
     switch (cluster) {
     case 1:
-        err = a.n_slots <= 4096 ? launch_rows<256, 1>(a, kv, dev, stream)
-                                : launch_rows<512, 1>(a, kv, dev, stream);
+        err = rows <= 2 * dev.sm_count || a.n_slots > 6144 ? launch_rows<512, 1>(a, kv, dev, stream)
+                                                           : launch_rows<256, 1>(a, kv, dev, stream);
         break;
     case 2: err = launch_rows<512, 2>(a, kv, dev, stream); break;
     case 4: err = launch_rows<512, 4>(a, kv, dev, stream); break;
