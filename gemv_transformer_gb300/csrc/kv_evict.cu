@@ -80,10 +80,66 @@ __device__ __forceinline__ void warp_offsets(Select<T, C> &sh, int &a, int &b, i
     }
 }
 
+// The moves of one row, dealt out to `warps` warps: each has kBatch loads in flight, of 32
+// lanes' 16 bytes: one move's k and v, or (PER = 2) those of two moves of 128-byte rows.
+// The next moves are looked up while these moves' rows are on their way.
+template <int PER>
+__device__ __forceinline__ void move_rows(const EvictArgs &a, const KvView &kv, int row_bytes,
+                                          long long base, const Move *list, int total, int warp,
+                                          int warps) {
+    const int lane = threadIdx.x & 31, quads = row_bytes / 16;  // of k; as many of v
+    constexpr int per = PER, batch = kBatch * PER;
+    const int sub = PER == 1 ? 0 : lane / (32 / PER), first = PER == 1 ? lane : lane % (32 / PER);
+    long long to, at;
+    auto look_up = [&](int i0) {
+        to = at = -1;
+        if (lane < batch && i0 + lane < total) {
+            const Move m = list[i0 + lane];
+            a.acc_out[base + m.dst] = m.weight;
+            a.pos_out[base + m.dst] = m.pos;
+            at = m.at;
+            to = m.at < 0 ? -1 : m.to;
+        }
+    };
+    int i0 = warp * batch;
+    look_up(i0);
+    for (; i0 < total; i0 += warps * batch) {
+        const long long to_now = to, at_now = at;
+        for (int q0 = 0; q0 < 2 * quads; q0 += 32) {
+            const int q = q0 + first;
+            const bool of_v = q >= quads, in_row = q < 2 * quads;
+            const long long in = 16ll * (of_v ? q - quads : q);
+            char *pool = of_v ? kv.v : kv.k;
+            uint4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const bool live = __shfl_sync(0xFFFFFFFFu, to_now, i * per + sub) >= 0 && in_row;
+                const long long src = __shfl_sync(0xFFFFFFFFu, at_now, i * per + sub);
+                if (live) x[i] = *reinterpret_cast<const uint4 *>(pool + src + in);
+            }
+            if (q0 == 0) look_up(i0 + warps * batch);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const long long dst = __shfl_sync(0xFFFFFFFFu, to_now, i * per + sub);
+                if (dst >= 0 && in_row) *reinterpret_cast<uint4 *>(pool + dst + in) = x[i];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void move_all(const EvictArgs &a, const KvView &kv, int row_bytes,
+                                         long long base, const Move *list, int total, int warp,
+                                         int warps) {
+    if (row_bytes == 128)
+        move_rows<2>(a, kv, row_bytes, base, list, total, warp, warps);
+    else
+        move_rows<1>(a, kv, row_bytes, base, list, total, warp, warps);
+}
+
 // C: the CTAs of a row; with one, its barriers are the CTA's.
 template <int T, int C>
 __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView kv, int row_bytes,
-                                                  int key_room) {
+                                                                 int key_room, int *counts) {
     extern __shared__ __align__(16) uint8_t smem[];
     Select<T, C> &sh = *reinterpret_cast<Select<T, C> *>(smem);
     uint32_t *s_key = reinterpret_cast<uint32_t *>(smem + sizeof(Select<T, C>));
@@ -123,6 +179,7 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
     const int share = ((len + C - 1) / C + 31) & ~31;
     const int b0 = min(len, rank * share), b1 = min(len, b0 + share), mine = b1 - b0;
     if (len <= keep) {  // within the budget: the whole cluster leaves here
+        if (counts && threadIdx.x == 0 && rank == 0) counts[id] = 0;
         if (!in_place)
             for (int j = b0 + threadIdx.x; j < b1; j += T) {
                 a.acc_out[base + j] = acc[j];
@@ -207,12 +264,11 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
         constexpr int kMine = kBins / T;
         const int top = kBins - kMine * (threadIdx.x + 1);  // this thread's lowest bin
         int count[kMine] = {}, sum = 0;
-        const int4 *counts4 = reinterpret_cast<const int4 *>(counter(pass, top));
+        const int2 *counts2 = reinterpret_cast<const int2 *>(counter(pass, top));
 #pragma unroll
-        for (int i = 0; i < kMine / 4; ++i) {
-            const int4 v = counts4[i];
-            count[4 * i] = v.x, count[4 * i + 1] = v.y;
-            count[4 * i + 2] = v.z, count[4 * i + 3] = v.w;
+        for (int i = 0; i < kMine / 2; ++i) {
+            const int2 v = counts2[i];
+            count[2 * i] = v.x, count[2 * i + 1] = v.y;
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) sum += count[i];
@@ -330,7 +386,7 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
         }
     }
     // Every move, in slot order.
-    Move *list = ONE && total <= kShort
+    Move *list = ONE && total <= kShort && !counts
                      ? sh.list
                      : static_cast<Move *>(a.workspace) + (long long)id * min(a.keep, a.n_slots);
     tie = same;
@@ -368,44 +424,21 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
     sync_row();  // the list is complete; no shared memory of another CTA is read below
     pdl_launch();
 
-    // The moves, kBatch per warp at a time; the next batch is looked up while this one's rows
-    // are on their way.
-    const int warps = C * (T / 32), quads = row_bytes / 16;  // of k; as many of v
-    long long to, at;
-    auto look_up = [&](int i0) {
-        to = at = -1;
-        if (lane < kBatch && i0 + lane < total) {
-            const Move m = list[i0 + lane];
-            a.acc_out[base + m.dst] = m.weight;
-            a.pos_out[base + m.dst] = m.pos;
-            at = m.at;
-            to = m.at < 0 ? -1 : m.to;
-        }
-    };
-    int i0 = (rank * (T / 32) + warp) * kBatch;
-    look_up(i0);
-    for (; i0 < total; i0 += warps * kBatch) {
-        const long long to_now = to, at_now = at;
-        for (int q0 = 0; q0 < 2 * quads; q0 += 32) {
-            const int q = q0 + lane;
-            const bool of_v = q >= quads;
-            const long long in = 16ll * (of_v ? q - quads : q);
-            char *pool = of_v ? kv.v : kv.k;
-            uint4 x[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const bool live = __shfl_sync(0xFFFFFFFFu, to_now, i) >= 0 && q < 2 * quads;
-                const long long src = __shfl_sync(0xFFFFFFFFu, at_now, i);
-                if (live) x[i] = *reinterpret_cast<const uint4 *>(pool + src + in);
-            }
-            if (q0 == 0) look_up(i0 + warps * kBatch);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const long long dst = __shfl_sync(0xFFFFFFFFu, to_now, i);
-                if (dst >= 0 && q < 2 * quads) *reinterpret_cast<uint4 *>(pool + dst + in) = x[i];
-            }
-        }
+    if (counts) {  // many moves of few rows: evict_move_kernel's
+        if (threadIdx.x == 0 && rank == 0) counts[id] = total;
+        return;
     }
+    move_all(a, kv, row_bytes, base, list, total, rank * (T / 32) + warp, C * (T / 32));
+}
+
+// The moves of rows whose selection left them: blocks_per_row blocks to each.
+__global__ void __launch_bounds__(256, 4) evict_move_kernel(EvictArgs a, KvView kv, int row_bytes,
+                                                            const int *counts, int blocks_per_row) {
+    pdl_enter();
+    const int id = blockIdx.x / blocks_per_row, block = blockIdx.x - id * blocks_per_row;
+    move_all(a, kv, row_bytes, (long long)id * a.acc_stride,
+             static_cast<const Move *>(a.workspace) + (long long)id * min(a.keep, a.n_slots),
+             counts[id], block * 8 + (threadIdx.x >> 5), blocks_per_row * 8);
 }
 
 // Lengths in place: after every row of a sequence has read them.
@@ -415,10 +448,12 @@ __global__ void evict_lens_kernel(EvictArgs a) {
     if (s < a.n_seq) a.lens_out[s] = min(max(a.lens[s], 0), min(a.keep, a.n_slots));
 }
 
+int row_bytes_of(const KvView &kv) { return kv.head_dim * (kv.dtype == kF32 ? 4 : 2); }
+
 template <int T, int C>
-cudaError_t launch_rows(const EvictArgs &a, const KvView &kv, const DeviceInfo &dev,
+cudaError_t launch_rows(const EvictArgs &a, const KvView &kv, int *counts, const DeviceInfo &dev,
                         cudaStream_t stream) {
-    const int row_bytes = kv.head_dim * (kv.dtype == kF32 ? 4 : 2);
+    const int row_bytes = row_bytes_of(kv);
     const long long share = ((a.n_slots + (long long)C - 1) / C + 31) & ~31ll;
     const int key_room = (int)(share < kMaxKeys ? share : kMaxKeys);
     static std::atomic<unsigned long long> done{0};
@@ -440,14 +475,15 @@ cudaError_t launch_rows(const EvictArgs &a, const KvView &kv, const DeviceInfo &
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<T, C>, a, kv, row_bytes, key_room);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<T, C>, a, kv, row_bytes, key_room, counts);
 }
 
 }  // namespace
 
 size_t evict_workspace_bytes(const KvView &kv, int n_seq, int n_slots, int keep) {
     if (keep > n_slots) keep = n_slots;
-    return ((size_t)n_seq * kv.n_heads * keep * sizeof(Move) + 255) & ~(size_t)255;
+    // The moves, and how many each row has.
+    return ((size_t)n_seq * kv.n_heads * (keep * sizeof(Move) + sizeof(int)) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -458,21 +494,36 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     // moves (8 rows of 20000 slots, one over: 1 CTA 17.5 us, 8 take 10.8; of 2049: 6.3 and 7.9;
     // 8 rows of 4096 cut to 1024: 26.2 and 12.4).  512 threads while two such CTAs per SM hold
     // all rows or the rows are long, else 256 (512 rows of 2049: 10.3 us, with 512 14.7;
-    // of 8193 37.1 and 30.8).
+    // of 8193 37.1 and 30.8); 1024 where one CTA per SM holds few long rows.
     const long long moves = a.keep < a.n_slots - a.keep ? a.keep : a.n_slots - a.keep;
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&
            (a.n_slots / cluster > 4096 || moves / cluster > 128))
         cluster *= 2;
+    // Where half the GPU or more has no row and 8 MB or more may move, the moves are a launch
+    // of their own over all SMs.
+    const int row_bytes = row_bytes_of(kv);
+    int *counts = nullptr;
+    if (rows * cluster <= dev.sm_count && rows * moves * row_bytes * 2 >= 8ll << 20)
+        counts = reinterpret_cast<int *>(static_cast<Move *>(a.workspace) +
+                                         rows * (a.keep < a.n_slots ? a.keep : a.n_slots));
     cudaError_t err;
     switch (cluster) {
     case 1:
-        err = rows <= 2 * dev.sm_count || a.n_slots > 6144 ? launch_rows<512, 1>(a, kv, dev, stream)
-                                                           : launch_rows<256, 1>(a, kv, dev, stream);
+        err = rows <= 2 * dev.sm_count || a.n_slots > 6144 ? launch_rows<512, 1>(a, kv, counts, dev, stream)
+                                                           : launch_rows<256, 1>(a, kv, counts, dev, stream);
         break;
-    case 2: err = launch_rows<512, 2>(a, kv, dev, stream); break;
-    case 4: err = launch_rows<512, 4>(a, kv, dev, stream); break;
-    default: err = launch_rows<512, 8>(a, kv, dev, stream);
+    case 2: err = launch_rows<512, 2>(a, kv, counts, dev, stream); break;
+    case 4: err = launch_rows<512, 4>(a, kv, counts, dev, stream); break;
+    default:
+        err = rows * 8 <= dev.sm_count && a.n_slots > 65536
+                  ? launch_rows<1024, 8>(a, kv, counts, dev, stream)
+                  : launch_rows<512, 8>(a, kv, counts, dev, stream);
+    }
+    if (err == cudaSuccess && counts) {
+        const int blocks_per_row = (int)((4ll * dev.sm_count + rows - 1) / rows);
+        err = launch_pdl(evict_move_kernel, dim3((unsigned)(rows * blocks_per_row)), dim3(256), 0,
+                         stream, a, kv, row_bytes, (const int *)counts, blocks_per_row);
     }
     if (err != cudaSuccess || a.lens_out != a.lens) return err;
     return launch_pdl(evict_lens_kernel, dim3((a.n_seq + 255) / 256), dim3(256), 0, stream, a);

@@ -203,3 +203,57 @@ def test_cache_beyond_4_gib():
     for pool, want in ((k, x[0]), (v, x[1])):
         got = torch.cat([pool[order[0], 0], pool[order[1], 0]])[:20].cpu()
         assert torch.equal(got, want[at])
+
+
+@pytest.mark.parametrize("n,hkv,length,keep,d,kind", [
+    (1, 1, 400000, 250000, 8, "bf16"),   # longer than eight CTAs' key arrays hold
+    (1, 1, 350001, 350000, 8, "bf16"),
+    (2, 1, 20000, 9000, 128, "f32"),     # few rows, many bytes: moved by all SMs
+    (1, 3, 30000, 12000, 256, "f16"),
+    (2, 2, 70000, 30000, 64, "bf16")])
+@pytest.mark.parametrize("ties", [False, True])
+def test_long_rows_by_their_own_numbers(n, hkv, length, keep, d, kind, ties):
+    """Rows that hold their slot's number: each survivor is where the rule puts it."""
+    page = 64
+    pages = -(-length // page)
+    g = np.random.default_rng(length + ties)
+    table = np.stack([g.permutation(pages) + s * pages for s in range(n)]).astype(np.int32)
+    from kv_helpers import TYPES
+    shape = (n * pages, hkv, page, d)
+    k = torch.zeros(shape, dtype=TYPES[kind], device="cuda")
+    bits_of = {2: torch.int16, 4: torch.int32}[k.element_size()]
+    number = torch.arange(pages * page, device="cuda")
+    for s in range(n):
+        at = torch.from_numpy(table[s]).cuda().long()
+        low, high = (number & 0x7FFF).view(pages, page), (number >> 15).view(pages, page)
+        for h in range(hkv):  # the first two values are the slot's number
+            k.view(bits_of)[at, h, :, 0] = low.to(bits_of)
+            k.view(bits_of)[at, h, :, 1] = high.to(bits_of)
+    v = k.clone()
+    acc = g.integers(0, 50, (n, hkv, length)).astype(np.float32) if ties else \
+        np.exp(2 * g.standard_normal((n, hkv, length))).astype(np.float32)
+    pos = np.broadcast_to(np.arange(length, dtype=np.int32), (n, hkv, length)).copy()
+    accd, posd = dev(acc), dev(pos)
+    lens = dev(np.full(n, length, np.int32))
+    cache = wq.kv_cache(k, v)
+    size = wq.wq_kv_evict_workspace_bytes(cache, n, pages, keep)
+    torch.cuda.synchronize()
+    wq.check(wq.wq_kv_evict(cache, n, dev(table), pages, lens, lens.clone(), keep, 3, 500, accd, posd,
+                            accd, posd, length, lens, workspace(size), size))
+    torch.cuda.synchronize()
+    status_ok()
+    assert lens.tolist() == [keep] * n
+    for s in range(n):
+        rows = torch.from_numpy(table[s]).cuda().long()
+        for h in range(hkv):
+            rank = np.where((pos[s, h] < 3) | (pos[s, h] >= length - 500), np.inf, acc[s, h])
+            stay = np.zeros(length, bool)
+            stay[np.argsort(-rank, kind="stable")[:keep]] = True
+            want = np.arange(keep)
+            want[~stay[:keep]] = keep + np.flatnonzero(stay[keep:])
+            assert np.array_equal(posd[s, h, :keep].cpu().numpy(), want)
+            assert np.array_equal(accd[s, h, :keep].cpu().numpy(), acc[s, h][want])
+            for pool in (k, v):
+                row = pool.view(bits_of)[rows, h].view(-1, d)[:keep].long()
+                assert np.array_equal((row[:, 0] + (row[:, 1] << 15)).cpu().numpy(), want)
+                assert not row[:, 2:].any()
