@@ -1,7 +1,8 @@
 """Python binding of libwq (the weight-format GEMM/GEMV library for sm_103a).
 
 Argument marshalling only: every function forwards to the C entry point of the
-same name in ``_build/libwq.so`` (declared in ``include/wq.h``); all the work runs
+same name in ``_build/libwq.so`` (declared in ``include/wq.h``), through ctypes or, for
+the calls of a decode step, the C module ``_build/_wq_calls.so``; all the work runs
 in the library's CUDA kernels.  There is no CPU fallback: if the library is not
 built, or no CUDA device is present, the calls raise.
 
@@ -12,11 +13,13 @@ integer, or ``None`` for torch's current stream on the current device.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libwq.so")
+CALLS_PATH = os.path.join(HERE, "_build", "_wq_calls.so")
 
 WQ_BF16, WQ_Q8_0, WQ_Q4_0, WQ_F16, WQ_F32 = 0, 1, 2, 3, 4
 WQ_BIAS, WQ_GELU, WQ_RESIDUAL, WQ_TC_BF16 = 1, 2, 4, 256
@@ -116,22 +119,11 @@ def _open(path: str):
     lib.wq_gemm_dual.restype = ci
     lib.wq_embed.argtypes = [ci, ci, ci, ci, vp, vp, vp, vp, vp, vp]
     lib.wq_embed.restype = ci
-    cl, cp = ctypes.c_int64, ctypes.POINTER(KvCache)
+    cp = ctypes.POINTER(KvCache)
     lib.wq_rope_table.argtypes = [ci, ci, ctypes.c_double, ctypes.POINTER(RopeScaling), vp, vp]
     lib.wq_rope_table.restype = ci
-    lib.wq_rope.argtypes = [ci, ci, ci, ci, cu, vp, cl, vp, vp, ci, vp, cl, vp]
-    lib.wq_rope.restype = ci
-    lib.wq_kv_append.argtypes = [cp, ci, ci, ci, cu, vp, cl, vp, cl, vp, cl, vp, vp, ci, ci, vp,
-                                 vp, vp, ci, vp, cl, vp, vp, cl, vp]
-    lib.wq_kv_append.restype = ci
-    lib.wq_attn_paged.argtypes = [cp, ci, ci, ctypes.c_float, ci, vp, cl, vp, ci, vp, vp, cl, vp,
-                                  cl, vp, vp, vp, cl, vp, sz, vp]
-    lib.wq_attn_paged.restype = ci
     lib.wq_attn_paged_workspace_bytes.argtypes = [cp, ci, ci, ci, ci]
     lib.wq_attn_paged_workspace_bytes.restype = sz
-    lib.wq_kv_evict.argtypes = [cp, ci, vp, ci, vp, vp, ci, ci, ci, vp, vp, vp, vp, cl, vp, vp,
-                                sz, vp]
-    lib.wq_kv_evict.restype = ci
     lib.wq_kv_evict_workspace_bytes.argtypes = [cp, ci, ci, ci]
     lib.wq_kv_evict_workspace_bytes.restype = sz
     lib.wq_get_device_status.argtypes = [vp]
@@ -152,6 +144,28 @@ def load():
         if _lib is None:
             _lib = _open(LIB_PATH)
         return _lib
+
+
+_calls = None
+
+
+def _load_calls():
+    """The marshalling module of the decode-step calls, bound to the process-wide libwq."""
+    global _calls
+    lib = load()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(CALLS_PATH):
+                raise RuntimeError(f"the binding is not built ({CALLS_PATH} missing): run "
+                                   "gemv_transformer_gb300.build.build()")
+            spec = importlib.util.spec_from_file_location("_wq_calls", CALLS_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                       for f in ("wq_rope", "wq_kv_append", "wq_attn_paged", "wq_kv_evict")),
+                     _current_stream)
+            _calls = mod
+        return _calls
 
 
 def _p(x):
@@ -263,27 +277,27 @@ def wq_rope_table(rows, rot, base, scaling, table, stream=None) -> int:
 
 def wq_rope(n, n_heads, head_dim, rot, flags, x, x_stride, pos, table, table_rows, out,
             out_stride, stream=None) -> int:
-    return load().wq_rope(n, n_heads, head_dim, rot, flags, _p(x), x_stride, _p(pos), _p(table),
-                          table_rows, _p(out), out_stride, _s(stream))
+    return (_calls or _load_calls()).wq_rope(n, n_heads, head_dim, rot, flags, x, x_stride, pos,
+                                             table, table_rows, out, out_stride, stream)
 
 
 def wq_kv_append(cache, n_tok, h_q, rot, flags, q, q_stride, k, k_stride, v, v_stride, pos, table,
                  table_rows, n_seq, seq, slot, page_table, max_pages, q_out=None, q_out_stride=0,
                  acc=None, slot_pos=None, acc_stride=0, stream=None) -> int:
-    return load().wq_kv_append(cache, n_tok, h_q, rot, flags, _p(q), q_stride, _p(k), k_stride,
-                               _p(v), v_stride, _p(pos), _p(table), table_rows, n_seq, _p(seq),
-                               _p(slot), _p(page_table), max_pages, _p(q_out), q_out_stride,
-                               _p(acc), _p(slot_pos), acc_stride, _s(stream))
+    return (_calls or _load_calls()).wq_kv_append(
+        cache, n_tok, h_q, rot, flags, q, q_stride, k, k_stride, v, v_stride, pos, table,
+        table_rows, n_seq, seq, slot, page_table, max_pages, q_out, q_out_stride, acc, slot_pos,
+        acc_stride, stream)
 
 
 def wq_attn_paged(cache, n_seq, h_q, scale, window, q, q_stride, page_table, max_pages, lens,
                   mask=None, mask_stride=0, out=None, out_stride=0, lse=None, acc_in=None,
                   acc_out=None, acc_stride=0, workspace=None, workspace_bytes=0,
                   stream=None) -> int:
-    return load().wq_attn_paged(cache, n_seq, h_q, scale, window, _p(q), q_stride, _p(page_table),
-                                max_pages, _p(lens), _p(mask), mask_stride, _p(out), out_stride,
-                                _p(lse), _p(acc_in), _p(acc_out), acc_stride, _p(workspace),
-                                workspace_bytes, _s(stream))
+    return (_calls or _load_calls()).wq_attn_paged(
+        cache, n_seq, h_q, scale, window, q, q_stride, page_table, max_pages, lens, mask,
+        mask_stride, out, out_stride, lse, acc_in, acc_out, acc_stride, workspace,
+        workspace_bytes, stream)
 
 
 def wq_attn_paged_workspace_bytes(cache, n_seq, h_q, max_pages, with_acc) -> int:
@@ -293,9 +307,9 @@ def wq_attn_paged_workspace_bytes(cache, n_seq, h_q, max_pages, with_acc) -> int
 def wq_kv_evict(cache, n_seq, page_table, max_pages, lens, seen, keep, sinks, recent, acc,
                 slot_pos, acc_out, pos_out, acc_stride, lens_out, workspace=None,
                 workspace_bytes=0, stream=None) -> int:
-    return load().wq_kv_evict(cache, n_seq, _p(page_table), max_pages, _p(lens), _p(seen), keep,
-                              sinks, recent, _p(acc), _p(slot_pos), _p(acc_out), _p(pos_out),
-                              acc_stride, _p(lens_out), _p(workspace), workspace_bytes, _s(stream))
+    return (_calls or _load_calls()).wq_kv_evict(
+        cache, n_seq, page_table, max_pages, lens, seen, keep, sinks, recent, acc, slot_pos,
+        acc_out, pos_out, acc_stride, lens_out, workspace, workspace_bytes, stream)
 
 
 def wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep) -> int:

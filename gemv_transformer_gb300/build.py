@@ -1,7 +1,8 @@
 """Build libwq.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
 
 Each ``csrc/*.cu`` is compiled in parallel to an object, then linked into
-``gemv_transformer_gb300/_build/libwq.so`` with the static CUDA runtime.
+``gemv_transformer_gb300/_build/libwq.so`` with the static CUDA runtime.  ``py_calls.c``, the
+binding's marshalling of the decode-step calls, is compiled with gcc beside it.
 Run ``python -m gemv_transformer_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -12,12 +13,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libwq.so")
+CALLS = os.path.join(OUT_DIR, "_wq_calls.so")
+CALLS_SRC = os.path.join(CSRC, "py_calls.c")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,14 +42,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
@@ -67,8 +71,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
+    def compile_calls():
+        tmp = CALLS + f".{os.getpid()}.tmp"
+        cmd = ["gcc", "-O2", "-std=gnu11", "-shared", "-fPIC", "-I",
+               sysconfig.get_paths()["include"], "-o", tmp, CALLS_SRC]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed on {CALLS_SRC}:\n{r.stderr}")
+        os.replace(tmp, CALLS)
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, _sources()))
+        calls.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
