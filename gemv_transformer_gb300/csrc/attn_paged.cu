@@ -249,22 +249,26 @@ struct Cursor {
 // The workspace: the rows that are split, their parts, and for the weight sums where each row
 // is, its heads' lse and every score.
 struct Room {
-    int4 *rows;         // [n_seq * rows], for the weight sums: the row's first CTA, its CTAs,
-                        // the first's part
+    int4 *rows;         // [n_seq * rows], where there are no more rows than CTAs and for the
+                        // weight sums: the row's first CTA, its CTAs, the first's part
     int4 *splits;       // [grid] the row that a CTA begins and others go on with: (sequence,
                         // row, CTAs, the first's part); no CTAs: none
     float *parts, *lse, *scores;
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-__host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part_floats) {
+__host__ __device__ inline size_t rows_bytes(int n_seq, int h_q, bool with_acc) {
+    return up256((with_acc ? (size_t)n_seq * h_q : 0) * 16 + kMaxCtas * 16);  // a row has a head
+}
+__host__ __device__ inline Room room_of(void *p, int n_seq, int h_q, size_t part_floats,
+                                        bool with_acc) {
     char *c = static_cast<char *>(p);
     Room r;
     r.splits = reinterpret_cast<int4 *>(c);
     c += up256(kMaxCtas * 16);
     r.parts = reinterpret_cast<float *>(c);
     c += up256(2ull * kMaxCtas * part_floats * 4);
-    r.rows = reinterpret_cast<int4 *>(c);  // a row has a head at least
-    c += up256((size_t)n_seq * h_q * 16);
+    r.rows = reinterpret_cast<int4 *>(c);
+    c += rows_bytes(n_seq, h_q, with_acc);
     r.lse = reinterpret_cast<float *>(c);
     c += up256((size_t)n_seq * h_q * 4);
     r.scores = reinterpret_cast<float *>(c);
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
-    const Room room = room_of(a.workspace, a.n_seq, a.h_q, S::kPart);
+    const Room room = room_of(a.workspace, a.n_seq, a.h_q, S::kPart, a.acc_out != nullptr);
     const int rows = kv.n_heads * head_tiles;
     __shared__ long long s_total;
 
@@ -892,7 +896,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             if (begins && threadIdx.x == 0) {
                 const int n = ends ? 1 : owner_of_end() - (int)blockIdx.x + 1;
                 if (n > 1) room.splits[blockIdx.x] = make_int4(use.s, use.row, n, leads ? 0 : 1);
-                if (a.acc_out)
+                if (a.acc_out || (long long)a.n_seq * rows <= gridDim.x)
                     room.rows[(long long)use.s * rows + use.row] =
                         make_int4(blockIdx.x, n, leads ? 0 : 1, 0);
             }
@@ -1022,95 +1026,128 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
     return top == -INFINITY && sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
-// After the split kernel.  The first grid * row_heads blocks join the parts of the rows that
-// several CTAs shared: block (CTA, head) the row that the CTA begins.  The others sum the
-// weights, acc_out[s][h][j] = acc_in + sum over the group's heads of exp(x_j - lse): block
-// (sequence and kv head, piece of the slots).  Both are chains of loads that wait for one
-// another, so whatever does not wait (the parts' o, the scores) is asked for before it is
-// known what it is worth.
-constexpr int kJoinWarps = 8, kAhead = 4;
+// After the split kernel.  The first `joins` blocks join the parts of the rows that several
+// CTAs shared: each row where there are no more rows than CTAs, else the row that a CTA begins.
+// With few rows a block is a head of a row and its warps share the parts;
+// with more a block is a row, a warp joins a head of a few parts, and the block's warps meet
+// for a head of many.
+// The other blocks sum the weights, acc_out[s][h][j] = acc_in + sum over the group's heads of
+// exp(x_j - lse): block (sequence and kv head, piece of the slots).  All are chains of loads
+// that wait for one another, so whatever does not wait (the parts' o, the scores) is asked for
+// before it is known what it is worth.
+constexpr int kJoinWarps = 8, kAhead = 4, kFewParts = 16;
 constexpr int kSlotsPer = 4, kPiece = kSlotsPer * kJoinWarps * 32;  // slots of a block
 __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     attn_join_kernel(AttnArgs a, int n_heads, int head_dim, int head_tiles, int heads, int dp,
-                     int grid, int row_heads, int pieces) {
+                     int grid, int joins, int blocks_per_row, int pieces) {
     __shared__ float s_f[kMaxCtas];
     __shared__ float4 s_o[kJoinWarps][64];
     __shared__ float s_red[2];
     extern __shared__ float s_lse[];  // [group], for the weight sums
     pdl_wait();
     const int part_floats = heads * (dp + 2);
-    const Room room = room_of(a.workspace, a.n_seq, a.h_q, part_floats);
+    const Room room =
+        room_of(a.workspace, a.n_seq, a.h_q, part_floats, a.acc_out != nullptr);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x < grid * row_heads) {
-        const int cta = blockIdx.x / row_heads, head = blockIdx.x - cta * row_heads;
-        const int4 split = room.splits[cta];
-        const int s = split.x, n = split.z;
-        const int h = split.y / head_tiles, in_group = (split.y - h * head_tiles) * heads + head;
-        if (n == 0 || in_group >= a.group) return;
-        auto part = [&](int i) {
-            return room.parts + (2ll * (cta + i) + (i == 0 ? split.w : 0)) * part_floats;
-        };
+    const int rows = n_heads * head_tiles;
+    if ((int)blockIdx.x < joins) {
+        const bool by_rows = (long long)a.n_seq * rows <= grid;
+        const int item = blockIdx.x / blocks_per_row;
+        const int4 r = by_rows ? room.rows[item] : room.splits[item];
+        const int s = by_rows ? item / rows : r.x, row = by_rows ? item - s * rows : r.y;
+        const int first = by_rows ? r.x : item, n = by_rows ? r.y : r.z;
+        const int skip = by_rows ? r.z : r.w;
+        if (n <= 1) return;  // written by its CTA, or no row
+        const int h = row / head_tiles, head0 = (row - h * head_tiles) * heads;
         const int quads = head_dim / 4;
-        auto o_of = [&](int i, int q) {
+        auto part = [&](int i) {
+            return room.parts + (2ll * (first + i) + (i == 0 ? skip : 0)) * part_floats;
+        };
+        auto o_of = [&](int i, int head, int q) {
             return *reinterpret_cast<const float4 *>(part(i) + 2 * heads + head * dp + 4 * q);
         };
-        float4 ahead[kAhead];  // this warp's first parts of dims 4 lane ..
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (warp + u * kJoinWarps < n && lane < quads) ahead[u] = o_of(warp + u * kJoinWarps, lane);
-        if (warp == 0) {
-            float top, sum;
-            join_head(n, head, heads, part, s_f, top, sum);
-            if (lane == 0) {
-                s_red[0] = top;
-                s_red[1] = sum;
-            }
-        }
-        __syncthreads();
-        const float top = s_red[0], sum = s_red[1];
-        const bool none = top == -INFINITY && sum == 0.f;
-        const int qh = h * a.group + in_group;
-        for (int q = lane; q < quads; q += 32) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto add = [&](const float4 &x, float f) {
-                v.x += f * x.x;
-                v.y += f * x.y;
-                v.z += f * x.z;
-                v.w += f * x.w;
-            };
-            int i = warp;
-            if (q == lane) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (warp + u * kJoinWarps < n) add(ahead[u], s_f[warp + u * kJoinWarps]);
-                i += kAhead * kJoinWarps;
-            }
-#pragma unroll 4
-            for (; i < n; i += kJoinWarps) add(o_of(i, q), s_f[i]);
-            s_o[warp][q] = v;
-        }
-        __syncthreads();
-        for (int q = threadIdx.x; q < quads; q += kJoinWarps * 32) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [](float4 &v, const float4 &x, float f) {
+            v.x += f * x.x;
+            v.y += f * x.y;
+            v.z += f * x.z;
+            v.w += f * x.w;
+        };
+        auto store = [&](int head, int q, const float4 &v, float top, float sum) {
+            const bool none = top == -INFINITY && sum == 0.f;
             const float inv = none ? 0.f : 1.f / sum;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                v.x += s_o[w][q].x;
-                v.y += s_o[w][q].y;
-                v.z += s_o[w][q].z;
-                v.w += s_o[w][q].w;
-            }
+            const int qh = h * a.group + head0 + head;
             *reinterpret_cast<float4 *>(a.out + s * a.out_stride + (long long)qh * head_dim +
                                         4 * q) =
                 none ? make_float4(0.f, 0.f, 0.f, 0.f)
                      : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            if (q == 0 && a.lse) a.lse[(long long)s * a.h_q + qh] = lse_of(top, sum);
+        };
+        const bool by_head = blocks_per_row > 1;
+        if (!by_head && n <= kFewParts) {
+            for (int head = warp; head < heads && head0 + head < a.group; head += kJoinWarps) {
+                float4 ahead[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (u < n && lane < quads) ahead[u] = o_of(u, head, lane);
+                float *f = s_f + warp * kFewParts, top, sum;
+                join_head(n, head, heads, part, f, top, sum);
+                __syncwarp();
+                for (int q = lane; q < quads; q += 32) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int from = q == lane ? kAhead : 0;
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u)
+                        if (u < n && u < from) add(v, ahead[u], f[u]);
+                    for (int i = from; i < n; ++i) add(v, o_of(i, head, q), f[i]);
+                    store(head, q, v, top, sum);
+                }
+                __syncwarp();
+            }
+            return;
         }
-        if (threadIdx.x == 0 && a.lse) a.lse[(long long)s * a.h_q + qh] = lse_of(top, sum);
+        const int head1 = by_head ? blockIdx.x - item * blocks_per_row : 0;
+        const int head2 = by_head ? head1 + 1 : heads;
+        for (int head = head1; head < head2 && head0 + head < a.group; ++head) {
+            float4 ahead[kAhead];  // this warp's first parts of dims 4 lane ..
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (warp + u * kJoinWarps < n && lane < quads)
+                    ahead[u] = o_of(warp + u * kJoinWarps, head, lane);
+            if (warp == 0) {
+                float top, sum;
+                join_head(n, head, heads, part, s_f, top, sum);
+                if (lane == 0) {
+                    s_red[0] = top;
+                    s_red[1] = sum;
+                }
+            }
+            __syncthreads();
+            const float top = s_red[0], sum = s_red[1];
+            for (int q = lane; q < quads; q += 32) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                int i = warp;
+                if (q == lane) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u, i += kJoinWarps)
+                        if (i < n) add(v, ahead[u], s_f[i]);
+                }
+#pragma unroll 4
+                for (; i < n; i += kJoinWarps) add(v, o_of(i, head, q), s_f[i]);
+                s_o[warp][q] = v;
+            }
+            __syncthreads();
+            for (int q = threadIdx.x; q < quads; q += kJoinWarps * 32) {
+                float4 v = s_o[0][q];
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) add(v, s_o[w][q], 1.f);
+                store(head, q, v, top, sum);
+            }
+            __syncthreads();  // s_f, s_o and s_red are the next head's
+        }
         return;
     }
 
-    const int id = (blockIdx.x - grid * row_heads) / pieces;
-    const int piece = blockIdx.x - grid * row_heads - id * pieces;
+    const int id = (blockIdx.x - joins) / pieces, piece = blockIdx.x - joins - id * pieces;
     const int s = id / n_heads, h = id - s * n_heads;
     const Span span = span_of(a, s);
     const int j0 = piece * kPiece + threadIdx.x;
@@ -1227,12 +1264,14 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
                      a, kv, head_tiles);
     if (err != cudaSuccess) return err;
     const int row_heads = min(a.group, S::kHeads);
+    const int blocks_per_row = rows * row_heads <= 2 * dev.sm_count ? row_heads : 1;
+    const int joins = (int)(rows <= slots ? rows : slots) * blocks_per_row;
     const int pieces = a.acc_out ? (int)((a.n_slots + (long long)kPiece - 1) / kPiece) : 0;
-    const long long blocks = (long long)slots * row_heads + (long long)a.n_seq * kv.n_heads * pieces;
+    const long long blocks = joins + (long long)a.n_seq * kv.n_heads * pieces;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     return launch_pdl(attn_join_kernel, dim3((unsigned)blocks), dim3(kJoinWarps * 32),
                       a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads, kv.head_dim, head_tiles,
-                      S::kHeads, DP, slots, row_heads, pieces);
+                      S::kHeads, DP, slots, joins, blocks_per_row, pieces);
 }
 
 template <int DT>
@@ -1259,10 +1298,10 @@ cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &d
 
 size_t attn_workspace_bytes(const KvView &kv, int n_seq, int h_q, int n_slots, bool with_acc) {
     const int dp = padded_dim(kv.head_dim), ht = head_tile(h_q / kv.n_heads, dp, kv.dtype);
-    size_t bytes = up256(kMaxCtas * 16) + up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4);
+    size_t bytes = up256(kMaxCtas * 16) + up256(2ull * kMaxCtas * ht * 8 * (dp + 2) * 4) +
+                   rows_bytes(n_seq, h_q, with_acc);
     if (with_acc)
-        bytes += up256((size_t)n_seq * h_q * 16) + up256((size_t)n_seq * h_q * 4) +
-                 up256((size_t)n_seq * h_q * n_slots * 4);
+        bytes += up256((size_t)n_seq * h_q * 4) + up256((size_t)n_seq * h_q * n_slots * 4);
     return bytes;
 }
 

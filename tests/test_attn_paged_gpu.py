@@ -350,3 +350,15 @@ def test_calls_of_a_step_are_captured_in_a_graph():
     for a, b in zip((q, out, acc, acc2, pos2, lens2, *c.pools), want):
         assert np.array_equal(bits(a), bits(b))
     assert lens2.tolist() == [200, 41]
+
+
+@pytest.mark.parametrize("n,hq,long", [(300, 6, 30000), (60, 8, 40000), (3, 6, 50000)])
+@pytest.mark.parametrize("with_acc", [False, True])
+def test_one_long_row_among_short_ones(n, hq, long, with_acc):
+    """The long rows are in dozens of parts, the others whole or in two: more rows than CTAs,
+    fewer, few."""
+    g = np.random.default_rng(n)
+    lens = [int(x) for x in g.integers(0, 6, n)]
+    lens[n // 2] = long
+    c = Cache(g, lens, 2, 64, "bf16", 64, max_pages=-(-long // 64))
+    check(c, lens, hq, queries(g, n, hq, 64), 0.125, with_acc=with_acc)
