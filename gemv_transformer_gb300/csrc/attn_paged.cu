@@ -7,7 +7,12 @@
 // and parts (m, l, o) of a row are joined by the same rule, always in slot order.
 //
 // What bounds it: every live slot's k and v are read once and used group times (4 group
-// operations per 2 bytes of a bf16 cache), so the cache's bytes set the floor.
+// operations per 2 bytes of a bf16 cache), so the cache's bytes set the floor.  Measured (the
+// whole call, back to back; 6704 GB/s is this GPU's copy rate): 64 sequences of 1 to 8192 slots, 8
+// kv heads of 128 in bf16, 64 query heads, 1.08 GB: 167 us, 6430 GB/s; one sequence of
+// 131072, 32 query heads: 89 us, 6010 GB/s, of which 7 us pass before the first tile is done
+// (lengths, page numbers, the tile: three loads that wait for one another) and 4 after the
+// last (the join).  Shorter calls are that chain: 391 slots 7.0 us.
 //
 // Products: the heads of a group are the rows of mma.sync operands, eight heads to a
 // fragment, and an f32 value is split into terms of the operand's type that are exact
@@ -26,8 +31,10 @@
 //
 // Loads: each warp keeps a ring of tiles of KT slots (k and v) in flight by cp.async and
 // waits for no other warp: a CTA's warps meet only where a row (sequence, kv head, up to
-// 16 query heads) ends.  A slot that takes no part (beyond the length, masked by -inf, in
-// a page out of range) is filled with zeros in shared memory and not read.
+// 16 query heads) ends.  64 KB per CTA and three CTAs per SM (two where registers or a row of
+// 256 dims want it): 12 warps hide the chain of a tile better than 8 with a deeper ring
+// (131072 slots: 91 and 110 us).  A slot that takes no part (beyond the length, masked by
+// -inf, in a page out of range) is filled with zeros in shared memory and not read.
 //
 // Work: the rows' tiles, one row after another, are dealt out in equal contiguous ranges to
 // a fixed grid, whatever the lengths; a CTA finds its range from the lengths.  A row within
