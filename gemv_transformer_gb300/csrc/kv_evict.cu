@@ -4,14 +4,14 @@
 // eleven bits of an order-preserving key at a time; the slots that stay but lie beyond the
 // budget then move, in order, into the slots below it that go.  Only they move: a cache
 // over its budget by one slot a step moves one slot, not the half of the cache that keeping
-// the order would.
+// the order would.  A row over by one needs no more than its minimum.
 //
 // What bounds it: 8 bytes read per slot (weight, position), 8 written per slot kept, and two
-// rows of k and v read and written per slot moved; with few rows, or one slot over, the
-// chain of three histograms.  Measured: 512 rows of 2049 slots, one over: 10.3 us (17 MB; 2.6
-// at the copy rate), of which 3 load the keys, 3 find the bound, 2 rank the slots and 1
-// moves; 32 rows of 65536 cut to 4096: 58 us (145 MB; 21.6), of which 6, 7 and 14, and 24
-// move 126 MB in rows of 256 bytes.
+// rows of k and v read and written per slot moved; with few rows the chain of three
+// histograms, or with one slot over of three loads.  Measured: 512 rows of 2049 slots, one
+// over: 4.6 us (17 MB; 2.6 at the copy rate; 10.1 by histograms); 32 rows of 65536 cut to 4096:
+// 58 us (145 MB; 21.6), of which 6 load the keys, 7 find the bound, 14 rank and list the
+// slots, and 24 move 126 MB in rows of 256 bytes.
 //
 // A row is a cluster of 1, 2, 4 or 8 CTAs, so that a few long rows fill the GPU: each holds
 // the keys of its share of the slots in shared memory, the histograms and counts are
@@ -141,6 +141,109 @@ __device__ __forceinline__ void move_all(const EvictArgs &a, const KvView &kv, i
         move_rows<1>(a, kv, row_bytes, base, list, total, warp, warps);
 }
 
+// One slot over the budget: the steady state of a cache that is cut after every token.  The
+// slot of the least key goes (of equal ones the highest) and the last slot takes its place:
+// a minimum in place of the histograms and ranks, and the last slot's rows, which move
+// whichever slot goes, are read beside the weights.  8 rows of 2049 slots 2.7 us (by histograms
+// 7.0), of 65536 4.6 (12.5); 1024 rows of 2049 8.1 (17.5).
+template <int T, int C>
+__device__ __forceinline__ void evict_one(const EvictArgs &a, const KvView &kv, Select<T, C> &sh,
+                                          int row_bytes, long long base, int s, int h, int b0,
+                                          int b1, int from) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, last = a.keep;
+    const int rank = C == 1 ? 0 : cg::this_cluster().block_rank();
+    const bool mover = rank == 0 && warp == 0, copies = a.acc_out != a.acc || a.pos_out != a.slot_pos;
+    const int quads = row_bytes / 16;  // of k; as many of v
+    long long at = -1;
+    float w_last = 0.f;
+    int p_last = 0;
+    if (mover) {
+        at = kv.row(s, h, last);
+        w_last = a.acc[base + last];
+        p_last = a.slot_pos[base + last];
+    }
+    constexpr int B = 8;  // slots of a thread in flight
+    uint32_t key = kHeld;
+    int slot = -1;
+    for (int j0 = b0 + threadIdx.x; j0 < b1; j0 += B * T) {
+        float w[B];
+        int p[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (j0 + i * T < b1) w[i] = a.acc[base + j0 + i * T], p[i] = a.slot_pos[base + j0 + i * T];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int j = j0 + i * T;
+            if (j >= b1) continue;
+            const uint32_t x = key_of(w[i], p[i], a.sinks, from);
+            if (x <= key) key = x, slot = j;
+            if (copies && j < last) {
+                a.acc_out[base + j] = w[i];
+                a.pos_out[base + j] = p[i];
+            }
+        }
+    }
+    // The last slot's k and v: four pieces of 512 bytes hold rows of 256 dims in f32.
+    uint4 x[4];
+    if (mover && at >= 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int q = lane + 32 * i;
+            if (q < 2 * quads)
+                x[i] = *reinterpret_cast<const uint4 *>(
+                    (q < quads ? kv.k : kv.v) + at + 16ll * (q < quads ? q : q - quads));
+        }
+    }
+    // The least key, then its highest slot.
+    auto least = [&]() {
+        const uint32_t k = __reduce_min_sync(0xFFFFFFFFu, key);
+        slot = __reduce_max_sync(0xFFFFFFFFu, key == k ? slot : -1);
+        key = k;
+    };
+    least();
+    int *const keys = sh.scan[0], *const slots = sh.scan[1];
+    if (lane == 0) keys[warp] = (int)key, slots[warp] = slot;
+    __syncthreads();
+    if (C > 1) {
+        // Every CTA's goes to the first, beside the warps' own.
+        if (warp == 0) {
+            key = lane < T / 32 ? (uint32_t)keys[lane] : kHeld;
+            slot = lane < T / 32 ? slots[lane] : -1;
+            least();
+            if (lane == 0) {
+                cg::cluster_group cluster = cg::this_cluster();
+                int *to = cluster.map_shared_rank(&sh.hist[0][0], 0);
+                to[rank] = (int)key;
+                to[C + rank] = slot;
+            }
+        }
+        cg::this_cluster().sync();
+    }
+    pdl_launch();
+    if (!mover) return;
+    constexpr int kFrom = C > 1 ? C : T / 32;
+    const int *const all_keys = C > 1 ? &sh.hist[0][0] : keys;
+    const int *const all_slots = C > 1 ? &sh.hist[0][C] : slots;
+    key = lane < kFrom ? (uint32_t)all_keys[lane] : kHeld;
+    slot = lane < kFrom ? all_slots[lane] : -1;
+    least();
+    if (slot == last) return;
+    const long long to = kv.row(s, h, slot);
+    if (lane == 0) {
+        a.acc_out[base + slot] = w_last;
+        a.pos_out[base + slot] = p_last;
+        if (to < 0 || at < 0) record_status(a.status, kStBadIndex);
+    }
+    if (to < 0 || at < 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int q = lane + 32 * i;
+        if (q < 2 * quads)
+            *reinterpret_cast<uint4 *>((q < quads ? kv.k : kv.v) + to +
+                                       16ll * (q < quads ? q : q - quads)) = x[i];
+    }
+}
+
 // C: the CTAs of a row; with one, its barriers are the CTA's.
 template <int T, int C>
 __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView kv, int row_bytes,
@@ -190,6 +293,11 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
                 a.acc_out[base + j] = acc[j];
                 a.pos_out[base + j] = pos[j];
             }
+        return;
+    }
+    if (len == keep + 1) {
+        evict_one<T, C>(a, kv, sh, row_bytes, base, s, h, b0, b1, from);
+        if (counts && threadIdx.x == 0 && rank == 0) counts[id] = 0;
         return;
     }
     const bool held_keys = mine <= key_room;
@@ -496,10 +604,10 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     const long long rows = (long long)a.n_seq * kv.n_heads;
     if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
     // More CTAs to a row while two per SM are not reached and each has over 4096 slots or 128
-    // moves (8 rows of 20000 slots, one over: 1 CTA 17.5 us, 8 take 10.8; of 2049: 6.3 and 7.9;
+    // moves (8 rows of 20000 slots, one over: 1 CTA 6.3 us, 8 take 3.5; of 2049: 2.7 and 3.2;
     // 8 rows of 4096 cut to 1024: 26.2 and 12.4).  512 threads while two such CTAs per SM hold
-    // all rows or the rows are long, else 256 (512 rows of 2049: 10.3 us, with 512 14.7;
-    // of 8193 37.1 and 30.8); 1024 where one CTA per SM holds few long rows.
+    // all rows or the rows are long, else 256 (512 rows of 2049, one over: 4.7 us, with 512
+    // 5.8; of 8193 19.2 and 16.0); 1024 where one CTA per SM holds few long rows.
     const long long moves = a.keep < a.n_slots - a.keep ? a.keep : a.n_slots - a.keep;
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&

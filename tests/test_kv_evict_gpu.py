@@ -257,3 +257,58 @@ def test_long_rows_by_their_own_numbers(n, hkv, length, keep, d, kind, ties):
                 row = pool.view(bits_of)[rows, h].view(-1, d)[:keep].long()
                 assert np.array_equal((row[:, 0] + (row[:, 1] << 15)).cpu().numpy(), want)
                 assert not row[:, 2:].any()
+
+
+@pytest.mark.parametrize("n,h,keep,d,kind,page,major", [
+    (1, 1, 1, 64, "bf16", 1, "head"), (3, 2, 255, 128, "f16", 7, "gap"),
+    (70, 8, 300, 8, "bf16", 64, "token"),   # short rows, more than two per SM
+    (1, 2, 6000, 256, "f32", 100, "head"),  # two, four and eight CTAs to a row
+    (2, 1, 12001, 72, "bf16", 64, "token"), (1, 1, 30000, 8, "f32", 64, "head")])
+@pytest.mark.parametrize("how", ["real", "equal", "nan", "held", "last"])
+def test_one_over_the_budget(n, h, keep, d, kind, page, major, how):
+    """The least slot goes, of equal ones the highest, and the last takes its place; rows at
+    and below the budget are among them."""
+    g = np.random.default_rng(keep + d)
+    lens = [keep + 1 if s % 3 != 2 else keep - s % 2 for s in range(n)]
+    c = Cache(g, lens, h, d, kind, page, major, fill=1.0)
+    cap = c.max_pages * page
+    acc = sums(g, n, h, cap)
+    pos = positions(g, n, h, cap, [keep + 9] * n)
+    sinks, recent = min(2, keep), keep // 3
+    if how == "equal":
+        acc[:] = 0.25
+    elif how == "nan":
+        acc[:, :, g.integers(0, cap, 3)] = np.nan
+        acc[:, :, g.integers(0, cap, 3)] = -np.inf
+    elif how == "held":  # more than the budget: the highest slot goes
+        pos[:] = g.integers(0, 2, pos.shape)
+    elif how == "last":  # nothing moves
+        acc[:, :, keep] = -1.0
+        pos[:, :, keep] = sinks
+    seen = [max(keep + 9, cap)] * n
+    run_evict(c, lens, seen, keep, sinks, recent, acc, pos, in_place=how in ("real", "held"))
+
+
+def test_one_over_with_pages_out_of_range():
+    """The last slot's page, then the page of the slot that goes: neither is read or written."""
+    g = np.random.default_rng(9)
+    c = Cache(g, [65, 65], 1, 64, "bf16", 16, fill=1.0)
+    c.pages[0, 4] = -1
+    c.pages[1, 1] = 10 ** 6
+    c.pages_dev = dev(c.pages)
+    acc = 1 + sums(g, 2, 1, 80)
+    acc[:, :, 20] = 0.5
+    pos = np.tile(np.arange(80, dtype=np.int32), (2, 1, 1))
+    before = [p.clone() for p in c.pools]
+    accd, posd = dev(acc), dev(pos)
+    lens = dev(np.array([65, 65], np.int32))
+    size = wq.wq_kv_evict_workspace_bytes(c.desc, 2, 5, 64)
+    wq.check(wq.wq_kv_evict(c.desc, 2, c.pages_dev, 5, lens, lens.clone(), 64, 0, 0, accd, posd,
+                            accd, posd, 80, lens, workspace(size), size))
+    torch.cuda.synchronize()
+    assert wq.wq_get_device_status() == wq.WQ_ERR_BAD_INDEX
+    assert lens.tolist() == [64, 64]
+    for now, was in zip(c.pools, before):
+        assert np.array_equal(bits(now), bits(was))
+    assert (accd[:, 0, 20].cpu().numpy() == acc[:, 0, 64]).all()
+    assert (posd[:, 0, 20] == 64).all()
