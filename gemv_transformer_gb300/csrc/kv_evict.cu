@@ -10,7 +10,7 @@
 // rows of k and v read and written per slot moved; with few rows the chain of three
 // histograms, or with one slot over of three loads.  Measured: 512 rows of 2049 slots, one
 // over: 4.6 us (17 MB; 2.6 at the copy rate; 10.1 by histograms); 32 rows of 65536 cut to 4096:
-// 58 us (145 MB; 21.6), of which 6 load the keys, 7 find the bound, 14 rank and list the
+// 54 us (145 MB; 21.6), of which 6 load the keys, 7 find the bound, 10 rank and list the
 // slots, and 24 move 126 MB in rows of 256 bytes.
 //
 // A row is a cluster of 1, 2, 4 or 8 CTAs, so that a few long rows fill the GPU: each holds
@@ -35,12 +35,12 @@ constexpr int kBatch = 8;            // moves that a warp has in flight
 constexpr int kDigit = 11, kBins = 1 << kDigit, kPasses = 3;  // 11 + 11 + 10 bits
 constexpr int kShort = 128;          // moves that a single CTA lists in shared memory
 
-// One move.  The hole's owner writes `to` and `dst`, the mover's the rest.
-struct __align__(16) Move {
-    long long to, at;  // byte offsets of the rows, -1 for a page out of range
-    int dst;
-    float weight;
-    int pos, pad;
+// One move between slots.  The hole's owner writes `to`, the mover's `at`; where their rows
+// are is looked up by the warp that moves them, ahead of its loads (by those who list the
+// moves, with weights and offsets in the list: 4 % to 25 % slower, 48 for 35 us for 8 rows of
+// 65536 cut to 60000).
+struct __align__(8) Move {
+    int to, at;
 };
 
 constexpr uint32_t kHeld = 0xFFFFFFFFu, kZero = 0x80000000u;
@@ -90,8 +90,10 @@ __device__ __forceinline__ void warp_offsets(Select<T, C> &sh, int &a, int &b, i
 // The next moves are looked up while these moves' rows are on their way.
 template <int PER>
 __device__ __forceinline__ void move_rows(const EvictArgs &a, const KvView &kv, int row_bytes,
-                                          long long base, const Move *list, int total, int warp,
+                                          int id, const Move *list, int total, int warp,
                                           int warps) {
+    const int s = id / kv.n_heads, h = id - s * kv.n_heads;
+    const long long base = (long long)id * a.acc_stride;
     const int lane = threadIdx.x & 31, quads = row_bytes / 16;  // of k; as many of v
     constexpr int per = PER, batch = kBatch * PER;
     const int sub = PER == 1 ? 0 : lane / (32 / PER), first = PER == 1 ? lane : lane % (32 / PER);
@@ -100,10 +102,16 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, const KvView &kv, 
         to = at = -1;
         if (lane < batch && i0 + lane < total) {
             const Move m = list[i0 + lane];
-            a.acc_out[base + m.dst] = m.weight;
-            a.pos_out[base + m.dst] = m.pos;
-            at = m.at;
-            to = m.at < 0 ? -1 : m.to;
+            at = kv.row(s, h, m.at);
+            to = kv.row(s, h, m.to);
+            const float w = a.acc[base + m.at];
+            const int p = a.slot_pos[base + m.at];
+            if (at < 0 || to < 0) {
+                record_status(a.status, kStBadIndex);
+                to = -1;
+            }
+            a.acc_out[base + m.to] = w;
+            a.pos_out[base + m.to] = p;
         }
     };
     int i0 = warp * batch;
@@ -133,12 +141,12 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, const KvView &kv, 
 }
 
 __device__ __forceinline__ void move_all(const EvictArgs &a, const KvView &kv, int row_bytes,
-                                         long long base, const Move *list, int total, int warp,
+                                         int id, const Move *list, int total, int warp,
                                          int warps) {
     if (row_bytes == 128)
-        move_rows<2>(a, kv, row_bytes, base, list, total, warp, warps);
+        move_rows<2>(a, kv, row_bytes, id, list, total, warp, warps);
     else
-        move_rows<1>(a, kv, row_bytes, base, list, total, warp, warps);
+        move_rows<1>(a, kv, row_bytes, id, list, total, warp, warps);
 }
 
 // One slot over the budget: the steady state of a cache that is cut after every token.  The
@@ -510,26 +518,10 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
         int all;  // holes in the low half, movers in the high one
         const int at = lane_offsets(__popc(v & 15u) | __popc(v >> 4) << 16, all);
         Move *to_hole = list + holes + (at & 0xFFFF), *to_mover = list + movers + (at >> 16);
-        long long row[4];
-        float w[4];
-        int p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (v >> i & 17u) row[i] = kv.row(s, h, j + i);
-            if (v >> i & 16u) w[i] = acc[j + i], p[i] = pos[j + i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!(v >> i & 17u)) continue;
-            if (row[i] < 0) record_status(a.status, kStBadIndex);
-            if (v >> i & 1u) {
-                to_hole->to = row[i];
-                to_hole++->dst = j + i;
-            } else {
-                to_mover->at = row[i];
-                to_mover->weight = w[i];
-                to_mover++->pos = p[i];
-            }
+            if (v >> i & 1u) (to_hole++)->to = j + i;
+            if (v >> i & 16u) (to_mover++)->at = j + i;
         }
         holes += all & 0xFFFF;
         movers += all >> 16;
@@ -541,7 +533,7 @@ __global__ void __launch_bounds__(T, 1024 / T) evict_kernel(EvictArgs a, KvView 
         if (threadIdx.x == 0 && rank == 0) counts[id] = total;
         return;
     }
-    move_all(a, kv, row_bytes, base, list, total, rank * (T / 32) + warp, C * (T / 32));
+    move_all(a, kv, row_bytes, id, list, total, rank * (T / 32) + warp, C * (T / 32));
 }
 
 // The moves of rows whose selection left them: blocks_per_row blocks to each.
@@ -549,7 +541,7 @@ __global__ void __launch_bounds__(256, 4) evict_move_kernel(EvictArgs a, KvView 
                                                             const int *counts, int blocks_per_row) {
     pdl_enter();
     const int id = blockIdx.x / blocks_per_row, block = blockIdx.x - id * blocks_per_row;
-    move_all(a, kv, row_bytes, (long long)id * a.acc_stride,
+    move_all(a, kv, row_bytes, id,
              static_cast<const Move *>(a.workspace) + (long long)id * min(a.keep, a.n_slots),
              counts[id], block * 8 + (threadIdx.x >> 5), blocks_per_row * 8);
 }
