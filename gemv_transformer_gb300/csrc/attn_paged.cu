@@ -998,30 +998,33 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
     }
 }
 
+constexpr int kJoinAtOnce = 64;  // parts whose m and l a warp asks for at once
+
 // m and l of a row's head joined over n parts by one warp; the parts' factors go to f if given.
 template <typename Part>
 __device__ __forceinline__ void join_head(int n, int head, int heads, Part part, float *f,
                                           float &top, float &sum) {
     const int lane = threadIdx.x & 31;
-    float m[2], l[2];  // the first 64 parts' at once
+    constexpr int kAtOnce = kJoinAtOnce / 32;
+    float m[kAtOnce], l[kAtOnce];  // the first parts'
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAtOnce; ++u) {
         const int i = lane + 32 * u;
         m[u] = i < n ? part(i)[head] : -INFINITY;
         l[u] = i < n ? part(i)[heads + head] : 0.f;
     }
     top = fmaxf(m[0], m[1]);
-    for (int i = lane + 64; i < n; i += 32) top = fmaxf(top, part(i)[head]);
+    for (int i = lane + kJoinAtOnce; i < n; i += 32) top = fmaxf(top, part(i)[head]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     sum = 0.f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAtOnce; ++u) {
         const float x = exp_diff(m[u], top);
         if (f && lane + 32 * u < n) f[lane + 32 * u] = x;
         sum += x * l[u];
     }
-    for (int i = lane + 64; i < n; i += 32) {
+    for (int i = lane + kJoinAtOnce; i < n; i += 32) {
         const float x = exp_diff(part(i)[head], top);
         if (f) f[i] = x;
         sum += x * part(i)[heads + head];
@@ -1041,15 +1044,16 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // The other blocks sum the weights, acc_out[s][h][j] = acc_in + sum over the group's heads of
 // exp(x_j - lse): block (sequence and kv head, piece of the slots).  All are chains of loads
 // that wait for one another, so whatever does not wait (the parts' o, the scores) is asked for
-// before it is known what it is worth.
+// before it is known what it is worth.  MANY: rows have over 64 parts on average.
 constexpr int kJoinWarps = 8, kAhead = 4, kFewParts = 16;
 constexpr int kSlotsPer = 4, kPiece = kSlotsPer * kJoinWarps * 32;  // slots of a block
+template <bool MANY>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     attn_join_kernel(AttnArgs a, int n_heads, int head_dim, int head_tiles, int heads, int dp,
                      int grid, int joins, int blocks_per_row, int pieces) {
     __shared__ float s_f[kMaxCtas];
     __shared__ float4 s_o[kJoinWarps][64];
-    __shared__ float s_red[2];
+    __shared__ float s_red[2], s_top[MANY ? kJoinWarps : 1][16], s_sum[MANY ? kJoinWarps : 1][16];
     extern __shared__ float s_lse[];  // [group], for the weight sums
     pdl_wait();
     const int part_floats = heads * (dp + 2);
@@ -1172,26 +1176,57 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) ahead[u][i] = i < a.group ? score(i, j) : -INFINITY;
     }
-    // The group's lse: whole rows have theirs.
-    for (int i = warp; i < a.group; i += kJoinWarps) {
-        const int ht = i / heads;
-        const float whole = room.lse[q0 + i];  // of a split row: whatever is there, not used
+    // The group's lse: whole rows have theirs, and of a row of few parts a warp joins a head.
+    // MANY: a lane joins a head of every (8 * 32 / heads)-th part: their m and l are short runs
+    // of neighbours, of which a warp to a head reads a sector for each value (120000 slots, a
+    // row of 8 heads in 456 parts: 27 us, 55 by warps; 57 parts: 58 and 57; 2 parts 16 and 14).
+    for (int ht = 0; ht < head_tiles; ++ht) {
         const int4 row = room.rows[(long long)id * head_tiles + ht];
         const int first = row.x, n = row.y, skip = row.z;
-        float e;
-        if (n > 1) {
-            float top, sum;
-            join_head(
-                n, i - ht * heads, heads,
-                [&](int k) {
-                    return room.parts + (2ll * (first + k) + (k == 0 ? skip : 0)) * part_floats;
-                },
-                nullptr, top, sum);
-            e = lse_of(top, sum);
-        } else {
-            e = whole;
+        const int in_tile = min(heads, a.group - ht * heads);
+        float *lse = s_lse + ht * heads;
+        auto part = [&](int k) {
+            return room.parts + (2ll * (first + k) + (k == 0 ? skip : 0)) * part_floats;
+        };
+        if (!MANY || n <= 1) {
+            for (int head = warp; head < in_tile; head += kJoinWarps) {
+                const float whole = room.lse[q0 + ht * heads + head];  // unused if split
+                float top, sum;
+                if (n > 1) join_head(n, head, heads, part, (float *)nullptr, top, sum);
+                if (lane == 0) lse[head] = n > 1 ? lse_of(top, sum) : whole;
+            }
+            continue;
         }
-        if (lane == 0) s_lse[i] = e;
+        const int per = 32 / heads, head = lane & (heads - 1);
+        float top = -INFINITY, sum = 0.f;
+        auto join = [&](float m, float l) {
+            const float t = fmaxf(top, m);
+            sum = sum * exp_diff(top, t) + l * exp_diff(m, t);
+            top = t;
+        };
+        for (int k0 = warp * per + lane / heads; k0 < n; k0 += kAhead * kJoinWarps * per) {
+            float m[kAhead], l[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = k0 + u * kJoinWarps * per;
+                m[u] = k < n ? part(k)[head] : -INFINITY;
+                l[u] = k < n ? part(k)[heads + head] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) join(m[u], l[u]);
+        }
+        for (int o = heads; o < 32; o <<= 1) {
+            const float m = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+            const float l = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            join(m, l);
+        }
+        __syncthreads();  // the tile before has been read
+        if (lane < heads) s_top[warp][head] = top, s_sum[warp][head] = sum;
+        __syncthreads();
+        if (warp == 0 && lane < in_tile) {
+            for (int w = 1; w < kJoinWarps; ++w) join(s_top[w][head], s_sum[w][head]);
+            lse[head] = lse_of(top, sum);
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -1276,7 +1311,8 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     const int pieces = a.acc_out ? (int)((a.n_slots + (long long)kPiece - 1) / kPiece) : 0;
     const long long blocks = joins + (long long)a.n_seq * kv.n_heads * pieces;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    return launch_pdl(attn_join_kernel, dim3((unsigned)blocks), dim3(kJoinWarps * 32),
+    const bool many = rows * kJoinAtOnce < slots;
+    return launch_pdl(many ? attn_join_kernel<true> : attn_join_kernel<false>, dim3((unsigned)blocks), dim3(kJoinWarps * 32),
                       a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads, kv.head_dim, head_tiles,
                       S::kHeads, DP, slots, joins, blocks_per_row, pieces);
 }

@@ -605,11 +605,12 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&
            (a.n_slots / cluster > 4096 || moves / cluster > 128))
         cluster *= 2;
-    // Where half the GPU or more has no row and 8 MB or more may move, the moves are a launch
-    // of their own over all SMs.
+    // Where SMs have no row and a CTA may have 80 KB or more to move, the moves are a launch of
+    // their own over all SMs (3 rows of 9293 cut to 3506, 214 KB: 12.8 us, by the rows' CTAs
+    // 18.3; 105 KB: 13.4 and 14.9; 62 KB: 15.2 and 12.2).
     const int row_bytes = row_bytes_of(kv);
     int *counts = nullptr;
-    if (rows * cluster <= dev.sm_count && rows * moves * row_bytes * 2 >= 8ll << 20)
+    if (rows * cluster <= dev.sm_count && moves * row_bytes * 2 >= cluster * (80ll << 10))
         counts = reinterpret_cast<int *>(static_cast<Move *>(a.workspace) +
                                          rows * (a.keep < a.n_slots ? a.keep : a.n_slots));
     cudaError_t err;
