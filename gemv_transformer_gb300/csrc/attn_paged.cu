@@ -1045,9 +1045,11 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // exp(x_j - lse): block (sequence and kv head, piece of the slots).  All are chains of loads
 // that wait for one another, so whatever does not wait (the parts' o, the scores) is asked for
 // before it is known what it is worth.  MANY: rows have over 64 parts on average.
+// SLOTS: of a thread; sixteen scores of them are in flight (one after another of a slot's heads,
+// four at a time, took 47 us for a group of 32 over 20000 slots, this 40).
 constexpr int kJoinWarps = 8, kAhead = 4, kFewParts = 16;
-constexpr int kSlotsPer = 4, kPiece = kSlotsPer * kJoinWarps * 32;  // slots of a block
-template <bool MANY>
+constexpr int piece_of(int slots) { return slots * kJoinWarps * 32; }
+template <bool MANY, int SLOTS>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     attn_join_kernel(AttnArgs a, int n_heads, int head_dim, int head_tiles, int heads, int dp,
                      int grid, int joins, int blocks_per_row, int pieces) {
@@ -1161,21 +1163,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     const int id = (blockIdx.x - joins) / pieces, piece = blockIdx.x - joins - id * pieces;
     const int s = id / n_heads, h = id - s * n_heads;
     const Span span = span_of(a, s);
-    const int j0 = piece * kPiece + threadIdx.x;
-    if (piece * kPiece >= span.len) return;
+    const int j0 = piece * piece_of(SLOTS) + threadIdx.x;
+    if (piece * piece_of(SLOTS) >= span.len) return;
     const long long q0 = (long long)s * a.h_q + h * a.group;
     const long long at = (long long)id * a.acc_stride;
-    auto score = [&](int i, int j) {  // of slots that take part; the others have none
-        return j < span.len && j >= span.first ? room.scores[(q0 + i) * a.n_slots + j] : -INFINITY;
-    };
-    float ahead[kSlotsPer][kAhead], w[kSlotsPer];
+    constexpr int kHeadsAhead = 16 / SLOTS;
+    float ahead[SLOTS][kHeadsAhead], w[SLOTS];
+    auto ask = [&](int i0) {  // the scores of slots that take part; the others have none
 #pragma unroll
-    for (int u = 0; u < kSlotsPer; ++u) {
+        for (int u = 0; u < SLOTS; ++u) {
+            const int j = j0 + u * kJoinWarps * 32;
+            const bool live = j < span.len && j >= span.first;
+#pragma unroll
+            for (int i = 0; i < kHeadsAhead; ++i)
+                ahead[u][i] = live && i0 + i < a.group
+                                  ? room.scores[(q0 + i0 + i) * a.n_slots + j] : -INFINITY;
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) {
         const int j = j0 + u * kJoinWarps * 32;
         w[u] = a.acc_in && j < span.len ? a.acc_in[at + j] : 0.f;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) ahead[u][i] = i < a.group ? score(i, j) : -INFINITY;
     }
+    ask(0);
     // The group's lse: whole rows have theirs, and of a row of few parts a warp joins a head.
     // MANY: a lane joins a head of every (8 * 32 / heads)-th part: their m and l are short runs
     // of neighbours, of which a warp to a head reads a sector for each value (120000 slots, a
@@ -1229,20 +1239,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
         }
     }
     __syncthreads();
+    float sum[SLOTS] = {};
+    for (int i0 = 0; i0 < a.group; i0 += kHeadsAhead) {
 #pragma unroll
-    for (int u = 0; u < kSlotsPer; ++u) {
-        const int j = j0 + u * kJoinWarps * 32;
-        if (j >= span.len) continue;
-        float sum = 0.f;
+        for (int i = 0; i < kHeadsAhead; ++i) {
+            const float e = i0 + i < a.group ? s_lse[i0 + i] : -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i < a.group && s_lse[i] != -INFINITY) sum += exp_diff(ahead[u][i], s_lse[i]);
-#pragma unroll 4
-        for (int i = kAhead; i < a.group; ++i) {
-            const float x = score(i, j), e = s_lse[i];
-            sum += e == -INFINITY ? 0.f : exp_diff(x, e);
+            for (int u = 0; u < SLOTS; ++u)
+                if (e != -INFINITY) sum[u] += exp_diff(ahead[u][i], e);
         }
-        a.acc_out[at + j] = w[u] + sum;
+        if (i0 + kHeadsAhead < a.group) ask(i0 + kHeadsAhead);
+    }
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) {
+        const int j = j0 + u * kJoinWarps * 32;
+        if (j < span.len) a.acc_out[at + j] = w[u] + sum[u];
     }
 }
 
@@ -1308,11 +1319,16 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     const int row_heads = min(a.group, S::kHeads);
     const int blocks_per_row = rows * row_heads <= 2 * dev.sm_count ? row_heads : 1;
     const int joins = (int)(rows <= slots ? rows : slots) * blocks_per_row;
-    const int pieces = a.acc_out ? (int)((a.n_slots + (long long)kPiece - 1) / kPiece) : 0;
+    const int slots_per = a.n_slots <= piece_of(1) ? 1 : 4;
+    const int pieces =
+        a.acc_out ? (int)((a.n_slots + (long long)piece_of(slots_per) - 1) / piece_of(slots_per)) : 0;
     const long long blocks = joins + (long long)a.n_seq * kv.n_heads * pieces;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     const bool many = rows * kJoinAtOnce < slots;
-    return launch_pdl(many ? attn_join_kernel<true> : attn_join_kernel<false>, dim3((unsigned)blocks), dim3(kJoinWarps * 32),
+    return launch_pdl(slots_per == 1 ? attn_join_kernel<false, 1>
+                      : many         ? attn_join_kernel<true, 4>
+                                     : attn_join_kernel<false, 4>,
+                      dim3((unsigned)blocks), dim3(kJoinWarps * 32),
                       a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads, kv.head_dim, head_tiles,
                       S::kHeads, DP, slots, joins, blocks_per_row, pieces);
 }

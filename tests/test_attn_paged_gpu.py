@@ -362,3 +362,24 @@ def test_one_long_row_among_short_ones(n, hq, long, with_acc):
     lens[n // 2] = long
     c = Cache(g, lens, 2, 64, "bf16", 64, max_pages=-(-long // 64))
     check(c, lens, hq, queries(g, n, hq, 64), 0.125, with_acc=with_acc)
+
+
+@pytest.mark.parametrize("n,length,hq,hkv,d,kind", [
+    (1, 20000, 5, 1, 64, "bf16"),     # one row in hundreds of parts
+    (2, 9000, 40, 1, 64, "f16"),      # and several tiles of heads to a group
+    (1, 9000, 34, 2, 128, "f32"),
+    (90, 200, 20, 1, 128, "bf16"),    # short caches, a group of more heads than in flight
+    (40, 700, 33, 1, 64, "f16")])
+@pytest.mark.parametrize("masked", [False, True])
+def test_weights_of_large_groups(n, length, hq, hkv, d, kind, masked):
+    g = np.random.default_rng(length + hq)
+    lens = [length] + [int(x) for x in g.integers(length // 2, length, n - 1)]
+    c = Cache(g, lens, hkv, d, kind, 16)
+    cap = c.max_pages * 16
+    mask = None
+    if masked:
+        mask = np.where(g.random((n, cap)) < 0.3, -np.inf, 0.1).astype(np.float32)
+        mask[-1, :cap // 2] = -np.inf
+    acc_in = np.abs(g.standard_normal((n, hkv, cap))).astype(np.float32)
+    check(c, lens, hq, queries(g, n, hq, d), d ** -0.5, window=length // 2 if masked else 0,
+          mask=mask, acc_in=acc_in, with_acc=True)
