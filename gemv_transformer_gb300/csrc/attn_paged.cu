@@ -19,13 +19,18 @@
 // together, the first two in rows g and g + 8 of one product:
 //   bf16 cache  q and p as three bf16 terms (24 bits): a second product has the third, or,
 //               of four heads or fewer, rows 4 to 7 of the first;
-//   f16 cache   two f16 terms (22 bits) of q scaled by a power of two per head to a
-//               largest value near 2^10, and of 2^12 p, so that no term is subnormal;
+//   f16 cache   the same with f16 terms, of q scaled by a power of two per head to a
+//               largest value near 2^10, and of 2^12 p;
 //   f32 cache   two tf32 terms (22 bits) of q, p, k and v.
 // 16-bit operands alone would leave 2^-9.  The tensor core truncates when it
 // accumulates (measured: 1 + 0.92 ulp added 1000 times stays 1), so no accumulation is
 // longer than head_dim / 16 steps of q.k, and every tile's p.v is added to o by an f32
 // FMA that rescales it anyway.
+//
+// A k that is not finite has to show: a slot takes no part by its mask, length or page, never by
+// its score.  A score of -inf would be that slot's weight 0, so every type has a product of an
+// infinite k that is NaN, whatever q: the zero rows beside the third terms (0 inf), or for f32 k
+// minus its high part.
 //
 // p's accumulator fragment is the next product's operand without a move.
 //
@@ -54,7 +59,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxCtas = 456;  // three on each of 152 SMs
 
-// Q4 (bf16): groups of at most four heads, whose third terms take rows 4 to 7 of the one
+// Q4 (16-bit types): groups of at most four heads, whose third terms take rows 4 to 7 of the one
 // product.
 template <int DT, int DP, int HT, bool Q4> struct Shape {
     static constexpr bool k16 = DT != kF32;
@@ -73,7 +78,7 @@ template <int DT, int DP, int HT, bool Q4> struct Shape {
     static constexpr bool kQReg = k16 && HT * DP <= 128;  // q's fragments in registers
     static constexpr int kStep = k16 ? 16 : 8;         // dims of a product step
     static constexpr int kSteps = DP / kStep;
-    static constexpr bool k3 = DT == kBF16 && !Q4;     // a second product for the third term
+    static constexpr bool k3 = k16 && !Q4;             // a second product for the third term
     static constexpr int kQWords = k3 ? 6 : 4;         // registers of a step's fragment
     static constexpr int kQ = W * kStages * kTile;     // q fragments, unless in registers
     static constexpr int kQBytes = kQReg ? 0 : HT * kSteps * 32 * kQWords * 4;
@@ -137,21 +142,21 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// The terms of a pair, packed: t[0] + t[1] (+ t[2]) = (x, y).
+// The terms of a pair, packed: t[0] + t[1] + t[2] = (x, y).
 template <int DT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3]) {
-    if (DT == kBF16) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 3; ++i) {
+        if (DT == kBF16) {
             t[i] = bf16x2(x, y);
             x -= bf16_lo(t[i]);
             y -= bf16_hi(t[i]);
+        } else {
+            t[i] = f16x2(x, y);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&t[i]));
+            x -= h.x;
+            y -= h.y;
         }
-    } else {
-        t[0] = f16x2(x, y);
-        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&t[0]));
-        t[1] = f16x2(x - h.x, y - h.y);
-        t[2] = 0u;
     }
 }
 
@@ -1337,7 +1342,7 @@ template <int DT>
 cudaError_t launch_type(const AttnArgs &a, const KvView &kv, const DeviceInfo &dev,
                         cudaStream_t stream) {
     const int dp = padded_dim(kv.head_dim), ht = head_tile(a.group, dp, DT);
-    if constexpr (DT == kBF16)
+    if constexpr (DT != kF32)
         if (a.group <= 4)
             return dp == 64    ? launch_shape<DT, 64, 1, true>(a, kv, dev, stream)
                    : dp == 128 ? launch_shape<DT, 128, 1, true>(a, kv, dev, stream)
