@@ -15,12 +15,17 @@
 // last (the join).  Shorter calls are that chain: 391 slots 7.0 us.
 //
 // Products: the heads of a group are the rows of mma.sync operands, eight heads to a
-// fragment, and an f32 value is split into terms of the operand's type that are exact
-// together, the first two in rows g and g + 8 of one product:
+// fragment, and an f32 value is split into terms of the operand's type, the first two in rows
+// g and g + 8 of one product:
 //   bf16 cache  q and p as three bf16 terms (24 bits): a second product has the third, or,
 //               of four heads or fewer, rows 4 to 7 of the first;
-//   f16 cache   the same with f16 terms, of q scaled by a power of two per head to a
-//               largest value near 2^10, and of 2^12 p;
+//   f16 cache   tf32 products: k and v are exact in them, q and p two terms, each rounded
+//               (within 2^-23; three, 24 bits, of four heads or fewer).  Two f16 terms are
+//               faster (32 sequences to 4096: 64/8 heads of 128 56 us and 59, 128/8 77 and
+//               106, 8/8 of 64 35 and 42) but lose small values: the rest of a p of e^-25 has
+//               no f16 exponent (that p was off by 4 %).  Rests scaled up by 2^12 in rows of
+//               their own reach 2^-39 of the largest value and end there, and a sum with
+//               subnormal operands in it kept fewer bits (3e-6 of that p lost);
 //   f32 cache   two tf32 terms (22 bits) of q, p, k and v.
 // 16-bit operands alone would leave 2^-9.  The tensor core truncates when it
 // accumulates (measured: 1 + 0.92 ulp added 1000 times stays 1), so no accumulation is
@@ -30,7 +35,7 @@
 // A k that is not finite has to show: a slot takes no part by its mask, length or page, never by
 // its score.  A score of -inf would be that slot's weight 0, so every type has a product of an
 // infinite k that is NaN, whatever q: the zero rows beside the third terms (0 inf), or for f32 k
-// minus its high part.
+// minus its high part.  Where f16 has two terms, a score of -inf has its k looked at.
 //
 // p's accumulator fragment is the next product's operand without a move.
 //
@@ -62,7 +67,8 @@ constexpr int kMaxCtas = 456;  // three on each of 152 SMs
 // Q4 (16-bit types): groups of at most four heads, whose third terms take rows 4 to 7 of the one
 // product.
 template <int DT, int DP, int HT, bool Q4> struct Shape {
-    static constexpr bool k16 = DT != kF32;
+    static constexpr bool k16 = DT != kF32;            // elements of 16 bits
+    static constexpr bool kTf = DT != kBF16;           // tf32 products
     static constexpr int kEb = k16 ? 2 : 4;            // bytes of an element
     static constexpr int kRow = DP * kEb;              // bytes of a slot's row in the ring
     static constexpr int kEpc = 16 / kEb;              // elements of a 16-byte chunk
@@ -72,13 +78,13 @@ template <int DT, int DP, int HT, bool Q4> struct Shape {
     static constexpr int W = DP == 256 ? 3 : 4;        // warps
     static constexpr int kCtas = HT * DP == 256 ? 2 : 3;  // per SM
     static constexpr int kTile = 2 * KT * kRow;        // bytes: k, then v
-    static constexpr int kStages = DP == 64 ? 4 : HT * DP == 256 && DP == 128 ? 3 : 2;
+    static constexpr int kStages = DP == 64 ? 4 : HT * DP == 256 && DP == 128 && !kTf ? 3 : 2;
     static constexpr int BT = W * KT;                  // slots of a CTA's tile
     static constexpr int kHeads = HT * 8;              // query heads of a row
-    static constexpr bool kQReg = k16 && HT * DP <= 128;  // q's fragments in registers
-    static constexpr int kStep = k16 ? 16 : 8;         // dims of a product step
+    static constexpr bool kQReg = !kTf && HT * DP <= 128;  // q's fragments in registers
+    static constexpr int kStep = kTf ? 8 : 16;         // dims of a product step
     static constexpr int kSteps = DP / kStep;
-    static constexpr bool k3 = k16 && !Q4;             // a second product for the third term
+    static constexpr bool k3 = !kTf && !Q4;            // a second product for the third term
     static constexpr int kQWords = k3 ? 6 : 4;         // registers of a step's fragment
     static constexpr int kQ = W * kStages * kTile;     // q fragments, unless in registers
     static constexpr int kQBytes = kQReg ? 0 : HT * kSteps * 32 * kQWords * 4;
@@ -87,8 +93,7 @@ template <int DT, int DP, int HT, bool Q4> struct Shape {
     static constexpr int kL = kM + W * kHeads * 4;                 // [W][kHeads]
     static constexpr int kTop = kL + W * kHeads * 4;               // [kHeads]
     static constexpr int kSum = kTop + kHeads * 4;                 // [kHeads]
-    static constexpr int kScale = kSum + kHeads * 4;               // [kHeads], f16's powers of two
-    static constexpr int kSmem = kScale + kHeads * 4;
+    static constexpr int kSmem = kSum + kHeads * 4;
     static constexpr int kPart = kHeads * (DP + 2);    // floats of a part: m, l, o (16-byte rows)
     static_assert(kHeads * DP * 4 <= kTile, "a warp's o fits the tile just used");
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "CTAs per SM");
@@ -138,26 +143,23 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
 // The terms of a pair, packed: t[0] + t[1] + t[2] = (x, y).
-template <int DT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        if (DT == kBF16) {
-            t[i] = bf16x2(x, y);
-            x -= bf16_lo(t[i]);
-            y -= bf16_hi(t[i]);
-        } else {
-            t[i] = f16x2(x, y);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&t[i]));
-            x -= h.x;
-            y -= h.y;
-        }
+        t[i] = bf16x2(x, y);
+        x -= bf16_lo(t[i]);
+        y -= bf16_hi(t[i]);
     }
+}
+// x's column of a tf32 fragment, (t0, t1): its terms in rows g and g + 8, or with THIRD, in
+// the lanes of rows 4 to 7, what two terms leave and 0.
+template <bool THIRD>
+__device__ __forceinline__ void split_tf32(float x, bool third, uint32_t &t0, uint32_t &t1) {
+    t0 = tf32(x);
+    const float rest = x - __uint_as_float(t0);
+    t1 = tf32(rest);
+    if (THIRD && third) t0 = __float_as_uint(rest - __uint_as_float(t1)), t1 = 0u;
 }
 
 // ---------------------------------------------------------------- products --
@@ -171,22 +173,19 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
           "f"(c2), "f"(c3));
 }
-template <int DT>
-__device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
-                                       float c2, float c3) {
-    if (DT == kBF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-            "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
-              "f"(c3));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-            "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
-              "f"(c3));
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                         float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+          "f"(c3));
+}
+// A pair of f16 as tf32 operands.
+__device__ __forceinline__ uint2 widen(uint32_t x) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
 }
 // An f32 value as its high 11 bits and the rest, for two tf32 products.
 __device__ __forceinline__ uint32_t high11(uint32_t x) { return x & 0xFFFFE000u; }
@@ -446,14 +445,12 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
 
     // The row's query heads, scaled, as the first product's operand: rows g and g + 8 of a
     // fragment are the first two terms of head g.  In registers where they fit: every warp
-    // makes its own.  Else a 16-bit head tile is made by one warp, f32 ones by all.
-    // f16: `back` undoes the power of two that brings q near 2^10.
+    // makes its own.  Else a bf16 head tile is made by one warp, tf32 ones by all.
     uint32_t qr[S::kQReg ? HT * S::kSteps : 1][S::kQWords];
-    float back[HT];
     // Asked for first and turned into operands later, so that other loads go in between.
     constexpr int kRaw = S::kQReg ? HT * S::kSteps * 2
-                         : S::k16 ? S::kSteps * 2
-                                  : (HT * S::kSteps * 32 + kThreads - 1) / kThreads;
+                         : !S::kTf ? S::kSteps * 2
+                                   : (HT * S::kSteps * 32 + kThreads - 1) / kThreads;
     float2 raw[kRaw];
     auto fetch_q = [&](const Cursor &at) {
         const int h = at.row / head_tiles, ht0 = (at.row - h * head_tiles) * S::kHeads;
@@ -465,61 +462,43 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
         };
 #pragma unroll
         for (int i = 0; i < kRaw; ++i) {
-            if (S::k16) {
+            if (!S::kTf) {
                 const int ht = S::kQReg ? i / (2 * S::kSteps) : warp;
                 if (ht >= HT) break;
                 raw[i] = q2(ht * 8 + (Q4 ? g & 3 : g), i % (2 * S::kSteps) * 8 + 2 * c);
-            } else {  // tf32: a lane's dims are those of its 16-byte chunks of a key
+            } else {  // a lane's dims are those of its registers of a key
                 const int f = i * kThreads + threadIdx.x;
                 const int l = f & 31, ks = (f >> 5) % S::kSteps, ht = (f >> 5) / S::kSteps;
-                if (ht < HT)
-                    raw[i] = q2(ht * 8 + (l >> 2), 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1));
+                const int dim = S::k16 ? 8 * ks + 2 * (l & 3)
+                                       : 16 * (ks >> 1) + 4 * (l & 3) + 2 * (ks & 1);
+                if (ht < HT) raw[i] = q2(ht * 8 + (Q4 ? l >> 2 & 3 : l >> 2), dim);
             }
         }
     };
     auto make_q = [&]() {
-        if (!S::k16) {
+        if (S::kTf) {
 #pragma unroll
             for (int i = 0; i < kRaw; ++i) {
                 const int f = i * kThreads + threadIdx.x;
                 if (f >= HT * S::kSteps * 32) break;
-                const float x = raw[i].x * a.scale, y = raw[i].y * a.scale;
+                const bool third = f & 16;  // rows 4 to 7
                 uint4 t;
-                t.x = tf32(x);
-                t.y = tf32(x - __uint_as_float(t.x));
-                t.z = tf32(y);
-                t.w = tf32(y - __uint_as_float(t.z));
+                split_tf32<Q4>(raw[i].x * a.scale, third, t.x, t.y);
+                split_tf32<Q4>(raw[i].y * a.scale, third, t.z, t.w);
                 *reinterpret_cast<uint4 *>(smem + S::kQ + f * 16) = t;
             }
         }
 #pragma unroll
-        for (int u = 0; u < (S::kQReg ? HT : S::k16 ? 1 : 0); ++u) {
+        for (int u = 0; u < (S::kQReg ? HT : S::kTf ? 0 : 1); ++u) {
             const int ht = S::kQReg ? u : warp;
             if (ht >= HT) break;
             const float2 *r = raw + (S::kQReg ? u * S::kSteps * 2 : 0);
-            float up = 1.f;
-            if (DT == kF16) {
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < S::kSteps * 2; ++i)
-                    top = fmaxf(top, fmaxf(fabsf(r[i].x * a.scale), fabsf(r[i].y * a.scale)));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                int e = 0;
-                if (top > 0.f && top < INFINITY) e = max(-100, ilogbf(top));
-                up = exp2f((float)(10 - e));
-                const float down = exp2f((float)(e - 10));
-                if (S::kQReg)
-                    back[u] = down;
-                else if (c == 0)
-                    reinterpret_cast<float *>(smem + S::kScale)[ht * 8 + g] = down;
-            }
 #pragma unroll
             for (int ks = 0; ks < S::kSteps; ++ks) {
                 uint32_t t0[3], t1[3];
                 const float2 x = r[2 * ks], y = r[2 * ks + 1];
-                split2<DT>(x.x * a.scale * up, x.y * a.scale * up, t0);
-                split2<DT>(y.x * a.scale * up, y.y * a.scale * up, t1);
+                split2(x.x * a.scale, x.y * a.scale, t0);
+                split2(y.x * a.scale, y.y * a.scale, t1);
                 const int f = ht * S::kSteps + ks;
                 if (Q4 && g >= 4) t0[0] = t0[2], t1[0] = t1[2], t0[1] = t1[1] = 0u;
                 if (S::kQReg) {
@@ -536,14 +515,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             }
         }
     };
-    // After the barrier that follows make_q.
-    auto take_scales = [&]() {
-        if (DT == kF16 && !S::kQReg)
-#pragma unroll
-            for (int h = 0; h < HT; ++h)
-                back[h] = reinterpret_cast<const float *>(smem + S::kScale)[h * 8 + g];
-    };
-
     // The first tiles' page numbers and the queries are on their way together, ahead of
     // the tiles, whose loads would hold them up.
     Ask asked[kStages];
@@ -562,7 +533,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
     // in only when they are done: with both early, CTAs of a next call wait beside these and
     // 131072 slots back to back take 130 us in place of 93.
     if (!CL) pdl_launch();
-    take_scales();
 
     constexpr int OI = DP / 8;  // 16-bit: o[i] = dims 8 i + 2 c, + 1; f32: see its loop
     float o[HT][OI][2], m[HT], l[HT];
@@ -589,12 +559,26 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             const int key = (mat >> 1) * 8 + mrow;
             const uint32_t at = kb + key * S::kRow;
 #pragma unroll
-            for (int ks = 0; ks < S::kSteps; ++ks) {
+            for (int ks = 0; ks < DP / 16; ++ks) {
                 if (2 * ks >= live_chunks) break;
                 uint32_t kf[4];
                 ldmatrix4<false>(kf, at + (((2 * ks + (mat & 1)) ^ mrow) << 4));
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
+                for (int h = 0; h < (S::kTf ? HT : 0); ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {  // even and odd chunks' sums
+                        const uint4 v = lds128(smem_addr(smem) + S::kQ +
+                                               ((h * S::kSteps + 2 * ks + j) * 32 + lane) * 16);
+                        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 b = widen(kf[2 * n + j]);
+                            float(&x)[4] = sc[h][n][j];
+                            mma_tf32(x, q, b.x, b.y, x[0], x[1], x[2], x[3]);
+                        }
+                    }
+#pragma unroll
+                for (int h = 0; h < (S::kTf ? 0 : HT); ++h) {
                     uint32_t q[6];
                     const int f = h * S::kSteps + ks;
                     if (S::kQReg) {
@@ -612,11 +596,11 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float(&x)[4] = sc[h][n][0], (&y)[4] = sc[h][n][1];
-                        mma_16<DT>(x, q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1], x[0], x[1],
-                                   x[2], x[3]);
+                        mma_bf16(x, q[0], q[1], q[2], q[3], kf[2 * n], kf[2 * n + 1], x[0], x[1],
+                                 x[2], x[3]);
                         if (S::k3)
-                            mma_16<DT>(y, q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1], y[0], y[1],
-                                       y[2], y[3]);
+                            mma_bf16(y, q[4], 0u, q[5], 0u, kf[2 * n], kf[2 * n + 1], y[0], y[1],
+                                     y[2], y[3]);
                     }
                 }
             }
@@ -649,8 +633,20 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[h][0][j][i] += lo[h][j][i];
         }
-        uint32_t pt[HT][2][3];  // 16-bit: the terms of p at slots 2c, 2c + 1 (+ 8)
-        uint32_t pf[HT][4];     // f32: p's fragment
+        // Is there a k that is not finite in a slot of the tile (f16)?
+        auto endless = [&](int slot) {
+            bool any = false;
+            for (int ch = 0; ch < live_chunks; ++ch) {
+                const uint4 v = lds128(kb + slot * S::kRow + ((ch ^ swizzle_k<DT>(slot)) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    any |= (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
+            }
+            return any;
+        };
+        uint32_t pt[HT][2][3];   // bf16: the terms of p at slots 2c, 2c + 1 (+ 8)
+        uint32_t pf[HT][NT][4];  // tf32: p's fragments
         float corr[HT];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
@@ -661,9 +657,9 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                 const float(&v)[2][4] = sc[h][n];
                 float x0 = (v[0][0] + v[1][0]) + (v[0][2] + v[1][2]);
                 float x1 = (v[0][1] + v[1][1]) + (v[0][3] + v[1][3]);
-                if (DT == kF16) {
-                    x0 *= back[h];
-                    x1 *= back[h];
+                if (DT == kF16 && !Q4) {
+                    if (x0 == -INFINITY && endless(n * 8 + 2 * c)) x0 = NAN;
+                    if (x1 == -INFINITY && endless(n * 8 + 2 * c + 1)) x1 = NAN;
                 }
                 if (Q4) {  // heads 0 to 3 now also in the lanes of rows 4 to 7
                     x0 += __shfl_xor_sync(0xFFFFFFFFu, x0, 16);
@@ -698,20 +694,14 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float p0 = exp_diff(xs[n][0], top), p1 = exp_diff(xs[n][1], top);
-                if (DT == kF16) {
-                    p0 *= 4096.f;
-                    p1 *= 4096.f;
-                }
+                const float p0 = exp_diff(xs[n][0], top), p1 = exp_diff(xs[n][1], top);
                 sum += p0 + p1;
-                if (S::k16) {
-                    split2<DT>(p0, p1, pt[h][n]);
-                    if (Q4 && g >= 4) pt[h][n][0] = pt[h][n][2], pt[h][n][1] = 0u;
+                if (S::kTf) {
+                    split_tf32<Q4>(p0, g >= 4, pf[h][n][0], pf[h][n][1]);
+                    split_tf32<Q4>(p1, g >= 4, pf[h][n][2], pf[h][n][3]);
                 } else {
-                    pf[h][0] = tf32(p0);
-                    pf[h][1] = tf32(p0 - __uint_as_float(pf[h][0]));
-                    pf[h][2] = tf32(p1);
-                    pf[h][3] = tf32(p1 - __uint_as_float(pf[h][2]));
+                    split2(p0, p1, pt[h][n]);
+                    if (Q4 && g >= 4) pt[h][n][0] = pt[h][n][2], pt[h][n][1] = 0u;
                 }
             }
             l[h] = l[h] * corr[h] + sum;
@@ -732,15 +722,29 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                 for (int h = 0; h < HT; ++h) {
                     const uint32_t(&p0)[3] = pt[h][0], (&p1)[3] = pt[h][1];
                     float t[4][4];
+                    if (S::kTf) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        mma_16<DT>(t[u], p0[0], p0[1], p1[0], p1[1], vf[2 * u], vf[2 * u + 1], 0.f,
-                                   0.f, 0.f, 0.f);
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const uint2 b = widen(vf[2 * u + n]);
+                                if (n == 0)
+                                    mma_tf32(t[u], pf[h][n], b.x, b.y, 0.f, 0.f, 0.f, 0.f);
+                                else
+                                    mma_tf32(t[u], pf[h][n], b.x, b.y, t[u][0], t[u][1], t[u][2],
+                                             t[u][3]);
+                            }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mma_bf16(t[u], p0[0], p0[1], p1[0], p1[1], vf[2 * u], vf[2 * u + 1],
+                                     0.f, 0.f, 0.f, 0.f);
+                    }
                     if (S::k3)
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            mma_16<DT>(t[u], p0[2], 0u, p1[2], 0u, vf[2 * u], vf[2 * u + 1],
-                                       t[u][0], t[u][1], t[u][2], t[u][3]);
+                            mma_bf16(t[u], p0[2], 0u, p1[2], 0u, vf[2 * u], vf[2 * u + 1],
+                                     t[u][0], t[u][1], t[u][2], t[u][3]);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         float(&to)[2] = o[h][2 * i + u];
@@ -762,10 +766,10 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                     float t[4][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mma_tf32(t[e], pf[h], high11(w0[e]), high11(w1[e]), 0.f, 0.f, 0.f, 0.f);
+                        mma_tf32(t[e], pf[h][0], high11(w0[e]), high11(w1[e]), 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mma_tf32(t[e], pf[h], rest11(w0[e]), rest11(w1[e]), t[e][0], t[e][1],
+                        mma_tf32(t[e], pf[h][0], rest11(w0[e]), rest11(w1[e]), t[e][0], t[e][1],
                                  t[e][2], t[e][3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -795,10 +799,9 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             float sum = l[h];
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-            const float unit = DT == kF16 ? 1.f / 4096.f : 1.f;
             if (c == 0) {
                 s_m[warp * S::kHeads + h * 8 + g] = m[h];
-                s_l[warp * S::kHeads + h * 8 + g] = sum * unit;
+                s_l[warp * S::kHeads + h * 8 + g] = sum;
             }
             float *to = mo + (h * 8 + g) * DP;
             if (Q4) {
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
 #pragma unroll
                 for (int i = 0; i < OI; ++i)
                     *reinterpret_cast<float2 *>(to + 8 * i + 2 * c) =
-                        make_float2(o[h][i][0] * unit, o[h][i][1] * unit);
+                        make_float2(o[h][i][0], o[h][i][1]);
             } else {
 #pragma unroll
                 for (int i = 0; i < S::kChunks / 8; ++i)
@@ -922,7 +925,6 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                 make_q();
             }
             __syncthreads();
-            take_scales();
         }
         if (!CL || !last) {
             use.next(a, rows, S::BT);

@@ -1,8 +1,10 @@
 """wq_attn_paged where the operands' terms matter: values that are not finite, weights and
 query components far below their largest, values with every mantissa bit set, large groups.
 
-The bounds are the header's: a product within 2^-22 of exact, sums in f32, and for f16 caches a
-floor (below).  They are derived beside each test."""
+The bounds are the header's: a product within 2^-22 of exact, sums in f32.  They are derived
+beside each test."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -58,3 +60,90 @@ def test_a_value_that_is_not_finite(kind, bad, hq, d, lens):
             else:
                 assert not np.isfinite(mine[:, dim]).any() and np.isfinite(lse[1]).all()
                 assert np.isfinite(np.delete(mine, dim, 1)).all()
+
+
+def two_slots(kind, score, v, d=64, hq=2, extra=0):
+    """Slots with scores 0 and `score` (from the mask; k is 0) and values v [2]."""
+    c = Cache(np.random.default_rng(0), [2 + extra], 1, d, kind, 16)
+    k, vals = np.zeros((1, 2 + extra, d), np.float32), np.zeros((1, 2 + extra, d), np.float32)
+    vals[:, 0], vals[:, 1] = v[0], v[1]
+    fill(c, k, vals)
+    mask = np.full((1, 2 + extra), -np.inf, np.float32)
+    mask[0, :2] = 0.0, score
+    out, lse, _ = call(c, [2 + extra], hq, np.ones((1, hq, d), np.float32), 0.125, mask=mask)
+    return out[0].astype(np.float64), c.host()[1][c.pages[0, 0], 0, :2, 0]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("hq", [2, 5, 12])
+@pytest.mark.parametrize("v", [(1e-7, 60000.0), (-6.1e-5, 50000.0), (1.0, 1.0), (0.0, 60000.0)])
+def test_weights_far_below_the_largest(kind, hq, v):
+    """Scores are exact here, so what is left is exp and the sums, 2^-19 of sum p |v|."""
+    for score in (-3.0, -8.31, -12.5, -15.1, -19.4, -25.0, -30.2, -36.6, -50.3, -80.0):
+        out, host = two_slots(kind, score, v, hq=hq)
+        e = np.exp(np.float64(np.float32(score)))
+        want = (host[0] + e * host[1]) / (1 + e)
+        size = (abs(host[0]) + e * abs(host[1])) / (1 + e)
+        assert (np.abs(out - want) <= 2.0 ** -19 * size).all(), (score, out[0, 0], want)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("hq", [1, 7, 16])
+def test_query_components_far_below_the_largest(kind, hq):
+    """The largest component of each head meets a k of 0, a small one a k that is not: the score
+    is one product, and with one slot lse is the score.  A product within 2^-22, and two roundings
+    of 2^-24 where terms are added."""
+    g = np.random.default_rng(hq)
+    d, at = 64, 11
+    for power in range(0, 81, 4):
+        c = Cache(g, [1], 1, d, kind, 16)
+        k, q = np.zeros((1, 1, d), np.float32), np.zeros((1, hq, d), np.float32)
+        k[..., at] = 60000.0
+        q[..., 3] = 1 + g.random(hq)
+        q[..., at] = (1 + g.random(hq)) * 2.0 ** -power
+        fill(c, k, k)
+        _, lse, _ = call(c, [1], hq, q, 1.0)
+        kk = c.host()[0][c.pages[0, 0], 0, 0, at]
+        want = q[0, :, at].astype(np.float64) * kk
+        assert (np.abs(lse[0] - want) <= (2.0 ** -22 + 2.0 ** -23) * np.abs(want)).all(), power
+
+
+def test_spread_scores_and_values_of_every_size_f16():
+    """Scores from 0 to -40 under values from 1e-7 to 6e4, the largest where the weights are
+    least, whole rows and split ones.  The mask gives the scores, k is 0, so they are exact."""
+    g = np.random.default_rng(3)
+    d = 64
+    for size, hq in ((64, 3), (900, 8), (9000, 2), (9000, 16)):
+        c = Cache(g, [size], 1, d, "f16", 16)
+        mask = -np.sort(40 * g.random(size)).astype(np.float32)[None]
+        mask[0, 0] = 0.0
+        v = (np.exp(-mask[0].astype(np.float64)) * 1e-7).clip(1e-7, 6e4)[:, None]
+        v = v * g.choice([-1.0, 1.0], (size, d))
+        order = g.permutation(size)
+        mask, v = mask[:, order], v[order]
+        fill(c, np.zeros((1, size, d)), v[None])
+        out, lse, _ = call(c, [size], hq, np.ones((1, hq, d), np.float32), 0.125, mask=mask)
+        vh = np.concatenate(list(c.host()[1][c.pages[0], 0]))[:size]
+        p = np.exp(mask[0].astype(np.float64))
+        p /= p.sum()
+        assert (np.abs(out[0] - p @ vh) <= 2.0 ** -19 * (p @ np.abs(vh))).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hq", [3, 8, 16])
+def test_small_values_beside_large_ones_of_no_weight(kind, hq):
+    """In one tile: a v of 6e4 at a weight of e^-27, below f16's range, v of 6e-5 at weights near
+    2^-10, v of 0 at the largest: sums may not be aligned to what is not there."""
+    g = np.random.default_rng(hq)
+    d = 64
+    c = Cache(g, [16], 1, d, kind, 16)
+    mask = (-10 * math.log(2) + 0.2 * g.standard_normal(16)).astype(np.float32)[None]
+    mask[0, 0], mask[0, 9] = 0.0, -27.0
+    v = 6e-5 * (1 + g.random((16, d)))
+    v[0], v[9] = 0.0, 60000.0
+    fill(c, np.zeros((1, 16, d)), v[None])
+    out, _, _ = call(c, [16], hq, np.ones((1, hq, d), np.float32), 0.125, mask=mask)
+    p = np.exp(mask[0].astype(np.float64))
+    p /= p.sum()
+    vh = c.host()[1][c.pages[0, 0], 0]
+    assert (np.abs(out[0] - p @ vh) <= 2.0 ** -19 * (p @ np.abs(vh))).all()
