@@ -26,7 +26,11 @@
 //               no f16 exponent (that p was off by 4 %).  Rests scaled up by 2^12 in rows of
 //               their own reach 2^-39 of the largest value and end there, and a sum with
 //               subnormal operands in it kept fewer bits (3e-6 of that p lost);
-//   f32 cache   two tf32 terms (22 bits) of q, p, k and v.
+//   f32 cache   tf32 products: q and p two terms, each rounded (within 2^-23), k and v
+//               three that cut them at 11 bits (exact), in three products.  Two are faster
+//               (32 sequences to 4096, 32/8 heads of 128 102 us and 118) but lose up to
+//               3 2^-23 of k and v, always toward zero; rounded ones would take the largest
+//               finite values to infinity.
 // 16-bit operands alone would leave 2^-9.  The tensor core truncates when it
 // accumulates (measured: 1 + 0.92 ulp added 1000 times stays 1), so no accumulation is
 // longer than head_dim / 16 steps of q.k, and every tile's p.v is added to o by an f32
@@ -187,10 +191,17 @@ __device__ __forceinline__ uint2 widen(uint32_t x) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x));
     return make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
 }
-// An f32 value as its high 11 bits and the rest, for two tf32 products.
-__device__ __forceinline__ uint32_t high11(uint32_t x) { return x & 0xFFFFE000u; }
-__device__ __forceinline__ uint32_t rest11(uint32_t x) {
-    return __float_as_uint(__uint_as_float(x) - __uint_as_float(high11(x)));
+// An f32 value as three of 11, 11 and 2 bits.
+struct Cut {
+    uint32_t t[3];
+};
+__device__ __forceinline__ Cut cut3(uint32_t x) {
+    Cut c;
+    c.t[0] = x & 0xFFFFE000u;
+    const float rest = __uint_as_float(x) - __uint_as_float(c.t[0]);
+    c.t[1] = __float_as_uint(rest) & 0xFFFFE000u;
+    c.t[2] = __float_as_uint(rest - __uint_as_float(c.t[1]));
+    return c;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -610,7 +621,7 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
             for (int i = 0; i < S::kChunks / 4; ++i) {
                 if (4 * i >= live_chunks) break;
                 const uint4 v = lds128(kb + g * S::kRow + (((4 * i + c) ^ swizzle_k<DT>(g)) << 4));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const Cut k[4] = {cut3(v.x), cut3(v.y), cut3(v.z), cut3(v.w)};
 #pragma unroll
                 for (int h = 0; h < HT; ++h)
 #pragma unroll
@@ -620,10 +631,10 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                         const uint32_t q[4] = {f.x, f.y, f.z, f.w};
                         // Four sums: high and low parts, even and odd steps.
                         float(&x)[4] = sc[h][0][j], (&y)[4] = lo[h][j];
-                        mma_tf32(x, q, high11(w[2 * j]), high11(w[2 * j + 1]), x[0], x[1], x[2],
-                                 x[3]);
-                        mma_tf32(y, q, rest11(w[2 * j]), rest11(w[2 * j + 1]), y[0], y[1], y[2],
-                                 y[3]);
+                        const Cut &b0 = k[2 * j], &b1 = k[2 * j + 1];
+                        mma_tf32(x, q, b0.t[0], b1.t[0], x[0], x[1], x[2], x[3]);
+                        mma_tf32(y, q, b0.t[2], b1.t[2], y[0], y[1], y[2], y[3]);
+                        mma_tf32(y, q, b0.t[1], b1.t[1], y[0], y[1], y[2], y[3]);
                     }
             }
 #pragma unroll
@@ -760,17 +771,17 @@ __global__ void __launch_bounds__(Shape<DT, DP, HT, Q4>::W * 32, Shape<DT, DP, H
                 if (8 * i >= live_chunks) break;
                 const uint32_t at = vb + 2 * c * S::kRow + (((g + 8 * i) ^ (2 * c)) << 4);
                 const uint4 v0 = lds128(at), v1 = lds128(at + S::kRow);
-                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                const Cut c0[4] = {cut3(v0.x), cut3(v0.y), cut3(v0.z), cut3(v0.w)};
+                const Cut c1[4] = {cut3(v1.x), cut3(v1.y), cut3(v1.z), cut3(v1.w)};
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
-                    float t[4][4];
+                    float t[4][4] = {};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_tf32(t[e], pf[h][0], high11(w0[e]), high11(w1[e]), 0.f, 0.f, 0.f, 0.f);
+                    for (int part = 2; part >= 0; --part)  // the small ones first
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_tf32(t[e], pf[h][0], rest11(w0[e]), rest11(w1[e]), t[e][0], t[e][1],
-                                 t[e][2], t[e][3]);
+                        for (int e = 0; e < 4; ++e)
+                            mma_tf32(t[e], pf[h][0], c0[e].t[part], c1[e].t[part], t[e][0],
+                                     t[e][1], t[e][2], t[e][3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float(&to)[2] = o[h][i * 4 + e];

@@ -334,7 +334,8 @@ WQ_API wq_status wq_embed(int n_ids, int rows, int k, int wtype, const void *W,
  * and its output projection: rotate q and k by their positions, write k and v into
  * the pages of a cache, attend with one new token per sequence, and keep the cache
  * within a budget.  Activations are f32 as everywhere in this library; the cache
- * holds bf16, f16 or f32.  All products and sums are f32 or better.
+ * holds bf16, f16 or f32.  Sums are f32 or better, and so are products but for the
+ * attention's, which are within 2^-22 of exact.
  */
 
 /* Pair layout and direction of a rotation. */

@@ -147,3 +147,29 @@ def test_small_values_beside_large_ones_of_no_weight(kind, hq):
     p /= p.sum()
     vh = c.host()[1][c.pages[0, 0], 0]
     assert (np.abs(out[0] - p @ vh) <= 2.0 ** -19 * (p @ np.abs(vh))).all()
+
+
+# 24 significant bits whose low 13 are the most that two terms of 11 bits can lose.
+FULL = 1 + 2.0 ** -11 + 2.0 ** -22 + 2.0 ** -23
+
+
+def test_keys_and_values_of_24_bits_f32():
+    """One slot: lse is the score, one product of q and k (scale 1, so q is not rounded before),
+    within 2^-22 and two roundings of 2^-24 where terms are added; out is v times a weight of
+    exactly 1, within 2^-22."""
+    g = np.random.default_rng(4)
+    d, hq = 64, 16
+    for at in (0, 1, 2, 3, 17, 63):
+        for size in (FULL, -FULL, 1000 * FULL, 2.0 ** -30 * FULL, 2 - 2.0 ** -23):
+            c = Cache(g, [1], 2, d, "f32", 16)
+            k = np.zeros((2, 1, d), np.float32)
+            v = (size * (1 + 2.0 ** -23 * g.integers(0, 64, (2, 1, d)))).astype(np.float32)
+            k[..., at] = size
+            q = (1 + 2.0 ** -23 * g.integers(0, 1 << 23, (1, hq, d))).astype(np.float32)
+            q[0, ::2, at] = (1 + 2.0 ** -23 * g.integers(0, 1 << 14, hq // 2)).astype(np.float32)
+            fill(c, k, v)
+            out, lse, _ = call(c, [1], hq, q, 1.0)
+            want = q[0, :, at].astype(np.float64) * np.float64(np.float32(size))
+            assert (np.abs(lse[0] - want) <= (2.0 ** -22 + 2.0 ** -23) * np.abs(want)).all(), (at, size)
+            v = np.repeat(v[:, 0], hq // 2, 0).astype(np.float64)
+            assert (np.abs(out[0] - v) <= 2.0 ** -22 * np.abs(v)).all(), size
