@@ -1066,6 +1066,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // SLOTS: of a thread; sixteen scores of them are in flight (one after another of a slot's heads,
 // four at a time, took 47 us for a group of 32 over 20000 slots, this 40).
 constexpr int kJoinWarps = 8, kAhead = 4, kFewParts = 16;
+constexpr int kLse = 1024;  // heads whose lse a block holds at a time, for the weight sums
 constexpr int piece_of(int slots) { return slots * kJoinWarps * 32; }
 template <bool MANY, int SLOTS>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4)
@@ -1074,7 +1075,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     __shared__ float s_f[kMaxCtas];
     __shared__ float4 s_o[kJoinWarps][64];
     __shared__ float s_red[2], s_top[MANY ? kJoinWarps : 1][16], s_sum[MANY ? kJoinWarps : 1][16];
-    extern __shared__ float s_lse[];  // [group], for the weight sums
+    __shared__ float s_lse[kLse];
     pdl_wait();
     const int part_floats = heads * (dp + 2);
     const Room room =
@@ -1208,65 +1209,69 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     // MANY: a lane joins a head of every (8 * 32 / heads)-th part: their m and l are short runs
     // of neighbours, of which a warp to a head reads a sector for each value (120000 slots, a
     // row of 8 heads in 456 parts: 27 us, 55 by warps; 57 parts: 58 and 57; 2 parts 16 and 14).
-    for (int ht = 0; ht < head_tiles; ++ht) {
-        const int4 row = room.rows[(long long)id * head_tiles + ht];
-        const int first = row.x, n = row.y, skip = row.z;
-        const int in_tile = min(heads, a.group - ht * heads);
-        float *lse = s_lse + ht * heads;
-        auto part = [&](int k) {
-            return room.parts + (2ll * (first + k) + (k == 0 ? skip : 0)) * part_floats;
-        };
-        if (!MANY || n <= 1) {
-            for (int head = warp; head < in_tile; head += kJoinWarps) {
-                const float whole = room.lse[q0 + ht * heads + head];  // unused if split
-                float top, sum;
-                if (n > 1) join_head(n, head, heads, part, (float *)nullptr, top, sum);
-                if (lane == 0) lse[head] = n > 1 ? lse_of(top, sum) : whole;
-            }
-            continue;
-        }
-        const int per = 32 / heads, head = lane & (heads - 1);
-        float top = -INFINITY, sum = 0.f;
-        auto join = [&](float m, float l) {
-            const float t = fmaxf(top, m);
-            sum = sum * exp_diff(top, t) + l * exp_diff(m, t);
-            top = t;
-        };
-        for (int k0 = warp * per + lane / heads; k0 < n; k0 += kAhead * kJoinWarps * per) {
-            float m[kAhead], l[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int k = k0 + u * kJoinWarps * per;
-                m[u] = k < n ? part(k)[head] : -INFINITY;
-                l[u] = k < n ? part(k)[heads + head] : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) join(m[u], l[u]);
-        }
-        for (int o = heads; o < 32; o <<= 1) {
-            const float m = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-            const float l = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            join(m, l);
-        }
-        __syncthreads();  // the tile before has been read
-        if (lane < heads) s_top[warp][head] = top, s_sum[warp][head] = sum;
-        __syncthreads();
-        if (warp == 0 && lane < in_tile) {
-            for (int w = 1; w < kJoinWarps; ++w) join(s_top[w][head], s_sum[w][head]);
-            lse[head] = lse_of(top, sum);
-        }
-    }
-    __syncthreads();
     float sum[SLOTS] = {};
-    for (int i0 = 0; i0 < a.group; i0 += kHeadsAhead) {
+    for (int g0 = 0; g0 < a.group; g0 += kLse) {
+        const int g1 = min(a.group, g0 + kLse);
+        if (g0 > 0) __syncthreads();  // the heads before have been read
+        for (int ht = g0 / heads; ht * heads < g1; ++ht) {
+            const int4 row = room.rows[(long long)id * head_tiles + ht];
+            const int first = row.x, n = row.y, skip = row.z;
+            const int in_tile = min(heads, a.group - ht * heads);
+            float *lse = s_lse + ht * heads - g0;
+            auto part = [&](int k) {
+                return room.parts + (2ll * (first + k) + (k == 0 ? skip : 0)) * part_floats;
+            };
+            if (!MANY || n <= 1) {
+                for (int head = warp; head < in_tile; head += kJoinWarps) {
+                    const float whole = room.lse[q0 + ht * heads + head];  // unused if split
+                    float top, sum;
+                    if (n > 1) join_head(n, head, heads, part, (float *)nullptr, top, sum);
+                    if (lane == 0) lse[head] = n > 1 ? lse_of(top, sum) : whole;
+                }
+                continue;
+            }
+            const int per = 32 / heads, head = lane & (heads - 1);
+            float top = -INFINITY, sum = 0.f;
+            auto join = [&](float m, float l) {
+                const float t = fmaxf(top, m);
+                sum = sum * exp_diff(top, t) + l * exp_diff(m, t);
+                top = t;
+            };
+            for (int k0 = warp * per + lane / heads; k0 < n; k0 += kAhead * kJoinWarps * per) {
+                float m[kAhead], l[kAhead];
 #pragma unroll
-        for (int i = 0; i < kHeadsAhead; ++i) {
-            const float e = i0 + i < a.group ? s_lse[i0 + i] : -INFINITY;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int k = k0 + u * kJoinWarps * per;
+                    m[u] = k < n ? part(k)[head] : -INFINITY;
+                    l[u] = k < n ? part(k)[heads + head] : 0.f;
+                }
 #pragma unroll
-            for (int u = 0; u < SLOTS; ++u)
-                if (e != -INFINITY) sum[u] += exp_diff(ahead[u][i], e);
+                for (int u = 0; u < kAhead; ++u) join(m[u], l[u]);
+            }
+            for (int o = heads; o < 32; o <<= 1) {
+                const float m = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+                const float l = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                join(m, l);
+            }
+            __syncthreads();  // the tile before has been read
+            if (lane < heads) s_top[warp][head] = top, s_sum[warp][head] = sum;
+            __syncthreads();
+            if (warp == 0 && lane < in_tile) {
+                for (int w = 1; w < kJoinWarps; ++w) join(s_top[w][head], s_sum[w][head]);
+                lse[head] = lse_of(top, sum);
+            }
         }
-        if (i0 + kHeadsAhead < a.group) ask(i0 + kHeadsAhead);
+        __syncthreads();
+        for (int i0 = g0; i0 < g1; i0 += kHeadsAhead) {
+#pragma unroll
+            for (int i = 0; i < kHeadsAhead; ++i) {
+                const float e = i0 + i < g1 ? s_lse[i0 + i - g0] : -INFINITY;
+#pragma unroll
+                for (int u = 0; u < SLOTS; ++u)
+                    if (e != -INFINITY) sum[u] += exp_diff(ahead[u][i], e);
+            }
+            if (i0 + kHeadsAhead < a.group) ask(i0 + kHeadsAhead);
+        }
     }
 #pragma unroll
     for (int u = 0; u < SLOTS; ++u) {
@@ -1331,9 +1336,6 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     static std::atomic<unsigned long long> done{0};
     cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, false>, S::kSmem, dev, done);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_kernel<DT, DP, HT, Q4, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
-                     a, kv, head_tiles);
-    if (err != cudaSuccess) return err;
     const int row_heads = min(a.group, S::kHeads);
     const int blocks_per_row = rows * row_heads <= 2 * dev.sm_count ? row_heads : 1;
     const int joins = (int)(rows <= slots ? rows : slots) * blocks_per_row;
@@ -1342,13 +1344,15 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
         a.acc_out ? (int)((a.n_slots + (long long)piece_of(slots_per) - 1) / piece_of(slots_per)) : 0;
     const long long blocks = joins + (long long)a.n_seq * kv.n_heads * pieces;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    err = launch_pdl(attn_kernel<DT, DP, HT, Q4, false>, dim3(slots), dim3(S::W * 32), S::kSmem, stream,
+                     a, kv, head_tiles);
+    if (err != cudaSuccess) return err;
     const bool many = rows * kJoinAtOnce < slots;
     return launch_pdl(slots_per == 1 ? attn_join_kernel<false, 1>
                       : many         ? attn_join_kernel<true, 4>
                                      : attn_join_kernel<false, 4>,
-                      dim3((unsigned)blocks), dim3(kJoinWarps * 32),
-                      a.acc_out ? a.group * 4 : 0, stream, a, kv.n_heads, kv.head_dim, head_tiles,
-                      S::kHeads, DP, slots, joins, blocks_per_row, pieces);
+                      dim3((unsigned)blocks), dim3(kJoinWarps * 32), 0, stream, a, kv.n_heads,
+                      kv.head_dim, head_tiles, S::kHeads, DP, slots, joins, blocks_per_row, pieces);
 }
 
 template <int DT>

@@ -173,3 +173,13 @@ def test_keys_and_values_of_24_bits_f32():
             assert (np.abs(lse[0] - want) <= (2.0 ** -22 + 2.0 ** -23) * np.abs(want)).all(), (at, size)
             v = np.repeat(v[:, 0], hq // 2, 0).astype(np.float64)
             assert (np.abs(out[0] - v) <= 2.0 ** -22 * np.abs(v)).all(), size
+
+
+@pytest.mark.parametrize("n,length,hq,hkv", [(1, 700, 12000, 1), (1, 3000, 9600, 1),
+                                             (2, 40, 20100, 2)])
+def test_weights_of_a_group_of_thousands(n, length, hq, hkv):
+    g = np.random.default_rng(hq)
+    lens = [length - 3 * i for i in range(n)]
+    c = Cache(g, lens, hkv, 8, "bf16", 16)
+    acc_in = np.abs(g.standard_normal((n, hkv, c.max_pages * 16))).astype(np.float32)
+    check(c, lens, hq, queries(g, n, hq, 8), 0.35, acc_in=acc_in, with_acc=True)
