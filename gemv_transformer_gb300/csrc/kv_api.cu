@@ -98,7 +98,8 @@ wq_status wq_rope_table(int rows, int rot, double base, const wq_rope_scaling *s
             return WQ_ERR_INVALID_ARG;
     }
     if (sc.magnitude == 0.0)
-        sc.magnitude = sc.kind == WQ_ROPE_YARN ? 0.1 * std::log(sc.factor) + 1.0 : 1.0;
+        sc.magnitude =
+            sc.kind == WQ_ROPE_YARN && sc.factor > 1.0 ? 0.1 * std::log(sc.factor) + 1.0 : 1.0;
     DeviceInfo dev;
     if (!device_info(dev)) return WQ_ERR_CUDA;
     return cuda_status(launch_rope_table(rows, rot, base, sc, table, dev, (cudaStream_t)stream));

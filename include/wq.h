@@ -364,7 +364,8 @@ typedef struct {
     int32_t original;  /* YARN, BANDS: > 0 */
     double factor;     /* > 0 (all but PLAIN) */
     double low, high;  /* YARN, BANDS: 0 < low < high */
-    double magnitude;  /* multiplies cos and sin; 0: 1, or 0.1 ln(factor) + 1 with YARN */
+    double magnitude;  /* multiplies cos and sin; 0: 1, or with YARN 0.1 ln(factor) + 1 where
+                          factor > 1 */
 } wq_rope_scaling;
 
 /* table[p][i] = (m cos(p f_i), m sin(p f_i)), f32 [rows][rot/2][2], 16-byte aligned, for

@@ -38,7 +38,7 @@ def frequencies(rot, base, kind=PLAIN, factor=1.0, low=1.0, high=32.0, original=
 def table(rows, rot, base, magnitude=None, kind=PLAIN, factor=1.0, **scaling):
     """[rows][rot/2][2] of m cos, m sin."""
     if magnitude is None:
-        magnitude = 0.1 * math.log(factor) + 1.0 if kind == YARN else 1.0
+        magnitude = 0.1 * math.log(factor) + 1.0 if kind == YARN and factor > 1 else 1.0
     a = np.arange(rows, dtype=np.float64)[:, None] * frequencies(rot, base, kind, factor, **scaling)
     return magnitude * np.stack([np.cos(a), np.sin(a)], -1)
 
