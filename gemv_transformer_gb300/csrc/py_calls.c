@@ -29,8 +29,10 @@ static wq_status (*f_evict)(const wq_kv_cache *, int, const int32_t *, int, cons
 static PyObject *current_stream; /* () -> int */
 static PyObject *s_data_ptr, *s_cuda_stream;
 
-/* Each converter stores one argument; on failure it sets an exception and counts. */
+/* Each converter returns one argument; on failure it sets an exception and counts.  After a
+ * failure the others return at once: no Python may run with an exception set. */
 static long long as_i64(PyObject *o, int *bad) {
+    if (*bad) return 0;
     if (PyLong_Check(o)) {
         const long long v = PyLong_AsLongLong(o);
         if (v == -1 && PyErr_Occurred()) ++*bad;
@@ -49,14 +51,15 @@ static long long as_i64(PyObject *o, int *bad) {
 
 static int as_int(PyObject *o, int *bad) {
     const long long v = as_i64(o, bad);
-    if (v < INT_MIN || v > (long long)UINT_MAX) {
-        if (!*bad) PyErr_SetString(PyExc_OverflowError, "argument does not fit a C int");
+    if (!*bad && (v < INT_MIN || v > (long long)UINT_MAX)) {
+        PyErr_SetString(PyExc_OverflowError, "argument does not fit a C int");
         ++*bad;
     }
     return (int)v;
 }
 
 static float as_float(PyObject *o, int *bad) {
+    if (*bad) return 0.f;
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) ++*bad;
     return (float)v;
@@ -64,7 +67,7 @@ static float as_float(PyObject *o, int *bad) {
 
 /* None, an address, or an object with data_ptr() (a tensor). */
 static void *as_ptr(PyObject *o, int *bad) {
-    if (o == Py_None) return NULL;
+    if (*bad || o == Py_None) return NULL;
     if (PyLong_Check(o)) {
         void *p = PyLong_AsVoidPtr(o);
         if (!p && PyErr_Occurred()) ++*bad;
@@ -83,6 +86,7 @@ static void *as_ptr(PyObject *o, int *bad) {
 
 /* None (torch's current stream), a cudaStream_t as an int, or an object with cuda_stream. */
 static wq_stream_t as_stream(PyObject *o, int *bad) {
+    if (*bad) return NULL;
     if (PyLong_Check(o)) return (wq_stream_t)as_ptr(o, bad);
     PyObject *r = o == Py_None ? PyObject_CallNoArgs(current_stream)
                                : PyObject_GetAttr(o, s_cuda_stream);
@@ -97,7 +101,7 @@ static wq_stream_t as_stream(PyObject *o, int *bad) {
 
 /* None or a KvCache (its bytes are copied, so nothing is held). */
 static const wq_kv_cache *as_cache(PyObject *o, wq_kv_cache *room, int *bad) {
-    if (o == Py_None) return NULL;
+    if (*bad || o == Py_None) return NULL;
     Py_buffer view;
     if (PyObject_GetBuffer(o, &view, PyBUF_SIMPLE) != 0) {
         ++*bad;
