@@ -163,7 +163,7 @@ def _load_calls():
             spec.loader.exec_module(mod)
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                        for f in ("wq_rope", "wq_kv_append", "wq_attn_paged", "wq_kv_evict")),
-                     _current_stream)
+                     _current_stream, KvCache)
             _calls = mod
         return _calls
 

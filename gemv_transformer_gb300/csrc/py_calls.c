@@ -27,6 +27,7 @@ static wq_status (*f_evict)(const wq_kv_cache *, int, const int32_t *, int, cons
                             const int32_t *, int, int, int, const float *, const int32_t *,
                             float *, int32_t *, int64_t, int32_t *, void *, size_t, wq_stream_t);
 static PyObject *current_stream; /* () -> int */
+static PyObject *cache_type;     /* KvCache */
 static PyObject *s_data_ptr, *s_cuda_stream;
 
 /* Each converter returns one argument; on failure it sets an exception and counts.  After a
@@ -103,6 +104,11 @@ static wq_stream_t as_stream(PyObject *o, int *bad) {
 static const wq_kv_cache *as_cache(PyObject *o, wq_kv_cache *room, int *bad) {
     if (*bad || o == Py_None) return NULL;
     Py_buffer view;
+    if (!PyObject_TypeCheck(o, (PyTypeObject *)cache_type)) {
+        PyErr_Format(PyExc_TypeError, "cache: a KvCache is wanted, got %s", Py_TYPE(o)->tp_name);
+        ++*bad;
+        return NULL;
+    }
     if (PyObject_GetBuffer(o, &view, PyBUF_SIMPLE) != 0) {
         ++*bad;
         return NULL;
@@ -110,7 +116,7 @@ static const wq_kv_cache *as_cache(PyObject *o, wq_kv_cache *room, int *bad) {
     if (view.len == (Py_ssize_t)sizeof(*room)) {
         *room = *(const wq_kv_cache *)view.buf;
     } else {
-        PyErr_SetString(PyExc_TypeError, "cache: a KvCache is wanted");
+        PyErr_SetString(PyExc_TypeError, "cache: not the size of a wq_kv_cache");
         ++*bad;
     }
     PyBuffer_Release(&view);
@@ -202,12 +208,16 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                  acc_out, pos_out, acc_stride, lens_out, room, bytes, s));
 }
 
-/* bind(rope, append, attn, evict, current_stream): the entry points' addresses. */
+/* bind(rope, append, attn, evict, current_stream, KvCache): the first four are addresses. */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int bad = 0;
-    if (!count_is(n, 5)) return NULL;
+    if (!count_is(n, 6)) return NULL;
     void *f[4];
     for (int i = 0; i < 4; ++i) f[i] = P(i);
+    if (!bad && !PyType_Check(a[5])) {
+        PyErr_SetString(PyExc_TypeError, "KvCache: a type is wanted");
+        ++bad;
+    }
     if (bad) return NULL;
     f_rope = (__typeof__(f_rope))f[0];
     f_append = (__typeof__(f_append))f[1];
@@ -215,6 +225,8 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     f_evict = (__typeof__(f_evict))f[3];
     Py_INCREF(a[4]);
     Py_XSETREF(current_stream, a[4]);
+    Py_INCREF(a[5]);
+    Py_XSETREF(cache_type, a[5]);
     Py_RETURN_NONE;
 }
 

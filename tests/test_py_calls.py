@@ -1,5 +1,7 @@
 """Arguments of the calls that the C module marshals: wrong types and sizes raise what ctypes
 would, whatever the other arguments are (CPU only; no call gets as far as a launch)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -108,3 +110,27 @@ def test_nothing_is_asked_after_an_error():
     with pytest.raises(TypeError):
         wq.wq_rope(*a)
     assert all(x.asked == 0 for x in a if isinstance(x, Tensor))
+
+
+class LikeCache(ctypes.Structure):
+    """The bytes of a KvCache under another name."""
+    _fields_ = wq.KvCache._fields_
+
+
+class SubCache(wq.KvCache):
+    pass
+
+
+@pytest.mark.parametrize("name", NAMES[1:])
+def test_only_a_cache_is_a_cache(name):
+    for wrong in (bytes(64), bytearray(64), np.zeros(8), (ctypes.c_int64 * 8)(), LikeCache(),
+                  bytearray(63), "x", 5, wq.RopeScaling()):
+        a = good(name)
+        a[0] = wrong
+        with pytest.raises(TypeError):
+            getattr(wq, name)(*a)
+    a = good(name)
+    a[0] = SubCache.from_buffer_copy(cache())
+    assert getattr(wq, name)(*a) == wq.WQ_ERR_INVALID_ARG
+    a[0] = None
+    assert getattr(wq, name)(*a) == wq.WQ_ERR_INVALID_ARG
