@@ -2,8 +2,8 @@
 
 Argument marshalling only: every function forwards to the C entry point of the
 same name in ``_build/libwq.so`` (declared in ``include/wq.h``), through ctypes or, for
-the calls of a decode step, the C module ``_build/_wq_calls.so``; all the work runs
-in the library's CUDA kernels.  There is no CPU fallback: if the library is not
+the calls of a decode step, the C module ``_build/_wq_calls.so`` where it was built; all the
+work runs in the library's CUDA kernels.  There is no CPU fallback: if the library is not
 built, or no CUDA device is present, the calls raise.
 
 Tensor arguments may be ``torch.Tensor`` (device memory) or raw integer device
@@ -14,8 +14,10 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 import threading
+import types
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libwq.so")
@@ -122,6 +124,18 @@ def _open(path: str):
     cp = ctypes.POINTER(KvCache)
     lib.wq_rope_table.argtypes = [ci, ci, ctypes.c_double, ctypes.POINTER(RopeScaling), vp, vp]
     lib.wq_rope_table.restype = ci
+    i64, cf = ctypes.c_int64, ctypes.c_float
+    lib.wq_rope.argtypes = [ci, ci, ci, ci, cu, vp, i64, vp, vp, ci, vp, i64, vp]
+    lib.wq_rope.restype = ci
+    lib.wq_kv_append.argtypes = [cp, ci, ci, ci, cu, vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, vp,
+                                 vp, vp, ci, vp, i64, vp, vp, i64, vp]
+    lib.wq_kv_append.restype = ci
+    lib.wq_attn_paged.argtypes = [cp, ci, ci, cf, ci, vp, i64, vp, ci, vp, vp, i64, vp, i64, vp, vp,
+                                  vp, i64, vp, sz, vp]
+    lib.wq_attn_paged.restype = ci
+    lib.wq_kv_evict.argtypes = [cp, ci, vp, ci, vp, vp, ci, ci, ci, vp, vp, vp, vp, i64, vp, vp, sz,
+                                vp]
+    lib.wq_kv_evict.restype = ci
     lib.wq_attn_paged_workspace_bytes.argtypes = [cp, ci, ci, ci, ci]
     lib.wq_attn_paged_workspace_bytes.restype = sz
     lib.wq_kv_evict_workspace_bytes.argtypes = [cp, ci, ci, ci]
@@ -149,20 +163,36 @@ def load():
 _calls = None
 
 
+_CALLS = ("wq_rope", "wq_kv_append", "wq_attn_paged", "wq_kv_evict")
+
+
+def _through_ctypes(f):
+    kinds = f.argtypes[:-1]
+
+    def call(*args):
+        if len(args) != len(f.argtypes):
+            raise TypeError(f"{len(f.argtypes)} arguments are wanted, got {len(args)}")
+        return f(*(_p(x) if t is ctypes.c_void_p else
+                   operator.index(x) if t in (ctypes.c_int, ctypes.c_uint, ctypes.c_int64,
+                                              ctypes.c_size_t) else x
+                   for x, t in zip(args, kinds)), _s(args[-1]))
+    return call
+
+
 def _load_calls():
-    """The marshalling module of the decode-step calls, bound to the process-wide libwq."""
+    """The marshalling module of the decode-step calls, bound to the process-wide libwq; the
+    same calls through ctypes (some microseconds slower) where it was not built."""
     global _calls
     lib = load()
     with _lock:
+        if _calls is None and not os.path.exists(CALLS_PATH):
+            _calls = types.SimpleNamespace(**{f: _through_ctypes(getattr(lib, f)) for f in _CALLS})
         if _calls is None:
-            if not os.path.exists(CALLS_PATH):
-                raise RuntimeError(f"the binding is not built ({CALLS_PATH} missing): run "
-                                   "gemv_transformer_gb300.build.build()")
             spec = importlib.util.spec_from_file_location("_wq_calls", CALLS_PATH)
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                       for f in ("wq_rope", "wq_kv_append", "wq_attn_paged", "wq_kv_evict")),
+                       for f in _CALLS),
                      _current_stream, KvCache)
             _calls = mod
         return _calls

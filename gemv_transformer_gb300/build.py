@@ -2,7 +2,8 @@
 
 Each ``csrc/*.cu`` is compiled in parallel to an object, then linked into
 ``gemv_transformer_gb300/_build/libwq.so`` with the static CUDA runtime.  ``py_calls.c``, the
-binding's marshalling of the decode-step calls, is compiled with gcc beside it.
+binding's marshalling of the decode-step calls, is compiled with gcc beside it where gcc and
+Python's headers are there; the library does not need it, and the binding does without.
 Run ``python -m gemv_transformer_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -41,23 +42,56 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
 def _deps():
-    return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+        glob.glob(os.path.join(CSRC, "*.h")) + _headers()
+
+
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and \
+        all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps + [__file__])
+
+
+def _can_build_calls() -> bool:
+    return shutil.which("gcc") is not None and \
+        os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
+def _calls_up_to_date() -> bool:
+    return not _can_build_calls() or _newer(CALLS, [CALLS_SRC] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
+    return _newer(LIB, _deps()) and _calls_up_to_date()
+
+
+def _build_calls():
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    cmd = ["gcc", "-O2", "-std=gnu11", "-shared", "-fPIC", "-I",
+           sysconfig.get_paths()["include"], "-o", tmp, CALLS_SRC]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {CALLS_SRC}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every kernel for sm_103a and link libwq.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
+    if force or not _newer(LIB, _deps()):
+        _build_lib(verbose, ptxas_info)
+    if not _can_build_calls():
+        sys.stderr.write("py_calls.c: no gcc or no Python.h, the binding will use ctypes alone\n")
+    elif force or not _calls_up_to_date():
+        _build_calls()
+    return LIB
+
+
+def _build_lib(verbose: bool, ptxas_info: bool) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -71,26 +105,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    def compile_calls():
-        tmp = CALLS + f".{os.getpid()}.tmp"
-        cmd = ["gcc", "-O2", "-std=gnu11", "-shared", "-fPIC", "-I",
-               sysconfig.get_paths()["include"], "-o", tmp, CALLS_SRC]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"gcc failed on {CALLS_SRC}:\n{r.stderr}")
-        os.replace(tmp, CALLS)
-
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, _sources()))
-        calls.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
