@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function forwards to the C entry point of the
 same name in ``_build/libwq.so`` (declared in ``include/wq.h``), through ctypes or, for
-the calls of a decode step, the C module ``_build/_wq_calls.so`` where it was built; all the
+the calls of a decode step, the C module ``_build/_wq_calls.*.so`` where it was built; all the
 work runs in the library's CUDA kernels.  There is no CPU fallback: if the library is not
 built, or no CUDA device is present, the calls raise.
 
@@ -13,6 +13,7 @@ integer, or ``None`` for torch's current stream on the current device.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
 import importlib.util
 import operator
 import os
@@ -21,7 +22,8 @@ import types
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libwq.so")
-CALLS_PATH = os.path.join(HERE, "_build", "_wq_calls.so")
+CALLS_PATH = os.path.join(HERE, "_build",
+                          "_wq_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 WQ_BF16, WQ_Q8_0, WQ_Q4_0, WQ_F16, WQ_F32 = 0, 1, 2, 3, 4
 WQ_BIAS, WQ_GELU, WQ_RESIDUAL, WQ_TC_BF16 = 1, 2, 4, 256

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -21,7 +22,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libwq.so")
-CALLS = os.path.join(OUT_DIR, "_wq_calls.so")
+# Named for the interpreter that it is built for: another one builds its own.
+CALLS = os.path.join(OUT_DIR, "_wq_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 CALLS_SRC = os.path.join(CSRC, "py_calls.c")
 INCLUDE = os.path.join(ROOT, "include")
 

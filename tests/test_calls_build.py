@@ -1,5 +1,7 @@
 """The library is built and called where the binding's C module cannot be built."""
 import os
+import sys
+import sysconfig
 
 import numpy as np
 import pytest
@@ -67,3 +69,10 @@ def test_the_same_results_through_ctypes(no_module):
     assert hasattr(wq._calls, "bind")
     for a, b in zip(slow, fast):
         assert np.array_equal(a, b)
+
+
+def test_the_module_is_one_interpreter_s():
+    """Its name carries the interpreter's tag, and the binding loads that name alone."""
+    tag = sysconfig.get_config_var("EXT_SUFFIX")
+    assert sys.implementation.cache_tag.split("-")[-1] in tag
+    assert os.path.basename(wqbuild.CALLS) == os.path.basename(wq.CALLS_PATH) == "_wq_calls" + tag
