@@ -1301,18 +1301,32 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     const int slots = min(kMaxCtas, S::kCtas * dev.sm_count);
     if (rows > 0x7FFFFFFFll / 8) return cudaErrorInvalidConfiguration;
 
-    // A cluster per row where a CTA has at most four tiles: no parts, no second launch (one
-    // sequence, 8 rows of 1024 slots: 7.9 us, split and joined 9.1; of 4096 15.9 and 12.8).
-    // More CTAs to a row while one per SM is not reached, or two where one has over two tiles
-    // (32 rows of 256 slots: 4 CTAs a row 6.6 us, 8 take 8.3; of 2048 15.9 and 13.3), and
-    // where rows alone are more than fit, one each (800 rows of 256: 30.0 us, split 32.9).
+    // A cluster per row, no parts and no second launch, while all rows' CTAs are resident and a
+    // CTA has at most four tiles, or two where its cluster is of eight: there the split
+    // kernel has SMs to spare.  More CTAs to a row while one per SM is not reached, or two
+    // where one has over two tiles.  Cluster and split, us, by a CTA's tiles:
+    //                                         1          2          3          4
+    //   32/8 of 128 bf16,  8 rows (of 8)  7.3  8.7   8.8  9.3  10.1  9.5  11.5  9.9
+    //                     32 rows (of 8)  7.5  9.6  10.8 12.0  12.4 12.7  14.1 13.8
+    //                     96 rows (of 4)            10.6 12.9  12.1 14.0  13.9 15.8
+    //                    256 rows (of 1)  8.5  9.0  10.3 12.1  11.8 13.5  13.6 14.9
+    //                    800 rows (of 1) 15.7 14.2  19.3 19.0  22.4 22.5  27.8 27.8
+    //   16/16 of 64 f16,  16 rows (of 8)  7.2  8.5   8.4  9.5   9.6  9.1  10.9 10.6
+    //                    192 rows (of 2)  6.8  7.7   9.0 11.6  10.4 12.8  11.8 14.3
+    //                    512 rows (of 1) 12.5 10.2  15.1 12.9  17.9 14.3  20.7 16.3
+    //   16/4 of 256 bf16,  4 rows (of 8)  8.6 10.6  10.6 10.8  12.4 11.1  14.4 11.1
+    //                    128 rows (of 2)            12.9 15.6  14.9 18.3  17.1 20.3
+    //   32/2 of 256 f32,   4 rows (of 8)  9.3 11.2  12.1 11.5  14.8 11.9  17.6 12.2
+    //                    128 rows (of 2)            15.6 19.7  19.1 22.9  22.4 26.2
     // The cache's size stands for the lengths, which are not known here.
     const long long span = a.window > 0 && a.window < a.n_slots ? a.window : a.n_slots;
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= slots && span > cluster * S::BT &&
            (rows * cluster * 2 <= dev.sm_count || span > 2 * cluster * S::BT))
         cluster *= 2;
-    const bool small = span <= 4ll * cluster * S::BT && (!a.acc_out || head_tiles == 1);
+    const bool small = rows * cluster <= slots &&
+                       span <= (cluster == 8 ? 2ll : 4ll) * cluster * S::BT &&
+                       (!a.acc_out || head_tiles == 1);
     if (small) {
         static std::atomic<unsigned long long> done{0};
         cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, true>, S::kSmem, dev, done);
