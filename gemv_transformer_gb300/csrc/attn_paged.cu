@@ -1350,6 +1350,9 @@ cudaError_t launch_shape(const AttnArgs &a, const KvView &kv, const DeviceInfo &
     static std::atomic<unsigned long long> done{0};
     cudaError_t err = ensure_smem(attn_kernel<DT, DP, HT, Q4, false>, S::kSmem, dev, done);
     if (err != cudaSuccess) return err;
+    // A block of the join is a head of a row while two of them per SM are not reached (131072
+    // slots, 8 rows of 4 heads 91 us, a row each 98; 4 sequences of 16384, 32 rows of 8 heads
+    // 35 and 43; beyond, 16 of 4096 38 and 36, 32 of 4096 64 and 58).
     const int row_heads = min(a.group, S::kHeads);
     const int blocks_per_row = rows * row_heads <= 2 * dev.sm_count ? row_heads : 1;
     const int joins = (int)(rows <= slots ? rows : slots) * blocks_per_row;
