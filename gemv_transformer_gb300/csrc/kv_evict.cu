@@ -599,7 +599,9 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     // moves (8 rows of 20000 slots, one over: 1 CTA 6.3 us, 8 take 3.5; of 2049: 2.7 and 3.2;
     // 8 rows of 4096 cut to 1024: 26.2 and 12.4).  512 threads while two such CTAs per SM hold
     // all rows or the rows are long, else 256 (512 rows of 2049, one over: 4.7 us, with 512
-    // 5.8; of 8193 19.2 and 16.0); 1024 where one CTA per SM holds few long rows.
+    // 5.8; of 8193 19.2 and 16.0).  1024 for few long rows, whose clusters of eight CTAs, of
+    // an SM each, all find room at once (4 rows of 131072 cut to 16384 37 us, with 512 46; 14 rows
+    // 97 and 108; 14 rows of 70000 cut to 60000 64 and 67, 16 rows 70 and 60).
     const long long moves = a.keep < a.n_slots - a.keep ? a.keep : a.n_slots - a.keep;
     int cluster = 1;
     while (cluster < 8 && rows * cluster * 2 <= 2 * dev.sm_count &&
@@ -622,7 +624,7 @@ cudaError_t launch_kv_evict(const EvictArgs &a, const KvView &kv, const DeviceIn
     case 2: err = launch_rows<512, 2>(a, kv, counts, dev, stream); break;
     case 4: err = launch_rows<512, 4>(a, kv, counts, dev, stream); break;
     default:
-        err = rows * 8 <= dev.sm_count && a.n_slots > 65536
+        err = rows <= 14 && a.n_slots > 65536
                   ? launch_rows<1024, 8>(a, kv, counts, dev, stream)
                   : launch_rows<512, 8>(a, kv, counts, dev, stream);
     }
