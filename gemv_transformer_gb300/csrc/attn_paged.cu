@@ -4,13 +4,13 @@
 // cache with the keys split into parts that are joined.  x_j = scale q.k_j + mask_j,
 // p = softmax(x) by one pass with a running maximum m and sum l:
 //   m' = max(m, x), l' = l e^(m-m') + e^(x-m'), o' = o e^(m-m') + e^(x-m') v,
-// and parts (m, l, o) of a row are joined by the same rule, always in slot order.
+// and parts (m, l, o) of a row are joined by the same rule, in an order that the lengths fix.
 //
 // What bounds it: every live slot's k and v are read once and used group times (4 group
 // operations per 2 bytes of a bf16 cache), so the cache's bytes set the floor.  Measured (the
 // whole call, back to back; 6704 GB/s is this GPU's copy rate): 64 sequences of 1 to 8192 slots, 8
 // kv heads of 128 in bf16, 64 query heads, 1.08 GB: 167 us, 6430 GB/s; one sequence of
-// 131072, 32 query heads: 89 us, 6010 GB/s, of which 7 us pass before the first tile is done
+// 131072, 32 query heads: 90 us, 5960 GB/s, of which 7 us pass before the first tile is done
 // (lengths, page numbers, the tile: three loads that wait for one another) and 4 after the
 // last (the join).  Shorter calls are that chain: 391 slots 7.0 us.
 //
