@@ -37,7 +37,8 @@ def fill(c, k, v):
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
 @pytest.mark.parametrize("hq,d,lens", [(2, 64, [1, 40]), (8, 128, [1, 70]), (14, 64, [20, 3000]),
-                                       (32, 128, [33, 5]), (6, 256, [1, 50])])
+                                       (32, 128, [33, 5]), (6, 256, [1, 50]), (12, 128, [300, 90]),
+                                       (20, 256, [7, 2500])])
 def test_a_value_that_is_not_finite(kind, bad, hq, d, lens):
     """In k: every head that reads it; in v: its dim of them.  The query has components of either
     sign, some exact in any type, some with residuals of either sign, one 0."""
