@@ -36,13 +36,19 @@ WQ_MOE_WINDOW_SLOTS = 256
 WQ_ROPE_INTERLEAVED, WQ_ROPE_TRANSPOSE = 1, 2
 WQ_ROPE_PLAIN, WQ_ROPE_LINEAR, WQ_ROPE_NTK, WQ_ROPE_YARN, WQ_ROPE_BANDS = 0, 1, 2, 3, 4
 
+WQ_AXES_DEALT, WQ_AXES_RESTART = 4, 8
+WQ_HEAD_NONE, WQ_HEAD_RMS, WQ_HEAD_LAYER = 0, 1, 2
+
 EXPORTS = ("wq_gemm", "wq_gemm_ws", "wq_gemm_alpha", "wq_gemm_dual", "wq_gemm_workspace_bytes",
            "wq_gemm_noalloc",
            "wq_gemm_ln_ws", "wq_gemm_ln_workspace_bytes", "wq_gemv",
            "wq_moe_gemv", "wq_weight_bytes", "wq_dequantize", "wq_embed", "wq_get_device_status",
            "wq_status_string", "wq_set_wait_limit",
            "wq_rope_table", "wq_rope", "wq_kv_append", "wq_attn_paged",
-           "wq_attn_paged_workspace_bytes", "wq_kv_evict", "wq_kv_evict_workspace_bytes")
+           "wq_attn_paged_workspace_bytes", "wq_kv_evict", "wq_kv_evict_workspace_bytes",
+           "wq_norm_rope", "wq_norm_rope_grad", "wq_norm_rope_grad_workspace_bytes",
+           "wq_kv_append_norm", "wq_attn_tokens", "wq_attn_tokens_workspace_bytes",
+           "wq_kv_accept")
 
 _lock = threading.Lock()
 _lib = None
@@ -62,6 +68,57 @@ class KvCache(ctypes.Structure):
                 ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class HeadNorm(ctypes.Structure):
+    """wq_head_norm."""
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class RopeAxes(ctypes.Structure):
+    """wq_rope_axes."""
+    _fields_ = [("rot", ctypes.c_int32), ("flags", ctypes.c_uint32), ("axes", ctypes.c_int32),
+                ("pairs", ctypes.c_int32 * 4), ("table_rows", ctypes.c_int32),
+                ("table_pairs", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("pos", ctypes.c_void_p), ("pos_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p)]
+
+
+class AttnForm(ctypes.Structure):
+    """wq_attn_form."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("tree", ctypes.c_void_p),
+                ("tree_stride", ctypes.c_int64), ("pos", ctypes.c_void_p)]
+
+
+def head_norm(kind, eps=1e-6, weight=None, bias=None) -> HeadNorm:
+    """The descriptor of a norm of heads.  Like the others it keeps addresses, not the tensors."""
+    return HeadNorm(kind, eps, _p(weight), _p(bias))
+
+
+def rope_axes(rot, flags, pairs, pos, table) -> RopeAxes:
+    """The descriptor of a rotation: `pairs` of each axis, pos int32 [axes][tokens] (or [tokens])
+    and table f32 [rows][pairs of the table][2], tensors with contiguous last dimensions."""
+    if not 1 <= len(pairs) <= 4:
+        raise ValueError("one to four axes")
+    step = pos.stride(0) if pos.dim() == 2 else 0
+    return RopeAxes(rot, flags, len(pairs), (ctypes.c_int32 * 4)(*pairs), table.shape[0],
+                    table.shape[1], 0, pos.data_ptr(), step, table.data_ptr())
+
+
+def attn_form(softcap=0.0, window=0, slopes=None, first=None, prefix=None, tree=None,
+              pos=None) -> AttnForm:
+    """The descriptor of what wq_attn_tokens' tokens see; tree: int32 [tokens][words]."""
+    return AttnForm(softcap, window, _p(slopes), _p(first), _p(prefix), _p(tree),
+                    0 if tree is None else tree.stride(0), _p(pos))
+
+
+def kv_caches(ks, vs):
+    """The descriptors of several layers' pools, for wq_kv_accept."""
+    caches = [kv_cache(k, v) for k, v in zip(ks, vs, strict=True)]
+    return (KvCache * len(caches))(*caches)
 
 
 def kv_cache(k, v) -> KvCache:
@@ -142,6 +199,24 @@ def _open(path: str):
     lib.wq_attn_paged_workspace_bytes.restype = sz
     lib.wq_kv_evict_workspace_bytes.argtypes = [cp, ci, ci, ci]
     lib.wq_kv_evict_workspace_bytes.restype = sz
+    np_, xp, fp = (ctypes.POINTER(t) for t in (HeadNorm, RopeAxes, AttnForm))
+    lib.wq_norm_rope.argtypes = [ci, ci, ci, np_, xp, vp, i64, ci, vp, i64, vp]
+    lib.wq_norm_rope.restype = ci
+    lib.wq_norm_rope_grad.argtypes = [ci, ci, ci, np_, xp, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                      sz, vp]
+    lib.wq_norm_rope_grad.restype = ci
+    lib.wq_norm_rope_grad_workspace_bytes.argtypes = [ci, ci, ci]
+    lib.wq_norm_rope_grad_workspace_bytes.restype = sz
+    lib.wq_kv_append_norm.argtypes = [cp, ci, ci, np_, np_, xp, vp, i64, vp, i64, vp, i64, ci, vp,
+                                      vp, vp, ci, ci, vp, i64, vp, vp, i64, vp]
+    lib.wq_kv_append_norm.restype = ci
+    lib.wq_attn_tokens.argtypes = [cp, ci, ci, ci, cf, fp, ci, vp, i64, vp, vp, ci, vp, ci, vp,
+                                   i64, vp, vp, sz, vp]
+    lib.wq_attn_tokens.restype = ci
+    lib.wq_attn_tokens_workspace_bytes.argtypes = [cp, ci, ci, ci, ci]
+    lib.wq_attn_tokens_workspace_bytes.restype = sz
+    lib.wq_kv_accept.argtypes = [cp, ci, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.wq_kv_accept.restype = ci
     lib.wq_get_device_status.argtypes = [vp]
     lib.wq_get_device_status.restype = ci
     lib.wq_status_string.argtypes = [ci]
@@ -346,6 +421,58 @@ def wq_kv_evict(cache, n_seq, page_table, max_pages, lens, seen, keep, sinks, re
 
 def wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep) -> int:
     return load().wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep)
+
+
+def wq_norm_rope(n, n_heads, head_dim, norm, rope, x, x_stride, out_type, out, out_stride,
+                 stream=None) -> int:
+    return load().wq_norm_rope(n, n_heads, head_dim, norm, rope, _p(x), x_stride, out_type,
+                               _p(out), out_stride, _s(stream))
+
+
+def wq_norm_rope_grad(n, n_heads, head_dim, norm, rope, x, x_stride, grad_out, grad_out_stride,
+                      grad_x, grad_x_stride, grad_weight=None, grad_bias=None, workspace=None,
+                      workspace_bytes=0, stream=None) -> int:
+    return load().wq_norm_rope_grad(n, n_heads, head_dim, norm, rope, _p(x), x_stride,
+                                    _p(grad_out), grad_out_stride, _p(grad_x), grad_x_stride,
+                                    _p(grad_weight), _p(grad_bias), _p(workspace),
+                                    int(workspace_bytes), _s(stream))
+
+
+def wq_norm_rope_grad_workspace_bytes(n, n_heads, head_dim) -> int:
+    return load().wq_norm_rope_grad_workspace_bytes(n, n_heads, head_dim)
+
+
+def wq_kv_append_norm(cache, n_tok, h_q, q_norm, k_norm, rope, q, q_stride, k, k_stride, v,
+                      v_stride, n_seq, seq, slot, page_table, max_pages, q_type=WQ_F32,
+                      q_out=None, q_out_stride=0, acc=None, slot_pos=None, acc_stride=0,
+                      stream=None) -> int:
+    return load().wq_kv_append_norm(cache, n_tok, h_q, q_norm, k_norm, rope, _p(q), q_stride,
+                                    _p(k), k_stride, _p(v), v_stride, n_seq, _p(seq), _p(slot),
+                                    _p(page_table), max_pages, q_type, _p(q_out), q_out_stride,
+                                    _p(acc), _p(slot_pos), acc_stride, _s(stream))
+
+
+def wq_attn_tokens(cache, n_seq, n_tok, h_q, scale, form, q_type, q, q_stride, starts, page_table,
+                   max_pages, lens, out_type, out, out_stride, lse=None, workspace=None,
+                   workspace_bytes=0, stream=None) -> int:
+    return load().wq_attn_tokens(cache, n_seq, n_tok, h_q, scale, form, q_type, _p(q), q_stride,
+                                 _p(starts), _p(page_table), max_pages, _p(lens), out_type,
+                                 _p(out), out_stride, _p(lse), _p(workspace),
+                                 int(workspace_bytes), _s(stream))
+
+
+def wq_attn_tokens_workspace_bytes(cache, n_seq, n_tok, h_q, q_type) -> int:
+    return load().wq_attn_tokens_workspace_bytes(cache, n_seq, n_tok, h_q, q_type)
+
+
+def wq_kv_accept(caches, n_seq, n_tok, page_table, max_pages, starts, parent, tokens, choice, lens,
+                 path, accepted, next, lens_out, stream=None) -> int:
+    """caches: kv_caches(...), or one KvCache."""
+    if isinstance(caches, KvCache):
+        caches = (KvCache * 1)(caches)
+    return load().wq_kv_accept(caches, len(caches), n_seq, n_tok, _p(page_table), max_pages,
+                               _p(starts), _p(parent), _p(tokens), _p(choice), _p(lens), _p(path),
+                               _p(accepted), _p(next), _p(lens_out), _s(stream))
 
 
 def wq_get_device_status(stream=None) -> int:

@@ -1,0 +1,502 @@
+// attn_tokens.cu -- attention of several new tokens per sequence over a paged cache: the plan, the
+// join of parts, and the kernel in f32 arithmetic that takes every type and head size.
+//
+// x = cap(scale q.k) + slope (pos_k - pos_q), p = softmax(x) with a running maximum and sum,
+// in log2 units: y = x log2 e, p = 2^(y - m).
+//
+// attn_rows_kernel takes f32 caches, f32 queries over f16 caches and heads above 128 dims: k and v
+// are widened to f32 in shared memory and every product is an f32 FMA, so it is exact to f32 and
+// bound by the FMA pipe (4 head_dim operations per row and slot) from about 16 rows of a group on.
+// A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the output;
+// the 16 lanes of a row join its maximum and sum by shuffles.
+#include "attn_tokens.cuh"
+
+namespace wq {
+namespace tok {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+// Inclusive scan over the block; `total` of all.
+__device__ __forceinline__ long long block_scan(long long x, long long *s_warp, long long &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = warp_scan(x, lane);
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) s_warp[lane] = warp_scan(s_warp[lane], lane);
+    __syncthreads();
+    if (warp > 0) x += s_warp[warp - 1];
+    total = s_warp[31];
+    __syncthreads();
+    return x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_plan_kernel(TokensArgs a, int heads, int rt, int kt, int dp, int grid) {
+    __shared__ long long s_warp[32];
+    __shared__ int s_first[kPlanThreads + 1];
+    pdl_enter();
+    const int group = a.group.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
+    // Row tiles of the sequences, kPlanThreads sequences at a time.
+    int n_tiles = 0;
+    long long cost = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
+        int mine = 0;
+        if (s0 + (int)threadIdx.x < a.n_seq) {
+            bool bad = false;
+            const Seq q = seq_of(a, s0 + threadIdx.x, bad);
+            if (bad) record_status(a.status, kStBadIndex);
+            mine = (int)(((long long)q.count * group + rt - 1) / rt);
+        }
+        long long all;
+        const long long upto = block_scan(mine, s_warp, all);
+        s_first[threadIdx.x + 1] = n_tiles + (int)upto;
+        if (threadIdx.x == 0) s_first[0] = n_tiles;
+        __syncthreads();
+        // A warp lists a sequence's tiles.
+        for (int i = warp; i < kPlanThreads && s0 + i < a.n_seq; i += kPlanThreads / 32) {
+            const int first = s_first[i], count = s_first[i + 1] - first;
+            if (count == 0) continue;
+            bool bad = false;
+            const int s = s0 + i;
+            const Seq q = seq_of(a, s, bad);
+            const bool each = a.first || (a.tree && a.window > 0);
+            for (int r = lane; r < count; r += 32) {
+                const int row0 = r * rt, row1 = min(row0 + rt, q.count * group);
+                const int j0 = row0 / group, j1 = (row1 - 1) / group;
+                int lo = INT_MAX, hi = 0, lo_most = 0, hi_least = INT_MAX;
+                // Without per-token arrays the bounds rise from token to token.
+                for (int j = j0; j <= j1; j = each || j == j1 ? j + 1 : j1) {
+                    const See v = see_of(a, q, s, j);
+                    int l = v.lo, h = v.hi;
+                    if (v.own_end > v.own) {  // its own slots may lie below its window
+                        h = v.own_end;
+                        l = min(l, max(v.own, 0));
+                    }
+                    lo = min(lo, l);
+                    hi = max(hi, h);
+                    lo_most = max(lo_most, v.lo);
+                    hi_least = min(hi_least, v.hi);
+                }
+                Tile t{s, row0, 0, 0, lo_most, hi_least, 0, 0};
+                if (hi > lo) t.k0 = lo / kt, t.k1 = (hi + kt - 1) / kt;
+                room.tiles[first + r] = t;
+            }
+        }
+        n_tiles += (int)all;
+        __syncthreads();
+    }
+    // Costs before each row tile.
+    for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x;
+        long long mine = 0;
+        if (i < n_tiles) mine = room.tiles[i].k1 - room.tiles[i].k0 + kRowCost;
+        long long all;
+        const long long upto = block_scan(mine, s_warp, all);
+        if (i < n_tiles) room.before[i] = cost + upto - mine;
+        cost += all;
+    }
+    if (threadIdx.x == 0) room.before[n_tiles] = cost;
+    __syncthreads();
+    for (int b = threadIdx.x; b <= grid; b += kPlanThreads) {
+        Begin p{heads, 0, 0, n_tiles};
+        if (b < grid && cost > 0) {
+            const long long total = cost * heads;
+            const long long at = total / grid * b + min((long long)b, total % grid);
+            const int head = (int)(at / cost);
+            const long long in = at - head * cost;
+            int x = 0, y = n_tiles;  // before[x] <= in < before[y]
+            while (y - x > 1) {
+                const int mid = (x + y) / 2;
+                if (room.before[mid] <= in) x = mid; else y = mid;
+            }
+            p.head = head;
+            p.tile = x;
+            p.off = (int)(in - room.before[x]);
+            const Tile t = room.tiles[x];
+            if (p.off > 0 && p.off >= t.k1 - t.k0) {  // in the end of a row tile
+                p.off = 0;
+                if (++p.tile == n_tiles) p.tile = 0, ++p.head;
+            }
+        }
+        room.plan[b] = p;
+    }
+}
+
+// Joins the parts of the row tile that CTA blockIdx.x + 1 begins within, if that CTA is the first to.
+// A thread takes one row and four dims at a time.
+__global__ void __launch_bounds__(256)
+    attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
+    pdl_enter();
+    const int group = a.group.d;
+    const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
+    const int b = blockIdx.x + 1;
+    const Begin p = room.plan[b], before = room.plan[b - 1];
+    if (p.off == 0 || p.head >= kv.n_heads) return;
+    if (before.head == p.head && before.tile == p.tile && before.off > 0) return;
+    int n = 1;  // CTAs that begin within it
+    for (; b + n < grid; ++n) {
+        const Begin q = room.plan[b + n];
+        if (q.head != p.head || q.tile != p.tile || q.off == 0) break;
+    }
+    const Tile tile = room.tiles[p.tile];
+    bool bad = false;
+    const Seq q = seq_of(a, tile.seq, bad);
+    const int rows = min(rt, q.count * group - tile.row0);
+    const TypedOut out{a.out, a.out_type};
+    // The parts: the second of CTA b - 1, then the first of CTAs b, b + 1, ...
+    auto place = [&](int i) { return (size_t)(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)); };
+    const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+    if (row >= rows) return;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i <= n; ++i) m = fmaxf(m, room.part_ml[place(i) * rt + row].x);
+    const float safe = m == -INFINITY ? 0.f : m;
+    for (int i = 0; i <= n; ++i) {
+        const float2 ml = room.part_ml[place(i) * rt + row];
+        l = fmaf(ml.y, exp2f(ml.x - safe), l);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int rr = tile.row0 + row, j = a.group.div(rr), g = rr - j * group;
+    const int t = q.t0 + j, h = p.head * group + g;
+    for (int c = threadIdx.x >> 5; c * 4 < kv.head_dim; c += 8) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i <= n; ++i) {
+            const float f = exp2f(room.part_ml[place(i) * rt + row].x - safe);
+            const float4 v = room.part_o[(place(i) * (dp / 4) + c) * rt + row];
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        }
+        out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
+                 make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    if (a.lse && threadIdx.x < 32) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+}
+
+// ------------------------------------------------------------------ f32 arithmetic --
+
+template <typename T> __device__ __forceinline__ float to_f32(T x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(x);
+    else return __bfloat162float(x);
+}
+// Eight values of a row as f32.
+template <typename T> __device__ __forceinline__ void load8(const void *p, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 x = reinterpret_cast<const float4 *>(p)[0],
+                     y = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        const T *t = reinterpret_cast<const T *>(&x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+    }
+}
+
+template <int DP, int R> struct RowsShape {
+    static constexpr int KT = DP > 128 ? 32 : 64;
+    static constexpr int RT = 16 * R;
+    static constexpr int kPitch = DP + 4;       // floats of a row of q or k: rows four banks apart
+    static constexpr int kQ = RT * kPitch, kK = KT * kPitch, kV = KT * DP, kP = RT * (KT + 4);
+    static constexpr int kSmem = (kQ + kK + kV + kP) * 4;
+};
+
+template <typename T, int DP, int R>
+__global__ void __launch_bounds__(256)
+    attn_rows_kernel(TokensArgs a, KvView kv, int grid) {
+    using S = RowsShape<DP, R>;
+    constexpr int KT = S::KT, RT = S::RT, NK = KT / 16, ND = DP / 16;
+    extern __shared__ __align__(16) float s_rows[];
+    float *s_q = s_rows, *s_k = s_q + S::kQ, *s_v = s_k + S::kK, *s_p = s_v + S::kV;
+    pdl_enter();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.group.d;
+    const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, RT, DP, grid);
+    Walk walk(room, blockIdx.x, room.plan[grid].pad);
+    const TypedOut out{a.out, a.out_type};
+    const int d = kv.head_dim;
+    Stretch st;
+    while (walk.next(st)) {
+        bool bad = false;
+        const Seq q = seq_of(a, st.tile.seq, bad);
+        const int rows = min(RT, q.count * group - st.tile.row0);
+        __syncthreads();
+        for (int i = threadIdx.x; i < RT * (DP / 8); i += 256) {
+            const int r = i / (DP / 8), c = i - r * (DP / 8);
+            float v[8] = {};
+            if (r < rows && c * 8 < d) {
+                const int rr = st.tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
+                const long long at = (q.t0 + j) * a.q_stride +
+                                     (long long)(st.head * group + g) * d + c * 8;
+                if (a.q_type == kF32)
+                    load8<float>(static_cast<const float *>(a.q) + at, v);
+                else if (a.q_type == kBF16)
+                    load8<__nv_bfloat16>(static_cast<const __nv_bfloat16 *>(a.q) + at, v);
+                else
+                    load8<__half>(static_cast<const __half *>(a.q) + at, v);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_q[r * S::kPitch + c * 8 + e] = v[e];
+        }
+        See see[R];
+        float slope[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = ty * R + i;
+            const int rr = st.tile.row0 + min(r, rows - 1), j = a.group.div(rr);
+            see[i] = see_of(a, q, st.tile.seq, j);
+            slope[i] = a.slopes ? a.slopes[st.head * group + rr - j * group] : 0.f;
+        }
+        float m[R], l[R], o[R][ND];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < ND; ++e) o[i][e] = 0.f;
+        }
+        for (int kt = st.k0; kt < st.k1; ++kt) {
+            const int j0 = kt * KT;
+            __syncthreads();
+            // k and v, zero beyond the live slots and where a page is out of range.
+            uint32_t lost = 0;  // (bit 0) a slot without a page, (bit 1) a v that is not finite
+            for (int i = threadIdx.x; i < KT * (DP / 8); i += 256) {
+                const int r = i / (DP / 8), c = i - r * (DP / 8), j = j0 + r;
+                float x[8] = {}, y[8] = {};
+                if (j < q.len) {
+                    const long long at = kv.row(st.tile.seq, st.head, j);
+                    if (at < 0) {
+                        lost |= 1u;
+                    } else if (c * 8 < d) {
+                        load8<T>(kv.k + at + c * 8 * sizeof(T), x);
+                        load8<T>(kv.v + at + c * 8 * sizeof(T), y);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s_k[r * S::kPitch + c * 8 + e] = x[e];
+                    s_v[r * DP + c * 8 + e] = y[e];
+                    if (!isfinite(y[e])) lost |= 2u;
+                }
+            }
+            const int none = __syncthreads_or(lost & 1u), odd = __syncthreads_or(lost & 2u);
+            if (none && threadIdx.x == 0) record_status(a.status, kStBadIndex);
+            float x[R][NK];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int n = 0; n < NK; ++n) x[i][n] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < DP; c += 4) {
+                float4 qa[R], ka[NK];
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    qa[i] = *reinterpret_cast<const float4 *>(s_q + (ty * R + i) * S::kPitch + c);
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+                    ka[n] = *reinterpret_cast<const float4 *>(s_k + (tx + 16 * n) * S::kPitch + c);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int n = 0; n < NK; ++n) {
+                        x[i][n] = fmaf(qa[i].x, ka[n].x, x[i][n]);
+                        x[i][n] = fmaf(qa[i].y, ka[n].y, x[i][n]);
+                        x[i][n] = fmaf(qa[i].z, ka[n].z, x[i][n]);
+                        x[i][n] = fmaf(qa[i].w, ka[n].w, x[i][n]);
+                    }
+            }
+            const bool whole = j0 >= st.tile.lo && j0 + KT <= st.tile.hi && !none;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                uint32_t seen[KT / 32];
+#pragma unroll
+                for (int w = 0; w < KT / 32; ++w)
+                    seen[w] = whole ? 0xFFFFFFFFu : seen32(a, see[i], j0 + 32 * w);
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const int r = tx + 16 * n, j = j0 + r;
+                    float y = x[i][n] * a.scale;
+                    if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
+                    if (a.slopes) y = fmaf(slope[i], (float)(slot_pos(a, q, j) - see[i].pos), y);
+                    bool in = seen[r >> 5] >> (r & 31) & 1u;
+                    if (none && in) in = kv.row(st.tile.seq, st.head, j) >= 0;
+                    // A score that is not a number stays one: only slots that are not seen are -inf.
+                    x[i][n] = in ? y * kLog2e : -INFINITY;
+                    if (!in) seen[r >> 5] &= ~(1u << (r & 31));
+                    top = fmaxf(top, x[i][n]);
+                }
+#pragma unroll
+                for (int s = 8; s > 0; s >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+                const float now = fmaxf(m[i], top), safe = now == -INFINITY ? 0.f : now;
+                const float f = exp2f(m[i] - safe);
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const int r = tx + 16 * n;
+                    const float p = exp2f(x[i][n] - safe);
+                    sum += p;
+                    // -1 marks a slot that is not seen where 0 times v would not be 0.
+                    const bool in = seen[r >> 5] >> (r & 31) & 1u;
+                    s_p[(ty * R + i) * (KT + 4) + r] = odd && !in ? -1.f : p;
+                }
+#pragma unroll
+                for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+                l[i] = fmaf(l[i], f, sum);
+                m[i] = now;
+#pragma unroll
+                for (int e = 0; e < ND; ++e) o[i][e] *= f;
+            }
+            __syncwarp();  // a row's 16 lanes are in one warp
+            if (!odd) {
+#pragma unroll 2
+                for (int r = 0; r < KT; r += 4) {
+                    float4 pa[R];
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        pa[i] = *reinterpret_cast<const float4 *>(s_p + (ty * R + i) * (KT + 4) + r);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < ND; e += 4) {
+                            const float4 v = *reinterpret_cast<const float4 *>(
+                                s_v + (r + k) * DP + (e / 4) * 64 + tx * 4);
+#pragma unroll
+                            for (int i = 0; i < R; ++i) {
+                                const float p = k == 0   ? pa[i].x
+                                                : k == 1 ? pa[i].y
+                                                : k == 2 ? pa[i].z
+                                                         : pa[i].w;
+                                o[i][e] = fmaf(p, v.x, o[i][e]);
+                                o[i][e + 1] = fmaf(p, v.y, o[i][e + 1]);
+                                o[i][e + 2] = fmaf(p, v.z, o[i][e + 2]);
+                                o[i][e + 3] = fmaf(p, v.w, o[i][e + 3]);
+                            }
+                        }
+                }
+            } else {
+                for (int r = 0; r < KT; ++r)
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float p = s_p[(ty * R + i) * (KT + 4) + r];
+                        if (p == -1.f) continue;
+#pragma unroll
+                        for (int e = 0; e < ND; ++e)
+                            o[i][e] = fmaf(p, s_v[r * DP + (e / 4) * 64 + tx * 4 + (e & 3)], o[i][e]);
+                    }
+            }
+        }
+        // Dims (e / 4) * 64 + tx * 4 + e % 4 of the thread's rows.
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = ty * R + i;
+            if (r >= rows) continue;
+            if (st.part >= 0) {
+                const size_t part = 2 * blockIdx.x + st.part;
+#pragma unroll
+                for (int e = 0; e < ND; e += 4)
+                    room.part_o[(part * (DP / 4) + (e / 4) * 16 + tx) * RT + r] =
+                        make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
+                if (tx == 0) room.part_ml[part * RT + r] = make_float2(m[i], l[i]);
+                continue;
+            }
+            const int rr = st.tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
+            const int t = q.t0 + j, h = st.head * group + g;
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+            for (int e = 0; e < ND; e += 4) {
+                const int c = (e / 4) * 64 + tx * 4;
+                if (c < d)
+                    out.put4(t * a.out_stride + (long long)h * d + c,
+                             make_float4(o[i][e] * inv, o[i][e + 1] * inv, o[i][e + 2] * inv,
+                                         o[i][e + 3] * inv));
+            }
+            if (a.lse && tx == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m[i], l[i]);
+        }
+    }
+}
+
+// Rows of a thread: one where the sequences have few rows, else four.
+int rows_per_thread(int n_seq, int n_tok, int group) {
+    return (long long)n_tok * group <= 24ll * n_seq ? 1 : 4;
+}
+int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+
+template <typename T, int DP, int R>
+cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
+                        cudaStream_t stream) {
+    using S = RowsShape<DP, R>;
+    static std::atomic<unsigned long long> raised{0};
+    cudaError_t err = ensure_smem(attn_rows_kernel<T, DP, R>, S::kSmem, dev, raised);
+    if (err != cudaSuccess) return err;
+    const int grid = kMaxGrid;
+    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, grid, stream);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, a, kv,
+                     grid);
+    if (err != cudaSuccess) return err;
+    return launch_attn_parts(a, kv, S::RT, DP, grid, stream);
+}
+template <typename T>
+cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
+                             cudaStream_t stream) {
+    const bool one = rows_per_thread(a.n_seq, a.n_tok, a.group.d) == 1;
+    switch (padded_dim(kv.head_dim)) {
+    case 64: return one ? launch_rows<T, 64, 1>(a, kv, dev, stream)
+                        : launch_rows<T, 64, 4>(a, kv, dev, stream);
+    case 128: return one ? launch_rows<T, 128, 1>(a, kv, dev, stream)
+                         : launch_rows<T, 128, 4>(a, kv, dev, stream);
+    default: return one ? launch_rows<T, 256, 1>(a, kv, dev, stream)
+                        : launch_rows<T, 256, 4>(a, kv, dev, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
+                             int grid, cudaStream_t stream) {
+    return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kv.n_heads, rt,
+                      kt, dp, grid);
+}
+
+cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
+                              cudaStream_t stream) {
+    if (grid < 2) return cudaSuccess;
+    return launch_pdl(attn_parts_kernel, dim3(grid - 1, (rt + 31) / 32), dim3(256), 0, stream, a,
+                      kv, rt, dp, grid);
+}
+
+}  // namespace tok
+
+size_t tokens_workspace_bytes(const KvView &kv, int n_seq, int n_tok, int h_q, int q_type) {
+    const int group = h_q / kv.n_heads;
+    int rt, kt, dp;
+    if (tok::tokens_tc_takes(kv, q_type)) {
+        tok::tokens_tc_shape(n_seq, n_tok, group, q_type, kv.head_dim, rt, kt, dp);
+    } else {
+        rt = 16 * tok::rows_per_thread(n_seq, n_tok, group);
+        dp = tok::padded_dim(kv.head_dim);
+    }
+    return tok::room_of(nullptr, n_seq, n_tok, group, rt, dp, tok::kMaxGrid).bytes;
+}
+
+cudaError_t launch_attn_tokens(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
+                               cudaStream_t stream) {
+    if (tok::tokens_tc_takes(kv, a.q_type)) return tok::launch_tokens_tc(a, kv, dev, stream);
+    switch (kv.dtype) {
+    case kBF16: return tok::launch_rows_type<__nv_bfloat16>(a, kv, dev, stream);
+    case kF16: return tok::launch_rows_type<__half>(a, kv, dev, stream);
+    default: return tok::launch_rows_type<float>(a, kv, dev, stream);
+    }
+}
+
+}  // namespace wq

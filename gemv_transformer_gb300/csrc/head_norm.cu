@@ -1,0 +1,544 @@
+// head_norm.cu -- norms of heads with rotary positions on several axes in the same pass: on packed
+// rows, their gradient, and the append of queries, keys and values to the pages of a cache.
+//
+// cortiq-engine 0.8.49 src/gpu_wgpu/nemotron_audio.rs, kernel ae_qk, normalises each head of q and
+// k (LayerNorm) and turns it by a table of cosines and sines.
+//
+//   y = w (x - mu) r + b, r = 1 / sqrt(mean((x - mu)^2) + eps), then pairs of y turned.
+// Gradient, g = R^T dout, h = (x - mu) r, u = w g:
+//   dx = r (u - h mean(u h) - mean(u)), the last term for LayerNorm only;
+//   dw = sum g h, db = sum g over rows and heads.
+//
+// What bounds it: bytes.  A head is held by G lanes of a warp, eight values each in two runs of
+// four (head_units.cuh), so its sums are log2 G shuffles and every value is read and written
+// once; a group of lanes takes up to kHeadsPer heads of a row, whose loads are in flight
+// together and share the row's angles.
+#include <initializer_list>
+
+#include "head_units.cuh"
+#include "kv_internal.h"
+#include "wq_device.cuh"
+
+namespace wq {
+namespace {
+
+constexpr int kHeadsPer = 4;
+constexpr int kThreads = 256;
+constexpr int kGradHeads = 2;
+
+// A lane's units of a head.
+template <int N, int U> struct Held {
+    Vals<N> a[U], b[U];
+};
+
+// The lanes' common view of a head: G lanes, unit lane + G i for i < U.
+template <int N, int G, int U> struct Lanes {
+    int lane, units, head_dim;
+    Place place[U];
+    __device__ __forceinline__ Lanes(const AxesView &ax, int d) : head_dim(d) {
+        lane = threadIdx.x & (G - 1);
+        units = (d + 2 * N - 1) / (2 * N);
+#pragma unroll
+        for (int i = 0; i < U; ++i) place[i] = place_of<N>(lane + G * i, ax.rot, ax.flags);
+    }
+    __device__ __forceinline__ bool has(int i) const { return lane + G * i < units; }
+    // An odd head_dim ends in a single value.
+    __device__ __forceinline__ bool both(int i) const { return N > 1 || place[i].b < head_dim; }
+    __device__ __forceinline__ void load(Held<N, U> &x, const float *p) const {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (has(i)) x.a[i] = load_vals<N>(p + place[i].a);
+            if (has(i) && both(i)) x.b[i] = load_vals<N>(p + place[i].b);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void store(const Held<N, U> &x, T *p) const {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (has(i)) store_vals(p + place[i].a, x.a[i]);
+            if (has(i) && both(i)) store_vals(p + place[i].b, x.b[i]);
+        }
+    }
+    // Weights or biases: `fill` where there are none.
+    __device__ __forceinline__ void load_or(Held<N, U> &x, const float *p, float fill) const {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                x.a[i].v[j] = p && has(i) ? p[place[i].a + j] : fill;
+                x.b[i].v[j] = p && has(i) && both(i) ? p[place[i].b + j] : fill;
+            }
+    }
+    // Values that are not part of the head are 0 in every sum.
+    __device__ __forceinline__ void zero_rest(Held<N, U> &x) const {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (!has(i)) x.a[i].v[j] = 0.f;
+                if (!has(i) || !both(i)) x.b[i].v[j] = 0.f;
+            }
+    }
+    __device__ __forceinline__ static float sum_group(float v) {
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    }
+    template <typename F> __device__ __forceinline__ float sum(F f) const {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) v += f(i, j, false) + f(i, j, true);
+        return sum_group(v);
+    }
+    // x becomes h = (x - mu) r; values beyond the head stay 0.  Returns r.
+    __device__ __forceinline__ float hat(Held<N, U> &x, const NormView &nv) const {
+        if (nv.kind == WQ_HEAD_LAYER) {
+            const float mu =
+                sum([&](int i, int j, bool b) { return b ? x.b[i].v[j] : x.a[i].v[j]; }) / head_dim;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int j = 0; j < N; ++j) x.a[i].v[j] -= mu, x.b[i].v[j] -= mu;
+            zero_rest(x);
+        }
+        const float ms = sum([&](int i, int j, bool b) {
+                             const float v = b ? x.b[i].v[j] : x.a[i].v[j];
+                             return v * v;
+                         }) / head_dim;
+        const float r = 1.f / sqrtf(ms + nv.eps);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) x.a[i].v[j] *= r, x.b[i].v[j] *= r;
+        return r;
+    }
+    __device__ __forceinline__ void norm(Held<N, U> &x, const NormView &nv) const {
+        zero_rest(x);
+        hat(x, nv);
+        Held<N, U> w, c;
+        load_or(w, nv.weight, 1.f);
+        load_or(c, nv.bias, 0.f);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                x.a[i].v[j] = fmaf(x.a[i].v[j], w.a[i].v[j], c.a[i].v[j]);
+                x.b[i].v[j] = fmaf(x.b[i].v[j], w.b[i].v[j], c.b[i].v[j]);
+            }
+    }
+};
+
+// A row's positions; false where one that turns something is out of range.
+struct Where {
+    int p[4];
+    __device__ __forceinline__ bool load(const AxesView &ax, long long t) {
+        bool ok = true;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            p[a] = a < ax.axes ? ax.pos[a * ax.pos_stride + t] : 0;
+            if (a < ax.axes && (ax.used >> a & 1) && (unsigned)p[a] >= (unsigned)ax.table_rows)
+                ok = false;
+        }
+        return ok;
+    }
+    __device__ __forceinline__ int of(int axis) const {
+        return axis == 0 ? p[0] : axis == 1 ? p[1] : axis == 2 ? p[2] : p[3];
+    }
+};
+
+// The angles of unit u's N pairs.
+template <int N>
+__device__ __forceinline__ Angles<N> angles_of(const AxesView &ax, const Where &w, int u,
+                                               unsigned flags) {
+    if (ax.straight)
+        return load_angles<N>(ax.table + (long long)w.p[0] * ax.table_pairs + u * N, flags);
+    Angles<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int code = ax.code[u * N + j];
+        const float2 cs = ax.table[(long long)w.of(code >> 8) * ax.table_pairs + (code & 255)];
+        r.c[j] = cs.x;
+        r.s[j] = flags & WQ_ROPE_TRANSPOSE ? -cs.y : cs.y;
+    }
+    return r;
+}
+
+template <int N, int G, int U> struct Turns {
+    Angles<N> cs[U];
+    __device__ __forceinline__ void load(const Lanes<N, G, U> &l, const AxesView &ax,
+                                         const Where &w, unsigned flags) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (l.place[i].turn) cs[i] = angles_of<N>(ax, w, l.lane + G * i, flags);
+    }
+    __device__ __forceinline__ void apply(const Lanes<N, G, U> &l, Held<N, U> &x,
+                                          unsigned flags) const {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (l.place[i].turn) turn<N>(x.a[i], x.b[i], cs[i], flags);
+    }
+};
+
+// Groups of lanes over rows and blocks of heads.
+struct HeadDeal {
+    FastDiv per_row;  // blocks of heads in a row
+    int heads_per;
+    unsigned count;
+};
+
+template <typename T, int N, int G, int U>
+__global__ void __launch_bounds__(kThreads)
+    norm_rope_kernel(const __grid_constant__ AxesView ax, NormView nv, HeadDeal deal, int head_dim,
+                     const float *x, long long x_stride, int n_heads, T *out, long long out_stride,
+                     long long t0) {
+    pdl_enter();
+    const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    // Every lane stays for the shuffles.
+    const bool live = at < deal.count;
+    const unsigned row = deal.per_row.div(live ? at : 0u);
+    const int h0 = live ? (int)(at - row * deal.per_row.d) * deal.heads_per : 0;
+    const int n = live ? min(deal.heads_per, n_heads - h0) : 0;
+    const long long t = t0 + row;
+    const Lanes<N, G, U> l(ax, head_dim);
+    const float *xi = x + t * x_stride + (long long)h0 * head_dim;
+    T *o = out + t * out_stride + (long long)h0 * head_dim;
+    Held<N, U> v[kHeadsPer] = {};
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) l.load(v[i], xi + i * head_dim);
+    Where w;
+    const bool ok = w.load(ax, t);
+    if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
+    Turns<N, G, U> turns;
+    if (ok) turns.load(l, ax, w, ax.flags);
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i) {
+        if (i >= deal.heads_per) break;
+        if (nv.kind != WQ_HEAD_NONE) l.norm(v[i], nv);
+        if (i < n && ok) {
+            turns.apply(l, v[i], ax.flags);
+            l.store(v[i], o + i * head_dim);
+        }
+    }
+}
+
+template <int DT, typename Q, int N, int G, int U>
+__global__ void __launch_bounds__(kThreads)
+    append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
+                       AppendNormArgs a, KvView kv, HeadDeal deal, int t0) {
+    pdl_enter();
+    using T = typename KvType<DT>::T;
+    const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    const bool live = at < deal.count;
+    const unsigned row_at = deal.per_row.div(live ? at : 0u);
+    const int d = kv.head_dim, heads = a.h_q + 2 * kv.n_heads;
+    const int h0 = live ? (int)(at - row_at * deal.per_row.d) * deal.heads_per : 0;
+    const int n = live ? min(deal.heads_per, heads - h0) : 0;
+    const int t = t0 + (int)row_at;
+    const int slot = a.slot[t];
+    const int seq = a.seq ? a.seq[t] : t;
+    const Lanes<N, G, U> l(ax, d);
+    // Heads in the order q, k, v.  The values do not wait for the slot.
+    Held<N, U> v[kHeadsPer] = {};
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i)
+        if (i < n) {
+            const int head = h0 + i;
+            const float *x =
+                head < a.h_q ? a.q + t * a.q_stride + (long long)head * d
+                : head < a.h_q + kv.n_heads
+                    ? a.k + t * a.k_stride + (long long)(head - a.h_q) * d
+                    : a.v + t * a.v_stride + (long long)(head - a.h_q - kv.n_heads) * d;
+            l.load(v[i], x);
+        }
+    Where w;
+    bool ok = w.load(ax, t);
+    ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
+    const long long row = ok ? kv.row(seq, 0, slot) : -1;
+    ok = ok && row >= 0;
+    if (live && !ok && slot >= 0 && l.lane == 0) record_status(ax.status, kStBadIndex);
+    Turns<N, G, U> turns;
+    if (ok) turns.load(l, ax, w, ax.flags);
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i) {
+        if (i >= deal.heads_per) break;
+        const int head = h0 + i;
+        const bool is_q = head < a.h_q, is_k = !is_q && head < a.h_q + kv.n_heads;
+        // The lanes of a warp may hold heads of both kinds: all of them run both norms' shuffles.
+        if (q_norm.kind != WQ_HEAD_NONE && __any_sync(0xFFFFFFFFu, is_q && i < n)) {
+            Held<N, U> y = v[i];
+            l.norm(y, q_norm);
+            if (is_q) v[i] = y;
+        }
+        if (k_norm.kind != WQ_HEAD_NONE && __any_sync(0xFFFFFFFFu, is_k && i < n)) {
+            Held<N, U> y = v[i];
+            l.norm(y, k_norm);
+            if (is_k) v[i] = y;
+        }
+        if (i >= n || !ok) continue;
+        if (is_q || is_k) turns.apply(l, v[i], ax.flags);
+        if (is_q) {
+            l.store(v[i], static_cast<Q *>(a.q_out) + t * a.q_out_stride + (long long)head * d);
+            continue;
+        }
+        const int h = head - a.h_q - (is_k ? 0 : kv.n_heads);
+        l.store(v[i], reinterpret_cast<T *>((is_k ? kv.k : kv.v) + row + h * kv.head_stride));
+        if (is_k && l.lane == 0) {
+            const long long to = ((long long)seq * kv.n_heads + h) * a.acc_stride + slot;
+            if (a.acc) a.acc[to] = 0.f;
+            if (a.slot_pos) a.slot_pos[to] = w.p[0];
+        }
+    }
+}
+
+// Groups of lanes stride over the heads, so that a lane's dims, and with them its sums for dw and
+// db, stay the same; the blocks' sums are added by grad_sums_kernel in a fixed order.
+template <int N, int G, int U>
+__global__ void __launch_bounds__(kThreads)
+    norm_rope_grad_kernel(const __grid_constant__ AxesView ax, NormView nv, HeadDeal deal,
+                          int head_dim, const float *x, long long x_stride, const float *grad,
+                          long long grad_stride, int n_heads, float *grad_x,
+                          long long grad_x_stride, float *parts) {
+    extern __shared__ float s_sums[];  // [groups][2][head_dim]
+    pdl_enter();
+    const Lanes<N, G, U> l(ax, head_dim);
+    const unsigned flags = ax.flags | WQ_ROPE_TRANSPOSE;
+    const unsigned groups = gridDim.x * (unsigned)(kThreads / G);
+    const unsigned first = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    Held<N, U> wt, sum_w = {}, sum_b = {};
+    l.load_or(wt, nv.kind != WQ_HEAD_NONE ? nv.weight : nullptr, 1.f);
+    const unsigned steps = (deal.count + groups - 1) / groups;
+    for (unsigned step = 0; step < steps; ++step) {
+        const unsigned long long where = (unsigned long long)step * groups + first;
+        const bool live = where < deal.count;
+        const unsigned at = live ? (unsigned)where : 0u;
+        const unsigned t = deal.per_row.div(at);
+        const int h0 = (int)(at - t * deal.per_row.d) * deal.heads_per;
+        const int n = live ? min(deal.heads_per, n_heads - h0) : 0;
+        Held<N, U> v[kGradHeads] = {}, g[kGradHeads] = {};
+#pragma unroll
+        for (int i = 0; i < kGradHeads; ++i)
+            if (i < n) {
+                l.load(v[i], x + t * x_stride + (long long)(h0 + i) * head_dim);
+                l.load(g[i], grad + t * grad_stride + (long long)(h0 + i) * head_dim);
+            }
+        Where w;
+        const bool ok = w.load(ax, t);
+        if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
+        Turns<N, G, U> turns;
+        if (ok) turns.load(l, ax, w, flags);
+#pragma unroll
+        for (int i = 0; i < kGradHeads; ++i) {
+            if (i >= deal.heads_per) break;
+            const bool mine = i < n && ok;
+            if (mine) turns.apply(l, g[i], flags);
+            if (nv.kind != WQ_HEAD_NONE) {
+                l.zero_rest(v[i]);
+                l.zero_rest(g[i]);
+                const float r = l.hat(v[i], nv);
+                if (mine) {
+#pragma unroll
+                    for (int k = 0; k < U; ++k)
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            sum_w.a[k].v[j] = fmaf(g[i].a[k].v[j], v[i].a[k].v[j], sum_w.a[k].v[j]);
+                            sum_w.b[k].v[j] = fmaf(g[i].b[k].v[j], v[i].b[k].v[j], sum_w.b[k].v[j]);
+                            sum_b.a[k].v[j] += g[i].a[k].v[j];
+                            sum_b.b[k].v[j] += g[i].b[k].v[j];
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        g[i].a[k].v[j] *= wt.a[k].v[j];
+                        g[i].b[k].v[j] *= wt.b[k].v[j];
+                    }
+                const float uh = l.sum([&](int k, int j, bool b) {
+                                     return b ? g[i].b[k].v[j] * v[i].b[k].v[j]
+                                              : g[i].a[k].v[j] * v[i].a[k].v[j];
+                                 }) / head_dim;
+                float mu = 0.f;
+                if (nv.kind == WQ_HEAD_LAYER)
+                    mu = l.sum([&](int k, int j, bool b) {
+                             return b ? g[i].b[k].v[j] : g[i].a[k].v[j];
+                         }) / head_dim;
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        g[i].a[k].v[j] = r * (g[i].a[k].v[j] - v[i].a[k].v[j] * uh - mu);
+                        g[i].b[k].v[j] = r * (g[i].b[k].v[j] - v[i].b[k].v[j] * uh - mu);
+                    }
+            }
+            if (mine) l.store(g[i], grad_x + t * grad_x_stride + (long long)(h0 + i) * head_dim);
+        }
+    }
+    if (!parts) return;
+    float *mine = s_sums + (threadIdx.x / G) * 2 * head_dim;
+    l.store(sum_w, mine);
+    l.store(sum_b, mine + head_dim);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * head_dim; c += kThreads) {
+        float s = 0.f;
+        for (int gr = 0; gr < kThreads / G; ++gr) s += s_sums[gr * 2 * head_dim + c];
+        parts[(long long)blockIdx.x * 2 * head_dim + c] = s;
+    }
+}
+
+// dw and db from the blocks' sums: 32 columns of a block, 32 threads to a column.
+__global__ void __launch_bounds__(1024) grad_sums_kernel(const float *parts, int blocks,
+                                                         int head_dim, float *grad_weight,
+                                                         float *grad_bias) {
+    __shared__ float s[32][33];
+    pdl_enter();
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float v = 0.f;
+    if (c < 2 * head_dim)
+        for (int b = threadIdx.y; b < blocks; b += 32) v += parts[(long long)b * 2 * head_dim + c];
+    s[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    // Row y's warp adds column y of the block.
+    const float total = warp_sum(s[threadIdx.x][threadIdx.y]);
+    const int col = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && col < 2 * head_dim) {
+        if (col < head_dim) {
+            if (grad_weight) grad_weight[col] = total;
+        } else if (grad_bias) {
+            grad_bias[col - head_dim] = total;
+        }
+    }
+}
+
+bool all16(std::initializer_list<const void *> ps, std::initializer_list<long long> bytes) {
+    for (const void *p : ps)
+        if ((uintptr_t)p & 15u) return false;
+    for (long long s : bytes)
+        if (s % 16) return false;
+    return true;
+}
+
+// heads_most heads to a group when that still leaves every SM its 2048 threads.
+HeadDeal deal_of(long long rows, int heads, int lanes, int heads_most, const DeviceInfo &dev) {
+    HeadDeal d;
+    d.heads_per = rows * ((heads + heads_most - 1) / heads_most) * lanes >= 2048ll * dev.sm_count
+                      ? heads_most : 1;
+    d.per_row = make_fast_div((uint32_t)((heads + d.heads_per - 1) / d.heads_per));
+    d.count = 0;
+    return d;
+}
+
+// F is called with the units' shape: pairs of a run, lanes of a head, units of a lane.
+template <typename F> cudaError_t by_shape(bool wide, int head_dim, F f) {
+    if (!wide) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>(),
+                        std::integral_constant<int, 4>());
+    constexpr std::integral_constant<int, 4> four{};
+    constexpr std::integral_constant<int, 1> one{};
+    if (head_dim <= 64) return f(four, std::integral_constant<int, 8>(), one);
+    if (head_dim <= 128) return f(four, std::integral_constant<int, 16>(), one);
+    return f(four, std::integral_constant<int, 32>(), one);
+}
+int lanes_of(bool wide, int head_dim) {
+    return !wide || head_dim > 128 ? 32 : head_dim > 64 ? 16 : 8;
+}
+
+template <typename F> cudaError_t by_type(int type, F f) {
+    switch (type) {
+    case kBF16: return f(static_cast<__nv_bfloat16 *>(nullptr));
+    case kF16: return f(static_cast<__half *>(nullptr));
+    default: return f(static_cast<float *>(nullptr));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int n_heads,
+                             int head_dim, const float *x, long long x_stride, int out_type,
+                             void *out, long long out_stride, const DeviceInfo &dev,
+                             cudaStream_t stream) {
+    const int ob = out_type == kF32 ? 4 : 2;
+    // A run of four 16-bit values is 8 bytes; the rows' 16-byte rule covers it.
+    const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
+                      all16({x, out}, {4 * x_stride, ob * out_stride});
+    HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kHeadsPer, dev);
+    // Launches of so many rows that their threads are counted in 31 bits.
+    const long long step = (0x7FFFFF00ll / lanes_of(wide, head_dim)) / deal.per_row.d;
+    for (long long t0 = 0; t0 < n; t0 += step) {
+        deal.count = (unsigned)((n - t0 < step ? n - t0 : step) * deal.per_row.d);
+        const cudaError_t err = by_type(out_type, [&](auto *type) {
+            using T = std::remove_pointer_t<decltype(type)>;
+            return by_shape(wide, head_dim, [&](auto N, auto G, auto U) {
+                const unsigned per = kThreads / G.value;
+                return launch_pdl(norm_rope_kernel<T, N.value, G.value, U.value>,
+                                  dim3((deal.count + per - 1) / per), dim3(kThreads), 0, stream, ax,
+                                  nv, deal, head_dim, x, x_stride, n_heads, static_cast<T *>(out),
+                                  out_stride, t0);
+            });
+        });
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const NormView &k_norm,
+                               const AppendNormArgs &a, const KvView &kv, const DeviceInfo &dev,
+                               cudaStream_t stream) {
+    const int qb = a.q_type == kF32 ? 4 : 2;
+    const bool q16 = a.h_q == 0 || all16({a.q, a.q_out}, {4 * a.q_stride, qb * a.q_out_stride});
+    const bool wide =
+        ax.rot % 8 == 0 && q16 && all16({a.k, a.v}, {4 * a.k_stride, 4 * a.v_stride});
+    const int d = kv.head_dim, heads = a.h_q + 2 * kv.n_heads;
+    HeadDeal deal = deal_of(a.n_tok, heads, lanes_of(wide, d), kHeadsPer, dev);
+    const long long step = (0x7FFFFF00ll / lanes_of(wide, d)) / deal.per_row.d;
+    for (long long t0 = 0; t0 < a.n_tok; t0 += step) {
+        deal.count = (unsigned)((a.n_tok - t0 < step ? a.n_tok - t0 : step) * deal.per_row.d);
+        auto by_cache = [&](auto DT) {
+            return by_type(a.q_type, [&](auto *type) {
+                using Q = std::remove_pointer_t<decltype(type)>;
+                return by_shape(wide, d, [&](auto N, auto G, auto U) {
+                    const unsigned per = kThreads / G.value;
+                    return launch_pdl(
+                        append_norm_kernel<DT.value, Q, N.value, G.value, U.value>,
+                        dim3((deal.count + per - 1) / per), dim3(kThreads), 0, stream, ax, q_norm,
+                        k_norm, a, kv, deal, (int)t0);
+                });
+            });
+        };
+        const cudaError_t err =
+            kv.dtype == kBF16 ? by_cache(std::integral_constant<int, kBF16>())
+            : kv.dtype == kF16 ? by_cache(std::integral_constant<int, kF16>())
+                               : by_cache(std::integral_constant<int, kF32>());
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n, int n_heads,
+                                  int head_dim, const float *x, long long x_stride,
+                                  const float *grad, long long grad_stride, float *grad_x,
+                                  long long grad_x_stride, float *grad_weight, float *grad_bias,
+                                  void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
+    const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
+                      all16({x, grad, grad_x}, {4 * x_stride, 4 * grad_stride, 4 * grad_x_stride});
+    HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kGradHeads, dev);
+    deal.count = (unsigned)n * deal.per_row.d;
+    const bool sums = grad_weight || grad_bias;
+    float *parts = sums ? static_cast<float *>(workspace) : nullptr;
+    unsigned blocks = 0;
+    const cudaError_t err = by_shape(wide, head_dim, [&](auto N, auto G, auto U) {
+        constexpr int per = kThreads / G.value;
+        blocks = (deal.count + per - 1) / per;
+        if (blocks > (unsigned)kGradBlocks) blocks = kGradBlocks;
+        const size_t smem = sums ? (size_t)per * 2 * head_dim * 4 : 0;  // at most 16 KiB
+        return launch_pdl(norm_rope_grad_kernel<N.value, G.value, U.value>, dim3(blocks),
+                          dim3(kThreads), smem, stream, ax, nv, deal, head_dim, x, x_stride, grad,
+                          grad_stride, n_heads, grad_x, grad_x_stride, parts);
+    });
+    if (err != cudaSuccess || !sums) return err;
+    return launch_pdl(grad_sums_kernel, dim3((2 * head_dim + 31) / 32), dim3(32, 32), 0, stream,
+                      static_cast<const float *>(parts), (int)blocks, head_dim, grad_weight,
+                      grad_bias);
+}
+
+}  // namespace wq

@@ -70,6 +70,72 @@ RopeArgs rope_args(int head_dim, int rot, unsigned flags, const int32_t *pos, co
             dev.status};
 }
 
+bool float_type(int type) { return type == WQ_F32 || type == WQ_BF16 || type == WQ_F16; }
+
+bool norm_ok(const wq_head_norm *norm, NormView &out) {
+    out = NormView{WQ_HEAD_NONE, 0.f, nullptr, nullptr};
+    if (!norm || norm->kind == WQ_HEAD_NONE) return true;
+    if (norm->kind != WQ_HEAD_RMS && norm->kind != WQ_HEAD_LAYER) return false;
+    if (!std::isfinite(norm->eps) || norm->eps < 0.f) return false;
+    if (!aligned(norm->weight, 4) || !aligned(norm->bias, 4)) return false;
+    out = NormView{norm->kind, norm->eps, norm->weight, norm->bias};
+    return true;
+}
+
+// The rotation's restrictions; fills the kernels' view of it, which pair by which axis and column.
+bool axes_ok(const wq_rope_axes *r, int head_dim, AxesView &out) {
+    out = AxesView{};
+    if (head_dim <= 0 || head_dim > kMaxHeadDim) return false;
+    if (!r || r->rot == 0) return true;
+    if (r->rot < 0 || r->rot > head_dim || r->rot % 2) return false;
+    const unsigned known = WQ_ROPE_INTERLEAVED | WQ_AXES_DEALT | WQ_AXES_RESTART;
+    if ((r->flags & ~known) || r->axes < 1 || r->axes > 4) return false;
+    if (r->table_rows <= 0 || r->table_pairs <= 0 || r->table_pairs > 128) return false;
+    if (!r->pos || !r->table || !aligned(r->table, 16) || !aligned(r->pos, 4)) return false;
+    if (r->axes > 1 && (r->pos_stride < 0 || r->pos_stride > INT64_MAX / 64)) return false;
+    const int half = r->rot / 2;
+    long long sum = 0;
+    for (int a = 0; a < r->axes; ++a) {
+        if (r->pairs[a] < 0 || r->pairs[a] > half) return false;
+        sum += r->pairs[a];
+        if ((r->flags & WQ_AXES_DEALT) && a > 0 && r->pairs[a] > 0 &&
+            (r->pairs[a] - 1) * r->axes + a >= half)
+            return false;
+        if (r->pairs[a] > 0) out.used |= 1u << a;
+    }
+    if (sum != half) return false;
+    int seen[4] = {0, 0, 0, 0};
+    bool plain = r->table_pairs % 2 == 0;
+    for (int i = 0, axis = 0, left = r->pairs[0]; i < half; ++i) {
+        if (r->flags & WQ_AXES_DEALT) {
+            axis = i / r->axes < r->pairs[i % r->axes] ? i % r->axes : 0;
+        } else {
+            while (left == 0) left = r->pairs[++axis];
+            --left;
+        }
+        const int col = r->flags & WQ_AXES_RESTART ? seen[axis]++ : i;
+        if (col >= r->table_pairs) return false;
+        out.code[i] = (uint16_t)(axis << 8 | col);
+        plain = plain && axis == 0 && col == i;
+    }
+    out.rot = r->rot;
+    out.flags = r->flags & WQ_ROPE_INTERLEAVED;
+    out.axes = r->axes;
+    out.table_rows = r->table_rows;
+    out.table_pairs = r->table_pairs;
+    out.straight = plain;
+    out.pos = r->pos;
+    out.pos_stride = r->pos_stride;
+    out.table = reinterpret_cast<const float2 *>(r->table);
+    return true;
+}
+
+// Rows of n_heads heads of a 16- or 32-bit type at x + t * stride.
+bool typed_rows_ok(const void *x, int type, int64_t stride, int n_heads, int head_dim) {
+    return x && aligned(x, element_bytes(type)) && stride >= (int64_t)n_heads * head_dim &&
+           stride <= INT64_MAX / 64 / 0x7FFFFFFF;
+}
+
 int cut(int n, long long to) { return to < n ? (int)to : n; }
 
 }  // namespace
@@ -261,6 +327,217 @@ wq_status wq_kv_evict(const wq_kv_cache *cache, int n_seq, const int32_t *page_t
     a.workspace = workspace;
     a.status = dev.status;
     return cuda_status(launch_kv_evict(a, kv, dev, (cudaStream_t)stream));
+}
+
+wq_status wq_norm_rope(int n, int n_heads, int head_dim, const wq_head_norm *norm,
+                       const wq_rope_axes *rope, const float *x, int64_t x_stride, int out_type,
+                       void *out, int64_t out_stride, wq_stream_t stream) {
+    NormView nv;
+    AxesView ax;
+    if (n <= 0 || n_heads <= 0 || !norm_ok(norm, nv) || !axes_ok(rope, head_dim, ax))
+        return WQ_ERR_INVALID_ARG;
+    if (!float_type(out_type) || !rows_ok(x, x_stride, n_heads, head_dim) ||
+        !typed_rows_ok(out, out_type, out_stride, n_heads, head_dim))
+        return WQ_ERR_INVALID_ARG;
+    if (out == x && (out_stride != x_stride || out_type != WQ_F32)) return WQ_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    ax.status = dev.status;
+    return cuda_status(launch_norm_rope(ax, nv, n, n_heads, head_dim, x, x_stride, out_type, out,
+                                        out_stride, dev, (cudaStream_t)stream));
+}
+
+size_t wq_norm_rope_grad_workspace_bytes(int n, int n_heads, int head_dim) {
+    if (n <= 0 || n_heads <= 0 || head_dim <= 0 || head_dim > kMaxHeadDim) return 0;
+    return (size_t)kGradBlocks * 2 * head_dim * sizeof(float);
+}
+
+wq_status wq_norm_rope_grad(int n, int n_heads, int head_dim, const wq_head_norm *norm,
+                            const wq_rope_axes *rope, const float *x, int64_t x_stride,
+                            const float *grad_out, int64_t grad_out_stride, float *grad_x,
+                            int64_t grad_x_stride, float *grad_weight, float *grad_bias,
+                            void *workspace, size_t workspace_bytes, wq_stream_t stream) {
+    NormView nv;
+    AxesView ax;
+    if (n <= 0 || n_heads <= 0 || !norm_ok(norm, nv) || !axes_ok(rope, head_dim, ax))
+        return WQ_ERR_INVALID_ARG;
+    if (!rows_ok(x, x_stride, n_heads, head_dim) ||
+        !rows_ok(grad_out, grad_out_stride, n_heads, head_dim) ||
+        !rows_ok(grad_x, grad_x_stride, n_heads, head_dim))
+        return WQ_ERR_INVALID_ARG;
+    if ((grad_x == x && grad_x_stride != x_stride) ||
+        (grad_x == grad_out && grad_x_stride != grad_out_stride))
+        return WQ_ERR_INVALID_ARG;
+    const bool sums = grad_weight || grad_bias;
+    if (sums && nv.kind == WQ_HEAD_NONE) return WQ_ERR_INVALID_ARG;
+    if (!aligned(grad_weight, 4) || !aligned(grad_bias, 4)) return WQ_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes,
+                      sums ? wq_norm_rope_grad_workspace_bytes(n, n_heads, head_dim) : 0))
+        return WQ_ERR_INVALID_ARG;
+    if ((long long)n * n_heads > 0x7FFFFFFF) return WQ_ERR_TOO_LARGE;
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    ax.status = dev.status;
+    return cuda_status(launch_norm_rope_grad(ax, nv, n, n_heads, head_dim, x, x_stride, grad_out,
+                                             grad_out_stride, grad_x, grad_x_stride, grad_weight,
+                                             grad_bias, workspace, dev, (cudaStream_t)stream));
+}
+
+wq_status wq_kv_append_norm(const wq_kv_cache *cache, int n_tok, int h_q,
+                            const wq_head_norm *q_norm, const wq_head_norm *k_norm,
+                            const wq_rope_axes *rope, const float *q, int64_t q_stride,
+                            const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                            int n_seq, const int32_t *seq, const int32_t *slot,
+                            const int32_t *page_table, int max_pages, int q_type, void *q_out,
+                            int64_t q_out_stride, float *acc, int32_t *slot_pos,
+                            int64_t acc_stride, wq_stream_t stream) {
+    KvView kv;
+    NormView qn, kn;
+    AxesView ax;
+    if (!view_of(cache, n_seq, page_table, max_pages, kv)) return WQ_ERR_INVALID_ARG;
+    if (n_tok <= 0 || h_q < 0 || !page_table || !slot || (!seq && n_seq < n_tok))
+        return WQ_ERR_INVALID_ARG;
+    if (!norm_ok(q_norm, qn) || !norm_ok(k_norm, kn) || !axes_ok(rope, kv.head_dim, ax))
+        return WQ_ERR_INVALID_ARG;
+    if (!rows_ok(k, k_stride, kv.n_heads, kv.head_dim) ||
+        !rows_ok(v, v_stride, kv.n_heads, kv.head_dim))
+        return WQ_ERR_INVALID_ARG;
+    if (h_q > 0 && (!float_type(q_type) || !rows_ok(q, q_stride, h_q, kv.head_dim) ||
+                    !typed_rows_ok(q_out, q_type, q_out_stride, h_q, kv.head_dim) ||
+                    (q_out == q && (q_out_stride != q_stride || q_type != WQ_F32))))
+        return WQ_ERR_INVALID_ARG;
+    if ((acc || slot_pos) && acc_stride < 1) return WQ_ERR_INVALID_ARG;
+    if (slot_pos && ax.rot == 0) return WQ_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    ax.status = dev.status;
+    AppendNormArgs a{};
+    a.n_tok = n_tok;
+    a.h_q = h_q;
+    a.n_seq = n_seq;
+    a.n_slots = max_pages * (int)kv.page_size.d;
+    if (acc || slot_pos) a.n_slots = cut(a.n_slots, acc_stride);
+    a.q_type = h_q > 0 ? q_type : WQ_F32;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.seq = seq;
+    a.slot = slot;
+    a.acc = acc;
+    a.slot_pos = slot_pos;
+    a.acc_stride = acc_stride;
+    return cuda_status(launch_append_norm(ax, qn, kn, a, kv, dev, (cudaStream_t)stream));
+}
+
+size_t wq_attn_tokens_workspace_bytes(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q,
+                                      int q_type) {
+    KvView kv;
+    if (!view_of(cache, n_seq, nullptr, 1, kv) || n_tok <= 0 || h_q <= 0 || h_q % kv.n_heads ||
+        !float_type(q_type) || (long long)n_tok * h_q > kMaxSlots)
+        return 0;
+    return tokens_workspace_bytes(kv, n_seq, n_tok, h_q, q_type);
+}
+
+wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q, float scale,
+                         const wq_attn_form *form, int q_type, const void *q, int64_t q_stride,
+                         const int32_t *starts, const int32_t *page_table, int max_pages,
+                         const int32_t *lens, int out_type, void *out, int64_t out_stride,
+                         float *lse, void *workspace, size_t workspace_bytes,
+                         wq_stream_t stream) {
+    KvView kv;
+    if (!view_of(cache, n_seq, page_table, max_pages, kv)) return WQ_ERR_INVALID_ARG;
+    if (n_tok <= 0 || h_q <= 0 || h_q % kv.n_heads || !std::isfinite(scale) ||
+        (long long)n_tok * h_q > kMaxSlots)
+        return WQ_ERR_INVALID_ARG;
+    if (!float_type(q_type) || (out_type != q_type && out_type != WQ_F32))
+        return WQ_ERR_INVALID_ARG;
+    if (!starts || !page_table || !lens) return WQ_ERR_INVALID_ARG;
+    if (!typed_rows_ok(q, q_type, q_stride, h_q, kv.head_dim) ||
+        !typed_rows_ok(out, out_type, out_stride, h_q, kv.head_dim))
+        return WQ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || q_stride * element_bytes(q_type) % 16 ||
+        out_stride * element_bytes(out_type) % 16)
+        return WQ_ERR_INVALID_ARG;
+    wq_attn_form f{};
+    if (form) f = *form;
+    if (!std::isfinite(f.softcap) || f.softcap < 0.f || f.window < 0) return WQ_ERR_INVALID_ARG;
+    if ((f.tree && (f.prefix || f.tree_stride < 1)) || (f.pos && !f.tree))
+        return WQ_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes,
+                      tokens_workspace_bytes(kv, n_seq, n_tok, h_q, q_type)))
+        return WQ_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    TokensArgs a{};
+    a.n_seq = n_seq;
+    a.n_tok = n_tok;
+    a.h_q = h_q;
+    a.n_slots = max_pages * (int)kv.page_size.d;
+    a.group = make_fast_div((uint32_t)(h_q / kv.n_heads));
+    a.scale = scale;
+    a.softcap = f.softcap;
+    a.window = f.window;
+    a.slopes = f.slopes;
+    a.first = f.first;
+    a.prefix = f.prefix;
+    a.pos = f.pos;
+    a.tree = f.tree;
+    a.tree_stride = f.tree_stride;
+    a.q_type = q_type;
+    a.out_type = out_type;
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.starts = starts;
+    a.lens = lens;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status = dev.status;
+    a.wait_limit = wait_limit();
+    return cuda_status(launch_attn_tokens(a, kv, dev, (cudaStream_t)stream));
+}
+
+wq_status wq_kv_accept(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,
+                       const int32_t *page_table, int max_pages, const int32_t *starts,
+                       const int32_t *parent, const int32_t *tokens, const int32_t *choice,
+                       const int32_t *lens, int32_t *path, int32_t *accepted, int32_t *next,
+                       int32_t *lens_out, wq_stream_t stream) {
+    if (!caches || n_caches <= 0 || n_tok <= 0) return WQ_ERR_INVALID_ARG;
+    if (!page_table || !starts || !parent || !tokens || !choice || !lens || !path || !accepted ||
+        !next || !lens_out || lens_out == lens)
+        return WQ_ERR_INVALID_ARG;
+    KvView kv, other;
+    for (int i = 0; i < n_caches; ++i) {
+        if (!view_of(&caches[i], n_seq, page_table, max_pages, i ? other : kv))
+            return WQ_ERR_INVALID_ARG;
+        const wq_kv_cache &c = caches[i], &f = caches[0];
+        if (c.dtype != f.dtype || c.n_pages != f.n_pages || c.page_size != f.page_size ||
+            c.n_heads != f.n_heads || c.head_dim != f.head_dim ||
+            c.page_stride != f.page_stride || c.head_stride != f.head_stride ||
+            c.token_stride != f.token_stride)
+            return WQ_ERR_INVALID_ARG;
+    }
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    AcceptArgs a{n_seq, n_tok, max_pages * (int)kv.page_size.d, starts, parent, tokens, choice,
+                 lens, path, accepted, next, lens_out, dev.status};
+    for (int c0 = 0; c0 < n_caches; c0 += kAcceptCaches) {
+        AcceptPools pools{};
+        pools.count = n_caches - c0 < kAcceptCaches ? n_caches - c0 : kAcceptCaches;
+        for (int i = 0; i < pools.count; ++i) {
+            pools.k[i] = static_cast<char *>(caches[c0 + i].k);
+            pools.v[i] = static_cast<char *>(caches[c0 + i].v);
+        }
+        const cudaError_t err = launch_kv_accept(a, kv, pools, c0 == 0, (cudaStream_t)stream);
+        if (err != cudaSuccess) return WQ_ERR_CUDA;
+    }
+    return WQ_OK;
 }
 
 }  // extern "C"

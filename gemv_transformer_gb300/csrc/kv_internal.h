@@ -56,6 +56,94 @@ struct EvictArgs {
     unsigned *status;
 };
 
+// A norm of heads as the kernels see it.
+struct NormView {
+    int kind;  // WQ_HEAD_*
+    float eps;
+    const float *weight, *bias;
+};
+
+// Rotary positions on several axes: pair i by column code[i] & 255 at the position on axis
+// code[i] >> 8.
+struct AxesView {
+    int rot;
+    unsigned flags;  // WQ_ROPE_INTERLEAVED
+    int axes;        // 0 where rot is 0
+    unsigned used;   // bit a: axis a has pairs
+    int table_rows, table_pairs;
+    bool straight;   // pair i by column i on axis 0, columns in 16-byte runs
+    const int32_t *pos;
+    long long pos_stride;
+    const float2 *table;
+    unsigned *status;
+    uint16_t code[128];
+};
+
+struct AppendNormArgs {
+    int n_tok, h_q, n_seq, n_slots, q_type;
+    const float *q, *k, *v;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    void *q_out;
+    const int32_t *seq, *slot;
+    float *acc;
+    int32_t *slot_pos;
+    long long acc_stride;
+};
+
+constexpr int kGradBlocks = 608;  // four on each of 152 SMs
+
+struct TokensArgs {
+    int n_seq, n_tok, h_q, n_slots;  // n_slots: max_pages * page_size
+    FastDiv group;                   // query heads per kv head
+    float scale, softcap;
+    int window;
+    const float *slopes;
+    const int32_t *first, *prefix, *pos;
+    const uint32_t *tree;
+    long long tree_stride;
+    int q_type, out_type;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;  // in elements
+    const int32_t *starts, *lens;
+    float *lse;
+    void *workspace;
+    unsigned *status;
+    unsigned long long wait_limit;
+};
+
+struct AcceptArgs {
+    int n_seq, n_tok, n_slots;
+    const int32_t *starts, *parent, *tokens, *choice, *lens;
+    int32_t *path, *accepted, *next, *lens_out;
+    unsigned *status;
+};
+// The pools of up to kAcceptCaches layers; the rest of their description is the first's.
+constexpr int kAcceptCaches = 48;
+struct AcceptPools {
+    int count;
+    char *k[kAcceptCaches], *v[kAcceptCaches];
+};
+
+cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int n_heads,
+                             int head_dim, const float *x, long long x_stride, int out_type,
+                             void *out, long long out_stride, const DeviceInfo &dev,
+                             cudaStream_t stream);
+cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const NormView &k_norm,
+                               const AppendNormArgs &a, const KvView &kv, const DeviceInfo &dev,
+                               cudaStream_t stream);
+// workspace: kGradBlocks * 2 * head_dim floats where a sum is wanted.
+cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n, int n_heads,
+                                  int head_dim, const float *x, long long x_stride,
+                                  const float *grad, long long grad_stride, float *grad_x,
+                                  long long grad_x_stride, float *grad_weight, float *grad_bias,
+                                  void *workspace, const DeviceInfo &dev, cudaStream_t stream);
+size_t tokens_workspace_bytes(const KvView &kv, int n_seq, int n_tok, int h_q, int q_type);
+cudaError_t launch_attn_tokens(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
+                               cudaStream_t stream);
+cudaError_t launch_kv_accept(const AcceptArgs &a, const KvView &kv, const AcceptPools &pools,
+                             bool write_path, cudaStream_t stream);
+
 cudaError_t launch_rope_table(int rows, int rot, double base, const wq_rope_scaling &sc,
                               float *table, const DeviceInfo &dev, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &r, const float *x, long long x_stride, int n, int n_heads,

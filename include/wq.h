@@ -515,6 +515,190 @@ WQ_API wq_status wq_kv_evict(const wq_kv_cache *cache, int n_seq, const int32_t 
 WQ_API size_t wq_kv_evict_workspace_bytes(const wq_kv_cache *cache, int n_seq, int max_pages,
                                           int keep);
 
+/* ---------------------------------------------- several new tokens per sequence --
+ *
+ * The same part of a layer for a prompt, a piece of one, or a tree of drafted tokens: norms
+ * of the heads and rotary positions on several axes in one pass, attention of a sequence's
+ * new tokens over its pages, and what follows the verification of a draft.
+ */
+
+/* A norm of each head's head_dim values x:  y = w (x - mu) / sqrt(mean((x - mu)^2) + eps) + b. */
+enum {
+    WQ_HEAD_NONE = 0,  /* y = x; the other fields are not read */
+    WQ_HEAD_RMS = 1,   /* mu = 0 */
+    WQ_HEAD_LAYER = 2  /* mu = mean(x) */
+};
+typedef struct {
+    int32_t kind;
+    float eps;           /* >= 0, finite */
+    const float *weight; /* device f32 [head_dim], 4-byte aligned; NULL: ones */
+    const float *bias;   /* the same; NULL: zeros */
+} wq_head_norm;
+
+/* Rotary positions on 1 to 4 axes (time, height, width).  Pair i < rot/2 (WQ_ROPE_INTERLEAVED:
+ * dims 2i and 2i+1, else i and i + rot/2) is turned by the angle of column col(i) at the
+ * token's position on axis(i):
+ *   runs (no flag)  the first pairs[0] pairs on axis 0, the next pairs[1] on axis 1, ...
+ *   WQ_AXES_DEALT   axis(i) = i % axes while i / axes < pairs[i % axes], else 0
+ * pairs' sum is rot / 2; dealt, axes - 1 of them fit: (pairs[a] - 1) axes + a < rot / 2 for a > 0.
+ *   col(i) = i, or with WQ_AXES_RESTART the number of pairs of the same axis before i. */
+enum {
+    WQ_AXES_DEALT = 4u,
+    WQ_AXES_RESTART = 8u
+};
+typedef struct {
+    int32_t rot;        /* 0: no rotation, the other fields are not read */
+    uint32_t flags;     /* WQ_ROPE_INTERLEAVED, WQ_AXES_DEALT, WQ_AXES_RESTART */
+    int32_t axes;
+    int32_t pairs[4];   /* of the first `axes` axes, each >= 0 */
+    int32_t table_rows; /* positions of the table */
+    int32_t table_pairs; /* columns of the table, above every col(i) */
+    int32_t reserved;   /* 0 */
+    const int32_t *pos; /* token t's position on axis a: pos[a * pos_stride + t] */
+    int64_t pos_stride;
+    const float *table; /* [table_rows][table_pairs][2], wq_rope_table's of rot = 2 table_pairs */
+} wq_rope_axes;
+
+/*
+ * out = R(norm(x)) for each of n_heads heads of n rows: the norm, then the rotation of its
+ * first rope->rot values, in one pass; one rounding where out_type (WQ_F32, WQ_BF16, WQ_F16)
+ * is a 16-bit type.  norm or rope NULL: none.
+ * x: f32; out: out_type; rows' strides in elements, from n_heads * head_dim to 2^26; any
+ * address aligned to the element is taken, 16-byte multiples and head_dim and rot multiples of
+ * 8 are faster.  out may equal x with the same stride and WQ_F32.
+ * A position outside [0, table_rows) on an axis that has pairs leaves its row of out
+ * unwritten and records WQ_ERR_BAD_INDEX in the device status.
+ * Errors: WQ_ERR_INVALID_ARG for n, n_heads <= 0, head_dim <= 0 or above 256, rot < 0, odd or
+ * above head_dim, axes outside 1..4, pairs as above, columns beyond table_pairs, table_pairs
+ * above 128, null pos or table, a table not 16-byte aligned, table_rows <= 0, unknown flags,
+ * kinds or types, an eps below 0 or not finite, misaligned weights, null or misaligned x or
+ * out, strides too small, x == out with another stride or type. */
+WQ_API wq_status wq_norm_rope(int n, int n_heads, int head_dim, const wq_head_norm *norm,
+                              const wq_rope_axes *rope, const float *x, int64_t x_stride,
+                              int out_type, void *out, int64_t out_stride, wq_stream_t stream);
+
+/*
+ * The gradient of wq_norm_rope (WQ_F32): with g = R^T grad_out, h = (x - mu) r, r = 1 / sqrt(...),
+ * u = w g and means over a head's values,
+ *   grad_x = r (u - h mean(u h) - [WQ_HEAD_LAYER] mean(u)),   no norm: grad_x = g
+ *   grad_weight = sum g h,  grad_bias = sum g  over all rows and heads (f32 [head_dim], each
+ * may be NULL; they are set, not added to).
+ * grad_x may equal grad_out or x with the same stride, else nothing overlaps.  A row with a
+ * position out of range has its grad_x left unwritten and adds nothing to the sums.
+ * workspace: at least wq_norm_rope_grad_workspace_bytes(n, n_heads, head_dim) bytes, 256-byte
+ * aligned; it is overwritten.  NULL is taken where neither sum is wanted.
+ * Errors: as wq_norm_rope; WQ_ERR_INVALID_ARG for a sum without a norm and for a missing,
+ * misaligned or small workspace; WQ_ERR_TOO_LARGE for n * n_heads above 2^31 - 1. */
+WQ_API wq_status wq_norm_rope_grad(int n, int n_heads, int head_dim, const wq_head_norm *norm,
+                                   const wq_rope_axes *rope, const float *x, int64_t x_stride,
+                                   const float *grad_out, int64_t grad_out_stride, float *grad_x,
+                                   int64_t grad_x_stride, float *grad_weight, float *grad_bias,
+                                   void *workspace, size_t workspace_bytes, wq_stream_t stream);
+
+/* Workspace bytes of wq_norm_rope_grad; 0 for invalid arguments. */
+WQ_API size_t wq_norm_rope_grad_workspace_bytes(int n, int n_heads, int head_dim);
+
+/*
+ * wq_kv_append with norms and several axes: q_out[t] = R(q_norm(q[t])) in q_type (WQ_F32, WQ_BF16
+ * or WQ_F16), and into slot slot[t] of sequence seq[t] R(k_norm(k[t])) and v[t], each rounded
+ * once to the cache's type.  q_norm, k_norm, rope may be NULL.  slot_pos is set to the
+ * position on axis 0 (it needs a rope with rot > 0).
+ * q_out may equal q with the same stride and WQ_F32.  All else as wq_kv_append. */
+WQ_API wq_status wq_kv_append_norm(const wq_kv_cache *cache, int n_tok, int h_q,
+                                   const wq_head_norm *q_norm, const wq_head_norm *k_norm,
+                                   const wq_rope_axes *rope, const float *q, int64_t q_stride,
+                                   const float *k, int64_t k_stride, const float *v,
+                                   int64_t v_stride, int n_seq, const int32_t *seq,
+                                   const int32_t *slot, const int32_t *page_table, int max_pages,
+                                   int q_type, void *q_out, int64_t q_out_stride, float *acc,
+                                   int32_t *slot_pos, int64_t acc_stride, wq_stream_t stream);
+
+/* What wq_attn_tokens' tokens see and how their scores are formed; all zero: causal. */
+typedef struct {
+    float softcap;         /* c > 0: scores become c tanh(score / c); 0: none */
+    int32_t window;        /* W > 0: only slots less than W positions before the token's */
+    const float *slopes;   /* f32 [h_q]: slope[h] (pos(slot) - pos(token)) is added to the scores
+                              (after the cap); NULL: none */
+    const int32_t *first;  /* int32 [n_tok]: only slots >= first[t] (packed documents); or NULL */
+    const int32_t *prefix; /* int32 [n_seq]: the live slots below prefix[s] are seen by all of the
+                              sequence's tokens (subject to first and window); or NULL */
+    const uint32_t *tree;  /* [n_tok][tree_stride]: bit b (word b / 32, bit b % 32) of token t's row:
+                              t sees its sequence's b-th new token; or NULL */
+    int64_t tree_stride;   /* words, enough for the most new tokens that a sequence has */
+    const int32_t *pos;    /* int32 [n_tok], only with tree: the new tokens' positions; or NULL */
+} wq_attn_form;
+
+/*
+ * Attention of the new tokens of n_seq sequences over their live slots.  Sequence s's new
+ * tokens are the rows starts[s] .. starts[s+1] - 1 of q; their k and v are in its last
+ * T = starts[s+1] - starts[s] live slots (wq_kv_append_norm put them there): token j's
+ * in slot B + j with B = lens[s] - T.  Token j sees
+ *   no tree  the slots below max(B + j + 1, min(prefix[s], lens[s])),
+ *   tree     the slots below B, and B + b for each bit b < T of its row (its own is a bit too),
+ * of them those >= first[t], and with a window those with pos(token) - pos(slot) < W.
+ * pos(slot j) = j, and of a new token B + j, or pos[t] where that is given.  Over what it sees
+ *   x = cap(scale q . k) + slope[h] (pos(slot) - pos(token)),  p = softmax(x),
+ *   out = sum p v,  lse = ln sum exp(x),
+ * for each of h_q query heads; query head h reads kv head h / (h_q / kv heads).
+ * A token that sees nothing has out 0 and lse -inf.  What a token does not see does not
+ * reach its results, whatever it holds.
+ * q: q_type (WQ_F32, WQ_BF16, WQ_F16), rows of h_q heads; out: out_type, q_type or WQ_F32;
+ * strides in elements.  lse: f32 [n_tok][h_q] or NULL.
+ * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products); 16-bit
+ * queries over a cache of their type with head_dim <= 128: tensor-core products, in which p is
+ * rounded to that type (2^-9 of it for bf16, 2^-12 for f16; p is at most 2^0 and f16 weights
+ * below 2^-24 are lost); all others as f32 queries.
+ * Rows of q at or beyond starts[n_seq] are not read and theirs of out not written.
+ * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not
+ * like that is left out, a length below T or above max_pages * page_size is cut to the slots
+ * that there are, and a page out of range that holds live slots leaves them out; each records
+ * WQ_ERR_BAD_INDEX in the device status.
+ * form (read on the host, not kept) NULL: causal, no cap.
+ * workspace: as wq_attn_paged's, of wq_attn_tokens_workspace_bytes(...) bytes.
+ * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, n_tok, h_q, max_pages <= 0, h_q
+ * not a multiple of the kv heads, a scale that is not finite, a softcap below 0 or not finite,
+ * window < 0, tree with prefix, tree_stride < 1, pos without tree, unknown types, null q, starts,
+ * page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
+ * or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
+ * missing, misaligned or small workspace. */
+WQ_API wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q,
+                                float scale, const wq_attn_form *form, int q_type, const void *q,
+                                int64_t q_stride, const int32_t *starts,
+                                const int32_t *page_table, int max_pages, const int32_t *lens,
+                                int out_type, void *out, int64_t out_stride, float *lse,
+                                void *workspace, size_t workspace_bytes, wq_stream_t stream);
+
+/* Workspace bytes of wq_attn_tokens; 0 for invalid arguments. */
+WQ_API size_t wq_attn_tokens_workspace_bytes(const wq_kv_cache *cache, int n_seq, int n_tok,
+                                             int h_q, int q_type);
+
+/*
+ * After the verification of drafted trees: keep each sequence's accepted path.
+ * Sequence s's new tokens are nodes 0 .. T-1 of a tree (rows starts[s] .. starts[s+1] - 1 of
+ * parent, tokens and choice; their slots as in wq_attn_tokens): node 0 is the root, the token
+ * that was known, and parent[c] < c the node that c was drafted after.  choice[c] is the token
+ * that the model chose after node c.  The path begins at the root and goes on, from node c,
+ * to the lowest child whose token is choice[c]; it ends where there is none.
+ *   path[starts[s] + i] = the path's i-th node, -1 beyond it (int32 [n_tok])
+ *   accepted[s] = the path's nodes (at least 1), next[s] = choice of its last node
+ *   lens_out[s] = B + accepted[s]
+ * and in each of n_caches caches (a model's layers, alike but for k and v; the array is read
+ * on the host) the k and v of the path's i-th node move from slot B + path[i] to B + i.  The
+ * slots behind them keep what they hold.
+ * A sequence without new tokens: accepted 0, next -1, lens_out = lens.  One whose starts or
+ * length are not as in wq_attn_tokens is treated like that, its path is left unwritten, and
+ * a node whose pages are out of range is not moved; both record WQ_ERR_BAD_INDEX.
+ * Sequences may not share pages that this call writes; nothing overlaps an output.
+ * Errors: WQ_ERR_INVALID_ARG for the caches' restrictions or caches that differ in more than k
+ * and v, n_caches <= 0, n_seq, n_tok, max_pages <= 0, max_pages * page_size above 2^30, a null
+ * argument, lens_out == lens. */
+WQ_API wq_status wq_kv_accept(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,
+                              const int32_t *page_table, int max_pages, const int32_t *starts,
+                              const int32_t *parent, const int32_t *tokens,
+                              const int32_t *choice, const int32_t *lens, int32_t *path,
+                              int32_t *accepted, int32_t *next, int32_t *lens_out,
+                              wq_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the current device's sticky
  * status word: WQ_OK, WQ_ERR_DEVICE_TIMEOUT, WQ_ERR_BAD_EXPERT or
  * WQ_ERR_BAD_INDEX (the first recorded since the last call); WQ_ERR_CUDA if the
