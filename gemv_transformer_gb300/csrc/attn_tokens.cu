@@ -479,14 +479,14 @@ cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int
 
 size_t tokens_workspace_bytes(const KvView &kv, int n_seq, int n_tok, int h_q, int q_type) {
     const int group = h_q / kv.n_heads;
-    int rt, kt, dp;
+    int rt, dp, grid = tok::kMaxGrid;
     if (tok::tokens_tc_takes(kv, q_type)) {
-        tok::tokens_tc_shape(n_seq, n_tok, group, q_type, kv.head_dim, rt, kt, dp);
+        tok::tokens_tc_shape(n_seq, n_tok, group, q_type, kv.head_dim, rt, dp, grid);
     } else {
         rt = 16 * tok::rows_per_thread(n_seq, n_tok, group);
         dp = tok::padded_dim(kv.head_dim);
     }
-    return tok::room_of(nullptr, n_seq, n_tok, group, rt, dp, tok::kMaxGrid).bytes;
+    return tok::room_of(nullptr, n_seq, n_tok, group, rt, dp, grid).bytes;
 }
 
 cudaError_t launch_attn_tokens(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,

@@ -36,6 +36,9 @@ __device__ __forceinline__ Seq seq_of(const TokensArgs &a, int s, bool &bad) {
     return q;
 }
 
+// Positions are held where the differences of two, or of one and a slot, fit 32 bits.
+__device__ __forceinline__ int near(int pos) { return min(max(pos, 1 - (1 << 30)), 1 << 30); }
+
 // The slots that token j of a sequence sees: [lo, hi), and with a tree, of the new tokens' slots
 // [own, own_end) those whose bit is set.
 struct See {
@@ -48,9 +51,8 @@ __device__ __forceinline__ See see_of(const TokensArgs &a, const Seq &q, int s, 
     See v{};
     const int t = q.t0 + j;
     v.first = a.first ? max(a.first[t], 0) : 0;
-    v.pos = a.pos ? a.pos[t] : q.base + j;
+    v.pos = a.pos ? near(a.pos[t]) : q.base + j;
     v.lo = v.first;
-    // 64 bits: positions are any int32.
     if (a.window > 0)
         v.lo = (int)max((long long)v.lo, min((long long)v.pos - a.window + 1, (long long)q.len));
     if (a.tree) {
@@ -86,7 +88,7 @@ __device__ __forceinline__ uint32_t seen32(const TokensArgs &a, const See &v, in
         if (v.own_pos) {
             for (uint32_t left = own; left; left &= left - 1) {
                 const int i = __ffs(left) - 1;
-                if ((long long)v.pos - v.own_pos[b0 + i] >= a.window) own &= ~(1u << i);
+                if (v.pos - near(v.own_pos[b0 + i]) >= a.window) own &= ~(1u << i);
             }
         }
         m |= own;
@@ -95,7 +97,7 @@ __device__ __forceinline__ uint32_t seen32(const TokensArgs &a, const See &v, in
 }
 // Position of slot j, for the distance bias.
 __device__ __forceinline__ int slot_pos(const TokensArgs &a, const Seq &q, int j) {
-    return a.pos && j >= q.base && j < q.len ? a.pos[q.t0 + j - q.base] : j;
+    return a.pos && j >= q.base && j < q.len ? near(a.pos[q.t0 + j - q.base]) : j;
 }
 
 // --------------------------------------------------------------------- workspace --
@@ -206,8 +208,8 @@ cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int
 
 // The tensor-core kernels (attn_tokens_tc.cu).
 bool tokens_tc_takes(const KvView &kv, int q_type);
-void tokens_tc_shape(int n_seq, int n_tok, int group, int q_type, int head_dim, int &rt, int &kt,
-                     int &dp);
+void tokens_tc_shape(int n_seq, int n_tok, int group, int q_type, int head_dim, int &rt, int &dp,
+                     int &grid);
 cudaError_t launch_tokens_tc(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                              cudaStream_t stream);
 

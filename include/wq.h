@@ -624,8 +624,9 @@ typedef struct {
                               sequence's tokens (subject to first and window); or NULL */
     const uint32_t *tree;  /* [n_tok][tree_stride]: bit b (word b / 32, bit b % 32) of token t's row:
                               t sees its sequence's b-th new token; or NULL */
-    int64_t tree_stride;   /* words, enough for the most new tokens that a sequence has */
-    const int32_t *pos;    /* int32 [n_tok], only with tree: the new tokens' positions; or NULL */
+    int64_t tree_stride;   /* words; what lies beyond a row's words is not seen */
+    const int32_t *pos;    /* int32 [n_tok], only with tree: the new tokens' positions (held within
+                              +-2^30); or NULL */
 } wq_attn_form;
 
 /*
