@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                     lo_most = max(lo_most, v.lo);
                     hi_least = min(hi_least, v.hi);
                 }
-                Tile t{s, row0, 0, 0, lo_most, hi_least, 0, 0};
+                Tile t{s, row0, 0, 0, lo_most, hi_least, 0, 0, q};
                 if (hi > lo) t.k0 = lo / kt, t.k1 = (hi + kt - 1) / kt;
                 room.tiles[first + r] = t;
             }
@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(256)
         if (q.head != p.head || q.tile != p.tile || q.off == 0) break;
     }
     const Tile tile = room.tiles[p.tile];
-    bool bad = false;
-    const Seq q = seq_of(a, tile.seq, bad);
+    const Seq q = tile.q;
     const int rows = min(rt, q.count * group - tile.row0);
     const TypedOut out{a.out, a.out_type};
     // The parts: the second of CTA b - 1, then the first of CTAs b, b + 1, ...
@@ -221,13 +220,12 @@ __global__ void __launch_bounds__(256)
     pdl_enter();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.group.d;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, RT, DP, grid);
-    Walk walk(room, blockIdx.x, room.plan[grid].pad);
+    Walk walk(room, blockIdx.x);
     const TypedOut out{a.out, a.out_type};
     const int d = kv.head_dim;
     Stretch st;
     while (walk.next(st)) {
-        bool bad = false;
-        const Seq q = seq_of(a, st.tile.seq, bad);
+        const Seq q = st.tile.q;
         const int rows = min(RT, q.count * group - st.tile.row0);
         __syncthreads();
         for (int i = threadIdx.x; i < RT * (DP / 8); i += 256) {

@@ -102,14 +102,16 @@ __device__ __forceinline__ int slot_pos(const TokensArgs &a, const Seq &q, int j
 
 // --------------------------------------------------------------------- workspace --
 
-struct Tile {
+struct __align__(16) Tile {
     int seq, row0;
     int k0, k1;        // key tiles
     int lo, hi;        // every row of the tile sees [lo, hi)
     int pad0, pad1;
+    Seq q;             // the sequence's
 };
 struct Begin {
-    int head, tile, off, pad;  // where a CTA's range starts: kv head, row tile, key tiles into it
+    int head, tile, off;  // where a CTA's range starts: kv head, row tile, key tiles into it
+    int tiles;            // row tiles of all sequences
 };
 struct Room {
     Begin *plan;         // [grid + 1]
@@ -153,9 +155,10 @@ struct Walk {
     const Room &room;
     Begin at, end;
     int tiles;
-    __device__ __forceinline__ Walk(const Room &r, int cta, int n_tiles) : room(r), tiles(n_tiles) {
+    __device__ __forceinline__ Walk(const Room &r, int cta) : room(r) {
         at = r.plan[cta];
         end = r.plan[cta + 1];
+        tiles = at.tiles;
     }
     __device__ __forceinline__ bool next(Stretch &s) {
         if (at.head > end.head || (at.head == end.head && at.tile > end.tile)) return false;

@@ -1,15 +1,16 @@
 // attn_tokens_tc.cu -- attention of several new tokens per sequence on the tcgen05 tensor cores.
 //
-// S = Q K^T and T = P V for 128 rows (new tokens x heads of a group) and a tile of KT slots, both
-// accumulated in tensor memory; between them two warpgroups of 128 threads, a thread to a row,
-// turn S into weights against a running maximum, and add the previous tile's T to an output in
-// registers: o = o 2^(m_old - m) + T.  So no sum on the tensor core is longer than one
-// tile (it truncates when it accumulates), and a rescale is part of an FMA that is needed
-// anyway.
+// S = Q K^T and P V for 128 rows (new tokens x heads of a group) and a tile of KT slots, both in
+// tensor memory; between them two warpgroups of 128 threads, a thread to a row, turn S into
+// weights p = 2^(S - m).
 //
-//   16-bit q    one product each; p is rounded to the cache's type, its sum is not.
+//   16-bit q    one product each; p is rounded to the cache's type, its sum is not.  The output
+//               stays in tensor memory: m is only raised, and the output scaled, when a row's
+//               maximum has outgrown it by more than 2^8, which after the first tiles is rare.
 //   f32 q       (bf16 caches) q and p as three bf16 terms, 24 bits, whose products are exact: three
-//               products each, the smallest terms first.
+//               products each, the smallest terms first.  The tensor core truncates when it
+//               accumulates, so P V of a tile, T, is added to an output in registers: o = o 2^(m_old -
+//               m) + T.
 //
 // PAIR: two row tiles, one to a warpgroup, share every k and v tile: prompts, where the products
 // bound it.  Otherwise one row tile, whose slot tiles the warpgroups take in turn and join at
@@ -22,6 +23,10 @@
 // A v that is not finite under a weight of 0 would reach rows that do not see it: where not all
 // rows see all of a tile the warpgroups look through its v first, take such slots out, and add
 // them to the rows that see them by FMA.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
 #include "attn_tokens.cuh"
 #include "tc_ptx.cuh"
 
@@ -67,19 +72,31 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kMisc, "the small arrays fit before the tiles");
 
-// A's rows in tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accum) {
+// Shared-memory descriptors by their low words (the address, and for MN-major the bytes between
+// 64-element chunks of the contiguous dimension); the high word, groups of eight rows 1024 bytes
+// apart in the 128-byte swizzle, is the same for all.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t chunk) {
+    return (addr >> 4) | (chunk >> 4) << 16;
+}
+// D += or = A B with A in shared memory, or (ts) in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accum) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\t"
+        "mov.b64 y, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accum), "n"(kDescHigh)
         : "memory");
 }
-// 64-column chunks of the contiguous dimension `chunk` bytes apart, groups of eight rows 1024.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t chunk) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(chunk >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accum), "n"(kDescHigh)
+        : "memory");
 }
 template <int ET> __host__ __device__ constexpr uint32_t idesc_of(int N, bool b_mn) {
     return (1u << 4) | (ET == kBF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
@@ -208,16 +225,91 @@ struct Ctx {
 
 // -------------------------------------------------------------------- loader warps --
 
-// The k and v tiles of the CTA's range, one after another, by cp.async; a tile's barriers are
-// arrived at when the next one is under way and it has landed.  Slots beyond the live ones and
-// in pages out of range are zeros.
+// The page of slot j, asked for a tile ahead of its use; -2 for one that is not live.
+__device__ __forceinline__ int page_of(const KvView &kv, int seq, int j, int len) {
+    if (j >= len) return -2;
+    return kv.page_table[(long long)seq * kv.max_pages + kv.page_size.div((uint32_t)j)];
+}
+
+// The k and v tiles of the CTA's range, one after another, by TMA, one warp: where the pages are
+// whole groups of eight rows, boxes of the largest number of rows that divides a page and a tile.
+// What lies beyond the live slots of a page, or of a box that was not asked for, is whatever
+// memory holds: no row sees it, and look() takes it out.
 template <typename S>
-__device__ void load_tiles(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
+__device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensorMap *k_map,
+                           const CUtensorMap *v_map, int box, const Room &room, const Ctx &c) {
+    const int lane = threadIdx.x & 31, boxes = S::KT / box, from = lane * box;
+    const bool mine = lane < boxes;
+    Walk walk(room, blockIdx.x);
+    Stretch st;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(st)) {
+        const int len = mine ? st.tile.q.len : 0, seq = st.tile.seq;
+        int j = st.k0 * S::KT + from, page = page_of(kv, seq, j, len);
+        for (int kt = st.k0; kt < st.k1; ++kt, ++n, j += S::KT) {
+            const int next = kt + 1 < st.k1 ? page_of(kv, seq, j + S::KT, len) : -2;
+            const bool live = (unsigned)page < (unsigned)kv.n_pages;
+            const uint32_t lost = __ballot_sync(0xFFFFFFFFu, !live && page != -2);
+            const uint32_t bytes =
+                __popc(__ballot_sync(0xFFFFFFFFu, live)) * box * 128 * (S::DP / 64);
+            const int row = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t i = 2 * n + v, slot = i % S::kSlots;
+                if (!c.warp_wait(&c.sh->empty[slot], (i / S::kSlots & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (v) {
+                        for (int g = 0; g < S::KT / 32; ++g) {
+                            uint32_t none = 0;
+                            for (uint32_t left = lost; left; left &= left - 1) {
+                                const int first = (__ffs(left) - 1) * box - 32 * g;
+                                none |= below(first + box) & ~below(first);
+                            }
+                            c.sh->none[slot][g] = none;
+                        }
+                        if (lost) record_status(a.status, kStBadIndex);
+                    }
+                    mbar_arrive_expect_tx(&c.sh->full[slot], bytes);
+                }
+                __syncwarp();
+                if (live) {
+                    const uint32_t to = c.ring + slot * S::kSlot + from * 128;
+#pragma unroll
+                    for (int h = 0; h < S::DP / 64; ++h)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx"
+                            "::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                                to + h * (S::KT * 128)),
+                            "l"(reinterpret_cast<uint64_t>(v ? v_map : k_map)), "r"(64 * h),
+                            "r"(row), "r"(st.head), "r"(page), "r"(smem_addr(&c.sh->full[slot]))
+                            : "memory");
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            page = next;
+        }
+    }
+    // The last copies have landed before shared memory is given up, after an abort too.
+    const uint32_t asked = 2 * n, back = asked < (uint32_t)S::kSlots ? asked : S::kSlots;
+    for (uint32_t i = asked - back; i < asked; ++i)
+        mbar_wait(&c.sh->full[i % S::kSlots], i / S::kSlots & 1, kDrainPolls);
+}
+
+// The same by cp.async and three warps for pages of any size; a tile's barriers are arrived at
+// when the next one is under way and it has landed.  Slots beyond the live ones and in pages out
+// of range are zeros.
+template <typename S>
+__device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
     constexpr int kLanes = S::DP / 8;         // 16-byte chunks, a lane each, of a row
     constexpr int kRows = 32 / kLanes;        // rows of a warp's copy
     constexpr int kGroups = S::KT / 32;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 9;
-    Walk walk(room, blockIdx.x, room.plan[kGrid].pad);
+    Walk walk(room, blockIdx.x);
     Stretch st;
     uint32_t n = 0;         // tiles asked for
     uint32_t landed = 0;    // tiles whose barriers were arrived at
@@ -231,42 +323,41 @@ __device__ void load_tiles(const TokensArgs &a, const KvView &kv, const Room &ro
     const int chunk = lane % kLanes;
     const bool in_dim = chunk * 8 < kv.head_dim;
     while (ok && walk.next(st)) {
-        bool bad = false;
-        const Seq q = seq_of(a, st.tile.seq, bad);
-        for (int kt = st.k0; kt < st.k1; ++kt, ++n) {
-            // This lane's rows of the tile: lane + 32 g.
-            long long at[kGroups];
+        const int len = st.tile.q.len, seq = st.tile.seq;
+        int page[kGroups];  // of this lane's rows: lane + 32 g
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int j = kt * S::KT + 32 * g + lane;
-                at[g] = -1;
-                if (j < q.len) {
-                    at[g] = kv.row(st.tile.seq, st.head, j);
-                    if (at[g] < 0) at[g] = -2;
-                }
-            }
+        for (int g = 0; g < kGroups; ++g)
+            page[g] = page_of(kv, seq, st.k0 * S::KT + 32 * g + lane, len);
+        for (int kt = st.k0; kt < st.k1; ++kt, ++n) {
+            int next[kGroups];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                next[g] = kt + 1 < st.k1
+                              ? page_of(kv, seq, (kt + 1) * S::KT + 32 * g + lane, len) : -2;
             const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
             const uint32_t kp = (2 * n / S::kSlots & 1) ^ 1, vp = ((2 * n + 1) / S::kSlots & 1) ^ 1;
             if (!c.warp_wait(&c.sh->empty[ks], kp) || !c.warp_wait(&c.sh->empty[vs], vp)) {
                 ok = false;
                 break;
             }
-            if (warp == 0) {
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const uint32_t none = __ballot_sync(0xFFFFFFFFu, at[g] == -2);
-                    if (lane == 0) {
-                        c.sh->none[vs][g] = none;
-                        if (none) record_status(a.status, kStBadIndex);
-                    }
-                }
-            }
             const uint32_t k_to = c.ring + ks * S::kSlot, v_to = c.ring + vs * S::kSlot;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
+                const int j = kt * S::KT + 32 * g + lane;
+                const bool there = (unsigned)page[g] < (unsigned)kv.n_pages;
+                const uint32_t none = __ballot_sync(0xFFFFFFFFu, !there && page[g] != -2);
+                if (warp == 0 && lane == 0) {
+                    c.sh->none[vs][g] = none;
+                    if (none) record_status(a.status, kStBadIndex);
+                }
+                const int in = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
+                const long long at = there ? (long long)page[g] * kv.page_stride +
+                                                 (long long)st.head * kv.head_stride +
+                                                 (long long)in * kv.token_stride
+                                           : -1;
                 for (int i = warp; i < 32 / kRows; i += 3) {
                     const int r = i * kRows + lane / kLanes, row = 32 * g + r;
-                    const long long from = __shfl_sync(0xFFFFFFFFu, at[g], r);
+                    const long long from = __shfl_sync(0xFFFFFFFFu, at, r);
                     const bool live = from >= 0 && in_dim;
                     const long long src = live ? from + chunk * 16 : 0;
                     const uint32_t to = (chunk >> 3) * (S::KT * 128) + row * 128 +
@@ -274,6 +365,7 @@ __device__ void load_tiles(const TokensArgs &a, const KvView &kv, const Room &ro
                     cp16(k_to + to, kv.k + src, live);
                     cp16(v_to + to, kv.v + src, live);
                 }
+                page[g] = next[g];
             }
             cp_commit();
             if (n > landed) {
@@ -291,7 +383,7 @@ __device__ void load_tiles(const TokensArgs &a, const KvView &kv, const Room &ro
 template <typename S>
 __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx &c) {
     const uint32_t tmem = c.sh->tmem;
-    Walk walk(room, blockIdx.x, room.plan[kGrid].pad);
+    Walk walk(room, blockIdx.x);
     Stretch st;
     uint32_t base = 0;                 // tiles before this stretch
     uint32_t stretches = 0;
@@ -302,32 +394,33 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
         return c.wait(&c.sh->full[i % S::kSlots], i / S::kSlots & 1);
     };
     auto scores = [&](int wg, uint32_t tile) {  // S of a warpgroup from the tile's k
-        const uint32_t k = c.ring + 2 * tile % S::kSlots * S::kSlot;
+        const uint32_t k = desc_low(c.ring + 2 * tile % S::kSlots * S::kSlot, 16);
         uint32_t accum = 0;
 #pragma unroll
         for (int t = S::TERMS - 1; t >= 0; --t) {
-            const uint32_t q = c.stage + t * S::kQTerm + (S::PAIR ? wg * (128 * S::DP * 2) : 0);
+            const uint32_t q =
+                desc_low(c.stage + t * S::kQTerm + (S::PAIR ? wg * (128 * S::DP * 2) : 0), 16);
 #pragma unroll
             for (int h = 0; h < S::DP / 64; ++h)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    tc_mma(tmem + wg * 256 + kColS, smem_desc_sw128(q + h * S::kHalf + 32 * s),
-                           smem_desc_sw128(k + h * (S::KT * 128) + 32 * s), kId, accum);
+                    mma_ss(tmem + wg * 256 + kColS, q + (h * S::kHalf + 32 * s >> 4),
+                           k + (h * (S::KT * 128) + 32 * s >> 4), kId, accum);
                     accum = 1;
                 }
         }
         tc_commit(&c.sh->s_full[wg]);
     };
-    auto values = [&](int wg, uint32_t tile) {  // T of a warpgroup from the tile's v
-        const uint32_t v = c.ring + (2 * tile + 1) % S::kSlots * S::kSlot;
-        uint32_t accum = 0;
+    auto values = [&](int wg, uint32_t tile) {  // P V of a warpgroup from the tile's v
+        const uint32_t v =
+            desc_low(c.ring + (2 * tile + 1) % S::kSlots * S::kSlot, S::KT * 128);
+        uint32_t accum = S::TERMS == 1;  // on top of the output, which began as zeros
 #pragma unroll
         for (int t = S::TERMS - 1; t >= 0; --t) {
             const uint32_t p = tmem + wg * 256 + (t == 0 ? kColP0 : t == 1 ? kColP1 : kColP2);
 #pragma unroll
             for (int s = 0; s < S::KT / 16; ++s) {
-                tc_mma_ts(tmem + wg * 256 + kColT, p + 8 * s,
-                          smem_desc_mn(v + 2048 * s, S::KT * 128), vId, accum);
+                mma_ts(tmem + wg * 256 + kColT, p + 8 * s, v + (2048 * s >> 4), vId, accum);
                 accum = 1;
             }
         }
@@ -429,70 +522,451 @@ __device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, co
     }
 }
 
-template <typename S>
-__device__ void softmax_rows(const TokensArgs &a, const KvView &kv, const Room &room,
-                             const Ctx &c) {
-    constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
-    constexpr bool kFast = S::TERMS == 1;
-    Shared *const sh = c.sh;
-    const int wg = threadIdx.x >> 7, r = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
-    const int row = S::PAIR ? threadIdx.x : r;  // of the row tile
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t tm = sh->tmem + lanes + wg * 256;
-    const int group = a.group.d;
-    // A form beyond scale and mask is worked out once and written back in log2 units.
-    const bool formed = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
-    const float to_log2 = formed ? 1.f : a.scale * kLog2e;
-    const TypedOut out{a.out, a.out_type};
+// tanh of the cap for f32 queries, within a few 2^-24 of itself: Lambert's continued fraction cut to
+// z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4) (off by 2e-9 at 0.5), beyond it by exponentials.
+__device__ __forceinline__ float fine_tanh(float x) {
+    const float z = x * x;
+    const float small = x * fmaf(z, z + 105.f, 945.f) / fmaf(z, fmaf(z, 15.f, 420.f), 945.f);
+    return z < 0.25f ? small : fast_tanh(x);
+}
 
+// A softmax thread's row of a stretch, and what the two kinds of softmax share.
+template <typename S> struct Row {
+    static constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
+    static constexpr int kParts = DP / 64;             // rows of 128 bytes of a v
+    static constexpr int kScan = S::PAIR ? 256 : 128;  // threads that look through a v tile
+    static constexpr int kEach = KT * kParts > kScan ? KT * kParts / kScan : 1;
+    const TokensArgs &a;
+    const KvView &kv;
+    const Ctx &c;
+    Shared *const sh;
+    const int wg, r, row;  // row of the row tile
+    const uint32_t tm;     // the warpgroup's columns, this warp's lanes
+    const bool formed;     // more than a positive scale: worked out once, written back in log2 units
+    const float to_log2;
     uint32_t met[2] = {0, 0}, odd_turn = 0;
-    uint64_t *const scan_bar = S::PAIR ? &sh->meet[0] : &sh->meet[1 + wg];
-    auto meet = [&](int which) {  // 0: both warpgroups, 1: those that look through a v tile
-        uint64_t *const bar = which == 0 ? &sh->meet[0] : scan_bar;
-        const uint32_t turn = S::PAIR ? met[0]++ : met[which]++;
+    // Of the stretch:
+    Seq q;
+    See see;
+    float slope;
+    bool live;
+    int t, h;
+
+    __device__ __forceinline__ Row(const TokensArgs &a_, const KvView &kv_, const Ctx &c_)
+        : a(a_), kv(kv_), c(c_), sh(c_.sh), wg(threadIdx.x >> 7), r(threadIdx.x & 127),
+          row(S::PAIR ? threadIdx.x : threadIdx.x & 127),
+          tm(c_.sh->tmem + ((threadIdx.x & 96u) << 16) + (threadIdx.x >> 7) * 256),
+          formed(a_.softcap > 0.f || a_.slopes || !(a_.scale > 0.f)),
+          to_log2(formed ? 1.f : a_.scale * kLog2e) {}
+
+    __device__ __forceinline__ void begin(const Stretch &st) {
+        q = st.tile.q;
+        const int group = a.group.d;
+        live = row < min(S::RT, q.count * group - st.tile.row0);
+        const int rr = st.tile.row0 + (live ? row : 0), j = a.group.div(rr), g = rr - j * group;
+        see = See{};
+        if (live) see = see_of(a, q, st.tile.seq, j);
+        slope = a.slopes ? a.slopes[st.head * group + g] * kLog2e : 0.f;
+        t = q.t0 + j, h = st.head * group + g;
+    }
+    // 0: both warpgroups; 1: those that look through a v tile together.
+    __device__ __forceinline__ bool meet(int which) {
+        uint64_t *const bar = &sh->meet[S::PAIR || which == 0 ? 0 : 1 + wg];
+        const uint32_t turn = met[S::PAIR ? 0 : which]++;
         mbar_arrive(bar);
         return c.warp_wait(bar, turn & 1);
+    }
+    // Scores in tensor memory to log2 units after cap and bias, those that are not seen to -inf.
+    __device__ __forceinline__ void form(int j0, bool mixed, const uint32_t *none) {
+#pragma unroll 1
+        for (int ch = 0; ch < kChunks; ++ch) {
+            const int jc = j0 + 32 * ch;
+            uint32_t v[32];
+            ld32(v, tm + kColS + 32 * ch);
+            wait_ld(v);
+            if (formed) {
+                const bool own = a.pos && jc + 32 > q.base;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float y = __uint_as_float(v[e]) * a.scale;
+                    if (a.softcap > 0.f) {
+                        const float z = __fdividef(y, a.softcap);
+                        y = a.softcap * (S::TERMS == 1 ? fast_tanh(z) : fine_tanh(z));
+                    }
+                    v[e] = __float_as_uint(y * kLog2e);
+                }
+                if (a.slopes) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int far = (own ? slot_pos(a, q, jc + e) : jc + e) - see.pos;
+                        v[e] = __float_as_uint(fmaf(slope, (float)far, __uint_as_float(v[e])));
+                    }
+                }
+            }
+            if (mixed) {
+                const uint32_t in = seen32(a, see, jc) & ~none[ch];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!(in >> e & 1u)) v[e] = 0xFF800000u;
+            }
+            st32(tm + kColS + 32 * ch, v);
+        }
+        wait_st();
+    }
+    // Finds the slots of a v tile that are not finite; `any` is the same for all that look.
+    struct Odd {
+        uint32_t any, *words;
+        bool mine;
     };
+    __device__ __forceinline__ bool look(uint32_t v_at, Odd &o) {
+        const int at = S::PAIR ? threadIdx.x : r;
+        const int slot = at % KT, part0 = at / KT, scan_warp = at >> 5;
+        o.mine = false;
+        if (part0 < kParts) {
+#pragma unroll 1
+            for (int p = 0; p < kEach; ++p) {
+                const uint32_t line = v_at + (part0 + p) * (KT * 128) + slot * 128;
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    const uint4 w = lds16(line + (((ch + slot) & 7) << 4));
+                    o.mine |= odd16x2<S::ET>(w.x) || odd16x2<S::ET>(w.y) ||
+                              odd16x2<S::ET>(w.z) || odd16x2<S::ET>(w.w);
+                }
+            }
+        }
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, o.mine);
+        // Two sets taken in turn: a warpgroup may be a tile ahead of the other's reading.
+        o.words = &sh->odd[S::PAIR ? odd_turn++ & 1 : wg][0][0];
+        if ((threadIdx.x & 31) == 0)
+            o.words[scan_warp * 32 / KT * 4 + scan_warp * 32 % KT / 32] = found;
+        if (!meet(1)) return false;
+        o.any = 0;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) o.any |= word(o, ch);
+        return true;
+    }
+    __device__ __forceinline__ static uint32_t word(const Odd &o, int ch) {
+        uint32_t w = o.words[ch];
+        if (kScan / KT > 1 && kParts > 1) w |= o.words[4 + ch];
+        return w;
+    }
+    // f(slot, p) for each of them that the row sees, p its weight against the maximum `safe`; every
+    // lane comes along.
+    template <typename F>
+    __device__ __forceinline__ void each_odd(const Odd &o, int j0, const uint32_t *none, float safe,
+                                             F f) {
+#pragma unroll 1
+        for (int ch = 0; ch < kChunks; ++ch) {
+            const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~none[ch];
+#pragma unroll 1
+            for (uint32_t left = word(o, ch); left; left &= left - 1) {
+                const int b = __ffs(left) - 1;
+                __syncwarp();
+                const float x = ld1(tm + kColS + 32 * ch + b);
+                f(32 * ch + b, (in >> b & 1u) != 0, ex2(fmaf(x, to_log2, -safe)));
+            }
+        }
+    }
+    // Eight dims of a slot's v.
+    __device__ __forceinline__ static void v8(uint32_t v_at, int slot, int chunk, float (&x)[8]) {
+        const uint4 u = lds16(v_at + (chunk >> 3) * (KT * 128) + slot * 128 +
+                              (((chunk & 7) ^ (slot & 7)) << 4));
+        const uint32_t z[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = widen<S::ET>(z[k >> 1], k & 1);
+    }
+    // Takes those slots out of the tile once every row has them.
+    __device__ __forceinline__ bool clear(uint32_t v_at, const Odd &o) {
+        if (!meet(1)) return false;
+        const int at = S::PAIR ? threadIdx.x : r;
+        const int slot = at % KT, part0 = at / KT;
+        if (word(o, slot >> 5) >> (slot & 31) & 1u) {
+#pragma unroll 1
+            for (int p = 0; p < kEach && part0 + p < kParts; ++p)
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch)
+                    sts16(v_at + (part0 + p) * (KT * 128) + slot * 128 + ch * 16,
+                          make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_proxy_async_smem();
+        return true;
+    }
+    // Dims e .. e + 7 of the row's result.
+    __device__ __forceinline__ void put8(int e, const float (&x)[8]) const {
+        if (e >= kv.head_dim) return;
+        const long long to = t * a.out_stride + (long long)h * kv.head_dim + e;
+        if (a.out_type == kF32) {
+            float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + to) =
+                make_uint4(pack2<S::ET>(x[0], x[1]), pack2<S::ET>(x[2], x[3]),
+                           pack2<S::ET>(x[4], x[5]), pack2<S::ET>(x[6], x[7]));
+        }
+    }
+    // Dims e .. e + 7 of the row's sums: its result, or its part.
+    __device__ __forceinline__ void finish(const Room &room, const Stretch &st, float m, float l,
+                                           int e, const float (&x)[8]) const {
+        if (st.part >= 0) {
+            const size_t part = 2 * blockIdx.x + st.part;
+            room.part_o[(part * (DP / 4) + e / 4) * S::RT + row] =
+                make_float4(x[0], x[1], x[2], x[3]);
+            room.part_o[(part * (DP / 4) + e / 4 + 1) * S::RT + row] =
+                make_float4(x[4], x[5], x[6], x[7]);
+            if (e == 0) room.part_ml[part * S::RT + row] = make_float2(m, l);
+            return;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = x[k] * inv;
+        put8(e, y);
+        if (e == 0 && a.lse) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+    }
+};
 
-    Walk walk(room, blockIdx.x, room.plan[kGrid].pad);
+// Two f32 operations of one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
+        "mov.b64 r, {%5, %5};\n\tfma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a0, float a1) {
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a0), "f"(a1));
+}
+
+// 16-bit queries: the output in tensor memory.
+template <typename S>
+__device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
+    constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
+    constexpr float kGrow = 8.f;  // p is at most 2^8: f16 holds it, and its sum
+    Row<S> w(a, kv, c);
+    Shared *const sh = c.sh;
+    Walk walk(room, blockIdx.x);
     Stretch st;
     uint32_t base = 0, mine = 0;  // tiles before this stretch; tiles of this warpgroup
     bool again = false;
     while (walk.next(st)) {
         __syncwarp();
-        bool bad = false;
-        const Seq q = seq_of(a, st.tile.seq, bad);
-        const int rows = min(S::RT, q.count * group - st.tile.row0);
-        const bool live = row < rows;
-        const int rr = st.tile.row0 + (live ? row : 0), j = a.group.div(rr), g = rr - j * group;
-        See see{};
-        if (live) see = see_of(a, q, st.tile.seq, j);
-        const float slope = a.slopes ? a.slopes[st.head * group + g] * kLog2e : 0.f;
+        w.begin(st);
         const int n = st.k1 - st.k0;
+        float m = -INFINITY, l = 0.f;
+        bool some = false;
+        if (n > 0) {
+            if (!S::PAIR && again && !w.meet(0)) return;  // the last stretch's join was read
+            again = true;
+            uint32_t zero[32] = {};
+#pragma unroll
+            for (int ch = 0; ch < DP / 32; ++ch) st32(w.tm + kColT + 32 * ch, zero);
+            if (S::PAIR)
+                load_q<S>(a, kv, w.q, st, c, w.wg * 128, 128, w.r, 128);
+            else
+                load_q<S>(a, kv, w.q, st, c, 0, 128, threadIdx.x, 256);
+            fence_proxy_async_smem();
+            mbar_arrive(&sh->q_ready);
+        }
+        for (int i = S::PAIR ? 0 : w.wg; i < n; i += S::PAIR ? 1 : 2) {
+            const uint32_t vi = 2 * (base + i) + 1, vs = vi % S::kSlots;
+            if (!c.warp_wait(&sh->full[vs], vi / S::kSlots & 1)) return;
+            if (!c.warp_wait(&sh->s_full[w.wg], mine & 1)) return;
+            tc_fence_after();
+            const int j0 = (st.k0 + i) * KT;
+            uint32_t lost = 0;
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
+            const bool mixed = j0 < st.tile.lo || j0 + KT > st.tile.hi || lost;
+            if (w.formed || mixed) w.form(j0, mixed, sh->none[vs]);
+            uint32_t s[kChunks][32];
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+                wait_ld(s[ch]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    top[(e >> 1) & 3] = fmaxf(top[(e >> 1) & 3],
+                                              fmaxf(__uint_as_float(s[ch][e]),
+                                                    __uint_as_float(s[ch][e + 1])));
+            }
+            const float now =
+                fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * w.to_log2);
+            if (__any_sync(0xFFFFFFFFu, now > m + kGrow || m == -INFINITY)) {
+                const float f = ex2(m - (now == -INFINITY ? 0.f : now));
+                m = now;
+                l *= f;
+                if (some) {
+                    if (!c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int ch = 0; ch < DP / 32; ++ch) {
+                        uint32_t v[32];
+                        ld32(v, w.tm + kColT + 32 * ch);
+                        wait_ld(v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        st32(w.tm + kColT + 32 * ch, v);
+                    }
+                }
+            }
+            const float safe = m == -INFINITY ? 0.f : m;
+            if (mixed) {
+                const uint32_t v_at = c.ring + vs * S::kSlot;
+                typename Row<S>::Odd odd;
+                if (!w.look(v_at, odd)) return;
+                if (odd.any) {
+                    if (some && !c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
+                    tc_fence_after();
+                    wait_st();
+#pragma unroll 1
+                    for (int ch = 0; ch < DP / 32; ++ch) {
+                        uint32_t v[32];
+                        ld32(v, w.tm + kColT + 32 * ch);
+                        wait_ld(v);
+                        w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool in, float p) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                float x[8];
+                                w.v8(v_at, slot, 4 * ch + e / 8, x);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    if (in)
+                                        v[e + k] = __float_as_uint(
+                                            fmaf(p, x[k], __uint_as_float(v[e + k])));
+                            }
+                        });
+                        st32(w.tm + kColT + 32 * ch, v);
+                    }
+                    if (!w.clear(v_at, odd)) return;
+                }
+            }
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float x, y;
+                    fma2(x, y, __uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1]),
+                         w.to_log2, -safe);
+                    x = ex2(x), y = ex2(y);
+                    add2(sums[2 * (e & 1)], sums[2 * (e & 1) + 1], x, y);
+                    p[e] = pack2<S::ET>(x, y);
+                }
+                st16(w.tm + kColP0 + 16 * ch, p);
+            }
+            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh->p_ready[w.wg]);
+            ++mine;
+            some = true;
+        }
+        base += n;
+        if (some && !c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
+        tc_fence_after();
+        float fa = 1.f, fb = 0.f;
+        if (!S::PAIR && n > 0) {
+            // The two warpgroups' halves of the slots.
+            if (!w.meet(0)) return;  // every product of q is done
+            if (w.wg == 1) {
+#pragma unroll 1
+                for (int ch = 0; ch < DP / 32; ++ch) {
+                    uint32_t v[32];
+                    ld32(v, w.tm + kColT + 32 * ch);
+                    wait_ld(v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(
+                                         c.stage + ((32 * ch + e) * 128 + w.r) * 4),
+                                     "r"(v[e])
+                                     : "memory");
+                }
+                sh->ml[w.r] = make_float2(m, l);
+            }
+            if (!w.meet(0)) return;
+            if (w.wg == 1) continue;
+            const float2 other = sh->ml[w.r];
+            const float both = fmaxf(m, other.x), safe = both == -INFINITY ? 0.f : both;
+            fa = ex2(m - safe), fb = ex2(other.x - safe);
+            m = both;
+            l = fmaf(l, fa, other.y * fb);
+        } else if (!S::PAIR && w.wg == 1) {
+            continue;
+        }
+#pragma unroll 1
+        for (int ch = 0; ch < DP / 32; ++ch) {
+            uint32_t v[32] = {};
+            if (n > 0) {
+                ld32(v, w.tm + kColT + 32 * ch);
+                wait_ld(v);
+                if (!S::PAIR) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x;
+                        asm volatile("ld.shared.f32 %0, [%1];"
+                                     : "=f"(x)
+                                     : "r"(c.stage + ((32 * ch + e) * 128 + w.r) * 4)
+                                     : "memory");
+                        v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), fa, x * fb));
+                    }
+                }
+            }
+            if (w.live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v[e + k]);
+                    w.finish(room, st, m, l, 32 * ch + e, x);
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
 
+// f32 queries: the output in registers.
+template <typename S>
+__device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
+    constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
+    static_assert(!S::PAIR, "one row tile");
+    Row<S> w(a, kv, c);
+    Shared *const sh = c.sh;
+    Walk walk(room, blockIdx.x);
+    Stretch st;
+    uint32_t base = 0, mine = 0;
+    bool again = false;
+    while (walk.next(st)) {
+        __syncwarp();
+        w.begin(st);
+        const int n = st.k1 - st.k0;
         float o[DP];
 #pragma unroll
         for (int e = 0; e < DP; ++e) o[e] = 0.f;
         float m = -INFINITY, l = 0.f, f = 0.f;
         bool pending = false;
         if (n > 0) {
-            if (!S::PAIR && again && !meet(0)) return;  // the last stretch's join was read
-            if (S::PAIR)
-                load_q<S>(a, kv, q, st, c, wg * 128, 128, r, 128);
-            else
-                load_q<S>(a, kv, q, st, c, 0, 128, threadIdx.x, 256);
+            if (again && !w.meet(0)) return;  // the last stretch's join was read
             again = true;
+            load_q<S>(a, kv, w.q, st, c, 0, 128, threadIdx.x, 256);
             fence_proxy_async_smem();
             mbar_arrive(&sh->q_ready);
         }
         // o = o f + T of the tile before.
         auto take = [&]() {
-            if (!c.warp_wait(&sh->t_full[wg], (mine - 1) & 1)) return false;
+            if (!c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int ch = 0; ch < DP / 32; ++ch) {
                 uint32_t v[32];
-                ld32(v, tm + kColT + 32 * ch);
+                ld32(v, w.tm + kColT + 32 * ch);
                 wait_ld(v);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -500,187 +974,102 @@ __device__ void softmax_rows(const TokensArgs &a, const KvView &kv, const Room &
             }
             return true;
         };
-        for (int i = S::PAIR ? 0 : wg; i < n; i += S::PAIR ? 1 : 2) {
+        for (int i = w.wg; i < n; i += 2) {
             if (pending && !take()) return;
             const uint32_t vi = 2 * (base + i) + 1, vs = vi % S::kSlots;
             if (!c.warp_wait(&sh->full[vs], vi / S::kSlots & 1)) return;
-            if (!c.warp_wait(&sh->s_full[wg], mine & 1)) return;
+            if (!c.warp_wait(&sh->s_full[w.wg], mine & 1)) return;
             tc_fence_after();
             const int j0 = (st.k0 + i) * KT;
-            uint32_t none[kChunks], lost = 0;
+            uint32_t lost = 0;
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) lost |= none[ch] = sh->none[vs][ch];
+            for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
             const bool mixed = j0 < st.tile.lo || j0 + KT > st.tile.hi || lost;
+            if (w.formed || mixed) w.form(j0, mixed, sh->none[vs]);
             float top = -INFINITY;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t v[32];
-                ld32(v, tm + kColS + 32 * ch);
+                ld32(v, w.tm + kColS + 32 * ch);
                 wait_ld(v);
-                if (formed) {
-                    const int from = j0 + 32 * ch - see.pos;
-                    const bool own = a.pos && j0 + 32 * ch + 32 > q.base;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float y = __uint_as_float(v[e]) * a.scale;
-                        if (a.softcap > 0.f)
-                            y = a.softcap * (kFast ? fast_tanh(__fdividef(y, a.softcap))
-                                                   : tanhf(y / a.softcap));
-                        y *= kLog2e;
-                        if (a.slopes) {
-                            const int far =
-                                own ? slot_pos(a, q, j0 + 32 * ch + e) - see.pos : from + e;
-                            y = fmaf(slope, (float)far, y);
-                        }
-                        v[e] = __float_as_uint(y);
-                    }
-                }
-                if (mixed) {
-                    const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~none[ch];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(in >> e & 1u)) v[e] = 0xFF800000u;
-                }
-                if (formed || mixed) st32(tm + kColS + 32 * ch, v);
-                float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    t0 = fmaxf(t0, __uint_as_float(v[e]));
-                    t1 = fmaxf(t1, __uint_as_float(v[e + 1]));
-                }
-                top = fmaxf(top, fmaxf(t0, t1));
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
             }
-            if (formed || mixed) wait_st();
-            const float now = fmaxf(m, top * to_log2);
+            const float now = fmaxf(m, top * w.to_log2);
             const float safe = now == -INFINITY ? 0.f : now;
             const float fl = ex2(m - safe);
             f = fl;
             m = now;
             if (mixed) {
-                // Rows of 128 bytes of v: a thread looks through one, or through both of its slot's.
                 const uint32_t v_at = c.ring + vs * S::kSlot;
-                constexpr int kParts = DP / 64;                  // rows of 128 bytes to a slot
-                constexpr int kScan = S::PAIR ? 256 : 128;       // threads
-                constexpr int kEach = KT * kParts > kScan ? KT * kParts / kScan : 1;
-                const int at = S::PAIR ? threadIdx.x : r;
-                const int slot = at % KT, part0 = at / KT, scan_warp = at >> 5;
-                bool mine_odd = false;
-                if (part0 < kParts) {
-#pragma unroll
-                    for (int p = 0; p < kEach; ++p) {
-                        const int part = part0 + p;
-                        const uint32_t line = v_at + part * (KT * 128) + slot * 128;
-#pragma unroll
-                        for (int ch = 0; ch < 8; ++ch) {
-                            const uint4 w = lds16(line + (((ch + slot) & 7) << 4));
-                            mine_odd |= odd16x2<S::ET>(w.x) || odd16x2<S::ET>(w.y) ||
-                                        odd16x2<S::ET>(w.z) || odd16x2<S::ET>(w.w);
-                        }
-                    }
-                }
-                const uint32_t found = __ballot_sync(0xFFFFFFFFu, mine_odd);
-                // Words of this tile's slots, by the warp that looked: two sets taken in turn.
-                uint32_t *const words = S::PAIR ? &sh->odd[odd_turn & 1][0][0]
-                                                : &sh->odd[wg][0][0];
-                if ((threadIdx.x & 31) == 0)
-                    words[scan_warp * 32 / KT * 4 + scan_warp * 32 % KT / 32] = found;
-                if (!meet(1)) return;
-                uint32_t any = 0, w[kChunks];
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    w[ch] = words[ch];
-                    if (kScan / KT > 1 && kParts > 1) w[ch] |= words[4 + ch];
-                    any |= w[ch];
-                }
-                ++odd_turn;
-                if (any) {
+                typename Row<S>::Odd odd;
+                if (!w.look(v_at, odd)) return;
+                if (odd.any) {
 #pragma unroll
                     for (int e = 0; e < DP; ++e) o[e] *= f;
                     f = 1.f;
+                    w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool in, float p) {
 #pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch) {
-                        const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~none[ch];
-                        for (uint32_t left = w[ch]; left; left &= left - 1) {
-                            const int b = __ffs(left) - 1, s = 32 * ch + b;
-                            __syncwarp();
-                            const float x = ld1(tm + kColS + s);
-                            if (!(in >> b & 1u)) continue;
-                            const float p = ex2(fmaf(x, to_log2, -safe));
+                        for (int e = 0; e < DP; e += 8) {
+                            float x[8];
+                            w.v8(v_at, slot, e / 8, x);
 #pragma unroll
-                            for (int e = 0; e < DP; e += 8) {
-                                const int chunk = e / 8;
-                                const uint4 u = lds16(v_at + (chunk >> 3) * (KT * 128) + s * 128 +
-                                                      (((chunk & 7) ^ (s & 7)) << 4));
-                                const uint32_t z[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    o[e + k] = fmaf(p, widen<S::ET>(z[k >> 1], k & 1), o[e + k]);
-                            }
+                            for (int k = 0; k < 8; ++k)
+                                if (in) o[e + k] = fmaf(p, x[k], o[e + k]);
                         }
-                    }
-                    if (!meet(1)) return;
-                    if (mine_odd || (w[slot >> 5] >> (slot & 31) & 1u)) {
-#pragma unroll
-                        for (int p = 0; p < kEach; ++p)
-                            if (part0 + p < kParts)
-#pragma unroll
-                                for (int ch = 0; ch < 8; ++ch)
-                                    sts16(v_at + (part0 + p) * (KT * 128) + slot * 128 + ch * 16,
-                                          make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    fence_proxy_async_smem();
+                    });
+                    if (!w.clear(v_at, odd)) return;
                 }
             }
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t v[32];
-                ld32(v, tm + kColS + 32 * ch);
+                ld32(v, w.tm + kColS + 32 * ch);
                 wait_ld(v);
-                float p[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    p[e] = ex2(fmaf(__uint_as_float(v[e]), to_log2, -safe));
-                    sums[e & 3] += p[e];
+                    const float p = ex2(fmaf(__uint_as_float(v[e]), w.to_log2, -safe));
+                    sums[e & 3] += p;
+                    v[e] = __float_as_uint(p);
                 }
 #pragma unroll
                 for (int t = 0; t < S::TERMS; ++t) {
-                    uint32_t w[16];
+                    uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        w[e] = pack2<S::ET>(p[2 * e], p[2 * e + 1]);
-                        if (t + 1 < S::TERMS) {
-                            p[2 * e] -= bf16_lo(w[e]);
-                            p[2 * e + 1] -= bf16_hi(w[e]);
-                        }
+                        p[e] = pack2<S::ET>(__uint_as_float(v[2 * e]),
+                                            __uint_as_float(v[2 * e + 1]));
+                        v[2 * e] = __float_as_uint(__uint_as_float(v[2 * e]) - bf16_lo(p[e]));
+                        v[2 * e + 1] =
+                            __float_as_uint(__uint_as_float(v[2 * e + 1]) - bf16_hi(p[e]));
                     }
-                    st16(tm + (t == 0 ? kColP0 : t == 1 ? kColP1 : kColP2) + 16 * ch, w);
+                    st16(w.tm + (t == 0 ? kColP0 : t == 1 ? kColP1 : kColP2) + 16 * ch, p);
                 }
             }
             l = fmaf(l, fl, (sums[0] + sums[1]) + (sums[2] + sums[3]));
             wait_st();
             tc_fence_before();
-            mbar_arrive(&sh->p_ready[wg]);
+            mbar_arrive(&sh->p_ready[w.wg]);
             ++mine;
             pending = true;
         }
         if (pending && !take()) return;
         base += n;
-
-        if (!S::PAIR && n > 0) {
+        if (n > 0) {
             // The two warpgroups' halves of the slots.
-            if (!meet(0)) return;  // every product of q is done
-            if (wg == 1) {
+            if (!w.meet(0)) return;  // every product of q is done
+            if (w.wg == 1) {
 #pragma unroll
                 for (int e = 0; e < DP; ++e)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.stage + (e * 128 + r) * 4),
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.stage + (e * 128 + w.r) * 4),
                                  "f"(o[e])
                                  : "memory");
-                sh->ml[r] = make_float2(m, l);
+                sh->ml[w.r] = make_float2(m, l);
             }
-            if (!meet(0)) return;
-            if (wg == 0) {
-                const float2 other = sh->ml[r];
+            if (!w.meet(0)) return;
+            if (w.wg == 0) {
+                const float2 other = sh->ml[w.r];
                 const float both = fmaxf(m, other.x), safe = both == -INFINITY ? 0.f : both;
                 const float fa = ex2(m - safe), fb = ex2(other.x - safe);
                 m = both;
@@ -690,49 +1079,27 @@ __device__ void softmax_rows(const TokensArgs &a, const KvView &kv, const Room &
                     float x;
                     asm volatile("ld.shared.f32 %0, [%1];"
                                  : "=f"(x)
-                                 : "r"(c.stage + (e * 128 + r) * 4)
+                                 : "r"(c.stage + (e * 128 + w.r) * 4)
                                  : "memory");
                     o[e] = fmaf(o[e], fa, x * fb);
                 }
             }
         }
-        if (!live || (!S::PAIR && wg == 1)) continue;
-        if (st.part >= 0) {
-            const size_t part = 2 * blockIdx.x + st.part;
-#pragma unroll
-            for (int e = 0; e < DP; e += 4)
-                room.part_o[(part * (DP / 4) + e / 4) * S::RT + row] =
-                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            room.part_ml[part * S::RT + row] = make_float2(m, l);
-            continue;
-        }
-        const int t = q.t0 + j, h = st.head * group + g;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const long long to = t * a.out_stride + (long long)h * kv.head_dim;
+        if (!w.live || w.wg == 1) continue;
 #pragma unroll
         for (int e = 0; e < DP; e += 8) {
-            if (e >= kv.head_dim) break;
-            if (a.out_type == kF32) {
-                out.put4(to + e, make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv,
-                                             o[e + 3] * inv));
-                out.put4(to + e + 4, make_float4(o[e + 4] * inv, o[e + 5] * inv, o[e + 6] * inv,
-                                                 o[e + 7] * inv));
-            } else {
-                uint4 w;
-                w.x = pack2<S::ET>(o[e] * inv, o[e + 1] * inv);
-                w.y = pack2<S::ET>(o[e + 2] * inv, o[e + 3] * inv);
-                w.z = pack2<S::ET>(o[e + 4] * inv, o[e + 5] * inv);
-                w.w = pack2<S::ET>(o[e + 6] * inv, o[e + 7] * inv);
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + to + e) = w;
-            }
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = o[e + k];
+            w.finish(room, st, m, l, e, x);
         }
-        if (a.lse) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
     }
 }
 
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tokens_tc_kernel(TokensArgs a, KvView kv) {
+    attn_tokens_tc_kernel(TokensArgs a, KvView kv, const __grid_constant__ CUtensorMap k_map,
+                          const __grid_constant__ CUtensorMap v_map, int box) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctx c;
     c.sh = reinterpret_cast<Shared *>(smem);
@@ -743,8 +1110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     pdl_launch();
     if (threadIdx.x == 0) {
+        if (box) prefetch_tmap(&k_map), prefetch_tmap(&v_map);
         for (int i = 0; i < kMostSlots; ++i) {
-            mbar_init(&c.sh->full[i], kLoaders);
+            mbar_init(&c.sh->full[i], box ? 1 : kLoaders);
             mbar_init(&c.sh->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -771,15 +1139,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     pdl_wait();
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, a.group.d, S::RT, S::DP, kGrid);
-    // 384 threads of 168 registers at the launch; 224 for each row's output and 56 for the others
-    // add up to the same.
+    // 384 threads of 168 registers at the launch: 2 x 216 + 72 and 2 x 224 + 56 are 3 x 168.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        softmax_rows<S>(a, kv, room, c);
+        if constexpr (S::TERMS == 1)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if constexpr (S::TERMS == 1)
+            softmax_16<S>(a, kv, room, c);
+        else
+            softmax_32<S>(a, kv, room, c);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (S::TERMS == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp > 8) {
-            load_tiles<S>(a, kv, room, c);
+            fence_proxy_async_global();  // k and v may be an earlier kernel's plain stores
+            if (!box)
+                load_rows<S>(a, kv, room, c);
+            else if (warp == 9)
+                load_boxes<S>(a, kv, &k_map, &v_map, box, room, c);
         } else if ((threadIdx.x & 31) == 0) {
             issue_products<S>(a, room, c);
             // Every product is done before tensor memory and the tiles are given up.
@@ -803,6 +1183,44 @@ bool pairs_rows(int n_seq, int n_tok, int group) {
     return (long long)n_tok * group > 128ll * n_seq;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult st;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &st) == cudaSuccess &&
+            st == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        known.store(fn, std::memory_order_release);
+    }
+    return fn;
+}
+// A pool as [page][head][row][dim] in boxes of `box` rows of 64 dims, zeros beyond head_dim.
+bool pool_map(CUtensorMap &map, const KvView &kv, char *pool, int box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, kv.page_size.d, (cuuint64_t)kv.n_heads,
+                                (cuuint64_t)kv.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)kv.token_stride, (cuuint64_t)kv.head_stride,
+                                   (cuuint64_t)kv.page_stride};
+    for (cuuint64_t st : strides)
+        if (st >= (1ull << 40)) return false;
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    return encode && encode(&map,
+                            kv.dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            4, pool, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Rows of a box: the largest power of two, 8 at least, that divides a page and a tile; 0: none.
+int box_of(const KvView &kv, int kt) {
+    int box = kt;
+    while (kv.page_size.d % box) box /= 2;
+    return box >= 8 ? box : 0;
+}
+
 template <int DP, int TERMS, bool PAIR, int ET>
 cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                          cudaStream_t stream) {
@@ -812,7 +1230,11 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     if (err != cudaSuccess) return err;
     err = launch_attn_plan(a, kv, S::RT, S::KT, DP, kGrid, stream);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv);
+    CUtensorMap k_map{}, v_map{};
+    int box = box_of(kv, S::KT);
+    if (box && !(pool_map(k_map, kv, kv.k, box) && pool_map(v_map, kv, kv.v, box))) box = 0;
+    err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv,
+                     k_map, v_map, box);
     if (err != cudaSuccess) return err;
     return launch_attn_parts(a, kv, S::RT, DP, kGrid, stream);
 }
