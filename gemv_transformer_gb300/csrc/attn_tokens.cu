@@ -16,6 +16,7 @@ namespace tok {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanTiles = 2048;
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
@@ -43,6 +44,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     attn_plan_kernel(TokensArgs a, int heads, int rt, int kt, int dp, int grid) {
     __shared__ long long s_warp[32];
     __shared__ int s_first[kPlanThreads + 1];
+    __shared__ long long s_before[kPlanTiles];  // the first tiles' costs, for the searches below
     pdl_enter();
     const int group = a.group.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         long long all;
         const long long upto = block_scan(mine, s_warp, all);
         if (i < n_tiles) room.before[i] = cost + upto - mine;
+        if (i < n_tiles && i < kPlanTiles) s_before[i] = cost + upto - mine;
         cost += all;
     }
     if (threadIdx.x == 0) room.before[n_tiles] = cost;
@@ -117,11 +120,11 @@ __global__ void __launch_bounds__(kPlanThreads)
             int x = 0, y = n_tiles;  // before[x] <= in < before[y]
             while (y - x > 1) {
                 const int mid = (x + y) / 2;
-                if (room.before[mid] <= in) x = mid; else y = mid;
+                if ((mid < kPlanTiles ? s_before[mid] : room.before[mid]) <= in) x = mid; else y = mid;
             }
             p.head = head;
             p.tile = x;
-            p.off = (int)(in - room.before[x]);
+            p.off = (int)(in - (x < kPlanTiles ? s_before[x] : room.before[x]));
             const Tile t = room.tiles[x];
             if (p.off > 0 && p.off >= t.k1 - t.k0) {  // in the end of a row tile
                 p.off = 0;
@@ -133,7 +136,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // Joins the parts of the row tile that CTA blockIdx.x + 1 begins within, if that CTA is the first to.
-// A thread takes one row and four dims at a time.
+// A thread takes four dims of one row, with the loads of kAtOnce parts in flight.
+constexpr int kAtOnce = 8;
 __global__ void __launch_bounds__(256)
     attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
     pdl_enter();
@@ -143,41 +147,57 @@ __global__ void __launch_bounds__(256)
     const Begin p = room.plan[b], before = room.plan[b - 1];
     if (p.off == 0 || p.head >= kv.n_heads) return;
     if (before.head == p.head && before.tile == p.tile && before.off > 0) return;
-    int n = 1;  // CTAs that begin within it
-    for (; b + n < grid; ++n) {
-        const Begin q = room.plan[b + n];
-        if (q.head != p.head || q.tile != p.tile || q.off == 0) break;
-    }
     const Tile tile = room.tiles[p.tile];
     const Seq q = tile.q;
-    const int rows = min(rt, q.count * group - tile.row0);
-    const TypedOut out{a.out, a.out_type};
+    const int at = blockIdx.y * 256 + threadIdx.x;
+    const int row = at % rt, c = at / rt;  // rt is a power of two
+    const bool mine = row < min(rt, q.count * group - tile.row0) && 4 * c < kv.head_dim;
+    // CTAs that begin within it.
+    int n = 1;
+    for (bool more = true; more;) {
+        Begin next[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            next[i] = room.plan[min(b + n + i, grid)];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (more) {
+                more = next[i].head == p.head && next[i].tile == p.tile && next[i].off > 0;
+                n += more;
+            }
+    }
+    if (!mine) return;
     // The parts: the second of CTA b - 1, then the first of CTAs b, b + 1, ...
     auto place = [&](int i) { return (size_t)(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)); };
-    const int row = blockIdx.y * 32 + (threadIdx.x & 31);
-    if (row >= rows) return;
     float m = -INFINITY, l = 0.f;
-    for (int i = 0; i <= n; ++i) m = fmaxf(m, room.part_ml[place(i) * rt + row].x);
-    const float safe = m == -INFINITY ? 0.f : m;
-    for (int i = 0; i <= n; ++i) {
-        const float2 ml = room.part_ml[place(i) * rt + row];
-        l = fmaf(ml.y, exp2f(ml.x - safe), l);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 <= n; i0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const size_t part = place(min(i0 + i, n));
+            ml[i] = room.part_ml[part * rt + row];
+            v[i] = room.part_o[(part * (dp / 4) + c) * rt + row];
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (i0 + i > n) break;
+            const float now = fmaxf(m, ml[i].x), safe = now == -INFINITY ? 0.f : now;
+            const float f = exp2f(m - safe), g = exp2f(ml[i].x - safe);
+            m = now;
+            l = fmaf(l, f, ml[i].y * g);
+            o.x = fmaf(o.x, f, v[i].x * g), o.y = fmaf(o.y, f, v[i].y * g);
+            o.z = fmaf(o.z, f, v[i].z * g), o.w = fmaf(o.w, f, v[i].w * g);
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int rr = tile.row0 + row, j = a.group.div(rr), g = rr - j * group;
     const int t = q.t0 + j, h = p.head * group + g;
-    for (int c = threadIdx.x >> 5; c * 4 < kv.head_dim; c += 8) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i <= n; ++i) {
-            const float f = exp2f(room.part_ml[place(i) * rt + row].x - safe);
-            const float4 v = room.part_o[(place(i) * (dp / 4) + c) * rt + row];
-            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-        }
-        out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
-                 make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    }
-    if (a.lse && threadIdx.x < 32) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+    const TypedOut out{a.out, a.out_type};
+    out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
+             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (a.lse && c == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
 }
 
 // ------------------------------------------------------------------ f32 arithmetic --
@@ -225,14 +245,15 @@ __global__ void __launch_bounds__(256)
     const int d = kv.head_dim;
     Stretch st;
     while (walk.next(st)) {
-        const Seq q = st.tile.q;
-        const int rows = min(RT, q.count * group - st.tile.row0);
+        const Tile tile = room.tiles[st.tile];
+        const Seq q = tile.q;
+        const int rows = min(RT, q.count * group - tile.row0);
         __syncthreads();
         for (int i = threadIdx.x; i < RT * (DP / 8); i += 256) {
             const int r = i / (DP / 8), c = i - r * (DP / 8);
             float v[8] = {};
             if (r < rows && c * 8 < d) {
-                const int rr = st.tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
+                const int rr = tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
                 const long long at = (q.t0 + j) * a.q_stride +
                                      (long long)(st.head * group + g) * d + c * 8;
                 if (a.q_type == kF32)
@@ -250,8 +271,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = ty * R + i;
-            const int rr = st.tile.row0 + min(r, rows - 1), j = a.group.div(rr);
-            see[i] = see_of(a, q, st.tile.seq, j);
+            const int rr = tile.row0 + min(r, rows - 1), j = a.group.div(rr);
+            see[i] = see_of(a, q, tile.seq, j);
             slope[i] = a.slopes ? a.slopes[st.head * group + rr - j * group] : 0.f;
         }
         float m[R], l[R], o[R][ND];
@@ -270,7 +291,7 @@ __global__ void __launch_bounds__(256)
                 const int r = i / (DP / 8), c = i - r * (DP / 8), j = j0 + r;
                 float x[8] = {}, y[8] = {};
                 if (j < q.len) {
-                    const long long at = kv.row(st.tile.seq, st.head, j);
+                    const long long at = kv.row(tile.seq, st.head, j);
                     if (at < 0) {
                         lost |= 1u;
                     } else if (c * 8 < d) {
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(256)
                         x[i][n] = fmaf(qa[i].w, ka[n].w, x[i][n]);
                     }
             }
-            const bool whole = j0 >= st.tile.lo && j0 + KT <= st.tile.hi && !none;
+            const bool whole = j0 >= tile.lo && j0 + KT <= tile.hi && !none;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 uint32_t seen[KT / 32];
@@ -326,7 +347,7 @@ __global__ void __launch_bounds__(256)
                     if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
                     if (a.slopes) y = fmaf(slope[i], (float)(slot_pos(a, q, j) - see[i].pos), y);
                     bool in = seen[r >> 5] >> (r & 31) & 1u;
-                    if (none && in) in = kv.row(st.tile.seq, st.head, j) >= 0;
+                    if (none && in) in = kv.row(tile.seq, st.head, j) >= 0;
                     // A score that is not a number stays one: only slots that are not seen are -inf.
                     x[i][n] = in ? y * kLog2e : -INFINITY;
                     if (!in) seen[r >> 5] &= ~(1u << (r & 31));
@@ -407,7 +428,7 @@ __global__ void __launch_bounds__(256)
                 if (tx == 0) room.part_ml[part * RT + r] = make_float2(m[i], l[i]);
                 continue;
             }
-            const int rr = st.tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
+            const int rr = tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
             const int t = q.t0 + j, h = st.head * group + g;
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
@@ -469,7 +490,7 @@ cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int 
 cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
                               cudaStream_t stream) {
     if (grid < 2) return cudaSuccess;
-    return launch_pdl(attn_parts_kernel, dim3(grid - 1, (rt + 31) / 32), dim3(256), 0, stream, a,
+    return launch_pdl(attn_parts_kernel, dim3(grid - 1, (rt * (kv.head_dim / 4) + 255) / 256), dim3(256), 0, stream, a,
                       kv, rt, dp, grid);
 }
 

@@ -147,31 +147,32 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int n_tok, int group
 
 // One stretch of a CTA's range: key tiles [k0, k1) of a row tile for a kv head.
 struct Stretch {
-    Tile tile;
-    int head, k0, k1;
+    int tile, head, k0, k1;
     int part;  // -1: all of the row tile; else its place in this CTA's two parts
 };
+// The stretches of a CTA, one after another.  Little of it stays in registers: what it needs it
+// reads again.
 struct Walk {
-    const Room &room;
-    Begin at, end;
-    int tiles;
-    __device__ __forceinline__ Walk(const Room &r, int cta) : room(r) {
-        at = r.plan[cta];
-        end = r.plan[cta + 1];
-        tiles = at.tiles;
+    const Begin *plan;
+    const Tile *tiles;
+    int head, tile, off;
+    __device__ __forceinline__ Walk(const Room &r, int cta) : plan(r.plan + cta), tiles(r.tiles) {
+        head = plan->head, tile = plan->tile, off = plan->off;
     }
     __device__ __forceinline__ bool next(Stretch &s) {
-        if (at.head > end.head || (at.head == end.head && at.tile > end.tile)) return false;
-        const bool last = at.head == end.head && at.tile == end.tile;
-        if (last && at.off >= end.off) return false;
-        s.tile = room.tiles[at.tile];
-        s.head = at.head;
-        s.k0 = s.tile.k0 + at.off;
-        s.k1 = last ? s.tile.k0 + end.off : s.tile.k1;
-        s.part = at.off > 0 ? 0 : s.k1 < s.tile.k1 ? 1 : -1;
-        at.off = 0;
-        if (++at.tile == tiles) at.tile = 0, ++at.head;
-        if (last) at.head = end.head + 1;
+        const int to_head = plan[1].head, to_tile = plan[1].tile, to_off = plan[1].off;
+        if (head > to_head || (head == to_head && tile > to_tile)) return false;
+        const bool last = head == to_head && tile == to_tile;
+        if (last && off >= to_off) return false;
+        const int k0 = tiles[tile].k0, k1 = tiles[tile].k1;
+        s.tile = tile;
+        s.head = head;
+        s.k0 = k0 + off;
+        s.k1 = last ? k0 + to_off : k1;
+        s.part = off > 0 ? 0 : s.k1 < k1 ? 1 : -1;
+        off = 0;
+        if (++tile == plan->tiles) tile = 0, ++head;
+        if (last) head = to_head + 1;
         return true;
     }
 };

@@ -26,6 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "attn_tokens.cuh"
 #include "tc_ptx.cuh"
@@ -37,11 +38,13 @@ namespace {
 using namespace tc;
 
 constexpr int kGrid = 152;       // one CTA on each SM
-constexpr int kThreads = 384;    // two softmax warpgroups; an MMA warp and three loader warps
-constexpr int kLoaders = 96;
-constexpr int kMostSlots = 8;
+constexpr int kTeam = 128;       // a warpgroup: a thread to a row of its tile
+constexpr int kSoft = 2 * kTeam;
+constexpr int kThreads = kSoft + 128;  // an MMA warp, two for k and v, one for q
+constexpr int kLoaders = 64;      // of pages that are no boxes
+constexpr int kMostV = 6;
 constexpr int kSmemMost = 227 * 1024;
-constexpr int kMisc = 2048;      // barriers and small arrays, before the 1024-byte aligned part
+constexpr int kMisc = 3072;      // barriers and small arrays, before the 1024-byte aligned part
 
 // Tensor memory columns of a warpgroup (256 each).
 constexpr uint32_t kColS = 0, kColP0 = 0, kColP1 = 64, kColP2 = 96, kColT = 128;
@@ -53,24 +56,25 @@ template <int DP_, int TERMS_, bool PAIR_, int ET_> struct TcShape {
     static constexpr int RT = PAIR ? 256 : 128;
     static constexpr int kHalf = 128 * 128;            // 128 rows of 64 dims
     static constexpr int kQTerm = RT * DP * 2;
-    static constexpr int kJoin = PAIR ? 0 : 128 * DP * 4;
-    static constexpr int kStage = TERMS * kQTerm > kJoin ? TERMS * kQTerm : kJoin;
+    static constexpr int kStage = TERMS * kQTerm;
     static constexpr int kSlot = KT * DP * 2;          // a k or a v tile
-    static constexpr int kFit = (kSmemMost - kMisc - 1024 - kStage) / kSlot;
-    static constexpr int kSlots = kFit < kMostSlots ? kFit : kMostSlots;
-    static constexpr int kSmem = kMisc + 1024 + kStage + kSlots * kSlot;
-    static_assert(kSlots >= 4, "a k and a v tile of each warpgroup");
+    static constexpr int kFit = (kSmemMost - kMisc - kStage) / kSlot;
+    static constexpr int kAhead = PAIR ? 1 : 0;        // a step brings v of tile g, k of g + kAhead
+    static constexpr int NV = (kFit - kAhead) / 2 < kMostV ? (kFit - kAhead) / 2 : kMostV;
+    static constexpr int NK = NV + kAhead;             // places for v and k tiles
+    static constexpr int kSmem = kMisc + kStage + (NK + NV) * kSlot;
+    static_assert(NV >= 2, "a tile for each warpgroup");
 };
 
 struct Shared {
-    uint64_t full[kMostSlots], empty[kMostSlots];
-    uint64_t s_full[2], p_ready[2], t_full[2], q_ready, meet[3], drain;
-    uint32_t none[kMostSlots][4];   // of a v tile: slots whose page is out of range
-    uint32_t odd[2][2][4];          // slots whose v is not finite
-    float2 ml[128];
+    uint64_t first, full[kMostV], done[kMostV];
+    uint64_t s_full[2], p_ready[2], t_full[2], q_ready, q_free, meet[3], drain;
+    alignas(16) uint32_t none[kMostV][4];  // of a v tile: slots whose page is out of range
+    uint32_t odd[2][4][4];          // slots whose v is not finite
+    float2 ml[2][128];              // maxima and sums of the warpgroups' rows
     uint32_t tmem, abort;
 };
-static_assert(sizeof(Shared) <= kMisc, "the small arrays fit before the tiles");
+static_assert(sizeof(Shared) <= kMisc && offsetof(Shared, none) % 16 == 0, "read as 16 bytes");
 
 // Shared-memory descriptors by their low words (the address, and for MN-major the bytes between
 // 64-element chunks of the contiguous dimension); the high word, groups of eight rows 1024 bytes
@@ -146,7 +150,7 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
         "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+template <int N> __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[N]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16};" ::"r"(at),
@@ -211,11 +215,16 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
 
 struct Ctx {
     Shared *sh;
-    uint32_t stage, ring;  // shared-memory addresses of q and of the k and v tiles
+    uint32_t stage, k_ring, v_ring;  // shared-memory addresses of q and of the k and v tiles
     unsigned long long limit;
     unsigned *status;
     __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
         return wait_or_abort(bar, parity, &sh->abort, limit, status);
+    }
+    // One arrival of a warp, after what its lanes did.
+    __device__ __forceinline__ void warp_arrive(uint64_t *bar) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
     }
     // A warp gives up as one.
     __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) const {
@@ -224,161 +233,260 @@ struct Ctx {
 };
 
 // -------------------------------------------------------------------- loader warps --
+//
+// The key tiles of a CTA's range are one stream, numbered g across its stretches.  Step g brings
+// v of tile g and k of tile g + kAhead (where that is 1, k of tile 0 comes by itself, `first`) and
+// has one barrier, full[g % NV]; done[g % NV] says that the products of tile g are over.  k of tile
+// g + kAhead takes the place of tile g - NV's, whose scores came before its values.
 
-// The page of slot j, asked for a tile ahead of its use; -2 for one that is not live.
+// The page of slot j; -2 for one that is not live.
 __device__ __forceinline__ int page_of(const KvView &kv, int seq, int j, int len) {
     if (j >= len) return -2;
     return kv.page_table[(long long)seq * kv.max_pages + kv.page_size.div((uint32_t)j)];
 }
 
-// The k and v tiles of the CTA's range, one after another, by TMA, one warp: where the pages are
-// whole groups of eight rows, boxes of the largest number of rows that divides a page and a tile.
-// What lies beyond the live slots of a page, or of a box that was not asked for, is whatever
-// memory holds: no row sees it, and look() takes it out.
+// The tiles of the stream, and what a stretch has for all of its tiles.
+template <typename S> struct Stream {
+    Walk walk;
+    const Tile *tiles;
+    Stretch st;
+    int kt, seq, len;
+    bool more;
+    __device__ __forceinline__ Stream(const Room &room) : walk(room, blockIdx.x), tiles(room.tiles) {
+        open();
+    }
+    __device__ __forceinline__ void open() {
+        do more = walk.next(st);
+        while (more && st.k0 == st.k1);
+        if (!more) return;
+        kt = st.k0, seq = tiles[st.tile].seq, len = tiles[st.tile].q.len;
+    }
+    __device__ __forceinline__ void next() {
+        if (++kt == st.k1) open();
+    }
+};
+
+// By TMA, one warp: where the pages are whole groups of eight rows, boxes of the largest number of
+// rows that divides a page and a tile.  What lies beyond the live slots of a page, or of a box that
+// was not asked for, is whatever memory holds: no row sees it, and look() takes it out.
 template <typename S>
 __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensorMap *k_map,
                            const CUtensorMap *v_map, int box, const Room &room, const Ctx &c) {
-    const int lane = threadIdx.x & 31, boxes = S::KT / box, from = lane * box;
-    const bool mine = lane < boxes;
-    Walk walk(room, blockIdx.x);
-    Stretch st;
-    uint32_t n = 0;
-    bool ok = true;
-    while (ok && walk.next(st)) {
-        const int len = mine ? st.tile.q.len : 0, seq = st.tile.seq;
-        int j = st.k0 * S::KT + from, page = page_of(kv, seq, j, len);
-        for (int kt = st.k0; kt < st.k1; ++kt, ++n, j += S::KT) {
-            const int next = kt + 1 < st.k1 ? page_of(kv, seq, j + S::KT, len) : -2;
-            const bool live = (unsigned)page < (unsigned)kv.n_pages;
-            const uint32_t lost = __ballot_sync(0xFFFFFFFFu, !live && page != -2);
-            const uint32_t bytes =
-                __popc(__ballot_sync(0xFFFFFFFFu, live)) * box * 128 * (S::DP / 64);
-            const int row = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
+    const int lane = threadIdx.x & 31, from = lane * box;
+    const bool mine = lane < S::KT / box;
+    struct Box {
+        int page, row, head;
+        bool live;
+        uint32_t lost;   // of all lanes
+        uint32_t bytes;
+    };
+    Stream<S> in(room);
+    auto ask = [&]() {
+        Box x{-2, 0, 0, false, 0u, 0u};
+        if (!in.more) return x;
+        const int j = in.kt * S::KT + from;
+        x.head = in.st.head;
+        x.row = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
+        if (mine) x.page = page_of(kv, in.seq, j, in.len);
+        return x;
+    };
+    auto settle = [&](Box &x) {  // once the page is there
+        x.live = (unsigned)x.page < (unsigned)kv.n_pages;
+        x.lost = __ballot_sync(0xFFFFFFFFu, !x.live && x.page != -2);
+        x.bytes = __popc(__ballot_sync(0xFFFFFFFFu, x.live)) * box * 128 * (S::DP / 64);
+    };
+    auto copy = [&](const Box &x, const CUtensorMap *map, uint32_t to, uint64_t *bar) {
+        if (!x.live) return;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint32_t i = 2 * n + v, slot = i % S::kSlots;
-                if (!c.warp_wait(&c.sh->empty[slot], (i / S::kSlots & 1) ^ 1)) {
-                    ok = false;
-                    break;
+        for (int h = 0; h < S::DP / 64; ++h)
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + from * 128 + h * (S::KT * 128)),
+                "l"(reinterpret_cast<uint64_t>(map)), "r"(64 * h), "r"(x.row), "r"(x.head),
+                "r"(x.page), "r"(smem_addr(bar))
+                : "memory");
+    };
+    if (!in.more) return;
+    Box cur = ask();
+    if (S::kAhead) {
+        settle(cur);
+        if (lane == 0) mbar_arrive_expect_tx(&c.sh->first, cur.bytes);
+        __syncwarp();
+        copy(cur, k_map, c.k_ring, &c.sh->first);
+    }
+    uint32_t g = 0;
+    for (bool some = true; some; ++g) {
+        Box v = cur;
+        in.next();
+        some = in.more;
+        cur = ask();
+        const uint32_t slot = g % S::NV;
+        if (g >= (uint32_t)S::NV && !c.warp_wait(&c.sh->done[slot], (g / S::NV & 1) ^ 1)) break;
+        settle(S::kAhead ? cur : v);
+        const Box &k = S::kAhead ? cur : v;
+        if (lane == 0) {
+            for (int i = 0; i < S::KT / 32; ++i) {
+                uint32_t none = 0;
+                for (uint32_t left = v.lost; left; left &= left - 1) {
+                    const int at = (__ffs(left) - 1) * box - 32 * i;
+                    none |= below(at + box) & ~below(at);
                 }
-                if (lane == 0) {
-                    if (v) {
-                        for (int g = 0; g < S::KT / 32; ++g) {
-                            uint32_t none = 0;
-                            for (uint32_t left = lost; left; left &= left - 1) {
-                                const int first = (__ffs(left) - 1) * box - 32 * g;
-                                none |= below(first + box) & ~below(first);
-                            }
-                            c.sh->none[slot][g] = none;
-                        }
-                        if (lost) record_status(a.status, kStBadIndex);
-                    }
-                    mbar_arrive_expect_tx(&c.sh->full[slot], bytes);
-                }
-                __syncwarp();
-                if (live) {
-                    const uint32_t to = c.ring + slot * S::kSlot + from * 128;
-#pragma unroll
-                    for (int h = 0; h < S::DP / 64; ++h)
-                        asm volatile(
-                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx"
-                            "::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                                to + h * (S::KT * 128)),
-                            "l"(reinterpret_cast<uint64_t>(v ? v_map : k_map)), "r"(64 * h),
-                            "r"(row), "r"(st.head), "r"(page), "r"(smem_addr(&c.sh->full[slot]))
-                            : "memory");
-                }
-                __syncwarp();
+                c.sh->none[slot][i] = none;
             }
-            if (!ok) break;
-            page = next;
+            if (v.lost) record_status(a.status, kStBadIndex);
+            mbar_arrive_expect_tx(&c.sh->full[slot], v.bytes + k.bytes);
         }
+        __syncwarp();
+        copy(k, k_map, c.k_ring + (g + S::kAhead) % S::NK * S::kSlot, &c.sh->full[slot]);
+        copy(v, v_map, c.v_ring + slot * S::kSlot, &c.sh->full[slot]);
     }
     // The last copies have landed before shared memory is given up, after an abort too.
-    const uint32_t asked = 2 * n, back = asked < (uint32_t)S::kSlots ? asked : S::kSlots;
-    for (uint32_t i = asked - back; i < asked; ++i)
-        mbar_wait(&c.sh->full[i % S::kSlots], i / S::kSlots & 1, kDrainPolls);
+    if (S::kAhead) mbar_wait(&c.sh->first, 0, kDrainPolls);
+    for (uint32_t i = g < (uint32_t)S::NV ? 0 : g - S::NV; i < g; ++i)
+        mbar_wait(&c.sh->full[i % S::NV], i / S::NV & 1, kDrainPolls);
 }
 
-// The same by cp.async and three warps for pages of any size; a tile's barriers are arrived at
-// when the next one is under way and it has landed.  Slots beyond the live ones and in pages out
+// The same by cp.async and two warps for pages of any size; a step's barrier is arrived at once it
+// has landed, when the next one is under way or has to wait.  Slots beyond the live ones and in pages out
 // of range are zeros.
 template <typename S>
 __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
     constexpr int kLanes = S::DP / 8;         // 16-byte chunks, a lane each, of a row
     constexpr int kRows = 32 / kLanes;        // rows of a warp's copy
     constexpr int kGroups = S::KT / 32;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 9;
-    Walk walk(room, blockIdx.x);
-    Stretch st;
-    uint32_t n = 0;         // tiles asked for
-    uint32_t landed = 0;    // tiles whose barriers were arrived at
-    bool ok = true;
-    auto land = [&]() {
-        fence_proxy_async_smem();
-        mbar_arrive(&c.sh->full[2 * landed % S::kSlots]);
-        mbar_arrive(&c.sh->full[(2 * landed + 1) % S::kSlots]);
-        ++landed;
-    };
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoft / 32 - 1;
     const int chunk = lane % kLanes;
     const bool in_dim = chunk * 8 < kv.head_dim;
-    while (ok && walk.next(st)) {
-        const int len = st.tile.q.len, seq = st.tile.seq;
-        int page[kGroups];  // of this lane's rows: lane + 32 g
+    struct Rows {
+        int page[kGroups], j, head;  // of this lane's rows: lane + 32 i
+    };
+    Stream<S> in(room);
+    auto ask = [&]() {
+        Rows x;
+        x.j = in.kt * S::KT + lane, x.head = in.st.head;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            page[g] = page_of(kv, seq, st.k0 * S::KT + 32 * g + lane, len);
-        for (int kt = st.k0; kt < st.k1; ++kt, ++n) {
-            int next[kGroups];
+        for (int i = 0; i < kGroups; ++i)
+            x.page[i] = in.more ? page_of(kv, in.seq, x.j + 32 * i, in.len) : -2;
+        return x;
+    };
+    auto copy = [&](const Rows &x, const char *pool, uint32_t ring) {
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-                next[g] = kt + 1 < st.k1
-                              ? page_of(kv, seq, (kt + 1) * S::KT + 32 * g + lane, len) : -2;
-            const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
-            const uint32_t kp = (2 * n / S::kSlots & 1) ^ 1, vp = ((2 * n + 1) / S::kSlots & 1) ^ 1;
-            if (!c.warp_wait(&c.sh->empty[ks], kp) || !c.warp_wait(&c.sh->empty[vs], vp)) {
+        for (int i = 0; i < kGroups; ++i) {
+            const int j = x.j + 32 * i;
+            const int row_in = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
+            const long long at = (unsigned)x.page[i] < (unsigned)kv.n_pages
+                                     ? (long long)x.page[i] * kv.page_stride +
+                                           (long long)x.head * kv.head_stride +
+                                           (long long)row_in * kv.token_stride
+                                     : -1;
+            for (int k = warp; k < 32 / kRows; k += kLoaders / 32) {
+                const int r = k * kRows + lane / kLanes, row = 32 * i + r;
+                const long long from = __shfl_sync(0xFFFFFFFFu, at, r);
+                const bool live = from >= 0 && in_dim;
+                cp16(ring + (chunk >> 3) * (S::KT * 128) + row * 128 +
+                         (((chunk & 7) ^ (row & 7)) << 4),
+                     pool + (live ? from + chunk * 16 : 0), live);
+            }
+        }
+    };
+    if (!in.more) return;
+    Rows cur = ask();
+    if (S::kAhead) {
+        copy(cur, kv.k, c.k_ring);
+        cp_commit();
+        cp_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(&c.sh->first);
+    }
+    uint32_t g = 0, landed = 0;
+    auto land = [&]() {
+        fence_proxy_async_smem();
+        mbar_arrive(&c.sh->full[landed++ % S::NV]);
+    };
+    bool ok = true;
+    for (bool some = true; some; ++g) {
+        const Rows v = cur;
+        in.next();
+        some = in.more;
+        cur = ask();
+        const uint32_t slot = g % S::NV;
+        if (g >= (uint32_t)S::NV) {
+            uint64_t *const bar = &c.sh->done[slot];
+            const uint32_t turn = (g / S::NV & 1) ^ 1;
+            // What it waits for may wait for the step before.
+            if (landed < g && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, turn))) {
+                cp_wait<0>();
+                land();
+            }
+            if (!c.warp_wait(bar, turn)) {
                 ok = false;
                 break;
             }
-            const uint32_t k_to = c.ring + ks * S::kSlot, v_to = c.ring + vs * S::kSlot;
+        }
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int j = kt * S::KT + 32 * g + lane;
-                const bool there = (unsigned)page[g] < (unsigned)kv.n_pages;
-                const uint32_t none = __ballot_sync(0xFFFFFFFFu, !there && page[g] != -2);
-                if (warp == 0 && lane == 0) {
-                    c.sh->none[vs][g] = none;
-                    if (none) record_status(a.status, kStBadIndex);
-                }
-                const int in = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
-                const long long at = there ? (long long)page[g] * kv.page_stride +
-                                                 (long long)st.head * kv.head_stride +
-                                                 (long long)in * kv.token_stride
-                                           : -1;
-                for (int i = warp; i < 32 / kRows; i += 3) {
-                    const int r = i * kRows + lane / kLanes, row = 32 * g + r;
-                    const long long from = __shfl_sync(0xFFFFFFFFu, at, r);
-                    const bool live = from >= 0 && in_dim;
-                    const long long src = live ? from + chunk * 16 : 0;
-                    const uint32_t to = (chunk >> 3) * (S::KT * 128) + row * 128 +
-                                        (((chunk & 7) ^ (row & 7)) << 4);
-                    cp16(k_to + to, kv.k + src, live);
-                    cp16(v_to + to, kv.v + src, live);
-                }
-                page[g] = next[g];
+        for (int i = 0; i < kGroups; ++i) {
+            const uint32_t none = __ballot_sync(
+                0xFFFFFFFFu, (unsigned)v.page[i] >= (unsigned)kv.n_pages && v.page[i] != -2);
+            if (warp == 0 && lane == 0) {
+                c.sh->none[slot][i] = none;
+                if (none) record_status(a.status, kStBadIndex);
             }
-            cp_commit();
-            if (n > landed) {
-                cp_wait<1>();
-                land();
-            }
+        }
+        if (!S::kAhead || some)
+            copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlot);
+        copy(v, kv.v, c.v_ring + slot * S::kSlot);
+        cp_commit();
+        if (landed < g) {
+            cp_wait<1>();
+            land();
         }
     }
     cp_wait<0>();
-    while (ok && landed < n) land();
+    while (ok && landed < g) land();
+}
+
+// q of a stretch of 16-bit queries, by one warp, while the stretch before ends: its place is free when
+// the last scores are done.
+template <typename S>
+__device__ void load_queries(const TokensArgs &a, const KvView &kv, const Room &room,
+                             const Ctx &c) {
+    constexpr int kChunks = S::DP / 8;
+    const int lane = threadIdx.x & 31, group = a.group.d;
+    Walk walk(room, blockIdx.x);
+    Stretch st;
+    uint32_t n = 0;
+    while (walk.next(st)) {
+        if (st.k0 == st.k1) continue;
+        const Tile *const tile = room.tiles + st.tile;
+        const int row0 = tile->row0, t0 = tile->q.t0, rows = tile->q.count * group - row0;
+        if (n > 0 && !c.warp_wait(&c.sh->q_free, (n - 1) & 1)) return;
+#pragma unroll 4
+        for (int i = lane; i < S::RT * kChunks; i += 32) {
+            const int r = i / kChunks, ch = i % kChunks;
+            const bool live = r < rows && ch * 8 < kv.head_dim;
+            const int rr = row0 + r, j = a.group.div(live ? rr : 0), h = rr - j * group;
+            const long long at = (t0 + j) * a.q_stride +
+                                 (long long)(st.head * group + h) * kv.head_dim + ch * 8;
+            // Row r of its tile of 128 rows.
+            cp16(c.stage + (r >> 7) * (128 * S::DP * 2) + (ch >> 3) * S::kHalf + (r & 127) * 128 +
+                     (((ch & 7) ^ (r & 7)) << 4),
+                 static_cast<const uint16_t *>(a.q) + (live ? at : 0), live);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_proxy_async_smem();
+        c.warp_arrive(&c.sh->q_ready);
+        ++n;
+    }
 }
 
 // ------------------------------------------------------------------------ MMA warp --
+//
+// A wait that is over takes this thread 100 cycles, a commit 50 and the second in a row 360, in
+// which no product is issued (64 cycles each): it has one wait for a step and one for each
+// warpgroup's p.  That a tile's products are over, the second warpgroup sees by its next scores
+// (pairs: it says done), or a commit of its own tells (one row tile, where loads bound it and
+// should not wait for scores).
 
 template <typename S>
 __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx &c) {
@@ -386,15 +494,19 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
     Walk walk(room, blockIdx.x);
     Stretch st;
     uint32_t base = 0;                 // tiles before this stretch
-    uint32_t stretches = 0;
-    uint32_t done[2] = {0, 0};         // tiles of each warpgroup whose P was taken
+    uint32_t stretches = 0, seen = 0;  // seen: steps that have been waited for
+    uint32_t taken = 0;                // parity of each warpgroup's p
     constexpr uint32_t kId = idesc_of<S::ET>(S::KT, false), vId = idesc_of<S::ET>(S::DP, true);
 
-    auto slot_full = [&](uint32_t i) {
-        return c.wait(&c.sh->full[i % S::kSlots], i / S::kSlots & 1);
+    auto step = [&](uint32_t g) {
+        if (g < seen) return true;
+        if (!c.wait(&c.sh->full[g % S::NV], g / S::NV & 1)) return false;
+        tc_fence_after();
+        seen = g + 1;
+        return true;
     };
     auto scores = [&](int wg, uint32_t tile) {  // S of a warpgroup from the tile's k
-        const uint32_t k = desc_low(c.ring + 2 * tile % S::kSlots * S::kSlot, 16);
+        const uint32_t k = desc_low(c.k_ring + tile % S::NK * S::kSlot, 16);
         uint32_t accum = 0;
 #pragma unroll
         for (int t = S::TERMS - 1; t >= 0; --t) {
@@ -411,10 +523,14 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
         }
         tc_commit(&c.sh->s_full[wg]);
     };
-    auto values = [&](int wg, uint32_t tile) {  // P V of a warpgroup from the tile's v
-        const uint32_t v =
-            desc_low(c.ring + (2 * tile + 1) % S::kSlots * S::kSlot, S::KT * 128);
+    // P V of a warpgroup from the tile's v.  That it is over shows by the next scores; `last` has
+    // none.
+    auto values = [&](int wg, uint32_t tile, bool last) {
+        const uint32_t v = desc_low(c.v_ring + tile % S::NV * S::kSlot, S::KT * 128);
         uint32_t accum = S::TERMS == 1;  // on top of the output, which began as zeros
+        if (!c.wait(&c.sh->p_ready[wg], taken >> wg & 1)) return false;
+        taken ^= 1u << wg;
+        tc_fence_after();
 #pragma unroll
         for (int t = S::TERMS - 1; t >= 0; --t) {
             const uint32_t p = tmem + wg * 256 + (t == 0 ? kColP0 : t == 1 ? kColP1 : kColP2);
@@ -424,7 +540,8 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
                 accum = 1;
             }
         }
-        tc_commit(&c.sh->t_full[wg]);
+        if (S::TERMS > 1 || last) tc_commit(&c.sh->t_full[wg]);
+        return true;
     };
     while (walk.next(st)) {
         const int n = st.k1 - st.k0;
@@ -432,45 +549,41 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
         if (!c.wait(&c.sh->q_ready, stretches++ & 1)) return;
         tc_fence_after();
         if (S::PAIR) {
-            if (!slot_full(2 * base)) return;
+            // k of the stretch's first tile came with the step before.
+            if (base == 0 && !c.wait(&c.sh->first, 0)) return;
             tc_fence_after();
             scores(0, base);
             scores(1, base);
-            tc_commit(&c.sh->empty[2 * base % S::kSlots]);
+            if (n == 1) tc_commit(&c.sh->q_free);
             for (int i = 0; i < n; ++i) {
                 const uint32_t tile = base + i;
-                if (!slot_full(2 * tile + 1)) return;
-                if (i + 1 < n && !slot_full(2 * tile + 2)) return;
+                const bool last = i + 1 == n;
+                if (!step(tile)) return;
 #pragma unroll
                 for (int wg = 0; wg < 2; ++wg) {
-                    if (!c.wait(&c.sh->p_ready[wg], done[wg]++ & 1)) return;
-                    tc_fence_after();
-                    values(wg, tile);
-                    if (i + 1 < n) scores(wg, tile + 1);
+                    if (!values(wg, tile, last)) return;
+                    if (!last) scores(wg, tile + 1);
                 }
-                tc_commit(&c.sh->empty[(2 * tile + 1) % S::kSlots]);
-                if (i + 1 < n) tc_commit(&c.sh->empty[(2 * tile + 2) % S::kSlots]);
+                if (i + 2 == n) tc_commit(&c.sh->q_free);
             }
         } else {
-            for (int i = 0; i < 2 && i < n; ++i) {
-                if (!slot_full(2 * (base + i))) return;
-                tc_fence_after();
-                scores(i, base + i);
-                tc_commit(&c.sh->empty[2 * (base + i) % S::kSlots]);
+            if (!step(base)) return;
+            scores(0, base);
+            if (n > 1) {
+                if (!step(base + 1)) return;
+                scores(1, base + 1);
             }
+            if (n <= 2) tc_commit(&c.sh->q_free);
             for (int i = 0; i < n; ++i) {
                 const uint32_t tile = base + i;
                 const int wg = i & 1;
-                if (!slot_full(2 * tile + 1)) return;
-                if (!c.wait(&c.sh->p_ready[wg], done[wg]++ & 1)) return;
-                tc_fence_after();
-                values(wg, tile);
-                tc_commit(&c.sh->empty[(2 * tile + 1) % S::kSlots]);
-                if (i + 2 < n) {
-                    if (!slot_full(2 * tile + 4)) return;
-                    tc_fence_after();
+                const bool last = i + 2 >= n;
+                if (!values(wg, tile, last)) return;
+                tc_commit(&c.sh->done[tile % S::NV]);
+                if (!last) {
+                    if (!step(tile + 2)) return;
                     scores(wg, tile + 2);
-                    tc_commit(&c.sh->empty[(2 * tile + 4) % S::kSlots]);
+                    if (i + 3 == n) tc_commit(&c.sh->q_free);
                 }
             }
         }
@@ -480,103 +593,131 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
 
 // -------------------------------------------------------------- softmax warpgroups --
 
-template <typename S>
-__device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, const Seq &q,
-                                       const Stretch &st, const Ctx &c, int first, int count,
-                                       int thread, int threads) {
-    constexpr int kChunks = S::DP / 8;
-    const int group = a.group.d, rows = q.count * group - st.tile.row0, d = kv.head_dim;
-    for (int i = thread; i < count * kChunks; i += threads) {
-        const int r = first + i / kChunks, ch = i % kChunks;
-        const bool live = r < rows && ch * 8 < d;
-        const int rr = st.tile.row0 + r, j = a.group.div(live ? rr : 0), g = rr - j * group;
-        const long long at =
-            (q.t0 + j) * a.q_stride + (long long)(st.head * group + g) * d + ch * 8;
-        // Row r of its tile of 128 rows.
-        const uint32_t to = c.stage + (r >> 7) * (128 * S::DP * 2) + (ch >> 3) * S::kHalf +
-                            (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        if (S::TERMS == 1) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (live) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
-            sts16(to, v);
-        } else {
-            float x[8] = {};
-            if (live) {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at);
-                const float4 u = p[0], v = p[1];
-                x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-                x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-            }
+// COUNT rows of q from row `first` by THREADS threads.
+template <typename S, int COUNT, int THREADS>
+__device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, const Tile &tile,
+                                       int head, const Ctx &c, int first, int thread) {
+    constexpr int kChunks = S::DP / 8, kItems = COUNT * kChunks / THREADS;
+    constexpr int kBatch = S::TERMS == 1 ? (kItems < 8 ? kItems : 8) : 2;  // loads in flight
+    const int group = a.group.d, row0 = tile.row0, t0 = tile.q.t0, d = kv.head_dim;
+    const int rows = tile.q.count * group - row0;
+#pragma unroll 1
+    for (int b = 0; b < kItems; b += kBatch) {
+        uint4 x[kBatch][S::TERMS == 1 ? 1 : 2];
+        uint32_t to[kBatch];
 #pragma unroll
-            for (int t = 0; t < S::TERMS; ++t) {
-                uint32_t w[4];
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = thread + (b + k) * THREADS;
+            const int r = first + i / kChunks, ch = i % kChunks;
+            const bool live = r < rows && ch * 8 < d;
+            const int rr = row0 + r, j = a.group.div(live ? rr : 0);
+            const int g = rr - j * group;
+            const long long at =
+                (t0 + j) * a.q_stride + (long long)(head * group + g) * d + ch * 8;
+            // Row r of its tile of 128 rows.
+            to[k] = c.stage + (r >> 7) * (128 * S::DP * 2) + (ch >> 3) * S::kHalf +
+                    (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+            const char *const from =
+                static_cast<const char *>(a.q) + at * (S::TERMS == 1 ? 2 : 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = pack2<kBF16>(x[2 * e], x[2 * e + 1]);
-                    x[2 * e] -= bf16_lo(w[e]);
-                    x[2 * e + 1] -= bf16_hi(w[e]);
+            for (int h = 0; h < (S::TERMS == 1 ? 1 : 2); ++h)
+                x[k][h] = live ? reinterpret_cast<const uint4 *>(from)[h]
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if constexpr (S::TERMS == 1) {
+                sts16(to[k], x[k][0]);
+            } else {
+                float y[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    y[4 * h] = __uint_as_float(x[k][h].x), y[4 * h + 1] = __uint_as_float(x[k][h].y);
+                    y[4 * h + 2] = __uint_as_float(x[k][h].z);
+                    y[4 * h + 3] = __uint_as_float(x[k][h].w);
                 }
-                sts16(to + t * S::kQTerm, make_uint4(w[0], w[1], w[2], w[3]));
+#pragma unroll
+                for (int t = 0; t < S::TERMS; ++t) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = pack2<kBF16>(y[2 * e], y[2 * e + 1]);
+                        y[2 * e] -= bf16_lo(w[e]);
+                        y[2 * e + 1] -= bf16_hi(w[e]);
+                    }
+                    sts16(to[k] + t * S::kQTerm, make_uint4(w[0], w[1], w[2], w[3]));
+                }
             }
         }
     }
 }
 
 // tanh of the cap for f32 queries, within a few 2^-24 of itself: Lambert's continued fraction cut to
-// z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4) (off by 2e-9 at 0.5), beyond it by exponentials.
+// z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4) up to 0.5 (off by 2e-9 there), beyond it
+// (e - 1) / (e + 1) with e = exp(2 z); one division, no branch, NaN stays NaN.
 __device__ __forceinline__ float fine_tanh(float x) {
     const float z = x * x;
-    const float small = x * fmaf(z, z + 105.f, 945.f) / fmaf(z, fmaf(z, 15.f, 420.f), 945.f);
-    return z < 0.25f ? small : fast_tanh(x);
+    const float held = x > 10.f ? 10.f : x < -10.f ? -10.f : x;  // tanh is 1 to 2^-27 there
+    const float e = ex2(held * (2.f * kLog2e));
+    const float n0 = x * fmaf(z, z + 105.f, 945.f), d0 = fmaf(z, fmaf(z, 15.f, 420.f), 945.f);
+    const bool small = z < 0.25f;
+    const float n = small ? n0 : e - 1.f, d = small ? d0 : e + 1.f;
+    return __fdividef(n, d);
 }
 
-// A softmax thread's row of a stretch, and what the two kinds of softmax share.
+// A softmax thread's row, and what the two kinds of softmax share.  What only border tiles and a
+// stretch's end ask for is worked out there again: a tile's scores want the registers (spills go
+// to L2: shared memory has taken L1).
 template <typename S> struct Row {
     static constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
     static constexpr int kParts = DP / 64;             // rows of 128 bytes of a v
-    static constexpr int kScan = S::PAIR ? 256 : 128;  // threads that look through a v tile
+    static constexpr int kScan = S::PAIR ? kSoft : kTeam;  // threads that look through a v
+    // Rows of 128 bytes to a thread, or threads to a row.
     static constexpr int kEach = KT * kParts > kScan ? KT * kParts / kScan : 1;
+    static constexpr int kPieces = KT * kParts > kScan ? 1 : kScan / (KT * kParts);
     const TokensArgs &a;
     const KvView &kv;
     const Ctx &c;
-    Shared *const sh;
-    const int wg, r, row;  // row of the row tile
-    const uint32_t tm;     // the warpgroup's columns, this warp's lanes
-    const bool formed;     // more than a positive scale: worked out once, written back in log2 units
+    const Tile *tile;    // of the stretch
+    int head;
+    const uint32_t tm;   // the warpgroup's columns, this warp's lanes
     const float to_log2;
-    uint32_t met[2] = {0, 0}, odd_turn = 0;
-    // Of the stretch:
-    Seq q;
-    See see;
-    float slope;
-    bool live;
-    int t, h;
+    uint32_t turns = 0;  // parities of meet(0) and meet(1), and bit 3 of look()
 
     __device__ __forceinline__ Row(const TokensArgs &a_, const KvView &kv_, const Ctx &c_)
-        : a(a_), kv(kv_), c(c_), sh(c_.sh), wg(threadIdx.x >> 7), r(threadIdx.x & 127),
-          row(S::PAIR ? threadIdx.x : threadIdx.x & 127),
-          tm(c_.sh->tmem + ((threadIdx.x & 96u) << 16) + (threadIdx.x >> 7) * 256),
-          formed(a_.softcap > 0.f || a_.slopes || !(a_.scale > 0.f)),
-          to_log2(formed ? 1.f : a_.scale * kLog2e) {}
+        : a(a_), kv(kv_), c(c_), tm(c_.sh->tmem + ((threadIdx.x & 96u) << 16) + wg() * 256),
+          to_log2(formed() ? 1.f : a_.scale * kLog2e) {}
 
-    __device__ __forceinline__ void begin(const Stretch &st) {
-        q = st.tile.q;
-        const int group = a.group.d;
-        live = row < min(S::RT, q.count * group - st.tile.row0);
-        const int rr = st.tile.row0 + (live ? row : 0), j = a.group.div(rr), g = rr - j * group;
-        see = See{};
-        if (live) see = see_of(a, q, st.tile.seq, j);
-        slope = a.slopes ? a.slopes[st.head * group + g] * kLog2e : 0.f;
-        t = q.t0 + j, h = st.head * group + g;
+    __device__ __forceinline__ static int wg() { return threadIdx.x / kTeam; }
+    __device__ __forceinline__ static int r() { return threadIdx.x & 127; }
+    __device__ __forceinline__ static int row() { return S::PAIR ? wg() * 128 + r() : r(); }
+    // More than a positive scale: worked out once, written back in log2 units.
+    __device__ __forceinline__ bool formed() const {
+        return a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
+    }
+    // The row's place: token of the sequence and query head; false beyond the tile's rows.
+    __device__ __forceinline__ bool place(int &j, int &h) const {
+        const int group = a.group.d, rr = tile->row0 + row();
+        const bool live = rr < tile->q.count * group;
+        j = a.group.div(live ? rr : 0);
+        h = head * group + (live ? rr : 0) - j * group;
+        return live;
+    }
+    __device__ __forceinline__ See see() const {
+        int j, h;
+        return place(j, h) ? see_of(a, tile->q, tile->seq, j) : See{};
     }
     // 0: both warpgroups; 1: those that look through a v tile together.
     __device__ __forceinline__ bool meet(int which) {
-        uint64_t *const bar = &sh->meet[S::PAIR || which == 0 ? 0 : 1 + wg];
-        const uint32_t turn = met[S::PAIR ? 0 : which]++;
-        mbar_arrive(bar);
-        return c.warp_wait(bar, turn & 1);
+        uint64_t *const bar = &c.sh->meet[S::PAIR || which == 0 ? 0 : 1 + wg()];
+        const int bit = S::PAIR ? 0 : which;
+        const uint32_t turn = turns >> bit & 1;
+        turns ^= 1u << bit;
+        c.warp_arrive(bar);
+        return c.warp_wait(bar, turn);
     }
-    // Scores in tensor memory to log2 units after cap and bias, those that are not seen to -inf.
+    // This thread's scores in tensor memory to log2 units after cap and bias, those that are not
+    // seen to -inf.
     __device__ __forceinline__ void form(int j0, bool mixed, const uint32_t *none) {
 #pragma unroll 1
         for (int ch = 0; ch < kChunks; ++ch) {
@@ -584,27 +725,35 @@ template <typename S> struct Row {
             uint32_t v[32];
             ld32(v, tm + kColS + 32 * ch);
             wait_ld(v);
-            if (formed) {
-                const bool own = a.pos && jc + 32 > q.base;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float y = __uint_as_float(v[e]) * a.scale;
-                    if (a.softcap > 0.f) {
-                        const float z = __fdividef(y, a.softcap);
-                        y = a.softcap * (S::TERMS == 1 ? fast_tanh(z) : fine_tanh(z));
-                    }
-                    v[e] = __float_as_uint(y * kLog2e);
-                }
-                if (a.slopes) {
+            if (formed()) {
+                if (a.softcap > 0.f) {
+                    const float in = a.scale / a.softcap, out = a.softcap * kLog2e;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const int far = (own ? slot_pos(a, q, jc + e) : jc + e) - see.pos;
+                        const float z = __uint_as_float(v[e]) * in;
+                        v[e] = __float_as_uint(out * (S::TERMS == 1 ? fast_tanh(z) : fine_tanh(z)));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) * a.scale * kLog2e);
+                }
+                if (a.slopes) {
+                    int j, h;
+                    place(j, h);
+                    const float slope = a.slopes[h] * kLog2e;
+                    const Seq q = tile->q;
+                    const bool own = a.pos && jc + 32 > q.base;
+                    const int pos = a.pos ? near(a.pos[q.t0 + j]) : q.base + j;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int far = (own ? slot_pos(a, q, jc + e) : jc + e) - pos;
                         v[e] = __float_as_uint(fmaf(slope, (float)far, __uint_as_float(v[e])));
                     }
                 }
             }
             if (mixed) {
-                const uint32_t in = seen32(a, see, jc) & ~none[ch];
+                const uint32_t in = seen32(a, see(), jc) & ~none[ch];
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     if (!(in >> e & 1u)) v[e] = 0xFF800000u;
@@ -616,38 +765,50 @@ template <typename S> struct Row {
     // Finds the slots of a v tile that are not finite; `any` is the same for all that look.
     struct Odd {
         uint32_t any, *words;
-        bool mine;
     };
+    // The slot, and the first of its rows of 128 bytes or the piece of one, of a thread that looks.
+    struct Line {
+        int at, slot, part, piece;
+    };
+    __device__ __forceinline__ Line line() const {
+        Line n;
+        n.at = S::PAIR ? threadIdx.x : threadIdx.x % kTeam;
+        n.slot = n.at % KT;
+        const int rest = n.at / KT;
+        n.part = kEach > 1 ? rest * kEach : rest % kParts;
+        n.piece = kEach > 1 ? 0 : rest / kParts;
+        return n;
+    }
     __device__ __forceinline__ bool look(uint32_t v_at, Odd &o) {
-        const int at = S::PAIR ? threadIdx.x : r;
-        const int slot = at % KT, part0 = at / KT, scan_warp = at >> 5;
-        o.mine = false;
-        if (part0 < kParts) {
+        const Line n = line();
+        bool mine = false;
 #pragma unroll 1
-            for (int p = 0; p < kEach; ++p) {
-                const uint32_t line = v_at + (part0 + p) * (KT * 128) + slot * 128;
+        for (int p = 0; p < kEach; ++p) {
+            const uint32_t at = v_at + (n.part + p) * (KT * 128) + n.slot * 128;
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    const uint4 w = lds16(line + (((ch + slot) & 7) << 4));
-                    o.mine |= odd16x2<S::ET>(w.x) || odd16x2<S::ET>(w.y) ||
-                              odd16x2<S::ET>(w.z) || odd16x2<S::ET>(w.w);
-                }
+            for (int ch = 0; ch < 8 / kPieces; ++ch) {
+                const uint4 w = lds16(at + (((ch + n.piece * (8 / kPieces) + n.slot) & 7) << 4));
+                mine |= odd16x2<S::ET>(w.x) || odd16x2<S::ET>(w.y) || odd16x2<S::ET>(w.z) ||
+                        odd16x2<S::ET>(w.w);
             }
         }
-        const uint32_t found = __ballot_sync(0xFFFFFFFFu, o.mine);
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, mine);
         // Two sets taken in turn: a warpgroup may be a tile ahead of the other's reading.
-        o.words = &sh->odd[S::PAIR ? odd_turn++ & 1 : wg][0][0];
-        if ((threadIdx.x & 31) == 0)
-            o.words[scan_warp * 32 / KT * 4 + scan_warp * 32 % KT / 32] = found;
+        o.words = &c.sh->odd[S::PAIR ? turns >> 3 & 1 : wg()][0][0];
+        turns ^= 8u;
+        if ((threadIdx.x & 31) == 0) o.words[n.at / KT * 4 + n.slot / 32] = found;
+        tc_fence_before();
         if (!meet(1)) return false;
+        tc_fence_after();
         o.any = 0;
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) o.any |= word(o, ch);
         return true;
     }
     __device__ __forceinline__ static uint32_t word(const Odd &o, int ch) {
-        uint32_t w = o.words[ch];
-        if (kScan / KT > 1 && kParts > 1) w |= o.words[4 + ch];
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < kScan / KT; ++i) w |= o.words[4 * i + ch];
         return w;
     }
     // f(slot, p) for each of them that the row sees, p its weight against the maximum `safe`; every
@@ -657,7 +818,7 @@ template <typename S> struct Row {
                                              F f) {
 #pragma unroll 1
         for (int ch = 0; ch < kChunks; ++ch) {
-            const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~none[ch];
+            const uint32_t in = seen32(a, see(), j0 + 32 * ch) & ~none[ch];
 #pragma unroll 1
             for (uint32_t left = word(o, ch); left; left &= left - 1) {
                 const int b = __ffs(left) - 1;
@@ -677,51 +838,107 @@ template <typename S> struct Row {
     }
     // Takes those slots out of the tile once every row has them.
     __device__ __forceinline__ bool clear(uint32_t v_at, const Odd &o) {
+        tc_fence_before();
         if (!meet(1)) return false;
-        const int at = S::PAIR ? threadIdx.x : r;
-        const int slot = at % KT, part0 = at / KT;
-        if (word(o, slot >> 5) >> (slot & 31) & 1u) {
+        tc_fence_after();
+        const Line n = line();
+        if (word(o, n.slot >> 5) >> (n.slot & 31) & 1u) {
 #pragma unroll 1
-            for (int p = 0; p < kEach && part0 + p < kParts; ++p)
+            for (int p = 0; p < kEach; ++p)
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch)
-                    sts16(v_at + (part0 + p) * (KT * 128) + slot * 128 + ch * 16,
+                for (int ch = 0; ch < 8 / kPieces; ++ch)
+                    sts16(v_at + (n.part + p) * (KT * 128) + n.slot * 128 +
+                              (ch + n.piece * (8 / kPieces)) * 16,
                           make_uint4(0u, 0u, 0u, 0u));
         }
         fence_proxy_async_smem();
         return true;
     }
-    // Dims e .. e + 7 of the row's result.
-    __device__ __forceinline__ void put8(int e, const float (&x)[8]) const {
-        if (e >= kv.head_dim) return;
-        const long long to = t * a.out_stride + (long long)h * kv.head_dim + e;
-        if (a.out_type == kF32) {
-            float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
-            p[0] = make_float4(x[0], x[1], x[2], x[3]);
-            p[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + to) =
-                make_uint4(pack2<S::ET>(x[0], x[1]), pack2<S::ET>(x[2], x[3]),
-                           pack2<S::ET>(x[4], x[5]), pack2<S::ET>(x[6], x[7]));
+    // The two warpgroups' halves of the slots, their outputs in tensor memory: each writes half of
+    // the dims.
+    __device__ __forceinline__ bool join(const Room &room, const Stretch &st, bool any, bool live,
+                                         int j, int h, float m, float l) {
+        c.sh->ml[wg()][r()] = make_float2(m, l);
+        wait_st();
+        tc_fence_before();
+        if (!meet(0)) return false;
+        tc_fence_after();
+        const float2 x0 = c.sh->ml[0][r()], x1 = c.sh->ml[1][r()];
+        const float both = fmaxf(x0.x, x1.x), safe = both == -INFINITY ? 0.f : both;
+        const float f0 = ex2(x0.x - safe), f1 = ex2(x1.x - safe);
+        const float sum = fmaf(x0.y, f0, x1.y * f1);
+        const uint32_t t0 = tm - wg() * 256 + kColT, t1 = t0 + 256;
+#pragma unroll 1
+        for (int ch = wg() * (DP / 64); ch < (wg() + 1) * (DP / 64); ++ch) {
+            uint32_t v[32] = {}, u[32] = {};
+            if (any) {
+                ld32(v, t0 + 32 * ch);
+                ld32(u, t1 + 32 * ch);
+                wait_ld(v);
+                wait_ld(u);
+            }
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                x[e] = fmaf(__uint_as_float(v[e]), f0, __uint_as_float(u[e]) * f1);
+            if (live) finish(room, st, j, h, both, sum, 32 * ch, x);
+            __syncwarp();
         }
+        tc_fence_before();
+        if (!meet(0)) return false;  // both have read both
+        tc_fence_after();
+        return true;
     }
-    // Dims e .. e + 7 of the row's sums: its result, or its part.
-    __device__ __forceinline__ void finish(const Room &room, const Stretch &st, float m, float l,
-                                           int e, const float (&x)[8]) const {
+    // Dims e .. e + 31 of the row's sums: its result, or its part.
+    __device__ __forceinline__ void finish(const Room &room, const Stretch &st, int j, int h, float m,
+                                           float l, int e, float (&x)[32]) const {
         if (st.part >= 0) {
             const size_t part = 2 * blockIdx.x + st.part;
-            room.part_o[(part * (DP / 4) + e / 4) * S::RT + row] =
-                make_float4(x[0], x[1], x[2], x[3]);
-            room.part_o[(part * (DP / 4) + e / 4 + 1) * S::RT + row] =
-                make_float4(x[4], x[5], x[6], x[7]);
-            if (e == 0) room.part_ml[part * S::RT + row] = make_float2(m, l);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+                room.part_o[(part * (DP / 4) + (e + k) / 4) * S::RT + row()] =
+                    make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+            if (e == 0) room.part_ml[part * S::RT + row()] = make_float2(m, l);
             return;
         }
+        const int t = tile->q.t0 + j;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        float y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = x[k] * inv;
-        put8(e, y);
+        for (int k = 0; k < 32; ++k) x[k] *= inv;
+        const long long to = t * a.out_stride + (long long)h * kv.head_dim + e;
+        if (a.out_type == kF32) {
+            float *const p = static_cast<float *>(a.out) + to;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                if (e + k >= kv.head_dim) break;
+                reinterpret_cast<float4 *>(p + k)[0] = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                reinterpret_cast<float4 *>(p + k)[1] =
+                    make_float4(x[k + 4], x[k + 5], x[k + 6], x[k + 7]);
+            }
+        } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = pack2<S::ET>(x[2 * k], x[2 * k + 1]);
+            uint16_t *const p = static_cast<uint16_t *>(a.out) + to;
+            if (a.wide_out) {  // 32 bytes at a time: whole sectors
+#pragma unroll
+                for (int k = 0; k < 16; k += 8) {
+                    if (e + 2 * k >= kv.head_dim) break;
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                     p + 2 * k),
+                                 "r"(w[k]), "r"(w[k + 1]), "r"(w[k + 2]), "r"(w[k + 3]),
+                                 "r"(w[k + 4]), "r"(w[k + 5]), "r"(w[k + 6]), "r"(w[k + 7])
+                                 : "memory");
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    if (e + 2 * k >= kv.head_dim) break;
+                    *reinterpret_cast<uint4 *>(p + 2 * k) =
+                        make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                }
+            }
+        }
         if (e == 0 && a.lse) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
     }
 };
@@ -745,45 +962,47 @@ template <typename S>
 __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
     constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
     constexpr float kGrow = 8.f;  // p is at most 2^8: f16 holds it, and its sum
-    Row<S> w(a, kv, c);
+    using R = Row<S>;
+    R w(a, kv, c);
     Shared *const sh = c.sh;
     Walk walk(room, blockIdx.x);
     Stretch st;
-    uint32_t base = 0, mine = 0;  // tiles before this stretch; tiles of this warpgroup
-    bool again = false;
+    // Tiles before this stretch, tiles of this warpgroup, stretches in which it had any.
+    uint32_t base = 0, mine = 0, ended = 0;
     while (walk.next(st)) {
         __syncwarp();
-        w.begin(st);
+        w.tile = room.tiles + st.tile;
+        w.head = st.head;
         const int n = st.k1 - st.k0;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;  // the row's maximum in use, its sum
         bool some = false;
         if (n > 0) {
-            if (!S::PAIR && again && !w.meet(0)) return;  // the last stretch's join was read
-            again = true;
             uint32_t zero[32] = {};
 #pragma unroll
             for (int ch = 0; ch < DP / 32; ++ch) st32(w.tm + kColT + 32 * ch, zero);
-            if (S::PAIR)
-                load_q<S>(a, kv, w.q, st, c, w.wg * 128, 128, w.r, 128);
-            else
-                load_q<S>(a, kv, w.q, st, c, 0, 128, threadIdx.x, 256);
-            fence_proxy_async_smem();
-            mbar_arrive(&sh->q_ready);
         }
-        for (int i = S::PAIR ? 0 : w.wg; i < n; i += S::PAIR ? 1 : 2) {
-            const uint32_t vi = 2 * (base + i) + 1, vs = vi % S::kSlots;
-            if (!c.warp_wait(&sh->full[vs], vi / S::kSlots & 1)) return;
-            if (!c.warp_wait(&sh->s_full[w.wg], mine & 1)) return;
-            tc_fence_after();
+        const int lo = w.tile->lo, hi = w.tile->hi;  // every row of the tile sees [lo, hi)
+        for (int i = S::PAIR ? 0 : w.wg(); i < n; i += S::PAIR ? 1 : 2) {
+            const uint32_t g = base + i, vs = g % S::NV;
             const int j0 = (st.k0 + i) * KT;
-            uint32_t lost = 0;
-#pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
-            const bool mixed = j0 < st.tile.lo || j0 + KT > st.tile.hi || lost;
-            if (w.formed || mixed) w.form(j0, mixed, sh->none[vs]);
+            if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
+            tc_fence_after();
+            if (S::PAIR && threadIdx.x == kTeam && i > 0) mbar_arrive(&sh->done[(g - 1) % S::NV]);
+            __syncwarp();
             uint32_t s[kChunks][32];
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
+            if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
+            const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
+            const bool mixed =
+                j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
+            if (w.formed() || mixed) {
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) wait_ld(s[ch]);
+                w.form(j0, mixed, sh->none[vs]);
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
+            }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
@@ -794,15 +1013,28 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                                               fmaxf(__uint_as_float(s[ch][e]),
                                                     __uint_as_float(s[ch][e + 1])));
             }
+            float safe = m == -INFINITY ? 0.f : m, sums[4] = {0.f, 0.f, 0.f, 0.f};
+            auto weigh = [&](int ch) {  // the chunk's weights take the place of its scores
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float x, y;
+                    fma2(x, y, __uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1]),
+                         w.to_log2, -safe);
+                    x = ex2(x), y = ex2(y);
+                    add2(sums[2 * (e & 1)], sums[2 * (e & 1) + 1], x, y);
+                    s[ch][e] = pack2<S::ET>(x, y);
+                }
+            };
+            // The first weights are worked out while the maximum is, which seldom changes.
+            weigh(0);
             const float now =
                 fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * w.to_log2);
             if (__any_sync(0xFFFFFFFFu, now > m + kGrow || m == -INFINITY)) {
                 const float f = ex2(m - (now == -INFINITY ? 0.f : now));
                 m = now;
+                safe = m == -INFINITY ? 0.f : m;
                 l *= f;
-                if (some) {
-                    if (!c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
-                    tc_fence_after();
+                if (some) {  // the last P V came before these scores
 #pragma unroll 1
                     for (int ch = 0; ch < DP / 32; ++ch) {
                         uint32_t v[32];
@@ -814,15 +1046,16 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                         st32(w.tm + kColT + 32 * ch, v);
                     }
                 }
+                ld32(s[0], w.tm + kColS);
+                wait_ld(s[0]);
+                sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
+                weigh(0);
             }
-            const float safe = m == -INFINITY ? 0.f : m;
             if (mixed) {
-                const uint32_t v_at = c.ring + vs * S::kSlot;
-                typename Row<S>::Odd odd;
+                const uint32_t v_at = c.v_ring + vs * S::kSlot;
+                typename R::Odd odd;
                 if (!w.look(v_at, odd)) return;
                 if (odd.any) {
-                    if (some && !c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
-                    tc_fence_after();
                     wait_st();
 #pragma unroll 1
                     for (int ch = 0; ch < DP / 32; ++ch) {
@@ -846,88 +1079,43 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                     if (!w.clear(v_at, odd)) return;
                 }
             }
-            float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float x, y;
-                    fma2(x, y, __uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1]),
-                         w.to_log2, -safe);
-                    x = ex2(x), y = ex2(y);
-                    add2(sums[2 * (e & 1)], sums[2 * (e & 1) + 1], x, y);
-                    p[e] = pack2<S::ET>(x, y);
-                }
-                st16(w.tm + kColP0 + 16 * ch, p);
+                if (ch > 0) weigh(ch);
+                st16(w.tm + kColP0 + 16 * ch, s[ch]);
             }
-            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             wait_st();
             tc_fence_before();
-            mbar_arrive(&sh->p_ready[w.wg]);
+            c.warp_arrive(&sh->p_ready[w.wg()]);
+            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             ++mine;
             some = true;
         }
         base += n;
-        if (some && !c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return;
-        tc_fence_after();
-        float fa = 1.f, fb = 0.f;
-        if (!S::PAIR && n > 0) {
-            // The two warpgroups' halves of the slots.
-            if (!w.meet(0)) return;  // every product of q is done
-            if (w.wg == 1) {
+        if (some) {
+            if (!c.warp_wait(&sh->t_full[w.wg()], ended & 1)) return;
+            tc_fence_after();
+            ++ended;
+            if (S::PAIR && threadIdx.x == kTeam) mbar_arrive(&sh->done[(base - 1) % S::NV]);
+        }
+        int j, h;
+        const bool live = w.place(j, h);
+        if (S::PAIR) {
 #pragma unroll 1
-                for (int ch = 0; ch < DP / 32; ++ch) {
-                    uint32_t v[32];
+            for (int ch = 0; ch < DP / 32; ++ch) {
+                uint32_t v[32] = {};
+                if (n > 0) {
                     ld32(v, w.tm + kColT + 32 * ch);
                     wait_ld(v);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(
-                                         c.stage + ((32 * ch + e) * 128 + w.r) * 4),
-                                     "r"(v[e])
-                                     : "memory");
                 }
-                sh->ml[w.r] = make_float2(m, l);
-            }
-            if (!w.meet(0)) return;
-            if (w.wg == 1) continue;
-            const float2 other = sh->ml[w.r];
-            const float both = fmaxf(m, other.x), safe = both == -INFINITY ? 0.f : both;
-            fa = ex2(m - safe), fb = ex2(other.x - safe);
-            m = both;
-            l = fmaf(l, fa, other.y * fb);
-        } else if (!S::PAIR && w.wg == 1) {
-            continue;
-        }
-#pragma unroll 1
-        for (int ch = 0; ch < DP / 32; ++ch) {
-            uint32_t v[32] = {};
-            if (n > 0) {
-                ld32(v, w.tm + kColT + 32 * ch);
-                wait_ld(v);
-                if (!S::PAIR) {
+                float x[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float x;
-                        asm volatile("ld.shared.f32 %0, [%1];"
-                                     : "=f"(x)
-                                     : "r"(c.stage + ((32 * ch + e) * 128 + w.r) * 4)
-                                     : "memory");
-                        v[e] = __float_as_uint(fmaf(__uint_as_float(v[e]), fa, x * fb));
-                    }
-                }
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+                if (live) w.finish(room, st, j, h, m, l, 32 * ch, x);
+                __syncwarp();
             }
-            if (w.live) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    float x[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v[e + k]);
-                    w.finish(room, st, m, l, 32 * ch + e, x);
-                }
-            }
-            __syncwarp();
+        } else if (!w.join(room, st, n > 0, live, j, h, m, l)) {
+            return;
         }
     }
 }
@@ -942,10 +1130,10 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
     Walk walk(room, blockIdx.x);
     Stretch st;
     uint32_t base = 0, mine = 0;
-    bool again = false;
     while (walk.next(st)) {
         __syncwarp();
-        w.begin(st);
+        w.tile = room.tiles + st.tile;
+        w.head = st.head;
         const int n = st.k1 - st.k0;
         float o[DP];
 #pragma unroll
@@ -953,15 +1141,14 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
         float m = -INFINITY, l = 0.f, f = 0.f;
         bool pending = false;
         if (n > 0) {
-            if (again && !w.meet(0)) return;  // the last stretch's join was read
-            again = true;
-            load_q<S>(a, kv, w.q, st, c, 0, 128, threadIdx.x, 256);
+            load_q<S, 128, kSoft>(a, kv, *w.tile, st.head, c, 0, threadIdx.x);
             fence_proxy_async_smem();
-            mbar_arrive(&sh->q_ready);
+            c.warp_arrive(&sh->q_ready);
         }
+        const int lo = w.tile->lo, hi = w.tile->hi;  // every row of the tile sees [lo, hi)
         // o = o f + T of the tile before.
         auto take = [&]() {
-            if (!c.warp_wait(&sh->t_full[w.wg], (mine - 1) & 1)) return false;
+            if (!c.warp_wait(&sh->t_full[w.wg()], (mine - 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int ch = 0; ch < DP / 32; ++ch) {
@@ -974,18 +1161,18 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             }
             return true;
         };
-        for (int i = w.wg; i < n; i += 2) {
+        for (int i = w.wg(); i < n; i += 2) {
             if (pending && !take()) return;
-            const uint32_t vi = 2 * (base + i) + 1, vs = vi % S::kSlots;
-            if (!c.warp_wait(&sh->full[vs], vi / S::kSlots & 1)) return;
-            if (!c.warp_wait(&sh->s_full[w.wg], mine & 1)) return;
+            const uint32_t g = base + i, vs = g % S::NV;
+            if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
+            if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
             tc_fence_after();
             const int j0 = (st.k0 + i) * KT;
             uint32_t lost = 0;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
-            const bool mixed = j0 < st.tile.lo || j0 + KT > st.tile.hi || lost;
-            if (w.formed || mixed) w.form(j0, mixed, sh->none[vs]);
+            const bool mixed = j0 < lo || j0 + KT > hi || lost;
+            if (w.formed() || mixed) w.form(j0, mixed, sh->none[vs]);
             float top = -INFINITY;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
@@ -1001,7 +1188,7 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             f = fl;
             m = now;
             if (mixed) {
-                const uint32_t v_at = c.ring + vs * S::kSlot;
+                const uint32_t v_at = c.v_ring + vs * S::kSlot;
                 typename Row<S>::Odd odd;
                 if (!w.look(v_at, odd)) return;
                 if (odd.any) {
@@ -1050,49 +1237,25 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             l = fmaf(l, fl, (sums[0] + sums[1]) + (sums[2] + sums[3]));
             wait_st();
             tc_fence_before();
-            mbar_arrive(&sh->p_ready[w.wg]);
+            c.warp_arrive(&sh->p_ready[w.wg()]);
             ++mine;
             pending = true;
         }
         if (pending && !take()) return;
         base += n;
         if (n > 0) {
-            // The two warpgroups' halves of the slots.
-            if (!w.meet(0)) return;  // every product of q is done
-            if (w.wg == 1) {
 #pragma unroll
-                for (int e = 0; e < DP; ++e)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.stage + (e * 128 + w.r) * 4),
-                                 "f"(o[e])
-                                 : "memory");
-                sh->ml[w.r] = make_float2(m, l);
+            for (int ch = 0; ch < DP / 32; ++ch) {
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(o[32 * ch + e]);
+                st32(w.tm + kColT + 32 * ch, v);
             }
-            if (!w.meet(0)) return;
-            if (w.wg == 0) {
-                const float2 other = sh->ml[w.r];
-                const float both = fmaxf(m, other.x), safe = both == -INFINITY ? 0.f : both;
-                const float fa = ex2(m - safe), fb = ex2(other.x - safe);
-                m = both;
-                l = fmaf(l, fa, other.y * fb);
-#pragma unroll
-                for (int e = 0; e < DP; ++e) {
-                    float x;
-                    asm volatile("ld.shared.f32 %0, [%1];"
-                                 : "=f"(x)
-                                 : "r"(c.stage + (e * 128 + w.r) * 4)
-                                 : "memory");
-                    o[e] = fmaf(o[e], fa, x * fb);
-                }
-            }
+            wait_st();
         }
-        if (!w.live || w.wg == 1) continue;
-#pragma unroll
-        for (int e = 0; e < DP; e += 8) {
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = o[e + k];
-            w.finish(room, st, m, l, e, x);
-        }
+        int j, h;
+        const bool live = w.place(j, h);
+        if (!w.join(room, st, n > 0, live, j, h, m, l)) return;
     }
 }
 
@@ -1103,31 +1266,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctx c;
     c.sh = reinterpret_cast<Shared *>(smem);
-    c.stage = (smem_addr(smem) + kMisc + 1023) & ~1023u;
-    c.ring = c.stage + S::kStage;
+    // Tiles lie on 1024-byte boundaries; the array is declared so, and nothing is done if it is not.
+    c.stage = smem_addr(smem) + kMisc;
+    if (c.stage & 1023u) {
+        if (threadIdx.x == 0) record_status(a.status, kStTimeout);
+        return;
+    }
+    c.k_ring = c.stage + S::kStage;
+    c.v_ring = c.k_ring + S::NK * S::kSlot;
     c.limit = a.wait_limit;
     c.status = a.status;
     const int warp = threadIdx.x >> 5;
     pdl_launch();
     if (threadIdx.x == 0) {
         if (box) prefetch_tmap(&k_map), prefetch_tmap(&v_map);
-        for (int i = 0; i < kMostSlots; ++i) {
+        mbar_init(&c.sh->first, box ? 1 : kLoaders);
+        for (int i = 0; i < kMostV; ++i) {
             mbar_init(&c.sh->full[i], box ? 1 : kLoaders);
-            mbar_init(&c.sh->empty[i], 1);
+            mbar_init(&c.sh->done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.sh->s_full[i], 1);
-            mbar_init(&c.sh->p_ready[i], 128);
+            mbar_init(&c.sh->p_ready[i], kTeam / 32);
             mbar_init(&c.sh->t_full[i], 1);
-            mbar_init(&c.sh->meet[1 + i], 128);
+            mbar_init(&c.sh->meet[1 + i], kTeam / 32);
         }
-        mbar_init(&c.sh->meet[0], 256);
-        mbar_init(&c.sh->q_ready, 256);
+        mbar_init(&c.sh->meet[0], kSoft / 32);
+        mbar_init(&c.sh->q_ready, S::TERMS == 1 ? 1 : kSoft / 32);
+        mbar_init(&c.sh->q_free, 1);
         mbar_init(&c.sh->drain, 1);
         c.sh->abort = 0u;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    constexpr int kMma = kSoft / 32;
+    if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&c.sh->tmem)),
                      "r"(512u)
@@ -1139,27 +1311,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     pdl_wait();
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, a.group.d, S::RT, S::DP, kGrid);
-    // 384 threads of 168 registers at the launch: 2 x 216 + 72 and 2 x 224 + 56 are 3 x 168.
-    if (warp < 8) {
-        if constexpr (S::TERMS == 1)
+    // What the softmax threads take over their share of the launch's registers the others give:
+    // 384 x 168 = 256 x 216 + 128 x 72 = 256 x 224 + 128 x 56.
+    if (warp < kMma) {
+        if constexpr (S::TERMS == 1) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        if constexpr (S::TERMS == 1)
             softmax_16<S>(a, kv, room, c);
-        else
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
             softmax_32<S>(a, kv, room, c);
+        }
     } else {
         if constexpr (S::TERMS == 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp > 8) {
+        if (warp > kMma) {
             fence_proxy_async_global();  // k and v may be an earlier kernel's plain stores
-            if (!box)
+            if (warp == kMma + 3) {
+                if constexpr (S::TERMS == 1) load_queries<S>(a, kv, room, c);
+            } else if (!box) {
                 load_rows<S>(a, kv, room, c);
-            else if (warp == 9)
+            } else if (warp == kMma + 1) {
                 load_boxes<S>(a, kv, &k_map, &v_map, box, room, c);
+            }
         } else if ((threadIdx.x & 31) == 0) {
             issue_products<S>(a, room, c);
             // Every product is done before tensor memory and the tiles are given up.
@@ -1170,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kMma) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.sh->tmem),
                      "r"(512u)

@@ -490,6 +490,8 @@ wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q
     a.tree_stride = f.tree_stride;
     a.q_type = q_type;
     a.out_type = out_type;
+    a.wide_out = aligned(out, 32) && out_stride * element_bytes(out_type) % 32 == 0 &&
+                 kv.head_dim * element_bytes(out_type) % 32 == 0;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;

@@ -102,6 +102,7 @@ struct TokensArgs {
     const uint32_t *tree;
     long long tree_stride;
     int q_type, out_type;
+    bool wide_out;  // rows of out in whole 32-byte runs
     const void *q;
     void *out;
     long long q_stride, out_stride;  // in elements
