@@ -41,7 +41,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long *s_warp, 
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_plan_kernel(TokensArgs a, int heads, int rt, int kt, int dp, int grid) {
+    attn_plan_kernel(TokensArgs a, int heads, int rt, int kt, int dp, int grid, int row_cost) {
     __shared__ long long s_warp[32];
     __shared__ int s_first[kPlanThreads + 1];
     __shared__ long long s_before[kPlanTiles];  // the first tiles' costs, for the searches below
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
         const int i = i0 + threadIdx.x;
         long long mine = 0;
-        if (i < n_tiles) mine = room.tiles[i].k1 - room.tiles[i].k0 + kRowCost;
+        if (i < n_tiles) mine = room.tiles[i].k1 - room.tiles[i].k0 + row_cost;
         long long all;
         const long long upto = block_scan(mine, s_warp, all);
         if (i < n_tiles) room.before[i] = cost + upto - mine;
@@ -458,7 +458,7 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     cudaError_t err = ensure_smem(attn_rows_kernel<T, DP, R>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
     const int grid = kMaxGrid;
-    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, grid, stream);
+    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, grid, 2, stream);
     if (err != cudaSuccess) return err;
     err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, a, kv,
                      grid);
@@ -482,9 +482,9 @@ cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const Device
 }  // namespace
 
 cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
-                             int grid, cudaStream_t stream) {
+                             int grid, int row_cost, cudaStream_t stream) {
     return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kv.n_heads, rt,
-                      kt, dp, grid);
+                      kt, dp, grid, row_cost);
 }
 
 cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,

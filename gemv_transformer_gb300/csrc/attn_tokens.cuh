@@ -17,7 +17,6 @@ namespace wq {
 namespace tok {
 
 constexpr int kMaxGrid = 304;  // two CTAs on each of 152 SMs
-constexpr int kRowCost = 2;    // a row tile's start and end count as so many key tiles
 
 // A sequence's part in the call.
 struct Seq {
@@ -205,8 +204,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return m == -INFINITY ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
+// row_cost: a row tile's start and end count as so many key tiles.
 cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
-                             int grid, cudaStream_t stream);
+                             int grid, int row_cost, cudaStream_t stream);
 cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
                               cudaStream_t stream);
 

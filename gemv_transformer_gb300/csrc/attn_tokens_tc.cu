@@ -346,8 +346,8 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
         mbar_wait(&c.sh->full[i % S::NV], i / S::NV & 1, kDrainPolls);
 }
 
-// The same by cp.async and two warps for pages of any size; a step's barrier is arrived at once it
-// has landed, when the next one is under way or has to wait.  Slots beyond the live ones and in pages out
+// The same by cp.async and two warps for pages of any size; a step's barrier is arrived at when
+// it has landed and NV - 1 others are under way, or the next one has to wait.  Slots beyond the live ones and in pages out
 // of range are zeros.
 template <typename S>
 __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
@@ -416,7 +416,7 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
             // What it waits for may wait for the step before.
             if (landed < g && !__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, turn))) {
                 cp_wait<0>();
-                land();
+                while (landed < g) land();
             }
             if (!c.warp_wait(bar, turn)) {
                 ok = false;
@@ -436,8 +436,8 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
             copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlot);
         copy(v, kv.v, c.v_ring + slot * S::kSlot);
         cp_commit();
-        if (landed < g) {
-            cp_wait<1>();
+        if (g + 1 - landed >= (uint32_t)S::NV) {
+            cp_wait<S::NV - 1>();
             land();
         }
     }
@@ -446,10 +446,11 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
 }
 
 // q of a stretch of 16-bit queries, by one warp, while the stretch before ends: its place is free when
-// the last scores are done.
+// the last scores are done.  By TMA where whole tokens make up 128 rows (q_box tokens of group
+// heads; the rows beyond the sequence's are another's, and written by no one), else by cp.async.
 template <typename S>
-__device__ void load_queries(const TokensArgs &a, const KvView &kv, const Room &room,
-                             const Ctx &c) {
+__device__ void load_queries(const TokensArgs &a, const KvView &kv, const CUtensorMap *q_map,
+                             int q_box, const Room &room, const Ctx &c) {
     constexpr int kChunks = S::DP / 8;
     const int lane = threadIdx.x & 31, group = a.group.d;
     Walk walk(room, blockIdx.x);
@@ -459,7 +460,27 @@ __device__ void load_queries(const TokensArgs &a, const KvView &kv, const Room &
         if (st.k0 == st.k1) continue;
         const Tile *const tile = room.tiles + st.tile;
         const int row0 = tile->row0, t0 = tile->q.t0, rows = tile->q.count * group - row0;
-        if (n > 0 && !c.warp_wait(&c.sh->q_free, (n - 1) & 1)) return;
+        if (n > 0 && !c.warp_wait(&c.sh->q_free, (n - 1) & 1)) break;
+        if (q_box) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&c.sh->q_ready, S::kQTerm);
+#pragma unroll
+                for (int x = 0; x < S::RT / 128 * (S::DP / 64); ++x) {
+                    const int r = x / (S::DP / 64) * 128, h = x % (S::DP / 64);
+                    asm volatile(
+                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx"
+                        "::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                            c.stage + r * (S::DP * 2) + h * S::kHalf),
+                        "l"(reinterpret_cast<uint64_t>(q_map)), "r"(64 * h),
+                        "r"(st.head * group), "r"(t0 + (int)a.group.div(row0 + r)),
+                        "r"(smem_addr(&c.sh->q_ready))
+                        : "memory");
+                }
+            }
+            __syncwarp();
+            ++n;
+            continue;
+        }
 #pragma unroll 4
         for (int i = lane; i < S::RT * kChunks; i += 32) {
             const int r = i / kChunks, ch = i % kChunks;
@@ -478,6 +499,8 @@ __device__ void load_queries(const TokensArgs &a, const KvView &kv, const Room &
         c.warp_arrive(&c.sh->q_ready);
         ++n;
     }
+    // The last copy has landed before shared memory is given up.
+    if (q_box && n > 0) mbar_wait(&c.sh->q_ready, (n - 1) & 1, kDrainPolls);
 }
 
 // ------------------------------------------------------------------------ MMA warp --
@@ -1262,7 +1285,8 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tokens_tc_kernel(TokensArgs a, KvView kv, const __grid_constant__ CUtensorMap k_map,
-                          const __grid_constant__ CUtensorMap v_map, int box) {
+                          const __grid_constant__ CUtensorMap v_map,
+                          const __grid_constant__ CUtensorMap q_map, int box, int q_box) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctx c;
     c.sh = reinterpret_cast<Shared *>(smem);
@@ -1280,6 +1304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch();
     if (threadIdx.x == 0) {
         if (box) prefetch_tmap(&k_map), prefetch_tmap(&v_map);
+        if (q_box) prefetch_tmap(&q_map);
         mbar_init(&c.sh->first, box ? 1 : kLoaders);
         for (int i = 0; i < kMostV; ++i) {
             mbar_init(&c.sh->full[i], box ? 1 : kLoaders);
@@ -1327,9 +1352,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp > kMma) {
-            fence_proxy_async_global();  // k and v may be an earlier kernel's plain stores
+            fence_proxy_async_global();  // q, k and v may be an earlier kernel's plain stores
             if (warp == kMma + 3) {
-                if constexpr (S::TERMS == 1) load_queries<S>(a, kv, room, c);
+                if constexpr (S::TERMS == 1) load_queries<S>(a, kv, &q_map, q_box, room, c);
             } else if (!box) {
                 load_rows<S>(a, kv, room, c);
             } else if (warp == kMma + 1) {
@@ -1389,6 +1414,26 @@ bool pool_map(CUtensorMap &map, const KvView &kv, char *pool, int box) {
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// q as [token][head][dim], in boxes of a group's heads of as many tokens as make up 128 rows; the number
+// of tokens, or 0.
+int query_map(CUtensorMap &map, const TokensArgs &a, const KvView &kv) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    const int group = a.group.d;
+    if (!encode || a.q_type == kF32 || group > 128 || 128 % group) return 0;
+    const cuuint64_t dims[3] = {(cuuint64_t)kv.head_dim, (cuuint64_t)a.h_q, (cuuint64_t)a.n_tok};
+    const cuuint64_t strides[2] = {(cuuint64_t)kv.head_dim * 2, (cuuint64_t)a.q_stride * 2};
+    if (strides[1] >= (1ull << 40)) return 0;
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return encode(&map,
+                  a.q_type == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  3, const_cast<void *>(a.q), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? 128 / group : 0;
+}
 // Rows of a box: the largest power of two, 8 at least, that divides a page and a tile; 0: none.
 int box_of(const KvView &kv, int kt) {
     int box = kt;
@@ -1403,13 +1448,14 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = ensure_smem(attn_tokens_tc_kernel<S>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
-    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, kGrid, stream);
+    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, kGrid, PAIR ? 4 : 2, stream);
     if (err != cudaSuccess) return err;
-    CUtensorMap k_map{}, v_map{};
+    CUtensorMap k_map{}, v_map{}, q_map{};
+    const int q_box = query_map(q_map, a, kv);
     int box = box_of(kv, S::KT);
     if (box && !(pool_map(k_map, kv, kv.k, box) && pool_map(v_map, kv, kv.v, box))) box = 0;
     err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv,
-                     k_map, v_map, box);
+                     k_map, v_map, q_map, box, q_box);
     if (err != cudaSuccess) return err;
     return launch_attn_parts(a, kv, S::RT, DP, kGrid, stream);
 }

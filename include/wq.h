@@ -649,7 +649,7 @@ typedef struct {
  * queries over a cache of their type with head_dim <= 128: tensor-core products, in which p is
  * rounded to that type (2^-9 of it for bf16, 2^-12 for f16; p is at most 2^0 and f16 weights
  * below 2^-24 are lost); all others as f32 queries.
- * Rows of q at or beyond starts[n_seq] are not read and theirs of out not written.
+ * Rows of q at or beyond starts[n_seq] reach no result, and theirs of out are not written.
  * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not
  * like that is left out, a length below T or above max_pages * page_size is cut to the slots
  * that there are, and a page out of range that holds live slots leaves them out; each records
