@@ -44,13 +44,14 @@ __global__ void __launch_bounds__(kPlanThreads)
     attn_plan_kernel(TokensArgs a, int heads, int rt, int kt, int dp, int grid, int row_cost) {
     __shared__ long long s_warp[32];
     __shared__ int s_first[kPlanThreads + 1];
-    __shared__ long long s_before[kPlanTiles];  // the first tiles' costs, for the searches below
+    __shared__ int s_keys[kPlanTiles];          // key tiles of the first row tiles,
+    __shared__ long long s_before[kPlanTiles];  // and the costs before them
     pdl_enter();
     const int group = a.group.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
+    if (threadIdx.x < 2 * grid) room.joined[threadIdx.x] = 0u;
     // Row tiles of the sequences, kPlanThreads sequences at a time.
     int n_tiles = 0;
-    long long cost = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         int mine = 0;
         if (s0 + (int)threadIdx.x < a.n_seq) {
@@ -64,17 +65,20 @@ __global__ void __launch_bounds__(kPlanThreads)
         s_first[threadIdx.x + 1] = n_tiles + (int)upto;
         if (threadIdx.x == 0) s_first[0] = n_tiles;
         __syncthreads();
-        // A warp lists a sequence's tiles.
-        for (int i = warp; i < kPlanThreads && s0 + i < a.n_seq; i += kPlanThreads / 32) {
+        // A warp lists a sequence's tiles, all warps those of few sequences.
+        const int here = min(a.n_seq - s0, kPlanThreads);
+        int share = 1;  // warps to a sequence
+        while (2 * share * here <= kPlanThreads / 32) share *= 2;
+        for (int i = warp / share; i < here; i += kPlanThreads / 32 / share) {
             const int first = s_first[i], count = s_first[i + 1] - first;
             if (count == 0) continue;
             bool bad = false;
             const int s = s0 + i;
             const Seq q = seq_of(a, s, bad);
             const bool each = a.first || (a.tree && a.window > 0);
-            for (int r = lane; r < count; r += 32) {
+            for (int r = warp % share * 32 + lane; r < count; r += 32 * share) {
                 const int row0 = r * rt, row1 = min(row0 + rt, q.count * group);
-                const int j0 = row0 / group, j1 = (row1 - 1) / group;
+                const int j0 = a.group.div(row0), j1 = a.group.div(row1 - 1);
                 int lo = INT_MAX, hi = 0, lo_most = 0, hi_least = INT_MAX;
                 // Without per-token arrays the bounds rise from token to token.
                 for (int j = j0; j <= j1; j = each || j == j1 ? j + 1 : j1) {
@@ -92,112 +96,60 @@ __global__ void __launch_bounds__(kPlanThreads)
                 Tile t{s, row0, 0, 0, lo_most, hi_least, 0, 0, q};
                 if (hi > lo) t.k0 = lo / kt, t.k1 = (hi + kt - 1) / kt;
                 room.tiles[first + r] = t;
+                if (first + r < kPlanTiles) s_keys[first + r] = t.k1 - t.k0;
             }
         }
         n_tiles += (int)all;
         __syncthreads();
     }
+    auto keys = [&](int i) {
+        return i < kPlanTiles ? s_keys[i] : room.tiles[i].k1 - room.tiles[i].k0;
+    };
     // Costs before each row tile.
+    long long cost = 0;
     for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
         const int i = i0 + threadIdx.x;
         long long mine = 0;
-        if (i < n_tiles) mine = room.tiles[i].k1 - room.tiles[i].k0 + row_cost;
+        if (i < n_tiles) mine = keys(i) + row_cost;
         long long all;
         const long long upto = block_scan(mine, s_warp, all);
-        if (i < n_tiles) room.before[i] = cost + upto - mine;
-        if (i < n_tiles && i < kPlanTiles) s_before[i] = cost + upto - mine;
+        if (i < n_tiles) (i < kPlanTiles ? s_before[i] : room.before[i]) = cost + upto - mine;
         cost += all;
     }
-    if (threadIdx.x == 0) room.before[n_tiles] = cost;
     __syncthreads();
+    auto before = [&](int i) { return i < kPlanTiles ? s_before[i] : room.before[i]; };
     for (int b = threadIdx.x; b <= grid; b += kPlanThreads) {
-        Begin p{heads, 0, 0, n_tiles};
+        Begin p{heads, 0, 0, n_tiles, 0, 0, 0, 0};
         if (b < grid && cost > 0) {
-            const long long total = cost * heads;
-            const long long at = total / grid * b + min((long long)b, total % grid);
+            // CTA b begins at each b + min(b, rest).
+            const long long total = cost * heads, each = total / grid, rest = total % grid;
+            auto owner = [&](long long t) {
+                const long long cut = rest * (each + 1);
+                return (int)(t < cut ? t / (each + 1) : rest + (t - cut) / each);
+            };
+            const long long at = each * b + min((long long)b, rest);
             const int head = (int)(at / cost);
             const long long in = at - head * cost;
-            int x = 0, y = n_tiles;  // before[x] <= in < before[y]
+            int x = 0, y = n_tiles;  // before(x) <= in < before(y)
             while (y - x > 1) {
                 const int mid = (x + y) / 2;
-                if ((mid < kPlanTiles ? s_before[mid] : room.before[mid]) <= in) x = mid; else y = mid;
+                if (before(mid) <= in) x = mid; else y = mid;
             }
             p.head = head;
             p.tile = x;
-            p.off = (int)(in - (x < kPlanTiles ? s_before[x] : room.before[x]));
-            const Tile t = room.tiles[x];
-            if (p.off > 0 && p.off >= t.k1 - t.k0) {  // in the end of a row tile
+            p.off = (int)(in - before(x));
+            const int n = keys(x);
+            if (p.off > 0 && p.off < n) {
+                const long long begin = head * cost + before(x);
+                p.lead = owner(begin);
+                p.parts = owner(begin + n - 1) - p.lead + 1;
+            } else if (p.off > 0) {  // in the end of a row tile
                 p.off = 0;
                 if (++p.tile == n_tiles) p.tile = 0, ++p.head;
             }
         }
         room.plan[b] = p;
     }
-}
-
-// Joins the parts of the row tile that CTA blockIdx.x + 1 begins within, if that CTA is the first to.
-// A thread takes four dims of one row, with the loads of kAtOnce parts in flight.
-constexpr int kAtOnce = 8;
-__global__ void __launch_bounds__(256)
-    attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
-    pdl_enter();
-    const int group = a.group.d;
-    const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
-    const int b = blockIdx.x + 1;
-    const Begin p = room.plan[b], before = room.plan[b - 1];
-    if (p.off == 0 || p.head >= kv.n_heads) return;
-    if (before.head == p.head && before.tile == p.tile && before.off > 0) return;
-    const Tile tile = room.tiles[p.tile];
-    const Seq q = tile.q;
-    const int at = blockIdx.y * 256 + threadIdx.x;
-    const int row = at % rt, c = at / rt;  // rt is a power of two
-    const bool mine = row < min(rt, q.count * group - tile.row0) && 4 * c < kv.head_dim;
-    // CTAs that begin within it.
-    int n = 1;
-    for (bool more = true; more;) {
-        Begin next[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            next[i] = room.plan[min(b + n + i, grid)];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            if (more) {
-                more = next[i].head == p.head && next[i].tile == p.tile && next[i].off > 0;
-                n += more;
-            }
-    }
-    if (!mine) return;
-    // The parts: the second of CTA b - 1, then the first of CTAs b, b + 1, ...
-    auto place = [&](int i) { return (size_t)(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)); };
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 <= n; i0 += kAtOnce) {
-        float2 ml[kAtOnce];
-        float4 v[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const size_t part = place(min(i0 + i, n));
-            ml[i] = room.part_ml[part * rt + row];
-            v[i] = room.part_o[(part * (dp / 4) + c) * rt + row];
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            if (i0 + i > n) break;
-            const float now = fmaxf(m, ml[i].x), safe = now == -INFINITY ? 0.f : now;
-            const float f = exp2f(m - safe), g = exp2f(ml[i].x - safe);
-            m = now;
-            l = fmaf(l, f, ml[i].y * g);
-            o.x = fmaf(o.x, f, v[i].x * g), o.y = fmaf(o.y, f, v[i].y * g);
-            o.z = fmaf(o.z, f, v[i].z * g), o.w = fmaf(o.w, f, v[i].w * g);
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int rr = tile.row0 + row, j = a.group.div(rr), g = rr - j * group;
-    const int t = q.t0 + j, h = p.head * group + g;
-    const TypedOut out{a.out, a.out_type};
-    out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
-             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (a.lse && c == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
 }
 
 // ------------------------------------------------------------------ f32 arithmetic --
@@ -236,6 +188,7 @@ __global__ void __launch_bounds__(256)
     using S = RowsShape<DP, R>;
     constexpr int KT = S::KT, RT = S::RT, NK = KT / 16, ND = DP / 16;
     extern __shared__ __align__(16) float s_rows[];
+    __shared__ int s_join[3];
     float *s_q = s_rows, *s_k = s_q + S::kQ, *s_v = s_k + S::kK, *s_p = s_v + S::kV;
     pdl_enter();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.group.d;
@@ -415,19 +368,57 @@ __global__ void __launch_bounds__(256)
             }
         }
         // Dims (e / 4) * 64 + tx * 4 + e % 4 of the thread's rows.
+        if (st.part >= 0) {
+            const size_t part = 2 * blockIdx.x + st.part;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int r = ty * R + i;
-            if (r >= rows) continue;
-            if (st.part >= 0) {
-                const size_t part = 2 * blockIdx.x + st.part;
+            for (int i = 0; i < R; ++i) {
+                const int r = ty * R + i;
 #pragma unroll
                 for (int e = 0; e < ND; e += 4)
                     room.part_o[(part * (DP / 4) + (e / 4) * 16 + tx) * RT + r] =
                         make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
                 if (tx == 0) room.part_ml[part * RT + r] = make_float2(m[i], l[i]);
-                continue;
             }
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                int lead, parts;
+                s_join[0] = part_last(room, st, blockIdx.x, 0, lead, parts);
+                s_join[1] = lead, s_join[2] = parts;
+            }
+            __syncthreads();
+            if (!s_join[0]) continue;
+            __threadfence();
+            const int lead = s_join[1], parts = s_join[2];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = ty * R + i;
+                m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < ND; ++e) o[i][e] = 0.f;
+                for (int k = 0; k < parts; ++k) {
+                    const size_t from = part_place(lead, k);
+                    const float2 ml = __ldcg(room.part_ml + from * RT + r);
+                    const float now = fmaxf(m[i], ml.x), safe = now == -INFINITY ? 0.f : now;
+                    const float f = exp2f(m[i] - safe), g = exp2f(ml.x - safe);
+                    m[i] = now;
+                    l[i] = fmaf(l[i], f, ml.y * g);
+#pragma unroll
+                    for (int e = 0; e < ND; e += 4) {
+                        const float4 v =
+                            __ldcg(room.part_o + (from * (DP / 4) + (e / 4) * 16 + tx) * RT + r);
+                        o[i][e] = fmaf(o[i][e], f, v.x * g);
+                        o[i][e + 1] = fmaf(o[i][e + 1], f, v.y * g);
+                        o[i][e + 2] = fmaf(o[i][e + 2], f, v.z * g);
+                        o[i][e + 3] = fmaf(o[i][e + 3], f, v.w * g);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = ty * R + i;
+            if (r >= rows) continue;
             const int rr = tile.row0 + r, j = a.group.div(rr), g = rr - j * group;
             const int t = q.t0 + j, h = st.head * group + g;
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
@@ -460,10 +451,8 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     const int grid = kMaxGrid;
     err = launch_attn_plan(a, kv, S::RT, S::KT, DP, grid, 2, stream);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, a, kv,
-                     grid);
-    if (err != cudaSuccess) return err;
-    return launch_attn_parts(a, kv, S::RT, DP, grid, stream);
+    return launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, a, kv,
+                      grid);
 }
 template <typename T>
 cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -485,13 +474,6 @@ cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int 
                              int grid, int row_cost, cudaStream_t stream) {
     return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kv.n_heads, rt,
                       kt, dp, grid, row_cost);
-}
-
-cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
-                              cudaStream_t stream) {
-    if (grid < 2) return cudaSuccess;
-    return launch_pdl(attn_parts_kernel, dim3(grid - 1, (rt * (kv.head_dim / 4) + 255) / 256), dim3(256), 0, stream, a,
-                      kv, rt, dp, grid);
 }
 
 }  // namespace tok

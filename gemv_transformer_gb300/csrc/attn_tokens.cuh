@@ -6,8 +6,8 @@
 // KT slots.  attn_plan_kernel lists the row tiles with the key tiles that any of their rows sees,
 // sums their costs, and cuts the whole (all kv heads, one after another) into equal contiguous
 // ranges, one for each CTA of a fixed grid, whatever the lengths.  A row tile within one CTA
-// is written by it; the parts of the others are joined by attn_parts_kernel by the rule of
-// the running softmax, in an order that the lengths fix.
+// is written by it; the parts of the others are joined by whichever of their CTAs is the last to
+// finish, by the rule of the running softmax, in an order that the lengths fix.
 #pragma once
 
 #include "kv_internal.h"
@@ -108,12 +108,16 @@ struct __align__(16) Tile {
     int pad0, pad1;
     Seq q;             // the sequence's
 };
-struct Begin {
+struct __align__(16) Begin {
     int head, tile, off;  // where a CTA's range starts: kv head, row tile, key tiles into it
     int tiles;            // row tiles of all sequences
+    int lead, parts;      // off > 0: the first CTA that works on that row tile, and how many do
+    int pad0, pad1;
 };
 struct Room {
     Begin *plan;         // [grid + 1]
+    unsigned *joined;    // [grid][2]: parts that are there of the row tile that a CTA leads, by
+                         // warpgroup where those go by themselves; zeroed by the plan
     long long *before;   // [tiles + 1]: cost of the row tiles before each
     Tile *tiles;
     float2 *part_ml;     // [2 grid][RT]: running maximum (log2 units) and sum
@@ -132,6 +136,8 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int n_tok, int group
     size_t at = 0;
     r.plan = reinterpret_cast<Begin *>(c + at);
     at += up256((kMaxGrid + 1) * sizeof(Begin));
+    r.joined = reinterpret_cast<unsigned *>(c + at);
+    at += up256(kMaxGrid * 2 * sizeof(unsigned));
     r.before = reinterpret_cast<long long *>(c + at);
     at += up256((tiles + 1) * sizeof(long long));
     r.tiles = reinterpret_cast<Tile *>(c + at);
@@ -147,8 +153,21 @@ __host__ __device__ inline Room room_of(void *p, int n_seq, int n_tok, int group
 // One stretch of a CTA's range: key tiles [k0, k1) of a row tile for a kv head.
 struct Stretch {
     int tile, head, k0, k1;
-    int part;  // -1: all of the row tile; else its place in this CTA's two parts
+    int part;         // -1: all of the row tile; else its place in this CTA's two parts
 };
+// Part i of a row tile: the second of the first CTA's, then the first of each other's.
+__device__ __forceinline__ size_t part_place(int lead, int i) {
+    return i == 0 ? 2 * lead + 1 : 2 * (lead + i);
+}
+// A part's CTA says that it is written; true for the one that is the last of them.  Called by one
+// thread after a barrier behind the writers' fences; a fence and a barrier follow for the readers.
+__device__ __forceinline__ bool part_last(const Room &room, const Stretch &st, int cta, int which,
+                                          int &lead, int &parts) {
+    const Begin *const b = room.plan + cta + st.part;  // (part 1: the next CTA begins in it)
+    lead = b->lead, parts = b->parts;
+    __threadfence();
+    return atomicAdd(room.joined + 2 * lead + which, 1u) == (unsigned)parts - 1;
+}
 // The stretches of a CTA, one after another.  Little of it stays in registers: what it needs it
 // reads again.
 struct Walk {
@@ -207,9 +226,6 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // row_cost: a row tile's start and end count as so many key tiles.
 cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
                              int grid, int row_cost, cudaStream_t stream);
-cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
-                              cudaStream_t stream);
-
 // The tensor-core kernels (attn_tokens_tc.cu).
 bool tokens_tc_takes(const KvView &kv, int q_type);
 void tokens_tc_shape(int n_seq, int n_tok, int group, int q_type, int head_dim, int &rt, int &dp,

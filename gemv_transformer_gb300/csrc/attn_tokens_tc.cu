@@ -72,6 +72,7 @@ struct Shared {
     alignas(16) uint32_t none[kMostV][4];  // of a v tile: slots whose page is out of range
     uint32_t odd[2][4][4];          // slots whose v is not finite
     float2 ml[2][128];              // maxima and sums of the warpgroups' rows
+    int last[2][3];                 // part_last(), its first CTA and number of parts
     uint32_t tmem, abort;
 };
 static_assert(sizeof(Shared) <= kMisc && offsetof(Shared, none) % 16 == 0, "read as 16 bytes");
@@ -705,7 +706,7 @@ template <typename S> struct Row {
     int head;
     const uint32_t tm;   // the warpgroup's columns, this warp's lanes
     const float to_log2;
-    uint32_t turns = 0;  // parities of meet(0) and meet(1), and bit 3 of look()
+    uint32_t turns = 0;  // parities of the meetings of both and of this one, and bit 3 of look()
 
     __device__ __forceinline__ Row(const TokensArgs &a_, const KvView &kv_, const Ctx &c_)
         : a(a_), kv(kv_), c(c_), tm(c_.sh->tmem + ((threadIdx.x & 96u) << 16) + wg() * 256),
@@ -730,10 +731,11 @@ template <typename S> struct Row {
         int j, h;
         return place(j, h) ? see_of(a, tile->q, tile->seq, j) : See{};
     }
-    // 0: both warpgroups; 1: those that look through a v tile together.
+    // 0: both warpgroups; 1: those that look through a v tile together; 2: this warpgroup.
     __device__ __forceinline__ bool meet(int which) {
-        uint64_t *const bar = &c.sh->meet[S::PAIR || which == 0 ? 0 : 1 + wg()];
-        const int bit = S::PAIR ? 0 : which;
+        const bool alone = S::PAIR ? which == 2 : which > 0;
+        uint64_t *const bar = &c.sh->meet[alone ? 1 + wg() : 0];
+        const int bit = alone;
         const uint32_t turn = turns >> bit & 1;
         turns ^= 1u << bit;
         c.warp_arrive(bar);
@@ -904,26 +906,83 @@ template <typename S> struct Row {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 x[e] = fmaf(__uint_as_float(v[e]), f0, __uint_as_float(u[e]) * f1);
-            if (live) finish(room, st, j, h, both, sum, 32 * ch, x);
+            if (st.part >= 0)
+                put_part(room, st, 32 * ch, x);
+            else if (live)
+                finish(j, h, both, sum, 32 * ch, x);
             __syncwarp();
         }
+        if (st.part >= 0 && !join_parts(room, st, live, j, h, both, sum, wg() * (DP / 2),
+                                        (wg() + 1) * (DP / 2)))
+            return false;
         tc_fence_before();
         if (!meet(0)) return false;  // both have read both
         tc_fence_after();
         return true;
     }
-    // Dims e .. e + 31 of the row's sums: its result, or its part.
-    __device__ __forceinline__ void finish(const Room &room, const Stretch &st, int j, int h, float m,
-                                           float l, int e, float (&x)[32]) const {
-        if (st.part >= 0) {
-            const size_t part = 2 * blockIdx.x + st.part;
+    // The part of a row tile that other CTAs work on too: written, and joined here if it is the last
+    // of them, dims d0 .. d1 of this thread's row by this thread.
+    __device__ __forceinline__ void put_part(const Room &room, const Stretch &st, int e,
+                                             const float (&x)[32]) const {
+        const size_t part = 2 * blockIdx.x + st.part;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-                room.part_o[(part * (DP / 4) + (e + k) / 4) * S::RT + row()] =
-                    make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-            if (e == 0) room.part_ml[part * S::RT + row()] = make_float2(m, l);
-            return;
+        for (int k = 0; k < 32; k += 4)
+            room.part_o[(part * (DP / 4) + (e + k) / 4) * S::RT + row()] =
+                make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    }
+    __device__ __forceinline__ bool join_parts(const Room &room, const Stretch &st, bool live, int j,
+                                               int h, float m, float l, int d0, int d1) {
+        if (d0 == 0)
+            room.part_ml[(2 * blockIdx.x + st.part) * S::RT + row()] = make_float2(m, l);
+        __threadfence();
+        // Pairs: a warpgroup has rows of its own.
+        const int which = S::PAIR ? wg() : 0, meeting = S::PAIR ? 2 : 0;
+        if (!meet(meeting)) return false;
+        if (threadIdx.x == which * kTeam) {
+            int lead, parts;
+            c.sh->last[which][0] = part_last(room, st, blockIdx.x, which, lead, parts);
+            c.sh->last[which][1] = lead, c.sh->last[which][2] = parts;
         }
+        if (!meet(meeting)) return false;
+        if (!c.sh->last[which][0]) return true;
+        __threadfence();
+        const int lead = c.sh->last[which][1], parts = c.sh->last[which][2];
+        float top = -INFINITY, sum = 0.f;
+        for (int i = 0; i < parts; ++i)
+            top = fmaxf(top, __ldcg(room.part_ml + part_place(lead, i) * S::RT + row()).x);
+        const float safe = top == -INFINITY ? 0.f : top;
+        for (int i = 0; i < parts; ++i) {
+            const float2 x = __ldcg(room.part_ml + part_place(lead, i) * S::RT + row());
+            sum = fmaf(x.y, ex2(x.x - safe), sum);
+        }
+#pragma unroll 1
+        for (int e = d0; e < d1; e += 32) {
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            for (int i = 0; i < parts; ++i) {
+                const size_t part = part_place(lead, i);
+                const float f = ex2(__ldcg(room.part_ml + part * S::RT + row()).x - safe);
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = __ldcg(room.part_o + (part * (DP / 4) + e / 4 + k) * S::RT + row());
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    o[4 * k] = fmaf(v[k].x, f, o[4 * k]);
+                    o[4 * k + 1] = fmaf(v[k].y, f, o[4 * k + 1]);
+                    o[4 * k + 2] = fmaf(v[k].z, f, o[4 * k + 2]);
+                    o[4 * k + 3] = fmaf(v[k].w, f, o[4 * k + 3]);
+                }
+            }
+            if (live) finish(j, h, top, sum, e, o);
+        }
+        __syncwarp();
+        return true;
+    }
+    // Dims e .. e + 31 of the row's result from its sums.
+    __device__ __forceinline__ void finish(int j, int h, float m, float l, int e,
+                                           float (&x)[32]) const {
         const int t = tile->q.t0 + j;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -1134,9 +1193,13 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                 float x[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-                if (live) w.finish(room, st, j, h, m, l, 32 * ch, x);
+                if (st.part >= 0)
+                    w.put_part(room, st, 32 * ch, x);
+                else if (live)
+                    w.finish(j, h, m, l, 32 * ch, x);
                 __syncwarp();
             }
+            if (st.part >= 0 && !w.join_parts(room, st, live, j, h, m, l, 0, DP)) return;
         } else if (!w.join(room, st, n > 0, live, j, h, m, l)) {
             return;
         }
@@ -1454,10 +1517,8 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     const int q_box = query_map(q_map, a, kv);
     int box = box_of(kv, S::KT);
     if (box && !(pool_map(k_map, kv, kv.k, box) && pool_map(v_map, kv, kv.v, box))) box = 0;
-    err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv,
-                     k_map, v_map, q_map, box, q_box);
-    if (err != cudaSuccess) return err;
-    return launch_attn_parts(a, kv, S::RT, DP, kGrid, stream);
+    return launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv,
+                      k_map, v_map, q_map, box, q_box);
 }
 template <int DP>
 cudaError_t launch_dim(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
