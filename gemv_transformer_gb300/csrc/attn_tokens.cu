@@ -17,6 +17,10 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 2048;
+#ifndef WQ_LEAST
+#define WQ_LEAST 3
+#endif
+constexpr int kLeastCost = WQ_LEAST;  // a CTA's range is no shorter
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
@@ -120,14 +124,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     auto before = [&](int i) { return i < kPlanTiles ? s_before[i] : room.before[i]; };
     for (int b = threadIdx.x; b <= grid; b += kPlanThreads) {
         Begin p{heads, 0, 0, n_tiles, 0, 0, 0, 0};
-        if (b < grid && cost > 0) {
+        if (cost > 0) {
             // CTA b begins at each b + min(b, rest).
-            const long long total = cost * heads, each = total / grid, rest = total % grid;
+            const long long total = cost * heads;
+            const int ctas = (int)max(1ll, min((long long)grid, total / kLeastCost));
+            const long long each = total / ctas, rest = total % ctas;
             auto owner = [&](long long t) {
                 const long long cut = rest * (each + 1);
                 return (int)(t < cut ? t / (each + 1) : rest + (t - cut) / each);
             };
-            const long long at = each * b + min((long long)b, rest);
+            const long long at = min(total, each * b + min((long long)b, rest));
             const int head = (int)(at / cost);
             const long long in = at - head * cost;
             int x = 0, y = n_tiles;  // before(x) <= in < before(y)

@@ -267,12 +267,13 @@ template <typename S> struct Stream {
     }
 };
 
-// By TMA, one warp: where the pages are whole groups of eight rows, boxes of the largest number of
+// By TMA, one warp for k and one for v (a lane's copies are issued one after another, 65 cycles
+// each): where the pages are whole groups of eight rows, boxes of the largest number of
 // rows that divides a page and a tile.  What lies beyond the live slots of a page, or of a box that
 // was not asked for, is whatever memory holds: no row sees it, and look() takes it out.
 template <typename S>
-__device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensorMap *k_map,
-                           const CUtensorMap *v_map, int box, const Room &room, const Ctx &c) {
+__device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensorMap *map,
+                           bool is_v, int box, const Room &room, const Ctx &c) {
     const int lane = threadIdx.x & 31, from = lane * box;
     const bool mine = lane < S::KT / box;
     struct Box {
@@ -296,7 +297,7 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
         x.lost = __ballot_sync(0xFFFFFFFFu, !x.live && x.page != -2);
         x.bytes = __popc(__ballot_sync(0xFFFFFFFFu, x.live)) * box * 128 * (S::DP / 64);
     };
-    auto copy = [&](const Box &x, const CUtensorMap *map, uint32_t to, uint64_t *bar) {
+    auto copy = [&](const Box &x, uint32_t to, uint64_t *bar) {
         if (!x.live) return;
 #pragma unroll
         for (int h = 0; h < S::DP / 64; ++h)
@@ -307,42 +308,56 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
                 "r"(x.page), "r"(smem_addr(bar))
                 : "memory");
     };
-    if (!in.more) return;
+    const bool ahead = S::kAhead && !is_v;
+    bool here = in.more;  // is there a step
     Box cur = ask();
-    if (S::kAhead) {
+    if (ahead && here) {
         settle(cur);
         if (lane == 0) mbar_arrive_expect_tx(&c.sh->first, cur.bytes);
         __syncwarp();
-        copy(cur, k_map, c.k_ring, &c.sh->first);
+        copy(cur, c.k_ring, &c.sh->first);
+        in.next();
+        cur = ask();
     }
     uint32_t g = 0;
-    for (bool some = true; some; ++g) {
-        Box v = cur;
-        in.next();
-        some = in.more;
-        cur = ask();
+    bool ok = true;
+    for (; here; ++g) {
+        Box x = cur;
+        const bool some = in.more;  // of x
+        if (some) {
+            in.next();
+            cur = ask();
+        }
         const uint32_t slot = g % S::NV;
-        if (g >= (uint32_t)S::NV && !c.warp_wait(&c.sh->done[slot], (g / S::NV & 1) ^ 1)) break;
-        settle(S::kAhead ? cur : v);
-        const Box &k = S::kAhead ? cur : v;
+        if (g >= (uint32_t)S::NV && !c.warp_wait(&c.sh->done[slot], (g / S::NV & 1) ^ 1)) {
+            ok = false;
+            break;
+        }
+        settle(x);
         if (lane == 0) {
-            for (int i = 0; i < S::KT / 32; ++i) {
-                uint32_t none = 0;
-                for (uint32_t left = v.lost; left; left &= left - 1) {
-                    const int at = (__ffs(left) - 1) * box - 32 * i;
-                    none |= below(at + box) & ~below(at);
+            if (is_v) {
+                for (int i = 0; i < S::KT / 32; ++i) {
+                    uint32_t none = 0;
+                    for (uint32_t left = x.lost; left; left &= left - 1) {
+                        const int at = (__ffs(left) - 1) * box - 32 * i;
+                        none |= below(at + box) & ~below(at);
+                    }
+                    c.sh->none[slot][i] = none;
                 }
-                c.sh->none[slot][i] = none;
+                if (x.lost) record_status(a.status, kStBadIndex);
             }
-            if (v.lost) record_status(a.status, kStBadIndex);
-            mbar_arrive_expect_tx(&c.sh->full[slot], v.bytes + k.bytes);
+            mbar_arrive_expect_tx(&c.sh->full[slot], x.bytes);
         }
         __syncwarp();
-        copy(k, k_map, c.k_ring + (g + S::kAhead) % S::NK * S::kSlot, &c.sh->full[slot]);
-        copy(v, v_map, c.v_ring + slot * S::kSlot, &c.sh->full[slot]);
+        copy(x, is_v ? c.v_ring + slot * S::kSlot : c.k_ring + (g + S::kAhead) % S::NK * S::kSlot,
+             &c.sh->full[slot]);
+        here = ahead ? some : in.more;
     }
-    // The last copies have landed before shared memory is given up, after an abort too.
-    if (S::kAhead) mbar_wait(&c.sh->first, 0, kDrainPolls);
+    // The last copies have landed before shared memory is given up.  After an abort the other warp
+    // may have asked for steps that this one has not: it waits for both.
+    if (!ok && lane == 0)
+        for (uint32_t i = g; i < g + S::NV; ++i) mbar_arrive(&c.sh->full[i % S::NV]);
+    if (ahead && g > 0) mbar_wait(&c.sh->first, 0, kDrainPolls);
     for (uint32_t i = g < (uint32_t)S::NV ? 0 : g - S::NV; i < g; ++i)
         mbar_wait(&c.sh->full[i % S::NV], i / S::NV & 1, kDrainPolls);
 }
@@ -915,6 +930,7 @@ template <typename S> struct Row {
         if (st.part >= 0 && !join_parts(room, st, live, j, h, both, sum, wg() * (DP / 2),
                                         (wg() + 1) * (DP / 2)))
             return false;
+        __syncwarp();
         tc_fence_before();
         if (!meet(0)) return false;  // both have read both
         tc_fence_after();
@@ -946,38 +962,57 @@ template <typename S> struct Row {
         if (!meet(meeting)) return false;
         if (!c.sh->last[which][0]) return true;
         __threadfence();
+        if (!live) return true;
         const int lead = c.sh->last[which][1], parts = c.sh->last[which][2];
+        // Loads of several parts in flight: one SM reads them all.
+        auto ml_of = [&](int i) {
+            return __ldcg(room.part_ml + part_place(lead, min(i, parts - 1)) * S::RT + row());
+        };
         float top = -INFINITY, sum = 0.f;
-        for (int i = 0; i < parts; ++i)
-            top = fmaxf(top, __ldcg(room.part_ml + part_place(lead, i) * S::RT + row()).x);
-        const float safe = top == -INFINITY ? 0.f : top;
-        for (int i = 0; i < parts; ++i) {
-            const float2 x = __ldcg(room.part_ml + part_place(lead, i) * S::RT + row());
-            sum = fmaf(x.y, ex2(x.x - safe), sum);
+        for (int i0 = 0; i0 < parts; i0 += 8) {
+            float2 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = ml_of(i0 + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i0 + i >= parts) break;
+                const float now = fmaxf(top, x[i].x), safe = now == -INFINITY ? 0.f : now;
+                sum = fmaf(sum, ex2(top - safe), x[i].y * ex2(x[i].x - safe));
+                top = now;
+            }
         }
+        const float safe = top == -INFINITY ? 0.f : top;
 #pragma unroll 1
         for (int e = d0; e < d1; e += 32) {
             float o[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            for (int i = 0; i < parts; ++i) {
-                const size_t part = part_place(lead, i);
-                const float f = ex2(__ldcg(room.part_ml + part * S::RT + row()).x - safe);
-                float4 v[8];
+            for (int i0 = 0; i0 < parts; i0 += 2) {
+                float f[2];
+                float4 v[2][8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = __ldcg(room.part_o + (part * (DP / 4) + e / 4 + k) * S::RT + row());
+                for (int i = 0; i < 2; ++i) {
+                    f[i] = ml_of(i0 + i).x;
+                    const size_t part = part_place(lead, min(i0 + i, parts - 1));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    o[4 * k] = fmaf(v[k].x, f, o[4 * k]);
-                    o[4 * k + 1] = fmaf(v[k].y, f, o[4 * k + 1]);
-                    o[4 * k + 2] = fmaf(v[k].z, f, o[4 * k + 2]);
-                    o[4 * k + 3] = fmaf(v[k].w, f, o[4 * k + 3]);
+                    for (int k = 0; k < 8; ++k)
+                        v[i][k] = __ldcg(room.part_o + (part * (DP / 4) + e / 4 + k) * S::RT + row());
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i0 + i >= parts) break;
+                    const float g = ex2(f[i] - safe);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        o[4 * k] = fmaf(v[i][k].x, g, o[4 * k]);
+                        o[4 * k + 1] = fmaf(v[i][k].y, g, o[4 * k + 1]);
+                        o[4 * k + 2] = fmaf(v[i][k].z, g, o[4 * k + 2]);
+                        o[4 * k + 3] = fmaf(v[i][k].w, g, o[4 * k + 3]);
+                    }
                 }
             }
-            if (live) finish(j, h, top, sum, e, o);
+            finish(j, h, top, sum, e, o);
         }
-        __syncwarp();
         return true;
     }
     // Dims e .. e + 31 of the row's result from its sums.
@@ -1370,7 +1405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_box) prefetch_tmap(&q_map);
         mbar_init(&c.sh->first, box ? 1 : kLoaders);
         for (int i = 0; i < kMostV; ++i) {
-            mbar_init(&c.sh->full[i], box ? 1 : kLoaders);
+            mbar_init(&c.sh->full[i], box ? 2 : kLoaders);
             mbar_init(&c.sh->done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1420,8 +1455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (S::TERMS == 1) load_queries<S>(a, kv, &q_map, q_box, room, c);
             } else if (!box) {
                 load_rows<S>(a, kv, room, c);
-            } else if (warp == kMma + 1) {
-                load_boxes<S>(a, kv, &k_map, &v_map, box, room, c);
+            } else {
+                const bool is_v = warp == kMma + 2;
+                load_boxes<S>(a, kv, is_v ? &v_map : &k_map, is_v, box, room, c);
             }
         } else if ((threadIdx.x & 31) == 0) {
             issue_products<S>(a, room, c);
