@@ -158,6 +158,55 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 }
 
+// Joins the parts of the row tile that CTA blockIdx.x leads and others go on with.  A thread takes
+// four dims of a row at a time, with the loads of kAtOnce parts in flight.
+constexpr int kAtOnce = 8;
+__global__ void __launch_bounds__(256)
+    attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
+    pdl_enter();
+    const int group = a.group.d;
+    const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
+    const Begin p = room.plan[blockIdx.x + 1];
+    if (p.off == 0 || p.lead != (int)blockIdx.x) return;
+    const Tile tile = room.tiles[p.tile];
+    const Seq q = tile.q;
+    const int rows = min(rt, q.count * group - tile.row0);
+    const TypedOut out{a.out, a.out_type};
+    for (int at = blockIdx.y * 256 + threadIdx.x; at < rt * (kv.head_dim / 4);
+         at += gridDim.y * 256) {
+        const int row = at % rt, c = at / rt;  // rt is a power of two
+        if (row >= rows) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < p.parts; i0 += kAtOnce) {
+            float2 ml[kAtOnce];
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const size_t part = part_place(p.lead, min(i0 + i, p.parts - 1));
+                ml[i] = room.part_ml[part * rt + row];
+                v[i] = room.part_o[(part * (dp / 4) + c) * rt + row];
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (i0 + i >= p.parts) break;
+                const float now = fmaxf(m, ml[i].x), safe = now == -INFINITY ? 0.f : now;
+                const float f = exp2f(m - safe), g = exp2f(ml[i].x - safe);
+                m = now;
+                l = fmaf(l, f, ml[i].y * g);
+                o.x = fmaf(o.x, f, v[i].x * g), o.y = fmaf(o.y, f, v[i].y * g);
+                o.z = fmaf(o.z, f, v[i].z * g), o.w = fmaf(o.w, f, v[i].w * g);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int rr = tile.row0 + row, j = a.group.div(rr), g = rr - j * group;
+        const int t = q.t0 + j, h = p.head * group + g;
+        out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
+                 make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (a.lse && c == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+    }
+}
+
 // ------------------------------------------------------------------ f32 arithmetic --
 
 template <typename T> __device__ __forceinline__ float to_f32(T x) {
@@ -385,6 +434,7 @@ __global__ void __launch_bounds__(256)
                         make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
                 if (tx == 0) room.part_ml[part * RT + r] = make_float2(m[i], l[i]);
             }
+            if (!a.join_inside) continue;
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
@@ -455,10 +505,14 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     cudaError_t err = ensure_smem(attn_rows_kernel<T, DP, R>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
     const int grid = kMaxGrid;
-    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, grid, 2, stream);
+    TokensArgs b = a;
+    b.join_inside = joins_inside(a, kv, S::RT, grid);
+    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, grid, 2, stream);
     if (err != cudaSuccess) return err;
-    return launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, a, kv,
-                      grid);
+    err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, b, kv,
+                     grid);
+    if (err != cudaSuccess || b.join_inside) return err;
+    return launch_attn_parts(b, kv, S::RT, DP, grid, stream);
 }
 template <typename T>
 cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -480,6 +534,13 @@ cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int 
                              int grid, int row_cost, cudaStream_t stream) {
     return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kv.n_heads, rt,
                       kt, dp, grid, row_cost);
+}
+
+cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
+                              cudaStream_t stream) {
+    const int blocks = (rt * (kv.head_dim / 4) + 255) / 256;
+    return launch_pdl(attn_parts_kernel, dim3(grid - 1, blocks < 8 ? blocks : 8), dim3(256), 0,
+                      stream, a, kv, rt, dp, grid);
 }
 
 }  // namespace tok

@@ -6,8 +6,9 @@
 // KT slots.  attn_plan_kernel lists the row tiles with the key tiles that any of their rows sees,
 // sums their costs, and cuts the whole (all kv heads, one after another) into equal contiguous
 // ranges, one for each CTA of a fixed grid, whatever the lengths.  A row tile within one CTA
-// is written by it; the parts of the others are joined by whichever of their CTAs is the last to
-// finish, by the rule of the running softmax, in an order that the lengths fix.
+// is written by it; the parts of the others are joined by the rule of the running softmax, in an
+// order that the lengths fix: by whichever of their CTAs is the last to finish where a row tile
+// has few parts, else by attn_parts_kernel (one CTA alone reads 20 parts in 28 us).
 #pragma once
 
 #include "kv_internal.h"
@@ -226,6 +227,14 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // row_cost: a row tile's start and end count as so many key tiles.
 cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
                              int grid, int row_cost, cudaStream_t stream);
+// Does a row tile have few parts: are there as many row tiles as CTAs?  (That goes by the rows alone;
+// lengths are known on the device only.)
+inline bool joins_inside(const TokensArgs &a, const KvView &kv, int rt, int grid) {
+    return (long long)a.n_tok * a.group.d / rt * kv.n_heads >= grid;
+}
+cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
+                              cudaStream_t stream);
+
 // The tensor-core kernels (attn_tokens_tc.cu).
 bool tokens_tc_takes(const KvView &kv, int q_type);
 void tokens_tc_shape(int n_seq, int n_tok, int group, int q_type, int head_dim, int &rt, int &dp,

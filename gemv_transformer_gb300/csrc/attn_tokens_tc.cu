@@ -950,6 +950,7 @@ template <typename S> struct Row {
                                                int h, float m, float l, int d0, int d1) {
         if (d0 == 0)
             room.part_ml[(2 * blockIdx.x + st.part) * S::RT + row()] = make_float2(m, l);
+        if (!a.join_inside) return true;
         __threadfence();
         // Pairs: a warpgroup has rows of its own.
         const int which = S::PAIR ? wg() : 0, meeting = S::PAIR ? 2 : 0;
@@ -1547,14 +1548,18 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = ensure_smem(attn_tokens_tc_kernel<S>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
-    err = launch_attn_plan(a, kv, S::RT, S::KT, DP, kGrid, PAIR ? 4 : 2, stream);
+    TokensArgs b = a;
+    b.join_inside = joins_inside(a, kv, S::RT, kGrid);
+    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, kGrid, PAIR ? 4 : 2, stream);
     if (err != cudaSuccess) return err;
     CUtensorMap k_map{}, v_map{}, q_map{};
     const int q_box = query_map(q_map, a, kv);
     int box = box_of(kv, S::KT);
     if (box && !(pool_map(k_map, kv, kv.k, box) && pool_map(v_map, kv, kv.v, box))) box = 0;
-    return launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, a, kv,
-                      k_map, v_map, q_map, box, q_box);
+    err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, b, kv,
+                     k_map, v_map, q_map, box, q_box);
+    if (err != cudaSuccess || b.join_inside) return err;
+    return launch_attn_parts(b, kv, S::RT, DP, kGrid, stream);
 }
 template <int DP>
 cudaError_t launch_dim(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,

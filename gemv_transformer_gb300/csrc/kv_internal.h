@@ -102,7 +102,8 @@ struct TokensArgs {
     const uint32_t *tree;
     long long tree_stride;
     int q_type, out_type;
-    bool wide_out;  // rows of out in whole 32-byte runs
+    bool wide_out;     // rows of out in whole 32-byte runs
+    bool join_inside;  // parts of row tiles are joined by the last of their CTAs, not by a launch
     const void *q;
     void *out;
     long long q_stride, out_stride;  // in elements
