@@ -241,6 +241,8 @@ _calls = None
 
 
 _CALLS = ("wq_rope", "wq_kv_append", "wq_attn_paged", "wq_kv_evict")
+_TOKEN_CALLS = ("wq_norm_rope", "wq_norm_rope_grad", "wq_kv_append_norm", "wq_attn_tokens",
+                "wq_kv_accept")
 
 
 def _through_ctypes(f):
@@ -263,7 +265,8 @@ def _load_calls():
     lib = load()
     with _lock:
         if _calls is None and not os.path.exists(CALLS_PATH):
-            _calls = types.SimpleNamespace(**{f: _through_ctypes(getattr(lib, f)) for f in _CALLS})
+            _calls = types.SimpleNamespace(**{f: _through_ctypes(getattr(lib, f))
+                                              for f in _CALLS + _TOKEN_CALLS})
         if _calls is None:
             spec = importlib.util.spec_from_file_location("_wq_calls", CALLS_PATH)
             mod = importlib.util.module_from_spec(spec)
@@ -271,6 +274,9 @@ def _load_calls():
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                        for f in _CALLS),
                      _current_stream, KvCache)
+            mod.bind_tokens(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                              for f in _TOKEN_CALLS),
+                            HeadNorm, RopeAxes, AttnForm)
             _calls = mod
         return _calls
 
@@ -425,17 +431,16 @@ def wq_kv_evict_workspace_bytes(cache, n_seq, max_pages, keep) -> int:
 
 def wq_norm_rope(n, n_heads, head_dim, norm, rope, x, x_stride, out_type, out, out_stride,
                  stream=None) -> int:
-    return load().wq_norm_rope(n, n_heads, head_dim, norm, rope, _p(x), x_stride, out_type,
-                               _p(out), out_stride, _s(stream))
+    return (_calls or _load_calls()).wq_norm_rope(n, n_heads, head_dim, norm, rope, x, x_stride,
+                                                  out_type, out, out_stride, stream)
 
 
 def wq_norm_rope_grad(n, n_heads, head_dim, norm, rope, x, x_stride, grad_out, grad_out_stride,
                       grad_x, grad_x_stride, grad_weight=None, grad_bias=None, workspace=None,
                       workspace_bytes=0, stream=None) -> int:
-    return load().wq_norm_rope_grad(n, n_heads, head_dim, norm, rope, _p(x), x_stride,
-                                    _p(grad_out), grad_out_stride, _p(grad_x), grad_x_stride,
-                                    _p(grad_weight), _p(grad_bias), _p(workspace),
-                                    int(workspace_bytes), _s(stream))
+    return (_calls or _load_calls()).wq_norm_rope_grad(
+        n, n_heads, head_dim, norm, rope, x, x_stride, grad_out, grad_out_stride, grad_x,
+        grad_x_stride, grad_weight, grad_bias, workspace, workspace_bytes, stream)
 
 
 def wq_norm_rope_grad_workspace_bytes(n, n_heads, head_dim) -> int:
@@ -446,19 +451,17 @@ def wq_kv_append_norm(cache, n_tok, h_q, q_norm, k_norm, rope, q, q_stride, k, k
                       v_stride, n_seq, seq, slot, page_table, max_pages, q_type=WQ_F32,
                       q_out=None, q_out_stride=0, acc=None, slot_pos=None, acc_stride=0,
                       stream=None) -> int:
-    return load().wq_kv_append_norm(cache, n_tok, h_q, q_norm, k_norm, rope, _p(q), q_stride,
-                                    _p(k), k_stride, _p(v), v_stride, n_seq, _p(seq), _p(slot),
-                                    _p(page_table), max_pages, q_type, _p(q_out), q_out_stride,
-                                    _p(acc), _p(slot_pos), acc_stride, _s(stream))
+    return (_calls or _load_calls()).wq_kv_append_norm(
+        cache, n_tok, h_q, q_norm, k_norm, rope, q, q_stride, k, k_stride, v, v_stride, n_seq, seq,
+        slot, page_table, max_pages, q_type, q_out, q_out_stride, acc, slot_pos, acc_stride, stream)
 
 
 def wq_attn_tokens(cache, n_seq, n_tok, h_q, scale, form, q_type, q, q_stride, starts, page_table,
                    max_pages, lens, out_type, out, out_stride, lse=None, workspace=None,
                    workspace_bytes=0, stream=None) -> int:
-    return load().wq_attn_tokens(cache, n_seq, n_tok, h_q, scale, form, q_type, _p(q), q_stride,
-                                 _p(starts), _p(page_table), max_pages, _p(lens), out_type,
-                                 _p(out), out_stride, _p(lse), _p(workspace),
-                                 int(workspace_bytes), _s(stream))
+    return (_calls or _load_calls()).wq_attn_tokens(
+        cache, n_seq, n_tok, h_q, scale, form, q_type, q, q_stride, starts, page_table, max_pages,
+        lens, out_type, out, out_stride, lse, workspace, workspace_bytes, stream)
 
 
 def wq_attn_tokens_workspace_bytes(cache, n_seq, n_tok, h_q, q_type) -> int:
@@ -470,9 +473,9 @@ def wq_kv_accept(caches, n_seq, n_tok, page_table, max_pages, starts, parent, to
     """caches: kv_caches(...), or one KvCache."""
     if isinstance(caches, KvCache):
         caches = (KvCache * 1)(caches)
-    return load().wq_kv_accept(caches, len(caches), n_seq, n_tok, _p(page_table), max_pages,
-                               _p(starts), _p(parent), _p(tokens), _p(choice), _p(lens), _p(path),
-                               _p(accepted), _p(next), _p(lens_out), _s(stream))
+    return (_calls or _load_calls()).wq_kv_accept(
+        caches, len(caches), n_seq, n_tok, page_table, max_pages, starts, parent, tokens, choice,
+        lens, path, accepted, next, lens_out, stream)
 
 
 def wq_get_device_status(stream=None) -> int:
