@@ -63,10 +63,8 @@ template <int N, int G, int U> struct Lanes {
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                x.a[i].v[j] = p && has(i) ? p[place[i].a + j] : fill;
-                x.b[i].v[j] = p && has(i) && both(i) ? p[place[i].b + j] : fill;
-            }
+            for (int j = 0; j < N; ++j) x.a[i].v[j] = x.b[i].v[j] = fill;
+        if (p) load(x, p);
     }
     // Values that are not part of the head are 0 in every sum.
     __device__ __forceinline__ void zero_rest(Held<N, U> &x) const {
@@ -91,11 +89,13 @@ template <int N, int G, int U> struct Lanes {
             for (int j = 0; j < N; ++j) v += f(i, j, false) + f(i, j, true);
         return sum_group(v);
     }
-    // x becomes h = (x - mu) r; values beyond the head stay 0.  Returns r.
-    __device__ __forceinline__ float hat(Held<N, U> &x, const NormView &nv) const {
-        if (nv.kind == WQ_HEAD_LAYER) {
-            const float mu =
+    // x becomes h = (x - mu) r with the mean taken off for `layer`; values beyond the head stay 0.
+    // Returns r.  `summed`: a warp's lanes all take the sum for the mean.
+    __device__ __forceinline__ float hat(Held<N, U> &x, bool layer, bool summed, float eps) const {
+        if (summed) {
+            const float mean =
                 sum([&](int i, int j, bool b) { return b ? x.b[i].v[j] : x.a[i].v[j]; }) / head_dim;
+            const float mu = layer ? mean : 0.f;
 #pragma unroll
             for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -106,19 +106,19 @@ template <int N, int G, int U> struct Lanes {
                              const float v = b ? x.b[i].v[j] : x.a[i].v[j];
                              return v * v;
                          }) / head_dim;
-        const float r = 1.f / sqrtf(ms + nv.eps);
+        const float r = 1.f / sqrtf(ms + eps);
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int j = 0; j < N; ++j) x.a[i].v[j] *= r, x.b[i].v[j] *= r;
         return r;
     }
-    __device__ __forceinline__ void norm(Held<N, U> &x, const NormView &nv) const {
-        zero_rest(x);
-        hat(x, nv);
-        Held<N, U> w, c;
-        load_or(w, nv.weight, 1.f);
-        load_or(c, nv.bias, 0.f);
+    __device__ __forceinline__ float hat(Held<N, U> &x, const NormView &nv) const {
+        return hat(x, nv.kind == WQ_HEAD_LAYER, nv.kind == WQ_HEAD_LAYER, nv.eps);
+    }
+    // y of a head with its weights and biases.
+    __device__ __forceinline__ void weigh(Held<N, U> &x, const Held<N, U> &w,
+                                          const Held<N, U> &c) const {
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -212,10 +212,19 @@ __global__ void __launch_bounds__(kThreads)
     if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
     Turns<N, G, U> turns;
     if (ok) turns.load(l, ax, w, ax.flags);
+    Held<N, U> wt, bias;
+    if (nv.kind != WQ_HEAD_NONE) {
+        l.load_or(wt, nv.weight, 1.f);
+        l.load_or(bias, nv.bias, 0.f);
+    }
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i) {
         if (i >= deal.heads_per) break;
-        if (nv.kind != WQ_HEAD_NONE) l.norm(v[i], nv);
+        if (nv.kind != WQ_HEAD_NONE) {
+            l.zero_rest(v[i]);
+            l.hat(v[i], nv);
+            l.weigh(v[i], wt, bias);
+        }
         if (i < n && ok) {
             turns.apply(l, v[i], ax.flags);
             l.store(v[i], o + i * head_dim);
@@ -223,35 +232,40 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Blocks of heads are of q, of k or of v alone: a group of lanes has one norm.
+struct Roles {
+    int q_blocks, kv_blocks;
+};
+
 template <int DT, typename Q, int N, int G, int U>
 __global__ void __launch_bounds__(kThreads)
     append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
-                       AppendNormArgs a, KvView kv, HeadDeal deal, int t0) {
+                       AppendNormArgs a, KvView kv, HeadDeal deal, Roles roles, int t0) {
     pdl_enter();
     using T = typename KvType<DT>::T;
     const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
     const bool live = at < deal.count;
     const unsigned row_at = deal.per_row.div(live ? at : 0u);
-    const int d = kv.head_dim, heads = a.h_q + 2 * kv.n_heads;
-    const int h0 = live ? (int)(at - row_at * deal.per_row.d) * deal.heads_per : 0;
-    const int n = live ? min(deal.heads_per, heads - h0) : 0;
+    int block = live ? (int)(at - row_at * deal.per_row.d) : 0;
+    const int role = block < roles.q_blocks                     ? 0
+                     : block < roles.q_blocks + roles.kv_blocks ? 1
+                                                                : 2;
+    block -= role == 0 ? 0 : role == 1 ? roles.q_blocks : roles.q_blocks + roles.kv_blocks;
+    const int d = kv.head_dim, heads = role == 0 ? a.h_q : kv.n_heads;
+    const int h0 = block * deal.heads_per, n = live ? min(deal.heads_per, heads - h0) : 0;
     const int t = t0 + (int)row_at;
     const int slot = a.slot[t];
     const int seq = a.seq ? a.seq[t] : t;
     const Lanes<N, G, U> l(ax, d);
-    // Heads in the order q, k, v.  The values do not wait for the slot.
+    const float *const x = (role == 0   ? a.q + t * a.q_stride
+                            : role == 1 ? a.k + t * a.k_stride
+                                        : a.v + t * a.v_stride) +
+                           (long long)h0 * d;
+    // The values do not wait for the slot.
     Held<N, U> v[kHeadsPer] = {};
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i)
-        if (i < n) {
-            const int head = h0 + i;
-            const float *x =
-                head < a.h_q ? a.q + t * a.q_stride + (long long)head * d
-                : head < a.h_q + kv.n_heads
-                    ? a.k + t * a.k_stride + (long long)(head - a.h_q) * d
-                    : a.v + t * a.v_stride + (long long)(head - a.h_q - kv.n_heads) * d;
-            l.load(v[i], x);
-        }
+        if (i < n) l.load(v[i], x + i * d);
     Where w;
     bool ok = w.load(ax, t);
     ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
@@ -259,33 +273,40 @@ __global__ void __launch_bounds__(kThreads)
     ok = ok && row >= 0;
     if (live && !ok && slot >= 0 && l.lane == 0) record_status(ax.status, kStBadIndex);
     Turns<N, G, U> turns;
-    if (ok) turns.load(l, ax, w, ax.flags);
+    if (ok && role < 2) turns.load(l, ax, w, ax.flags);
+    // The lanes of a warp may hold both roles: all of them run the sums that either norm has.
+    const bool any = q_norm.kind != WQ_HEAD_NONE || k_norm.kind != WQ_HEAD_NONE;
+    const bool layer = q_norm.kind == WQ_HEAD_LAYER || k_norm.kind == WQ_HEAD_LAYER;
+    const int kind = role == 0 ? q_norm.kind : role == 1 ? k_norm.kind : WQ_HEAD_NONE;
+    const float eps = role == 0 ? q_norm.eps : k_norm.eps;
+    Held<N, U> wt, bias;
+    if (kind != WQ_HEAD_NONE) {
+        l.load_or(wt, role == 0 ? q_norm.weight : k_norm.weight, 1.f);
+        l.load_or(bias, role == 0 ? q_norm.bias : k_norm.bias, 0.f);
+    }
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i) {
         if (i >= deal.heads_per) break;
-        const int head = h0 + i;
-        const bool is_q = head < a.h_q, is_k = !is_q && head < a.h_q + kv.n_heads;
-        // The lanes of a warp may hold heads of both kinds: all of them run both norms' shuffles.
-        if (q_norm.kind != WQ_HEAD_NONE && __any_sync(0xFFFFFFFFu, is_q && i < n)) {
+        if (any) {
             Held<N, U> y = v[i];
-            l.norm(y, q_norm);
-            if (is_q) v[i] = y;
-        }
-        if (k_norm.kind != WQ_HEAD_NONE && __any_sync(0xFFFFFFFFu, is_k && i < n)) {
-            Held<N, U> y = v[i];
-            l.norm(y, k_norm);
-            if (is_k) v[i] = y;
+            l.zero_rest(y);
+            l.hat(y, kind == WQ_HEAD_LAYER, layer, eps);
+            if (kind != WQ_HEAD_NONE) {
+                l.weigh(y, wt, bias);
+                v[i] = y;
+            }
         }
         if (i >= n || !ok) continue;
-        if (is_q || is_k) turns.apply(l, v[i], ax.flags);
-        if (is_q) {
+        if (role < 2) turns.apply(l, v[i], ax.flags);
+        const int head = h0 + i;
+        if (role == 0) {
             l.store(v[i], static_cast<Q *>(a.q_out) + t * a.q_out_stride + (long long)head * d);
             continue;
         }
-        const int h = head - a.h_q - (is_k ? 0 : kv.n_heads);
-        l.store(v[i], reinterpret_cast<T *>((is_k ? kv.k : kv.v) + row + h * kv.head_stride));
-        if (is_k && l.lane == 0) {
-            const long long to = ((long long)seq * kv.n_heads + h) * a.acc_stride + slot;
+        l.store(v[i],
+                reinterpret_cast<T *>((role == 1 ? kv.k : kv.v) + row + head * kv.head_stride));
+        if (role == 1 && l.lane == 0) {
+            const long long to = ((long long)seq * kv.n_heads + head) * a.acc_stride + slot;
             if (a.acc) a.acc[to] = 0.f;
             if (a.slot_pos) a.slot_pos[to] = w.p[0];
         }
@@ -460,7 +481,7 @@ cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int 
     const int ob = out_type == kF32 ? 4 : 2;
     // A run of four 16-bit values is 8 bytes; the rows' 16-byte rule covers it.
     const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
-                      all16({x, out}, {4 * x_stride, ob * out_stride});
+                      all16({x, out, nv.weight, nv.bias}, {4 * x_stride, ob * out_stride});
     HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kHeadsPer, dev);
     // Launches of so many rows that their threads are counted in 31 bits.
     const long long step = (0x7FFFFF00ll / lanes_of(wide, head_dim)) / deal.per_row.d;
@@ -486,10 +507,14 @@ cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const
                                cudaStream_t stream) {
     const int qb = a.q_type == kF32 ? 4 : 2;
     const bool q16 = a.h_q == 0 || all16({a.q, a.q_out}, {4 * a.q_stride, qb * a.q_out_stride});
-    const bool wide =
-        ax.rot % 8 == 0 && q16 && all16({a.k, a.v}, {4 * a.k_stride, 4 * a.v_stride});
-    const int d = kv.head_dim, heads = a.h_q + 2 * kv.n_heads;
-    HeadDeal deal = deal_of(a.n_tok, heads, lanes_of(wide, d), kHeadsPer, dev);
+    const bool wide = ax.rot % 8 == 0 && q16 &&
+                      all16({a.k, a.v, q_norm.weight, q_norm.bias, k_norm.weight, k_norm.bias},
+                            {4 * a.k_stride, 4 * a.v_stride});
+    const int d = kv.head_dim;
+    HeadDeal deal = deal_of(a.n_tok, a.h_q + 2 * kv.n_heads, lanes_of(wide, d), kHeadsPer, dev);
+    const Roles roles{(a.h_q + deal.heads_per - 1) / deal.heads_per,
+                      (kv.n_heads + deal.heads_per - 1) / deal.heads_per};
+    deal.per_row = make_fast_div((uint32_t)(roles.q_blocks + 2 * roles.kv_blocks));
     const long long step = (0x7FFFFF00ll / lanes_of(wide, d)) / deal.per_row.d;
     for (long long t0 = 0; t0 < a.n_tok; t0 += step) {
         deal.count = (unsigned)((a.n_tok - t0 < step ? a.n_tok - t0 : step) * deal.per_row.d);
@@ -501,7 +526,7 @@ cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const
                     return launch_pdl(
                         append_norm_kernel<DT.value, Q, N.value, G.value, U.value>,
                         dim3((deal.count + per - 1) / per), dim3(kThreads), 0, stream, ax, q_norm,
-                        k_norm, a, kv, deal, (int)t0);
+                        k_norm, a, kv, deal, roles, (int)t0);
                 });
             });
         };
@@ -520,7 +545,8 @@ cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n,
                                   long long grad_x_stride, float *grad_weight, float *grad_bias,
                                   void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
     const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
-                      all16({x, grad, grad_x}, {4 * x_stride, 4 * grad_stride, 4 * grad_x_stride});
+                      all16({x, grad, grad_x, nv.weight},
+                            {4 * x_stride, 4 * grad_stride, 4 * grad_x_stride});
     HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kGradHeads, dev);
     deal.count = (unsigned)n * deal.per_row.d;
     const bool sums = grad_weight || grad_bias;
