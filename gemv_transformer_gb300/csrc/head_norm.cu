@@ -34,10 +34,12 @@ template <int N, int U> struct Held {
 // The lanes' common view of a head: G lanes, unit lane + G i for i < U.
 template <int N, int G, int U> struct Lanes {
     int lane, units, head_dim;
+    float inv_d;
     Place place[U];
     __device__ __forceinline__ Lanes(const AxesView &ax, int d) : head_dim(d) {
         lane = threadIdx.x & (G - 1);
         units = (d + 2 * N - 1) / (2 * N);
+        inv_d = 1.f / d;
 #pragma unroll
         for (int i = 0; i < U; ++i) place[i] = place_of<N>(lane + G * i, ax.rot, ax.flags);
     }
@@ -66,55 +68,64 @@ template <int N, int G, int U> struct Lanes {
             for (int j = 0; j < N; ++j) x.a[i].v[j] = x.b[i].v[j] = fill;
         if (p) load(x, p);
     }
-    // Values that are not part of the head are 0 in every sum.
-    __device__ __forceinline__ void zero_rest(Held<N, U> &x) const {
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (!has(i)) x.a[i].v[j] = 0.f;
-                if (!has(i) || !both(i)) x.b[i].v[j] = 0.f;
-            }
-    }
-    __device__ __forceinline__ static float sum_group(float v) {
-#pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        return v;
-    }
-    template <typename F> __device__ __forceinline__ float sum(F f) const {
+    // f(i, j, b) over a lane's values of a head, and its sums over the G lanes of H heads together:
+    // their shuffles are in flight at the same time.
+    template <typename F> __device__ __forceinline__ static float part(F f) {
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int j = 0; j < N; ++j) v += f(i, j, false) + f(i, j, true);
-        return sum_group(v);
+        return v;
     }
-    // x becomes h = (x - mu) r with the mean taken off for `layer`; values beyond the head stay 0.
-    // Returns r.  `summed`: a warp's lanes all take the sum for the mean.
-    __device__ __forceinline__ float hat(Held<N, U> &x, bool layer, bool summed, float eps) const {
+    template <int H> __device__ __forceinline__ static void sum_groups(float (&v)[H], int heads) {
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                if (h < heads) v[h] += __shfl_xor_sync(0xFFFFFFFFu, v[h], o);
+    }
+    // The first `heads` of x become (x - mu) r by the group's kind of norm (none: as they were); their
+    // r.  Values beyond a head are 0 and stay so.  `summed`: any lane of the launch takes a mean;
+    // a warp's lanes may have different kinds and shuffle together.
+    template <int H>
+    __device__ __forceinline__ void hat(Held<N, U> (&x)[H], int heads, int kind, bool summed,
+                                        float eps, float (&r)[H]) const {
         if (summed) {
-            const float mean =
-                sum([&](int i, int j, bool b) { return b ? x.b[i].v[j] : x.a[i].v[j]; }) / head_dim;
-            const float mu = layer ? mean : 0.f;
+            float mu[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                mu[h] = part([&](int i, int j, bool b) {
+                    return b ? x[h].b[i].v[j] : x[h].a[i].v[j];
+                });
+            sum_groups(mu, heads);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float m = kind == WQ_HEAD_LAYER ? mu[h] * inv_d : 0.f;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        x[h].a[i].v[j] -= has(i) ? m : 0.f;
+                        x[h].b[i].v[j] -= has(i) && both(i) ? m : 0.f;
+                    }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            r[h] = part([&](int i, int j, bool b) {
+                const float v = b ? x[h].b[i].v[j] : x[h].a[i].v[j];
+                return v * v;
+            });
+        sum_groups(r, heads);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            r[h] = kind == WQ_HEAD_NONE ? 1.f : rsqrtf(fmaf(r[h], inv_d, eps));
 #pragma unroll
             for (int i = 0; i < U; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j) x.a[i].v[j] -= mu, x.b[i].v[j] -= mu;
-            zero_rest(x);
+                for (int j = 0; j < N; ++j) x[h].a[i].v[j] *= r[h], x[h].b[i].v[j] *= r[h];
         }
-        const float ms = sum([&](int i, int j, bool b) {
-                             const float v = b ? x.b[i].v[j] : x.a[i].v[j];
-                             return v * v;
-                         }) / head_dim;
-        const float r = 1.f / sqrtf(ms + eps);
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) x.a[i].v[j] *= r, x.b[i].v[j] *= r;
-        return r;
-    }
-    __device__ __forceinline__ float hat(Held<N, U> &x, const NormView &nv) const {
-        return hat(x, nv.kind == WQ_HEAD_LAYER, nv.kind == WQ_HEAD_LAYER, nv.eps);
     }
     // y of a head with its weights and biases.
     __device__ __forceinline__ void weigh(Held<N, U> &x, const Held<N, U> &w,
@@ -147,16 +158,24 @@ struct Where {
     }
 };
 
+// The pairs' axes and columns in shared memory: lanes that read different parameters wait for one
+// another.
+__device__ __forceinline__ void stage_codes(const AxesView &ax, uint16_t *codes) {
+    if (ax.straight || ax.rot == 0) return;  // (the same for all)
+    for (int i = threadIdx.x; i < ax.rot / 2; i += kThreads) codes[i] = ax.code[i];
+    __syncthreads();
+}
+
 // The angles of unit u's N pairs.
 template <int N>
-__device__ __forceinline__ Angles<N> angles_of(const AxesView &ax, const Where &w, int u,
-                                               unsigned flags) {
+__device__ __forceinline__ Angles<N> angles_of(const AxesView &ax, const uint16_t *codes,
+                                               const Where &w, int u, unsigned flags) {
     if (ax.straight)
         return load_angles<N>(ax.table + (long long)w.p[0] * ax.table_pairs + u * N, flags);
     Angles<N> r;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int code = ax.code[u * N + j];
+        const int code = codes[u * N + j];
         const float2 cs = ax.table[(long long)w.of(code >> 8) * ax.table_pairs + (code & 255)];
         r.c[j] = cs.x;
         r.s[j] = flags & WQ_ROPE_TRANSPOSE ? -cs.y : cs.y;
@@ -167,10 +186,10 @@ __device__ __forceinline__ Angles<N> angles_of(const AxesView &ax, const Where &
 template <int N, int G, int U> struct Turns {
     Angles<N> cs[U];
     __device__ __forceinline__ void load(const Lanes<N, G, U> &l, const AxesView &ax,
-                                         const Where &w, unsigned flags) {
+                                         const uint16_t *codes, const Where &w, unsigned flags) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (l.place[i].turn) cs[i] = angles_of<N>(ax, w, l.lane + G * i, flags);
+            if (l.place[i].turn) cs[i] = angles_of<N>(ax, codes, w, l.lane + G * i, flags);
     }
     __device__ __forceinline__ void apply(const Lanes<N, G, U> &l, Held<N, U> &x,
                                           unsigned flags) const {
@@ -192,6 +211,8 @@ __global__ void __launch_bounds__(kThreads)
     norm_rope_kernel(const __grid_constant__ AxesView ax, NormView nv, HeadDeal deal, int head_dim,
                      const float *x, long long x_stride, int n_heads, T *out, long long out_stride,
                      long long t0) {
+    __shared__ uint16_t s_codes[128];
+    stage_codes(ax, s_codes);
     pdl_enter();
     const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
     // Every lane stays for the shuffles.
@@ -211,25 +232,23 @@ __global__ void __launch_bounds__(kThreads)
     const bool ok = w.load(ax, t);
     if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
     Turns<N, G, U> turns;
-    if (ok) turns.load(l, ax, w, ax.flags);
+    if (ok) turns.load(l, ax, s_codes, w, ax.flags);
     Held<N, U> wt, bias;
     if (nv.kind != WQ_HEAD_NONE) {
         l.load_or(wt, nv.weight, 1.f);
         l.load_or(bias, nv.bias, 0.f);
     }
+    if (nv.kind != WQ_HEAD_NONE) {
+        float r[kHeadsPer];
+        l.hat(v, deal.heads_per, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
+    }
 #pragma unroll
-    for (int i = 0; i < kHeadsPer; ++i) {
-        if (i >= deal.heads_per) break;
-        if (nv.kind != WQ_HEAD_NONE) {
-            l.zero_rest(v[i]);
-            l.hat(v[i], nv);
-            l.weigh(v[i], wt, bias);
-        }
+    for (int i = 0; i < kHeadsPer; ++i)
         if (i < n && ok) {
+            if (nv.kind != WQ_HEAD_NONE) l.weigh(v[i], wt, bias);
             turns.apply(l, v[i], ax.flags);
             l.store(v[i], o + i * head_dim);
         }
-    }
 }
 
 // Blocks of heads are of q, of k or of v alone: a group of lanes has one norm.
@@ -241,6 +260,8 @@ template <int DT, typename Q, int N, int G, int U>
 __global__ void __launch_bounds__(kThreads)
     append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
                        AppendNormArgs a, KvView kv, HeadDeal deal, Roles roles, int t0) {
+    __shared__ uint16_t s_codes[128];
+    stage_codes(ax, s_codes);
     pdl_enter();
     using T = typename KvType<DT>::T;
     const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
     ok = ok && row >= 0;
     if (live && !ok && slot >= 0 && l.lane == 0) record_status(ax.status, kStBadIndex);
     Turns<N, G, U> turns;
-    if (ok && role < 2) turns.load(l, ax, w, ax.flags);
+    if (ok && role < 2) turns.load(l, ax, s_codes, w, ax.flags);
     // The lanes of a warp may hold both roles: all of them run the sums that either norm has.
     const bool any = q_norm.kind != WQ_HEAD_NONE || k_norm.kind != WQ_HEAD_NONE;
     const bool layer = q_norm.kind == WQ_HEAD_LAYER || k_norm.kind == WQ_HEAD_LAYER;
@@ -284,18 +305,15 @@ __global__ void __launch_bounds__(kThreads)
         l.load_or(wt, role == 0 ? q_norm.weight : k_norm.weight, 1.f);
         l.load_or(bias, role == 0 ? q_norm.bias : k_norm.bias, 0.f);
     }
+    if (any) {
+        float r[kHeadsPer];
+        l.hat(v, deal.heads_per, kind, layer, eps, r);
+        if (kind != WQ_HEAD_NONE)
+#pragma unroll
+            for (int i = 0; i < kHeadsPer; ++i) l.weigh(v[i], wt, bias);
+    }
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i) {
-        if (i >= deal.heads_per) break;
-        if (any) {
-            Held<N, U> y = v[i];
-            l.zero_rest(y);
-            l.hat(y, kind == WQ_HEAD_LAYER, layer, eps);
-            if (kind != WQ_HEAD_NONE) {
-                l.weigh(y, wt, bias);
-                v[i] = y;
-            }
-        }
         if (i >= n || !ok) continue;
         if (role < 2) turns.apply(l, v[i], ax.flags);
         const int head = h0 + i;
@@ -322,6 +340,8 @@ __global__ void __launch_bounds__(kThreads)
                           long long grad_stride, int n_heads, float *grad_x,
                           long long grad_x_stride, float *parts) {
     extern __shared__ float s_sums[];  // [groups][2][head_dim]
+    __shared__ uint16_t s_codes[128];
+    stage_codes(ax, s_codes);
     pdl_enter();
     const Lanes<N, G, U> l(ax, head_dim);
     const unsigned flags = ax.flags | WQ_ROPE_TRANSPOSE;
@@ -348,17 +368,16 @@ __global__ void __launch_bounds__(kThreads)
         const bool ok = w.load(ax, t);
         if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
         Turns<N, G, U> turns;
-        if (ok) turns.load(l, ax, w, flags);
+        if (ok) turns.load(l, ax, s_codes, w, flags);
 #pragma unroll
-        for (int i = 0; i < kGradHeads; ++i) {
-            if (i >= deal.heads_per) break;
-            const bool mine = i < n && ok;
-            if (mine) turns.apply(l, g[i], flags);
-            if (nv.kind != WQ_HEAD_NONE) {
-                l.zero_rest(v[i]);
-                l.zero_rest(g[i]);
-                const float r = l.hat(v[i], nv);
-                if (mine) {
+        for (int i = 0; i < kGradHeads; ++i)
+            if (i < n && ok) turns.apply(l, g[i], flags);
+        if (nv.kind != WQ_HEAD_NONE) {
+            float r[kGradHeads], uh[kGradHeads], mu[kGradHeads];
+            l.hat(v, deal.heads_per, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
+#pragma unroll
+            for (int i = 0; i < kGradHeads; ++i) {
+                if (i < n && ok) {
 #pragma unroll
                     for (int k = 0; k < U; ++k)
 #pragma unroll
@@ -376,25 +395,32 @@ __global__ void __launch_bounds__(kThreads)
                         g[i].a[k].v[j] *= wt.a[k].v[j];
                         g[i].b[k].v[j] *= wt.b[k].v[j];
                     }
-                const float uh = l.sum([&](int k, int j, bool b) {
-                                     return b ? g[i].b[k].v[j] * v[i].b[k].v[j]
-                                              : g[i].a[k].v[j] * v[i].a[k].v[j];
-                                 }) / head_dim;
-                float mu = 0.f;
-                if (nv.kind == WQ_HEAD_LAYER)
-                    mu = l.sum([&](int k, int j, bool b) {
-                             return b ? g[i].b[k].v[j] : g[i].a[k].v[j];
-                         }) / head_dim;
+                uh[i] = l.part([&](int k, int j, bool b) {
+                    return b ? g[i].b[k].v[j] * v[i].b[k].v[j] : g[i].a[k].v[j] * v[i].a[k].v[j];
+                });
+                mu[i] = l.part([&](int k, int j, bool b) {
+                    return b ? g[i].b[k].v[j] : g[i].a[k].v[j];
+                });
+            }
+            l.sum_groups(uh, deal.heads_per);
+            if (nv.kind == WQ_HEAD_LAYER) l.sum_groups(mu, deal.heads_per);
+#pragma unroll
+            for (int i = 0; i < kGradHeads; ++i) {
+                const float h = uh[i] * l.inv_d;
+                const float m = nv.kind == WQ_HEAD_LAYER ? mu[i] * l.inv_d : 0.f;
 #pragma unroll
                 for (int k = 0; k < U; ++k)
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        g[i].a[k].v[j] = r * (g[i].a[k].v[j] - v[i].a[k].v[j] * uh - mu);
-                        g[i].b[k].v[j] = r * (g[i].b[k].v[j] - v[i].b[k].v[j] * uh - mu);
+                        g[i].a[k].v[j] = r[i] * (g[i].a[k].v[j] - v[i].a[k].v[j] * h - m);
+                        g[i].b[k].v[j] = r[i] * (g[i].b[k].v[j] - v[i].b[k].v[j] * h - m);
                     }
             }
-            if (mine) l.store(g[i], grad_x + t * grad_x_stride + (long long)(h0 + i) * head_dim);
         }
+#pragma unroll
+        for (int i = 0; i < kGradHeads; ++i)
+            if (i < n && ok)
+                l.store(g[i], grad_x + t * grad_x_stride + (long long)(h0 + i) * head_dim);
     }
     if (!parts) return;
     float *mine = s_sums + (threadIdx.x / G) * 2 * head_dim;
