@@ -78,19 +78,17 @@ template <int N, int G, int U> struct Lanes {
             for (int j = 0; j < N; ++j) v += f(i, j, false) + f(i, j, true);
         return v;
     }
-    template <int H> __device__ __forceinline__ static void sum_groups(float (&v)[H], int heads) {
+    template <int H> __device__ __forceinline__ static void sum_groups(float (&v)[H]) {
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1)
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-                if (h < heads) v[h] += __shfl_xor_sync(0xFFFFFFFFu, v[h], o);
+            for (int h = 0; h < H; ++h) v[h] += __shfl_xor_sync(0xFFFFFFFFu, v[h], o);
     }
-    // The first `heads` of x become (x - mu) r by the group's kind of norm (none: as they were); their
-    // r.  Values beyond a head are 0 and stay so.  `summed`: any lane of the launch takes a mean;
+    // x become (x - mu) r by the group's kind of norm (none: as they were); their r.  Values beyond a head are 0 and stay so.  `summed`: any lane of the launch takes a mean;
     // a warp's lanes may have different kinds and shuffle together.
     template <int H>
-    __device__ __forceinline__ void hat(Held<N, U> (&x)[H], int heads, int kind, bool summed,
-                                        float eps, float (&r)[H]) const {
+    __device__ __forceinline__ void hat(Held<N, U> (&x)[H], int kind, bool summed, float eps,
+                                        float (&r)[H]) const {
         if (summed) {
             float mu[H];
 #pragma unroll
@@ -98,7 +96,7 @@ template <int N, int G, int U> struct Lanes {
                 mu[h] = part([&](int i, int j, bool b) {
                     return b ? x[h].b[i].v[j] : x[h].a[i].v[j];
                 });
-            sum_groups(mu, heads);
+            sum_groups(mu);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float m = kind == WQ_HEAD_LAYER ? mu[h] * inv_d : 0.f;
@@ -117,7 +115,7 @@ template <int N, int G, int U> struct Lanes {
                 const float v = b ? x[h].b[i].v[j] : x[h].a[i].v[j];
                 return v * v;
             });
-        sum_groups(r, heads);
+        sum_groups(r);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             r[h] = kind == WQ_HEAD_NONE ? 1.f : rsqrtf(fmaf(r[h], inv_d, eps));
@@ -202,7 +200,6 @@ template <int N, int G, int U> struct Turns {
 // Groups of lanes over rows and blocks of heads.
 struct HeadDeal {
     FastDiv per_row;  // blocks of heads in a row
-    int heads_per;
     unsigned count;
 };
 
@@ -218,8 +215,8 @@ __global__ void __launch_bounds__(kThreads)
     // Every lane stays for the shuffles.
     const bool live = at < deal.count;
     const unsigned row = deal.per_row.div(live ? at : 0u);
-    const int h0 = live ? (int)(at - row * deal.per_row.d) * deal.heads_per : 0;
-    const int n = live ? min(deal.heads_per, n_heads - h0) : 0;
+    const int h0 = live ? (int)(at - row * deal.per_row.d) * kHeadsPer : 0;
+    const int n = live ? min(kHeadsPer, n_heads - h0) : 0;
     const long long t = t0 + row;
     const Lanes<N, G, U> l(ax, head_dim);
     const float *xi = x + t * x_stride + (long long)h0 * head_dim;
@@ -240,7 +237,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (nv.kind != WQ_HEAD_NONE) {
         float r[kHeadsPer];
-        l.hat(v, deal.heads_per, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
+        l.hat(v, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i)
@@ -273,7 +270,7 @@ __global__ void __launch_bounds__(kThreads)
                                                                 : 2;
     block -= role == 0 ? 0 : role == 1 ? roles.q_blocks : roles.q_blocks + roles.kv_blocks;
     const int d = kv.head_dim, heads = role == 0 ? a.h_q : kv.n_heads;
-    const int h0 = block * deal.heads_per, n = live ? min(deal.heads_per, heads - h0) : 0;
+    const int h0 = block * kHeadsPer, n = live ? min(kHeadsPer, heads - h0) : 0;
     const int t = t0 + (int)row_at;
     const int slot = a.slot[t];
     const int seq = a.seq ? a.seq[t] : t;
@@ -307,7 +304,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (any) {
         float r[kHeadsPer];
-        l.hat(v, deal.heads_per, kind, layer, eps, r);
+        l.hat(v, kind, layer, eps, r);
         if (kind != WQ_HEAD_NONE)
 #pragma unroll
             for (int i = 0; i < kHeadsPer; ++i) l.weigh(v[i], wt, bias);
@@ -355,8 +352,8 @@ __global__ void __launch_bounds__(kThreads)
         const bool live = where < deal.count;
         const unsigned at = live ? (unsigned)where : 0u;
         const unsigned t = deal.per_row.div(at);
-        const int h0 = (int)(at - t * deal.per_row.d) * deal.heads_per;
-        const int n = live ? min(deal.heads_per, n_heads - h0) : 0;
+        const int h0 = (int)(at - t * deal.per_row.d) * kGradHeads;
+        const int n = live ? min(kGradHeads, n_heads - h0) : 0;
         Held<N, U> v[kGradHeads] = {}, g[kGradHeads] = {};
 #pragma unroll
         for (int i = 0; i < kGradHeads; ++i)
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(kThreads)
             if (i < n && ok) turns.apply(l, g[i], flags);
         if (nv.kind != WQ_HEAD_NONE) {
             float r[kGradHeads], uh[kGradHeads], mu[kGradHeads];
-            l.hat(v, deal.heads_per, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
+            l.hat(v, nv.kind, nv.kind == WQ_HEAD_LAYER, nv.eps, r);
 #pragma unroll
             for (int i = 0; i < kGradHeads; ++i) {
                 if (i < n && ok) {
@@ -402,8 +399,8 @@ __global__ void __launch_bounds__(kThreads)
                     return b ? g[i].b[k].v[j] : g[i].a[k].v[j];
                 });
             }
-            l.sum_groups(uh, deal.heads_per);
-            if (nv.kind == WQ_HEAD_LAYER) l.sum_groups(mu, deal.heads_per);
+            l.sum_groups(uh);
+            if (nv.kind == WQ_HEAD_LAYER) l.sum_groups(mu);
 #pragma unroll
             for (int i = 0; i < kGradHeads; ++i) {
                 const float h = uh[i] * l.inv_d;
@@ -466,15 +463,8 @@ bool all16(std::initializer_list<const void *> ps, std::initializer_list<long lo
     return true;
 }
 
-// heads_most heads to a group when that still leaves every SM its 2048 threads.
-HeadDeal deal_of(long long rows, int heads, int lanes, int heads_most, const DeviceInfo &dev) {
-    HeadDeal d;
-    d.heads_per = rows * ((heads + heads_most - 1) / heads_most) * lanes >= 2048ll * dev.sm_count
-                      ? heads_most : 1;
-    d.per_row = make_fast_div((uint32_t)((heads + d.heads_per - 1) / d.heads_per));
-    d.count = 0;
-    return d;
-}
+HeadDeal deal_of(int blocks) { return {make_fast_div((uint32_t)blocks), 0u}; }
+int blocks_of(int heads, int per) { return (heads + per - 1) / per; }
 
 // F is called with the units' shape: pairs of a run, lanes of a head, units of a lane.
 template <typename F> cudaError_t by_shape(bool wide, int head_dim, F f) {
@@ -508,7 +498,7 @@ cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int 
     // A run of four 16-bit values is 8 bytes; the rows' 16-byte rule covers it.
     const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
                       all16({x, out, nv.weight, nv.bias}, {4 * x_stride, ob * out_stride});
-    HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kHeadsPer, dev);
+    HeadDeal deal = deal_of(blocks_of(n_heads, kHeadsPer));
     // Launches of so many rows that their threads are counted in 31 bits.
     const long long step = (0x7FFFFF00ll / lanes_of(wide, head_dim)) / deal.per_row.d;
     for (long long t0 = 0; t0 < n; t0 += step) {
@@ -537,10 +527,8 @@ cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const
                       all16({a.k, a.v, q_norm.weight, q_norm.bias, k_norm.weight, k_norm.bias},
                             {4 * a.k_stride, 4 * a.v_stride});
     const int d = kv.head_dim;
-    HeadDeal deal = deal_of(a.n_tok, a.h_q + 2 * kv.n_heads, lanes_of(wide, d), kHeadsPer, dev);
-    const Roles roles{(a.h_q + deal.heads_per - 1) / deal.heads_per,
-                      (kv.n_heads + deal.heads_per - 1) / deal.heads_per};
-    deal.per_row = make_fast_div((uint32_t)(roles.q_blocks + 2 * roles.kv_blocks));
+    const Roles roles{blocks_of(a.h_q, kHeadsPer), blocks_of(kv.n_heads, kHeadsPer)};
+    HeadDeal deal = deal_of(roles.q_blocks + 2 * roles.kv_blocks);
     const long long step = (0x7FFFFF00ll / lanes_of(wide, d)) / deal.per_row.d;
     for (long long t0 = 0; t0 < a.n_tok; t0 += step) {
         deal.count = (unsigned)((a.n_tok - t0 < step ? a.n_tok - t0 : step) * deal.per_row.d);
@@ -573,7 +561,7 @@ cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n,
     const bool wide = head_dim % 8 == 0 && ax.rot % 8 == 0 &&
                       all16({x, grad, grad_x, nv.weight},
                             {4 * x_stride, 4 * grad_stride, 4 * grad_x_stride});
-    HeadDeal deal = deal_of(n, n_heads, lanes_of(wide, head_dim), kGradHeads, dev);
+    HeadDeal deal = deal_of(blocks_of(n_heads, kGradHeads));
     deal.count = (unsigned)n * deal.per_row.d;
     const bool sums = grad_weight || grad_bias;
     float *parts = sums ? static_cast<float *>(workspace) : nullptr;
