@@ -46,18 +46,20 @@ template <int N, int G, int U> struct Lanes {
     __device__ __forceinline__ bool has(int i) const { return lane + G * i < units; }
     // An odd head_dim ends in a single value.
     __device__ __forceinline__ bool both(int i) const { return N > 1 || place[i].b < head_dim; }
-    __device__ __forceinline__ void load(Held<N, U> &x, const float *p) const {
+    // A head at p + at (elements): 32-bit offsets from a row's address, which is worked out once.
+    __device__ __forceinline__ void load(Held<N, U> &x, const float *p, unsigned at = 0) const {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (has(i)) x.a[i] = load_vals<N>(p + place[i].a);
-            if (has(i) && both(i)) x.b[i] = load_vals<N>(p + place[i].b);
+            if (has(i)) x.a[i] = load_vals<N>(p + (at + place[i].a));
+            if (has(i) && both(i)) x.b[i] = load_vals<N>(p + (at + place[i].b));
         }
     }
-    template <typename T> __device__ __forceinline__ void store(const Held<N, U> &x, T *p) const {
+    template <typename T>
+    __device__ __forceinline__ void store(const Held<N, U> &x, T *p, unsigned at = 0) const {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (has(i)) store_vals(p + place[i].a, x.a[i]);
-            if (has(i) && both(i)) store_vals(p + place[i].b, x.b[i]);
+            if (has(i)) store_vals(p + (at + place[i].a), x.a[i]);
+            if (has(i) && both(i)) store_vals(p + (at + place[i].b), x.b[i]);
         }
     }
     // Weights or biases: `fill` where there are none.
@@ -151,43 +153,32 @@ struct Where {
         }
         return ok;
     }
-    __device__ __forceinline__ int of(int axis) const {
-        return axis == 0 ? p[0] : axis == 1 ? p[1] : axis == 2 ? p[2] : p[3];
-    }
 };
 
-// The pairs' axes and columns in shared memory: lanes that read different parameters wait for one
-// another.
-__device__ __forceinline__ void stage_codes(const AxesView &ax, uint16_t *codes) {
-    if (ax.straight || ax.rot == 0) return;  // (the same for all)
-    for (int i = threadIdx.x; i < ax.rot / 2; i += kThreads) codes[i] = ax.code[i];
-    __syncthreads();
-}
-
-// The angles of unit u's N pairs.
-template <int N>
-__device__ __forceinline__ Angles<N> angles_of(const AxesView &ax, const uint16_t *codes,
-                                               const Where &w, int u, unsigned flags) {
-    if (ax.straight)
-        return load_angles<N>(ax.table + (long long)w.p[0] * ax.table_pairs + u * N, flags);
-    Angles<N> r;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int code = codes[u * N + j];
-        const float2 cs = ax.table[(long long)w.of(code >> 8) * ax.table_pairs + (code & 255)];
-        r.c[j] = cs.x;
-        r.s[j] = flags & WQ_ROPE_TRANSPOSE ? -cs.y : cs.y;
+// The angles of the rows that a block works on, [rows][rot / 2] in shared memory, where pairs go by
+// several axes: gathered once for all of a row's heads (each group of lanes for itself: an append
+// of 8002 tokens took 60 us).  Positions out of range leave zeros, which no one uses.
+__device__ __forceinline__ void stage_angles(const AxesView &ax, float2 *angles, long long t,
+                                             int rows) {
+    const int half = ax.rot >> 1;
+    for (int i = threadIdx.x; i < rows * half; i += kThreads) {
+        const int r = i / half, code = ax.code[i - r * half];
+        const int pos = ax.pos[(code >> 8) * ax.pos_stride + t + r];
+        angles[i] = (unsigned)pos < (unsigned)ax.table_rows
+                        ? ax.table[(long long)pos * ax.table_pairs + (code & 255)]
+                        : make_float2(0.f, 0.f);
     }
-    return r;
 }
+__device__ __forceinline__ bool stages(const AxesView &ax) { return ax.rot > 0 && !ax.straight; }
 
+// A row's angles: `at` is its first.
 template <int N, int G, int U> struct Turns {
     Angles<N> cs[U];
-    __device__ __forceinline__ void load(const Lanes<N, G, U> &l, const AxesView &ax,
-                                         const uint16_t *codes, const Where &w, unsigned flags) {
+    __device__ __forceinline__ void load(const Lanes<N, G, U> &l, const float2 *at,
+                                         unsigned flags) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (l.place[i].turn) cs[i] = angles_of<N>(ax, codes, w, l.lane + G * i, flags);
+            if (l.place[i].turn) cs[i] = load_angles<N>(at + (l.lane + G * i) * N, flags);
     }
     __device__ __forceinline__ void apply(const Lanes<N, G, U> &l, Held<N, U> &x,
                                           unsigned flags) const {
@@ -204,17 +195,16 @@ struct HeadDeal {
 };
 
 template <typename T, int N, int G, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
     norm_rope_kernel(const __grid_constant__ AxesView ax, NormView nv, HeadDeal deal, int head_dim,
                      const float *x, long long x_stride, int n_heads, T *out, long long out_stride,
                      long long t0) {
-    __shared__ uint16_t s_codes[128];
-    stage_codes(ax, s_codes);
+    extern __shared__ __align__(16) float2 s_angles[];
     pdl_enter();
-    const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    const unsigned first = blockIdx.x * (unsigned)(kThreads / G), at = first + threadIdx.x / G;
     // Every lane stays for the shuffles.
     const bool live = at < deal.count;
-    const unsigned row = deal.per_row.div(live ? at : 0u);
+    const unsigned row0 = deal.per_row.div(first), row = live ? deal.per_row.div(at) : row0;
     const int h0 = live ? (int)(at - row * deal.per_row.d) * kHeadsPer : 0;
     const int n = live ? min(kHeadsPer, n_heads - h0) : 0;
     const long long t = t0 + row;
@@ -224,12 +214,19 @@ __global__ void __launch_bounds__(kThreads)
     Held<N, U> v[kHeadsPer] = {};
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i)
-        if (i < n) l.load(v[i], xi + i * head_dim);
+        if (i < n) l.load(v[i], xi, i * head_dim);
     Where w;
     const bool ok = w.load(ax, t);
     if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
+    if (stages(ax)) {
+        const unsigned last = min(first + kThreads / G, deal.count) - 1;
+        stage_angles(ax, s_angles, t0 + row0, (int)(deal.per_row.div(last) - row0) + 1);
+        __syncthreads();
+    }
     Turns<N, G, U> turns;
-    if (ok) turns.load(l, ax, s_codes, w, ax.flags);
+    if (ok && ax.rot > 0)
+        turns.load(l, stages(ax) ? s_angles + (row - row0) * (ax.rot >> 1)
+                                 : ax.table + (long long)w.p[0] * ax.table_pairs, ax.flags);
     Held<N, U> wt, bias;
     if (nv.kind != WQ_HEAD_NONE) {
         l.load_or(wt, nv.weight, 1.f);
@@ -244,7 +241,7 @@ __global__ void __launch_bounds__(kThreads)
         if (i < n && ok) {
             if (nv.kind != WQ_HEAD_NONE) l.weigh(v[i], wt, bias);
             turns.apply(l, v[i], ax.flags);
-            l.store(v[i], o + i * head_dim);
+            l.store(v[i], o, i * head_dim);
         }
 }
 
@@ -254,16 +251,15 @@ struct Roles {
 };
 
 template <int DT, typename Q, int N, int G, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
     append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
                        AppendNormArgs a, KvView kv, HeadDeal deal, Roles roles, int t0) {
-    __shared__ uint16_t s_codes[128];
-    stage_codes(ax, s_codes);
+    extern __shared__ __align__(16) float2 s_angles[];
     pdl_enter();
     using T = typename KvType<DT>::T;
-    const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    const unsigned first = blockIdx.x * (unsigned)(kThreads / G), at = first + threadIdx.x / G;
     const bool live = at < deal.count;
-    const unsigned row_at = deal.per_row.div(live ? at : 0u);
+    const unsigned row0 = deal.per_row.div(first), row_at = live ? deal.per_row.div(at) : row0;
     int block = live ? (int)(at - row_at * deal.per_row.d) : 0;
     const int role = block < roles.q_blocks                     ? 0
                      : block < roles.q_blocks + roles.kv_blocks ? 1
@@ -283,15 +279,22 @@ __global__ void __launch_bounds__(kThreads)
     Held<N, U> v[kHeadsPer] = {};
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i)
-        if (i < n) l.load(v[i], x + i * d);
+        if (i < n) l.load(v[i], x, i * d);
     Where w;
     bool ok = w.load(ax, t);
     ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
     const long long row = ok ? kv.row(seq, 0, slot) : -1;
     ok = ok && row >= 0;
     if (live && !ok && slot >= 0 && l.lane == 0) record_status(ax.status, kStBadIndex);
+    if (stages(ax)) {
+        const unsigned last = min(first + kThreads / G, deal.count) - 1;
+        stage_angles(ax, s_angles, t0 + row0, (int)(deal.per_row.div(last) - row0) + 1);
+        __syncthreads();
+    }
     Turns<N, G, U> turns;
-    if (ok && role < 2) turns.load(l, ax, s_codes, w, ax.flags);
+    if (ok && role < 2 && ax.rot > 0)
+        turns.load(l, stages(ax) ? s_angles + (row_at - row0) * (ax.rot >> 1)
+                                 : ax.table + (long long)w.p[0] * ax.table_pairs, ax.flags);
     // The lanes of a warp may hold both roles: all of them run the sums that either norm has.
     const bool any = q_norm.kind != WQ_HEAD_NONE || k_norm.kind != WQ_HEAD_NONE;
     const bool layer = q_norm.kind == WQ_HEAD_LAYER || k_norm.kind == WQ_HEAD_LAYER;
@@ -309,22 +312,28 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = 0; i < kHeadsPer; ++i) l.weigh(v[i], wt, bias);
     }
+    if (!ok) return;
+    if (role == 0) {
+        Q *const o = static_cast<Q *>(a.q_out) + t * a.q_out_stride + (long long)h0 * d;
 #pragma unroll
-    for (int i = 0; i < kHeadsPer; ++i) {
-        if (i >= n || !ok) continue;
-        if (role < 2) turns.apply(l, v[i], ax.flags);
-        const int head = h0 + i;
-        if (role == 0) {
-            l.store(v[i], static_cast<Q *>(a.q_out) + t * a.q_out_stride + (long long)head * d);
-            continue;
+        for (int i = 0; i < kHeadsPer; ++i)
+            if (i < n) {
+                turns.apply(l, v[i], ax.flags);
+                l.store(v[i], o, i * d);
+            }
+        return;
+    }
+    char *o = (role == 1 ? kv.k : kv.v) + row + h0 * kv.head_stride;
+#pragma unroll
+    for (int i = 0; i < kHeadsPer; ++i, o += kv.head_stride)
+        if (i < n) {
+            if (role == 1) turns.apply(l, v[i], ax.flags);
+            l.store(v[i], reinterpret_cast<T *>(o));
         }
-        l.store(v[i],
-                reinterpret_cast<T *>((role == 1 ? kv.k : kv.v) + row + head * kv.head_stride));
-        if (role == 1 && l.lane == 0) {
-            const long long to = ((long long)seq * kv.n_heads + head) * a.acc_stride + slot;
-            if (a.acc) a.acc[to] = 0.f;
-            if (a.slot_pos) a.slot_pos[to] = w.p[0];
-        }
+    if (role == 1 && l.lane < n && (a.acc || a.slot_pos)) {
+        const long long to = ((long long)seq * kv.n_heads + h0 + l.lane) * a.acc_stride + slot;
+        if (a.acc) a.acc[to] = 0.f;
+        if (a.slot_pos) a.slot_pos[to] = w.p[0];
     }
 }
 
@@ -336,14 +345,15 @@ __global__ void __launch_bounds__(kThreads)
                           int head_dim, const float *x, long long x_stride, const float *grad,
                           long long grad_stride, int n_heads, float *grad_x,
                           long long grad_x_stride, float *parts) {
-    extern __shared__ float s_sums[];  // [groups][2][head_dim]
-    __shared__ uint16_t s_codes[128];
-    stage_codes(ax, s_codes);
+    // [groups][2][head_dim] at the end, and before it a step's angles
+    extern __shared__ __align__(16) float s_sums[];
+    float2 *const s_angles = reinterpret_cast<float2 *>(s_sums);
     pdl_enter();
     const Lanes<N, G, U> l(ax, head_dim);
     const unsigned flags = ax.flags | WQ_ROPE_TRANSPOSE;
     const unsigned groups = gridDim.x * (unsigned)(kThreads / G);
-    const unsigned first = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / G;
+    const unsigned block0 = blockIdx.x * (unsigned)(kThreads / G), first = block0 + threadIdx.x / G;
+    unsigned row0 = 0;
     Held<N, U> wt, sum_w = {}, sum_b = {};
     l.load_or(wt, nv.kind != WQ_HEAD_NONE ? nv.weight : nullptr, 1.f);
     const unsigned steps = (deal.count + groups - 1) / groups;
@@ -355,17 +365,32 @@ __global__ void __launch_bounds__(kThreads)
         const int h0 = (int)(at - t * deal.per_row.d) * kGradHeads;
         const int n = live ? min(kGradHeads, n_heads - h0) : 0;
         Held<N, U> v[kGradHeads] = {}, g[kGradHeads] = {};
+        const float *const xi = x + t * x_stride + (long long)h0 * head_dim;
+        const float *const gi = grad + t * grad_stride + (long long)h0 * head_dim;
 #pragma unroll
         for (int i = 0; i < kGradHeads; ++i)
             if (i < n) {
-                l.load(v[i], x + t * x_stride + (long long)(h0 + i) * head_dim);
-                l.load(g[i], grad + t * grad_stride + (long long)(h0 + i) * head_dim);
+                l.load(v[i], xi, i * head_dim);
+                l.load(g[i], gi, i * head_dim);
             }
         Where w;
         const bool ok = w.load(ax, t);
         if (live && !ok && l.lane == 0) record_status(ax.status, kStBadIndex);
+        if (stages(ax)) {
+            const unsigned long long from = (unsigned long long)step * groups + block0;
+            __syncthreads();  // the step before has its angles
+            if (from < deal.count) {
+                const unsigned last = (unsigned)min(from + kThreads / G,
+                                                    (unsigned long long)deal.count) - 1;
+                row0 = deal.per_row.div((unsigned)from);
+                stage_angles(ax, s_angles, row0, (int)(deal.per_row.div(last) - row0) + 1);
+            }
+            __syncthreads();
+        }
         Turns<N, G, U> turns;
-        if (ok) turns.load(l, ax, s_codes, w, flags);
+        if (ok && ax.rot > 0)
+            turns.load(l, stages(ax) ? s_angles + (live ? t - row0 : 0u) * (ax.rot >> 1)
+                                     : ax.table + (long long)w.p[0] * ax.table_pairs, flags);
 #pragma unroll
         for (int i = 0; i < kGradHeads; ++i)
             if (i < n && ok) turns.apply(l, g[i], flags);
@@ -414,12 +439,13 @@ __global__ void __launch_bounds__(kThreads)
                     }
             }
         }
+        float *const o = grad_x + t * grad_x_stride + (long long)h0 * head_dim;
 #pragma unroll
         for (int i = 0; i < kGradHeads; ++i)
-            if (i < n && ok)
-                l.store(g[i], grad_x + t * grad_x_stride + (long long)(h0 + i) * head_dim);
+            if (i < n && ok) l.store(g[i], o, i * head_dim);
     }
     if (!parts) return;
+    __syncthreads();
     float *mine = s_sums + (threadIdx.x / G) * 2 * head_dim;
     l.store(sum_w, mine);
     l.store(sum_b, mine + head_dim);
@@ -463,6 +489,12 @@ bool all16(std::initializer_list<const void *> ps, std::initializer_list<long lo
     return true;
 }
 
+// Shared memory of the angles of the rows that `groups` groups of lanes span at most.
+size_t angle_bytes(const AxesView &ax, const HeadDeal &deal, unsigned groups) {
+    if (ax.rot == 0 || ax.straight) return 0;
+    const unsigned per = deal.per_row.d, rows = per == 1 ? groups : (groups + per - 2) / per + 1;
+    return (size_t)rows * (ax.rot / 2) * sizeof(float2);  // at most 32 rows of 64, 16 KiB
+}
 HeadDeal deal_of(int blocks) { return {make_fast_div((uint32_t)blocks), 0u}; }
 int blocks_of(int heads, int per) { return (heads + per - 1) / per; }
 
@@ -508,9 +540,9 @@ cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int 
             return by_shape(wide, head_dim, [&](auto N, auto G, auto U) {
                 const unsigned per = kThreads / G.value;
                 return launch_pdl(norm_rope_kernel<T, N.value, G.value, U.value>,
-                                  dim3((deal.count + per - 1) / per), dim3(kThreads), 0, stream, ax,
-                                  nv, deal, head_dim, x, x_stride, n_heads, static_cast<T *>(out),
-                                  out_stride, t0);
+                                  dim3((deal.count + per - 1) / per), dim3(kThreads),
+                                  angle_bytes(ax, deal, per), stream, ax, nv, deal, head_dim, x,
+                                  x_stride, n_heads, static_cast<T *>(out), out_stride, t0);
             });
         });
         if (err != cudaSuccess) return err;
@@ -539,8 +571,9 @@ cudaError_t launch_append_norm(const AxesView &ax, const NormView &q_norm, const
                     const unsigned per = kThreads / G.value;
                     return launch_pdl(
                         append_norm_kernel<DT.value, Q, N.value, G.value, U.value>,
-                        dim3((deal.count + per - 1) / per), dim3(kThreads), 0, stream, ax, q_norm,
-                        k_norm, a, kv, deal, roles, (int)t0);
+                        dim3((deal.count + per - 1) / per), dim3(kThreads),
+                        angle_bytes(ax, deal, per), stream, ax, q_norm, k_norm, a, kv, deal, roles,
+                        (int)t0);
                 });
             });
         };
@@ -570,7 +603,8 @@ cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n,
         constexpr int per = kThreads / G.value;
         blocks = (deal.count + per - 1) / per;
         if (blocks > (unsigned)kGradBlocks) blocks = kGradBlocks;
-        const size_t smem = sums ? (size_t)per * 2 * head_dim * 4 : 0;  // at most 16 KiB
+        size_t smem = sums ? (size_t)per * 2 * head_dim * 4 : 0;  // at most 16 KiB
+        if (angle_bytes(ax, deal, per) > smem) smem = angle_bytes(ax, deal, per);
         return launch_pdl(norm_rope_grad_kernel<N.value, G.value, U.value>, dim3(blocks),
                           dim3(kThreads), smem, stream, ax, nv, deal, head_dim, x, x_stride, grad,
                           grad_stride, n_heads, grad_x, grad_x_stride, parts);
