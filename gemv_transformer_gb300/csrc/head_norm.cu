@@ -249,12 +249,19 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
 struct Roles {
     int q_blocks, kv_blocks;
 };
+// What a row's groups of lanes share, found by one thread: the row's offset in the pools (-1:
+// nothing is written) and its position on axis 0.
+struct Place1 {
+    long long row;
+    int pos, pad;
+};
 
 template <int DT, typename Q, int N, int G, int U>
 __global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
     append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
                        AppendNormArgs a, KvView kv, HeadDeal deal, Roles roles, int t0) {
     extern __shared__ __align__(16) float2 s_angles[];
+    __shared__ Place1 s_place[kThreads / G];
     pdl_enter();
     using T = typename KvType<DT>::T;
     const unsigned first = blockIdx.x * (unsigned)(kThreads / G), at = first + threadIdx.x / G;
@@ -268,8 +275,6 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
     const int d = kv.head_dim, heads = role == 0 ? a.h_q : kv.n_heads;
     const int h0 = block * kHeadsPer, n = live ? min(kHeadsPer, heads - h0) : 0;
     const int t = t0 + (int)row_at;
-    const int slot = a.slot[t];
-    const int seq = a.seq ? a.seq[t] : t;
     const Lanes<N, G, U> l(ax, d);
     const float *const x = (role == 0   ? a.q + t * a.q_stride
                             : role == 1 ? a.k + t * a.k_stride
@@ -280,21 +285,29 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
 #pragma unroll
     for (int i = 0; i < kHeadsPer; ++i)
         if (i < n) l.load(v[i], x, i * d);
-    Where w;
-    bool ok = w.load(ax, t);
-    ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
-    const long long row = ok ? kv.row(seq, 0, slot) : -1;
-    ok = ok && row >= 0;
-    if (live && !ok && slot >= 0 && l.lane == 0) record_status(ax.status, kStBadIndex);
-    if (stages(ax)) {
-        const unsigned last = min(first + kThreads / G, deal.count) - 1;
-        stage_angles(ax, s_angles, t0 + row0, (int)(deal.per_row.div(last) - row0) + 1);
+    {
+        const int rows =
+            (int)(deal.per_row.div(min(first + kThreads / G, deal.count) - 1) - row0) + 1;
+        if ((int)threadIdx.x < rows) {
+            const int tt = t0 + (int)row0 + threadIdx.x;
+            const int slot = a.slot[tt], seq = a.seq ? a.seq[tt] : tt;
+            Where w;
+            bool ok = w.load(ax, tt);
+            ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
+            const long long at_row = ok ? kv.row(seq, 0, slot) : -1;
+            if (at_row < 0 && slot >= 0) record_status(ax.status, kStBadIndex);
+            s_place[threadIdx.x] = {at_row, w.p[0], 0};
+        }
+        if (stages(ax)) stage_angles(ax, s_angles, t0 + row0, rows);
         __syncthreads();
     }
+    const Place1 place = s_place[row_at - row0];
+    const long long row = place.row;
+    const bool ok = row >= 0;
     Turns<N, G, U> turns;
     if (ok && role < 2 && ax.rot > 0)
         turns.load(l, stages(ax) ? s_angles + (row_at - row0) * (ax.rot >> 1)
-                                 : ax.table + (long long)w.p[0] * ax.table_pairs, ax.flags);
+                                 : ax.table + (long long)place.pos * ax.table_pairs, ax.flags);
     // The lanes of a warp may hold both roles: all of them run the sums that either norm has.
     const bool any = q_norm.kind != WQ_HEAD_NONE || k_norm.kind != WQ_HEAD_NONE;
     const bool layer = q_norm.kind == WQ_HEAD_LAYER || k_norm.kind == WQ_HEAD_LAYER;
@@ -331,9 +344,10 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
             l.store(v[i], reinterpret_cast<T *>(o));
         }
     if (role == 1 && l.lane < n && (a.acc || a.slot_pos)) {
+        const int slot = a.slot[t], seq = a.seq ? a.seq[t] : t;
         const long long to = ((long long)seq * kv.n_heads + h0 + l.lane) * a.acc_stride + slot;
         if (a.acc) a.acc[to] = 0.f;
-        if (a.slot_pos) a.slot_pos[to] = w.p[0];
+        if (a.slot_pos) a.slot_pos[to] = place.pos;
     }
 }
 
