@@ -7,8 +7,9 @@
 // attn_rows_kernel takes f32 caches, f32 queries over f16 caches and heads above 128 dims: k and v
 // are widened to f32 in shared memory and every product is an f32 FMA, so it is exact to f32 and
 // bound by the FMA pipe (4 head_dim operations per row and slot) from about 16 rows of a group on.
-// A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the output;
-// the 16 lanes of a row join its maximum and sum by shuffles.
+// A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the output,
+// two neighbouring dims to an instruction; the 16 lanes of a row join its maximum and sum by
+// shuffles.
 #include "attn_tokens.cuh"
 
 namespace wq {
@@ -229,6 +230,22 @@ template <typename T> __device__ __forceinline__ void load8(const void *p, float
     }
 }
 
+// Two f32 operations of one instruction, pairs of neighbouring dims.
+using Pair = unsigned long long;
+__device__ __forceinline__ void fma2(Pair &d, Pair a, Pair b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 floats_of(Pair x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
 template <int DP, int R> struct RowsShape {
     static constexpr int KT = DP > 128 ? 32 : 64;
     static constexpr int RT = 16 * R;
@@ -241,7 +258,7 @@ template <typename T, int DP, int R>
 __global__ void __launch_bounds__(256)
     attn_rows_kernel(TokensArgs a, KvView kv, int grid) {
     using S = RowsShape<DP, R>;
-    constexpr int KT = S::KT, RT = S::RT, NK = KT / 16, ND = DP / 16;
+    constexpr int KT = S::KT, RT = S::RT, NK = KT / 16, ND = DP / 32;
     extern __shared__ __align__(16) float s_rows[];
     __shared__ int s_join[3];
     float *s_q = s_rows, *s_k = s_q + S::kQ, *s_v = s_k + S::kK, *s_p = s_v + S::kV;
@@ -283,12 +300,13 @@ __global__ void __launch_bounds__(256)
             see[i] = see_of(a, q, tile.seq, j);
             slope[i] = a.slopes ? a.slopes[st.head * group + rr - j * group] : 0.f;
         }
-        float m[R], l[R], o[R][ND];
+        float m[R], l[R];
+        Pair o[R][ND];  // dims 32 e + 2 tx of the thread's rows
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < ND; ++e) o[i][e] = 0.f;
+            for (int e = 0; e < ND; ++e) o[i][e] = 0ull;
         }
         for (int kt = st.k0; kt < st.k1; ++kt) {
             const int j0 = kt * KT;
@@ -316,30 +334,37 @@ __global__ void __launch_bounds__(256)
             }
             const int none = __syncthreads_or(lost & 1u), odd = __syncthreads_or(lost & 2u);
             if (none && threadIdx.x == 0) record_status(a.status, kStBadIndex);
-            float x[R][NK];
+            Pair x2[R][NK];
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int n = 0; n < NK; ++n) x[i][n] = 0.f;
+                for (int n = 0; n < NK; ++n) x2[i][n] = 0ull;
 #pragma unroll 4
             for (int c = 0; c < DP; c += 4) {
-                float4 qa[R], ka[NK];
+                ulonglong2 qa[R], ka[NK];
 #pragma unroll
                 for (int i = 0; i < R; ++i)
-                    qa[i] = *reinterpret_cast<const float4 *>(s_q + (ty * R + i) * S::kPitch + c);
+                    qa[i] = *reinterpret_cast<const ulonglong2 *>(s_q + (ty * R + i) * S::kPitch + c);
 #pragma unroll
                 for (int n = 0; n < NK; ++n)
-                    ka[n] = *reinterpret_cast<const float4 *>(s_k + (tx + 16 * n) * S::kPitch + c);
+                    ka[n] =
+                        *reinterpret_cast<const ulonglong2 *>(s_k + (tx + 16 * n) * S::kPitch + c);
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int n = 0; n < NK; ++n) {
-                        x[i][n] = fmaf(qa[i].x, ka[n].x, x[i][n]);
-                        x[i][n] = fmaf(qa[i].y, ka[n].y, x[i][n]);
-                        x[i][n] = fmaf(qa[i].z, ka[n].z, x[i][n]);
-                        x[i][n] = fmaf(qa[i].w, ka[n].w, x[i][n]);
+                        fma2(x2[i][n], qa[i].x, ka[n].x);
+                        fma2(x2[i][n], qa[i].y, ka[n].y);
                     }
             }
+            float x[R][NK];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const float2 s = floats_of(x2[i][n]);
+                    x[i][n] = s.x + s.y;
+                }
             const bool whole = j0 >= tile.lo && j0 + KT <= tile.hi && !none;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -380,8 +405,10 @@ __global__ void __launch_bounds__(256)
                 for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
                 l[i] = fmaf(l[i], f, sum);
                 m[i] = now;
+                const Pair f2 = pair_of(f, f);
 #pragma unroll
-                for (int e = 0; e < ND; ++e) o[i][e] *= f;
+                for (int e = 0; e < ND; ++e)
+                    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(o[i][e]) : "l"(f2));
             }
             __syncwarp();  // a row's 16 lanes are in one warp
             if (!odd) {
@@ -392,23 +419,24 @@ __global__ void __launch_bounds__(256)
                     for (int i = 0; i < R; ++i)
                         pa[i] = *reinterpret_cast<const float4 *>(s_p + (ty * R + i) * (KT + 4) + r);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
+                        Pair p[R];
 #pragma unroll
-                        for (int e = 0; e < ND; e += 4) {
-                            const float4 v = *reinterpret_cast<const float4 *>(
-                                s_v + (r + k) * DP + (e / 4) * 64 + tx * 4);
-#pragma unroll
-                            for (int i = 0; i < R; ++i) {
-                                const float p = k == 0   ? pa[i].x
-                                                : k == 1 ? pa[i].y
-                                                : k == 2 ? pa[i].z
-                                                         : pa[i].w;
-                                o[i][e] = fmaf(p, v.x, o[i][e]);
-                                o[i][e + 1] = fmaf(p, v.y, o[i][e + 1]);
-                                o[i][e + 2] = fmaf(p, v.z, o[i][e + 2]);
-                                o[i][e + 3] = fmaf(p, v.w, o[i][e + 3]);
-                            }
+                        for (int i = 0; i < R; ++i) {
+                            const float w = k == 0   ? pa[i].x
+                                            : k == 1 ? pa[i].y
+                                            : k == 2 ? pa[i].z
+                                                     : pa[i].w;
+                            p[i] = pair_of(w, w);
                         }
+#pragma unroll
+                        for (int e = 0; e < ND; ++e) {
+                            const Pair v =
+                                *reinterpret_cast<const Pair *>(s_v + (r + k) * DP + 32 * e + 2 * tx);
+#pragma unroll
+                            for (int i = 0; i < R; ++i) fma2(o[i][e], p[i], v);
+                        }
+                    }
                 }
             } else {
                 for (int r = 0; r < KT; ++r)
@@ -418,20 +446,25 @@ __global__ void __launch_bounds__(256)
                         if (p == -1.f) continue;
 #pragma unroll
                         for (int e = 0; e < ND; ++e)
-                            o[i][e] = fmaf(p, s_v[r * DP + (e / 4) * 64 + tx * 4 + (e & 3)], o[i][e]);
+                            fma2(o[i][e], pair_of(p, p),
+                                 *reinterpret_cast<const Pair *>(s_v + r * DP + 32 * e + 2 * tx));
                     }
             }
         }
-        // Dims (e / 4) * 64 + tx * 4 + e % 4 of the thread's rows.
+        // Parts lie as [dims / 4][row][4].
+        auto part_at = [&](size_t part, int r, int e) {
+            const int c = 32 * e + 2 * tx;
+            return reinterpret_cast<float *>(room.part_o) +
+                   ((part * (DP / 4) + c / 4) * RT + r) * 4 + (c & 3);
+        };
         if (st.part >= 0) {
             const size_t part = 2 * blockIdx.x + st.part;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int r = ty * R + i;
 #pragma unroll
-                for (int e = 0; e < ND; e += 4)
-                    room.part_o[(part * (DP / 4) + (e / 4) * 16 + tx) * RT + r] =
-                        make_float4(o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]);
+                for (int e = 0; e < ND; ++e)
+                    *reinterpret_cast<float2 *>(part_at(part, r, e)) = floats_of(o[i][e]);
                 if (tx == 0) room.part_ml[part * RT + r] = make_float2(m[i], l[i]);
             }
             if (!a.join_inside) continue;
@@ -449,9 +482,10 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int r = ty * R + i;
+                float2 sum[ND];
                 m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-                for (int e = 0; e < ND; ++e) o[i][e] = 0.f;
+                for (int e = 0; e < ND; ++e) sum[e] = make_float2(0.f, 0.f);
                 for (int k = 0; k < parts; ++k) {
                     const size_t from = part_place(lead, k);
                     const float2 ml = __ldcg(room.part_ml + from * RT + r);
@@ -460,15 +494,15 @@ __global__ void __launch_bounds__(256)
                     m[i] = now;
                     l[i] = fmaf(l[i], f, ml.y * g);
 #pragma unroll
-                    for (int e = 0; e < ND; e += 4) {
-                        const float4 v =
-                            __ldcg(room.part_o + (from * (DP / 4) + (e / 4) * 16 + tx) * RT + r);
-                        o[i][e] = fmaf(o[i][e], f, v.x * g);
-                        o[i][e + 1] = fmaf(o[i][e + 1], f, v.y * g);
-                        o[i][e + 2] = fmaf(o[i][e + 2], f, v.z * g);
-                        o[i][e + 3] = fmaf(o[i][e + 3], f, v.w * g);
+                    for (int e = 0; e < ND; ++e) {
+                        const float2 v =
+                            __ldcg(reinterpret_cast<const float2 *>(part_at(from, r, e)));
+                        sum[e].x = fmaf(sum[e].x, f, v.x * g);
+                        sum[e].y = fmaf(sum[e].y, f, v.y * g);
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < ND; ++e) o[i][e] = pair_of(sum[e].x, sum[e].y);
             }
         }
 #pragma unroll
@@ -479,12 +513,12 @@ __global__ void __launch_bounds__(256)
             const int t = q.t0 + j, h = st.head * group + g;
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
-            for (int e = 0; e < ND; e += 4) {
-                const int c = (e / 4) * 64 + tx * 4;
+            for (int e = 0; e < ND; ++e) {
+                const int c = 32 * e + 2 * tx;
+                const float2 v = floats_of(o[i][e]);
                 if (c < d)
-                    out.put4(t * a.out_stride + (long long)h * d + c,
-                             make_float4(o[i][e] * inv, o[i][e + 1] * inv, o[i][e + 2] * inv,
-                                         o[i][e + 3] * inv));
+                    out.put2(t * a.out_stride + (long long)h * d + c,
+                             make_float2(v.x * inv, v.y * inv));
             }
             if (a.lse && tx == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m[i], l[i]);
         }
@@ -495,7 +529,9 @@ __global__ void __launch_bounds__(256)
 int rows_per_thread(int n_seq, int n_tok, int group) {
     return (long long)n_tok * group <= 24ll * n_seq ? 1 : 4;
 }
-int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+int padded_dim(int head_dim) {
+    return head_dim <= 64 ? 64 : head_dim <= 96 ? 96 : head_dim <= 128 ? 128 : 256;
+}
 
 template <typename T, int DP, int R>
 cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -521,6 +557,8 @@ cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const Device
     switch (padded_dim(kv.head_dim)) {
     case 64: return one ? launch_rows<T, 64, 1>(a, kv, dev, stream)
                         : launch_rows<T, 64, 4>(a, kv, dev, stream);
+    case 96: return one ? launch_rows<T, 96, 1>(a, kv, dev, stream)
+                        : launch_rows<T, 96, 4>(a, kv, dev, stream);
     case 128: return one ? launch_rows<T, 128, 1>(a, kv, dev, stream)
                          : launch_rows<T, 128, 4>(a, kv, dev, stream);
     default: return one ? launch_rows<T, 256, 1>(a, kv, dev, stream)

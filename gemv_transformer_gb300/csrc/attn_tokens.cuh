@@ -199,6 +199,15 @@ struct Walk {
 struct TypedOut {
     void *p;
     int type;
+    __device__ __forceinline__ void put2(long long at, float2 v) const {
+        if (type == kF32) {
+            reinterpret_cast<float2 *>(p)[at >> 1] = v;
+        } else if (type == kBF16) {
+            reinterpret_cast<__nv_bfloat162 *>(p)[at >> 1] = __floats2bfloat162_rn(v.x, v.y);
+        } else {
+            reinterpret_cast<__half2 *>(p)[at >> 1] = __floats2half2_rn(v.x, v.y);
+        }
+    }
     __device__ __forceinline__ void put4(long long at, float4 v) const {
         if (type == kF32) {
             reinterpret_cast<float4 *>(p)[at >> 2] = v;

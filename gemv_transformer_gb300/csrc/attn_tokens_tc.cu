@@ -1114,12 +1114,22 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
             const bool mixed =
                 j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
-            if (w.formed() || mixed) {
+            if (w.formed()) {
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) wait_ld(s[ch]);
                 w.form(j0, mixed, sh->none[vs]);
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
+            } else if (mixed) {
+                const See see = w.see();
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    wait_ld(s[ch]);
+                    const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~sh->none[vs][ch];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(in >> e & 1u)) s[ch][e] = 0xFF800000u;
+                }
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1166,6 +1176,12 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                 }
                 ld32(s[0], w.tm + kColS);
                 wait_ld(s[0]);
+                if (mixed && !w.formed()) {
+                    const uint32_t in = seen32(a, w.see(), j0) & ~sh->none[vs][0];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(in >> e & 1u)) s[0][e] = 0xFF800000u;
+                }
                 sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
                 weigh(0);
             }

@@ -23,7 +23,7 @@ namespace wq {
 namespace {
 
 constexpr int kHeadsPer = 4;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kGradHeads = 2;
 
 // A lane's units of a head.
@@ -195,7 +195,7 @@ struct HeadDeal {
 };
 
 template <typename T, int N, int G, int U>
-__global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, N == 4 ? 6 : 1)
     norm_rope_kernel(const __grid_constant__ AxesView ax, NormView nv, HeadDeal deal, int head_dim,
                      const float *x, long long x_stride, int n_heads, T *out, long long out_stride,
                      long long t0) {
@@ -257,7 +257,7 @@ struct Place1 {
 };
 
 template <int DT, typename Q, int N, int G, int U>
-__global__ void __launch_bounds__(kThreads, N == 4 ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, N == 4 ? 8 : 1)
     append_norm_kernel(const __grid_constant__ AxesView ax, NormView q_norm, NormView k_norm,
                        AppendNormArgs a, KvView kv, HeadDeal deal, Roles roles, int t0) {
     extern __shared__ __align__(16) float2 s_angles[];
