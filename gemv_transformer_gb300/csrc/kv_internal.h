@@ -90,7 +90,7 @@ struct AppendNormArgs {
     long long acc_stride;
 };
 
-constexpr int kGradBlocks = 912;  // six on each of 152 SMs
+constexpr int kGradBlocks = 608;  // four on each of 152 SMs: all at once
 
 struct TokensArgs {
     int n_seq, n_tok, h_q, n_slots;  // n_slots: max_pages * page_size
