@@ -18,10 +18,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 2048;
-#ifndef WQ_LEAST
-#define WQ_LEAST 3
-#endif
-constexpr int kLeastCost = WQ_LEAST;  // a CTA's range is no shorter
+// A CTA's range is no shorter, or the parts' sums cost more than they save: 1, 2, 3, 4 and 6 took
+// 31, 31, 25, 24 and 29 us for 4 sequences of 16 nodes behind 1000 slots.
+constexpr int kLeastCost = 3;
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
@@ -55,7 +54,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int group = a.group.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
     if (threadIdx.x < 2 * grid) room.joined[threadIdx.x] = 0u;
-    // Row tiles of the sequences, kPlanThreads sequences at a time.
+    // Row tiles of the sequences, kPlanThreads sequences at a time.  Ranges of `starts` that overlap
+    // may ask for more than there is room for: the rest is left out.
+    const long long most = most_tiles(a.n_seq, a.n_tok, group, rt);
     int n_tiles = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
         int mine = 0;
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         long long all;
         const long long upto = block_scan(mine, s_warp, all);
-        s_first[threadIdx.x + 1] = n_tiles + (int)upto;
+        if (mine > 0 && n_tiles + upto > most) record_status(a.status, kStBadIndex);
+        s_first[threadIdx.x + 1] = (int)min(n_tiles + upto, most);
         if (threadIdx.x == 0) s_first[0] = n_tiles;
         __syncthreads();
         // A warp lists a sequence's tiles, all warps those of few sequences.
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 if (first + r < kPlanTiles) s_keys[first + r] = t.k1 - t.k0;
             }
         }
-        n_tiles += (int)all;
+        n_tiles = (int)min(n_tiles + all, most);
         __syncthreads();
     }
     auto keys = [&](int i) {

@@ -230,7 +230,7 @@ struct TypedOut {
 
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return m == -INFINITY ? -INFINITY : fmaf(m, kLn2, logf(l));
+    return l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));  // (scores that are not numbers: NaN)
 }
 
 // row_cost: a row tile's start and end count as so many key tiles.

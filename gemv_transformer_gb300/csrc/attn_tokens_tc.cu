@@ -44,7 +44,7 @@ constexpr int kThreads = kSoft + 128;  // an MMA warp, two for k and v, one for 
 constexpr int kLoaders = 64;      // of pages that are no boxes
 constexpr int kMostV = 6;
 constexpr int kSmemMost = 227 * 1024;
-constexpr int kMisc = 3072;      // barriers and small arrays, before the 1024-byte aligned part
+constexpr int kMisc = 3 * 1024;    // barriers and small arrays, before the 1024-byte aligned part
 
 // Tensor memory columns of a warpgroup (256 each).
 constexpr uint32_t kColS = 0, kColP0 = 0, kColP1 = 64, kColP2 = 96, kColT = 128;
@@ -73,6 +73,7 @@ struct Shared {
     uint32_t odd[2][4][4];          // slots whose v is not finite
     float2 ml[2][128];              // maxima and sums of the warpgroups' rows
     int last[2][3];                 // part_last(), its first CTA and number of parts
+    uint32_t issued[2];             // steps of the loaders of k and of v
     uint32_t tmem, abort;
 };
 static_assert(sizeof(Shared) <= kMisc && offsetof(Shared, none) % 16 == 0, "read as 16 bytes");
@@ -186,7 +187,9 @@ template <int ET> __device__ __forceinline__ bool odd16x2(uint32_t w) {
     constexpr uint32_t e = ET == kBF16 ? 0x7F80u : 0x7C00u;
     return (w & e) == e || (w & (e << 16)) == (e << 16);
 }
-// The fast tanh of 16-bit queries: within 2^-22 of 1 for any x; inf and NaN come out right.
+// The fast tanh of 16-bit queries: within 2^-22 of 1 for any x, which a cap of kFastCap makes 2^-14 of
+// a weight, far below its rounding; inf and NaN come out right.
+constexpr float kFastCap = 256.f;
 __device__ __forceinline__ float fast_tanh(float x) {
     return 1.f - __fdividef(2.f, ex2(x * (2.f * kLog2e)) + 1.f);
 }
@@ -320,7 +323,6 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
         cur = ask();
     }
     uint32_t g = 0;
-    bool ok = true;
     for (; here; ++g) {
         Box x = cur;
         const bool some = in.more;  // of x
@@ -329,10 +331,7 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
             cur = ask();
         }
         const uint32_t slot = g % S::NV;
-        if (g >= (uint32_t)S::NV && !c.warp_wait(&c.sh->done[slot], (g / S::NV & 1) ^ 1)) {
-            ok = false;
-            break;
-        }
+        if (g >= (uint32_t)S::NV && !c.warp_wait(&c.sh->done[slot], (g / S::NV & 1) ^ 1)) break;
         settle(x);
         if (lane == 0) {
             if (is_v) {
@@ -353,12 +352,15 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
              &c.sh->full[slot]);
         here = ahead ? some : in.more;
     }
-    // The last copies have landed before shared memory is given up.  After an abort the other warp
-    // may have asked for steps that this one has not: it waits for both.
-    if (!ok && lane == 0)
-        for (uint32_t i = g; i < g + S::NV; ++i) mbar_arrive(&c.sh->full[i % S::NV]);
+    // The last copies have landed before shared memory is given up.  After an abort one warp may have
+    // asked for steps that the other has not: it arrives for those, and both wait for all.
+    if (lane == 0) c.sh->issued[is_v] = g;
+    asm volatile("bar.sync 1, 64;" ::: "memory");  // the loaders: each gets here, its waits are bounded
+    const uint32_t end = max(c.sh->issued[0], c.sh->issued[1]);
+    if (lane == 0)
+        for (uint32_t i = g; i < end; ++i) mbar_arrive(&c.sh->full[i % S::NV]);
     if (ahead && g > 0) mbar_wait(&c.sh->first, 0, kDrainPolls);
-    for (uint32_t i = g < (uint32_t)S::NV ? 0 : g - S::NV; i < g; ++i)
+    for (uint32_t i = end < (uint32_t)S::NV ? 0 : end - S::NV; i < end; ++i)
         mbar_wait(&c.sh->full[i % S::NV], i / S::NV & 1, kDrainPolls);
 }
 
@@ -768,10 +770,14 @@ template <typename S> struct Row {
             if (formed()) {
                 if (a.softcap > 0.f) {
                     const float in = a.scale / a.softcap, out = a.softcap * kLog2e;
+                    if (S::TERMS == 1 && a.softcap <= kFastCap) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float z = __uint_as_float(v[e]) * in;
-                        v[e] = __float_as_uint(out * (S::TERMS == 1 ? fast_tanh(z) : fine_tanh(z)));
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(out * fast_tanh(__uint_as_float(v[e]) * in));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(out * fine_tanh(__uint_as_float(v[e]) * in));
                     }
                 } else {
 #pragma unroll
@@ -867,6 +873,13 @@ template <typename S> struct Row {
                 f(32 * ch + b, (in >> b & 1u) != 0, ex2(fmaf(x, to_log2, -safe)));
             }
         }
+    }
+    __device__ __forceinline__ bool sees_odd(const Odd &o, int j0, const uint32_t *none) {
+        uint32_t some = 0;
+#pragma unroll 1
+        for (int ch = 0; ch < kChunks; ++ch)
+            some |= seen32(a, see(), j0 + 32 * ch) & ~none[ch] & word(o, ch);
+        return some != 0;
     }
     // Eight dims of a slot's v.
     __device__ __forceinline__ static void v8(uint32_t v_at, int slot, int chunk, float (&x)[8]) {
@@ -1092,7 +1105,9 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
         w.tile = room.tiles + st.tile;
         w.head = st.head;
         const int n = st.k1 - st.k0;
-        float m = -INFINITY, l = 0.f;  // the row's maximum in use, its sum
+        int j, h;
+        // The row's maximum in use and its sum; rows beyond the tile's have weights of 0.
+        float m = w.place(j, h) ? -INFINITY : INFINITY, l = 0.f;
         bool some = false;
         if (n > 0) {
             uint32_t zero[32] = {};
@@ -1158,8 +1173,12 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             const float now =
                 fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * w.to_log2);
             if (__any_sync(0xFFFFFFFFu, now > m + kGrow || m == -INFINITY)) {
-                const float f = ex2(m - (now == -INFINITY ? 0.f : now));
-                m = now;
+                // Each row by itself, so that its bits do not depend on its neighbours.
+                float f = 1.f;
+                if (now > m + kGrow || m == -INFINITY) {
+                    f = ex2(m - (now == -INFINITY ? 0.f : now));
+                    m = now;
+                }
                 safe = m == -INFINITY ? 0.f : m;
                 l *= f;
                 if (some) {  // the last P V came before these scores
@@ -1232,7 +1251,6 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             ++ended;
             if (S::PAIR && threadIdx.x == kTeam) mbar_arrive(&sh->done[(base - 1) % S::NV]);
         }
-        int j, h;
         const bool live = w.place(j, h);
         if (S::PAIR) {
 #pragma unroll 1
@@ -1330,9 +1348,12 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
                 typename Row<S>::Odd odd;
                 if (!w.look(v_at, odd)) return;
                 if (odd.any) {
+                    // Only for rows that see one: what else the tile's place holds changes no bit.
+                    if (w.sees_odd(odd, j0, sh->none[vs])) {
 #pragma unroll
-                    for (int e = 0; e < DP; ++e) o[e] *= f;
-                    f = 1.f;
+                        for (int e = 0; e < DP; ++e) o[e] *= f;
+                        f = 1.f;
+                    }
                     w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool in, float p) {
 #pragma unroll
                         for (int e = 0; e < DP; e += 8) {
@@ -1483,6 +1504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&c.sh->drain, 0, kDrainPolls);
         }
         __syncwarp();
+    }
+    if (warp < kMma) {  // a warp that gave up may have left a load or store of tensor memory under way
+        wait_st();
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();

@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxHeadDim = 256;
 constexpr long long kMaxSlots = 1ll << 30;  // a slot number and a tile beyond it fit an int
+constexpr int64_t kMaxStride = INT64_MAX / 64 / 0x7FFFFFFF;  // offsets of any row fit 64 bits
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 wq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA; }
@@ -57,7 +58,7 @@ bool rope_ok(int head_dim, int rot, unsigned flags, const int32_t *pos, const fl
 // Rows of n_heads heads at x + t * stride.
 bool rows_ok(const float *x, int64_t stride, int n_heads, int head_dim) {
     return x && aligned(x, 4) && stride >= (int64_t)n_heads * head_dim &&
-           stride <= INT64_MAX / 64 / 0x7FFFFFFF;
+           stride <= kMaxStride;
 }
 
 bool workspace_ok(const void *workspace, size_t bytes, size_t need) {
@@ -133,7 +134,7 @@ bool axes_ok(const wq_rope_axes *r, int head_dim, AxesView &out) {
 // Rows of n_heads heads of a 16- or 32-bit type at x + t * stride.
 bool typed_rows_ok(const void *x, int type, int64_t stride, int n_heads, int head_dim) {
     return x && aligned(x, element_bytes(type)) && stride >= (int64_t)n_heads * head_dim &&
-           stride <= INT64_MAX / 64 / 0x7FFFFFFF;
+           stride <= kMaxStride;
 }
 
 int cut(int n, long long to) { return to < n ? (int)to : n; }
@@ -466,7 +467,8 @@ wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q
     wq_attn_form f{};
     if (form) f = *form;
     if (!std::isfinite(f.softcap) || f.softcap < 0.f || f.window < 0) return WQ_ERR_INVALID_ARG;
-    if ((f.tree && (f.prefix || f.tree_stride < 1)) || (f.pos && !f.tree))
+    if ((f.tree && (f.prefix || f.tree_stride < 1 || f.tree_stride > kMaxStride)) ||
+        (f.pos && !f.tree))
         return WQ_ERR_INVALID_ARG;
     if (!workspace_ok(workspace, workspace_bytes,
                       tokens_workspace_bytes(kv, n_seq, n_tok, h_q, q_type)))

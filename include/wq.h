@@ -645,20 +645,22 @@ typedef struct {
  * reach its results, whatever it holds.
  * q: q_type (WQ_F32, WQ_BF16, WQ_F16), rows of h_q heads; out: out_type, q_type or WQ_F32;
  * strides in elements.  lse: f32 [n_tok][h_q] or NULL.
- * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products); 16-bit
+ * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products).  16-bit
  * queries over a cache of their type with head_dim <= 128: tensor-core products, in which p is
- * rounded to that type (2^-9 of it for bf16, 2^-12 for f16; p is at most 2^0 and f16 weights
- * below 2^-24 are lost); all others as f32 queries.
+ * rounded to that type (by half a step: 2^-8 of it for bf16, 2^-11 for f16, whose weights below
+ * 2^-24 of the largest are lost), and a sum over n slots may be cut short by n / 16 times 2^-23
+ * of it.  All others as f32 queries.
  * Rows of q at or beyond starts[n_seq] reach no result, and theirs of out are not written.
+ * Nothing overlaps out, lse or the workspace.
  * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not
- * like that is left out, a length below T or above max_pages * page_size is cut to the slots
+ * like that is left out (and of ranges that overlap, what n_tok rows do not hold), a length below T or above max_pages * page_size is cut to the slots
  * that there are, and a page out of range that holds live slots leaves them out; each records
  * WQ_ERR_BAD_INDEX in the device status.
  * form (read on the host, not kept) NULL: causal, no cap.
  * workspace: as wq_attn_paged's, of wq_attn_tokens_workspace_bytes(...) bytes.
  * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, n_tok, h_q, max_pages <= 0, h_q
  * not a multiple of the kv heads, a scale that is not finite, a softcap below 0 or not finite,
- * window < 0, tree with prefix, tree_stride < 1, pos without tree, unknown types, null q, starts,
+ * window < 0, tree with prefix, tree_stride < 1 or above 2^26, pos without tree, unknown types, null q, starts,
  * page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
  * or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
  * missing, misaligned or small workspace. */
@@ -683,8 +685,8 @@ WQ_API size_t wq_attn_tokens_workspace_bytes(const wq_kv_cache *cache, int n_seq
  *   path[starts[s] + i] = the path's i-th node, -1 beyond it (int32 [n_tok])
  *   accepted[s] = the path's nodes (at least 1), next[s] = choice of its last node
  *   lens_out[s] = B + accepted[s]
- * and in each of n_caches caches (a model's layers, alike but for k and v; the array is read
- * on the host) the k and v of the path's i-th node move from slot B + path[i] to B + i.  The
+ * and in each of n_caches caches (a model's layers, alike but for k and v, each listed once; the
+ * array is read on the host) the k and v of the path's i-th node move from slot B + path[i] to B + i.  The
  * slots behind them keep what they hold.
  * A sequence without new tokens: accepted 0, next -1, lens_out = lens.  One whose starts or
  * length are not as in wq_attn_tokens is treated like that, its path is left unwritten, and

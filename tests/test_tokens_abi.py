@@ -112,7 +112,7 @@ def form(**kw):
     dict(out=None), dict(out=A + 8), dict(os=255), dict(os=260), dict(wide=0), dict(wide=1 << 27),
     dict(n=1 << 28, hq=8, qs=512, os=512), dict(room=None), dict(room=A + 16), dict(size=1000),
     dict(form=form(softcap=-1.0)), dict(form=form(softcap=NAN)), dict(form=form(window=-1)),
-    dict(form=form(tree=A)), dict(form=form(tree=A, tree_stride=1, prefix=A)),
+    dict(form=form(tree=A)), dict(form=form(tree=A, tree_stride=1 << 40)), dict(form=form(tree=A, tree_stride=1, prefix=A)),
     dict(form=form(pos=A))] + [dict(c=cache(**c)) for c in CACHES])
 def test_attn_refusals(kw):
     assert attn(**kw) == BAD
