@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 constexpr int kAtOnce = 8;
 __global__ void __launch_bounds__(256)
     attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
-    pdl_enter();
+    // What follows is let in when this is over: a next call's blocks, let in early, would take the
+    // places of this one's (41 us instead of 24 for 4 sequences of 16 nodes, one call after another).
+    pdl_wait();
     const int group = a.group.d;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, rt, dp, grid);
     const Begin p = room.plan[blockIdx.x + 1];

@@ -70,7 +70,7 @@ struct Shared {
     uint64_t first, full[kMostV], done[kMostV];
     uint64_t s_full[2], p_ready[2], t_full[2], q_ready, q_free, meet[3], drain;
     alignas(16) uint32_t none[kMostV][4];  // of a v tile: slots whose page is out of range
-    uint32_t odd[2][4][4];          // slots whose v is not finite
+    uint32_t odd[2][2][2][4];       // of a warpgroup, by turns: slots whose v is not finite
     float2 ml[2][128];              // maxima and sums of the warpgroups' rows
     int last[2][3];                 // part_last(), its first CTA and number of parts
     uint32_t issued[2];             // steps of the loaders of k and of v
@@ -182,7 +182,17 @@ template <int ET> __device__ __forceinline__ float widen(uint32_t w, int half) {
     if (ET == kBF16) return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
     return __half2float(__ushort_as_half((unsigned short)(half ? w >> 16 : w & 0xFFFFu)));
 }
-// Has either half of w an exponent of all ones?
+// The larger of |a| and |b| in each half, NaN where there is one; and is either half not finite?
+template <int ET> __device__ __forceinline__ uint32_t most16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (ET == kBF16)
+        asm("{\n\t.reg .b32 x;\n\tabs.bf16x2 x, %2;\n\tmax.NaN.bf16x2 %0, %1, x;\n\t}"
+            : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("{\n\t.reg .b32 x;\n\tabs.f16x2 x, %2;\n\tmax.NaN.f16x2 %0, %1, x;\n\t}"
+            : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 template <int ET> __device__ __forceinline__ bool odd16x2(uint32_t w) {
     constexpr uint32_t e = ET == kBF16 ? 0x7F80u : 0x7C00u;
     return (w & e) == e || (w & (e << 16)) == (e << 16);
@@ -712,10 +722,10 @@ __device__ __forceinline__ float fine_tanh(float x) {
 template <typename S> struct Row {
     static constexpr int DP = S::DP, KT = S::KT, kChunks = KT / 32;
     static constexpr int kParts = DP / 64;             // rows of 128 bytes of a v
-    static constexpr int kScan = S::PAIR ? kSoft : kTeam;  // threads that look through a v
-    // Rows of 128 bytes to a thread, or threads to a row.
-    static constexpr int kEach = KT * kParts > kScan ? KT * kParts / kScan : 1;
-    static constexpr int kPieces = KT * kParts > kScan ? 1 : kScan / (KT * kParts);
+    // A warpgroup looks through a v by itself (both together: 60 us for pieces of prompts, where the
+    // one waits for the other): rows of 128 bytes to a thread, or threads to a row.
+    static constexpr int kEach = KT * kParts > kTeam ? KT * kParts / kTeam : 1;
+    static constexpr int kPieces = KT * kParts > kTeam ? 1 : kTeam / (KT * kParts);
     const TokensArgs &a;
     const KvView &kv;
     const Ctx &c;
@@ -723,7 +733,7 @@ template <typename S> struct Row {
     int head;
     const uint32_t tm;   // the warpgroup's columns, this warp's lanes
     const float to_log2;
-    uint32_t turns = 0;  // parities of the meetings of both and of this one, and bit 3 of look()
+    uint32_t turns = 0;  // parities of the meetings of both and of this one, and of look()
 
     __device__ __forceinline__ Row(const TokensArgs &a_, const KvView &kv_, const Ctx &c_)
         : a(a_), kv(kv_), c(c_), tm(c_.sh->tmem + ((threadIdx.x & 96u) << 16) + wg() * 256),
@@ -748,9 +758,8 @@ template <typename S> struct Row {
         int j, h;
         return place(j, h) ? see_of(a, tile->q, tile->seq, j) : See{};
     }
-    // 0: both warpgroups; 1: those that look through a v tile together; 2: this warpgroup.
-    __device__ __forceinline__ bool meet(int which) {
-        const bool alone = S::PAIR ? which == 2 : which > 0;
+    // The threads of this warpgroup, or of both.
+    __device__ __forceinline__ bool meet(bool alone) {
         uint64_t *const bar = &c.sh->meet[alone ? 1 + wg() : 0];
         const int bit = alone;
         const uint32_t turn = turns >> bit & 1;
@@ -800,9 +809,11 @@ template <typename S> struct Row {
             }
             if (mixed) {
                 const uint32_t in = seen32(a, see(), jc) & ~none[ch];
+                if (__any_sync(0xFFFFFFFFu, ~in)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!(in >> e & 1u)) v[e] = 0xFF800000u;
+                    for (int e = 0; e < 32; ++e)
+                        if (!(in >> e & 1u)) v[e] = 0xFF800000u;
+                }
             }
             st32(tm + kColS + 32 * ch, v);
         }
@@ -818,7 +829,7 @@ template <typename S> struct Row {
     };
     __device__ __forceinline__ Line line() const {
         Line n;
-        n.at = S::PAIR ? threadIdx.x : threadIdx.x % kTeam;
+        n.at = threadIdx.x % kTeam;
         n.slot = n.at % KT;
         const int rest = n.at / KT;
         n.part = kEach > 1 ? rest * kEach : rest % kParts;
@@ -827,24 +838,27 @@ template <typename S> struct Row {
     }
     __device__ __forceinline__ bool look(uint32_t v_at, Odd &o) {
         const Line n = line();
-        bool mine = false;
+        uint32_t most[4] = {};
 #pragma unroll 1
         for (int p = 0; p < kEach; ++p) {
             const uint32_t at = v_at + (n.part + p) * (KT * 128) + n.slot * 128;
 #pragma unroll
             for (int ch = 0; ch < 8 / kPieces; ++ch) {
                 const uint4 w = lds16(at + (((ch + n.piece * (8 / kPieces) + n.slot) & 7) << 4));
-                mine |= odd16x2<S::ET>(w.x) || odd16x2<S::ET>(w.y) || odd16x2<S::ET>(w.z) ||
-                        odd16x2<S::ET>(w.w);
+                most[0] = most16x2<S::ET>(most[0], w.x), most[1] = most16x2<S::ET>(most[1], w.y);
+                most[2] = most16x2<S::ET>(most[2], w.z), most[3] = most16x2<S::ET>(most[3], w.w);
             }
         }
+        const bool mine = odd16x2<S::ET>(most16x2<S::ET>(most16x2<S::ET>(most[0], most[1]),
+                                                         most16x2<S::ET>(most[2], most[3])));
         const uint32_t found = __ballot_sync(0xFFFFFFFFu, mine);
-        // Two sets taken in turn: a warpgroup may be a tile ahead of the other's reading.
-        o.words = &c.sh->odd[S::PAIR ? turns >> 3 & 1 : wg()][0][0];
-        turns ^= 8u;
+        // By turns: the next scores, and with them the look after the next, come after all of the
+        // warpgroup's weights.
+        o.words = &c.sh->odd[wg()][turns >> 2 & 1][0][0];
+        turns ^= 4u;
         if ((threadIdx.x & 31) == 0) o.words[n.at / KT * 4 + n.slot / 32] = found;
         tc_fence_before();
-        if (!meet(1)) return false;
+        if (!meet(true)) return false;
         tc_fence_after();
         o.any = 0;
 #pragma unroll
@@ -854,7 +868,7 @@ template <typename S> struct Row {
     __device__ __forceinline__ static uint32_t word(const Odd &o, int ch) {
         uint32_t w = 0;
 #pragma unroll
-        for (int i = 0; i < kScan / KT; ++i) w |= o.words[4 * i + ch];
+        for (int i = 0; i < kTeam / KT; ++i) w |= o.words[4 * i + ch];
         return w;
     }
     // f(slot, p) for each of them that the row sees, p its weight against the maximum `safe`; every
@@ -889,10 +903,11 @@ template <typename S> struct Row {
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = widen<S::ET>(z[k >> 1], k & 1);
     }
-    // Takes those slots out of the tile once every row has them.
+    // Takes those slots out of the tile once every row has them: with pairs, those of both
+    // warpgroups, which have found the same.
     __device__ __forceinline__ bool clear(uint32_t v_at, const Odd &o) {
         tc_fence_before();
-        if (!meet(1)) return false;
+        if (!meet(!S::PAIR)) return false;
         tc_fence_after();
         const Line n = line();
         if (word(o, n.slot >> 5) >> (n.slot & 31) & 1u) {
@@ -914,7 +929,7 @@ template <typename S> struct Row {
         c.sh->ml[wg()][r()] = make_float2(m, l);
         wait_st();
         tc_fence_before();
-        if (!meet(0)) return false;
+        if (!meet(false)) return false;
         tc_fence_after();
         const float2 x0 = c.sh->ml[0][r()], x1 = c.sh->ml[1][r()];
         const float both = fmaxf(x0.x, x1.x), safe = both == -INFINITY ? 0.f : both;
@@ -945,7 +960,7 @@ template <typename S> struct Row {
             return false;
         __syncwarp();
         tc_fence_before();
-        if (!meet(0)) return false;  // both have read both
+        if (!meet(false)) return false;  // both have read both
         tc_fence_after();
         return true;
     }
@@ -966,14 +981,14 @@ template <typename S> struct Row {
         if (!a.join_inside) return true;
         __threadfence();
         // Pairs: a warpgroup has rows of its own.
-        const int which = S::PAIR ? wg() : 0, meeting = S::PAIR ? 2 : 0;
-        if (!meet(meeting)) return false;
+        const int which = S::PAIR ? wg() : 0;
+        if (!meet(S::PAIR)) return false;
         if (threadIdx.x == which * kTeam) {
             int lead, parts;
             c.sh->last[which][0] = part_last(room, st, blockIdx.x, which, lead, parts);
             c.sh->last[which][1] = lead, c.sh->last[which][2] = parts;
         }
-        if (!meet(meeting)) return false;
+        if (!meet(S::PAIR)) return false;
         if (!c.sh->last[which][0]) return true;
         __threadfence();
         if (!live) return true;
@@ -1118,32 +1133,43 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
         for (int i = S::PAIR ? 0 : w.wg(); i < n; i += S::PAIR ? 1 : 2) {
             const uint32_t g = base + i, vs = g % S::NV;
             const int j0 = (st.k0 + i) * KT;
+            // What a border tile needs is found while its scores are under way.
+            if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
+            const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
+            const bool mixed =
+                j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
+            const uint32_t v_at = c.v_ring + vs * S::kSlot;
+            uint32_t in[kChunks];
+            typename R::Odd odd{};
+            if (mixed) {
+                if (!w.formed()) {
+                    const See see = w.see();
+#pragma unroll
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        in[ch] = seen32(a, see, j0 + 32 * ch) & ~sh->none[vs][ch];
+                }
+                if (!w.look(v_at, odd)) return;
+            }
             if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
             tc_fence_after();
             if (S::PAIR && threadIdx.x == kTeam && i > 0) mbar_arrive(&sh->done[(g - 1) % S::NV]);
             __syncwarp();
             uint32_t s[kChunks][32];
+            if (w.formed()) w.form(j0, mixed, sh->none[vs]);
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
-            if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
-            const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
-            const bool mixed =
-                j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
-            if (w.formed()) {
+            auto hide = [&](int ch) {  // the scores that are not seen
+                if (__any_sync(0xFFFFFFFFu, ~in[ch])) {
 #pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) wait_ld(s[ch]);
-                w.form(j0, mixed, sh->none[vs]);
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) ld32(s[ch], w.tm + kColS + 32 * ch);
-            } else if (mixed) {
-                const See see = w.see();
+                    for (int e = 0; e < 32; ++e)
+                        if (!(in[ch] >> e & 1u)) s[ch][e] = 0xFF800000u;
+                }
+            };
+            if (mixed && !w.formed()) {
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) {
                     wait_ld(s[ch]);
-                    const uint32_t in = seen32(a, see, j0 + 32 * ch) & ~sh->none[vs][ch];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(in >> e & 1u)) s[ch][e] = 0xFF800000u;
+                    hide(ch);
                 }
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1195,42 +1221,32 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                 }
                 ld32(s[0], w.tm + kColS);
                 wait_ld(s[0]);
-                if (mixed && !w.formed()) {
-                    const uint32_t in = seen32(a, w.see(), j0) & ~sh->none[vs][0];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(in >> e & 1u)) s[0][e] = 0xFF800000u;
-                }
+                if (mixed && !w.formed()) hide(0);
                 sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
                 weigh(0);
             }
-            if (mixed) {
-                const uint32_t v_at = c.v_ring + vs * S::kSlot;
-                typename R::Odd odd;
-                if (!w.look(v_at, odd)) return;
-                if (odd.any) {
-                    wait_st();
+            if (odd.any) {
+                wait_st();
 #pragma unroll 1
-                    for (int ch = 0; ch < DP / 32; ++ch) {
-                        uint32_t v[32];
-                        ld32(v, w.tm + kColT + 32 * ch);
-                        wait_ld(v);
-                        w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool in, float p) {
+                for (int ch = 0; ch < DP / 32; ++ch) {
+                    uint32_t v[32];
+                    ld32(v, w.tm + kColT + 32 * ch);
+                    wait_ld(v);
+                    w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool seen, float p) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                float x[8];
-                                w.v8(v_at, slot, 4 * ch + e / 8, x);
+                        for (int e = 0; e < 32; e += 8) {
+                            float x[8];
+                            w.v8(v_at, slot, 4 * ch + e / 8, x);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (in)
-                                        v[e + k] = __float_as_uint(
-                                            fmaf(p, x[k], __uint_as_float(v[e + k])));
-                            }
-                        });
-                        st32(w.tm + kColT + 32 * ch, v);
-                    }
-                    if (!w.clear(v_at, odd)) return;
+                            for (int k = 0; k < 8; ++k)
+                                if (seen)
+                                    v[e + k] = __float_as_uint(
+                                        fmaf(p, x[k], __uint_as_float(v[e + k])));
+                        }
+                    });
+                    st32(w.tm + kColT + 32 * ch, v);
                 }
+                if (!w.clear(v_at, odd)) return;
             }
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
@@ -1321,13 +1337,16 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             if (pending && !take()) return;
             const uint32_t g = base + i, vs = g % S::NV;
             if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
-            if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
-            tc_fence_after();
             const int j0 = (st.k0 + i) * KT;
             uint32_t lost = 0;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
             const bool mixed = j0 < lo || j0 + KT > hi || lost;
+            const uint32_t v_at = c.v_ring + vs * S::kSlot;
+            typename Row<S>::Odd odd{};
+            if (mixed && !w.look(v_at, odd)) return;
+            if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
+            tc_fence_after();
             if (w.formed() || mixed) w.form(j0, mixed, sh->none[vs]);
             float top = -INFINITY;
 #pragma unroll
@@ -1343,29 +1362,24 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             const float fl = ex2(m - safe);
             f = fl;
             m = now;
-            if (mixed) {
-                const uint32_t v_at = c.v_ring + vs * S::kSlot;
-                typename Row<S>::Odd odd;
-                if (!w.look(v_at, odd)) return;
-                if (odd.any) {
-                    // Only for rows that see one: what else the tile's place holds changes no bit.
-                    if (w.sees_odd(odd, j0, sh->none[vs])) {
+            if (odd.any) {
+                // Only for rows that see one: what else the tile's place holds changes no bit.
+                if (w.sees_odd(odd, j0, sh->none[vs])) {
 #pragma unroll
-                        for (int e = 0; e < DP; ++e) o[e] *= f;
-                        f = 1.f;
-                    }
-                    w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool in, float p) {
-#pragma unroll
-                        for (int e = 0; e < DP; e += 8) {
-                            float x[8];
-                            w.v8(v_at, slot, e / 8, x);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (in) o[e + k] = fmaf(p, x[k], o[e + k]);
-                        }
-                    });
-                    if (!w.clear(v_at, odd)) return;
+                    for (int e = 0; e < DP; ++e) o[e] *= f;
+                    f = 1.f;
                 }
+                w.each_odd(odd, j0, sh->none[vs], safe, [&](int slot, bool seen, float p) {
+#pragma unroll
+                    for (int e = 0; e < DP; e += 8) {
+                        float x[8];
+                        w.v8(v_at, slot, e / 8, x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (seen) o[e + k] = fmaf(p, x[k], o[e + k]);
+                    }
+                });
+                if (!w.clear(v_at, odd)) return;
             }
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

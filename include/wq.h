@@ -622,8 +622,8 @@ typedef struct {
     const int32_t *first;  /* int32 [n_tok]: only slots >= first[t] (packed documents); or NULL */
     const int32_t *prefix; /* int32 [n_seq]: the live slots below prefix[s] are seen by all of the
                               sequence's tokens (subject to first and window); or NULL */
-    const uint32_t *tree;  /* [n_tok][tree_stride]: bit b (word b / 32, bit b % 32) of token t's row:
-                              t sees its sequence's b-th new token; or NULL */
+    const uint32_t *tree;  /* [n_tok][tree_stride]: bit b (word b / 32, bit b % 32) of token t's
+                              row: t sees its sequence's b-th new token; or NULL */
     int64_t tree_stride;   /* words; what lies beyond a row's words is not seen */
     const int32_t *pos;    /* int32 [n_tok], only with tree: the new tokens' positions (held within
                               +-2^30); or NULL */
@@ -653,15 +653,15 @@ typedef struct {
  * Rows of q at or beyond starts[n_seq] reach no result, and theirs of out are not written.
  * Nothing overlaps out, lse or the workspace.
  * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not
- * like that is left out (and of ranges that overlap, what n_tok rows do not hold), a length below T or above max_pages * page_size is cut to the slots
- * that there are, and a page out of range that holds live slots leaves them out; each records
- * WQ_ERR_BAD_INDEX in the device status.
+ * like that is left out (and of ranges that overlap, what n_tok rows do not hold), a length
+ * below T or above max_pages * page_size is cut to the slots that there are, and a page out of
+ * range that holds live slots leaves them out; each records WQ_ERR_BAD_INDEX in the device status.
  * form (read on the host, not kept) NULL: causal, no cap.
  * workspace: as wq_attn_paged's, of wq_attn_tokens_workspace_bytes(...) bytes.
  * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, n_tok, h_q, max_pages <= 0, h_q
  * not a multiple of the kv heads, a scale that is not finite, a softcap below 0 or not finite,
- * window < 0, tree with prefix, tree_stride < 1 or above 2^26, pos without tree, unknown types, null q, starts,
- * page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
+ * window < 0, tree with prefix, tree_stride < 1 or above 2^26, pos without tree, unknown types,
+ * null q, starts, page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
  * or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
  * missing, misaligned or small workspace. */
 WQ_API wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q,
