@@ -72,7 +72,7 @@ struct Shared {
     alignas(16) uint32_t none[kMostV][4];  // of a v tile: slots whose page is out of range
     uint32_t odd[2][2][2][4];       // of a warpgroup, by turns: slots whose v is not finite
     float2 ml[2][128];              // maxima and sums of the warpgroups' rows
-    int last[2][3];                 // part_last(), its first CTA and number of parts
+    int last[2][2][3];              // of this CTA's two parts: part_last(), the first CTA, the parts
     uint32_t issued[2];             // steps of the loaders of k and of v
     uint32_t tmem, abort;
 };
@@ -980,69 +980,96 @@ template <typename S> struct Row {
             room.part_ml[(2 * blockIdx.x + st.part) * S::RT + row()] = make_float2(m, l);
         if (!a.join_inside) return true;
         __threadfence();
-        // Pairs: a warpgroup has rows of its own.
         const int which = S::PAIR ? wg() : 0;
         if (!meet(S::PAIR)) return false;
         if (threadIdx.x == which * kTeam) {
             int lead, parts;
-            c.sh->last[which][0] = part_last(room, st, blockIdx.x, which, lead, parts);
-            c.sh->last[which][1] = lead, c.sh->last[which][2] = parts;
+            int *const to = c.sh->last[st.part][which];
+            to[0] = part_last(room, st, blockIdx.x, which, lead, parts);
+            to[1] = lead, to[2] = parts;
         }
         if (!meet(S::PAIR)) return false;
-        if (!c.sh->last[which][0]) return true;
+        if (!c.sh->last[st.part][which][0]) return true;
         __threadfence();
         if (!live) return true;
-        const int lead = c.sh->last[which][1], parts = c.sh->last[which][2];
-        // Loads of several parts in flight: one SM reads them all.
-        auto ml_of = [&](int i) {
-            return __ldcg(room.part_ml + part_place(lead, min(i, parts - 1)) * S::RT + row());
-        };
-        float top = -INFINITY, sum = 0.f;
-        for (int i0 = 0; i0 < parts; i0 += 8) {
-            float2 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = ml_of(i0 + i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i0 + i >= parts) break;
-                const float now = fmaxf(top, x[i].x), safe = now == -INFINITY ? 0.f : now;
-                sum = fmaf(sum, ex2(top - safe), x[i].y * ex2(x[i].x - safe));
-                top = now;
-            }
-        }
-        const float safe = top == -INFINITY ? 0.f : top;
+        const Joined to = joined(room, st, -1, 0.f, 0.f);
 #pragma unroll 1
         for (int e = d0; e < d1; e += 32) {
-            float o[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            for (int i0 = 0; i0 < parts; i0 += 2) {
-                float f[2];
-                float4 v[2][8];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f[i] = ml_of(i0 + i).x;
-                    const size_t part = part_place(lead, min(i0 + i, parts - 1));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[i][k] = __ldcg(room.part_o + (part * (DP / 4) + e / 4 + k) * S::RT + row());
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i0 + i >= parts) break;
-                    const float g = ex2(f[i] - safe);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        o[4 * k] = fmaf(v[i][k].x, g, o[4 * k]);
-                        o[4 * k + 1] = fmaf(v[i][k].y, g, o[4 * k + 1]);
-                        o[4 * k + 2] = fmaf(v[i][k].z, g, o[4 * k + 2]);
-                        o[4 * k + 3] = fmaf(v[i][k].w, g, o[4 * k + 3]);
-                    }
-                }
-            }
-            finish(j, h, top, sum, e, o);
+            float x[32];
+            join_dims(room, to, e, x);
+            finish(j, h, to.m, to.l, e, x);
         }
         return true;
+    }
+    // Are all other parts of the row tile there?  Then this one joins them without being written: most
+    // row tiles of prompts, whose first part is its CTA's last work and whose others began with theirs.
+    // One thread looks, and a meeting later all know.
+    __device__ __forceinline__ void peek(const Room &room, const Stretch &st) const {
+        const int which = S::PAIR ? wg() : 0;
+        if (threadIdx.x != which * kTeam) return;
+        const Begin *const b = room.plan + blockIdx.x + st.part;
+        int *const to = c.sh->last[st.part][which];
+        const int lead = b->lead, parts = b->parts;
+        to[0] = *(volatile unsigned *)(room.joined + 2 * lead + which) == (unsigned)parts - 1;
+        to[1] = lead, to[2] = parts;
+    }
+    // The row's maximum and sum over all parts, of which this CTA's may be in its registers (own >= 0).
+    struct Joined {
+        int lead, parts, own;
+        float m, l, mine;
+    };
+    __device__ __forceinline__ Joined joined(const Room &room, const Stretch &st, int own, float m,
+                                             float l) const {
+        const int *const last = c.sh->last[st.part][S::PAIR ? wg() : 0];
+        Joined to{last[1], last[2], own, -INFINITY, 0.f, m};
+        for (int i0 = 0; i0 < to.parts; i0 += 8) {
+            float2 x[8];  // loads of several parts in flight: one SM reads them all
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __ldcg(room.part_ml +
+                              part_place(to.lead, min(i0 + i, to.parts - 1)) * S::RT + row());
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i0 + i >= to.parts) break;
+                if (i0 + i == own) x[i] = make_float2(m, l);
+                const float now = fmaxf(to.m, x[i].x), safe = now == -INFINITY ? 0.f : now;
+                to.l = fmaf(to.l, ex2(to.m - safe), x[i].y * ex2(x[i].x - safe));
+                to.m = now;
+            }
+        }
+        return to;
+    }
+    // Dims e .. e + 31 of all parts, in their order whoever joins them; x holds this CTA's if to.own >= 0.
+    __device__ __forceinline__ void join_dims(const Room &room, const Joined &to, int e,
+                                              float (&x)[32]) const {
+        const float safe = to.m == -INFINITY ? 0.f : to.m;
+        float o[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < to.parts; ++i) {
+            if (i == to.own) {
+                const float g = ex2(to.mine - safe);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = fmaf(x[k], g, o[k]);
+                continue;
+            }
+            const size_t part = part_place(to.lead, i);
+            const float top = __ldcg(room.part_ml + part * S::RT + row()).x;
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = __ldcg(room.part_o + (part * (DP / 4) + e / 4 + k) * S::RT + row());
+            const float g = ex2(top - safe);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[4 * k] = fmaf(v[k].x, g, o[4 * k]), o[4 * k + 1] = fmaf(v[k].y, g, o[4 * k + 1]);
+                o[4 * k + 2] = fmaf(v[k].z, g, o[4 * k + 2]);
+                o[4 * k + 3] = fmaf(v[k].w, g, o[4 * k + 3]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = o[k];
     }
     // Dims e .. e + 31 of the row's result from its sums.
     __device__ __forceinline__ void finish(int j, int h, float m, float l, int e,
@@ -1139,14 +1166,17 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             const bool mixed =
                 j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
             const uint32_t v_at = c.v_ring + vs * S::kSlot;
-            uint32_t in[kChunks];
+            uint32_t in[kChunks] = {};
             typename R::Odd odd{};
             if (mixed) {
                 if (!w.formed()) {
                     const See see = w.see();
+#pragma unroll 1  // little code: it is seldom in the instruction cache
+                    for (int ch = 0; ch < kChunks; ++ch) {
+                        const uint32_t x = seen32(a, see, j0 + 32 * ch) & ~sh->none[vs][ch];
 #pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        in[ch] = seen32(a, see, j0 + 32 * ch) & ~sh->none[vs][ch];
+                        for (int k = 0; k < kChunks; ++k) in[k] = k == ch ? x : in[k];
+                    }
                 }
                 if (!w.look(v_at, odd)) return;
             }
@@ -1261,6 +1291,8 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             some = true;
         }
         base += n;
+        const bool peeks = S::PAIR && st.part >= 0 && a.join_inside;
+        if (peeks) w.peek(room, st);
         if (some) {
             if (!c.warp_wait(&sh->t_full[w.wg()], ended & 1)) return;
             tc_fence_after();
@@ -1269,6 +1301,17 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
         }
         const bool live = w.place(j, h);
         if (S::PAIR) {
+            bool last = false;
+            typename R::Joined to{};
+            if (peeks) {
+                if (!w.meet(true)) return;
+                const int *const found = sh->last[st.part][w.wg()];
+                last = found[0];
+                if (last) {
+                    __threadfence();
+                    to = w.joined(room, st, st.part == 1 ? 0 : blockIdx.x - found[1], m, l);
+                }
+            }
 #pragma unroll 1
             for (int ch = 0; ch < DP / 32; ++ch) {
                 uint32_t v[32] = {};
@@ -1279,13 +1322,15 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
                 float x[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-                if (st.part >= 0)
+                if (st.part >= 0 && !last) {
                     w.put_part(room, st, 32 * ch, x);
-                else if (live)
-                    w.finish(j, h, m, l, 32 * ch, x);
+                } else if (live) {
+                    if (last) w.join_dims(room, to, 32 * ch, x);
+                    w.finish(j, h, last ? to.m : m, last ? to.l : l, 32 * ch, x);
+                }
                 __syncwarp();
             }
-            if (st.part >= 0 && !w.join_parts(room, st, live, j, h, m, l, 0, DP)) return;
+            if (st.part >= 0 && !last && !w.join_parts(room, st, live, j, h, m, l, 0, DP)) return;
         } else if (!w.join(room, st, n > 0, live, j, h, m, l)) {
             return;
         }
