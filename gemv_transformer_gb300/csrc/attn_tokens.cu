@@ -234,6 +234,17 @@ template <typename T> __device__ __forceinline__ void load8(const void *p, float
     }
 }
 
+// 16 bytes to shared memory, zeros where the source is not live.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Two f32 operations of one instruction, pairs of neighbouring dims.
 using Pair = unsigned long long;
 __device__ __forceinline__ void fma2(Pair &d, Pair a, Pair b) {
@@ -255,17 +266,22 @@ template <int DP, int R> struct RowsShape {
     static constexpr int RT = 16 * R;
     static constexpr int kPitch = DP + 4;       // floats of a row of q or k: rows four banks apart
     static constexpr int kQ = RT * kPitch, kK = KT * kPitch, kV = KT * DP, kP = RT * (KT + 4);
-    static constexpr int kSmem = (kQ + kK + kV + kP) * 4;
+    static constexpr int kSmem = (kQ + kK + kV + kP) * 4 + RT * (int)sizeof(See);
+    static constexpr int kCtas = 2 * (kSmem + 1200) <= 228 * 1024 ? 2 : 1;  // on an SM
+    static constexpr int kGrid = 152 * kCtas;
 };
 
 template <typename T, int DP, int R>
-__global__ void __launch_bounds__(256)
-    attn_rows_kernel(TokensArgs a, KvView kv, int grid) {
+__global__ void __launch_bounds__(256, RowsShape<DP, R>::kCtas)
+    attn_rows_kernel(TokensArgs a, KvView kv) {
     using S = RowsShape<DP, R>;
     constexpr int KT = S::KT, RT = S::RT, NK = KT / 16, ND = DP / 32;
+    constexpr bool kAsync = sizeof(T) == 4;
+    constexpr int grid = S::kGrid;
     extern __shared__ __align__(16) float s_rows[];
     __shared__ int s_join[3];
     float *s_q = s_rows, *s_k = s_q + S::kQ, *s_v = s_k + S::kK, *s_p = s_v + S::kV;
+    See *const s_see = reinterpret_cast<See *>(s_p + S::kP);
     pdl_enter();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.group.d;
     const Room room = room_of(a.workspace, a.n_seq, a.n_tok, group, RT, DP, grid);
@@ -295,14 +311,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int e = 0; e < 8; ++e) s_q[r * S::kPitch + c * 8 + e] = v[e];
         }
-        See see[R];
+        if (threadIdx.x < RT) {
+            const int rr = tile.row0 + min((int)threadIdx.x, rows - 1);
+            s_see[threadIdx.x] = see_of(a, q, tile.seq, a.group.div(rr));
+        }
         float slope[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int r = ty * R + i;
-            const int rr = tile.row0 + min(r, rows - 1), j = a.group.div(rr);
-            see[i] = see_of(a, q, tile.seq, j);
-            slope[i] = a.slopes ? a.slopes[st.head * group + rr - j * group] : 0.f;
+            const int rr = tile.row0 + min(ty * R + i, rows - 1);
+            slope[i] = a.slopes ? a.slopes[st.head * group + rr - a.group.div(rr) * group] : 0.f;
         }
         float m[R], l[R];
         Pair o[R][ND];  // dims 32 e + 2 tx of the thread's rows
@@ -312,32 +329,49 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int e = 0; e < ND; ++e) o[i][e] = 0ull;
         }
-        for (int kt = st.k0; kt < st.k1; ++kt) {
-            const int j0 = kt * KT;
-            __syncthreads();
-            // k and v, zero beyond the live slots and where a page is out of range.
-            uint32_t lost = 0;  // (bit 0) a slot without a page, (bit 1) a v that is not finite
+        // k and v of a tile, zero beyond the live slots and where a page is out of range.  f32 caches:
+        // k of the next tile is under way during the weights and products of this one, v during the
+        // next one's scores.  16-bit caches are widened on their way, both together.
+        uint32_t lost = 0;  // of the tile that is asked for: (bit 0) a slot without a page, (bit 1) a v
+                            // that is not finite
+        auto ask = [&](int kt, bool is_v) {
+            if (kt >= st.k1 || (!kAsync && !is_v)) return;
+            if (is_v) lost = 0;
             for (int i = threadIdx.x; i < KT * (DP / 8); i += 256) {
-                const int r = i / (DP / 8), c = i - r * (DP / 8), j = j0 + r;
-                float x[8] = {}, y[8] = {};
+                const int r = i / (DP / 8), c = i - r * (DP / 8), j = kt * KT + r;
+                long long at = -1;
                 if (j < q.len) {
-                    const long long at = kv.row(tile.seq, st.head, j);
-                    if (at < 0) {
-                        lost |= 1u;
-                    } else if (c * 8 < d) {
+                    at = kv.row(tile.seq, st.head, j);
+                    if (at < 0) lost |= 1u;
+                }
+                const bool live = at >= 0 && c * 8 < d;
+                if constexpr (kAsync) {
+                    const char *const from = (is_v ? kv.v : kv.k) + (live ? at + c * 32 : 0);
+                    const uint32_t to = smem_addr((is_v ? s_v + r * DP : s_k + r * S::kPitch) + c * 8);
+                    cp16(to, from, live);
+                    cp16(to + 16, from + (live ? 16 : 0), live);
+                } else {
+                    float x[8] = {}, y[8] = {};
+                    if (live) {
                         load8<T>(kv.k + at + c * 8 * sizeof(T), x);
                         load8<T>(kv.v + at + c * 8 * sizeof(T), y);
                     }
-                }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s_k[r * S::kPitch + c * 8 + e] = x[e];
-                    s_v[r * DP + c * 8 + e] = y[e];
-                    if (!isfinite(y[e])) lost |= 2u;
+                    for (int e = 0; e < 8; ++e) {
+                        s_k[r * S::kPitch + c * 8 + e] = x[e];
+                        s_v[r * DP + c * 8 + e] = y[e];
+                        if (!isfinite(y[e])) lost |= 2u;
+                    }
                 }
             }
-            const int none = __syncthreads_or(lost & 1u), odd = __syncthreads_or(lost & 2u);
-            if (none && threadIdx.x == 0) record_status(a.status, kStBadIndex);
+            if (kAsync) cp_commit();
+        };
+        ask(st.k0, false);
+        ask(st.k0, true);
+        for (int kt = st.k0; kt < st.k1; ++kt) {
+            const int j0 = kt * KT;
+            if (kAsync) cp_wait<1>();
+            __syncthreads();
             Pair x2[R][NK];
 #pragma unroll
             for (int i = 0; i < R; ++i)
@@ -369,20 +403,34 @@ __global__ void __launch_bounds__(256)
                     const float2 s = floats_of(x2[i][n]);
                     x[i][n] = s.x + s.y;
                 }
+            if constexpr (kAsync) {  // this thread's share of v
+                cp_wait<0>();
+                for (int i = threadIdx.x; i < KT * (DP / 8); i += 256) {
+                    const float4 *const y = reinterpret_cast<const float4 *>(s_v + i * 8);
+                    const float4 y0 = y[0], y1 = y[1];
+                    if (!(isfinite(y0.x) && isfinite(y0.y) && isfinite(y0.z) && isfinite(y0.w) &&
+                          isfinite(y1.x) && isfinite(y1.y) && isfinite(y1.z) && isfinite(y1.w)))
+                        lost |= 2u;
+                }
+            }
+            const int none = __syncthreads_or(lost & 1u), odd = __syncthreads_or(lost & 2u);
+            if (none && threadIdx.x == 0) record_status(a.status, kStBadIndex);
+            ask(kt + 1, false);
             const bool whole = j0 >= tile.lo && j0 + KT <= tile.hi && !none;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 uint32_t seen[KT / 32];
 #pragma unroll
                 for (int w = 0; w < KT / 32; ++w)
-                    seen[w] = whole ? 0xFFFFFFFFu : seen32(a, see[i], j0 + 32 * w);
+                    seen[w] = whole ? 0xFFFFFFFFu : seen32(a, s_see[ty * R + i], j0 + 32 * w);
+                const int pos = s_see[ty * R + i].pos;
                 float top = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
                     const int r = tx + 16 * n, j = j0 + r;
                     float y = x[i][n] * a.scale;
                     if (a.softcap > 0.f) y = a.softcap * tanhf(y / a.softcap);
-                    if (a.slopes) y = fmaf(slope[i], (float)(slot_pos(a, q, j) - see[i].pos), y);
+                    if (a.slopes) y = fmaf(slope[i], (float)(slot_pos(a, q, j) - pos), y);
                     bool in = seen[r >> 5] >> (r & 31) & 1u;
                     if (none && in) in = kv.row(tile.seq, st.head, j) >= 0;
                     // A score that is not a number stays one: only slots that are not seen are -inf.
@@ -454,6 +502,8 @@ __global__ void __launch_bounds__(256)
                                  *reinterpret_cast<const Pair *>(s_v + r * DP + 32 * e + 2 * tx));
                     }
             }
+            __syncthreads();
+            ask(kt + 1, true);
         }
         // Parts lie as [dims / 4][row][4].
         auto part_at = [&](size_t part, int r, int e) {
@@ -544,13 +594,12 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = ensure_smem(attn_rows_kernel<T, DP, R>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
-    const int grid = kMaxGrid;
+    const int grid = S::kGrid;
     TokensArgs b = a;
     b.join_inside = joins_inside(a, kv, S::RT, grid);
     err = launch_attn_plan(b, kv, S::RT, S::KT, DP, grid, 2, stream);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, b, kv,
-                     grid);
+    err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, b, kv);
     if (err != cudaSuccess || b.join_inside) return err;
     return launch_attn_parts(b, kv, S::RT, DP, grid, stream);
 }
