@@ -18,9 +18,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanTiles = 2048;
-// A CTA's range is no shorter, or the parts' sums cost more than they save: 1, 2, 3, 4 and 6 took
-// 31, 31, 25, 24 and 29 us for 4 sequences of 16 nodes behind 1000 slots.
-constexpr int kLeastCost = 3;
+// A CTA's range is no shorter, or the parts cost more than they save: 2, 3 and 6 took 19.6, 20.8 and
+// 28 us for 16 nodes behind 900 slots.
+constexpr int kLeastCost = 2;
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
@@ -597,7 +597,9 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     const int grid = S::kGrid;
     TokensArgs b = a;
     b.join_inside = joins_inside(a, kv, S::RT, grid);
-    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, grid, 2, stream);
+    // A row tile's start and end as a key tile: as two, three and four packed documents took 76, 84
+    // and 84 us instead of 69.
+    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, grid, 1, stream);
     if (err != cudaSuccess) return err;
     err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, b, kv);
     if (err != cudaSuccess || b.join_inside) return err;
