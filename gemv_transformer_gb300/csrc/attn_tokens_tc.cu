@@ -703,17 +703,63 @@ __device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, co
     }
 }
 
+// Two f32 operations of one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
+        "mov.b64 r, {%5, %5};\n\tfma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a0, float a1) {
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+        "mov.b64 r, {%6, %7};\n\tfma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The smaller, NaN where x is.
+__device__ __forceinline__ float held_below(float x, float top) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(top));
+    return y;
+}
+
 // tanh of the cap for f32 queries, within a few 2^-24 of itself: Lambert's continued fraction cut to
 // z (945 + 105 z^2 + z^4) / (945 + 420 z^2 + 15 z^4) up to 0.5 (off by 2e-9 there), beyond it
-// (e - 1) / (e + 1) with e = exp(2 z); one division, no branch, NaN stays NaN.
-__device__ __forceinline__ float fine_tanh(float x) {
-    const float z = x * x;
-    const float held = x > 10.f ? 10.f : x < -10.f ? -10.f : x;  // tanh is 1 to 2^-27 there
-    const float e = ex2(held * (2.f * kLog2e));
-    const float n0 = x * fmaf(z, z + 105.f, 945.f), d0 = fmaf(z, fmaf(z, 15.f, 420.f), 945.f);
-    const bool small = z < 0.25f;
-    const float n = small ? n0 : e - 1.f, d = small ? d0 : e + 1.f;
-    return __fdividef(n, d);
+// (e - 1) / (e + 1) with e = exp(2 z), z held below 10 (tanh is 1 to 2^-27 there); one division, no
+// branch, NaN stays NaN.  Two at a time.
+__device__ __forceinline__ float2 fine_tanh(float2 x) {
+    const float2 z = mul2(x, x);
+    const float2 e2 = mul2(make_float2(held_below(x.x, 10.f), held_below(x.y, 10.f)),
+                           both(2.f * kLog2e));
+    const float2 e = make_float2(ex2(e2.x), ex2(e2.y));
+    const float2 n0 = mul2(x, fma2(z, fma2(z, both(1.f), both(105.f)), both(945.f)));
+    const float2 d0 = fma2(z, fma2(z, both(15.f), both(420.f)), both(945.f));
+    const float2 n1 = fma2(e, both(1.f), both(-1.f)), d1 = fma2(e, both(1.f), both(1.f));
+    const bool sx = z.x < 0.25f, sy = z.y < 0.25f;
+    return mul2(make_float2(sx ? n0.x : n1.x, sy ? n0.y : n1.y),
+                make_float2(rcp(sx ? d0.x : d1.x), rcp(sy ? d0.y : d1.y)));
 }
 
 // A softmax thread's row, and what the two kinds of softmax share.  What only border tiles and a
@@ -768,8 +814,9 @@ template <typename S> struct Row {
         return c.warp_wait(bar, turn);
     }
     // This thread's scores in tensor memory to log2 units after cap and bias, those that are not
-    // seen to -inf.
-    __device__ __forceinline__ void form(int j0, bool mixed, const uint32_t *none) {
+    // seen to -inf; their maximum (where it is asked for: f32 queries).
+    __device__ __forceinline__ float form(int j0, bool mixed, const uint32_t *none) {
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
         for (int ch = 0; ch < kChunks; ++ch) {
             const int jc = j0 + 32 * ch;
@@ -785,8 +832,13 @@ template <typename S> struct Row {
                             v[e] = __float_as_uint(out * fast_tanh(__uint_as_float(v[e]) * in));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(out * fine_tanh(__uint_as_float(v[e]) * in));
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y = mul2(
+                                fine_tanh(mul2(make_float2(__uint_as_float(v[e]),
+                                                           __uint_as_float(v[e + 1])), both(in))),
+                                both(out));
+                            v[e] = __float_as_uint(y.x), v[e + 1] = __float_as_uint(y.y);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -816,8 +868,13 @@ template <typename S> struct Row {
                 }
             }
             st32(tm + kColS + 32 * ch, v);
+            if (S::TERMS > 1) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], __uint_as_float(v[e]));
+            }
         }
         wait_st();
+        return fmaxf(top[0], top[1]);
     }
     // Finds the slots of a v tile that are not finite; `any` is the same for all that look.
     struct Odd {
@@ -1116,20 +1173,6 @@ template <typename S> struct Row {
     }
 };
 
-// Two f32 operations of one instruction.
-__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
-    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
-        "mov.b64 r, {%5, %5};\n\tfma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float &x, float &y, float a0, float a1) {
-    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
-        "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(a0), "f"(a1));
-}
-
 // 16-bit queries: the output in tensor memory.
 template <typename S>
 __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
@@ -1392,15 +1435,18 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
             if (mixed && !w.look(v_at, odd)) return;
             if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
             tc_fence_after();
-            if (w.formed() || mixed) w.form(j0, mixed, sh->none[vs]);
             float top = -INFINITY;
+            if (w.formed() || mixed) {
+                top = w.form(j0, mixed, sh->none[vs]);
+            } else {
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t v[32];
-                ld32(v, w.tm + kColS + 32 * ch);
-                wait_ld(v);
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    uint32_t v[32];
+                    ld32(v, w.tm + kColS + 32 * ch);
+                    wait_ld(v);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                }
             }
             const float now = fmaxf(m, top * w.to_log2);
             const float safe = now == -INFINITY ? 0.f : now;
