@@ -4,12 +4,14 @@
 // x = cap(scale q.k) + slope (pos_k - pos_q), p = softmax(x) with a running maximum and sum,
 // in log2 units: y = x log2 e, p = 2^(y - m).
 //
-// attn_rows_kernel takes f32 caches, f32 queries over f16 caches and heads above 128 dims: k and v
-// are widened to f32 in shared memory and every product is an f32 FMA, so it is exact to f32 and
-// bound by the FMA pipe (4 head_dim operations per row and slot) from about 16 rows of a group on.
-// A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the output,
-// two neighbouring dims to an instruction; the 16 lanes of a row join its maximum and sum by
-// shuffles.
+// attn_rows_kernel takes f32 caches, f32 queries over f16 caches, mixed 16-bit types and heads above
+// 128 dims: k and v are f32 in shared memory and every product is an f32 FMA, so it is exact to f32.
+// What bounds it: the FMA pipe (4 head_dim operations per row and slot) and the shared memory that
+// feeds it (48 wavefronts to 64 FMA cycles), and for short rows how evenly 304 ranges share few
+// tiles.  A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the
+// output, two neighbouring dims to an instruction; the 16 lanes of a row join its maximum and sum
+// by shuffles.  Three packed batches of documents, 12/6 heads of 96, f32: 69 us, a quarter of the FMA
+// rate while a CTA works; 12 trees of f32 queries and an f32 cache to 6000 slots: 424 us.
 #include "attn_tokens.cuh"
 
 namespace wq {
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                     lo_most = max(lo_most, v.lo);
                     hi_least = min(hi_least, v.hi);
                 }
-                Tile t{s, row0, 0, 0, lo_most, hi_least, 0, 0, q};
+                Tile t{s, row0, 0, 0, lo_most, hi_least, q};
                 if (hi > lo) t.k0 = lo / kt, t.k1 = (hi + kt - 1) / kt;
                 room.tiles[first + r] = t;
                 if (first + r < kPlanTiles) s_keys[first + r] = t.k1 - t.k0;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     auto before = [&](int i) { return i < kPlanTiles ? s_before[i] : room.before[i]; };
     for (int b = threadIdx.x; b <= grid; b += kPlanThreads) {
-        Begin p{heads, 0, 0, n_tiles, 0, 0, 0, 0};
+        Begin p{heads, 0, 0, n_tiles, 0, 0};
         if (cost > 0) {
             // CTA b begins at each b + min(b, rest).
             const long long total = cost * heads;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // Joins the parts of the row tile that CTA blockIdx.x leads and others go on with.  A thread takes
-// four dims of a row at a time, with the loads of kAtOnce parts in flight.
+// four dims of a row at a time, with the loads of kAtOnce parts in flight.  (5 us of a call.)
 constexpr int kAtOnce = 8;
 __global__ void __launch_bounds__(256)
     attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
@@ -232,17 +234,6 @@ template <typename T> __device__ __forceinline__ void load8(const void *p, float
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
     }
-}
-
-// 16 bytes to shared memory, zeros where the source is not live.
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Two f32 operations of one instruction, pairs of neighbouring dims.

@@ -8,7 +8,8 @@
 // ranges, one for each CTA of a fixed grid, whatever the lengths.  A row tile within one CTA
 // is written by it; the parts of the others are joined by the rule of the running softmax, in an
 // order that the lengths fix: by whichever of their CTAs is the last to finish where a row tile
-// has few parts, else by attn_parts_kernel (one CTA alone reads 20 parts in 28 us).
+// has few parts (a 2048-token prompt: 57 us, with a launch for it 65), else by attn_parts_kernel
+// (one CTA alone reads 20 parts in 28 us).
 #pragma once
 
 #include "kv_internal.h"
@@ -102,18 +103,16 @@ __device__ __forceinline__ int slot_pos(const TokensArgs &a, const Seq &q, int j
 
 // --------------------------------------------------------------------- workspace --
 
-struct __align__(16) Tile {
+struct Tile {
     int seq, row0;
     int k0, k1;        // key tiles
     int lo, hi;        // every row of the tile sees [lo, hi)
-    int pad0, pad1;
     Seq q;             // the sequence's
 };
-struct __align__(16) Begin {
+struct Begin {
     int head, tile, off;  // where a CTA's range starts: kv head, row tile, key tiles into it
     int tiles;            // row tiles of all sequences
     int lead, parts;      // off > 0: the first CTA that works on that row tile, and how many do
-    int pad0, pad1;
 };
 struct Room {
     Begin *plan;         // [grid + 1]
@@ -228,6 +227,17 @@ struct TypedOut {
     }
 };
 
+// 16 bytes to shared memory, zeros where the source is not live.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));  // (scores that are not numbers: NaN)
@@ -236,8 +246,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // row_cost: a row tile's start and end count as so many key tiles.
 cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
                              int grid, int row_cost, cudaStream_t stream);
-// Does a row tile have few parts: are there as many row tiles as CTAs?  (That goes by the rows alone;
-// lengths are known on the device only.)
+// Does a row tile have few parts: are there as many row tiles as CTAs?  (That goes by the rows
+// alone; lengths are known on the device only.)
 inline bool joins_inside(const TokensArgs &a, const KvView &kv, int rt, int grid) {
     return (long long)a.n_tok * a.group.d / rt * kv.n_heads >= grid;
 }

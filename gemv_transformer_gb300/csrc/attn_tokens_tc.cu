@@ -13,16 +13,21 @@
 //               m) + T.
 //
 // PAIR: two row tiles, one to a warpgroup, share every k and v tile: prompts, where the products
-// bound it.  Otherwise one row tile, whose slot tiles the warpgroups take in turn and join at
-// the end: drafted trees, where the cache's bytes bound it and a second tile in flight hides the
-// chain of the first.
+// bound it (a prompt of 8192 tokens, 32/8 heads of 128: 421 us, 1306 TFLOP/s counting what is seen).
+// A tile's period is 3000 to 3500 cycles, products 2048 of it, the exponentials of 256 x 128 weights
+// another 2048 of their own unit, and what a warpgroup does between its scores and its weights.
+// Otherwise one row tile, whose slot tiles the warpgroups take in turn and join at the end: drafted
+// trees, where the cache's bytes bound it and a second tile in flight hides the chain of the
+// first (32 trees to 8192 slots: 117 us, 4.75 TB/s).  f32 queries: the three products of a score,
+// whose N is 64, are bound by shared memory (48 cycles in place of 32), the weights' chain comes
+// close to them (12 trees to 6000 slots: 81 us, with a cap 101).
 //
 // Shared memory is rows of 128 bytes in the 128-byte swizzle; k is K-major, v MN-major (its
 // dims are the contiguous ones), p is read from tensor memory over S.
 //
 // A v that is not finite under a weight of 0 would reach rows that do not see it: where not all
-// rows see all of a tile the warpgroups look through its v first, take such slots out, and add
-// them to the rows that see them by FMA.
+// rows see all of a tile each warpgroup looks through its v first, while the scores are under way,
+// takes such slots out, and adds them to the rows that see them by FMA.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -204,15 +209,6 @@ __device__ __forceinline__ float fast_tanh(float x) {
     return 1.f - __fdividef(2.f, ex2(x * (2.f * kLog2e)) + 1.f);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -375,8 +371,8 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
 }
 
 // The same by cp.async and two warps for pages of any size; a step's barrier is arrived at when
-// it has landed and NV - 1 others are under way, or the next one has to wait.  Slots beyond the live ones and in pages out
-// of range are zeros.
+// it has landed and NV - 1 others are under way, or the next one has to wait.  Slots beyond the
+// live ones and in pages out of range are zeros.
 template <typename S>
 __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
     constexpr int kLanes = S::DP / 8;         // 16-byte chunks, a lane each, of a row
@@ -473,8 +469,8 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
     while (ok && landed < g) land();
 }
 
-// q of a stretch of 16-bit queries, by one warp, while the stretch before ends: its place is free when
-// the last scores are done.  By TMA where whole tokens make up 128 rows (q_box tokens of group
+// q of a stretch of 16-bit queries, by one warp, while the stretch before ends: its place is free
+// when the last scores are done.  By TMA where whole tokens make up 128 rows (q_box tokens of group
 // heads; the rows beyond the sequence's are another's, and written by no one), else by cp.async.
 template <typename S>
 __device__ void load_queries(const TokensArgs &a, const KvView &kv, const CUtensorMap *q_map,
@@ -644,60 +640,50 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
 
 // -------------------------------------------------------------- softmax warpgroups --
 
-// COUNT rows of q from row `first` by THREADS threads.
-template <typename S, int COUNT, int THREADS>
+// f32 queries of a row tile as three bf16 terms, by all softmax threads.
+template <typename S>
 __device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, const Tile &tile,
-                                       int head, const Ctx &c, int first, int thread) {
-    constexpr int kChunks = S::DP / 8, kItems = COUNT * kChunks / THREADS;
-    constexpr int kBatch = S::TERMS == 1 ? (kItems < 8 ? kItems : 8) : 2;  // loads in flight
+                                       int head, const Ctx &c) {
+    constexpr int kChunks = S::DP / 8, kItems = 128 * kChunks / kSoft, kBatch = 2;
     const int group = a.group.d, row0 = tile.row0, t0 = tile.q.t0, d = kv.head_dim;
     const int rows = tile.q.count * group - row0;
 #pragma unroll 1
     for (int b = 0; b < kItems; b += kBatch) {
-        uint4 x[kBatch][S::TERMS == 1 ? 1 : 2];
+        uint4 x[kBatch][2];
         uint32_t to[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int i = thread + (b + k) * THREADS;
-            const int r = first + i / kChunks, ch = i % kChunks;
+            const int i = threadIdx.x + (b + k) * kSoft;
+            const int r = i / kChunks, ch = i % kChunks;
             const bool live = r < rows && ch * 8 < d;
             const int rr = row0 + r, j = a.group.div(live ? rr : 0);
             const int g = rr - j * group;
             const long long at =
                 (t0 + j) * a.q_stride + (long long)(head * group + g) * d + ch * 8;
-            // Row r of its tile of 128 rows.
-            to[k] = c.stage + (r >> 7) * (128 * S::DP * 2) + (ch >> 3) * S::kHalf +
-                    (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-            const char *const from =
-                static_cast<const char *>(a.q) + at * (S::TERMS == 1 ? 2 : 4);
+            to[k] = c.stage + (ch >> 3) * S::kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+            const uint4 *const from =
+                reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + at);
 #pragma unroll
-            for (int h = 0; h < (S::TERMS == 1 ? 1 : 2); ++h)
-                x[k][h] = live ? reinterpret_cast<const uint4 *>(from)[h]
-                               : make_uint4(0u, 0u, 0u, 0u);
+            for (int h = 0; h < 2; ++h) x[k][h] = live ? from[h] : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if constexpr (S::TERMS == 1) {
-                sts16(to[k], x[k][0]);
-            } else {
-                float y[8];
+            float y[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    y[4 * h] = __uint_as_float(x[k][h].x), y[4 * h + 1] = __uint_as_float(x[k][h].y);
-                    y[4 * h + 2] = __uint_as_float(x[k][h].z);
-                    y[4 * h + 3] = __uint_as_float(x[k][h].w);
+            for (int h = 0; h < 2; ++h) {
+                y[4 * h] = __uint_as_float(x[k][h].x), y[4 * h + 1] = __uint_as_float(x[k][h].y);
+                y[4 * h + 2] = __uint_as_float(x[k][h].z), y[4 * h + 3] = __uint_as_float(x[k][h].w);
+            }
+#pragma unroll
+            for (int t = 0; t < S::TERMS; ++t) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = pack2<kBF16>(y[2 * e], y[2 * e + 1]);
+                    y[2 * e] -= bf16_lo(w[e]);
+                    y[2 * e + 1] -= bf16_hi(w[e]);
                 }
-#pragma unroll
-                for (int t = 0; t < S::TERMS; ++t) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[e] = pack2<kBF16>(y[2 * e], y[2 * e + 1]);
-                        y[2 * e] -= bf16_lo(w[e]);
-                        y[2 * e + 1] -= bf16_hi(w[e]);
-                    }
-                    sts16(to[k] + t * S::kQTerm, make_uint4(w[0], w[1], w[2], w[3]));
-                }
+                sts16(to[k] + t * S::kQTerm, make_uint4(w[0], w[1], w[2], w[3]));
             }
         }
     }
@@ -1141,7 +1127,8 @@ template <typename S> struct Row {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
                 if (e + k >= kv.head_dim) break;
-                reinterpret_cast<float4 *>(p + k)[0] = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                reinterpret_cast<float4 *>(p + k)[0] =
+                    make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 reinterpret_cast<float4 *>(p + k)[1] =
                     make_float4(x[k + 4], x[k + 5], x[k + 6], x[k + 7]);
             }
@@ -1401,7 +1388,7 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
         float m = -INFINITY, l = 0.f, f = 0.f;
         bool pending = false;
         if (n > 0) {
-            load_q<S, 128, kSoft>(a, kv, *w.tile, st.head, c, 0, threadIdx.x);
+            load_q<S>(a, kv, *w.tile, st.head, c);
             fence_proxy_async_smem();
             c.warp_arrive(&sh->q_ready);
         }
@@ -1660,8 +1647,8 @@ bool pool_map(CUtensorMap &map, const KvView &kv, char *pool, int box) {
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// q as [token][head][dim], in boxes of a group's heads of as many tokens as make up 128 rows; the number
-// of tokens, or 0.
+// q as [token][head][dim], in boxes of a group's heads of as many tokens as make up 128 rows; the
+// number of tokens, or 0.
 int query_map(CUtensorMap &map, const TokensArgs &a, const KvView &kv) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
     const int group = a.group.d;

@@ -9,10 +9,13 @@
 //   dx = r (u - h mean(u h) - mean(u)), the last term for LayerNorm only;
 //   dw = sum g h, db = sum g over rows and heads.
 //
-// What bounds it: bytes.  A head is held by G lanes of a warp, eight values each in two runs of
-// four (head_units.cuh), so its sums are log2 G shuffles and every value is read and written
-// once; a group of lanes takes up to kHeadsPer heads of a row, whose loads are in flight
-// together and share the row's angles.
+// What bounds it: bytes, and for rows of several axes or types the instructions beside them.  A head
+// is held by G lanes of a warp, eight values each in two runs of four (head_units.cuh), so its sums
+// are log2 G shuffles and every value is read and written once; a group of lanes takes up to
+// kHeadsPer heads of a row, whose loads are in flight together and share the row's angles.
+// Measured: 4900 rows of 32 heads of 80 to bf16, LayerNorm, two axes 22 us (3.5 TB/s); gradient of 4096
+// rows of 40 heads of 128 48 us (5.3 TB/s); append of 8002 tokens of 28/4 heads of 128, three axes
+// 51 us (4.3 TB/s), of 256 tokens of 32/8 heads 5 us (the host's call).
 #include <initializer_list>
 
 #include "head_units.cuh"
@@ -22,9 +25,11 @@
 namespace wq {
 namespace {
 
+// Heads of a group of lanes: 1, 2 and 4 took 100, 63 and 60 us for an append of 8002 tokens.  Half the
+// lanes and twice the values to a lane, with two heads: 72 in place of 52.
 constexpr int kHeadsPer = 4;
+constexpr int kGradHeads = 2;  // and of the gradient, which holds x and dout: 1, 2, 4 took 64, 48, 59
 constexpr int kThreads = 128;
-constexpr int kGradHeads = 2;
 
 // A lane's units of a head.
 template <int N, int U> struct Held {
@@ -86,8 +91,9 @@ template <int N, int G, int U> struct Lanes {
 #pragma unroll
             for (int h = 0; h < H; ++h) v[h] += __shfl_xor_sync(0xFFFFFFFFu, v[h], o);
     }
-    // x become (x - mu) r by the group's kind of norm (none: as they were); their r.  Values beyond a head are 0 and stay so.  `summed`: any lane of the launch takes a mean;
-    // a warp's lanes may have different kinds and shuffle together.
+    // x become (x - mu) r by the group's kind of norm (none: as they were); their r.  Values beyond a
+    // head are 0 and stay so.  `summed`: any lane of the launch takes a mean; a warp's lanes may
+    // have different kinds and shuffle together.
     template <int H>
     __device__ __forceinline__ void hat(Held<N, U> (&x)[H], int kind, bool summed, float eps,
                                         float (&r)[H]) const {
@@ -253,7 +259,7 @@ struct Roles {
 // nothing is written) and its position on axis 0.
 struct Place1 {
     long long row;
-    int pos, pad;
+    int pos;
 };
 
 template <int DT, typename Q, int N, int G, int U>
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 8 : 1)
             ok = ok && (unsigned)seq < (unsigned)a.n_seq && slot >= 0 && slot < a.n_slots;
             const long long at_row = ok ? kv.row(seq, 0, slot) : -1;
             if (at_row < 0 && slot >= 0) record_status(ax.status, kStBadIndex);
-            s_place[threadIdx.x] = {at_row, w.p[0], 0};
+            s_place[threadIdx.x] = {at_row, w.p[0]};
         }
         if (stages(ax)) stage_angles(ax, s_angles, t0 + row0, rows);
         __syncthreads();
@@ -507,7 +513,7 @@ bool all16(std::initializer_list<const void *> ps, std::initializer_list<long lo
 size_t angle_bytes(const AxesView &ax, const HeadDeal &deal, unsigned groups) {
     if (ax.rot == 0 || ax.straight) return 0;
     const unsigned per = deal.per_row.d, rows = per == 1 ? groups : (groups + per - 2) / per + 1;
-    return (size_t)rows * (ax.rot / 2) * sizeof(float2);  // at most 32 rows of 64, 16 KiB
+    return (size_t)rows * (ax.rot / 2) * sizeof(float2);  // 16 groups, 32 pairs each: 4 KiB at most
 }
 HeadDeal deal_of(int blocks) { return {make_fast_div((uint32_t)blocks), 0u}; }
 int blocks_of(int heads, int per) { return (heads + per - 1) / per; }
@@ -617,7 +623,7 @@ cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n,
         constexpr int per = kThreads / G.value;
         blocks = (deal.count + per - 1) / per;
         if (blocks > (unsigned)kGradBlocks) blocks = kGradBlocks;
-        size_t smem = sums ? (size_t)per * 2 * head_dim * 4 : 0;  // at most 16 KiB
+        size_t smem = sums ? (size_t)per * 2 * head_dim * 4 : 0;  // at most 8 KiB
         if (angle_bytes(ax, deal, per) > smem) smem = angle_bytes(ax, deal, per);
         return launch_pdl(norm_rope_grad_kernel<N.value, G.value, U.value>, dim3(blocks),
                           dim3(kThreads), smem, stream, ax, nv, deal, head_dim, x, x_stride, grad,

@@ -250,6 +250,33 @@ def test_shapes_of_the_deal(kind, qtype, counts, contexts, hq, hkv, d):
     Case(10, counts, contexts, hq, hkv, d, kind, qtype, page=32).run().check()
 
 
+@pytest.mark.parametrize("kind,qtype", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"),
+                                        ("f32", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("tree", [False, True])
+def test_bits_depend_on_nothing_that_is_not_seen(kind, qtype, tree):
+    """Other sequences' queries and caches, rows behind the last sequence and slots that a token does
+    not see: NaN or large, they change no bit."""
+    c = Case(12, [40, 170], [90, 300], 4, 2, 64, kind, qtype, tree=tree, extra=9).run()
+    first = c.out.clone(), c.lse.clone()
+    c.q[40:] = float("nan")                    # the second sequence and the rows behind
+    c.out.fill_(9), c.lse.fill_(9)
+    c.run(c.out, c.lse)
+    assert torch.equal(c.out[:40], first[0][:40]) and torch.equal(c.lse[:40], first[1][:40])
+    c = Case(12, [40, 170], [90, 300], 4, 2, 64, kind, qtype, tree=tree, extra=9)
+    for value in (float("nan"), 1e4, float("inf")):
+        for s, j in ((0, 90 + 30), (1, 300 + 150), (1, 300 + 100)):
+            for pool in c.cache.pools:
+                pool[int(c.cache.pages[s, j // 16]), :, j % 16] = value
+        c.run()
+        for t in range(c.m):
+            s = int(t >= 40)
+            j = t - 40 * s
+            hidden = [30] if s == 0 else [150, 100]
+            sees = [b for b in hidden if (b in c.tree[t] if tree else b <= j)]
+            if not sees:
+                assert torch.equal(c.out[t], first[0][t]) and torch.equal(c.lse[t], first[1][t]), t
+
+
 def test_workspaces_cover_what_is_asked():
     """No more bytes are touched than the size says, for the sizes around a row tile."""
     for kind, qtype in (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")):
