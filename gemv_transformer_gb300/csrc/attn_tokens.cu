@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // four dims of a row at a time, with the loads of kAtOnce parts in flight.  (5 us of a call.)
 constexpr int kAtOnce = 8;
 __global__ void __launch_bounds__(256)
-    attn_parts_kernel(TokensArgs a, KvView kv, int rt, int dp, int grid) {
+    attn_parts_kernel(TokensArgs a, KvView kv, int passes, int rt, int dp, int grid) {
     // What follows is let in when this is over: a next call's blocks, let in early, would take the
     // places of this one's (41 us instead of 24 for 4 sequences of 16 nodes, one call after another).
     pdl_wait();
@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(256)
     const Seq q = tile.q;
     const int rows = min(rt, q.count * group - tile.row0);
     const TypedOut out{a.out, a.out_type};
-    for (int at = blockIdx.y * 256 + threadIdx.x; at < rt * (kv.head_dim / 4);
-         at += gridDim.y * 256) {
+    const int head = p.head / passes, dim0 = p.head % passes * dp;
+    const int dims = min(dp, kv.head_dim - dim0);
+    for (int at = blockIdx.y * 256 + threadIdx.x; at < rt * (dims / 4); at += gridDim.y * 256) {
         const int row = at % rt, c = at / rt;  // rt is a power of two
         if (row >= rows) continue;
         float m = -INFINITY, l = 0.f;
@@ -207,10 +208,10 @@ __global__ void __launch_bounds__(256)
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int rr = tile.row0 + row, j = a.group.div(rr), g = rr - j * group;
-        const int t = q.t0 + j, h = p.head * group + g;
-        out.put4(t * a.out_stride + (long long)h * kv.head_dim + 4 * c,
+        const int t = q.t0 + j, h = head * group + g;
+        out.put4(t * a.out_stride + (long long)h * kv.head_dim + dim0 + 4 * c,
                  make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (a.lse && c == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+        if (a.lse && dim0 + c == 0) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
     }
 }
 
@@ -587,14 +588,14 @@ cudaError_t launch_rows(const TokensArgs &a, const KvView &kv, const DeviceInfo 
     if (err != cudaSuccess) return err;
     const int grid = S::kGrid;
     TokensArgs b = a;
-    b.join_inside = joins_inside(a, kv, S::RT, grid);
+    b.join_inside = joins_inside(a, kv.n_heads, S::RT, grid);
     // A row tile's start and end as a key tile: as two, three and four packed documents took 76, 84
     // and 84 us instead of 69.
-    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, grid, 1, stream);
+    err = launch_attn_plan(b, kv.n_heads, S::RT, S::KT, DP, grid, 1, stream);
     if (err != cudaSuccess) return err;
     err = launch_pdl(attn_rows_kernel<T, DP, R>, dim3(grid), dim3(256), S::kSmem, stream, b, kv);
     if (err != cudaSuccess || b.join_inside) return err;
-    return launch_attn_parts(b, kv, S::RT, DP, grid, stream);
+    return launch_attn_parts(b, kv, 1, S::RT, DP, grid, stream);
 }
 template <typename T>
 cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
@@ -614,17 +615,17 @@ cudaError_t launch_rows_type(const TokensArgs &a, const KvView &kv, const Device
 
 }  // namespace
 
-cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
-                             int grid, int row_cost, cudaStream_t stream) {
-    return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, kv.n_heads, rt,
-                      kt, dp, grid, row_cost);
+cudaError_t launch_attn_plan(const TokensArgs &a, int heads, int rt, int kt, int dp, int grid,
+                             int row_cost, cudaStream_t stream) {
+    return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, heads, rt, kt, dp,
+                      grid, row_cost);
 }
 
-cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
-                              cudaStream_t stream) {
-    const int blocks = (rt * (kv.head_dim / 4) + 255) / 256;
+cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int passes, int rt, int dp,
+                              int grid, cudaStream_t stream) {
+    const int blocks = (rt * (min(dp, kv.head_dim) / 4) + 255) / 256;
     return launch_pdl(attn_parts_kernel, dim3(grid - 1, blocks < 8 ? blocks : 8), dim3(256), 0,
-                      stream, a, kv, rt, dp, grid);
+                      stream, a, kv, passes, rt, dp, grid);
 }
 
 }  // namespace tok

@@ -244,15 +244,16 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // row_cost: a row tile's start and end count as so many key tiles.
-cudaError_t launch_attn_plan(const TokensArgs &a, const KvView &kv, int rt, int kt, int dp,
-                             int grid, int row_cost, cudaStream_t stream);
+// heads: kv heads, times the passes over a head's dims.
+cudaError_t launch_attn_plan(const TokensArgs &a, int heads, int rt, int kt, int dp, int grid,
+                             int row_cost, cudaStream_t stream);
 // Does a row tile have few parts: are there as many row tiles as CTAs?  (That goes by the rows
 // alone; lengths are known on the device only.)
-inline bool joins_inside(const TokensArgs &a, const KvView &kv, int rt, int grid) {
-    return (long long)a.n_tok * a.group.d / rt * kv.n_heads >= grid;
+inline bool joins_inside(const TokensArgs &a, int heads, int rt, int grid) {
+    return (long long)a.n_tok * a.group.d / rt * heads >= grid;
 }
-cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int rt, int dp, int grid,
-                              cudaStream_t stream);
+cudaError_t launch_attn_parts(const TokensArgs &a, const KvView &kv, int passes, int rt, int dp,
+                              int grid, cudaStream_t stream);
 
 // The tensor-core kernels (attn_tokens_tc.cu).
 bool tokens_tc_takes(const KvView &kv, int q_type);

@@ -54,20 +54,24 @@ constexpr int kMisc = 3 * 1024;    // barriers and small arrays, before the 1024
 // Tensor memory columns of a warpgroup (256 each).
 constexpr uint32_t kColS = 0, kColP0 = 0, kColP1 = 64, kColP2 = 96, kColT = 128;
 
-template <int DP_, int TERMS_, bool PAIR_, int ET_> struct TcShape {
-    static constexpr int DP = DP_, TERMS = TERMS_, ET = ET_;
+template <int DQ_, int TERMS_, bool PAIR_, int ET_> struct TcShape {
+    // Dims of q and k, and of v in a pass: heads of 256 take two passes over the slots, each for half
+    // of the output (all of it and the scores of two warpgroups do not fit tensor memory).
+    static constexpr int DQ = DQ_, DP = DQ > 128 ? 128 : DQ, kPasses = DQ / DP;
+    static constexpr int TERMS = TERMS_, ET = ET_;
     static constexpr bool PAIR = PAIR_;
-    static constexpr int KT = TERMS == 1 ? 128 : 64;
+    static constexpr int KT = TERMS == 1 && DQ <= 128 ? 128 : 64;
     static constexpr int RT = PAIR ? 256 : 128;
     static constexpr int kHalf = 128 * 128;            // 128 rows of 64 dims
-    static constexpr int kQTerm = RT * DP * 2;
+    static constexpr int kQTerm = RT * DQ * 2;
     static constexpr int kStage = TERMS * kQTerm;
-    static constexpr int kSlot = KT * DP * 2;          // a k or a v tile
-    static constexpr int kFit = (kSmemMost - kMisc - kStage) / kSlot;
+    static constexpr int kSlotK = KT * DQ * 2, kSlotV = KT * DP * 2;  // a k and a v tile
     static constexpr int kAhead = PAIR ? 1 : 0;        // a step brings v of tile g, k of g + kAhead
-    static constexpr int NV = (kFit - kAhead) / 2 < kMostV ? (kFit - kAhead) / 2 : kMostV;
+    static constexpr int kFit =
+        (kSmemMost - kMisc - kStage - kAhead * kSlotK) / (kSlotK + kSlotV);
+    static constexpr int NV = kFit < kMostV ? kFit : kMostV;
     static constexpr int NK = NV + kAhead;             // places for v and k tiles
-    static constexpr int kSmem = kMisc + kStage + (NK + NV) * kSlot;
+    static constexpr int kSmem = kMisc + kStage + NK * kSlotK + NV * kSlotV;
     static_assert(NV >= 2, "a tile for each warpgroup");
 };
 
@@ -285,18 +289,20 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
                            bool is_v, int box, const Room &room, const Ctx &c) {
     const int lane = threadIdx.x & 31, from = lane * box;
     const bool mine = lane < S::KT / box;
+    const int chunks = (is_v ? S::DP : S::DQ) / 64;  // boxes of 64 dims
     struct Box {
-        int page, row, head;
+        int page, row, head, dim;
         bool live;
         uint32_t lost;   // of all lanes
         uint32_t bytes;
     };
     Stream<S> in(room);
     auto ask = [&]() {
-        Box x{-2, 0, 0, false, 0u, 0u};
+        Box x{-2, 0, 0, 0, false, 0u, 0u};
         if (!in.more) return x;
         const int j = in.kt * S::KT + from;
-        x.head = in.st.head;
+        x.head = in.st.head / S::kPasses;
+        if (is_v) x.dim = in.st.head % S::kPasses * S::DP;
         x.row = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
         if (mine) x.page = page_of(kv, in.seq, j, in.len);
         return x;
@@ -304,18 +310,20 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
     auto settle = [&](Box &x) {  // once the page is there
         x.live = (unsigned)x.page < (unsigned)kv.n_pages;
         x.lost = __ballot_sync(0xFFFFFFFFu, !x.live && x.page != -2);
-        x.bytes = __popc(__ballot_sync(0xFFFFFFFFu, x.live)) * box * 128 * (S::DP / 64);
+        x.bytes = __popc(__ballot_sync(0xFFFFFFFFu, x.live)) * box * 128 * chunks;
     };
     auto copy = [&](const Box &x, uint32_t to, uint64_t *bar) {
         if (!x.live) return;
 #pragma unroll
-        for (int h = 0; h < S::DP / 64; ++h)
+        for (int h = 0; h < S::DQ / 64; ++h) {
+            if (h == chunks) break;
             asm volatile(
                 "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + from * 128 + h * (S::KT * 128)),
-                "l"(reinterpret_cast<uint64_t>(map)), "r"(64 * h), "r"(x.row), "r"(x.head),
+                "l"(reinterpret_cast<uint64_t>(map)), "r"(x.dim + 64 * h), "r"(x.row), "r"(x.head),
                 "r"(x.page), "r"(smem_addr(bar))
                 : "memory");
+        }
     };
     const bool ahead = S::kAhead && !is_v;
     bool here = in.more;  // is there a step
@@ -354,7 +362,8 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
             mbar_arrive_expect_tx(&c.sh->full[slot], x.bytes);
         }
         __syncwarp();
-        copy(x, is_v ? c.v_ring + slot * S::kSlot : c.k_ring + (g + S::kAhead) % S::NK * S::kSlot,
+        copy(x, is_v ? c.v_ring + slot * S::kSlotV
+                     : c.k_ring + (g + S::kAhead) % S::NK * S::kSlotK,
              &c.sh->full[slot]);
         here = ahead ? some : in.more;
     }
@@ -375,25 +384,27 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
 // live ones and in pages out of range are zeros.
 template <typename S>
 __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
-    constexpr int kLanes = S::DP / 8;         // 16-byte chunks, a lane each, of a row
-    constexpr int kRows = 32 / kLanes;        // rows of a warp's copy
     constexpr int kGroups = S::KT / 32;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoft / 32 - 1;
-    const int chunk = lane % kLanes;
-    const bool in_dim = chunk * 8 < kv.head_dim;
     struct Rows {
-        int page[kGroups], j, head;  // of this lane's rows: lane + 32 i
+        int page[kGroups], j, head, dim;  // of this lane's rows: lane + 32 i
     };
     Stream<S> in(room);
     auto ask = [&]() {
         Rows x;
-        x.j = in.kt * S::KT + lane, x.head = in.st.head;
+        x.j = in.kt * S::KT + lane, x.head = in.st.head / S::kPasses;
+        x.dim = in.st.head % S::kPasses * S::DP;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
             x.page[i] = in.more ? page_of(kv, in.seq, x.j + 32 * i, in.len) : -2;
         return x;
     };
-    auto copy = [&](const Rows &x, const char *pool, uint32_t ring) {
+    // `dims` of the rows' dims from `dim` on, to a tile.
+    auto copy = [&](const Rows &x, const char *pool, uint32_t ring, auto dims, int dim) {
+        constexpr int kLanes = dims / 8;    // 16-byte chunks, a lane each, of a row
+        constexpr int kRows = 32 / kLanes;  // rows of a warp's copy
+        const int chunk = lane % kLanes;
+        const bool in_dim = dim + chunk * 8 < kv.head_dim;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int j = x.j + 32 * i;
@@ -409,14 +420,16 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
                 const bool live = from >= 0 && in_dim;
                 cp16(ring + (chunk >> 3) * (S::KT * 128) + row * 128 +
                          (((chunk & 7) ^ (row & 7)) << 4),
-                     pool + (live ? from + chunk * 16 : 0), live);
+                     pool + (live ? from + dim * 2 + chunk * 16 : 0), live);
             }
         }
     };
     if (!in.more) return;
+    constexpr std::integral_constant<int, S::DQ> dq{};
+    constexpr std::integral_constant<int, S::DP> dp{};
     Rows cur = ask();
     if (S::kAhead) {
-        copy(cur, kv.k, c.k_ring);
+        copy(cur, kv.k, c.k_ring, dq, 0);
         cp_commit();
         cp_wait<0>();
         fence_proxy_async_smem();
@@ -457,8 +470,8 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
             }
         }
         if (!S::kAhead || some)
-            copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlot);
-        copy(v, kv.v, c.v_ring + slot * S::kSlot);
+            copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlotK, dq, 0);
+        copy(v, kv.v, c.v_ring + slot * S::kSlotV, dp, v.dim);
         cp_commit();
         if (g + 1 - landed >= (uint32_t)S::NV) {
             cp_wait<S::NV - 1>();
@@ -475,7 +488,7 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
 template <typename S>
 __device__ void load_queries(const TokensArgs &a, const KvView &kv, const CUtensorMap *q_map,
                              int q_box, const Room &room, const Ctx &c) {
-    constexpr int kChunks = S::DP / 8;
+    constexpr int kChunks = S::DQ / 8;
     const int lane = threadIdx.x & 31, group = a.group.d;
     Walk walk(room, blockIdx.x);
     Stretch st;
@@ -484,19 +497,20 @@ __device__ void load_queries(const TokensArgs &a, const KvView &kv, const CUtens
         if (st.k0 == st.k1) continue;
         const Tile *const tile = room.tiles + st.tile;
         const int row0 = tile->row0, t0 = tile->q.t0, rows = tile->q.count * group - row0;
+        const int head0 = st.head / S::kPasses * group;
         if (n > 0 && !c.warp_wait(&c.sh->q_free, (n - 1) & 1)) break;
         if (q_box) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&c.sh->q_ready, S::kQTerm);
 #pragma unroll
-                for (int x = 0; x < S::RT / 128 * (S::DP / 64); ++x) {
-                    const int r = x / (S::DP / 64) * 128, h = x % (S::DP / 64);
+                for (int x = 0; x < S::RT / 128 * (S::DQ / 64); ++x) {
+                    const int r = x / (S::DQ / 64) * 128, h = x % (S::DQ / 64);
                     asm volatile(
                         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx"
                         "::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                            c.stage + r * (S::DP * 2) + h * S::kHalf),
+                            c.stage + r * (S::DQ * 2) + h * S::kHalf),
                         "l"(reinterpret_cast<uint64_t>(q_map)), "r"(64 * h),
-                        "r"(st.head * group), "r"(t0 + (int)a.group.div(row0 + r)),
+                        "r"(head0), "r"(t0 + (int)a.group.div(row0 + r)),
                         "r"(smem_addr(&c.sh->q_ready))
                         : "memory");
                 }
@@ -511,9 +525,9 @@ __device__ void load_queries(const TokensArgs &a, const KvView &kv, const CUtens
             const bool live = r < rows && ch * 8 < kv.head_dim;
             const int rr = row0 + r, j = a.group.div(live ? rr : 0), h = rr - j * group;
             const long long at = (t0 + j) * a.q_stride +
-                                 (long long)(st.head * group + h) * kv.head_dim + ch * 8;
+                                 (long long)(head0 + h) * kv.head_dim + ch * 8;
             // Row r of its tile of 128 rows.
-            cp16(c.stage + (r >> 7) * (128 * S::DP * 2) + (ch >> 3) * S::kHalf + (r & 127) * 128 +
+            cp16(c.stage + (r >> 7) * (128 * S::DQ * 2) + (ch >> 3) * S::kHalf + (r & 127) * 128 +
                      (((ch & 7) ^ (r & 7)) << 4),
                  static_cast<const uint16_t *>(a.q) + (live ? at : 0), live);
         }
@@ -553,14 +567,14 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
         return true;
     };
     auto scores = [&](int wg, uint32_t tile) {  // S of a warpgroup from the tile's k
-        const uint32_t k = desc_low(c.k_ring + tile % S::NK * S::kSlot, 16);
+        const uint32_t k = desc_low(c.k_ring + tile % S::NK * S::kSlotK, 16);
         uint32_t accum = 0;
 #pragma unroll
         for (int t = S::TERMS - 1; t >= 0; --t) {
             const uint32_t q =
-                desc_low(c.stage + t * S::kQTerm + (S::PAIR ? wg * (128 * S::DP * 2) : 0), 16);
+                desc_low(c.stage + t * S::kQTerm + (S::PAIR ? wg * (128 * S::DQ * 2) : 0), 16);
 #pragma unroll
-            for (int h = 0; h < S::DP / 64; ++h)
+            for (int h = 0; h < S::DQ / 64; ++h)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     mma_ss(tmem + wg * 256 + kColS, q + (h * S::kHalf + 32 * s >> 4),
@@ -573,7 +587,7 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
     // P V of a warpgroup from the tile's v.  That it is over shows by the next scores; `last` has
     // none.
     auto values = [&](int wg, uint32_t tile, bool last) {
-        const uint32_t v = desc_low(c.v_ring + tile % S::NV * S::kSlot, S::KT * 128);
+        const uint32_t v = desc_low(c.v_ring + tile % S::NV * S::kSlotV, S::KT * 128);
         uint32_t accum = S::TERMS == 1;  // on top of the output, which began as zeros
         if (!c.wait(&c.sh->p_ready[wg], taken >> wg & 1)) return false;
         taken ^= 1u << wg;
@@ -762,7 +776,7 @@ template <typename S> struct Row {
     const KvView &kv;
     const Ctx &c;
     const Tile *tile;    // of the stretch
-    int head;
+    int head, dim0;      // kv head, first dim of the pass
     const uint32_t tm;   // the warpgroup's columns, this warp's lanes
     const float to_log2;
     uint32_t turns = 0;  // parities of the meetings of both and of this one, and of look()
@@ -1121,12 +1135,13 @@ template <typename S> struct Row {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] *= inv;
-        const long long to = t * a.out_stride + (long long)h * kv.head_dim + e;
+        const int left = kv.head_dim - dim0 - e;  // dims of the head from here on
+        const long long to = t * a.out_stride + (long long)h * kv.head_dim + dim0 + e;
         if (a.out_type == kF32) {
             float *const p = static_cast<float *>(a.out) + to;
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
-                if (e + k >= kv.head_dim) break;
+                if (k >= left) break;
                 reinterpret_cast<float4 *>(p + k)[0] =
                     make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 reinterpret_cast<float4 *>(p + k)[1] =
@@ -1140,7 +1155,7 @@ template <typename S> struct Row {
             if (a.wide_out) {  // 32 bytes at a time: whole sectors
 #pragma unroll
                 for (int k = 0; k < 16; k += 8) {
-                    if (e + 2 * k >= kv.head_dim) break;
+                    if (2 * k >= left) break;
                     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                                      p + 2 * k),
                                  "r"(w[k]), "r"(w[k + 1]), "r"(w[k + 2]), "r"(w[k + 3]),
@@ -1150,13 +1165,13 @@ template <typename S> struct Row {
             } else {
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
-                    if (e + 2 * k >= kv.head_dim) break;
+                    if (2 * k >= left) break;
                     *reinterpret_cast<uint4 *>(p + 2 * k) =
                         make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
                 }
             }
         }
-        if (e == 0 && a.lse) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
+        if (dim0 + e == 0 && a.lse) a.lse[(long long)t * a.h_q + h] = lse_of(m, l);
     }
 };
 
@@ -1175,7 +1190,7 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
     while (walk.next(st)) {
         __syncwarp();
         w.tile = room.tiles + st.tile;
-        w.head = st.head;
+        w.head = st.head / S::kPasses, w.dim0 = st.head % S::kPasses * S::DP;
         const int n = st.k1 - st.k0;
         int j, h;
         // The row's maximum in use and its sum; rows beyond the tile's have weights of 0.
@@ -1192,10 +1207,15 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
             const int j0 = (st.k0 + i) * KT;
             // What a border tile needs is found while its scores are under way.
             if (!c.warp_wait(&sh->full[vs], g / S::NV & 1)) return;
-            const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
-            const bool mixed =
-                j0 < lo || j0 + KT > hi || (none.x | none.y | none.z | none.w) != 0;
-            const uint32_t v_at = c.v_ring + vs * S::kSlot;
+            uint32_t lost = 0;
+            if constexpr (kChunks == 4) {
+                const uint4 none = *reinterpret_cast<const uint4 *>(sh->none[vs]);
+                lost = none.x | none.y | none.z | none.w;
+            } else {
+                lost = sh->none[vs][0] | sh->none[vs][1];
+            }
+            const bool mixed = j0 < lo || j0 + KT > hi || lost;
+            const uint32_t v_at = c.v_ring + vs * S::kSlotV;
             uint32_t in[kChunks] = {};
             typename R::Odd odd{};
             if (mixed) {
@@ -1380,7 +1400,7 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
     while (walk.next(st)) {
         __syncwarp();
         w.tile = room.tiles + st.tile;
-        w.head = st.head;
+        w.head = st.head / S::kPasses, w.dim0 = st.head % S::kPasses * S::DP;
         const int n = st.k1 - st.k0;
         float o[DP];
 #pragma unroll
@@ -1417,7 +1437,7 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) lost |= sh->none[vs][ch];
             const bool mixed = j0 < lo || j0 + KT > hi || lost;
-            const uint32_t v_at = c.v_ring + vs * S::kSlot;
+            const uint32_t v_at = c.v_ring + vs * S::kSlotV;
             typename Row<S>::Odd odd{};
             if (mixed && !w.look(v_at, odd)) return;
             if (!c.warp_wait(&sh->s_full[w.wg()], mine & 1)) return;
@@ -1525,7 +1545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     c.k_ring = c.stage + S::kStage;
-    c.v_ring = c.k_ring + S::NK * S::kSlot;
+    c.v_ring = c.k_ring + S::NK * S::kSlotK;
     c.limit = a.wait_limit;
     c.status = a.status;
     const int warp = threadIdx.x >> 5;
@@ -1611,9 +1631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Two row tiles of 128 where the sequences have more rows than one on average.
-bool pairs_rows(int n_seq, int n_tok, int group) {
-    return (long long)n_tok * group > 128ll * n_seq;
+// Two row tiles of 128 where the sequences have more rows than one on average, and fit.
+bool pairs_rows(int n_seq, int n_tok, int group, int head_dim) {
+    return head_dim <= 128 && (long long)n_tok * group > 128ll * n_seq;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1674,18 +1694,20 @@ int box_of(const KvView &kv, int kt) {
     return box >= 8 ? box : 0;
 }
 
-template <int DP, int TERMS, bool PAIR, int ET>
+template <int DQ, int TERMS, bool PAIR, int ET>
 cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                          cudaStream_t stream) {
-    using S = TcShape<DP, TERMS, PAIR, ET>;
+    using S = TcShape<DQ, TERMS, PAIR, ET>;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = ensure_smem(attn_tokens_tc_kernel<S>, S::kSmem, dev, raised);
     if (err != cudaSuccess) return err;
     TokensArgs b = a;
-    b.join_inside = joins_inside(a, kv, S::RT, kGrid);
+    const int heads = kv.n_heads * S::kPasses;
+    b.join_inside = joins_inside(a, heads, S::RT, kGrid);
     // What a row tile's start and end cost in key tiles (a prompt of 8192 tokens as 2, 3, 4: 438, 419,
     // 421 us; trees of f32 queries as 1, 2, 3: 123, 122, 117).
-    err = launch_attn_plan(b, kv, S::RT, S::KT, DP, kGrid, PAIR || TERMS > 1 ? 3 : 2, stream);
+    err = launch_attn_plan(b, heads, S::RT, S::KT, S::DP, kGrid, PAIR || TERMS > 1 ? 3 : 2,
+                           stream);
     if (err != cudaSuccess) return err;
     CUtensorMap k_map{}, v_map{}, q_map{};
     const int q_box = query_map(q_map, a, kv);
@@ -1694,36 +1716,40 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, b, kv,
                      k_map, v_map, q_map, box, q_box);
     if (err != cudaSuccess || b.join_inside) return err;
-    return launch_attn_parts(b, kv, S::RT, DP, kGrid, stream);
+    return launch_attn_parts(b, kv, S::kPasses, S::RT, S::DP, kGrid, stream);
 }
-template <int DP>
+template <int DQ, bool PAIR>
+cudaError_t launch_16(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
+                      cudaStream_t stream) {
+    return kv.dtype == kBF16 ? launch_shape<DQ, 1, PAIR, kBF16>(a, kv, dev, stream)
+                             : launch_shape<DQ, 1, PAIR, kF16>(a, kv, dev, stream);
+}
+template <int DQ>
 cudaError_t launch_dim(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                        cudaStream_t stream) {
-    if (a.q_type == kF32) return launch_shape<DP, 3, false, kBF16>(a, kv, dev, stream);
-    const bool pair = pairs_rows(a.n_seq, a.n_tok, a.group.d);
-    if (kv.dtype == kBF16)
-        return pair ? launch_shape<DP, 1, true, kBF16>(a, kv, dev, stream)
-                    : launch_shape<DP, 1, false, kBF16>(a, kv, dev, stream);
-    return pair ? launch_shape<DP, 1, true, kF16>(a, kv, dev, stream)
-                : launch_shape<DP, 1, false, kF16>(a, kv, dev, stream);
+    if (a.q_type == kF32) return launch_shape<DQ, 3, false, kBF16>(a, kv, dev, stream);
+    return pairs_rows(a.n_seq, a.n_tok, a.group.d, kv.head_dim)
+               ? launch_16<DQ, true>(a, kv, dev, stream)
+               : launch_16<DQ, false>(a, kv, dev, stream);
 }
 
 }  // namespace
 
 bool tokens_tc_takes(const KvView &kv, int q_type) {
-    if (kv.head_dim > 128) return false;
-    return kv.dtype == kBF16 ? q_type != kF16 : kv.dtype == kF16 && q_type == kF16;
+    if (q_type == kv.dtype) return q_type != kF32;
+    return kv.dtype == kBF16 && q_type == kF32 && kv.head_dim <= 128;
 }
 
 void tokens_tc_shape(int n_seq, int n_tok, int group, int q_type, int head_dim, int &rt, int &dp,
                      int &grid) {
-    rt = q_type != kF32 && pairs_rows(n_seq, n_tok, group) ? 256 : 128;
+    rt = q_type != kF32 && pairs_rows(n_seq, n_tok, group, head_dim) ? 256 : 128;
     dp = head_dim <= 64 ? 64 : 128;
     grid = kGrid;
 }
 
 cudaError_t launch_tokens_tc(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                              cudaStream_t stream) {
+    if (kv.head_dim > 128) return launch_16<256, false>(a, kv, dev, stream);
     return kv.head_dim <= 64 ? launch_dim<64>(a, kv, dev, stream)
                              : launch_dim<128>(a, kv, dev, stream);
 }

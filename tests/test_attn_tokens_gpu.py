@@ -111,7 +111,7 @@ class Case:
         assert (got[:, self.hq * self.d:] == 9).all()
         got = got[:self.m, :self.hq * self.d].reshape(self.m, self.hq, self.d)
         lse = lse[:self.m]
-        tensor = self.qtype != "f32" and self.qtype == self.kind and self.d <= 128
+        tensor = self.qtype != "f32" and self.qtype == self.kind
         n = w["n"][:, None]
         ex = (self.d + 8) * U * w["sx"] + 8 * U * w["mx"]
         if self.softcap:
