@@ -289,7 +289,8 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
                            bool is_v, int box, const Room &room, const Ctx &c) {
     const int lane = threadIdx.x & 31, from = lane * box;
     const bool mine = lane < S::KT / box;
-    const int chunks = (is_v ? S::DP : S::DQ) / 64;  // boxes of 64 dims
+    // Boxes of 64 dims; known without is_v where there is one pass.
+    const int chunks = (S::kPasses > 1 && is_v ? S::DP : S::DQ) / 64;
     struct Box {
         int page, row, head, dim;
         bool live;
@@ -302,7 +303,7 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
         if (!in.more) return x;
         const int j = in.kt * S::KT + from;
         x.head = in.st.head / S::kPasses;
-        if (is_v) x.dim = in.st.head % S::kPasses * S::DP;
+        if (S::kPasses > 1 && is_v) x.dim = in.st.head % S::kPasses * S::DP;
         x.row = j - (int)(kv.page_size.div((uint32_t)j) * kv.page_size.d);
         if (mine) x.page = page_of(kv, in.seq, j, in.len);
         return x;
@@ -316,11 +317,11 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
         if (!x.live) return;
 #pragma unroll
         for (int h = 0; h < S::DQ / 64; ++h) {
-            if (h == chunks) break;
+            if (S::kPasses > 1 && h == chunks) break;
             asm volatile(
                 "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + from * 128 + h * (S::KT * 128)),
-                "l"(reinterpret_cast<uint64_t>(map)), "r"(x.dim + 64 * h), "r"(x.row), "r"(x.head),
+                "l"(reinterpret_cast<uint64_t>(map)), "r"((S::kPasses > 1 ? x.dim : 0) + 64 * h), "r"(x.row), "r"(x.head),
                 "r"(x.page), "r"(smem_addr(bar))
                 : "memory");
         }
@@ -384,27 +385,26 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
 // live ones and in pages out of range are zeros.
 template <typename S>
 __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &room, const Ctx &c) {
+    static_assert(S::kPasses == 1, "all of a head's dims");
+    constexpr int kLanes = S::DP / 8;         // 16-byte chunks, a lane each, of a row
+    constexpr int kRows = 32 / kLanes;        // rows of a warp's copy
     constexpr int kGroups = S::KT / 32;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kSoft / 32 - 1;
+    const int chunk = lane % kLanes;
+    const bool in_dim = chunk * 8 < kv.head_dim;
     struct Rows {
-        int page[kGroups], j, head, dim;  // of this lane's rows: lane + 32 i
+        int page[kGroups], j, head;  // of this lane's rows: lane + 32 i
     };
     Stream<S> in(room);
     auto ask = [&]() {
         Rows x;
-        x.j = in.kt * S::KT + lane, x.head = in.st.head / S::kPasses;
-        x.dim = in.st.head % S::kPasses * S::DP;
+        x.j = in.kt * S::KT + lane, x.head = in.st.head;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
             x.page[i] = in.more ? page_of(kv, in.seq, x.j + 32 * i, in.len) : -2;
         return x;
     };
-    // `dims` of the rows' dims from `dim` on, to a tile.
-    auto copy = [&](const Rows &x, const char *pool, uint32_t ring, auto dims, int dim) {
-        constexpr int kLanes = dims / 8;    // 16-byte chunks, a lane each, of a row
-        constexpr int kRows = 32 / kLanes;  // rows of a warp's copy
-        const int chunk = lane % kLanes;
-        const bool in_dim = dim + chunk * 8 < kv.head_dim;
+    auto copy = [&](const Rows &x, const char *pool, uint32_t ring) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int j = x.j + 32 * i;
@@ -420,16 +420,14 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
                 const bool live = from >= 0 && in_dim;
                 cp16(ring + (chunk >> 3) * (S::KT * 128) + row * 128 +
                          (((chunk & 7) ^ (row & 7)) << 4),
-                     pool + (live ? from + dim * 2 + chunk * 16 : 0), live);
+                     pool + (live ? from + chunk * 16 : 0), live);
             }
         }
     };
     if (!in.more) return;
-    constexpr std::integral_constant<int, S::DQ> dq{};
-    constexpr std::integral_constant<int, S::DP> dp{};
     Rows cur = ask();
     if (S::kAhead) {
-        copy(cur, kv.k, c.k_ring, dq, 0);
+        copy(cur, kv.k, c.k_ring);
         cp_commit();
         cp_wait<0>();
         fence_proxy_async_smem();
@@ -470,8 +468,8 @@ __device__ void load_rows(const TokensArgs &a, const KvView &kv, const Room &roo
             }
         }
         if (!S::kAhead || some)
-            copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlotK, dq, 0);
-        copy(v, kv.v, c.v_ring + slot * S::kSlotV, dp, v.dim);
+            copy(S::kAhead ? cur : v, kv.k, c.k_ring + (g + S::kAhead) % S::NK * S::kSlotK);
+        copy(v, kv.v, c.v_ring + slot * S::kSlotV);
         cp_commit();
         if (g + 1 - landed >= (uint32_t)S::NV) {
             cp_wait<S::NV - 1>();
@@ -776,7 +774,7 @@ template <typename S> struct Row {
     const KvView &kv;
     const Ctx &c;
     const Tile *tile;    // of the stretch
-    int head, dim0;      // kv head, first dim of the pass
+    int head, pass;      // kv head, pass over its dims
     const uint32_t tm;   // the warpgroup's columns, this warp's lanes
     const float to_log2;
     uint32_t turns = 0;  // parities of the meetings of both and of this one, and of look()
@@ -1135,6 +1133,7 @@ template <typename S> struct Row {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] *= inv;
+        const int dim0 = S::kPasses > 1 ? pass * DP : 0;
         const int left = kv.head_dim - dim0 - e;  // dims of the head from here on
         const long long to = t * a.out_stride + (long long)h * kv.head_dim + dim0 + e;
         if (a.out_type == kF32) {
@@ -1190,7 +1189,7 @@ __device__ void softmax_16(const TokensArgs &a, const KvView &kv, const Room &ro
     while (walk.next(st)) {
         __syncwarp();
         w.tile = room.tiles + st.tile;
-        w.head = st.head / S::kPasses, w.dim0 = st.head % S::kPasses * S::DP;
+        w.head = st.head / S::kPasses, w.pass = st.head % S::kPasses;
         const int n = st.k1 - st.k0;
         int j, h;
         // The row's maximum in use and its sum; rows beyond the tile's have weights of 0.
@@ -1400,7 +1399,7 @@ __device__ void softmax_32(const TokensArgs &a, const KvView &kv, const Room &ro
     while (walk.next(st)) {
         __syncwarp();
         w.tile = room.tiles + st.tile;
-        w.head = st.head / S::kPasses, w.dim0 = st.head % S::kPasses * S::DP;
+        w.head = st.head / S::kPasses, w.pass = st.head % S::kPasses;
         const int n = st.k1 - st.k0;
         float o[DP];
 #pragma unroll
@@ -1604,7 +1603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kMma + 3) {
                 if constexpr (S::TERMS == 1) load_queries<S>(a, kv, &q_map, q_box, room, c);
             } else if (!box) {
-                load_rows<S>(a, kv, room, c);
+                if constexpr (S::kPasses == 1) load_rows<S>(a, kv, room, c);
             } else {
                 const bool is_v = warp == kMma + 2;
                 load_boxes<S>(a, kv, is_v ? &v_map : &k_map, is_v, box, room, c);
@@ -1650,6 +1649,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     }
     return fn;
 }
+bool strides_fit(const KvView &kv) {  // a tensor map
+    return (kv.token_stride | kv.head_stride | kv.page_stride) < (1ll << 40);
+}
 // A pool as [page][head][row][dim] in boxes of `box` rows of 64 dims, zeros beyond head_dim.
 bool pool_map(CUtensorMap &map, const KvView &kv, char *pool, int box) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
@@ -1657,8 +1659,7 @@ bool pool_map(CUtensorMap &map, const KvView &kv, char *pool, int box) {
                                 (cuuint64_t)kv.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)kv.token_stride, (cuuint64_t)kv.head_stride,
                                    (cuuint64_t)kv.page_stride};
-    for (cuuint64_t st : strides)
-        if (st >= (1ull << 40)) return false;
+    if (!strides_fit(kv)) return false;
     const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
     return encode && encode(&map,
                             kv.dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1713,6 +1714,7 @@ cudaError_t launch_shape(const TokensArgs &a, const KvView &kv, const DeviceInfo
     const int q_box = query_map(q_map, a, kv);
     int box = box_of(kv, S::KT);
     if (box && !(pool_map(k_map, kv, kv.k, box) && pool_map(v_map, kv, kv.v, box))) box = 0;
+    if (S::kPasses > 1 && !box) return cudaErrorNotSupported;
     err = launch_pdl(attn_tokens_tc_kernel<S>, dim3(kGrid), dim3(kThreads), S::kSmem, stream, b, kv,
                      k_map, v_map, q_map, box, q_box);
     if (err != cudaSuccess || b.join_inside) return err;
@@ -1736,7 +1738,9 @@ cudaError_t launch_dim(const TokensArgs &a, const KvView &kv, const DeviceInfo &
 }  // namespace
 
 bool tokens_tc_takes(const KvView &kv, int q_type) {
-    if (q_type == kv.dtype) return q_type != kF32;
+    // Heads above 128 only where pages are boxes.
+    if (q_type == kv.dtype)
+        return q_type != kF32 && (kv.head_dim <= 128 || (kv.page_size.d % 8 == 0 && strides_fit(kv)));
     return kv.dtype == kBF16 && q_type == kF32 && kv.head_dim <= 128;
 }
 

@@ -646,10 +646,10 @@ typedef struct {
  * q: q_type (WQ_F32, WQ_BF16, WQ_F16), rows of h_q heads; out: out_type, q_type or WQ_F32;
  * strides in elements.  lse: f32 [n_tok][h_q] or NULL.
  * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products).  16-bit
- * queries over a cache of their type: tensor-core products, in which p is
- * rounded to that type (by half a step: 2^-8 of it for bf16, 2^-11 for f16, whose weights below
- * 2^-24 of the largest are lost), and a sum over n slots may be cut short by n / 16 times 2^-23
- * of it.  All others as f32 queries.
+ * queries over a cache of their type (heads above 128: in pages of a multiple of 8 slots):
+ * tensor-core products, in which p is rounded to that type (by half a step: 2^-8 of it for bf16,
+ * 2^-11 for f16, whose weights below 2^-24 of the largest are lost), and a sum over n slots may be
+ * cut short by n / 16 times 2^-23 of it.  All others as f32 queries.
  * Rows of q at or beyond starts[n_seq] reach no result, and theirs of out are not written.
  * Nothing overlaps out, lse or the workspace.
  * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not

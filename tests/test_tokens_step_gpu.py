@@ -282,6 +282,13 @@ def test_bits_depend_on_nothing_that_is_not_seen(kind, qtype, tree, d):
                 assert torch.equal(c.out[t], first[0][t]) and torch.equal(c.lse[t], first[1][t]), t
 
 
+@pytest.mark.parametrize("page,major", [(7, "head"), (8, "gap"), (24, "token"), (100, "head")])
+def test_pages_of_wide_heads(page, major):
+    for kind in ("bf16", "f16"):
+        Case(13, [20, 35], [210, 91], 4, 2, 256, kind, kind, page, major).run().check()
+        Case(14, [20, 35], [210, 91], 4, 2, 136, kind, kind, page, major, tree=True).run().check()
+
+
 def test_workspaces_cover_what_is_asked():
     """No more bytes are touched than the size says, for the sizes around a row tile."""
     for kind, qtype in (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")):
