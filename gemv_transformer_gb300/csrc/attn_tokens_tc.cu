@@ -13,7 +13,7 @@
 //               m) + T.
 //
 // PAIR: two row tiles, one to a warpgroup, share every k and v tile: prompts, where the products
-// bound it (a prompt of 8192 tokens, 32/8 heads of 128: 421 us, 1306 TFLOP/s counting what is seen).
+// bound it (a prompt of 8192 tokens, 32/8 heads of 128: 447 us, 1230 TFLOP/s counting what is seen).
 // A tile's period is 3000 to 3500 cycles, products 2048 of it, the exponentials of 256 x 128 weights
 // another 2048 of their own unit, and what a warpgroup does between its scores and its weights.
 // Otherwise one row tile, whose slot tiles the warpgroups take in turn and join at the end: drafted
@@ -321,8 +321,8 @@ __device__ void load_boxes(const TokensArgs &a, const KvView &kv, const CUtensor
             asm volatile(
                 "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to + from * 128 + h * (S::KT * 128)),
-                "l"(reinterpret_cast<uint64_t>(map)), "r"((S::kPasses > 1 ? x.dim : 0) + 64 * h), "r"(x.row), "r"(x.head),
-                "r"(x.page), "r"(smem_addr(bar))
+                "l"(reinterpret_cast<uint64_t>(map)), "r"((S::kPasses > 1 ? x.dim : 0) + 64 * h),
+                "r"(x.row), "r"(x.head), "r"(x.page), "r"(smem_addr(bar))
                 : "memory");
         }
     };

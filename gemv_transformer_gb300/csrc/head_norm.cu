@@ -13,7 +13,7 @@
 // is held by G lanes of a warp, eight values each in two runs of four (head_units.cuh), so its sums
 // are log2 G shuffles and every value is read and written once; a group of lanes takes up to
 // kHeadsPer heads of a row, whose loads are in flight together and share the row's angles.
-// Measured: 4900 rows of 32 heads of 80 to bf16, LayerNorm, two axes 22 us (3.5 TB/s); gradient of 4096
+// Measured: 4900 rows of 32 heads of 80 to bf16, LayerNorm, two axes 26 us (2.9 TB/s); gradient of 4096
 // rows of 40 heads of 128 48 us (5.3 TB/s); append of 8002 tokens of 28/4 heads of 128, three axes
 // 51 us (4.3 TB/s), of 256 tokens of 32/8 heads 5 us (the host's call).
 #include <initializer_list>
