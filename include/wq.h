@@ -642,7 +642,9 @@ typedef struct {
  *   out = sum p v,  lse = ln sum exp(x),
  * for each of h_q query heads; query head h reads kv head h / (h_q / kv heads).
  * A token that sees nothing has out 0 and lse -inf.  What a token does not see does not
- * reach its results, whatever it holds.
+ * reach its results, whatever it holds.  Infinities and NaN that it sees do: of its query and of a k as
+ * the formula says (of an infinite k that, or NaN, under f32 queries over a bf16 cache, whose terms
+ * may have either sign), of a v as values that are not finite in its dim.
  * q: q_type (WQ_F32, WQ_BF16, WQ_F16), rows of h_q heads; out: out_type, q_type or WQ_F32;
  * strides in elements.  lse: f32 [n_tok][h_q] or NULL.
  * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products).  16-bit
