@@ -652,18 +652,15 @@ __device__ void issue_products(const TokensArgs &a, const Room &room, const Ctx 
 
 // -------------------------------------------------------------- softmax warpgroups --
 
-// The first bf16 term of two values and what it leaves of them.  A finite value that rounds to infinity
-// keeps bf16's largest in its first term (the others hold the rest), an infinity leaves nothing
-// (inf - inf would make a NaN of it).
-__device__ __forceinline__ uint32_t first_term(float &lo, float &hi) {
-    uint32_t w = pack2<kBF16>(lo, hi);
-    if ((w & 0x7FFFu) == 0x7F80u && !isinf(lo)) --w;
-    if ((w & 0x7FFF0000u) == 0x7F800000u && !isinf(hi)) w -= 0x10000u;
-    lo = isinf(lo) ? 0.f : lo - bf16_lo(w);
-    hi = isinf(hi) ? 0.f : hi - bf16_hi(w);
-    return w;
+// Two bf16 values held within bf16's largest, their signs kept.
+__device__ __forceinline__ uint32_t held16x2(uint32_t w) {
+    uint32_t r;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0x7F7F7F7Fu));
+    return r;
 }
-// f32 queries of a row tile as three bf16 terms, by all softmax threads.
+// f32 queries of a row tile as three bf16 terms, by all softmax threads.  Only the last term may be
+// infinite: a finite value that bf16 rounds to infinity has the rest of it in the next term, and an
+// infinite one leaves an infinity, not inf - inf.  (A NaN does so too, as a NaN.)
 template <typename S>
 __device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, const Tile &tile,
                                        int head, const Ctx &c) {
@@ -702,11 +699,8 @@ __device__ __forceinline__ void load_q(const TokensArgs &a, const KvView &kv, co
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (t == 0) {
-                        w[e] = first_term(y[2 * e], y[2 * e + 1]);
-                        continue;
-                    }
                     w[e] = pack2<kBF16>(y[2 * e], y[2 * e + 1]);
+                    if (t + 1 < S::TERMS) w[e] = held16x2(w[e]);
                     y[2 * e] -= bf16_lo(w[e]);
                     y[2 * e + 1] -= bf16_hi(w[e]);
                 }
