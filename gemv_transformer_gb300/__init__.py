@@ -48,7 +48,7 @@ EXPORTS = ("wq_gemm", "wq_gemm_ws", "wq_gemm_alpha", "wq_gemm_dual", "wq_gemm_wo
            "wq_attn_paged_workspace_bytes", "wq_kv_evict", "wq_kv_evict_workspace_bytes",
            "wq_norm_rope", "wq_norm_rope_grad", "wq_norm_rope_grad_workspace_bytes",
            "wq_kv_append_norm", "wq_attn_tokens", "wq_attn_tokens_workspace_bytes",
-           "wq_kv_accept")
+           "wq_kv_accept", "wq_kv_accept_slots")
 
 _lock = threading.Lock()
 _lib = None
@@ -93,6 +93,11 @@ class AttnForm(ctypes.Structure):
                 ("tree_stride", ctypes.c_int64), ("pos", ctypes.c_void_p)]
 
 
+class SlotArrays(ctypes.Structure):
+    """wq_slot_arrays."""
+    _fields_ = [("acc", ctypes.c_void_p), ("slot_pos", ctypes.c_void_p)]
+
+
 def head_norm(kind, eps=1e-6, weight=None, bias=None) -> HeadNorm:
     """The descriptor of a norm of heads.  Like the others it keeps addresses, not the tensors."""
     return HeadNorm(kind, eps, _p(weight), _p(bias))
@@ -119,6 +124,13 @@ def kv_caches(ks, vs):
     """The descriptors of several layers' pools, for wq_kv_accept."""
     caches = [kv_cache(k, v) for k, v in zip(ks, vs, strict=True)]
     return (KvCache * len(caches))(*caches)
+
+
+def slot_arrays(accs, positions):
+    """The slots' weights and positions of several layers ([sequence][kv head][slot], or None), for
+    wq_kv_accept_slots."""
+    arrays = [SlotArrays(_p(a), _p(b)) for a, b in zip(accs, positions, strict=True)]
+    return (SlotArrays * len(arrays))(*arrays)
 
 
 def kv_cache(k, v) -> KvCache:
@@ -217,6 +229,9 @@ def _open(path: str):
     lib.wq_attn_tokens_workspace_bytes.restype = sz
     lib.wq_kv_accept.argtypes = [cp, ci, ci, ci, vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.wq_kv_accept.restype = ci
+    lib.wq_kv_accept_slots.argtypes = lib.wq_kv_accept.argtypes[:-1] + [
+        ctypes.POINTER(SlotArrays), i64, vp]
+    lib.wq_kv_accept_slots.restype = ci
     lib.wq_get_device_status.argtypes = [vp]
     lib.wq_get_device_status.restype = ci
     lib.wq_status_string.argtypes = [ci]
@@ -476,6 +491,22 @@ def wq_kv_accept(caches, n_seq, n_tok, page_table, max_pages, starts, parent, to
     return (_calls or _load_calls()).wq_kv_accept(
         caches, len(caches), n_seq, n_tok, page_table, max_pages, starts, parent, tokens, choice,
         lens, path, accepted, next, lens_out, stream)
+
+
+def wq_kv_accept_slots(caches, n_seq, n_tok, page_table, max_pages, starts, parent, tokens, choice,
+                       lens, path, accepted, next, lens_out, slots, acc_stride,
+                       stream=None) -> int:
+    """caches as wq_kv_accept's; slots: slot_arrays(...), one for each cache, or one SlotArrays."""
+    if isinstance(caches, KvCache):
+        caches = (KvCache * 1)(caches)
+    if isinstance(slots, SlotArrays):
+        slots = (SlotArrays * 1)(slots)
+    if slots is not None and len(slots) != len(caches):
+        raise TypeError("slots: not as many as the caches")
+    return load().wq_kv_accept_slots(
+        caches, len(caches), n_seq, n_tok, _p(page_table), max_pages, _p(starts), _p(parent),
+        _p(tokens), _p(choice), _p(lens), _p(path), _p(accepted), _p(next), _p(lens_out), slots,
+        acc_stride, _s(stream))
 
 
 def wq_get_device_status(stream=None) -> int:

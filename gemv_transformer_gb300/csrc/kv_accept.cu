@@ -1,5 +1,5 @@
 // kv_accept.cu -- the accepted path of a drafted tree, and its k and v moved together in every
-// layer's cache.
+// layer's cache; with them, where they are given, the slots' accumulated weights and positions.
 //
 // The path is a chain: the root, then again and again the lowest child of the last node whose token
 // is the one that the model chose after it.  A child's number is above its parent's, so one pass
@@ -7,9 +7,11 @@
 //
 // What bounds it: latency (a chain of loads of lengths, nodes, pages, rows); the rows moved are a
 // few kilobytes per layer.  One launch: each CTA finds its sequence's path itself with one warp,
-// 32 nodes at a time, and its threads then move one 16-byte column of one row each, so that no
-// thread reads what another one writes.  The i-th node's slot goes to slot i <= path[i]: in
+// 32 nodes at a time, and its threads then move one 16-byte column of one row each (of the weights and
+// positions 4 bytes of a head), so that no thread reads what another one writes.  The i-th node's slot goes to slot i <= path[i]: in
 // rising order a slot is read before it is overwritten.
+#include <type_traits>
+
 #include "kv_internal.h"
 #include "wq_device.cuh"
 
@@ -19,9 +21,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kInFlight = 8;  // rows that a thread reads before it writes them
 
+struct NoSlots {};
+
+// Slots: AcceptSlots, or NoSlots where there are none.
+template <typename Slots>
 __global__ void __launch_bounds__(kThreads)
     kv_accept_kernel(AcceptArgs a, KvView kv, const __grid_constant__ AcceptPools pools,
-                     FastDiv chunks, bool write_path) {
+                     FastDiv chunks, bool write_path, const __grid_constant__ Slots slots) {
+    constexpr bool kSlots = std::is_same<Slots, AcceptSlots>::value;
     pdl_enter();
     __shared__ int s_node[32], s_found;
     const int s = blockIdx.y, lane = threadIdx.x & 31;
@@ -42,10 +49,21 @@ __global__ void __launch_bounds__(kThreads)
     const unsigned at = blockIdx.x * kThreads + threadIdx.x;
     const unsigned row_at = chunks.div(at), chunk = at - row_at * chunks.d;
     const int head = row_at % kv.n_heads, pool = row_at / kv.n_heads;
-    const bool moves = pool < 2 * pools.count;
+    bool moves = pool < 2 * pools.count;
     char *col = !moves ? nullptr
                 : (pool & 1 ? pools.v[pool >> 1] : pools.k[pool >> 1]) +
                       (long long)head * kv.head_stride + chunk * 16;
+    bool word = false;  // a column of 4 bytes, by slot
+    if constexpr (kSlots) {
+        const unsigned wide = 2u * pools.count * kv.n_heads * chunks.d;
+        if (at >= wide) {  // of a head's weights or positions
+            const unsigned x = at - wide, array = x / kv.n_heads, h = x - array * kv.n_heads;
+            word = array < 2u * pools.count;
+            char *const p = !word ? nullptr : static_cast<char *>(slots.p[array]);
+            moves = p != nullptr;
+            col = p + (((slots.seq0 + s) * kv.n_heads + h) * slots.stride + base) * 4;
+        }
+    }
 
     int tip = 0, found = 1, want = a.choice[t0];  // of warp 0
     for (int c0 = 0; c0 < count; c0 += 32) {
@@ -91,12 +109,22 @@ __global__ void __launch_bounds__(kThreads)
                         if (write_path) record_status(a.status, kStBadIndex);
                         continue;
                     }
+                    if (kSlots && word) {
+                        to[j] = 4ll * dst;
+                        v[j].x = *reinterpret_cast<const uint32_t *>(col + 4ll * src);
+                        continue;
+                    }
                     to[j] = dest;
                     v[j] = *reinterpret_cast<const uint4 *>(col + from);
                 }
 #pragma unroll
-                for (int j = 0; j < kInFlight; ++j)
-                    if (to[j] >= 0) *reinterpret_cast<uint4 *>(col + to[j]) = v[j];
+                for (int j = 0; j < kInFlight; ++j) {
+                    if (to[j] < 0) continue;
+                    if (kSlots && word)
+                        *reinterpret_cast<uint32_t *>(col + to[j]) = v[j].x;
+                    else
+                        *reinterpret_cast<uint4 *>(col + to[j]) = v[j];
+                }
             }
         }
         found = i0 + n;
@@ -115,9 +143,9 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_kv_accept(const AcceptArgs &a, const KvView &kv, const AcceptPools &pools,
-                             bool write_path, cudaStream_t stream) {
+                             const AcceptSlots *slots, bool write_path, cudaStream_t stream) {
     const FastDiv chunks = make_fast_div(kv.head_dim * (kv.dtype == kF32 ? 4 : 2) / 16);
-    const long long columns = 2ll * pools.count * kv.n_heads * chunks.d;
+    const long long columns = 2ll * pools.count * kv.n_heads * (chunks.d + (slots ? 1 : 0));
     // Sequences are the grid's y, 65535 at most.
     for (int s0 = 0; s0 < a.n_seq; s0 += 65535) {
         AcceptArgs part = a;
@@ -126,10 +154,17 @@ cudaError_t launch_kv_accept(const AcceptArgs &a, const KvView &kv, const Accept
         part.starts += s0, part.lens += s0, part.accepted += s0, part.next += s0;
         part.lens_out += s0;
         view.page_table += (long long)s0 * kv.max_pages;
-        const cudaError_t err =
-            launch_pdl(kv_accept_kernel, dim3((unsigned)((columns + kThreads - 1) / kThreads),
-                                              (unsigned)part.n_seq),
-                       dim3(kThreads), 0, stream, part, view, pools, chunks, write_path);
+        const dim3 grid((unsigned)((columns + kThreads - 1) / kThreads), (unsigned)part.n_seq);
+        cudaError_t err;
+        if (slots) {
+            AcceptSlots its = *slots;
+            its.seq0 = s0;
+            err = launch_pdl(kv_accept_kernel<AcceptSlots>, grid, dim3(kThreads), 0, stream, part,
+                             view, pools, chunks, write_path, its);
+        } else {
+            err = launch_pdl(kv_accept_kernel<NoSlots>, grid, dim3(kThreads), 0, stream, part, view,
+                             pools, chunks, write_path, NoSlots{});
+        }
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;

@@ -139,6 +139,54 @@ bool typed_rows_ok(const void *x, int type, int64_t stride, int n_heads, int hea
 
 int cut(int n, long long to) { return to < n ? (int)to : n; }
 
+// wq_kv_accept; slots null: none.
+wq_status accept_paths(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,
+                       const int32_t *page_table, int max_pages, const int32_t *starts,
+                       const int32_t *parent, const int32_t *tokens, const int32_t *choice,
+                       const int32_t *lens, int32_t *path, int32_t *accepted, int32_t *next,
+                       int32_t *lens_out, const wq_slot_arrays *slots, int64_t acc_stride,
+                       wq_stream_t stream) {
+    if (!caches || n_caches <= 0 || n_tok <= 0) return WQ_ERR_INVALID_ARG;
+    if (!page_table || !starts || !parent || !tokens || !choice || !lens || !path || !accepted ||
+        !next || !lens_out || lens_out == lens)
+        return WQ_ERR_INVALID_ARG;
+    KvView kv, other;
+    for (int i = 0; i < n_caches; ++i) {
+        if (!view_of(&caches[i], n_seq, page_table, max_pages, i ? other : kv))
+            return WQ_ERR_INVALID_ARG;
+        const wq_kv_cache &c = caches[i], &f = caches[0];
+        if (c.dtype != f.dtype || c.n_pages != f.n_pages || c.page_size != f.page_size ||
+            c.n_heads != f.n_heads || c.head_dim != f.head_dim ||
+            c.page_stride != f.page_stride || c.head_stride != f.head_stride ||
+            c.token_stride != f.token_stride)
+            return WQ_ERR_INVALID_ARG;
+        if (slots && !(aligned(slots[i].acc, 4) && aligned(slots[i].slot_pos, 4)))
+            return WQ_ERR_INVALID_ARG;
+    }
+    DeviceInfo dev;
+    if (!device_info(dev)) return WQ_ERR_CUDA;
+    AcceptArgs a{n_seq, n_tok, max_pages * (int)kv.page_size.d, starts, parent, tokens, choice,
+                 lens, path, accepted, next, lens_out, dev.status};
+    if (slots) a.n_slots = cut(a.n_slots, acc_stride);
+    for (int c0 = 0; c0 < n_caches; c0 += kAcceptCaches) {
+        AcceptPools pools{};
+        AcceptSlots arrays{};
+        arrays.stride = acc_stride;
+        pools.count = n_caches - c0 < kAcceptCaches ? n_caches - c0 : kAcceptCaches;
+        for (int i = 0; i < pools.count; ++i) {
+            pools.k[i] = static_cast<char *>(caches[c0 + i].k);
+            pools.v[i] = static_cast<char *>(caches[c0 + i].v);
+            if (!slots) continue;
+            arrays.p[2 * i] = slots[c0 + i].acc;
+            arrays.p[2 * i + 1] = slots[c0 + i].slot_pos;
+        }
+        const cudaError_t err = launch_kv_accept(a, kv, pools, slots ? &arrays : nullptr, c0 == 0,
+                                                 (cudaStream_t)stream);
+        if (err != cudaSuccess) return WQ_ERR_CUDA;
+    }
+    return WQ_OK;
+}
+
 }  // namespace
 }  // namespace wq
 
@@ -512,36 +560,20 @@ wq_status wq_kv_accept(const wq_kv_cache *caches, int n_caches, int n_seq, int n
                        const int32_t *parent, const int32_t *tokens, const int32_t *choice,
                        const int32_t *lens, int32_t *path, int32_t *accepted, int32_t *next,
                        int32_t *lens_out, wq_stream_t stream) {
-    if (!caches || n_caches <= 0 || n_tok <= 0) return WQ_ERR_INVALID_ARG;
-    if (!page_table || !starts || !parent || !tokens || !choice || !lens || !path || !accepted ||
-        !next || !lens_out || lens_out == lens)
-        return WQ_ERR_INVALID_ARG;
-    KvView kv, other;
-    for (int i = 0; i < n_caches; ++i) {
-        if (!view_of(&caches[i], n_seq, page_table, max_pages, i ? other : kv))
-            return WQ_ERR_INVALID_ARG;
-        const wq_kv_cache &c = caches[i], &f = caches[0];
-        if (c.dtype != f.dtype || c.n_pages != f.n_pages || c.page_size != f.page_size ||
-            c.n_heads != f.n_heads || c.head_dim != f.head_dim ||
-            c.page_stride != f.page_stride || c.head_stride != f.head_stride ||
-            c.token_stride != f.token_stride)
-            return WQ_ERR_INVALID_ARG;
-    }
-    DeviceInfo dev;
-    if (!device_info(dev)) return WQ_ERR_CUDA;
-    AcceptArgs a{n_seq, n_tok, max_pages * (int)kv.page_size.d, starts, parent, tokens, choice,
-                 lens, path, accepted, next, lens_out, dev.status};
-    for (int c0 = 0; c0 < n_caches; c0 += kAcceptCaches) {
-        AcceptPools pools{};
-        pools.count = n_caches - c0 < kAcceptCaches ? n_caches - c0 : kAcceptCaches;
-        for (int i = 0; i < pools.count; ++i) {
-            pools.k[i] = static_cast<char *>(caches[c0 + i].k);
-            pools.v[i] = static_cast<char *>(caches[c0 + i].v);
-        }
-        const cudaError_t err = launch_kv_accept(a, kv, pools, c0 == 0, (cudaStream_t)stream);
-        if (err != cudaSuccess) return WQ_ERR_CUDA;
-    }
-    return WQ_OK;
+    return accept_paths(caches, n_caches, n_seq, n_tok, page_table, max_pages, starts, parent,
+                        tokens, choice, lens, path, accepted, next, lens_out, nullptr, 0, stream);
+}
+
+wq_status wq_kv_accept_slots(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,
+                             const int32_t *page_table, int max_pages, const int32_t *starts,
+                             const int32_t *parent, const int32_t *tokens, const int32_t *choice,
+                             const int32_t *lens, int32_t *path, int32_t *accepted, int32_t *next,
+                             int32_t *lens_out, const wq_slot_arrays *slots, int64_t acc_stride,
+                             wq_stream_t stream) {
+    if (!slots || acc_stride < 1) return WQ_ERR_INVALID_ARG;
+    return accept_paths(caches, n_caches, n_seq, n_tok, page_table, max_pages, starts, parent,
+                        tokens, choice, lens, path, accepted, next, lens_out, slots, acc_stride,
+                        stream);
 }
 
 }  // extern "C"

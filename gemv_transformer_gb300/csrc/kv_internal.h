@@ -126,6 +126,11 @@ struct AcceptPools {
     int count;
     char *k[kAcceptCaches], *v[kAcceptCaches];
 };
+// Their slots' weights and positions, by turns, each [n_seq][kv heads][stride] or null.
+struct AcceptSlots {
+    long long stride, seq0;  // seq0: the launch's first sequence
+    void *p[2 * kAcceptCaches];
+};
 
 cudaError_t launch_norm_rope(const AxesView &ax, const NormView &nv, int n, int n_heads,
                              int head_dim, const float *x, long long x_stride, int out_type,
@@ -143,8 +148,9 @@ cudaError_t launch_norm_rope_grad(const AxesView &ax, const NormView &nv, int n,
 size_t tokens_workspace_bytes(const KvView &kv, int n_seq, int n_tok, int h_q, int q_type);
 cudaError_t launch_attn_tokens(const TokensArgs &a, const KvView &kv, const DeviceInfo &dev,
                                cudaStream_t stream);
+// slots: null where there are none.
 cudaError_t launch_kv_accept(const AcceptArgs &a, const KvView &kv, const AcceptPools &pools,
-                             bool write_path, cudaStream_t stream);
+                             const AcceptSlots *slots, bool write_path, cudaStream_t stream);
 
 cudaError_t launch_rope_table(int rows, int rot, double base, const wq_rope_scaling &sc,
                               float *table, const DeviceInfo &dev, cudaStream_t stream);

@@ -645,6 +645,9 @@ typedef struct {
  * reach its results, whatever it holds.  Infinities and NaN that it sees do: of its query and of a k as
  * the formula says (of an infinite k that, or NaN, under f32 queries over a bf16 cache, whose terms
  * may have either sign), of a v as values that are not finite in its dim.
+ * Accumulated weights (acc) are not added to, as wq_attn_paged's acc_out does: a slot that only this
+ * call has read keeps the 0 that it was appended with, and of equal weights wq_kv_evict keeps the
+ * lower slots.
  * q: q_type (WQ_F32, WQ_BF16, WQ_F16), rows of h_q heads; out: out_type, q_type or WQ_F32;
  * strides in elements.  lse: f32 [n_tok][h_q] or NULL.
  * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products).  16-bit
@@ -689,7 +692,8 @@ WQ_API size_t wq_attn_tokens_workspace_bytes(const wq_kv_cache *cache, int n_seq
  *   lens_out[s] = B + accepted[s]
  * and in each of n_caches caches (a model's layers, alike but for k and v, each listed once; the
  * array is read on the host) the k and v of the path's i-th node move from slot B + path[i] to B + i.  The
- * slots behind them keep what they hold.
+ * slots behind them keep what they hold.  Accumulated weights and positions of the slots (acc and
+ * slot_pos) stay where they are: where wq_kv_evict is to read them, wq_kv_accept_slots moves them too.
  * A sequence without new tokens: accepted 0, next -1, lens_out = lens.  One whose starts or
  * length are not as in wq_attn_tokens is treated like that, its path is left unwritten, and
  * a node whose pages are out of range is not moved; both record WQ_ERR_BAD_INDEX.
@@ -703,6 +707,28 @@ WQ_API wq_status wq_kv_accept(const wq_kv_cache *caches, int n_caches, int n_seq
                               const int32_t *choice, const int32_t *lens, int32_t *path,
                               int32_t *accepted, int32_t *next, int32_t *lens_out,
                               wq_stream_t stream);
+
+/* Of one cache, for wq_kv_accept_slots: acc and slot_pos as wq_kv_append_norm set them, f32 and int32
+ * [n_seq][kv heads][acc_stride]; each may be NULL. */
+typedef struct {
+    float *acc;
+    int32_t *slot_pos;
+} wq_slot_arrays;
+
+/*
+ * wq_kv_accept, and with the k and v of a path's node move, in each head, the accumulated weight and
+ * the position of its slot, so that wq_kv_evict and wq_attn_paged go on with them.
+ * slots: n_caches of them, by cache, read on the host.  A length above acc_stride counts as one above
+ * max_pages * page_size.
+ * Errors: as wq_kv_accept; WQ_ERR_INVALID_ARG also for null slots, acc_stride < 1 and arrays that are
+ * not 4-byte aligned. */
+WQ_API wq_status wq_kv_accept_slots(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,
+                                    const int32_t *page_table, int max_pages,
+                                    const int32_t *starts, const int32_t *parent,
+                                    const int32_t *tokens, const int32_t *choice,
+                                    const int32_t *lens, int32_t *path, int32_t *accepted,
+                                    int32_t *next, int32_t *lens_out, const wq_slot_arrays *slots,
+                                    int64_t acc_stride, wq_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the current device's sticky
  * status word: WQ_OK, WQ_ERR_DEVICE_TIMEOUT, WQ_ERR_BAD_EXPERT or
