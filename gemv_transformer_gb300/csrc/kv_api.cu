@@ -9,6 +9,9 @@ namespace {
 
 constexpr int kMaxHeadDim = 256;
 constexpr long long kMaxSlots = 1ll << 30;  // a slot number and a tile beyond it fit an int
+// Of attention's scale and cap, and one by it the least cap: their quotient is finite in f32, as are
+// their products with log2 e.
+constexpr float kMostScale = (float)(1ull << 60);
 constexpr int64_t kMaxStride = INT64_MAX / 64 / 0x7FFFFFFF;  // offsets of any row fit 64 bits
 
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -515,6 +518,9 @@ wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q
     wq_attn_form f{};
     if (form) f = *form;
     if (!std::isfinite(f.softcap) || f.softcap < 0.f || f.window < 0) return WQ_ERR_INVALID_ARG;
+    if (std::fabs(scale) > kMostScale || f.softcap > kMostScale ||
+        (f.softcap > 0.f && f.softcap < 1.f / kMostScale))
+        return WQ_ERR_INVALID_ARG;
     if ((f.tree && (f.prefix || f.tree_stride < 1 || f.tree_stride > kMaxStride)) ||
         (f.pos && !f.tree))
         return WQ_ERR_INVALID_ARG;

@@ -664,9 +664,9 @@ typedef struct {
  * form (read on the host, not kept) NULL: causal, no cap.
  * workspace: as wq_attn_paged's, of wq_attn_tokens_workspace_bytes(...) bytes.
  * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, n_tok, h_q, max_pages <= 0, h_q
- * not a multiple of the kv heads, a scale that is not finite, a softcap below 0 or not finite,
- * window < 0, tree with prefix, tree_stride < 1 or above 2^26, pos without tree, unknown types,
- * null q, starts, page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
+ * not a multiple of the kv heads, a scale that is not finite or above 2^60 in size, a softcap that is
+ * neither 0 nor from 2^-60 to 2^60, window < 0, tree with prefix, tree_stride < 1 or above 2^26,
+ * pos without tree, unknown types, null q, starts, page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
  * or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
  * missing, misaligned or small workspace. */
 WQ_API wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q,

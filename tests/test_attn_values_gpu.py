@@ -107,3 +107,13 @@ def test_infinite_keys(kind, qtype, d, value):
     c.out.view(c.m, 4, d)[torch.from_numpy(void).cuda()] = 0
     c.lse[torch.from_numpy(void).cuda()] = 0
     c.check(w)
+
+
+@pytest.mark.parametrize("kind,qtype", TYPES)
+def test_the_largest_and_the_least_cap(kind, qtype):
+    """A cap of 2^60 changes no score by more than its roundings (8 units of the last place of the
+    score), one of 2^-60 makes all weights alike."""
+    c = Case(34, [20, 70], [40, 100], 4, 2, 128, kind, qtype, softcap=2.0 ** 60).run()
+    c.softcap = 0.0
+    c.check()
+    Case(35, [20, 70], [40, 100], 4, 2, 64, kind, qtype, softcap=2.0 ** -60).run().check()
