@@ -718,8 +718,8 @@ typedef struct {
 /*
  * wq_kv_accept, and with the k and v of a path's node move, in each head, the accumulated weight and
  * the position of its slot, so that wq_kv_evict and wq_attn_paged go on with them.
- * slots: n_caches of them, by cache, read on the host.  A length above acc_stride counts as one above
- * max_pages * page_size.
+ * slots: n_caches of them, by cache, read on the host; an array that several caches share is listed
+ * with one of them.  A length above acc_stride counts as one above max_pages * page_size.
  * Errors: as wq_kv_accept; WQ_ERR_INVALID_ARG also for null slots, acc_stride < 1 and arrays that are
  * not 4-byte aligned. */
 WQ_API wq_status wq_kv_accept_slots(const wq_kv_cache *caches, int n_caches, int n_seq, int n_tok,

@@ -195,3 +195,42 @@ def test_a_step_of_drafts_before_an_eviction():
         assert np.array_equal(p.cpu().view(torch.int16).numpy(), w)
     stayed = np.sort(draft.pos_dev[0].cpu().numpy()[0, :, :keep], -1)
     assert (stayed[:, -recent:] == np.arange(length - recent, length)).all()
+
+
+def test_more_sequences_than_a_launch_takes():
+    """66000 trees of three nodes: the root, and two children of which the model chose the second, the
+    first or none."""
+    n, page, d = 66000, 4, 8
+    g = np.random.default_rng(12)
+    f = dict(device="cuda")
+    pages = g.permutation(n).astype(np.int32)[:, None]
+    k, v = (torch.randn(n, 1, page, d, **f) for _ in range(2))
+    acc = torch.rand(n, 1, page, **f)
+    pos = torch.randint(0, 1 << 30, (n, 1, page), dtype=torch.int32, **f)
+    choice = g.integers(5, 8, n)  # children 5 and 6
+    tokens = np.tile([4, 5, 6], n).astype(np.int32)
+    chosen = np.stack([choice, np.zeros(n), np.full(n, 9)], 1).reshape(-1).astype(np.int32)
+    outs = [torch.full((3 * n,), 77, dtype=torch.int32, **f)] + [
+        torch.full((n,), 77, dtype=torch.int32, **f) for _ in range(3)]
+    wants = []
+    second = torch.from_numpy(choice == 6).cuda()
+    at = dev(pages[:, 0]).long()
+    for t, rows in ((k, at), (v, at), (acc, torch.arange(n, **f)), (pos, torch.arange(n, **f))):
+        w = t.clone()
+        r = rows[second]
+        w[r, :, 2] = t[r, :, 3]  # slot 1 + 2 to slot 1 + 1
+        wants.append(w)
+    wq.check(wq.wq_kv_accept_slots(
+        wq.kv_cache(k, v), n, 3 * n, dev(pages), 1, dev((3 * np.arange(n + 1)).astype(np.int32)),
+        dev(np.tile([-1, 0, 0], n).astype(np.int32)), dev(tokens), dev(chosen),
+        torch.full((n,), 4, dtype=torch.int32, **f), *outs, wq.slot_arrays([acc], [pos]), page))
+    torch.cuda.synchronize()
+    for got, want in zip((k, v, acc, pos), wants):
+        assert torch.equal(got, want)
+    path = np.full((n, 3), -1)
+    path[:, 0] = 0
+    path[choice == 5, 1], path[choice == 6, 1] = 1, 2
+    count = np.where(choice == 7, 1, 2)
+    assert (outs[0].cpu().numpy().reshape(n, 3) == path).all()
+    assert (outs[1].cpu().numpy() == count).all() and (outs[3].cpu().numpy() == 1 + count).all()
+    assert (outs[2].cpu().numpy() == np.choose(choice - 5, [0, 9, 7])).all()
