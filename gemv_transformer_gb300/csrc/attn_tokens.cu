@@ -4,13 +4,14 @@
 // x = cap(scale q.k) + slope (pos_k - pos_q), p = softmax(x) with a running maximum and sum,
 // in log2 units: y = x log2 e, p = 2^(y - m).
 //
-// attn_rows_kernel takes f32 caches, f32 queries over f16 caches, mixed 16-bit types and heads above
-// 128 dims: k and v are f32 in shared memory and every product is an f32 FMA, so it is exact to f32.
+// attn_rows_kernel takes f32 caches, f32 queries over f16 caches, mixed 16-bit types, and of heads above
+// 128 dims all but 16-bit ones in pages of a multiple of 8 slots: k and v are f32 in shared memory and
+// every product is an f32 FMA, so it is exact to f32.
 // What bounds it: the FMA pipe (4 head_dim operations per row and slot) and the shared memory that
 // feeds it (48 wavefronts to 64 FMA cycles), and for short rows how evenly 304 ranges share few
 // tiles.  A thread holds R rows by KT / 16 slots of the scores and R rows by DP / 16 dims of the
 // output, two neighbouring dims to an instruction; the 16 lanes of a row join its maximum and sum
-// by shuffles.  Three packed batches of documents, 12/6 heads of 96, f32: 69 us, a quarter of the FMA
+// by shuffles.  Three packed batches of documents, 12/6 heads of 96, f32: 67 us, a quarter of the FMA
 // rate while a CTA works; 12 trees of f32 queries and an f32 cache to 6000 slots: 424 us.
 #include "attn_tokens.cuh"
 

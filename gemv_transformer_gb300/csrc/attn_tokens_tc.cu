@@ -6,21 +6,23 @@
 //
 //   16-bit q    one product each; p is rounded to the cache's type, its sum is not.  The output
 //               stays in tensor memory: m is only raised, and the output scaled, when a row's
-//               maximum has outgrown it by more than 2^8, which after the first tiles is rare.
+//               maximum has outgrown it by more than 2^8, which after the first tiles is rare (a
+//               published step of others' work on attention for this generation).
 //   f32 q       (bf16 caches) q and p as three bf16 terms, 24 bits, whose products are exact: three
 //               products each, the smallest terms first.  The tensor core truncates when it
 //               accumulates, so P V of a tile, T, is added to an output in registers: o = o 2^(m_old -
 //               m) + T.
 //
 // PAIR: two row tiles, one to a warpgroup, share every k and v tile: prompts, where the products
-// bound it (a prompt of 8192 tokens, 32/8 heads of 128: 447 us, 1230 TFLOP/s counting what is seen).
-// A tile's period is 3000 to 3500 cycles, products 2048 of it, the exponentials of 256 x 128 weights
-// another 2048 of their own unit, and what a warpgroup does between its scores and its weights.
+// bound it (a prompt of 8192 tokens, 32/8 heads of 128: 443 us, 1240 TFLOP/s counting what is seen).
+// A tile's period is 3000 to 3500 cycles, products 2048 of it; the exponentials of 256 x 128 weights are
+// 1024 of their own unit (32 a cycle), and the rest is the chain from a warpgroup's scores to its
+// weights, of which a second warpgroup's products hide a part.
 // Otherwise one row tile, whose slot tiles the warpgroups take in turn and join at the end: drafted
 // trees, where the cache's bytes bound it and a second tile in flight hides the chain of the
 // first (32 trees to 8192 slots: 117 us, 4.75 TB/s).  f32 queries: the three products of a score,
 // whose N is 64, are bound by shared memory (48 cycles in place of 32), the weights' chain comes
-// close to them (12 trees to 6000 slots: 81 us, with a cap 101).
+// close to them (12 trees to 6000 slots: 82 us, with a cap 102).
 //
 // Shared memory is rows of 128 bytes in the 128-byte swizzle; k is K-major, v MN-major (its
 // dims are the contiguous ones), p is read from tensor memory over S.

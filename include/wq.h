@@ -562,7 +562,8 @@ typedef struct {
 /*
  * out = R(norm(x)) for each of n_heads heads of n rows: the norm, then the rotation of its
  * first rope->rot values, in one pass; one rounding where out_type (WQ_F32, WQ_BF16, WQ_F16)
- * is a 16-bit type.  norm or rope NULL: none.
+ * is a 16-bit type.  norm or rope NULL: none.  Sums are f32: a head whose sum of squares passes f32's
+ * range (values above 2^60) has no norm.
  * x: f32; out: out_type; rows' strides in elements, from n_heads * head_dim to 2^26; any
  * address aligned to the element is taken, 16-byte multiples and head_dim and rot multiples of
  * 8 are faster.  out may equal x with the same stride and WQ_F32.
@@ -653,8 +654,9 @@ typedef struct {
  * Sums are f32.  f32 queries: products are exact (f32 and f16 caches: f32 products).  16-bit
  * queries over a cache of their type (heads above 128: in pages of a multiple of 8 slots):
  * tensor-core products, in which p is rounded to that type (by half a step: 2^-8 of it for bf16,
- * 2^-11 for f16, whose weights below 2^-24 of the largest are lost), and a sum over n slots may be
- * cut short by n / 16 times 2^-23 of it.  All others as f32 queries.
+ * 2^-11 for f16, whose weights below 2^-24 of the largest are lost), a sum over n slots may be
+ * cut short by n / 16 times 2^-23 of it, and a capped score is within 2^-21 of the cap.  All others as
+ * f32 queries.
  * Rows of q at or beyond starts[n_seq] reach no result, and theirs of out are not written.
  * Nothing overlaps out, lse or the workspace.
  * starts: int32 [n_seq + 1], rising from >= 0 to at most n_tok; a sequence whose range is not
@@ -666,8 +668,8 @@ typedef struct {
  * Errors: WQ_ERR_INVALID_ARG for the cache's restrictions, n_seq, n_tok, h_q, max_pages <= 0, h_q
  * not a multiple of the kv heads, a scale that is not finite or above 2^60 in size, a softcap that is
  * neither 0 nor from 2^-60 to 2^60, window < 0, tree with prefix, tree_stride < 1 or above 2^26,
- * pos without tree, unknown types, null q, starts, page_table, lens or out, q or out not 16-byte aligned or with a stride below h_q * head_dim
- * or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
+ * pos without tree, unknown types, null q, starts, page_table, lens or out, q or out not 16-byte
+ * aligned or with a stride below h_q * head_dim or not a multiple of 16 bytes, max_pages * page_size above 2^30, n_tok * h_q above 2^30, a
  * missing, misaligned or small workspace. */
 WQ_API wq_status wq_attn_tokens(const wq_kv_cache *cache, int n_seq, int n_tok, int h_q,
                                 float scale, const wq_attn_form *form, int q_type, const void *q,
